@@ -476,6 +476,107 @@ kda_status kda_short_conv_fwd(const void *x, kda_dtype x_dtype, const float *wei
 kda_status kda_o_proj(const void *y, const void *w_o, void *out, kda_dtype out_dtype, int64_t rows,
                       int in_features, int out_features, void *stream);
 
+/*
+ * Full attention.  The hybrid stacks interleave KDA layers with layers of full attention
+ * (nnterp encyclopedia "Kimi-Linear", section 03: one block in four; Kimi-K3 atlas
+ * "final-block-state", the layer-type schedule).  The four calls below are what such a
+ * layer computes around its projections: positions, the paged 8-bit key/value cache, the
+ * decode step's attention over that cache and the prompt's attention.  The pages give no
+ * kernels for these; the formulas are stated here.
+ *
+ * Rows of q, k and v may lie a stride apart (slices of a fused projection): a stride is the
+ * distance of one token's row to the next in elements, at least heads * dim and a multiple
+ * of 16 bytes; within a row the heads are dense.  Index arrays and scales need only the
+ * alignment of their type, so slices of larger arrays are used as they lie.
+ */
+
+typedef enum kda_rotary_layout {
+    KDA_ROTARY_HALF = 0,        /* pairs (i, i + rotary_dim / 2) */
+    KDA_ROTARY_INTERLEAVED = 1  /* pairs (2i, 2i + 1) */
+} kda_rotary_layout;
+
+/*
+ * kda_rotary -- rotary positions: the first rotary_dim channels of every head turned in
+ * pairs (a, b) by the angle w = positions[t] * inv_freq[i],
+ *     (a, b) -> magnitude * (a cos w - b sin w, a sin w + b cos w),
+ * the other channels copied.
+ *
+ *   x, out     [tokens, heads, dim] dtype, x_stride / out_stride apart; out may be x itself
+ *              (same pointer, same stride), no other overlap
+ *   positions  [tokens] int32, any values: angles are reduced exactly
+ *   inv_freq   [rotary_dim / 2] double, radians per position (scaled for long contexts by
+ *              the caller), magnitude the factor that such a scaling puts on the rotated part
+ *   inverse    1: the transposed rotation (angles negated), which undoes a rotation of
+ *              magnitude 1 and is the gradient of any
+ * rotary_dim a multiple of 16, at most dim; dim a multiple of 8, at most 256
+ * (KDA_ERR_UNSUPPORTED otherwise).  tokens may be 0.
+ */
+kda_status kda_rotary(const void *x, kda_dtype dtype, int64_t x_stride, const int32_t *positions,
+                      const double *inv_freq, float magnitude, int rotary_dim, int layout, int inverse, void *out,
+                      int64_t out_stride, int64_t tokens, int heads, int dim, void *stream);
+
+/*
+ * kda_kv_append -- appends new tokens' keys and values to a paged 8-bit cache, the keys
+ * rotated on the way, and rotates the same tokens' queries.
+ *
+ * The cache: k_cache, v_cache [num_pages, kv_heads, page_size, dim] e4m3 codes, k_scale,
+ * v_scale [num_pages, kv_heads] float; a value is code * scale.  Scales are powers of two
+ * 2^e, -100 <= e <= 100, the smallest that holds a block's largest finite value within 448.
+ * Token j of sequence n lies at place j % page_size of page block_table[n][j / page_size].
+ * A page whose place 0 is written by the call gets a new scale; a page that holds earlier
+ * tokens keeps its scale or, if a new value needs it, takes a larger one, its codes then
+ * moving to it (an exponent shift, rounded where it ends among the subnormals).  Places
+ * behind the last token are left as they are.  Infinities and NaN are stored as NaN and
+ * do not count for the scale.
+ *
+ *   k, v         [tokens, kv_heads, dim] bf16, k_stride / v_stride apart
+ *   context_lens [n_seqs] int32: tokens in the cache before the call (not changed)
+ *   cu_seqlens   [n_seqs + 1] int32: sequence n's new tokens are rows
+ *                [cu_seqlens[n], cu_seqlens[n + 1]) (clamped to [0, tokens]); NULL: one new
+ *                token per sequence, tokens == n_seqs
+ *   block_table  [n_seqs, max_blocks] int32.  A token whose page is negative, not below
+ *                num_pages, or behind the table is not stored (padding).
+ *   inv_freq     as kda_rotary, the position being the token's place in its sequence;
+ *                NULL: nothing is rotated (rotary_dim 0)
+ *   q, q_out     [tokens, q_heads, dim] bf16, q q_stride apart, q_out dense; both or neither
+ *   k_out        [tokens, kv_heads, dim] bf16, dense, or NULL: the rotated keys
+ * dim 64 or 128; page_size 16, 32, 64 or 128 (KDA_ERR_UNSUPPORTED otherwise).
+ * No page may be written for two sequences in one call.
+ */
+kda_status kda_kv_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride, int64_t tokens,
+                         int kv_heads, int dim, void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                         int num_pages, int page_size, const int32_t *block_table, int max_blocks,
+                         const int32_t *context_lens, const int32_t *cu_seqlens, int n_seqs, const double *inv_freq,
+                         float magnitude, int rotary_dim, int layout, const void *q, int64_t q_stride, int q_heads,
+                         void *q_out, void *k_out, void *stream);
+
+/*
+ * kda_attn_decode -- one query token per sequence over the paged 8-bit cache.
+ *
+ *     o[n][i] = sum_j softmax_j(scale * q[n][i] . K_j) V_j,   j < seq_lens[n],
+ * K_j and V_j the cached (code * scale) rows of head i / (q_heads / kv_heads).
+ *
+ *   q         [n_seqs, q_heads, dim] bf16, q_stride apart; q_heads a multiple of kv_heads
+ *   cache     as kda_kv_append; scales may be any positive floats
+ *   seq_lens  [n_seqs] int32: tokens to attend to (with the new one), clamped to
+ *             [0, max_blocks * page_size].  0 gives a zero row and lse -INFINITY.
+ *   o         [n_seqs, q_heads, dim] o_dtype
+ *   lse       [n_seqs, q_heads] float or NULL: log(sum_j e^(scale q . K_j))
+ *   workspace device scratch of kda_attn_decode_workspace_size(q_heads, kv_heads, dim)
+ *             bytes, 16-byte aligned; calls that may overlap on the GPU (two captured
+ *             graphs among them) need workspaces of their own
+ * What lies in a page behind a sequence's last token is not read into the result, whatever
+ * it is.  A sequence with a page number out of [0, num_pages) gives NaN rows.
+ * dim 64 or 128; page_size 16, 32, 64 or 128.  Results do not depend on timing.
+ */
+size_t kda_attn_decode_workspace_size(int q_heads, int kv_heads, int dim);
+
+kda_status kda_attn_decode(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                           const float *k_scale, const float *v_scale, int num_pages, int page_size,
+                           const int32_t *block_table, int max_blocks, const int32_t *seq_lens, int n_seqs,
+                           int q_heads, int kv_heads, int dim, float scale, void *o, kda_dtype o_dtype, float *lse,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

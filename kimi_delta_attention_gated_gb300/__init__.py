@@ -10,6 +10,10 @@ Entry points (same names as the C ABI, minus the ``kda_`` prefix):
   recurrent_fwd   token-by-token form over T tokens, optional per-token states
   recurrent_step  one decode token per sequence with the fused gated norm
   gated_rmsnorm   y = RMSNorm_v(o) * w * sigmoid(gate) per (token, head)
+The full-attention layers beside the KDA layers:
+  rotary          rotary positions (rotary_inv_freq: the angles, scaled for long contexts)
+  kv_append       keys and values into a paged 8-bit cache (kv_cache), rotated on the way
+  attn_decode     one query token per sequence over that cache
 
 Inputs may live on the host: they are copied to the current CUDA device, and the
 results are copied back to the host, which makes the call end-to-end.
@@ -17,14 +21,17 @@ results are copied back to the host, which makes the call end-to-end.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
 __all__ = ["chunk_fwd", "chunk_fwd_logits", "recurrent_fwd", "recurrent_step", "recurrent_step_logits",
            "gated_rmsnorm", "short_conv", "o_proj", "launch_count", "device_status", "set_wait_limit",
            "workspace_size", "release_workspaces", "prepass_hits",
+           "KVCache", "kv_cache", "rotary_inv_freq", "rotary", "kv_append", "attn_decode", "attn_decode_workspace_size",
            "library_path", "KDAError", "MODE_AUTO", "MODE_TENSOR", "MODE_FP32", "MODE_SPLIT"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -90,6 +97,14 @@ def _load():
         for fn in ("kda_chunk_fwd", "kda_recurrent_fwd", "kda_recurrent_step", "kda_gated_rmsnorm",
                    "kda_short_conv_fwd", "kda_chunk_fwd_logits", "kda_recurrent_step_logits", "kda_o_proj",
                    "kda_recurrent_step_conv", "kda_chunk_fwd_host", "kda_chunk_fwd_logits_host"):
+            getattr(lib, fn).restype = ctypes.c_int
+        L = ctypes.c_int64
+        lib.kda_rotary.argtypes = [P, I, L, P, P, F, I, I, I, P, L, L, I, I, P]
+        lib.kda_kv_append.argtypes = [P, L, P, L, L, I, I, P, P, P, P, I, I, P, I, P, P, I, P, F, I, I, P, L, I, P, P, P]
+        lib.kda_attn_decode.argtypes = [P, L, P, P, P, P, I, I, P, I, P, I, I, I, I, F, P, I, P, P, Z, P]
+        lib.kda_attn_decode_workspace_size.argtypes = [I, I, I]
+        lib.kda_attn_decode_workspace_size.restype = Z
+        for fn in ("kda_rotary", "kda_kv_append", "kda_attn_decode"):
             getattr(lib, fn).restype = ctypes.c_int
         lib.kda_device_status.argtypes = [P]
         lib.kda_device_status.restype = ctypes.c_int
@@ -583,3 +598,263 @@ def o_proj(y, w_o, *, out_dtype=torch.bfloat16, out=None):
     if host:
         return _to_host((res,), True, (dest,))[0]
     return res
+
+
+# ---------------------------------------------------------------------------
+# full attention: rotary positions, the paged 8-bit cache, attention
+
+class KVCache(NamedTuple):
+    """A paged 8-bit key/value cache: codes float8_e4m3fn [pages, kv_heads, page_size, dim], one
+    power-of-two fp32 scale for each (page, head); a value is code * scale."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def kv_cache(num_pages, kv_heads, dim, page_size=64, device=None) -> KVCache:
+    """An empty cache on the device (default: the current CUDA device)."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    shape = (num_pages, kv_heads, page_size, dim)
+    codes = lambda: torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+    scale = lambda: torch.ones(shape[:2], dtype=torch.float32, device=device)
+    return KVCache(codes(), codes(), scale(), scale())
+
+
+def rotary_inv_freq(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, original_max_position=4096, beta_fast=32.0,
+                    beta_slow=1.0, device=None):
+    """(inv_freq, magnitude) for ``rotary`` and ``kv_append``: radians per position of each of the
+    rotary_dim / 2 pairs (float64) and the factor on the rotated channels.
+
+    scaling: None; "linear" (positions divided by ``factor``); "ntk" (the base raised to
+    base * factor^(R / (R - 2)), R = rotary_dim, so that the slowest pair turns ``factor``
+    times slower); "yarn" (a pair that makes at least ``beta_fast`` turns within
+    ``original_max_position`` positions is kept, one that makes at most ``beta_slow`` is divided
+    by ``factor``, those between are blended linearly in their number of turns; magnitude
+    0.1 ln(factor) + 1)."""
+    if rotary_dim <= 0 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and positive")
+    if not factor >= 1.0:
+        raise ValueError("factor must be at least 1")
+    pair = torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim
+    if scaling == "ntk" and rotary_dim > 2:
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    f = base ** -pair
+    magnitude = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if not beta_fast > beta_slow:
+            raise ValueError("yarn needs beta_fast > beta_slow")
+        turns = original_max_position * f / (2 * math.pi)
+        keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+        magnitude = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "none", "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    return f.to(device), magnitude
+
+
+_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def _layout(layout):
+    if layout not in _LAYOUTS:
+        raise ValueError(f'layout must be "half" or "interleaved", not {layout!r}')
+    return _LAYOUTS[layout]
+
+
+class _on:
+    """The tensors' device made current for a call (their stream is then its current one)."""
+
+    def __init__(self, device):
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _want(t, name, dtype, dim, device=None):
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be a tensor on {device or 'a CUDA device'}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, not {t.dim()}")
+    return t
+
+
+def _dense(t, name, dtype, dim, device=None):
+    """A small or in-place argument: used as it lies, so it has to be contiguous."""
+    if not _want(t, name, dtype, dim, device).is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _rows(t, name, dtype, device=None):
+    """[tokens, heads, dim] with dense rows a 16-byte multiple apart (slices of a fused
+    projection are used as they lie, anything else is copied) -> (tensor, row stride)."""
+    _want(t, name, dtype, 3, device)
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if s2 == 1 and (s1 == d or h == 1) and (n <= 1 or s0 >= h * d) and s0 * t.element_size() % 16 == 0 \
+            and t.data_ptr() % 16 == 0:
+        return t, max(s0, h * d)
+    return t.contiguous(), h * d
+
+
+def _check_cache(cache):
+    k, v, ks, vs = cache
+    dev = _dense(k, "cache.k", torch.float8_e4m3fn, 4).device
+    _dense(v, "cache.v", torch.float8_e4m3fn, 4, dev)
+    _dense(ks, "cache.k_scale", torch.float32, 2, dev)
+    _dense(vs, "cache.v_scale", torch.float32, 2, dev)
+    if v.shape != k.shape or ks.shape != k.shape[:2] or vs.shape != ks.shape:
+        raise ValueError("the cache's tensors do not fit together: codes [pages, kv_heads, page_size, dim], "
+                         "scales [pages, kv_heads]")
+    return k, v, ks, vs, dev
+
+
+def rotary(x, positions, inv_freq, *, magnitude=1.0, layout="half", inverse=False, out=None):
+    """Rotary positions: x [T, H, D] (bf16 or fp32) with the first 2 * len(inv_freq) channels of
+    each head turned in pairs by positions[t] * inv_freq[i] and multiplied by ``magnitude``; the
+    others are copied.  positions int32 [T] (angles are reduced exactly, however far);
+    inv_freq float64 (``rotary_inv_freq``).  layout "half": pairs (i, i + R/2), "interleaved":
+    (2i, 2i + 1).  ``inverse`` turns back (the gradient of the call without it).  ``out``:
+    a tensor like x, or x itself.  A host x is copied to the device and the result back."""
+    lib = _load()
+    lay = _layout(layout)
+    host = x.device.type != "cuda"
+    dev = _device_of(x, positions, inv_freq)
+    if x.dim() != 3:
+        raise ValueError("x must be [tokens, heads, dim]")
+    dest, out = (out, None) if host else (None, out)
+    if host:
+        x = _prep(x, dev)
+        positions, inv_freq = _prep(positions, dev), _prep(inv_freq, dev)
+    dt = _dt(x)
+    x, xs = _rows(x, "x", x.dtype)
+    T, H, D = x.shape
+    _dense(positions, "positions", torch.int32, 1, x.device)
+    _dense(inv_freq, "inv_freq", torch.float64, 1, x.device)
+    if positions.shape[0] != T:
+        raise ValueError("positions must have one entry per token")
+    if out is None:
+        out, os_ = torch.empty((T, H, D), dtype=x.dtype, device=x.device), H * D
+    else:
+        if out.shape != x.shape or out.device != x.device:
+            raise ValueError("out must be like x")
+        o, os_ = _rows(out, "out", x.dtype)
+        if o is not out:
+            raise ValueError("out must have dense rows, 16-byte aligned")
+    with _on(x.device):
+        _check(lib.kda_rotary(x.data_ptr(), dt, xs, positions.data_ptr(), inv_freq.data_ptr(), magnitude,
+                              2 * inv_freq.shape[0], lay, int(bool(inverse)), out.data_ptr(), os_, T, H, D, _stream()))
+    return _to_host((out,), True, (dest,))[0] if host else out
+
+
+def kv_append(k, v, cache, block_table, context_lens, *, cu_seqlens=None, inv_freq=None, magnitude=1.0, layout="half",
+              q=None, return_k=False, q_out=None, k_out=None):
+    """Appends new tokens to a paged 8-bit cache (in place) and rotates their keys and queries.
+
+    k, v [T, kv_heads, dim] bf16 and q [T, q_heads, dim] bf16 (optional) may be slices of a fused
+    projection; context_lens int32 [N]: tokens already in the cache; cu_seqlens int32 [N + 1] on
+    the device: which rows belong to which sequence, None for one token per sequence (T = N);
+    block_table int32 [N, max_blocks].  inv_freq None: no rotation; else the position is the
+    token's place in its sequence.  Tokens whose page is negative or out of range are not
+    stored.  Returns (rotated q or None, rotated keys if return_k or k_out is given else None).
+    Every tensor lies on the cache's device."""
+    lib = _load()
+    lay = _layout(layout)
+    ck, cv, ks, vs, dev = _check_cache(cache)
+    pages, Hk, P, D = ck.shape
+    k, k_stride = _rows(k, "k", torch.bfloat16, dev)
+    v, v_stride = _rows(v, "v", torch.bfloat16, dev)
+    T = k.shape[0]
+    if k.shape != (T, Hk, D) or v.shape != k.shape:
+        raise ValueError("k and v must be [tokens, kv_heads, dim] as the cache is")
+    _dense(block_table, "block_table", torch.int32, 2, dev)
+    _dense(context_lens, "context_lens", torch.int32, 1, dev)
+    N, max_blocks = block_table.shape
+    if context_lens.shape[0] != N:
+        raise ValueError("context_lens must have one entry per row of block_table")
+    cu = R = f = q_ptr = qo_ptr = ko_ptr = None
+    if cu_seqlens is not None:
+        cu = _dense(cu_seqlens, "cu_seqlens", torch.int32, 1, dev).data_ptr()
+        if cu_seqlens.shape[0] != N + 1:
+            raise ValueError("cu_seqlens must have one entry more than block_table has rows")
+    if inv_freq is not None:
+        f, R = _dense(inv_freq, "inv_freq", torch.float64, 1, dev).data_ptr(), 2 * inv_freq.shape[0]
+    Hq, q_stride = 0, 0
+    if q is not None:
+        q, q_stride = _rows(q, "q", torch.bfloat16, dev)
+        Hq = q.shape[1]
+        if q.shape != (T, Hq, D):
+            raise ValueError("q must be [tokens, q_heads, dim]")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        elif _dense(q_out, "q_out", torch.bfloat16, 3, dev).shape != q.shape:
+            raise ValueError("q_out must be like q")
+        q_ptr, qo_ptr = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k_out is None and return_k:
+        k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=dev)
+    if k_out is not None:
+        if _dense(k_out, "k_out", torch.bfloat16, 3, dev).shape != k.shape:
+            raise ValueError("k_out must be like k")
+        ko_ptr = k_out.data_ptr()
+    with _on(dev):
+        _check(lib.kda_kv_append(k.data_ptr(), k_stride, v.data_ptr(), v_stride, T, Hk, D, ck.data_ptr(), cv.data_ptr(),
+                                 ks.data_ptr(), vs.data_ptr(), pages, P, block_table.data_ptr(), max_blocks,
+                                 context_lens.data_ptr(), cu, N, f, magnitude, R or 0, lay, q_ptr, q_stride, Hq, qo_ptr,
+                                 ko_ptr, _stream()))
+    return q_out, k_out
+
+
+def attn_decode_workspace_size(q_heads, kv_heads, dim) -> int:
+    """Bytes of workspace one attn_decode call needs."""
+    return int(_load().kda_attn_decode_workspace_size(int(q_heads), int(kv_heads), int(dim)))
+
+
+def attn_decode(q, cache, block_table, seq_lens, *, scale=None, out_dtype=torch.bfloat16, return_lse=False, o=None,
+                workspace=None):
+    """One query token per sequence over the paged 8-bit cache: q [N, q_heads, dim] bf16 (rows may
+    be strided), seq_lens int32 [N] tokens to attend to (the new one included), block_table
+    int32 [N, max_blocks].  scale: default dim^-0.5.  Returns o [N, q_heads, dim] (zero for an
+    empty sequence, NaN where a needed page number is out of range) or, with return_lse,
+    (o, lse [N, q_heads] fp32).  workspace: a uint8 tensor of attn_decode_workspace_size(...)
+    bytes for this call alone, or None: taken from torch's allocator for the call."""
+    lib = _load()
+    ck, cv, ks, vs, dev = _check_cache(cache)
+    pages, Hk, P, D = ck.shape
+    q, q_stride = _rows(q, "q", torch.bfloat16, dev)
+    N, Hq, Dq = q.shape
+    if Dq != D:
+        raise ValueError("q must be [sequences, q_heads, dim] as the cache is")
+    _dense(block_table, "block_table", torch.int32, 2, dev)
+    _dense(seq_lens, "seq_lens", torch.int32, 1, dev)
+    if block_table.shape[0] != N or seq_lens.shape[0] != N:
+        raise ValueError("block_table and seq_lens must have one row per query")
+    if o is None:
+        o = torch.empty((N, Hq, D), dtype=out_dtype, device=dev)
+    elif _dense(o, "o", o.dtype, 3, dev).shape != q.shape:
+        raise ValueError("o must be like q")
+    lse = torch.empty((N, Hq), dtype=torch.float32, device=dev) if return_lse else None
+    with _on(dev):
+        if workspace is None:
+            workspace = torch.empty(lib.kda_attn_decode_workspace_size(Hq, Hk, D), dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
+        _check(lib.kda_attn_decode(q.data_ptr(), q_stride, ck.data_ptr(), cv.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+                                   pages, P, block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), N, Hq,
+                                   Hk, D, D ** -0.5 if scale is None else float(scale), o.data_ptr(), _dt(o),
+                                   None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _stream()))
+    return (o, lse) if return_lse else o

@@ -7,6 +7,7 @@
 #include <cstdio>
 #include <cstring>
 
+#include "kda_attn.cuh"
 #include "kda_internal.cuh"
 
 namespace kda {
@@ -54,6 +55,9 @@ using kda::set_error;
 namespace {
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+// Index arrays, scales and frequencies: their own size (slices of larger arrays are used as they lie).
+bool aligned_to(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
 
 bool dtype_ok(int d) { return d == KDA_BF16 || d == KDA_F32; }
 
@@ -427,6 +431,71 @@ kda_status step_impl(const char *fn, const void *q, const void *k, const void *v
     return kda::launch_recurrent(p, K, V, (cudaStream_t)stream);
 }
 
+// ---------------------------------------------------------------------------
+// full attention
+
+// A tensor of `rows` rows of `row` elements, `stride` elements apart.
+size_t strided_bytes(int64_t rows, int64_t row, int64_t stride, size_t esz) {
+    return rows == 0 ? 0 : ((size_t)(rows - 1) * stride + row) * esz;
+}
+
+kda_status check_stride(const char *fn, const char *name, int64_t stride, int64_t row, size_t esz) {
+    KDA_REQUIRE(stride >= row && stride * (int64_t)esz % 16 == 0, KDA_ERR_INVALID_ARG,
+                "%s: the stride of %s must be at least a row and a multiple of 16 bytes (got %lld elements)", fn, name,
+                (long long)stride);
+    return KDA_OK;
+}
+
+kda_status check_rotary_args(const char *fn, const double *inv_freq, float magnitude, int R, int layout, int dim) {
+    KDA_REQUIRE(layout == KDA_ROTARY_HALF || layout == KDA_ROTARY_INTERLEAVED, KDA_ERR_INVALID_ARG,
+                "%s: unknown rotary layout %d", fn, layout);
+    KDA_REQUIRE(R >= 0 && R <= dim, KDA_ERR_INVALID_ARG, "%s: rotary_dim=%d must lie in [0, dim]", fn, R);
+    KDA_REQUIRE(R % 16 == 0, KDA_ERR_UNSUPPORTED, "%s: rotary_dim=%d must be a multiple of 16", fn, R);
+    KDA_REQUIRE((R > 0) == (inv_freq != nullptr), KDA_ERR_INVALID_ARG,
+                "%s: inv_freq and rotary_dim > 0 come together", fn);
+    KDA_REQUIRE(std::isfinite(magnitude), KDA_ERR_INVALID_ARG, "%s: magnitude must be finite", fn);
+    KDA_REQUIRE(aligned_to(inv_freq, 8), KDA_ERR_INVALID_ARG, "%s: inv_freq must be 8-byte aligned", fn);
+    return KDA_OK;
+}
+
+kda_status check_cache_args(const char *fn, const void *k, const void *v, const float *ks, const float *vs,
+                            int num_pages, int page_size, const int32_t *table, int max_blocks, const int32_t *lens,
+                            int n_seqs, int q_heads, int kv_heads, int dim) {
+    KDA_REQUIRE(kv_heads > 0 && q_heads >= 0 && dim > 0 && n_seqs >= 0 && num_pages > 0 && max_blocks > 0,
+                KDA_ERR_INVALID_ARG, "%s: need positive heads, dim, num_pages and max_blocks", fn);
+    KDA_REQUIRE(dim == 64 || dim == 128, KDA_ERR_UNSUPPORTED, "%s: dim=%d (supported: 64, 128)", fn, dim);
+    KDA_REQUIRE(page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128, KDA_ERR_UNSUPPORTED,
+                "%s: page_size=%d (supported: 16, 32, 64, 128)", fn, page_size);
+    KDA_REQUIRE(k && v && ks && vs, KDA_ERR_INVALID_ARG, "%s: the cache and its scales must not be NULL", fn);
+    KDA_REQUIRE(n_seqs == 0 || (table && lens), KDA_ERR_INVALID_ARG,
+                "%s: block_table and the lengths must not be NULL", fn);
+    KDA_REQUIRE(q_heads % kv_heads == 0, KDA_ERR_INVALID_ARG, "%s: q_heads=%d is not a multiple of kv_heads=%d", fn,
+                q_heads, kv_heads);
+    KDA_REQUIRE(n_seqs <= 65535 && kv_heads <= 65535 && q_heads <= (1 << 20), KDA_ERR_UNSUPPORTED,
+                "%s: at most 65535 sequences and heads", fn);
+    KDA_REQUIRE((int64_t)max_blocks * page_size <= INT32_MAX - 256, KDA_ERR_INVALID_ARG,
+                "%s: max_blocks * page_size must stay below 2^31 - 256", fn);
+    KDA_REQUIRE(aligned16(k) && aligned16(v), KDA_ERR_INVALID_ARG, "%s: the cache must be 16-byte aligned", fn);
+    const void *words[] = {ks, vs, table, lens};
+    for (const void *ptr : words)
+        KDA_REQUIRE(aligned_to(ptr, 4), KDA_ERR_INVALID_ARG, "%s: scales, block_table and lengths must be 4-byte aligned",
+                    fn);
+    return KDA_OK;
+}
+
+// No output shares bytes with an input or with another output.
+kda_status check_apart(const char *fn, const Span *in, int n_in, const Span *out, int n_out) {
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = 0; j < n_in; ++j)
+            KDA_REQUIRE(!overlaps(out[i], in[j]), KDA_ERR_INVALID_ARG, "%s: %s must not overlap %s", fn, out[i].name,
+                        in[j].name);
+        for (int j = i + 1; j < n_out; ++j)
+            KDA_REQUIRE(!overlaps(out[i], out[j]), KDA_ERR_INVALID_ARG, "%s: %s must not overlap %s", fn,
+                        out[i].name, out[j].name);
+    }
+    return KDA_OK;
+}
+
 }  // namespace
 
 namespace kda {
@@ -713,6 +782,163 @@ kda_status kda_o_proj(const void *y, const void *w_o, void *out, kda_dtype out_d
     }
     return kda::launch_o_proj(y, w_o, out, out_dtype == KDA_BF16, rows, in_features, out_features,
                               (cudaStream_t)stream);
+}
+
+kda_status kda_rotary(const void *x, kda_dtype dtype, int64_t x_stride, const int32_t *positions,
+                      const double *inv_freq, float magnitude, int rotary_dim, int layout, int inverse, void *out,
+                      int64_t out_stride, int64_t tokens, int heads, int dim, void *stream) {
+    kda::g_err[0] = 0;
+    const char *fn = "kda_rotary";
+    KDA_REQUIRE(tokens >= 0 && heads > 0 && dim > 0, KDA_ERR_INVALID_ARG, "%s: need tokens >= 0, heads > 0, dim > 0",
+                fn);
+    KDA_REQUIRE(dtype_ok(dtype), KDA_ERR_UNSUPPORTED, "%s: unsupported dtype", fn);
+    KDA_REQUIRE(dim % 8 == 0 && dim <= 256, KDA_ERR_UNSUPPORTED, "%s: dim=%d must be a multiple of 8, at most 256", fn,
+                dim);
+    KDA_REQUIRE(heads <= (1 << 20) && tokens <= INT32_MAX, KDA_ERR_UNSUPPORTED, "%s: too many heads or tokens", fn);
+    KDA_REQUIRE(rotary_dim > 0, KDA_ERR_INVALID_ARG, "%s: rotary_dim must be positive", fn);
+    kda_status s = check_rotary_args(fn, inv_freq, magnitude, rotary_dim, layout, dim);
+    if (s != KDA_OK) return s;
+    KDA_REQUIRE(inverse == 0 || inverse == 1, KDA_ERR_INVALID_ARG, "%s: inverse must be 0 or 1", fn);
+    KDA_REQUIRE(tokens == 0 || (x && out && positions), KDA_ERR_INVALID_ARG,
+                "%s: x, positions and out must not be NULL", fn);
+    const int64_t row = (int64_t)heads * dim;
+    if ((s = check_stride(fn, "x", x_stride, row, esize(dtype))) != KDA_OK) return s;
+    if ((s = check_stride(fn, "out", out_stride, row, esize(dtype))) != KDA_OK) return s;
+    KDA_REQUIRE(aligned16(x) && aligned16(out) && aligned_to(positions, 4), KDA_ERR_INVALID_ARG,
+                "%s: x and out must be 16-byte aligned, positions 4-byte", fn);
+    const Span in[] = {{positions, (size_t)tokens * 4, "positions"},
+                       {inv_freq, (size_t)rotary_dim / 2 * 8, "inv_freq"},
+                       {x == out && x_stride == out_stride ? nullptr : x,
+                        strided_bytes(tokens, row, x_stride, esize(dtype)), "x"}};
+    const Span o[] = {{out, strided_bytes(tokens, row, out_stride, esize(dtype)), "out"}};
+    if ((s = check_apart(fn, in, 3, o, 1)) != KDA_OK) return s;
+    kda::RotaryParams r;
+    r.inv_freq = inv_freq;
+    r.magnitude = magnitude;
+    r.R = rotary_dim;
+    r.interleaved = layout == KDA_ROTARY_INTERLEAVED;
+    r.sign = inverse ? -1.f : 1.f;
+    return kda::launch_rotary(x, dtype == KDA_BF16, x_stride, positions, r, out, out_stride, tokens, heads, dim,
+                              (cudaStream_t)stream);
+}
+
+kda_status kda_kv_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride, int64_t tokens,
+                         int kv_heads, int dim, void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                         int num_pages, int page_size, const int32_t *block_table, int max_blocks,
+                         const int32_t *context_lens, const int32_t *cu_seqlens, int n_seqs, const double *inv_freq,
+                         float magnitude, int rotary_dim, int layout, const void *q, int64_t q_stride, int q_heads,
+                         void *q_out, void *k_out, void *stream) {
+    kda::g_err[0] = 0;
+    const char *fn = "kda_kv_append";
+    kda_status s = check_cache_args(fn, k_cache, v_cache, k_scale, v_scale, num_pages, page_size, block_table,
+                                    max_blocks, context_lens, n_seqs, q ? q_heads : kv_heads, kv_heads, dim);
+    if (s != KDA_OK) return s;
+    if ((s = check_rotary_args(fn, inv_freq, magnitude, rotary_dim, layout, dim)) != KDA_OK) return s;
+    KDA_REQUIRE(tokens >= 0 && tokens <= INT32_MAX, KDA_ERR_INVALID_ARG, "%s: need 0 <= tokens < 2^31", fn);
+    KDA_REQUIRE(tokens == 0 || (k && v), KDA_ERR_INVALID_ARG, "%s: k and v must not be NULL", fn);
+    KDA_REQUIRE((q != nullptr) == (q_out != nullptr), KDA_ERR_INVALID_ARG, "%s: q and q_out come together", fn);
+    KDA_REQUIRE(!q || q_heads > 0, KDA_ERR_INVALID_ARG, "%s: q needs q_heads > 0", fn);
+    KDA_REQUIRE(tokens == 0 || n_seqs > 0, KDA_ERR_INVALID_ARG, "%s: tokens without sequences", fn);
+    KDA_REQUIRE(cu_seqlens || tokens == n_seqs, KDA_ERR_INVALID_ARG,
+                "%s: without cu_seqlens there is one token per sequence (tokens=%lld, n_seqs=%d)", fn, (long long)tokens,
+                n_seqs);
+    const int64_t kr = (int64_t)kv_heads * dim, qr = (int64_t)q_heads * dim;
+    if ((s = check_stride(fn, "k", k_stride, kr, 2)) != KDA_OK) return s;
+    if ((s = check_stride(fn, "v", v_stride, kr, 2)) != KDA_OK) return s;
+    if (q && (s = check_stride(fn, "q", q_stride, qr, 2)) != KDA_OK) return s;
+    const void *ptrs[] = {k, v, q, q_out, k_out};
+    for (const void *ptr : ptrs)
+        KDA_REQUIRE(aligned16(ptr), KDA_ERR_INVALID_ARG, "%s: k, v, q, q_out and k_out must be 16-byte aligned", fn);
+    KDA_REQUIRE(aligned_to(cu_seqlens, 4), KDA_ERR_INVALID_ARG, "%s: cu_seqlens must be 4-byte aligned", fn);
+    const size_t blocks = (size_t)num_pages * kv_heads, codes = blocks * page_size * dim;
+    const Span in[] = {{k, strided_bytes(tokens, kr, k_stride, 2), "k"},
+                       {v, strided_bytes(tokens, kr, v_stride, 2), "v"},
+                       {q, q ? strided_bytes(tokens, qr, q_stride, 2) : 0, "q"},
+                       {block_table, (size_t)n_seqs * max_blocks * 4, "block_table"},
+                       {context_lens, (size_t)n_seqs * 4, "context_lens"},
+                       {cu_seqlens, ((size_t)n_seqs + 1) * 4, "cu_seqlens"},
+                       {inv_freq, (size_t)rotary_dim / 2 * 8, "inv_freq"}};
+    const Span out[] = {{k_cache, codes, "k_cache"},
+                        {v_cache, codes, "v_cache"},
+                        {k_scale, blocks * 4, "k_scale"},
+                        {v_scale, blocks * 4, "v_scale"},
+                        {q_out, q_out ? (size_t)tokens * qr * 2 : 0, "q_out"},
+                        {k_out, (size_t)tokens * kr * 2, "k_out"}};
+    if ((s = check_apart(fn, in, 7, out, 6)) != KDA_OK) return s;
+    kda::AppendParams p;
+    p.c = kda::PagedCache{static_cast<uint8_t *>(k_cache), static_cast<uint8_t *>(v_cache), k_scale, v_scale,
+                          block_table, context_lens, num_pages, max_blocks, kv_heads, page_size, dim, n_seqs};
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.v = static_cast<const __nv_bfloat16 *>(v);
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.cu_seqlens = cu_seqlens;
+    p.tokens = tokens;
+    p.rot = kda::RotaryParams{inv_freq, magnitude, rotary_dim, layout == KDA_ROTARY_INTERLEAVED, 1.f};
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.q_stride = q_stride;
+    p.Hq = q ? q_heads : 0;
+    p.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    p.k_out = static_cast<__nv_bfloat16 *>(k_out);
+    return kda::launch_kv_append(p, (cudaStream_t)stream);
+}
+
+size_t kda_attn_decode_workspace_size(int q_heads, int kv_heads, int dim) {
+    if (q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads != 0 || (dim != 64 && dim != 128)) return 0;
+    return kda::attn_decode_workspace_bytes(q_heads, kv_heads, dim);
+}
+
+kda_status kda_attn_decode(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                           const float *k_scale, const float *v_scale, int num_pages, int page_size,
+                           const int32_t *block_table, int max_blocks, const int32_t *seq_lens, int n_seqs,
+                           int q_heads, int kv_heads, int dim, float scale, void *o, kda_dtype o_dtype, float *lse,
+                           void *workspace, size_t workspace_bytes, void *stream) {
+    kda::g_err[0] = 0;
+    const char *fn = "kda_attn_decode";
+    KDA_REQUIRE(q_heads > 0, KDA_ERR_INVALID_ARG, "%s: need q_heads > 0", fn);
+    kda_status s = check_cache_args(fn, k_cache, v_cache, k_scale, v_scale, num_pages, page_size, block_table,
+                                    max_blocks, seq_lens, n_seqs, q_heads, kv_heads, dim);
+    if (s != KDA_OK) return s;
+    KDA_REQUIRE(dtype_ok(o_dtype), KDA_ERR_UNSUPPORTED, "%s: unsupported dtype", fn);
+    KDA_REQUIRE(std::isfinite(scale), KDA_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+    KDA_REQUIRE(n_seqs == 0 || (q && o), KDA_ERR_INVALID_ARG, "%s: q and o must not be NULL", fn);
+    const int64_t row = (int64_t)q_heads * dim;
+    if ((s = check_stride(fn, "q", q_stride, row, 2)) != KDA_OK) return s;
+    const void *ptrs[] = {q, o, workspace};
+    for (const void *ptr : ptrs)
+        KDA_REQUIRE(aligned16(ptr), KDA_ERR_INVALID_ARG, "%s: q, o and the workspace must be 16-byte aligned", fn);
+    KDA_REQUIRE(aligned_to(lse, 4), KDA_ERR_INVALID_ARG, "%s: lse must be 4-byte aligned", fn);
+    if (n_seqs == 0) return KDA_OK;
+    const size_t need = kda::attn_decode_workspace_bytes(q_heads, kv_heads, dim);
+    KDA_REQUIRE(workspace && workspace_bytes >= need, KDA_ERR_INVALID_ARG,
+                "%s: the workspace holds %zu bytes, this call needs %zu (kda_attn_decode_workspace_size)", fn,
+                workspace ? workspace_bytes : (size_t)0, need);
+    const size_t blocks = (size_t)num_pages * kv_heads, codes = blocks * page_size * dim;
+    const Span in[] = {{q, strided_bytes(n_seqs, row, q_stride, 2), "q"},
+                       {k_cache, codes, "k_cache"},
+                       {v_cache, codes, "v_cache"},
+                       {k_scale, blocks * 4, "k_scale"},
+                       {v_scale, blocks * 4, "v_scale"},
+                       {block_table, (size_t)n_seqs * max_blocks * 4, "block_table"},
+                       {seq_lens, (size_t)n_seqs * 4, "seq_lens"}};
+    const Span out[] = {{o, (size_t)n_seqs * row * esize(o_dtype), "o"},
+                        {lse, (size_t)n_seqs * q_heads * 4, "lse"},
+                        {workspace, need, "the workspace"}};
+    if ((s = check_apart(fn, in, 7, out, 3)) != KDA_OK) return s;
+    kda::DecodeParams p;
+    p.c = kda::PagedCache{static_cast<uint8_t *>(const_cast<void *>(k_cache)),
+                          static_cast<uint8_t *>(const_cast<void *>(v_cache)), const_cast<float *>(k_scale),
+                          const_cast<float *>(v_scale), block_table, seq_lens, num_pages, max_blocks, kv_heads,
+                          page_size, dim, n_seqs};
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.q_stride = q_stride;
+    p.Hq = q_heads;
+    p.scale = scale;
+    p.o = o;
+    p.o_bf16 = o_dtype == KDA_BF16;
+    p.lse = lse;
+    p.ws = static_cast<float *>(workspace);
+    return kda::launch_attn_decode(p, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,291 @@
+// kda_attn.cuh -- definitions shared by the full-attention operators: the position
+// rotation (kda_rotary.cu), the paged 8-bit key/value cache and its append
+// (kda_kv_append.cu), single-token attention over it (kda_attn_decode.cu) and the prompt's
+// attention (kda_attn_prompt.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+// ---------------------------------------------------------------------------
+// parameter blocks
+
+struct RotaryParams {
+    const double *inv_freq;  // [R / 2] radians per position, or null: no rotation
+    float magnitude;         // factor on the rotated channels
+    int R;                   // rotated channels: the first R of a head
+    int interleaved;         // pairs (2i, 2i + 1); else (i, i + R / 2)
+    float sign;              // -1: the transposed rotation
+};
+
+struct PagedCache {
+    uint8_t *k, *v;               // e4m3 codes [pages, Hk, P, D]
+    float *k_scale, *v_scale;     // [pages, Hk]
+    const int32_t *block_table;   // [N, max_blocks]
+    const int32_t *lens;          // [N] tokens in the cache
+    int n_pages, max_blocks, Hk, P, D, N;
+};
+
+struct AppendParams {
+    PagedCache c;                 // lens: tokens before this call
+    const __nv_bfloat16 *k, *v;   // rows of Hk * D, k_stride / v_stride elements apart
+    int64_t k_stride, v_stride;
+    const int32_t *cu_seqlens;    // [N + 1] or null: one token per sequence
+    int64_t tokens;
+    RotaryParams rot;
+    const __nv_bfloat16 *q;       // rows of Hq * D, or null
+    int64_t q_stride;
+    int Hq;
+    __nv_bfloat16 *q_out, *k_out; // dense [tokens, Hq, D] / [tokens, Hk, D]; k_out may be null
+};
+
+struct DecodeParams {
+    PagedCache c;                 // lens: tokens in the cache
+    const __nv_bfloat16 *q;       // rows of Hq * D, q_stride elements apart
+    int64_t q_stride;
+    int Hq;
+    float scale;
+    void *o;                      // [N, Hq, D]
+    int o_bf16;
+    float *lse;                   // [N, Hq] or null
+    float *ws;                    // partial results
+};
+
+struct PromptParams {
+    const __nv_bfloat16 *q, *k, *v;  // rows of Hq * D, Hk * D, Hk * DV
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *cu_q, *cu_k;      // [N + 1]
+    int64_t Tq, Tk;
+    int N, Hq, Hk, D, DV;
+    float scale;
+    void *o;                         // [Tq, Hq, DV]
+    int o_bf16;
+    float *lse;                      // [Tq, Hq] or null
+};
+
+kda_status launch_rotary(const void *x, int bf16, int64_t x_stride, const int32_t *positions, const RotaryParams &r,
+                         void *out, int64_t out_stride, int64_t T, int H, int D, cudaStream_t st);
+kda_status launch_kv_append(const AppendParams &p, cudaStream_t st);
+size_t attn_decode_workspace_bytes(int Hq, int Hk, int D);
+kda_status launch_attn_decode(const DecodeParams &p, cudaStream_t st);
+kda_status launch_attn_prompt(const PromptParams &p, cudaStream_t st);
+int take_attn_prompt_timeouts(cudaStream_t st);
+
+// ---------------------------------------------------------------------------
+// angles
+
+// One pair's turn per position as a 64-bit binary fraction of a full turn.  The fraction of
+// position p is then the integer product p * turn modulo 2^64, exact for any position: the
+// reduction to one turn is the integers' own wrap-around.  The double keeps 53 bits of the
+// turn, so a position of 2^20 is off by at most 2^-33 turns.
+__device__ __forceinline__ uint64_t turn_of(double inv_freq) {
+    double t = inv_freq * 0.15915494309189535;  // 1 / (2 pi)
+    t -= floor(t);
+    return (uint64_t)(t * 18446744073709551616.0);
+}
+
+// cos and sin of 2 pi * f / 2^64.  f is split into the nearest quarter turn and a rest of at
+// most 1/8 turn, held as an integer, so the rest's fp32 value is good to half an ulp however
+// small it is; on it (|a| <= pi/4) the Taylor series through a^10 and a^9 leave 1e-9.
+__device__ __forceinline__ void cos_sin_turn(uint64_t f, float &c, float &s) {
+    const uint32_t quarter = (uint32_t)((f + (1ull << 61)) >> 62);
+    const int64_t rest = (int64_t)(f - ((uint64_t)quarter << 62));
+    const float a = (float)rest * 3.4061215800304545e-19f;  // 2 pi / 2^64
+    const float a2 = a * a;
+    float pc = -1.f / 3628800.f;
+    pc = fmaf(pc, a2, 1.f / 40320.f);
+    pc = fmaf(pc, a2, -1.f / 720.f);
+    pc = fmaf(pc, a2, 1.f / 24.f);
+    pc = fmaf(pc, a2, -0.5f);
+    pc = fmaf(pc, a2, 1.f);
+    float ps = 1.f / 362880.f;
+    ps = fmaf(ps, a2, -1.f / 5040.f);
+    ps = fmaf(ps, a2, 1.f / 120.f);
+    ps = fmaf(ps, a2, -1.f / 6.f);
+    ps = fmaf(ps * a2, a, a);
+    const float x = (quarter & 1) ? ps : pc, y = (quarter & 1) ? pc : ps;
+    c = (quarter == 1 || quarter == 2) ? -x : x;
+    s = (quarter & 2) ? -y : y;
+}
+
+// a * b - c * d with the product's rounding error carried (two extra FMAs): within 1.5 ulp,
+// so an 8-bit code chosen from it rarely differs from the exact value's.
+__device__ __forceinline__ float diff_of_products(float a, float b, float c, float d) {
+    const float w = c * d;
+    const float e = fmaf(-c, d, w);
+    return fmaf(a, b, -w) + e;
+}
+
+// The pair (a, b) turned: (a cos - b sin, b cos + a sin).
+__device__ __forceinline__ void turn_pair(float a, float b, float2 cs, float &x, float &y) {
+    x = diff_of_products(a, cs.x, b, cs.y);
+    y = diff_of_products(b, cs.x, -a, cs.y);
+}
+
+// ---------------------------------------------------------------------------
+// 16-byte vectors of the two storage types as fp32
+
+template <typename T>
+struct Vec16;
+template <>
+struct Vec16<__nv_bfloat16> {
+    static constexpr int N = 8;
+    __device__ static void load(const uint4 &w, float (&x)[8]) {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(u[i] << 16);
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        }
+    }
+    __device__ static uint4 store(const float (&x)[8]) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+};
+template <>
+struct Vec16<float> {
+    static constexpr int N = 4;
+    __device__ static void load(const uint4 &w, float (&x)[4]) {
+        x[0] = __uint_as_float(w.x);
+        x[1] = __uint_as_float(w.y);
+        x[2] = __uint_as_float(w.z);
+        x[3] = __uint_as_float(w.w);
+    }
+    __device__ static uint4 store(const float (&x)[4]) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
+};
+
+// cos / sin (times the magnitude and the sign) of `n` tokens' pairs into cs[token][pair]: a
+// thread keeps to one pair, so its turn is formed once (the doubles are slow here).
+template <typename PosFn>
+__device__ __forceinline__ void fill_cos_sin(float2 *cs, const RotaryParams &r, int n, PosFn pos, int tid, int threads) {
+    const int np = r.R >> 1;
+    if (np == 0) return;
+    const int rows = threads / np, j = tid % np, row = tid / np;
+    if (row >= rows) return;
+    const uint64_t turn = turn_of(__ldg(r.inv_freq + j));
+    for (int t = row; t < n; t += rows) {
+        float c, s;
+        cos_sin_turn((uint64_t)(int64_t)pos(t) * turn, c, s);
+        cs[t * np + j] = make_float2(c * r.magnitude, s * r.magnitude * r.sign);
+    }
+}
+
+// Work units of one head: in the half layout a unit is two 16-byte vectors R / 2 channels
+// apart, in the interleaved layout one vector; each vector behind the rotated part is one.
+__host__ __device__ __forceinline__ int rotary_units(int D, int R, int interleaved, int vec) {
+    return (interleaved ? R / vec : R / (2 * vec)) + (D - R) / vec;
+}
+
+// Unit u of one head: x -> y.
+template <typename T>
+__device__ __forceinline__ void rotate_unit(const T *x, T *y, const float2 *cs, int u, int R, int interleaved) {
+    using V = Vec16<T>;
+    constexpr int N = V::N;
+    const int nrot = interleaved ? R / N : R / (2 * N);
+    if (u >= nrot) {
+        const int c = R + (u - nrot) * N;
+        *reinterpret_cast<uint4 *>(y + c) = *reinterpret_cast<const uint4 *>(x + c);
+        return;
+    }
+    float a[N];
+    if (interleaved) {
+        V::load(*reinterpret_cast<const uint4 *>(x + u * N), a);
+        float o[N];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) turn_pair(a[2 * i], a[2 * i + 1], cs[u * (N / 2) + i], o[2 * i], o[2 * i + 1]);
+        *reinterpret_cast<uint4 *>(y + u * N) = V::store(o);
+    } else {
+        float b[N], oa[N], ob[N];
+        const uint4 wa = *reinterpret_cast<const uint4 *>(x + u * N);
+        const uint4 wb = *reinterpret_cast<const uint4 *>(x + u * N + R / 2);
+        V::load(wa, a);
+        V::load(wb, b);
+#pragma unroll
+        for (int i = 0; i < N; ++i) turn_pair(a[i], b[i], cs[u * N + i], oa[i], ob[i]);
+        *reinterpret_cast<uint4 *>(y + u * N) = V::store(oa);
+        *reinterpret_cast<uint4 *>(y + u * N + R / 2) = V::store(ob);
+    }
+}
+
+// Rows of `n` tokens (token t at x + t * xs, y + t * ys, H heads of D) with cs filled.
+template <typename T>
+__device__ __forceinline__ void rotate_rows(const T *x, int64_t xs, T *y, int64_t ys, const float2 *cs,
+                                            const RotaryParams &r, int n, int H, int D, int tid, int threads) {
+    const int U = rotary_units(D, r.R, r.interleaved, Vec16<T>::N), per = H * U, np = r.R >> 1;
+    for (int i = tid; i < n * per; i += threads) {
+        const int t = i / per, rem = i - t * per, h = rem / U, u = rem - h * U;
+        rotate_unit<T>(x + t * xs + (int64_t)h * D, y + t * ys + (int64_t)h * D, cs + t * np, u, r.R, r.interleaved);
+    }
+}
+
+// Tokens a CTA of `threads` rotates at once: about four 16-byte vectors a thread, at most
+// what `room` cos / sin pairs of shared memory hold.
+__host__ __device__ __forceinline__ int rotary_tile_tokens(int H, int D, int R, int vec, int threads, int room) {
+    int n = threads * 4 * vec / (H * D);
+    if (R > 0 && n > room / (R / 2)) n = room / (R / 2);
+    return n < 1 ? 1 : n;
+}
+
+// ---------------------------------------------------------------------------
+// e4m3
+
+constexpr float kE4m3Max = 448.f;
+constexpr int kScaleExpLo = -100, kScaleExpHi = 100;
+
+// Two values as e4m3 codes, round to nearest even.  The block's scale keeps finite values
+// within 448; an infinity becomes NaN (the type has none), as does a NaN.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+    if (isinf(a)) a = __int_as_float(0x7fc00000);
+    if (isinf(b)) b = __int_as_float(0x7fc00000);
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
+
+// The smallest exponent e with amax <= 448 * 2^e, within the limits (448 = 1.75 * 2^8).
+__device__ __forceinline__ int scale_exp(float amax) {
+    const uint32_t b = __float_as_uint(amax);
+    const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return amax > 0.f ? max(kScaleExpLo, min(kScaleExpHi, e)) : kScaleExpLo;
+}
+
+__device__ __forceinline__ int exp_of_scale(float s) {
+    return max(kScaleExpLo, min(kScaleExpHi, (int)((__float_as_uint(s) >> 23) & 0xFFu) - 127));
+}
+
+// 4 codes multiplied by 2^d (d <= 0) and rounded to codes again.
+__device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float f) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3);
+        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        r |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x.x * f, x.y * f), __NV_SATFINITE, __NV_E4M3) << (16 * i);
+    }
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ float finite_abs(float x) {
+    const float a = fabsf(x);
+    return a <= 3.4028234663852886e38f ? a : 0.f;  // a NaN compares false
+}
+
+}  // namespace kda

@@ -1,0 +1,373 @@
+// kda_kv_append.cu -- appends keys and values to a paged 8-bit cache, with the keys (and the
+// step's queries) rotated on the way.
+//
+// The cache holds e4m3 codes [pages, Hk, P, D] and one scale for each (page, head).  Scales
+// are powers of two, 2^e with the smallest e that keeps the block's values within 448:
+//   - e4m3 is a floating type, so a finer scale would add no precision, only range;
+//   - when a later token of a part-filled page is larger, the page's earlier codes move to
+//     the new scale by an exact exponent shift (only codes that become subnormal are
+//     rounded again), so the order in which tokens arrive hardly matters.
+// A page whose first token is written here is taken as empty: its old scale is not read.
+//
+// Memory bound.  The tokens of one call that fall into one page are a run; one CTA takes a
+// run and some of the heads, holds the (rotated) values in registers between the pass that
+// finds each head's largest value and the pass that writes codes, so everything is read
+// once.  One token per sequence (a decode step) has a warp for each (sequence, head).
+// Queries are rotated by further CTAs of the same launch.
+#include "kda_attn.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRoom = 1024;  // cos / sin pairs of a query tile
+
+struct Grid {
+    int q_tile;     // tokens of a query CTA
+    int n_kv;       // CTAs of the keys and values; the query CTAs follow
+    int heads;      // heads of a run's CTA
+    int head_parts; // CTAs that share a run's heads
+};
+
+// Tokens of sequence n in this call, clamped to the tensors.
+__device__ __forceinline__ void new_tokens(const AppendParams &p, int n, int64_t &t0, int &len) {
+    int64_t a = p.cu_seqlens[n], b = p.cu_seqlens[n + 1];
+    a = max((int64_t)0, min(a, p.tokens));
+    b = max(a, min(b, p.tokens));
+    t0 = a;
+    len = (int)(b - a);
+}
+
+// Pages that the new tokens of sequence n touch.
+__device__ __forceinline__ int runs_of(const AppendParams &p, int n) {
+    int64_t t0;
+    int len;
+    new_tokens(p, n, t0, len);
+    const int ctx = max(p.c.lens[n], 0);
+    return len > 0 ? (int)(((int64_t)ctx + len - 1) / p.c.P - ctx / p.c.P) + 1 : 0;
+}
+
+// Position of token t (-> its angle), by bisection of cu_seqlens.
+__device__ __forceinline__ int position_of(const AppendParams &p, int64_t t) {
+    if (!p.cu_seqlens) return max(p.c.lens[t], 0);
+    int lo = 0, hi = p.c.N - 1;  // the last sequence that starts at or before t
+    while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (p.cu_seqlens[m] <= t)
+            lo = m;
+        else
+            hi = m - 1;
+    }
+    return max(p.c.lens[lo], 0) + (int)(t - p.cu_seqlens[lo]);
+}
+
+// One query tile.
+__device__ __forceinline__ void rotate_queries(const AppendParams &p, int tile, int q_tile, float2 *cs, int *pos) {
+    const int64_t t0 = (int64_t)tile * q_tile;
+    const int n = (int)min((int64_t)q_tile, p.tokens - t0), tid = threadIdx.x;
+    for (int t = tid; t < n; t += kThreads) pos[t] = position_of(p, t0 + t);
+    __syncthreads();
+    fill_cos_sin(cs, p.rot, n, [&](int t) { return pos[t]; }, tid, kThreads);
+    __syncthreads();
+    const int64_t row = (int64_t)p.Hq * p.c.D;
+    rotate_rows<__nv_bfloat16>(p.q + t0 * p.q_stride, p.q_stride, p.q_out + t0 * row, row, cs, p.rot, n, p.Hq, p.c.D, tid,
+                               kThreads);
+}
+
+// Channels [8v, 8v + 8) of one head's row x, rotated with cs (null: as they are).
+__device__ __forceinline__ void load_rotated(const __nv_bfloat16 *x, int v, const float2 *cs, const RotaryParams &r,
+                                             float (&y)[8]) {
+    using V = Vec16<__nv_bfloat16>;
+    V::load(*reinterpret_cast<const uint4 *>(x + v * 8), y);
+    const int c0 = v * 8;
+    if (!cs || c0 >= r.R) return;
+    if (r.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = y[2 * i], b = y[2 * i + 1];
+            turn_pair(a, b, cs[v * 4 + i], y[2 * i], y[2 * i + 1]);
+        }
+    } else {
+        const int half = r.R >> 1;
+        const bool second = c0 >= half;
+        const int partner = second ? c0 - half : c0 + half, j = second ? partner : c0;
+        float z[8];
+        V::load(*reinterpret_cast<const uint4 *>(x + partner), z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            y[i] = diff_of_products(y[i], cs[j + i].x, second ? -z[i] : z[i], cs[j + i].y);
+    }
+}
+
+// The scale's exponent of a block whose new values reach amax; off: tokens it already holds.
+__device__ __forceinline__ int block_exp(float amax, int off, int old) {
+    const int need = scale_exp(amax);
+    return off > 0 ? max(need, old) : need;
+}
+
+// ---------------------------------------------------------------------------
+// runs (any number of tokens per sequence)
+
+template <int ITERS>
+__global__ void __launch_bounds__(kThreads) append_run_kernel(const __grid_constant__ AppendParams p,
+                                                              const __grid_constant__ Grid g) {
+    extern __shared__ float2 cs[];
+    __shared__ int s_pos[kRoom];
+    __shared__ int s_seq, s_run;
+    __shared__ int s_scan[kWarps];
+    __shared__ float s_max[2][kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if ((int)blockIdx.x >= g.n_kv) {
+        rotate_queries(p, blockIdx.x - g.n_kv, g.q_tile, cs, s_pos);
+        return;
+    }
+    const int P = p.c.P, D = p.c.D, nv = D >> 3;
+    const int values = blockIdx.x & 1, part = (blockIdx.x >> 1) % g.head_parts, unit = (blockIdx.x >> 1) / g.head_parts;
+    // the unit-th run over all sequences
+    if (tid == 0) s_seq = -1;
+    __syncthreads();
+    int before = 0;
+    for (int n0 = 0; n0 < p.c.N; n0 += kThreads) {
+        const int n = n0 + tid;
+        const int r = n < p.c.N ? runs_of(p, n) : 0;
+        int x = r;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) s_scan[warp] = x;
+        __syncthreads();
+        int base = before, total = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) base += s_scan[w];
+            total += s_scan[w];
+        }
+        const int first = base + x - r;
+        if (r > 0 && unit >= first && unit < first + r) {
+            s_seq = n;
+            s_run = unit - first;
+        }
+        before += total;
+        __syncthreads();
+        if (before > unit) break;
+    }
+    const int seq = s_seq;
+    if (seq < 0) return;
+    int64_t t0;
+    int len;
+    new_tokens(p, seq, t0, len);
+    const int ctx = max(p.c.lens[seq], 0), block = ctx / P + s_run;
+    const int64_t pos0 = max((int64_t)block * P, (int64_t)ctx);
+    const int off = (int)(pos0 - (int64_t)block * P);  // tokens the page holds already
+    t0 += pos0 - ctx;
+    const int n = min(P - off, len - (int)(pos0 - ctx));
+    int page = block < p.c.max_blocks ? p.c.block_table[(int64_t)seq * p.c.max_blocks + block] : -1;
+    if (page >= p.c.n_pages) page = -1;  // no such page: the tokens are dropped (their rotated copies are not)
+
+    const __nv_bfloat16 *src = (values ? p.v : p.k) + t0 * (values ? p.v_stride : p.k_stride);
+    const int64_t stride = values ? p.v_stride : p.k_stride;
+    uint8_t *codes = values ? p.c.v : p.c.k;
+    float *scales = values ? p.c.v_scale : p.c.k_scale;
+    const bool turned = !values && p.rot.R > 0;
+    if (turned) {
+        fill_cos_sin(cs, p.rot, n, [&](int t) { return (int)(pos0 + t); }, tid, kThreads);
+        __syncthreads();
+    }
+    const int h0 = part * g.heads, h1 = min(h0 + g.heads, p.c.Hk), np = p.rot.R >> 1;
+    for (int h = h0; h < h1; ++h) {
+        float y[ITERS][8];
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < ITERS; ++i) {
+            const int x = tid + i * kThreads, t = x / nv, v = x - t * nv;
+            if (t < n) {
+                load_rotated(src + t * stride + h * D, v, turned ? cs + t * np : nullptr, p.rot, y[i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(y[i][e]));
+                if (!values && p.k_out)
+                    *reinterpret_cast<uint4 *>(p.k_out + ((t0 + t) * p.c.Hk + h) * D + v * 8) =
+                        Vec16<__nv_bfloat16>::store(y[i]);
+            }
+        }
+        if (page < 0) continue;
+        amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+        if (lane == 0) s_max[h & 1][warp] = amax;
+        const int64_t blk = (int64_t)page * p.c.Hk + h;
+        const int old = exp_of_scale(scales[blk]);
+        __syncthreads();  // also: every thread has read the old scale
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, s_max[h & 1][w]);
+        const int e = block_exp(amax, off, old);
+        uint8_t *dst = codes + blk * P * D;
+        if (off > 0 && e > old) {
+            const float f = exp2_int(max(old - e, -126));
+            uint32_t *w = reinterpret_cast<uint32_t *>(dst);
+            for (int i = tid; i < off * D / 4; i += kThreads) w[i] = rescale_codes(w[i], f);
+        }
+        if (tid == 0) scales[blk] = exp2_int(e);
+        const float inv = exp2_int(-e);
+#pragma unroll
+        for (int i = 0; i < ITERS; ++i) {
+            const int x = tid + i * kThreads, t = x / nv, v = x - t * nv;
+            if (t < n) {
+                uint2 w;
+                w.x = e4m3x2(y[i][0] * inv, y[i][1] * inv) | e4m3x2(y[i][2] * inv, y[i][3] * inv) << 16;
+                w.y = e4m3x2(y[i][4] * inv, y[i][5] * inv) | e4m3x2(y[i][6] * inv, y[i][7] * inv) << 16;
+                *reinterpret_cast<uint2 *>(dst + (int64_t)(off + t) * D + v * 8) = w;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// one token per sequence: a warp for each (sequence, head, keys or values)
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) append_step_kernel(const __grid_constant__ AppendParams p,
+                                                               const __grid_constant__ Grid g) {
+    constexpr int C = D / 32;  // channels of a lane
+    __shared__ float2 cs[kRoom];
+    __shared__ int s_pos[kRoom];
+    if ((int)blockIdx.x >= g.n_kv) {
+        rotate_queries(p, blockIdx.x - g.n_kv, g.q_tile, cs, s_pos);
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (item >= (int64_t)p.c.N * p.c.Hk * 2) return;
+    const int values = (int)(item & 1), h = (int)((item >> 1) % p.c.Hk), seq = (int)((item >> 1) / p.c.Hk);
+    const __nv_bfloat16 *x = values ? p.v + seq * p.v_stride + h * D : p.k + seq * p.k_stride + h * D;
+    const int c0 = lane * C, R = p.rot.R, half = R >> 1;
+    // the token's row and the place it goes to do not depend on each other: both loads are in flight
+    float own[C], other[C];
+    const bool turned = !values && c0 < R;
+    const bool second = turned && !p.rot.interleaved && c0 >= half;
+    const int partner = !turned || p.rot.interleaved ? c0 : second ? c0 - half : c0 + half;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        own[i] = __bfloat162float(x[c0 + i]);
+        other[i] = __bfloat162float(x[partner + i]);
+    }
+    const int ctx = max(p.c.lens[seq], 0), block = ctx / p.c.P, off = ctx - block * p.c.P;
+    int page = block < p.c.max_blocks ? p.c.block_table[(int64_t)seq * p.c.max_blocks + block] : -1;
+    if (page >= p.c.n_pages) page = -1;
+    float y[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) y[i] = own[i];
+    if (turned) {
+        if (p.rot.interleaved) {
+#pragma unroll
+            for (int i = 0; i < C / 2; ++i) {
+                float c, s;
+                cos_sin_turn((uint64_t)(int64_t)ctx * turn_of(__ldg(p.rot.inv_freq + c0 / 2 + i)), c, s);
+                turn_pair(own[2 * i], own[2 * i + 1], make_float2(c * p.rot.magnitude, s * p.rot.magnitude), y[2 * i],
+                          y[2 * i + 1]);
+            }
+        } else {
+            const int j0 = second ? partner : c0;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                float c, s;
+                cos_sin_turn((uint64_t)(int64_t)ctx * turn_of(__ldg(p.rot.inv_freq + j0 + i)), c, s);
+                y[i] = diff_of_products(own[i], c * p.rot.magnitude, second ? -other[i] : other[i], s * p.rot.magnitude);
+            }
+        }
+    }
+    if (!values && p.k_out) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) p.k_out[((int64_t)seq * p.c.Hk + h) * D + c0 + i] = __float2bfloat16_rn(y[i]);
+    }
+    if (page < 0) return;
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) amax = fmaxf(amax, finite_abs(y[i]));
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+    const int64_t blk = (int64_t)page * p.c.Hk + h;
+    float *scales = values ? p.c.v_scale : p.c.k_scale;
+    uint8_t *dst = (values ? p.c.v : p.c.k) + blk * p.c.P * D;
+    const int old = exp_of_scale(scales[blk]), e = block_exp(amax, off, old);
+    if (off > 0 && e > old) {
+        const float f = exp2_int(max(old - e, -126));
+        uint4 *w = reinterpret_cast<uint4 *>(dst);
+        for (int i = lane; i < off * D / 16; i += 32) {
+            uint4 u = w[i];
+            u.x = rescale_codes(u.x, f);
+            u.y = rescale_codes(u.y, f);
+            u.z = rescale_codes(u.z, f);
+            u.w = rescale_codes(u.w, f);
+            w[i] = u;
+        }
+    }
+    __syncwarp();  // every lane has read the old scale
+    if (lane == 0) scales[blk] = exp2_int(e);
+    const float inv = exp2_int(-e);
+#pragma unroll
+    for (int i = 0; i < C; i += 2)
+        *reinterpret_cast<uint16_t *>(dst + (int64_t)off * D + c0 + i) = (uint16_t)e4m3x2(y[i] * inv, y[i + 1] * inv);
+}
+
+template <int ITERS>
+kda_status run(const AppendParams &p, const Grid &g, unsigned grid, size_t smem, cudaStream_t st) {
+    if (smem > 32 * 1024) {
+        static DeviceOnce configured;
+        const int dev = current_device();
+        if (!configured.done(dev)) {
+            if (cudaFuncSetAttribute(append_run_kernel<ITERS>, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024) !=
+                cudaSuccess) {
+                set_error("kv_append: cannot reserve shared memory: %s", cudaGetErrorString(cudaGetLastError()));
+                return KDA_ERR_CUDA;
+            }
+            configured.set(dev);
+        }
+    }
+    append_run_kernel<ITERS><<<grid, kThreads, smem, st>>>(p, g);
+    note_launch();
+    return check_launch("append_run_kernel");
+}
+
+}  // namespace
+
+kda_status launch_kv_append(const AppendParams &p, cudaStream_t st) {
+    if (p.tokens == 0) return KDA_OK;
+    Grid g;
+    g.q_tile = p.q ? rotary_tile_tokens(p.Hq, p.c.D, p.rot.R, 8, kThreads, kRoom) : 1;
+    if (g.q_tile > kRoom) g.q_tile = kRoom;
+    const int64_t q_ctas = p.q ? (p.tokens + g.q_tile - 1) / g.q_tile : 0;
+    if (!p.cu_seqlens) {
+        const int64_t kv = ((int64_t)p.c.N * p.c.Hk * 2 + kWarps - 1) / kWarps;
+        g.n_kv = (int)kv;
+        g.heads = g.head_parts = 1;
+        const unsigned grid = (unsigned)(kv + q_ctas);
+        if (p.c.D == 128)
+            append_step_kernel<128><<<grid, kThreads, 0, st>>>(p, g);
+        else
+            append_step_kernel<64><<<grid, kThreads, 0, st>>>(p, g);
+        note_launch();
+        return check_launch("append_step_kernel");
+    }
+    // A sequence's n new tokens lie in at most n / P + 2 pages.
+    const int64_t runs = p.tokens / p.c.P + 2 * (int64_t)p.c.N;
+    // A CTA takes all heads of its run, so that cos and sin are formed once, unless the GPU
+    // would be left with fewer than four CTAs per SM.
+    g.heads = p.c.Hk;
+    while (g.heads > 1 && runs * 2 * ((p.c.Hk + g.heads - 1) / g.heads) < 4ll * sm_count()) g.heads = (g.heads + 1) / 2;
+    g.head_parts = (p.c.Hk + g.heads - 1) / g.heads;
+    const int64_t kv = runs * 2 * g.head_parts;
+    if (kv + q_ctas > INT32_MAX) {
+        set_error("kda_kv_append: too many tokens");
+        return KDA_ERR_UNSUPPORTED;
+    }
+    g.n_kv = (int)kv;
+    size_t smem = (size_t)p.c.P * p.rot.R / 2 * sizeof(float2);
+    if (p.q && smem < kRoom * sizeof(float2)) smem = kRoom * sizeof(float2);
+    const int vecs = p.c.P * p.c.D / 8;
+    const unsigned grid = (unsigned)(kv + q_ctas);
+    if (vecs <= kThreads) return run<1>(p, g, grid, smem, st);
+    if (vecs <= 2 * kThreads) return run<2>(p, g, grid, smem, st);
+    if (vecs <= 4 * kThreads) return run<4>(p, g, grid, smem, st);
+    return run<8>(p, g, grid, smem, st);
+}
+
+}  // namespace kda
