@@ -577,6 +577,33 @@ kda_status kda_attn_decode(const void *q, int64_t q_stride, const void *k_cache,
                            int q_heads, int kv_heads, int dim, float scale, void *o, kda_dtype o_dtype, float *lse,
                            void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * kda_attn_prompt -- causal attention over whole prompts, on the tensor cores.
+ *
+ *     o[i] = sum_{j < seen_i} softmax_j(scale * q_i . k_j) v_j,   seen_i = i + 1 + (keys - queries),
+ * for every query row i of a sequence; query head h reads key/value head
+ * h / (q_heads / kv_heads).  A sequence with more keys than queries continues a context whose
+ * rows come first; a row that sees nothing (more queries than keys) gives zero and lse
+ * -INFINITY.
+ *
+ *   q   [q_rows, q_heads, dim], k [k_rows, kv_heads, dim], v [k_rows, kv_heads, dim_v], bf16,
+ *       q_stride / k_stride / v_stride apart
+ *   o   [q_rows, q_heads, dim_v] o_dtype         lse [q_rows, q_heads] float or NULL:
+ *       log(sum_j e^(scale q_i . k_j))
+ *   cu_seqlens   [n_seqs + 1] int32: sequence n's queries are rows
+ *       [cu_seqlens[n], cu_seqlens[n + 1]) (clamped to [0, q_rows]); rows of no sequence are
+ *       left as they are.  NULL: n_seqs sequences of q_rows / n_seqs rows each.
+ *   cu_seqlens_k [n_seqs + 1] int32: the same for the keys.  NULL: as cu_seqlens where that is
+ *       given (k_rows == q_rows), else n_seqs sequences of k_rows / n_seqs rows.
+ * (dim, dim_v) one of (64, 64), (128, 128), (192, 128) (KDA_ERR_UNSUPPORTED otherwise); q_heads a
+ * multiple of kv_heads; scale finite and not 0.  Nothing a row does not see enters its result,
+ * be it infinite or NaN.  The weights are rounded to bf16 for the product with v.
+ */
+kda_status kda_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                           int64_t v_stride, int64_t q_rows, int64_t k_rows, int q_heads, int kv_heads, int dim,
+                           int dim_v, const int32_t *cu_seqlens, const int32_t *cu_seqlens_k, int n_seqs, float scale,
+                           void *o, kda_dtype o_dtype, float *lse, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

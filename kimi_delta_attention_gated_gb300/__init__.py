@@ -14,6 +14,7 @@ The full-attention layers beside the KDA layers:
   rotary          rotary positions (rotary_inv_freq: the angles, scaled for long contexts)
   kv_append       keys and values into a paged 8-bit cache (kv_cache), rotated on the way
   attn_decode     one query token per sequence over that cache
+  attn_prompt     causal attention over whole (packed) prompts
 
 Inputs may live on the host: they are copied to the current CUDA device, and the
 results are copied back to the host, which makes the call end-to-end.
@@ -32,6 +33,7 @@ __all__ = ["chunk_fwd", "chunk_fwd_logits", "recurrent_fwd", "recurrent_step", "
            "gated_rmsnorm", "short_conv", "o_proj", "launch_count", "device_status", "set_wait_limit",
            "workspace_size", "release_workspaces", "prepass_hits",
            "KVCache", "kv_cache", "rotary_inv_freq", "rotary", "kv_append", "attn_decode", "attn_decode_workspace_size",
+           "attn_prompt",
            "library_path", "KDAError", "MODE_AUTO", "MODE_TENSOR", "MODE_FP32", "MODE_SPLIT"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -104,7 +106,8 @@ def _load():
         lib.kda_attn_decode.argtypes = [P, L, P, P, P, P, I, I, P, I, P, I, I, I, I, F, P, I, P, P, Z, P]
         lib.kda_attn_decode_workspace_size.argtypes = [I, I, I]
         lib.kda_attn_decode_workspace_size.restype = Z
-        for fn in ("kda_rotary", "kda_kv_append", "kda_attn_decode"):
+        lib.kda_attn_prompt.argtypes = [P, L, P, L, P, L, L, L, I, I, I, I, P, P, I, F, P, I, P, P]
+        for fn in ("kda_rotary", "kda_kv_append", "kda_attn_decode", "kda_attn_prompt"):
             getattr(lib, fn).restype = ctypes.c_int
         lib.kda_device_status.argtypes = [P]
         lib.kda_device_status.restype = ctypes.c_int
@@ -665,60 +668,75 @@ def _layout(layout):
     return _LAYOUTS[layout]
 
 
-class _on:
-    """The tensors' device made current for a call (their stream is then its current one)."""
-
-    def __init__(self, device):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+# The current device and a device's current stream without torch.cuda's lazy-initialisation
+# and type checks, which cost more than a small kernel runs.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _want(t, name, dtype, dim, device=None):
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or (device is not None and t.device != device):
-        raise ValueError(f"{name} must be a tensor on {device or 'a CUDA device'}")
+def _call(fn, index, *args):
+    """One library call on device `index` and its current stream."""
+    if index == _current_device():
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status != 0:
+        _check(status)
+
+
+def _refuse(t, name, dtype, dim, index):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or (index is not None and t.get_device() != index):
+        raise ValueError(f"{name} must be a tensor on {'a CUDA device' if index is None else f'cuda:{index}'}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.dim() != dim:
         raise ValueError(f"{name} must have {dim} dimensions, not {t.dim()}")
-    return t
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _dense(t, name, dtype, dim, device=None):
-    """A small or in-place argument: used as it lies, so it has to be contiguous."""
-    if not _want(t, name, dtype, dim, device).is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+def _dense(t, name, dtype, dim, index):
+    """A small or in-place argument on device `index`: used as it lies, so it has to be
+    contiguous -> its address."""
+    try:
+        if t.dtype is dtype and t.get_device() == index and t.dim() == dim and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, dim, index)
 
 
-def _rows(t, name, dtype, device=None):
-    """[tokens, heads, dim] with dense rows a 16-byte multiple apart (slices of a fused
-    projection are used as they lie, anything else is copied) -> (tensor, row stride)."""
-    _want(t, name, dtype, 3, device)
+def _rows(t, name, dtype, index):
+    """[tokens, heads, dim] on device `index` with dense rows a 16-byte multiple apart (slices of a
+    fused projection are used as they lie, anything else is copied) -> (tensor, address, stride)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index or t.dim() != 3 or index < 0:
+        _refuse(t, name, dtype, 3, index if index >= 0 else None)
     n, h, d = t.shape
-    s0, s1, s2 = t.stride()
-    if s2 == 1 and (s1 == d or h == 1) and (n <= 1 or s0 >= h * d) and s0 * t.element_size() % 16 == 0 \
-            and t.data_ptr() % 16 == 0:
-        return t, max(s0, h * d)
-    return t.contiguous(), h * d
+    row, at = h * d, t.data_ptr()
+    if at % 16 == 0:
+        if t.is_contiguous():
+            return t, at, row
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and (s1 == d or h == 1) and (s0 >= row or n == 1) and s0 * t.element_size() % 16 == 0:
+            return t, at, max(s0, row)
+    t = t.clone(memory_format=torch.contiguous_format)
+    return t, t.data_ptr(), row
 
 
-def _check_cache(cache):
+def _cache_args(cache):
+    """(device index, kv_heads, page_size, dim, (k, v, k_scale, v_scale, pages, page_size))."""
     k, v, ks, vs = cache
-    dev = _dense(k, "cache.k", torch.float8_e4m3fn, 4).device
-    _dense(v, "cache.v", torch.float8_e4m3fn, 4, dev)
-    _dense(ks, "cache.k_scale", torch.float32, 2, dev)
-    _dense(vs, "cache.v_scale", torch.float32, 2, dev)
-    if v.shape != k.shape or ks.shape != k.shape[:2] or vs.shape != ks.shape:
+    index = k.get_device()
+    if index < 0:
+        raise ValueError("the cache must lie on a CUDA device")
+    ptrs = (_dense(k, "cache.k", torch.float8_e4m3fn, 4, index), _dense(v, "cache.v", torch.float8_e4m3fn, 4, index),
+            _dense(ks, "cache.k_scale", torch.float32, 2, index), _dense(vs, "cache.v_scale", torch.float32, 2, index))
+    shape = k.shape
+    pages, Hk, P, D = shape
+    if v.shape != shape or ks.shape != (pages, Hk) or vs.shape != (pages, Hk):
         raise ValueError("the cache's tensors do not fit together: codes [pages, kv_heads, page_size, dim], "
                          "scales [pages, kv_heads]")
-    return k, v, ks, vs, dev
+    return index, Hk, P, D, (*ptrs, pages, P)
 
 
 def rotary(x, positions, inv_freq, *, magnitude=1.0, layout="half", inverse=False, out=None):
@@ -728,35 +746,30 @@ def rotary(x, positions, inv_freq, *, magnitude=1.0, layout="half", inverse=Fals
     inv_freq float64 (``rotary_inv_freq``).  layout "half": pairs (i, i + R/2), "interleaved":
     (2i, 2i + 1).  ``inverse`` turns back (the gradient of the call without it).  ``out``:
     a tensor like x, or x itself.  A host x is copied to the device and the result back."""
-    lib = _load()
+    lib = _lib or _load()
     lay = _layout(layout)
-    host = x.device.type != "cuda"
-    dev = _device_of(x, positions, inv_freq)
-    if x.dim() != 3:
-        raise ValueError("x must be [tokens, heads, dim]")
-    dest, out = (out, None) if host else (None, out)
-    if host:
-        x = _prep(x, dev)
-        positions, inv_freq = _prep(positions, dev), _prep(inv_freq, dev)
-    dt = _dt(x)
-    x, xs = _rows(x, "x", x.dtype)
+    if not x.is_cuda:
+        dev = _device_of(positions, inv_freq)
+        y = rotary(_prep(x, dev), _prep(positions, dev), _prep(inv_freq, dev), magnitude=magnitude, layout=layout,
+                   inverse=inverse)
+        return _to_host((y,), True, (out,))[0]
+    index = x.get_device()
+    x, xp, xs = _rows(x, "x", torch.bfloat16 if x.dtype is torch.bfloat16 else torch.float32, index)
     T, H, D = x.shape
-    _dense(positions, "positions", torch.int32, 1, x.device)
-    _dense(inv_freq, "inv_freq", torch.float64, 1, x.device)
+    pos = _dense(positions, "positions", torch.int32, 1, index)
+    freq = _dense(inv_freq, "inv_freq", torch.float64, 1, index)
     if positions.shape[0] != T:
         raise ValueError("positions must have one entry per token")
     if out is None:
-        out, os_ = torch.empty((T, H, D), dtype=x.dtype, device=x.device), H * D
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        op, os_ = out.data_ptr(), H * D
     else:
-        if out.shape != x.shape or out.device != x.device:
-            raise ValueError("out must be like x")
-        o, os_ = _rows(out, "out", x.dtype)
-        if o is not out:
-            raise ValueError("out must have dense rows, 16-byte aligned")
-    with _on(x.device):
-        _check(lib.kda_rotary(x.data_ptr(), dt, xs, positions.data_ptr(), inv_freq.data_ptr(), magnitude,
-                              2 * inv_freq.shape[0], lay, int(bool(inverse)), out.data_ptr(), os_, T, H, D, _stream()))
-    return _to_host((out,), True, (dest,))[0] if host else out
+        o, op, os_ = _rows(out, "out", x.dtype, index)
+        if o is not out or out.shape != x.shape:
+            raise ValueError("out must be like x, with dense rows, 16-byte aligned")
+    _call(lib.kda_rotary, index, xp, _dt(x), xs, pos, freq, magnitude, 2 * inv_freq.shape[0], lay, 1 if inverse else 0,
+          op, os_, T, H, D)
+    return out
 
 
 def kv_append(k, v, cache, block_table, context_lens, *, cu_seqlens=None, inv_freq=None, magnitude=1.0, layout="half",
@@ -770,51 +783,48 @@ def kv_append(k, v, cache, block_table, context_lens, *, cu_seqlens=None, inv_fr
     token's place in its sequence.  Tokens whose page is negative or out of range are not
     stored.  Returns (rotated q or None, rotated keys if return_k or k_out is given else None).
     Every tensor lies on the cache's device."""
-    lib = _load()
+    lib = _lib or _load()
     lay = _layout(layout)
-    ck, cv, ks, vs, dev = _check_cache(cache)
-    pages, Hk, P, D = ck.shape
-    k, k_stride = _rows(k, "k", torch.bfloat16, dev)
-    v, v_stride = _rows(v, "v", torch.bfloat16, dev)
-    T = k.shape[0]
-    if k.shape != (T, Hk, D) or v.shape != k.shape:
+    index, Hk, P, D, cache_args = _cache_args(cache)
+    k, kp, k_stride = _rows(k, "k", torch.bfloat16, index)
+    v, vp, v_stride = _rows(v, "v", torch.bfloat16, index)
+    T, kh, kd = shape = k.shape
+    if kh != Hk or kd != D or v.shape != shape:
         raise ValueError("k and v must be [tokens, kv_heads, dim] as the cache is")
-    _dense(block_table, "block_table", torch.int32, 2, dev)
-    _dense(context_lens, "context_lens", torch.int32, 1, dev)
+    table = _dense(block_table, "block_table", torch.int32, 2, index)
+    ctx = _dense(context_lens, "context_lens", torch.int32, 1, index)
     N, max_blocks = block_table.shape
     if context_lens.shape[0] != N:
         raise ValueError("context_lens must have one entry per row of block_table")
-    cu = R = f = q_ptr = qo_ptr = ko_ptr = None
+    cu = freq = qp = qo = ko = None
+    R = Hq = q_stride = 0
     if cu_seqlens is not None:
-        cu = _dense(cu_seqlens, "cu_seqlens", torch.int32, 1, dev).data_ptr()
+        cu = _dense(cu_seqlens, "cu_seqlens", torch.int32, 1, index)
         if cu_seqlens.shape[0] != N + 1:
             raise ValueError("cu_seqlens must have one entry more than block_table has rows")
     if inv_freq is not None:
-        f, R = _dense(inv_freq, "inv_freq", torch.float64, 1, dev).data_ptr(), 2 * inv_freq.shape[0]
-    Hq, q_stride = 0, 0
+        freq, R = _dense(inv_freq, "inv_freq", torch.float64, 1, index), 2 * inv_freq.shape[0]
     if q is not None:
-        q, q_stride = _rows(q, "q", torch.bfloat16, dev)
-        Hq = q.shape[1]
-        if q.shape != (T, Hq, D):
+        q, qp, q_stride = _rows(q, "q", torch.bfloat16, index)
+        tq, Hq, dq = q.shape
+        if tq != T or dq != D:
             raise ValueError("q must be [tokens, q_heads, dim]")
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-        elif _dense(q_out, "q_out", torch.bfloat16, 3, dev).shape != q.shape:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        qo = _dense(q_out, "q_out", torch.bfloat16, 3, index)
+        if q_out.shape != q.shape:
             raise ValueError("q_out must be like q")
-        q_ptr, qo_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     if k_out is None and return_k:
-        k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=dev)
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
     if k_out is not None:
-        if _dense(k_out, "k_out", torch.bfloat16, 3, dev).shape != k.shape:
+        ko = _dense(k_out, "k_out", torch.bfloat16, 3, index)
+        if k_out.shape != shape:
             raise ValueError("k_out must be like k")
-        ko_ptr = k_out.data_ptr()
-    with _on(dev):
-        _check(lib.kda_kv_append(k.data_ptr(), k_stride, v.data_ptr(), v_stride, T, Hk, D, ck.data_ptr(), cv.data_ptr(),
-                                 ks.data_ptr(), vs.data_ptr(), pages, P, block_table.data_ptr(), max_blocks,
-                                 context_lens.data_ptr(), cu, N, f, magnitude, R or 0, lay, q_ptr, q_stride, Hq, qo_ptr,
-                                 ko_ptr, _stream()))
+    cp = cache_args
+    _call(lib.kda_kv_append, index, kp, k_stride, vp, v_stride, T, Hk, D, cp[0], cp[1], cp[2], cp[3], cp[4], P, table,
+          max_blocks, ctx, cu, N, freq, magnitude, R, lay, qp, q_stride, Hq, qo, ko)
     return q_out, k_out
 
 
@@ -831,30 +841,86 @@ def attn_decode(q, cache, block_table, seq_lens, *, scale=None, out_dtype=torch.
     empty sequence, NaN where a needed page number is out of range) or, with return_lse,
     (o, lse [N, q_heads] fp32).  workspace: a uint8 tensor of attn_decode_workspace_size(...)
     bytes for this call alone, or None: taken from torch's allocator for the call."""
-    lib = _load()
-    ck, cv, ks, vs, dev = _check_cache(cache)
-    pages, Hk, P, D = ck.shape
-    q, q_stride = _rows(q, "q", torch.bfloat16, dev)
+    lib = _lib or _load()
+    index, Hk, P, D, cache_args = _cache_args(cache)
+    q, qp, q_stride = _rows(q, "q", torch.bfloat16, index)
     N, Hq, Dq = q.shape
     if Dq != D:
         raise ValueError("q must be [sequences, q_heads, dim] as the cache is")
-    _dense(block_table, "block_table", torch.int32, 2, dev)
-    _dense(seq_lens, "seq_lens", torch.int32, 1, dev)
-    if block_table.shape[0] != N or seq_lens.shape[0] != N:
+    table = _dense(block_table, "block_table", torch.int32, 2, index)
+    lens = _dense(seq_lens, "seq_lens", torch.int32, 1, index)
+    rows, max_blocks = block_table.shape
+    if rows != N or seq_lens.shape[0] != N:
         raise ValueError("block_table and seq_lens must have one row per query")
     if o is None:
-        o = torch.empty((N, Hq, D), dtype=out_dtype, device=dev)
-    elif _dense(o, "o", o.dtype, 3, dev).shape != q.shape:
+        o = torch.empty((N, Hq, D), dtype=out_dtype, device=q.device)
+    elif o.shape != q.shape:
         raise ValueError("o must be like q")
-    lse = torch.empty((N, Hq), dtype=torch.float32, device=dev) if return_lse else None
-    with _on(dev):
-        if workspace is None:
-            workspace = torch.empty(lib.kda_attn_decode_workspace_size(Hq, Hk, D), dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
+    lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+    if workspace is None:
+        need = lib.kda_attn_decode_workspace_size(Hq, Hk, D)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    else:
+        need = workspace.numel() * workspace.element_size()
+        if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
-        _check(lib.kda_attn_decode(q.data_ptr(), q_stride, ck.data_ptr(), cv.data_ptr(), ks.data_ptr(), vs.data_ptr(),
-                                   pages, P, block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), N, Hq,
-                                   Hk, D, D ** -0.5 if scale is None else float(scale), o.data_ptr(), _dt(o),
-                                   None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), _stream()))
+    _call(lib.kda_attn_decode, index, qp, q_stride, *cache_args, table, max_blocks, lens, N, Hq, Hk, D,
+          D ** -0.5 if scale is None else float(scale), _dense(o, "o", o.dtype, 3, index), _dt(o),
+          None if lse is None else lse.data_ptr(), workspace.data_ptr(), need)
+    return (o, lse) if return_lse else o
+
+
+def attn_prompt(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, scale=None, out_dtype=torch.bfloat16, return_lse=False,
+                o=None):
+    """Causal attention over whole prompts: q [T, q_heads, D], k [S, kv_heads, D],
+    v [S, kv_heads, DV] bf16 (rows may be strided), (D, DV) one of (64, 64), (128, 128),
+    (192, 128); query head h reads key/value head h // (q_heads // kv_heads).
+
+    Packed sequences: cu_seqlens int32 [N + 1] on the device gives the queries' rows,
+    cu_seqlens_k the keys' (None: the same); without both there is one sequence, or, with
+    q [B, T, ..], k and v [B, S, ..], B of equal lengths.  Query i of a sequence sees its first
+    i + 1 + (keys - queries) keys: more keys than queries continue a context, and a row that
+    sees nothing is zero.  scale: default D^-0.5.  Returns o like q with DV channels or, with
+    return_lse, (o, lse) with lse the fp32 log-sum-exp of each row's scores.  Host tensors are
+    copied to the device and the results back."""
+    lib = _lib or _load()
+    if not q.is_cuda:
+        dev = _device_of(k, v, cu_seqlens, cu_seqlens_k)
+        r = attn_prompt(*(_prep(t, dev) for t in (q, k, v)), cu_seqlens=_prep(cu_seqlens, dev),
+                        cu_seqlens_k=_prep(cu_seqlens_k, dev), scale=scale, out_dtype=out_dtype, return_lse=return_lse)
+        r = _to_host(r if return_lse else (r,), True, (o, None))
+        return r if return_lse else r[0]
+    index, lead, N = q.get_device(), None, 1
+    if q.dim() == 4:
+        if cu_seqlens is not None or cu_seqlens_k is not None:
+            raise ValueError("packed sequences take q, k and v of three dimensions")
+        if k.dim() != 4 or v.dim() != 4 or k.shape[0] != q.shape[0] or v.shape[0] != q.shape[0]:
+            raise ValueError("q, k and v must have the same batch")
+        lead, N = q.shape[:2], q.shape[0]
+        q, k, v = q.flatten(0, 1), k.flatten(0, 1), v.flatten(0, 1)
+    q, qp, qs = _rows(q, "q", torch.bfloat16, index)
+    k, kp, ks = _rows(k, "k", torch.bfloat16, index)
+    v, vp, vs = _rows(v, "v", torch.bfloat16, index)
+    T, Hq, D = q.shape
+    S, Hk, Dk = k.shape
+    Sv, Hv, DV = v.shape
+    if Dk != D or Hv != Hk or Sv != S:
+        raise ValueError("k must be [keys, kv_heads, D] with q's D, v [keys, kv_heads, DV]")
+    cu = cuk = None
+    if cu_seqlens is not None:
+        cu = _dense(cu_seqlens, "cu_seqlens", torch.int32, 1, index)
+        N = cu_seqlens.shape[0] - 1
+    if cu_seqlens_k is not None:
+        cuk = _dense(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1, index)
+        if cu is None or cu_seqlens_k.shape[0] != N + 1:
+            raise ValueError("cu_seqlens_k must come with a cu_seqlens of the same length")
+    shape = (T, Hq, DV) if lead is None else (*lead, Hq, DV)
+    if o is None:
+        o = torch.empty(shape, dtype=out_dtype, device=q.device)
+    elif o.shape != shape:
+        raise ValueError("o must be like q with v's channels")
+    lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device) if return_lse else None
+    _call(lib.kda_attn_prompt, index, qp, qs, kp, ks, vp, vs, T, S, Hq, Hk, D, DV, cu, cuk, N,
+          D ** -0.5 if scale is None else float(scale), _dense(o, "o", o.dtype, len(shape), index), _dt(o),
+          None if lse is None else lse.data_ptr())
     return (o, lse) if return_lse else o

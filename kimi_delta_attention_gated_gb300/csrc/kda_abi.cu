@@ -556,12 +556,14 @@ kda_status kda_device_status(void *stream) {
     const int n_dec = kda::take_decode_timeouts(st);
     const int n_conv = kda::take_short_conv_timeouts(st);
     const int n_proj = kda::take_oproj_timeouts(st);
-    if (n_tc0 < 0 || n_prep < 0 || n_chain < 0 || n_dec < 0 || n_conv < 0 || n_proj < 0) return KDA_ERR_CUDA;
+    const int n_attn = kda::take_attn_prompt_timeouts(st);
+    if (n_tc0 < 0 || n_prep < 0 || n_chain < 0 || n_dec < 0 || n_conv < 0 || n_proj < 0 || n_attn < 0)
+        return KDA_ERR_CUDA;
     const int n_tc = n_tc0 + n_prep + n_chain;
-    if (n_tc + n_dec + n_conv + n_proj > 0) {
-        set_error("kda_device_status: bounded waits gave up in %d prefill, %d decode, %d short-convolution and %d "
-                  "output-projection CTAs; their outputs hold NaN",
-                  n_tc, n_dec, n_conv, n_proj);
+    if (n_tc + n_dec + n_conv + n_proj + n_attn > 0) {
+        set_error("kda_device_status: bounded waits gave up in %d prefill, %d decode, %d short-convolution, %d "
+                  "output-projection and %d prompt-attention CTAs; their outputs hold NaN",
+                  n_tc, n_dec, n_conv, n_proj, n_attn);
         return KDA_ERR_TIMEOUT;
     }
     return KDA_OK;
@@ -939,6 +941,75 @@ kda_status kda_attn_decode(const void *q, int64_t q_stride, const void *k_cache,
     p.lse = lse;
     p.ws = static_cast<float *>(workspace);
     return kda::launch_attn_decode(p, (cudaStream_t)stream);
+}
+
+kda_status kda_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                           int64_t v_stride, int64_t q_rows, int64_t k_rows, int q_heads, int kv_heads, int dim,
+                           int dim_v, const int32_t *cu_seqlens, const int32_t *cu_seqlens_k, int n_seqs, float scale,
+                           void *o, kda_dtype o_dtype, float *lse, void *stream) {
+    kda::g_err[0] = 0;
+    const char *fn = "kda_attn_prompt";
+    KDA_REQUIRE(q_rows >= 0 && k_rows >= 0 && q_heads > 0 && kv_heads > 0 && n_seqs >= 0, KDA_ERR_INVALID_ARG,
+                "%s: need rows >= 0, heads > 0, n_seqs >= 0", fn);
+    KDA_REQUIRE((dim == 64 && dim_v == 64) || (dim == 128 && dim_v == 128) || (dim == 192 && dim_v == 128),
+                KDA_ERR_UNSUPPORTED, "%s: dim=%d dim_v=%d (supported: 64/64, 128/128, 192/128)", fn, dim, dim_v);
+    KDA_REQUIRE(q_heads % kv_heads == 0, KDA_ERR_INVALID_ARG, "%s: q_heads=%d is not a multiple of kv_heads=%d", fn,
+                q_heads, kv_heads);
+    KDA_REQUIRE(q_rows <= (1 << 30) && k_rows <= (1 << 30) && q_heads <= 65535, KDA_ERR_UNSUPPORTED,
+                "%s: at most 2^30 rows and 65535 heads", fn);
+    KDA_REQUIRE(dtype_ok(o_dtype), KDA_ERR_UNSUPPORTED, "%s: unsupported dtype", fn);
+    KDA_REQUIRE(std::isfinite(scale) && scale != 0.f, KDA_ERR_INVALID_ARG, "%s: scale must be finite and not 0", fn);
+    KDA_REQUIRE(q_rows == 0 || (q && o), KDA_ERR_INVALID_ARG, "%s: q and o must not be NULL", fn);
+    KDA_REQUIRE(k_rows == 0 || (k && v), KDA_ERR_INVALID_ARG, "%s: k and v must not be NULL", fn);
+    KDA_REQUIRE(q_rows == 0 || n_seqs > 0, KDA_ERR_INVALID_ARG, "%s: rows without sequences", fn);
+    if (!cu_seqlens) {
+        KDA_REQUIRE(!cu_seqlens_k, KDA_ERR_INVALID_ARG, "%s: cu_seqlens_k without cu_seqlens", fn);
+        KDA_REQUIRE(n_seqs == 0 || (q_rows % n_seqs == 0 && k_rows % n_seqs == 0), KDA_ERR_INVALID_ARG,
+                    "%s: without cu_seqlens the rows must divide into n_seqs equal sequences", fn);
+    } else {
+        KDA_REQUIRE(cu_seqlens_k || q_rows == k_rows, KDA_ERR_INVALID_ARG,
+                    "%s: without cu_seqlens_k there are as many keys as queries", fn);
+    }
+    const int64_t qr = (int64_t)q_heads * dim, kr = (int64_t)kv_heads * dim, vr = (int64_t)kv_heads * dim_v,
+                  orow = (int64_t)q_heads * dim_v;
+    kda_status s;
+    if ((s = check_stride(fn, "q", q_stride, qr, 2)) != KDA_OK) return s;
+    if ((s = check_stride(fn, "k", k_stride, kr, 2)) != KDA_OK) return s;
+    if ((s = check_stride(fn, "v", v_stride, vr, 2)) != KDA_OK) return s;
+    const void *ptrs[] = {q, k, v, o};
+    for (const void *ptr : ptrs)
+        KDA_REQUIRE(aligned16(ptr), KDA_ERR_INVALID_ARG, "%s: q, k, v and o must be 16-byte aligned", fn);
+    KDA_REQUIRE(aligned_to(lse, 4) && aligned_to(cu_seqlens, 4) && aligned_to(cu_seqlens_k, 4), KDA_ERR_INVALID_ARG,
+                "%s: lse and cu_seqlens must be 4-byte aligned", fn);
+    const size_t cu_bytes = ((size_t)n_seqs + 1) * 4;
+    const Span in[] = {{q, strided_bytes(q_rows, qr, q_stride, 2), "q"},
+                       {k, strided_bytes(k_rows, kr, k_stride, 2), "k"},
+                       {v, strided_bytes(k_rows, vr, v_stride, 2), "v"},
+                       {cu_seqlens, cu_bytes, "cu_seqlens"},
+                       {cu_seqlens_k, cu_bytes, "cu_seqlens_k"}};
+    const Span out[] = {{o, (size_t)q_rows * orow * esize(o_dtype), "o"}, {lse, (size_t)q_rows * q_heads * 4, "lse"}};
+    if ((s = check_apart(fn, in, 5, out, 2)) != KDA_OK) return s;
+    kda::PromptParams p;
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.v = static_cast<const __nv_bfloat16 *>(v);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.cu_q = cu_seqlens;
+    p.cu_k = cu_seqlens_k ? cu_seqlens_k : cu_seqlens;
+    p.Tq = q_rows;
+    p.Tk = k_rows;
+    p.N = n_seqs;
+    p.Hq = q_heads;
+    p.Hk = kv_heads;
+    p.D = dim;
+    p.DV = dim_v;
+    p.scale = scale;
+    p.o = o;
+    p.o_bf16 = o_dtype == KDA_BF16;
+    p.lse = lse;
+    return kda::launch_attn_prompt(p, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -59,7 +59,7 @@ struct DecodeParams {
 struct PromptParams {
     const __nv_bfloat16 *q, *k, *v;  // rows of Hq * D, Hk * D, Hk * DV
     int64_t q_stride, k_stride, v_stride;
-    const int32_t *cu_q, *cu_k;      // [N + 1]
+    const int32_t *cu_q, *cu_k;      // [N + 1], or null: N sequences of equal lengths
     int64_t Tq, Tk;
     int N, Hq, Hk, D, DV;
     float scale;

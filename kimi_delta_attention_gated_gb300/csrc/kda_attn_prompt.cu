@@ -1,0 +1,611 @@
+// kda_attn_prompt.cu -- causal attention over whole prompts, packed sequences of different
+// lengths, grouped heads; on the tensor cores.
+//
+//   o_i = sum_{j < seen_i} softmax_j(scale * q_i . k_j) v_j,   seen_i = i + 1 + (keys - queries)
+//
+// Flash form: key blocks of 128 tokens pass by, and each row keeps a reference m, the sum l
+// of 2^(s - m) and the weighted sum O of the values (s the scores in units of log2).  m is the
+// row's maximum when it was last set; it is set anew (and l, O brought to it) only when a
+// block's maximum exceeds it by more than 8, so that the weights stay below 2^8 and O is
+// rarely touched; the result does not depend on which m was used.
+//
+// A CTA takes two query tiles of 128 rows: two heads of one key/value head where the group
+// is even (both read the same keys), else 256 consecutive rows of one head.
+//   warps 0-3, 4-7  softmax of tile 0 / 1, a thread per row: scores from TMEM, weights
+//                   rounded to bf16 back into TMEM over the scores, O rescaled in TMEM
+//   warp 8          issues the products: S_t = Q_t K^T (both operands in shared memory) and
+//                   O_t += P_t V (P from TMEM), alternating the tiles, so that one tile's
+//                   softmax runs beside the other's products
+//   warp 9          TMA: the two query tiles once, then rings of key and value blocks
+// TMEM: S_0, S_1 (P over them), O_0, O_1, 128 columns each.
+//
+// Weights are rounded to bf16 because the product takes one type and the values are bf16;
+// l sums the unrounded weights in fp32.
+//
+// What is masked never reaches a result: masked scores are replaced, not added to; value
+// rows behind the sequence's end are zeroed in shared memory (a zero weight would turn an
+// infinity there into NaN); a row that comes out NaN is looked at again, and where a value
+// of a later token of its own block caused it, it is computed alone (rescue_row).
+#include <cuda.h>
+#include <string.h>
+
+#include "kda_attn.cuh"
+#include "kda_chunk_common.cuh"
+#include "kda_tc_ptx.cuh"
+
+namespace kda {
+namespace {
+
+using namespace tc;
+using chunk::sdesc_at;
+
+constexpr int kTile = 128;             // query rows of a tile, and keys of a block
+constexpr int kMmaWarp = 8, kTmaWarp = 9;
+constexpr int kThreads = 320;
+constexpr uint32_t kPolls = 1u << 26;
+constexpr float kSlack = 8.f;          // log2: how far a block's maximum may exceed the reference
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ int g_attn_prompt_timeouts = 0;
+
+template <int D, int DV>
+struct Cfg {
+    static constexpr uint32_t QB = kTile * D * 2, KB = kTile * D * 2, VB = kTile * DV * 2;
+    static constexpr int KST = D == 64 ? 4 : 2, VST = D == 64 ? 4 : D == 192 ? 1 : 2;
+    static constexpr uint32_t Q = 0, K = 2 * QB, V = K + KST * KB, BARS = V + VST * VB;
+    static constexpr int NBAR = 2 + 2 * KST + 2 * VST + 1 + 2 + 2 + 2 + 1;
+    static constexpr uint32_t SMEM = BARS + NBAR * 8 + 64 + 1024;
+    static_assert(SMEM <= 232448, "shared memory budget");
+    static constexpr uint32_t T_S = 0, T_O = 256;  // TMEM columns of tile 0; tile 1's follow 128 later
+};
+
+struct Args {
+    PromptParams p;
+    int pair_heads;  // 1: two heads of a group share their rows; 0: 256 rows of one head
+    int n_heads;     // work items per unit: head pairs, or heads
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Query and key rows of sequence n, clamped to the tensors.
+struct Seq {
+    int q0, nq, k0, nk;
+};
+__device__ __forceinline__ Seq seq_of(const PromptParams &p, int n) {
+    auto range = [&p](const int32_t *cu, int n, int64_t T, int &at, int &len) {
+        if (!cu) {  // equal lengths
+            len = (int)(T / p.N);
+            at = n * len;
+            return;
+        }
+        int64_t a = __ldg(cu + n), b = __ldg(cu + n + 1);
+        a = max((int64_t)0, min(a, T));
+        b = max(a, min(b, T));
+        at = (int)a;
+        len = (int)(b - a);
+    };
+    Seq s;
+    range(p.cu_q, n, p.Tq, s.q0, s.nq);
+    range(p.cu_k, n, p.Tk, s.k0, s.nk);
+    return s;
+}
+
+// Units (runs of `rows` query rows of one sequence), longest first.  A unit's key is the
+// number of keys its last row sees (not clamped at 0: it grows strictly within a sequence).
+// Units of sequence s with a key of at least x:
+__device__ __forceinline__ int units_from(const Seq &s, int rows, int x) {
+    const int all = (s.nq + rows - 1) / rows, y = x - (s.nk - s.nq);  // the last row's number has to reach y
+    if (y <= 0) return all;
+    if (y > s.nq) return 0;
+    return all - ((y + rows - 1) / rows - 1);
+}
+
+__device__ __forceinline__ int warp_total(int x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// The rank-th unit: its sequence and its first row; false if there are fewer.  One warp.
+__device__ bool find_unit(const PromptParams &p, int rows, int rank, int &seq, int &row0) {
+    const int lane = threadIdx.x & 31;
+    auto count = [&](int x) {
+        int c = 0;
+        for (int n = lane; n < p.N; n += 32) c += units_from(seq_of(p, n), rows, x);
+        return warp_total(c);
+    };
+    int lo = INT_MAX, hi = INT_MIN;  // keys lie in (lo, hi]
+    for (int n = lane; n < p.N; n += 32) {
+        const Seq s = seq_of(p, n);
+        if (s.nq == 0) continue;
+        lo = min(lo, s.nk - s.nq);
+        hi = max(hi, s.nk);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lo > hi || rank >= count(lo)) return false;
+    while (lo < hi) {  // the largest x with more than `rank` units from it on
+        const int m = (int)(((int64_t)lo + hi + 1) >> 1);
+        if (count(m) > rank)
+            lo = m;
+        else
+            hi = m - 1;
+    }
+    int left = rank - count(lo + 1);  // among the sequences with a unit of key lo, in order
+    for (int n0 = 0; n0 < p.N; n0 += 32) {
+        const int n = n0 + lane;
+        int u = -1;
+        if (n < p.N) {
+            const Seq s = seq_of(p, n);
+            const int a = units_from(s, rows, lo);
+            if (a > units_from(s, rows, lo + 1)) u = (s.nq + rows - 1) / rows - a;
+        }
+        const uint32_t has = __ballot_sync(0xffffffffu, u >= 0);
+        if (left < __popc(has)) {
+            const int src = __fns(has, 0, left + 1);
+            seq = n0 + src;
+            row0 = __shfl_sync(0xffffffffu, u, src) * rows;
+            return true;
+        }
+        left -= __popc(has);
+    }
+    return false;
+}
+
+// One row computed alone, without what it does not see: m and l are its softmax's (they never
+// include masked scores).  Taken only where a NaN came out and a masked value is not finite.
+template <int D, int DV>
+__device__ __noinline__ void rescue_row(const PromptParams &p, const Seq &s, int row, int head, int seen, int blocks,
+                                        float m, float l, float c) {
+    const int kvh = head / (p.Hq / p.Hk);
+    const __nv_bfloat16 *v0 = p.v + (int64_t)s.k0 * p.v_stride + (int64_t)kvh * DV;
+    bool masked_bad = false;
+    for (int j = seen; j < min(blocks * kTile, s.nk) && !masked_bad; ++j)
+        for (int d = 0; d < DV; ++d) masked_bad |= !isfinite(__bfloat162float(v0[j * p.v_stride + d]));
+    if (!masked_bad) return;  // the NaN comes from what the row sees
+    const __nv_bfloat16 *q = p.q + (int64_t)(s.q0 + row) * p.q_stride + (int64_t)head * D;
+    const __nv_bfloat16 *k0 = p.k + (int64_t)s.k0 * p.k_stride + (int64_t)kvh * D;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    for (int d0 = 0; d0 < DV; d0 += 16) {
+        float acc[16] = {};
+        for (int j = 0; j < seen; ++j) {
+            float dot = 0.f;
+            for (int d = 0; d < D; ++d) dot = fmaf(__bfloat162float(q[d]), __bfloat162float(k0[j * p.k_stride + d]), dot);
+            const float w = ex2(fmaf(dot, c, -m));
+#pragma unroll
+            for (int d = 0; d < 16; ++d) acc[d] = fmaf(w, __bfloat162float(v0[j * p.v_stride + d0 + d]), acc[d]);
+        }
+#pragma unroll
+        for (int d = 0; d < 16; ++d)
+            st_out(p.o, ((int64_t)(s.q0 + row) * p.Hq + head) * DV + d0 + d, acc[d] * inv, p.o_bf16);
+    }
+}
+
+template <int D, int DV>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Args a) {
+    using L = Cfg<D, DV>;
+    const PromptParams &p = a.p;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(sm), sb16 = sb >> 4;
+    uint64_t *q_full = reinterpret_cast<uint64_t *>(sm + L::BARS);  // [2]
+    uint64_t *k_full = q_full + 2, *k_empty = k_full + L::KST;
+    uint64_t *v_full = k_empty + L::KST, *v_empty = v_full + L::VST;
+    uint64_t *v_raw = v_empty + L::VST;                             // a last value block, before its tail is zeroed
+    uint64_t *s_full = v_raw + 1, *p_ready = s_full + 2, *o_full = p_ready + 2;
+    uint64_t *drain = o_full + 2;
+    int *work = reinterpret_cast<int *>(drain + 1);                 // [0] found, [1] sequence, [2] first row
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(work + 4);
+    volatile int *abort_flag = work + 5;                            // a bounded wait gave up
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    const int item = blockIdx.x % a.n_heads, rank = blockIdx.x / a.n_heads;
+    if (warp == 0) {
+        int seq = 0, row0 = 0;
+        const bool found = find_unit(p, a.pair_heads ? kTile : 2 * kTile, rank, seq, row0);
+        if (lane == 0) {
+            work[0] = found;
+            work[1] = seq;
+            work[2] = row0;
+        }
+    }
+    if (warp == 1 && lane == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + i, 1);
+            mbar_init(s_full + i, 1);
+            mbar_init(p_ready + i, 4);
+            mbar_init(o_full + i, 1);
+        }
+        for (int i = 0; i < L::KST; ++i) {
+            mbar_init(k_full + i, 1);
+            mbar_init(k_empty + i, 1);
+        }
+        for (int i = 0; i < L::VST; ++i) {
+            mbar_init(v_full + i, 1);
+            mbar_init(v_empty + i, 1);
+        }
+        mbar_init(v_raw, 1);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tb = *tmem_slot;
+    int failed = 0;
+    if (work[0]) {
+        const Seq s = seq_of(p, work[1]);
+        const int row0 = work[2], group = p.Hq / p.Hk;
+        const int head0 = a.pair_heads ? 2 * item : item, kvh = head0 / group;
+        auto tile_row = [&](int t) { return a.pair_heads ? row0 : row0 + t * kTile; };
+        // key blocks that tile t sees
+        auto tile_blocks = [&](int t) {
+            const int r = tile_row(t), last = min(r + kTile, s.nq) - 1;
+            if (r >= s.nq) return 0;
+            const int seen = max(0, min(s.nk, last + 1 + s.nk - s.nq));
+            return (seen + kTile - 1) / kTile;
+        };
+        const int n0 = tile_blocks(0), n1 = tile_blocks(1), nb = max(n0, n1);
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            for (uint32_t i = 0; i < kPolls; ++i) {
+                if (mbar_try_wait(bar, parity)) return true;
+                if (*abort_flag) break;
+            }
+            *abort_flag = 1;
+            return false;
+        };
+
+        if (warp == kTmaWarp) {
+            // ---- loads
+            uint32_t raw = 0;
+            int nk_issued = 0, nv_issued = 0;
+            auto load_q = [&](int t) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full + t, L::QB);
+                    for (int x = 0; x < D; x += 64)
+                        tma_load_3d(sb + L::Q + t * L::QB + (x / 64) * kTile * 128, &map_q, q_full + t, x,
+                                    a.pair_heads ? head0 + t : head0, s.q0 + tile_row(t));
+                }
+            };
+            auto load_k = [&](int j) {
+                const int st = j % L::KST;
+                if (j >= L::KST && !wait(k_empty + st, (j / L::KST - 1) & 1)) return false;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(k_full + st, L::KB);
+                    for (int x = 0; x < D; x += 64)
+                        tma_load_3d(sb + L::K + st * L::KB + (x / 64) * kTile * 128, &map_k, k_full + st, x, kvh,
+                                    s.k0 + j * kTile);
+                }
+                ++nk_issued;
+                return true;
+            };
+            auto load_v = [&](int j) {
+                const int st = j % L::VST;
+                if (j >= L::VST && !wait(v_empty + st, (j / L::VST - 1) & 1)) return false;
+                const int rows = s.nk - j * kTile;  // of the sequence
+                uint64_t *bar = rows < kTile ? v_raw : v_full + st;
+                const uint32_t base = L::V + st * L::VB;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, L::VB);
+                    for (int x = 0; x < DV; x += 64)
+                        tma_load_3d(sb + base + (x / 64) * kTile * 128, &map_v, bar, x, kvh, s.k0 + j * kTile);
+                }
+                if (rows < kTile) {
+                    const bool ok = wait(v_raw, raw++ & 1);
+                    if (!ok) {  // the copy must still land before the CTA may exit
+                        mbar_wait(v_raw, (raw - 1) & 1, kPolls);
+                        return false;
+                    }
+                    for (int i = lane; i < (kTile - rows) * (DV / 64) * 8; i += 32) {
+                        const int r = rows + i / ((DV / 64) * 8), q = i % ((DV / 64) * 8);
+                        st_shared_v4(sb + base + (q >> 3) * kTile * 128 + r * 128 + (q & 7) * 16, 0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(v_full + st);
+                }
+                ++nv_issued;
+                return true;
+            };
+            bool ok = true;
+            if (n0) load_q(0);
+            if (nb) ok = load_k(0);
+            if (n1) load_q(1);
+            for (int j = 0; j < nb && ok; ++j) {
+                if (j + 1 < nb && L::KST > 1) ok = load_k(j + 1);
+                if (ok) ok = load_v(j);
+            }
+            if (!ok) failed = 1;
+            // every load lands before the CTA may exit
+            if (n0) mbar_wait(q_full, 0, kPolls);
+            if (n1) mbar_wait(q_full + 1, 0, kPolls);
+            for (int j = max(0, nk_issued - L::KST); j < nk_issued; ++j)
+                mbar_wait(k_full + j % L::KST, (j / L::KST) & 1, kPolls);
+            for (int j = max(0, nv_issued - L::VST); j < nv_issued; ++j)
+                mbar_wait(v_full + j % L::VST, (j / L::VST) & 1, kPolls);
+        } else if (warp == kMmaWarp) {
+            // ---- products
+            if (lane == 0) {
+                const uint32_t id_s = idesc_bf16(kTile, kTile, false, false, p.scale < 0.f);
+                const uint32_t id_o = idesc_bf16(kTile, DV, false, true);
+                auto scores = [&](int t, int j) {
+                    const uint32_t q = L::Q + t * L::QB, k = L::K + (j % L::KST) * L::KB;
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x) {
+                        const uint32_t off = (x / 4) * kTile * 128 + (x % 4) * 32;
+                        mma_ss(tb + L::T_S + t * 128, sdesc_at(sb16, q + off, 16, 1024), sdesc_at(sb16, k + off, 16, 1024),
+                               id_s, x ? 1u : 0u);
+                    }
+                    mma_commit(s_full + t);
+                };
+                bool ok = true;
+                if (nb) ok = wait(k_full, 0);
+                for (int t = 0; t < 2 && ok; ++t)
+                    if (t ? n1 : n0) {
+                        ok = wait(q_full + t, 0);
+                        fence_after_sync();
+                        if (ok) scores(t, 0);
+                    }
+                if (ok && nb) mma_commit(k_empty);
+                for (int j = 0; j < nb && ok; ++j) {
+                    const bool more = j + 1 < nb;
+                    ok = wait(v_full + j % L::VST, (j / L::VST) & 1);
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        const int nt = t ? n1 : n0;
+                        if (j < nt) {
+                            ok = wait(p_ready + t, j & 1);
+                            if (!ok) break;
+                            fence_after_sync();
+                            const uint32_t v = L::V + (j % L::VST) * L::VB;
+#pragma unroll
+                            for (int x = 0; x < kTile / 16; ++x)
+                                mma_ts(tb + L::T_O + t * 128, tb + L::T_S + t * 128 + x * 8,
+                                       sdesc_at(sb16, v + x * 2048, kTile * 128, 1024), id_o, (j | x) ? 1u : 0u);
+                            if (j + 1 == nt) mma_commit(o_full + t);
+                        }
+                        if (t == 1) mma_commit(v_empty + j % L::VST);
+                        if (j + 1 < nt) {
+                            ok = wait(k_full + (j + 1) % L::KST, ((j + 1) / L::KST) & 1);
+                            if (!ok) break;
+                            fence_after_sync();
+                            scores(t, j + 1);
+                        }
+                    }
+                    if (ok && more) mma_commit(k_empty + (j + 1) % L::KST);
+                }
+                if (!ok) failed = 1;
+                // nothing issued may still run, and no commit arrive, once the CTA has ended
+                mma_commit(drain);
+                mbar_wait(drain, 0, kPolls);
+            }
+            __syncwarp();
+        } else {
+            // ---- softmax of tile t, a thread per row
+            const int t = warp >> 2, nt = t ? n1 : n0, m_row = (warp & 3) * 32 + lane;
+            const int row = tile_row(t) + m_row, head = a.pair_heads ? head0 + t : head0;
+            const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t t_s = tb + lane_base + L::T_S + t * 128, t_o = tb + lane_base + L::T_O + t * 128;
+            const int seen = max(0, min(s.nk, row + 1 + s.nk - s.nq));
+            const int seen_first = max(0, min(s.nk, tile_row(t) + 1 + s.nk - s.nq));  // of the tile's first row
+            const float c = fabsf(p.scale) * kLog2e;
+            float m = -INFINITY, l = 0.f;
+            bool ok = true;
+            for (int j = 0; j < nt; ++j) {
+                ok = wait(s_full + t, j & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                fence_after_sync();
+                uint32_t r[128];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_ld32(t_s + 32 * i, r + 32 * i);
+                tmem_wait_ld();
+                float *x = reinterpret_cast<float *>(r);
+                if ((j + 1) * kTile > seen_first) {
+                    const int lim = seen - j * kTile;
+#pragma unroll
+                    for (int i = 0; i < 128; ++i)
+                        if (i >= lim) x[i] = -INFINITY;
+                }
+                float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+                const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                const bool raise = mb > m + kSlack;
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float f = raise ? ex2(m - mb) : 1.f;
+                    if (raise) m = mb;
+                    l *= f;
+                    if (j > 0) {  // the scores' arrival says that the products before them are done
+#pragma unroll 1
+                        for (int d = 0; d < DV; d += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(t_o + d, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st16(t_o + d, o);
+                        }
+                    }
+                }
+                const float mm = m == -INFINITY ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float u = ex2(fmaf(x[64 * h + 2 * i], c, -mm)), v = ex2(fmaf(x[64 * h + 2 * i + 1], c, -mm));
+                        sum[i & 1] += u;
+                        sum[2 + (i & 1)] += v;
+                        w[i] = pack_bf16x2(u, v);
+                    }
+                    tmem_st32(t_s + 32 * h, w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_st();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready + t);
+            }
+            if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait(o_full + t, 0));
+            fence_after_sync();
+            if (!ok) failed = 1;
+            const bool live = row < s.nq;
+            const int64_t out = (int64_t)(s.q0 + row) * p.Hq + head;
+            const float inv = !ok ? __int_as_float(0x7fc00000) : l == 0.f ? 0.f : 1.f / l;
+            bool nan = false;
+#pragma unroll 1
+            for (int d = 0; d < DV; d += 32) {
+                uint32_t r[32];
+                if (ok && nt > 0) {
+                    tmem_ld32(t_o + d, r);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[i] = 0;
+                }
+                float y[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    y[i] = __uint_as_float(r[i]) * inv;
+                    nan |= isnan(y[i]);
+                }
+                if (live) {
+                    if (p.o_bf16) {
+                        uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + out * DV + d);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            o[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                                              pack_bf16x2(y[8 * i + 4], y[8 * i + 5]),
+                                              pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+                    } else {
+                        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.o) + out * DV + d);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                    }
+                }
+            }
+            if (live) {
+                if (p.lse) p.lse[out] = !ok ? __int_as_float(0x7fc00000) : l == 0.f ? -INFINITY : (log2f(l) + m) * kLn2;
+                if (nan && ok) rescue_row<D, DV>(p, s, row, head, seen, nt, m, l, copysignf(c, p.scale));
+            }
+        }
+    }
+    fence_before_sync();
+    if (__syncthreads_or(failed) && threadIdx.x == 0) atomicAdd(&g_attn_prompt_timeouts, 1);
+    fence_after_sync();
+    if (warp == kMmaWarp) tmem_dealloc(tb, 512);
+}
+
+// A tensor of rows (heads of `dim` bf16 elements, `stride` elements from row to row) in boxes
+// of 64 channels x 1 head x 128 rows.
+bool encode(chunk::EncodeTiledFn enc, CUtensorMap *map, const void *base, int dim, int heads, int64_t rows,
+            int64_t stride) {
+    const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)kTile}, es[3] = {1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) set_error("attn_prompt: cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return r == CUDA_SUCCESS;
+}
+
+template <int D, int DV>
+kda_status run(const PromptParams &p, cudaStream_t st) {
+    using L = Cfg<D, DV>;
+    chunk::EncodeTiledFn enc = reinterpret_cast<chunk::EncodeTiledFn>(tensor_map_encoder());
+    if (!enc) {
+        set_error("attn_prompt: cuTensorMapEncodeTiled is not available from the driver");
+        return KDA_ERR_CUDA;
+    }
+    static DeviceOnce configured;
+    const int dev = current_device();
+    if (!configured.done(dev)) {
+        if (cudaFuncSetAttribute(attn_prompt_kernel<D, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) !=
+            cudaSuccess) {
+            set_error("attn_prompt: cannot reserve shared memory: %s", cudaGetErrorString(cudaGetLastError()));
+            return KDA_ERR_CUDA;
+        }
+        configured.set(dev);
+    }
+    CUtensorMap mq, mk, mv;
+    // without keys nothing is loaded; the map still needs an address
+    const bool keys = p.Tk > 0;
+    if (!encode(enc, &mq, p.q, D, p.Hq, p.Tq, p.q_stride) ||
+        !encode(enc, &mk, keys ? p.k : p.q, D, keys ? p.Hk : p.Hq, keys ? p.Tk : p.Tq, keys ? p.k_stride : p.q_stride) ||
+        !encode(enc, &mv, keys ? p.v : p.q, keys ? DV : D, keys ? p.Hk : p.Hq, keys ? p.Tk : p.Tq,
+                keys ? p.v_stride : p.q_stride))
+        return KDA_ERR_CUDA;
+    Args a;
+    memset(&a, 0, sizeof(a));
+    a.p = p;
+    a.pair_heads = (p.Hq / p.Hk) % 2 == 0;
+    a.n_heads = a.pair_heads ? p.Hq / 2 : p.Hq;
+    // A sequence of n rows has at most n / rows + 1 units.
+    const int64_t grid = (p.Tq / (a.pair_heads ? kTile : 2 * kTile) + p.N) * a.n_heads;
+    if (grid > INT32_MAX) {
+        set_error("kda_attn_prompt: too many tokens");
+        return KDA_ERR_UNSUPPORTED;
+    }
+    attn_prompt_kernel<D, DV><<<(unsigned)grid, kThreads, L::SMEM, st>>>(mq, mk, mv, a);
+    note_launch();
+    return check_launch("attn_prompt_kernel");
+}
+
+}  // namespace
+
+int take_attn_prompt_timeouts(cudaStream_t st) {
+    int n = 0;
+    const int zero = 0;
+    if (cudaMemcpyFromSymbolAsync(&n, g_attn_prompt_timeouts, sizeof(int), 0, cudaMemcpyDeviceToHost, st) !=
+            cudaSuccess ||
+        cudaMemcpyToSymbolAsync(g_attn_prompt_timeouts, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess) {
+        set_error("attn_prompt: cannot read the timeout counter: %s", cudaGetErrorString(cudaGetLastError()));
+        return -1;
+    }
+    return n;
+}
+
+kda_status launch_attn_prompt(const PromptParams &p, cudaStream_t st) {
+    if (p.Tq == 0) return KDA_OK;
+    if (p.D == 64) return run<64, 64>(p, st);
+    if (p.D == 128) return run<128, 128>(p, st);
+    return run<192, 128>(p, st);
+}
+
+}  // namespace kda
