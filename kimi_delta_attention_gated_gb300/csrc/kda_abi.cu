@@ -957,6 +957,7 @@ kda_status kda_attn_prompt(const void *q, int64_t q_stride, const void *k, int64
                 q_heads, kv_heads);
     KDA_REQUIRE(q_rows <= (1 << 30) && k_rows <= (1 << 30) && q_heads <= 65535, KDA_ERR_UNSUPPORTED,
                 "%s: at most 2^30 rows and 65535 heads", fn);
+    KDA_REQUIRE(n_seqs <= 16384, KDA_ERR_UNSUPPORTED, "%s: at most 16384 sequences", fn);
     KDA_REQUIRE(dtype_ok(o_dtype), KDA_ERR_UNSUPPORTED, "%s: unsupported dtype", fn);
     KDA_REQUIRE(std::isfinite(scale) && scale != 0.f, KDA_ERR_INVALID_ARG, "%s: scale must be finite and not 0", fn);
     KDA_REQUIRE(q_rows == 0 || (q && o), KDA_ERR_INVALID_ARG, "%s: q and o must not be NULL", fn);
