@@ -15,8 +15,10 @@
 //                   rounded to bf16 back into TMEM over the scores, in two halves, so that
 //                   the product with the first half's values runs beside the second's weights
 //   warp 8          issues the products: S_t = Q_t K^T (both operands in shared memory) and
-//                   O_t += P_t V (P from TMEM), alternating the tiles, so that one tile's
-//                   softmax runs beside the other's products
+//                   O_t += P_t V (P from TMEM), one tile's after the other's, so that one
+//                   tile's softmax runs beside the other's products.  (A warp for each tile
+//                   was slower, 418 against 367 us: their products then mix, and both tiles
+//                   wait for the sum of the two.)
 //   warp 9          TMA: the two query tiles once, then rings of key and value blocks
 // TMEM: S_0, S_1 (P over them), O_0, O_1, 128 columns each.
 //
@@ -38,7 +40,6 @@ namespace kda {
 namespace {
 
 using namespace tc;
-using chunk::sdesc_at;
 
 constexpr int kTile = 128;             // query rows of a tile, and keys of a block
 constexpr int kMmaWarp = 8, kTmaWarp = 9;
@@ -105,6 +106,12 @@ __device__ __forceinline__ bool elect_one() {
     return ok != 0;
 }
 
+// A 128-byte-swizzled operand's descriptor from its low word (address / 16 and leading offset);
+// the row groups are 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+    return (uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32 | lo;
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -156,22 +163,26 @@ __device__ __forceinline__ Seq seq_of(const PromptParams &p, int n) {
 // number of keys its last row sees (not clamped at 0: it grows strictly within a sequence).
 // x: the sequence's queries and how many more keys it has.  Its units with a key of at least
 // `key`:
-__device__ __forceinline__ int units_from(int2 x, int rows, int key) {
-    const int all = (x.x + rows - 1) / rows, y = key - x.y;  // the last row's number has to reach y
+__device__ __forceinline__ int units_from(int2 x, int shift, int key) {
+    const int rows = 1 << shift, all = (x.x + rows - 1) >> shift, y = key - x.y;  // the last row's number has to reach y
     if (y <= 0) return all;
     if (y > x.x) return 0;
-    return all - ((y + rows - 1) / rows - 1);
+    return all - (((y + rows - 1) >> shift) - 1);
 }
 
-// The rank-th unit: its sequence and its first row; false if there are fewer.  One warp;
+// The rank-th unit of 2^shift rows: its sequence and its first row; false if there are fewer.  One warp;
 // scratch: room for p.N int2 in shared memory.
-__device__ bool find_unit(const PromptParams &p, int rows, int rank, int2 *scratch, int &seq, int &row0) {
-    const int lane = threadIdx.x & 31;
+__device__ bool find_unit(const PromptParams &p, int shift, int rank, int2 *scratch, int &seq, int &row0) {
+    const int lane = threadIdx.x & 31, rows = 1 << shift;
     if (!p.cu_q) {  // equal lengths: round by round
-        const int nq = (int)(p.Tq / p.N), all = (nq + rows - 1) / rows, u = all - 1 - rank / p.N;
+        const int nq = (int)(p.Tq / p.N), all = (nq + rows - 1) >> shift, u = all - 1 - rank / p.N;
         seq = rank % p.N;
         row0 = u * rows;
         return u >= 0;
+    }
+    if (p.N == 1) {
+        row0 = (((seq_of(p, 0).nq + rows - 1) >> shift) - 1 - rank) * rows;
+        return row0 >= 0;
     }
     int lo = INT_MAX, hi = INT_MIN;  // keys lie in (lo, hi]
     for (int n = lane; n < p.N; n += 32) {
@@ -183,7 +194,7 @@ __device__ bool find_unit(const PromptParams &p, int rows, int rank, int2 *scrat
     }
     auto count = [&](int key) {  // each lane reads what it wrote
         int c = 0;
-        for (int n = lane; n < p.N; n += 32) c += units_from(scratch[n], rows, key);
+        for (int n = lane; n < p.N; n += 32) c += units_from(scratch[n], shift, key);
         return __reduce_add_sync(0xffffffffu, c);
     };
     lo = __reduce_min_sync(0xffffffffu, lo);
@@ -202,8 +213,8 @@ __device__ bool find_unit(const PromptParams &p, int rows, int rank, int2 *scrat
         int u = -1;
         if (n < p.N) {
             const int2 x = scratch[n];
-            const int a = units_from(x, rows, lo);
-            if (a > units_from(x, rows, lo + 1)) u = (x.x + rows - 1) / rows - a;
+            const int a = units_from(x, shift, lo);
+            if (a > units_from(x, shift, lo + 1)) u = ((x.x + rows - 1) >> shift) - a;
         }
         const uint32_t has = __ballot_sync(0xffffffffu, u >= 0);
         if (left < __popc(has)) {
@@ -215,6 +226,22 @@ __device__ bool find_unit(const PromptParams &p, int rows, int rank, int2 *scrat
         left -= __popc(has);
     }
     return false;
+}
+
+// Weights 2^(c y - m) of 64 scores as bf16 pairs and their sum (two halves).
+__device__ __forceinline__ void weights(const float (&y)[64], float c, float m, uint32_t (&w)[32], float2 &sum) {
+    const float mm = m == -INFINITY ? 0.f : m;  // a row that has seen nothing: every score is -inf
+    const float2 c2 = make_float2(c, c), m2 = make_float2(-mm, -mm);
+    float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        float2 e = fma2(make_float2(y[2 * i], y[2 * i + 1]), c2, m2);
+        e.x = ex2(e.x);
+        e.y = ex2(e.y);
+        s[i & 1] = add2(s[i & 1], e);
+        w[i] = pack_bf16x2(e.x, e.y);
+    }
+    sum = add2(s[0], s[1]);
 }
 
 // One row computed alone, without what it does not see: m and l are its softmax's (they never
@@ -270,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int item = blockIdx.x % a.n_heads, rank = blockIdx.x / a.n_heads;
     if (warp == 0) {
         int seq = 0, row0 = 0;
-        const bool found = find_unit(p, a.pair_heads ? kTile : 2 * kTile, rank, reinterpret_cast<int2 *>(sm), seq, row0);
+        const bool found = find_unit(p, a.pair_heads ? 7 : 8, rank, reinterpret_cast<int2 *>(sm), seq, row0);
         fence_async_smem();  // the scratch is the loads' room from here on
         if (lane == 0) {
             work[0] = found;
@@ -402,59 +429,65 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = max(0, nv_issued - L::VST); j < nv_issued; ++j)
                 mbar_wait(v_full + j % L::VST, (j / L::VST) & 1, kPolls);
         } else if (warp == kMmaWarp) {
-            // ---- products
+            // ---- products.  One thread's instructions come one at a time, about five cycles
+            // each, so the descriptors are bases plus constants.
             if (elect_one()) {
                 const uint32_t id_s = idesc_bf16(kTile, kTile, false, false, p.scale < 0.f);
                 const uint32_t id_o = idesc_bf16(kTile, DV, false, true);
-                auto scores = [&](int t, int j) {
-                    const uint32_t q = L::Q + t * L::QB, k = L::K + (j % L::KST) * L::KB;
+                const uint32_t lo_kmajor = sb16 | (16u >> 4) << 16, lo_v = sb16 | (kTile * 128u >> 4) << 16;
+                const uint32_t q_lo = lo_kmajor + (L::Q >> 4);
+                auto scores = [&](int t, uint32_t k_lo) {
 #pragma unroll
                     for (int x = 0; x < D / 16; ++x) {
-                        const uint32_t off = (x / 4) * kTile * 128 + (x % 4) * 32;
-                        mma_ss(tb + L::T_S + t * 128, sdesc_at(sb16, q + off, 16, 1024), sdesc_at(sb16, k + off, 16, 1024),
-                               id_s, x ? 1u : 0u);
+                        const uint32_t off = ((x / 4) * kTile * 128 + (x % 4) * 32) >> 4;
+                        mma_ss(tb + L::T_S + t * 128, desc_of(q_lo + (t * L::QB >> 4) + off), desc_of(k_lo + off), id_s, x > 0);
                     }
                     mma_commit(s_full + t);
                 };
                 bool ok = true;
                 if (nb) ok = wait(k_full, 0);
-                for (int t = 0; t < 2 && ok; ++t)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
                     if (t ? n1 : n0) {
-                        ok = wait(q_full + t, 0);
+                        ok = ok && wait(q_full + t, 0);
                         fence_after_sync();
-                        if (ok) scores(t, 0);
+                        if (ok) scores(t, lo_kmajor + (L::K >> 4));
                     }
-                if (ok && nb) mma_commit(k_empty);
+                if (nb) mma_commit(k_empty);
+                int ks = 0, vs = 0;            // ring places of the next keys and of this block's values
+                uint32_t kp = 0, vp = 0;       // and the parities of their rounds
                 for (int j = 0; j < nb && ok; ++j) {
+                    if (++ks == L::KST) ks = 0, kp ^= 1;
+                    const uint32_t k_lo = lo_kmajor + (L::K >> 4) + ks * (L::KB >> 4), v_lo = lo_v + (L::V >> 4) + vs * (L::VB >> 4);
                     const bool more = j + 1 < nb;
-                    ok = wait(v_full + j % L::VST, (j / L::VST) & 1);
-                    for (int t = 0; t < 2 && ok; ++t) {
+                    ok = wait(v_full + vs, vp);
+                    if (more) ok = ok && wait(k_full + ks, kp);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
                         const int nt = t ? n1 : n0;
-                        if (j < nt) {
-                            const uint32_t v = L::V + (j % L::VST) * L::VB;
+                        if (j < nt && ok) {
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                ok = wait(p_ready + 2 * t + h, j & 1);
+                                ok = ok && wait(p_ready + 2 * t + h, j & 1);
                                 if (!ok) break;
                                 fence_after_sync();
 #pragma unroll
                                 for (int x = 4 * h; x < 4 * h + 4; ++x)
-                                    mma_ts(tb + L::T_O + t * 128, tb + L::T_S + t * 128 + x * 8,
-                                           sdesc_at(sb16, v + x * 2048, kTile * 128, 1024), id_o, (j | x) ? 1u : 0u);
+                                    mma_ts(tb + L::T_O + t * 128, tb + L::T_S + t * 128 + x * 8, desc_of(v_lo + (x * 2048 >> 4)),
+                                           id_o, x > 0 ? 1u : j > 0);
                                 if (h == 0) mma_commit(o_half + t);
                             }
-                            if (!ok) break;
-                            if (j + 1 == nt) mma_commit(o_full + t);
-                        }
-                        if (t == 1) mma_commit(v_empty + j % L::VST);
-                        if (j + 1 < nt) {
-                            ok = wait(k_full + (j + 1) % L::KST, ((j + 1) / L::KST) & 1);
-                            if (!ok) break;
-                            fence_after_sync();
-                            scores(t, j + 1);
+                            // the next scores overwrite this block's weights: behind the product in the same queue
+                            if (ok && t == 1) mma_commit(v_empty + vs);
+                            if (ok && j + 1 < nt) scores(t, k_lo);
+                            if (ok && j + 1 == nt) mma_commit(o_full + t);
                         }
                     }
-                    if (ok && more) mma_commit(k_empty + (j + 1) % L::KST);
+                    if (ok) {
+                        if (j >= n1) mma_commit(v_empty + vs);
+                        if (more) mma_commit(k_empty + ks);
+                    }
+                    if (++vs == L::VST) vs = 0, vp ^= 1;
                 }
                 if (!ok) failed = 1;
                 // nothing issued may still run, and no commit arrive, once the CTA has ended
@@ -488,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(t_s + 96, x[1] + 32);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float *y = x[h];
+                    float(&y)[64] = x[h];
                     if (h) wait_ld64(y);
                     if (cut) {
 #pragma unroll
@@ -508,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float f = raise ? ex2(m - mb) : 1.f;
                         if (raise) m = mb;
                         l *= f;
-                        if (j > 0 || h > 0) {
+                        if (j | h) {
                             // the scores' arrival says that the products of the blocks before are done;
                             // the first half of this one has a barrier of its own
                             if (h) {
@@ -527,21 +560,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    const float mm = m == -INFINITY ? 0.f : m;
-                    const float2 c2 = make_float2(c, c), m2 = make_float2(-mm, -mm);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     uint32_t w[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float2 e = fma2(make_float2(y[2 * i], y[2 * i + 1]), c2, m2);
-                        e.x = ex2(e.x);
-                        e.y = ex2(e.y);
-                        sum[i & 1] = add2(sum[i & 1], e);
-                        w[i] = pack_bf16x2(e.x, e.y);
-                    }
+                    float2 sum;
+                    weights(y, c, m, w, sum);
                     tmem_st32(t_s + 32 * h, w);
-                    sum[0] = add2(sum[0], sum[1]);
-                    l += sum[0].x + sum[0].y;
+                    l += sum.x + sum.y;
                     tmem_wait_st();
                     fence_before_sync();
                     __syncwarp();
