@@ -14,12 +14,12 @@
 //   warps 0-3, 4-7  softmax of tile 0 / 1, a thread per row: scores from TMEM, weights
 //                   rounded to bf16 back into TMEM over the scores, in two halves, so that
 //                   the product with the first half's values runs beside the second's weights
-//   warp 8          issues the products: S_t = Q_t K^T (both operands in shared memory) and
-//                   O_t += P_t V (P from TMEM), one tile's after the other's, so that one
-//                   tile's softmax runs beside the other's products.  (A warp for each tile
-//                   was slower, 418 against 367 us: their products then mix, and both tiles
-//                   wait for the sum of the two.)
-//   warp 9          TMA: the two query tiles once, then rings of key and value blocks
+//   warps 8, 9      issue the products of tile 0 / 1: S_t = Q_t K^T (both operands in shared
+//                   memory) and O_t += P_t V (P from TMEM).  They take turns, a tile's O and
+//                   next S together, so that one tile's softmax runs beside the other's
+//                   products; a warp has done its waiting (100 to 200 cycles a barrier) when
+//                   its turn comes
+//   warp 10         TMA: the two query tiles once, then rings of key and value blocks
 // TMEM: S_0, S_1 (P over them), O_0, O_1, 128 columns each.
 //
 // Weights are rounded to bf16 because the product takes one type and the values are bf16;
@@ -42,9 +42,9 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = 128;             // query rows of a tile, and keys of a block
-constexpr int kMmaWarp = 8, kTmaWarp = 9;
-constexpr int kThreads = 320;
-constexpr uint32_t kPolls = 1u << 26;
+constexpr int kMmaWarp = 8, kTmaWarp = 10;
+constexpr int kThreads = 352;
+constexpr uint32_t kPolls = 1u << 21;  // a few seconds; a CTA waits for nothing but its own warps and loads
 constexpr float kSlack = 40.f;         // log2: how far a score may exceed the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -55,7 +55,7 @@ struct Cfg {
     static constexpr uint32_t QB = kTile * D * 2, KB = kTile * D * 2, VB = kTile * DV * 2;
     static constexpr int KST = D == 64 ? 4 : 2, VST = D == 64 ? 4 : D == 192 ? 1 : 2;
     static constexpr uint32_t Q = 0, K = 2 * QB, V = K + KST * KB, BARS = V + VST * VB;
-    static constexpr int NBAR = 2 + 2 * KST + 2 * VST + 1 + 2 + 4 + 2 + 2 + 1;
+    static constexpr int NBAR = 2 + 2 * KST + 2 * VST + 1 + 2 + 4 + 2 + 2;
     static constexpr uint32_t SMEM = BARS + NBAR * 8 + 64 + 1024;
     static_assert(SMEM <= 232448, "shared memory budget");
     static constexpr uint32_t T_S = 0, T_O = 256;  // TMEM columns of tile 0; tile 1's follow 128 later
@@ -86,14 +86,15 @@ __device__ __forceinline__ void wait_ld64(float *r) {
                      "+f"(r[i + 6]), "+f"(r[i + 7]), "+f"(r[i + 8]), "+f"(r[i + 9]), "+f"(r[i + 10]), "+f"(r[i + 11]),
                      "+f"(r[i + 12]), "+f"(r[i + 13]), "+f"(r[i + 14]), "+f"(r[i + 15]));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+// 32 columns from two runs of 16 registers.
+__device__ __forceinline__ void tmem_st16x2(uint32_t taddr, const float *r, const float *q) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
         "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
+        "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(q[0]), "f"(q[1]), "f"(q[2]),
+        "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]), "f"(q[8]), "f"(q[9]), "f"(q[10]), "f"(q[11]), "f"(q[12]),
+        "f"(q[13]), "f"(q[14]), "f"(q[15])
         : "memory");
 }
 
@@ -105,6 +106,18 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
     return ok != 0;
 }
+
+// The weights stored so far are in TMEM: tells the products' warp (one arrival per warp).
+__device__ __forceinline__ void hand_over(uint64_t *bar) {
+    tmem_wait_st();
+    fence_before_sync();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// The turn of the product warps: barrier 1 gives it to tile 0's, barrier 2 to tile 1's.
+__device__ __forceinline__ void turn_wait(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void turn_pass(int id) { asm volatile("barrier.cta.arrive %0, 64;" ::"r"(id) : "memory"); }
 
 // A 128-byte-swizzled operand's descriptor from its low word (address / 16 and leading offset);
 // the row groups are 1024 bytes apart.
@@ -228,20 +241,19 @@ __device__ bool find_unit(const PromptParams &p, int shift, int rank, int2 *scra
     return false;
 }
 
-// Weights 2^(c y - m) of 64 scores as bf16 pairs and their sum (two halves).
-__device__ __forceinline__ void weights(const float (&y)[64], float c, float m, uint32_t (&w)[32], float2 &sum) {
+// Weights 2^(c y - m) of 32 scores y, left as bf16 pairs in the words y[0, 16); their sum is
+// added to s (two pairs of halves).
+__device__ __forceinline__ void weights32(float *y, float c, float m, float2 (&s)[2]) {
     const float mm = m == -INFINITY ? 0.f : m;  // a row that has seen nothing: every score is -inf
     const float2 c2 = make_float2(c, c), m2 = make_float2(-mm, -mm);
-    float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < 16; ++i) {
         float2 e = fma2(make_float2(y[2 * i], y[2 * i + 1]), c2, m2);
         e.x = ex2(e.x);
         e.y = ex2(e.y);
         s[i & 1] = add2(s[i & 1], e);
-        w[i] = pack_bf16x2(e.x, e.y);
+        y[i] = __uint_as_float(pack_bf16x2(e.x, e.y));
     }
-    sum = add2(s[0], s[1]);
 }
 
 // One row computed alone, without what it does not see: m and l are its softmax's (they never
@@ -287,9 +299,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *v_full = k_empty + L::KST, *v_empty = v_full + L::VST;
     uint64_t *v_raw = v_empty + L::VST;                             // a last value block, before its tail is zeroed
     uint64_t *s_full = v_raw + 1, *p_ready = s_full + 2;            // p_ready[tile * 2 + half]
-    uint64_t *o_half = p_ready + 4, *o_full = o_half + 2;
+    uint64_t *o_full = p_ready + 4;
     uint64_t *drain = o_full + 2;
-    int *work = reinterpret_cast<int *>(drain + 1);                 // [0] found, [1] sequence, [2] first row
+    int *work = reinterpret_cast<int *>(drain + 2);                 // [0] found, [1] sequence, [2] first row
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(work + 4);
     volatile int *abort_flag = work + 5;                            // a bounded wait gave up
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -311,19 +323,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(s_full + i, 1);
             mbar_init(p_ready + 2 * i, 4);
             mbar_init(p_ready + 2 * i + 1, 4);
-            mbar_init(o_half + i, 1);
             mbar_init(o_full + i, 1);
+            mbar_init(drain + i, 1);
         }
         for (int i = 0; i < L::KST; ++i) {
             mbar_init(k_full + i, 1);
-            mbar_init(k_empty + i, 1);
+            mbar_init(k_empty + i, 2);
         }
         for (int i = 0; i < L::VST; ++i) {
             mbar_init(v_full + i, 1);
-            mbar_init(v_empty + i, 1);
+            mbar_init(v_empty + i, 2);
         }
         mbar_init(v_raw, 1);
-        mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -428,71 +439,80 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait(k_full + j % L::KST, (j / L::KST) & 1, kPolls);
             for (int j = max(0, nv_issued - L::VST); j < nv_issued; ++j)
                 mbar_wait(v_full + j % L::VST, (j / L::VST) & 1, kPolls);
-        } else if (warp == kMmaWarp) {
-            // ---- products.  One thread's instructions come one at a time, about five cycles
-            // each, so the descriptors are bases plus constants.
-            if (elect_one()) {
-                const uint32_t id_s = idesc_bf16(kTile, kTile, false, false, p.scale < 0.f);
-                const uint32_t id_o = idesc_bf16(kTile, DV, false, true);
-                const uint32_t lo_kmajor = sb16 | (16u >> 4) << 16, lo_v = sb16 | (kTile * 128u >> 4) << 16;
-                const uint32_t q_lo = lo_kmajor + (L::Q >> 4);
-                auto scores = [&](int t, uint32_t k_lo) {
+        } else if (warp >= kMmaWarp) {
+            // ---- products of tile t.  One thread's instructions come one at a time, about five
+            // cycles each, so the descriptors are bases plus constants.
+            const int t = warp - kMmaWarp, nt = t ? n1 : n0;
+            const uint32_t id_s = idesc_bf16(kTile, kTile, false, false, p.scale < 0.f);
+            const uint32_t id_o = idesc_bf16(kTile, DV, false, true);
+            const uint32_t lo_kmajor = sb16 | (16u >> 4) << 16, lo_v = sb16 | (kTile * 128u >> 4) << 16;
+            const uint32_t q_lo = lo_kmajor + ((L::Q + t * L::QB) >> 4), t_s = tb + L::T_S + t * 128, t_o = tb + L::T_O + t * 128;
+            auto scores = [&](uint32_t k_lo) {
 #pragma unroll
-                    for (int x = 0; x < D / 16; ++x) {
-                        const uint32_t off = ((x / 4) * kTile * 128 + (x % 4) * 32) >> 4;
-                        mma_ss(tb + L::T_S + t * 128, desc_of(q_lo + (t * L::QB >> 4) + off), desc_of(k_lo + off), id_s, x > 0);
-                    }
-                    mma_commit(s_full + t);
-                };
-                bool ok = true;
-                if (nb) ok = wait(k_full, 0);
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    if (t ? n1 : n0) {
-                        ok = ok && wait(q_full + t, 0);
-                        fence_after_sync();
-                        if (ok) scores(t, lo_kmajor + (L::K >> 4));
-                    }
-                if (nb) mma_commit(k_empty);
-                int ks = 0, vs = 0;            // ring places of the next keys and of this block's values
-                uint32_t kp = 0, vp = 0;       // and the parities of their rounds
-                for (int j = 0; j < nb && ok; ++j) {
-                    if (++ks == L::KST) ks = 0, kp ^= 1;
-                    const uint32_t k_lo = lo_kmajor + (L::K >> 4) + ks * (L::KB >> 4), v_lo = lo_v + (L::V >> 4) + vs * (L::VB >> 4);
-                    const bool more = j + 1 < nb;
-                    ok = wait(v_full + vs, vp);
-                    if (more) ok = ok && wait(k_full + ks, kp);
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int nt = t ? n1 : n0;
-                        if (j < nt && ok) {
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                ok = ok && wait(p_ready + 2 * t + h, j & 1);
-                                if (!ok) break;
-                                fence_after_sync();
-#pragma unroll
-                                for (int x = 4 * h; x < 4 * h + 4; ++x)
-                                    mma_ts(tb + L::T_O + t * 128, tb + L::T_S + t * 128 + x * 8, desc_of(v_lo + (x * 2048 >> 4)),
-                                           id_o, x > 0 ? 1u : j > 0);
-                                if (h == 0) mma_commit(o_half + t);
-                            }
-                            // the next scores overwrite this block's weights: behind the product in the same queue
-                            if (ok && t == 1) mma_commit(v_empty + vs);
-                            if (ok && j + 1 < nt) scores(t, k_lo);
-                            if (ok && j + 1 == nt) mma_commit(o_full + t);
-                        }
-                    }
-                    if (ok) {
-                        if (j >= n1) mma_commit(v_empty + vs);
-                        if (more) mma_commit(k_empty + ks);
-                    }
-                    if (++vs == L::VST) vs = 0, vp ^= 1;
+                for (int x = 0; x < D / 16; ++x) {
+                    const uint32_t off = ((x / 4) * kTile * 128 + (x % 4) * 32) >> 4;
+                    mma_ss(t_s, desc_of(q_lo + off), desc_of(k_lo + off), id_s, x > 0);
                 }
-                if (!ok) failed = 1;
-                // nothing issued may still run, and no commit arrive, once the CTA has ended
-                mma_commit(drain);
-                mbar_wait(drain, 0, kPolls);
+            };
+            bool ok = true;
+            if (nt) {
+                ok = wait(q_full + t, 0) && wait(k_full, 0);
+                fence_after_sync();
+                if (ok && elect_one()) {
+                    scores(lo_kmajor + (L::K >> 4));
+                    mma_commit(s_full + t);
+                    mma_commit(k_empty);
+                }
+            } else if (nb) {  // every block is let go of by both tiles
+                ok = wait(k_full, 0);
+                if (ok && elect_one()) mbar_arrive(k_empty);
+            }
+            int ks = 0, vs = 0;       // ring places of the next keys and of this block's values
+            uint32_t kp = 0, vp = 0;  // and the parities of their rounds
+            for (int j = 0; j < nb; ++j) {
+                if (++ks == L::KST) ks = 0, kp ^= 1;
+                const bool mine = j < nt, next = j + 1 < nt;
+                // (an idle tile follows the rings too, and lets go of every block)
+                ok = ok && wait(v_full + vs, vp);
+                if (j + 1 < nb) ok = ok && wait(k_full + ks, kp);
+                if (mine) ok = ok && wait(p_ready + 2 * t, j & 1);
+                fence_after_sync();
+                if (t || j) turn_wait(1 + t);
+                const uint32_t k_lo = lo_kmajor + (L::K >> 4) + ks * (L::KB >> 4), v_lo = lo_v + (L::V >> 4) + vs * (L::VB >> 4);
+                if (mine && ok && elect_one()) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        mma_ts(t_o, t_s + x * 8, desc_of(v_lo + (x * 2048 >> 4)), id_o, x > 0 ? 1u : j > 0);
+                }
+                if (mine) ok = ok && wait(p_ready + 2 * t + 1, j & 1);
+                fence_after_sync();
+                if (ok && elect_one()) {
+                    if (mine) {
+#pragma unroll
+                        for (int x = 4; x < 8; ++x) mma_ts(t_o, t_s + x * 8, desc_of(v_lo + (x * 2048 >> 4)), id_o, 1u);
+                        mma_commit(v_empty + vs);
+                        // the next scores overwrite this block's weights: behind the product in the same queue
+                        if (next) {
+                            scores(k_lo);
+                            mma_commit(s_full + t);
+                            mma_commit(k_empty + ks);
+                        } else {
+                            mma_commit(o_full + t);
+                        }
+                    } else {
+                        mbar_arrive(v_empty + vs);
+                    }
+                    if (!next && j + 1 < nb) mbar_arrive(k_empty + ks);
+                }
+                __syncwarp();
+                if (!t || j + 1 < nb) turn_pass(2 - t);
+                if (++vs == L::VST) vs = 0, vp ^= 1;
+            }
+            if (!ok) failed = 1;
+            // nothing issued may still run, and no commit arrive, once the CTA has ended
+            if (elect_one()) {
+                mma_commit(drain + t);
+                mbar_wait(drain + t, 0, kPolls);
             }
             __syncwarp();
         } else {
@@ -511,66 +531,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 fence_after_sync();
-                const int lim = seen - j * kTile;  // of this block's keys, how many the row sees
-                const bool cut = (j + 1) * kTile > seen_first;
-                float x[2][64];
-                tmem_ld32(t_s, x[0]);
-                tmem_ld32(t_s + 32, x[0] + 32);
-                wait_ld64(x[0]);
-                tmem_ld32(t_s + 64, x[1]);
-                tmem_ld32(t_s + 96, x[1] + 32);
+                float x[128];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float(&y)[64] = x[h];
-                    if (h) wait_ld64(y);
-                    if (cut) {
+                for (int i = 0; i < 128; i += 32) tmem_ld32(t_s + i, x + i);
+                wait_ld64(x);
+                wait_ld64(x + 64);
+                if ((j + 1) * kTile > seen_first) {
+                    const int lim = seen - j * kTile;  // of this block's keys, how many the row sees
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            if (64 * h + i >= lim) y[i] = -INFINITY;
-                    }
-                    float mx[4] = {y[0], y[1], y[2], y[3]};
+                    for (int i = 0; i < 128; ++i)
+                        if (i >= lim) x[i] = -INFINITY;
+                }
+                float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                    for (int i = 4; i < 60; i += 8)
+                for (int i = 4; i < 124; i += 8)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], y[i + e]), y[i + 4 + e]);
+                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], x[i + e]), x[i + 4 + e]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], y[60 + e]);
-                    const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                    const bool raise = mb > m + kSlack;
-                    if (__any_sync(0xffffffffu, raise)) {
-                        const float f = raise ? ex2(m - mb) : 1.f;
-                        if (raise) m = mb;
-                        l *= f;
-                        if (j | h) {
-                            // the scores' arrival says that the products of the blocks before are done;
-                            // the first half of this one has a barrier of its own
-                            if (h) {
-                                ok = __all_sync(0xffffffffu, wait(o_half + t, j & 1));
-                                if (!ok) break;
-                                fence_after_sync();
-                            }
+                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[124 + e]);
+                const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                const bool raise = mb > m + kSlack;
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float f = raise ? ex2(m - mb) : 1.f;
+                    if (raise) m = mb;
+                    l *= f;
+                    if (j > 0) {  // the scores' arrival says that the products before them are done
 #pragma unroll 1
-                            for (int d = 0; d < DV; d += 16) {
-                                uint32_t o[16];
-                                tmem_ld16(t_o + d, o);
-                                tmem_wait_ld();
+                        for (int d = 0; d < DV; d += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(t_o + d, o);
+                            tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                tmem_st16(t_o + d, o);
-                            }
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st16(t_o + d, o);
                         }
                     }
-                    uint32_t w[32];
-                    float2 sum;
-                    weights(y, c, m, w, sum);
-                    tmem_st32(t_s + 32 * h, w);
-                    l += sum.x + sum.y;
-                    tmem_wait_st();
-                    fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(p_ready + 2 * t + h);
                 }
-                if (!ok) break;
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                weights32(x, c, m, sum);
+                weights32(x + 32, c, m, sum);
+                tmem_st16x2(t_s, x, x + 32);
+                weights32(x + 64, c, m, sum);
+                hand_over(p_ready + 2 * t);
+                weights32(x + 96, c, m, sum);
+                tmem_st16x2(t_s + 32, x + 64, x + 96);
+                hand_over(p_ready + 2 * t + 1);
+                sum[0] = add2(sum[0], sum[1]);
+                l += sum[0].x + sum[0].y;
             }
             if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait(o_full + t, 0));
             fence_after_sync();
