@@ -869,7 +869,7 @@ kda_status kda_kv_append(const void *k, int64_t k_stride, const void *v, int64_t
     if ((s = check_apart(fn, in, 7, out, 6)) != KDA_OK) return s;
     kda::AppendParams p;
     p.c = kda::PagedCache{static_cast<uint8_t *>(k_cache), static_cast<uint8_t *>(v_cache), k_scale, v_scale,
-                          block_table, context_lens, num_pages, max_blocks, kv_heads, page_size, dim, n_seqs};
+                          block_table, context_lens, num_pages, max_blocks, kv_heads, page_size, dim, n_seqs, __builtin_ctz(page_size)};
     p.k = static_cast<const __nv_bfloat16 *>(k);
     p.v = static_cast<const __nv_bfloat16 *>(v);
     p.k_stride = k_stride;
@@ -931,7 +931,7 @@ kda_status kda_attn_decode(const void *q, int64_t q_stride, const void *k_cache,
     p.c = kda::PagedCache{static_cast<uint8_t *>(const_cast<void *>(k_cache)),
                           static_cast<uint8_t *>(const_cast<void *>(v_cache)), const_cast<float *>(k_scale),
                           const_cast<float *>(v_scale), block_table, seq_lens, num_pages, max_blocks, kv_heads,
-                          page_size, dim, n_seqs};
+                          page_size, dim, n_seqs, __builtin_ctz(page_size)};
     p.q = static_cast<const __nv_bfloat16 *>(q);
     p.q_stride = q_stride;
     p.Hq = q_heads;

@@ -29,6 +29,7 @@ struct PagedCache {
     const int32_t *block_table;   // [N, max_blocks]
     const int32_t *lens;          // [N] tokens in the cache
     int n_pages, max_blocks, Hk, P, D, N;
+    int p_shift;                  // P = 1 << p_shift
 };
 
 struct AppendParams {
@@ -81,33 +82,48 @@ int take_attn_prompt_timeouts(cudaStream_t st);
 
 // One pair's turn per position as a 64-bit binary fraction of a full turn.  The fraction of
 // position p is then the integer product p * turn modulo 2^64, exact for any position: the
-// reduction to one turn is the integers' own wrap-around.  The double keeps 53 bits of the
-// turn, so a position of 2^20 is off by at most 2^-33 turns.
+// reduction to one turn is the integers' own wrap-around.  Formed from the double's 53-bit
+// integer m and exponent with 64-bit integers (this GPU's double-precision rate is 1/50 of
+// its integer rate): m * 2^e / (2 pi) = m * C * 2^(e - 66) with C = 2^66 / (2 pi).
 __device__ __forceinline__ uint64_t turn_of(double inv_freq) {
-    double t = inv_freq * 0.15915494309189535;  // 1 / (2 pi)
-    t -= floor(t);
-    return (uint64_t)(t * 18446744073709551616.0);
+    const uint64_t b = (uint64_t)__double_as_longlong(inv_freq);
+    const int be = (int)(b >> 52) & 0x7FF;
+    const uint64_t m = be == 0 ? 0ull : (b & 0xFFFFFFFFFFFFFull) | 1ull << 52;  // subnormals are no turn at all
+    const uint64_t C = 11743562013128004906ull;
+    const uint64_t hi = __umul64hi(m, C), lo = m * C;
+    const int s = 2 - (be - 1075);  // the product's binary places behind the 64 that are kept
+    const uint64_t t = s >= 128  ? 0ull
+                       : s >= 64 ? hi >> (s - 64)
+                       : s > 0   ? hi << (64 - s) | lo >> s
+                       : s > -64 ? lo << -s
+                                 : 0ull;
+    return b >> 63 ? 0ull - t : t;
 }
 
 // cos and sin of 2 pi * f / 2^64.  f is split into the nearest quarter turn and a rest of at
-// most 1/8 turn, held as an integer, so the rest's fp32 value is good to half an ulp however
-// small it is; on it (|a| <= pi/4) the Taylor series through a^10 and a^9 leave 1e-9.
+// most 1/8 turn, held as an integer, so the rest's value is exact however small it is; it is
+// taken as a + d, a the fp32 value and d what that leaves out.  On |a| <= pi/4 the Taylor
+// series through a^10 and a^9 leave 1e-9; the last rounding is the only one that counts.
 __device__ __forceinline__ void cos_sin_turn(uint64_t f, float &c, float &s) {
     const uint32_t quarter = (uint32_t)((f + (1ull << 61)) >> 62);
     const int64_t rest = (int64_t)(f - ((uint64_t)quarter << 62));
-    const float a = (float)rest * 3.4061215800304545e-19f;  // 2 pi / 2^64
+    constexpr float kHi = 3.4061215800304545e-19f;  // 2 pi / 2^64
+    constexpr float kLo = (float)(6.283185307179586 / 18446744073709551616.0 - (double)kHi);
+    const float hi = (float)rest, lo = (float)(rest - (int64_t)hi);
+    const float a = hi * kHi;
+    const float d = fmaf(hi, kHi, -a) + fmaf(hi, kLo, lo * kHi);
     const float a2 = a * a;
     float pc = -1.f / 3628800.f;
     pc = fmaf(pc, a2, 1.f / 40320.f);
     pc = fmaf(pc, a2, -1.f / 720.f);
     pc = fmaf(pc, a2, 1.f / 24.f);
     pc = fmaf(pc, a2, -0.5f);
-    pc = fmaf(pc, a2, 1.f);
+    pc = 1.f + fmaf(pc, a2, -a * d);  // cos(a + d) = cos a - d sin a, sin a = a as far as it counts
     float ps = 1.f / 362880.f;
     ps = fmaf(ps, a2, -1.f / 5040.f);
     ps = fmaf(ps, a2, 1.f / 120.f);
     ps = fmaf(ps, a2, -1.f / 6.f);
-    ps = fmaf(ps * a2, a, a);
+    ps = a + fmaf(ps * a2, a, d);
     const float x = (quarter & 1) ? ps : pc, y = (quarter & 1) ? pc : ps;
     c = (quarter == 1 || quarter == 2) ? -x : x;
     s = (quarter & 2) ? -y : y;
@@ -121,10 +137,10 @@ __device__ __forceinline__ float diff_of_products(float a, float b, float c, flo
     return fmaf(a, b, -w) + e;
 }
 
-// The pair (a, b) turned: (a cos - b sin, b cos + a sin).
-__device__ __forceinline__ void turn_pair(float a, float b, float2 cs, float &x, float &y) {
-    x = diff_of_products(a, cs.x, b, cs.y);
-    y = diff_of_products(b, cs.x, -a, cs.y);
+// The pair (a, b) turned: magnitude * (a cos - b sin, b cos + a sin).
+__device__ __forceinline__ void turn_pair(float a, float b, float2 cs, float mag, float &x, float &y) {
+    x = diff_of_products(a, cs.x, b, cs.y) * mag;
+    y = diff_of_products(b, cs.x, -a, cs.y) * mag;
 }
 
 // ---------------------------------------------------------------------------
@@ -167,8 +183,8 @@ struct Vec16<float> {
     }
 };
 
-// cos / sin (times the magnitude and the sign) of `n` tokens' pairs into cs[token][pair]: a
-// thread keeps to one pair, so its turn is formed once (the doubles are slow here).
+// cos / sin (times the sign) of `n` tokens' pairs into cs[token][pair]: a
+// thread keeps to one pair, so its turn is formed once.
 template <typename PosFn>
 __device__ __forceinline__ void fill_cos_sin(float2 *cs, const RotaryParams &r, int n, PosFn pos, int tid, int threads) {
     const int np = r.R >> 1;
@@ -179,7 +195,7 @@ __device__ __forceinline__ void fill_cos_sin(float2 *cs, const RotaryParams &r, 
     for (int t = row; t < n; t += rows) {
         float c, s;
         cos_sin_turn((uint64_t)(int64_t)pos(t) * turn, c, s);
-        cs[t * np + j] = make_float2(c * r.magnitude, s * r.magnitude * r.sign);
+        cs[t * np + j] = make_float2(c, s * r.sign);
     }
 }
 
@@ -191,7 +207,7 @@ __host__ __device__ __forceinline__ int rotary_units(int D, int R, int interleav
 
 // Unit u of one head: x -> y.
 template <typename T>
-__device__ __forceinline__ void rotate_unit(const T *x, T *y, const float2 *cs, int u, int R, int interleaved) {
+__device__ __forceinline__ void rotate_unit(const T *x, T *y, const float2 *cs, int u, int R, int interleaved, float mag) {
     using V = Vec16<T>;
     constexpr int N = V::N;
     const int nrot = interleaved ? R / N : R / (2 * N);
@@ -205,7 +221,7 @@ __device__ __forceinline__ void rotate_unit(const T *x, T *y, const float2 *cs, 
         V::load(*reinterpret_cast<const uint4 *>(x + u * N), a);
         float o[N];
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) turn_pair(a[2 * i], a[2 * i + 1], cs[u * (N / 2) + i], o[2 * i], o[2 * i + 1]);
+        for (int i = 0; i < N / 2; ++i) turn_pair(a[2 * i], a[2 * i + 1], cs[u * (N / 2) + i], mag, o[2 * i], o[2 * i + 1]);
         *reinterpret_cast<uint4 *>(y + u * N) = V::store(o);
     } else {
         float b[N], oa[N], ob[N];
@@ -214,7 +230,7 @@ __device__ __forceinline__ void rotate_unit(const T *x, T *y, const float2 *cs, 
         V::load(wa, a);
         V::load(wb, b);
 #pragma unroll
-        for (int i = 0; i < N; ++i) turn_pair(a[i], b[i], cs[u * N + i], oa[i], ob[i]);
+        for (int i = 0; i < N; ++i) turn_pair(a[i], b[i], cs[u * N + i], mag, oa[i], ob[i]);
         *reinterpret_cast<uint4 *>(y + u * N) = V::store(oa);
         *reinterpret_cast<uint4 *>(y + u * N + R / 2) = V::store(ob);
     }
@@ -227,7 +243,7 @@ __device__ __forceinline__ void rotate_rows(const T *x, int64_t xs, T *y, int64_
     const int U = rotary_units(D, r.R, r.interleaved, Vec16<T>::N), per = H * U, np = r.R >> 1;
     for (int i = tid; i < n * per; i += threads) {
         const int t = i / per, rem = i - t * per, h = rem / U, u = rem - h * U;
-        rotate_unit<T>(x + t * xs + (int64_t)h * D, y + t * ys + (int64_t)h * D, cs + t * np, u, r.R, r.interleaved);
+        rotate_unit<T>(x + t * xs + (int64_t)h * D, y + t * ys + (int64_t)h * D, cs + t * np, u, r.R, r.interleaved, r.magnitude);
     }
 }
 

@@ -12,15 +12,15 @@
 // Memory bound.  The tokens of one call that fall into one page are a run; one CTA takes a
 // run and some of the heads, holds the (rotated) values in registers between the pass that
 // finds each head's largest value and the pass that writes codes, so everything is read
-// once.  One token per sequence (a decode step) has a warp for each (sequence, head).
-// Queries are rotated by further CTAs of the same launch.
+// once, and has the next head's rows on their way meanwhile.  One token per sequence (a
+// decode step) has a warp for each (sequence, head).  Queries are rotated by further CTAs
+// of the same launch.
 #include "kda_attn.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kStepThreads = 256;  // of a decode step's CTA
 constexpr int kRoom = 1024;  // cos / sin pairs of a query tile
 
 struct Grid {
@@ -63,40 +63,47 @@ __device__ __forceinline__ int position_of(const AppendParams &p, int64_t t) {
 }
 
 // One query tile.
+template <int THREADS>
 __device__ __forceinline__ void rotate_queries(const AppendParams &p, int tile, int q_tile, float2 *cs, int *pos) {
     const int64_t t0 = (int64_t)tile * q_tile;
     const int n = (int)min((int64_t)q_tile, p.tokens - t0), tid = threadIdx.x;
-    for (int t = tid; t < n; t += kThreads) pos[t] = position_of(p, t0 + t);
+    for (int t = tid; t < n; t += THREADS) pos[t] = position_of(p, t0 + t);
     __syncthreads();
-    fill_cos_sin(cs, p.rot, n, [&](int t) { return pos[t]; }, tid, kThreads);
+    fill_cos_sin(cs, p.rot, n, [&](int t) { return pos[t]; }, tid, THREADS);
     __syncthreads();
     const int64_t row = (int64_t)p.Hq * p.c.D;
     rotate_rows<__nv_bfloat16>(p.q + t0 * p.q_stride, p.q_stride, p.q_out + t0 * row, row, cs, p.rot, n, p.Hq, p.c.D, tid,
-                               kThreads);
+                               THREADS);
 }
 
-// Channels [8v, 8v + 8) of one head's row x, rotated with cs (null: as they are).
-__device__ __forceinline__ void load_rotated(const __nv_bfloat16 *x, int v, const float2 *cs, const RotaryParams &r,
-                                             float (&y)[8]) {
+// Channels [8v, 8v + 8) of a head's row, and in the half layout those of their partners.
+struct RowPiece {
+    uint4 own, other;
+};
+__device__ __forceinline__ int partner_of(int c0, const RotaryParams &r) {  // -1: none
+    const int half = r.R >> 1;
+    return r.interleaved || c0 >= r.R ? -1 : c0 >= half ? c0 - half : c0 + half;
+}
+__device__ __forceinline__ void turn_piece(const RowPiece &w, int v, const float2 *cs, const RotaryParams &r, float (&y)[8]) {
     using V = Vec16<__nv_bfloat16>;
-    V::load(*reinterpret_cast<const uint4 *>(x + v * 8), y);
+    V::load(w.own, y);
     const int c0 = v * 8;
     if (!cs || c0 >= r.R) return;
     if (r.interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float a = y[2 * i], b = y[2 * i + 1];
-            turn_pair(a, b, cs[v * 4 + i], y[2 * i], y[2 * i + 1]);
+            turn_pair(a, b, cs[v * 4 + i], r.magnitude, y[2 * i], y[2 * i + 1]);
         }
     } else {
         const int half = r.R >> 1;
         const bool second = c0 >= half;
-        const int partner = second ? c0 - half : c0 + half, j = second ? partner : c0;
+        const int j = second ? c0 - half : c0;
         float z[8];
-        V::load(*reinterpret_cast<const uint4 *>(x + partner), z);
+        V::load(w.other, z);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            y[i] = diff_of_products(y[i], cs[j + i].x, second ? -z[i] : z[i], cs[j + i].y);
+            y[i] = diff_of_products(y[i], cs[j + i].x, second ? -z[i] : z[i], cs[j + i].y) * r.magnitude;
     }
 }
 
@@ -109,9 +116,10 @@ __device__ __forceinline__ int block_exp(float amax, int off, int old) {
 // ---------------------------------------------------------------------------
 // runs (any number of tokens per sequence)
 
-template <int ITERS>
-__global__ void __launch_bounds__(kThreads) append_run_kernel(const __grid_constant__ AppendParams p,
-                                                              const __grid_constant__ Grid g) {
+template <int THREADS, int ITERS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_run_kernel(const __grid_constant__ AppendParams p,
+                                                                             const __grid_constant__ Grid g) {
+    constexpr int kThreads = THREADS, kWarps = THREADS / 32;
     extern __shared__ float2 cs[];
     __shared__ int s_pos[kRoom];
     __shared__ int s_seq, s_run;
@@ -119,7 +127,7 @@ __global__ void __launch_bounds__(kThreads) append_run_kernel(const __grid_const
     __shared__ float s_max[2][kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if ((int)blockIdx.x >= g.n_kv) {
-        rotate_queries(p, blockIdx.x - g.n_kv, g.q_tile, cs, s_pos);
+        rotate_queries<kThreads>(p, blockIdx.x - g.n_kv, g.q_tile, cs, s_pos);
         return;
     }
     const int P = p.c.P, D = p.c.D, nv = D >> 3;
@@ -176,14 +184,33 @@ __global__ void __launch_bounds__(kThreads) append_run_kernel(const __grid_const
         __syncthreads();
     }
     const int h0 = part * g.heads, h1 = min(h0 + g.heads, p.c.Hk), np = p.rot.R >> 1;
-    for (int h = h0; h < h1; ++h) {
-        float y[ITERS][8];
-        float amax = 0.f;
+    // this thread's pieces: token x / nv of the run, channels 8 (x % nv)
+    RowPiece raw[ITERS];
+    int old_next = kScaleExpLo;
+    auto fetch = [&](int h) {
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
             const int x = tid + i * kThreads, t = x / nv, v = x - t * nv;
             if (t < n) {
-                load_rotated(src + t * stride + h * D, v, turned ? cs + t * np : nullptr, p.rot, y[i]);
+                const __nv_bfloat16 *row = src + t * stride + h * D;
+                raw[i].own = __ldg(reinterpret_cast<const uint4 *>(row + v * 8));
+                const int pc = turned ? partner_of(v * 8, p.rot) : -1;
+                if (pc >= 0) raw[i].other = __ldg(reinterpret_cast<const uint4 *>(row + pc));
+            }
+        }
+        // a page that holds earlier tokens: its scale (no other CTA writes it)
+        if (off > 0 && page >= 0) old_next = exp_of_scale(scales[(int64_t)page * p.c.Hk + h]);
+    };
+    fetch(h0);
+    for (int h = h0; h < h1; ++h) {
+        float y[ITERS][8];
+        float amax = 0.f;
+        const int old = old_next;
+#pragma unroll
+        for (int i = 0; i < ITERS; ++i) {
+            const int x = tid + i * kThreads, t = x / nv, v = x - t * nv;
+            if (t < n) {
+                turn_piece(raw[i], v, turned ? cs + t * np : nullptr, p.rot, y[i]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(y[i][e]));
                 if (!values && p.k_out)
@@ -191,12 +218,12 @@ __global__ void __launch_bounds__(kThreads) append_run_kernel(const __grid_const
                         Vec16<__nv_bfloat16>::store(y[i]);
             }
         }
+        if (h + 1 < h1) fetch(h + 1);
         if (page < 0) continue;
         amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
         if (lane == 0) s_max[h & 1][warp] = amax;
         const int64_t blk = (int64_t)page * p.c.Hk + h;
-        const int old = exp_of_scale(scales[blk]);
-        __syncthreads();  // also: every thread has read the old scale
+        __syncthreads();  // also: every thread has read this head's old scale
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, s_max[h & 1][w]);
         const int e = block_exp(amax, off, old);
@@ -225,13 +252,14 @@ __global__ void __launch_bounds__(kThreads) append_run_kernel(const __grid_const
 // one token per sequence: a warp for each (sequence, head, keys or values)
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) append_step_kernel(const __grid_constant__ AppendParams p,
-                                                               const __grid_constant__ Grid g) {
+__global__ void __launch_bounds__(kStepThreads) append_step_kernel(const __grid_constant__ AppendParams p,
+                                                                   const __grid_constant__ Grid g) {
+    constexpr int kThreads = kStepThreads, kWarps = kThreads / 32;
     constexpr int C = D / 32;  // channels of a lane
     __shared__ float2 cs[kRoom];
     __shared__ int s_pos[kRoom];
     if ((int)blockIdx.x >= g.n_kv) {
-        rotate_queries(p, blockIdx.x - g.n_kv, g.q_tile, cs, s_pos);
+        rotate_queries<kThreads>(p, blockIdx.x - g.n_kv, g.q_tile, cs, s_pos);
         return;
     }
     const int lane = threadIdx.x & 31;
@@ -262,8 +290,7 @@ __global__ void __launch_bounds__(kThreads) append_step_kernel(const __grid_cons
             for (int i = 0; i < C / 2; ++i) {
                 float c, s;
                 cos_sin_turn((uint64_t)(int64_t)ctx * turn_of(__ldg(p.rot.inv_freq + c0 / 2 + i)), c, s);
-                turn_pair(own[2 * i], own[2 * i + 1], make_float2(c * p.rot.magnitude, s * p.rot.magnitude), y[2 * i],
-                          y[2 * i + 1]);
+                turn_pair(own[2 * i], own[2 * i + 1], make_float2(c, s), p.rot.magnitude, y[2 * i], y[2 * i + 1]);
             }
         } else {
             const int j0 = second ? partner : c0;
@@ -271,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) append_step_kernel(const __grid_cons
             for (int i = 0; i < C; ++i) {
                 float c, s;
                 cos_sin_turn((uint64_t)(int64_t)ctx * turn_of(__ldg(p.rot.inv_freq + j0 + i)), c, s);
-                y[i] = diff_of_products(own[i], c * p.rot.magnitude, second ? -other[i] : other[i], s * p.rot.magnitude);
+                y[i] = diff_of_products(own[i], c, second ? -other[i] : other[i], s) * p.rot.magnitude;
             }
         }
     }
@@ -308,47 +335,13 @@ __global__ void __launch_bounds__(kThreads) append_step_kernel(const __grid_cons
         *reinterpret_cast<uint16_t *>(dst + (int64_t)off * D + c0 + i) = (uint16_t)e4m3x2(y[i] * inv, y[i + 1] * inv);
 }
 
-template <int ITERS>
-kda_status run(const AppendParams &p, const Grid &g, unsigned grid, size_t smem, cudaStream_t st) {
-    if (smem > 32 * 1024) {
-        static DeviceOnce configured;
-        const int dev = current_device();
-        if (!configured.done(dev)) {
-            if (cudaFuncSetAttribute(append_run_kernel<ITERS>, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024) !=
-                cudaSuccess) {
-                set_error("kv_append: cannot reserve shared memory: %s", cudaGetErrorString(cudaGetLastError()));
-                return KDA_ERR_CUDA;
-            }
-            configured.set(dev);
-        }
-    }
-    append_run_kernel<ITERS><<<grid, kThreads, smem, st>>>(p, g);
-    note_launch();
-    return check_launch("append_run_kernel");
-}
-
-}  // namespace
-
-kda_status launch_kv_append(const AppendParams &p, cudaStream_t st) {
-    if (p.tokens == 0) return KDA_OK;
-    Grid g;
-    g.q_tile = p.q ? rotary_tile_tokens(p.Hq, p.c.D, p.rot.R, 8, kThreads, kRoom) : 1;
-    if (g.q_tile > kRoom) g.q_tile = kRoom;
-    const int64_t q_ctas = p.q ? (p.tokens + g.q_tile - 1) / g.q_tile : 0;
-    if (!p.cu_seqlens) {
-        const int64_t kv = ((int64_t)p.c.N * p.c.Hk * 2 + kWarps - 1) / kWarps;
-        g.n_kv = (int)kv;
-        g.heads = g.head_parts = 1;
-        const unsigned grid = (unsigned)(kv + q_ctas);
-        if (p.c.D == 128)
-            append_step_kernel<128><<<grid, kThreads, 0, st>>>(p, g);
-        else
-            append_step_kernel<64><<<grid, kThreads, 0, st>>>(p, g);
-        note_launch();
-        return check_launch("append_step_kernel");
-    }
+template <int THREADS, int ITERS>
+kda_status run(const AppendParams &p, Grid g, cudaStream_t st) {
     // A sequence's n new tokens lie in at most n / P + 2 pages.
     const int64_t runs = p.tokens / p.c.P + 2 * (int64_t)p.c.N;
+    g.q_tile = p.q ? rotary_tile_tokens(p.Hq, p.c.D, p.rot.R, 8, THREADS, kRoom) : 1;
+    if (g.q_tile > kRoom) g.q_tile = kRoom;
+    const int64_t q_ctas = p.q ? (p.tokens + g.q_tile - 1) / g.q_tile : 0;
     // A CTA takes all heads of its run, so that cos and sin are formed once, unless the GPU
     // would be left with fewer than four CTAs per SM.
     g.heads = p.c.Hk;
@@ -362,12 +355,52 @@ kda_status launch_kv_append(const AppendParams &p, cudaStream_t st) {
     g.n_kv = (int)kv;
     size_t smem = (size_t)p.c.P * p.rot.R / 2 * sizeof(float2);
     if (p.q && smem < kRoom * sizeof(float2)) smem = kRoom * sizeof(float2);
+    if (smem > 32 * 1024) {
+        static DeviceOnce configured;
+        const int dev = current_device();
+        if (!configured.done(dev)) {
+            if (cudaFuncSetAttribute(append_run_kernel<THREADS, ITERS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     64 * 1024) != cudaSuccess) {
+                set_error("kv_append: cannot reserve shared memory: %s", cudaGetErrorString(cudaGetLastError()));
+                return KDA_ERR_CUDA;
+            }
+            configured.set(dev);
+        }
+    }
+    append_run_kernel<THREADS, ITERS><<<(unsigned)(kv + q_ctas), THREADS, smem, st>>>(p, g);
+    note_launch();
+    return check_launch("append_run_kernel");
+}
+
+}  // namespace
+
+kda_status launch_kv_append(const AppendParams &p, cudaStream_t st) {
+    if (p.tokens == 0) return KDA_OK;
+    Grid g;
+    if (!p.cu_seqlens) {
+        constexpr int kWarps = kStepThreads / 32;
+        g.q_tile = p.q ? rotary_tile_tokens(p.Hq, p.c.D, p.rot.R, 8, kStepThreads, kRoom) : 1;
+        if (g.q_tile > kRoom) g.q_tile = kRoom;
+        const int64_t q_ctas = p.q ? (p.tokens + g.q_tile - 1) / g.q_tile : 0;
+        const int64_t kv = ((int64_t)p.c.N * p.c.Hk * 2 + kWarps - 1) / kWarps;
+        g.n_kv = (int)kv;
+        g.heads = g.head_parts = 1;
+        const unsigned grid = (unsigned)(kv + q_ctas);
+        if (p.c.D == 128)
+            append_step_kernel<128><<<grid, kStepThreads, 0, st>>>(p, g);
+        else
+            append_step_kernel<64><<<grid, kStepThreads, 0, st>>>(p, g);
+        note_launch();
+        return check_launch("append_step_kernel");
+    }
+    // One or two 16-byte pieces of a page's rows per thread: 64 registers and full occupancy
+    // (four pieces took 127, and a third of the bandwidth).
     const int vecs = p.c.P * p.c.D / 8;
-    const unsigned grid = (unsigned)(kv + q_ctas);
-    if (vecs <= kThreads) return run<1>(p, g, grid, smem, st);
-    if (vecs <= 2 * kThreads) return run<2>(p, g, grid, smem, st);
-    if (vecs <= 4 * kThreads) return run<4>(p, g, grid, smem, st);
-    return run<8>(p, g, grid, smem, st);
+    if (vecs <= 128) return run<128, 1>(p, g, st);
+    if (vecs <= 256) return run<256, 1>(p, g, st);
+    if (vecs <= 512) return run<256, 2>(p, g, st);
+    if (vecs <= 1024) return run<512, 2>(p, g, st);
+    return run<1024, 2>(p, g, st);
 }
 
 }  // namespace kda
