@@ -262,12 +262,12 @@ constexpr float kE4m3Max = 448.f;
 constexpr int kScaleExpLo = -100, kScaleExpHi = 100;
 
 // Two values as e4m3 codes, round to nearest even.  The block's scale keeps finite values
-// within 448; an infinity becomes NaN (the type has none), as does a NaN.
+// within 448.  NaN stays NaN; an infinity has to become one (the type has none), which is
+// looked at only where a block holds one.
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-    if (isinf(a)) a = __int_as_float(0x7fc00000);
-    if (isinf(b)) b = __int_as_float(0x7fc00000);
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
+__device__ __forceinline__ float no_infinity(float x) { return isinf(x) ? __int_as_float(0x7fc00000) : x; }
 
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
 

@@ -76,35 +76,36 @@ __device__ __forceinline__ void rotate_queries(const AppendParams &p, int tile, 
                                THREADS);
 }
 
-// Channels [8v, 8v + 8) of a head's row, and in the half layout those of their partners.
-struct RowPiece {
-    uint4 own, other;
-};
-__device__ __forceinline__ int partner_of(int c0, const RotaryParams &r) {  // -1: none
-    const int half = r.R >> 1;
-    return r.interleaved || c0 >= r.R ? -1 : c0 >= half ? c0 - half : c0 + half;
-}
-__device__ __forceinline__ void turn_piece(const RowPiece &w, int v, const float2 *cs, const RotaryParams &r, float (&y)[8]) {
+// Channels [8v, 8v + 8) of a head's row w, turned with cs (null: as they are); the row's
+// pieces lie in consecutive lanes, so the half layout's partner comes from another lane.
+__device__ __forceinline__ void turn_piece(const uint4 &w, int v, const float2 *cs, const RotaryParams &r, float (&y)[8]) {
     using V = Vec16<__nv_bfloat16>;
-    V::load(w.own, y);
-    const int c0 = v * 8;
-    if (!cs || c0 >= r.R) return;
+    V::load(w, y);
+    if (!cs) return;  // for the whole warp
+    const int c0 = v * 8, half = r.R >> 1;
     if (r.interleaved) {
+        if (c0 >= r.R) return;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float a = y[2 * i], b = y[2 * i + 1];
             turn_pair(a, b, cs[v * 4 + i], r.magnitude, y[2 * i], y[2 * i + 1]);
         }
-    } else {
-        const int half = r.R >> 1;
-        const bool second = c0 >= half;
-        const int j = second ? c0 - half : c0;
-        float z[8];
-        V::load(w.other, z);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            y[i] = diff_of_products(y[i], cs[j + i].x, second ? -z[i] : z[i], cs[j + i].y) * r.magnitude;
+        return;
     }
+    const bool second = c0 >= half;
+    const int lane = threadIdx.x & 31, j = second ? c0 - half : c0;
+    const int from = c0 >= r.R ? lane : second ? lane - (half >> 3) : lane + (half >> 3);
+    uint4 o;
+    o.x = __shfl_sync(0xffffffffu, w.x, from);
+    o.y = __shfl_sync(0xffffffffu, w.y, from);
+    o.z = __shfl_sync(0xffffffffu, w.z, from);
+    o.w = __shfl_sync(0xffffffffu, w.w, from);
+    if (c0 >= r.R) return;
+    float z[8];
+    V::load(o, z);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        y[i] = diff_of_products(y[i], cs[j + i].x, second ? -z[i] : z[i], cs[j + i].y) * r.magnitude;
 }
 
 // The scale's exponent of a block whose new values reach amax; off: tokens it already holds.
@@ -116,7 +117,15 @@ __device__ __forceinline__ int block_exp(float amax, int off, int old) {
 // ---------------------------------------------------------------------------
 // runs (any number of tokens per sequence)
 
-template <int THREADS, int ITERS>
+// The queries of a long call, in a launch of their own: their CTAs need half the registers of
+// a run's.  (In one launch the eight prompts of [512, 16384] tokens took 442 us.)
+__global__ void __launch_bounds__(kStepThreads) append_queries_kernel(const __grid_constant__ AppendParams p, int q_tile) {
+    __shared__ float2 cs[kRoom];
+    __shared__ int s_pos[kRoom];
+    rotate_queries<kStepThreads>(p, blockIdx.x, q_tile, cs, s_pos);
+}
+
+template <int D, int THREADS, int ITERS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_run_kernel(const __grid_constant__ AppendParams p,
                                                                              const __grid_constant__ Grid g) {
     constexpr int kThreads = THREADS, kWarps = THREADS / 32;
@@ -130,7 +139,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_run_kernel(con
         rotate_queries<kThreads>(p, blockIdx.x - g.n_kv, g.q_tile, cs, s_pos);
         return;
     }
-    const int P = p.c.P, D = p.c.D, nv = D >> 3;
+    constexpr int nv = D >> 3;
+    const int P = p.c.P;
     const int values = blockIdx.x & 1, part = (blockIdx.x >> 1) % g.head_parts, unit = (blockIdx.x >> 1) / g.head_parts;
     // the unit-th run over all sequences
     if (tid == 0) s_seq = -1;
@@ -184,41 +194,43 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_run_kernel(con
         __syncthreads();
     }
     const int h0 = part * g.heads, h1 = min(h0 + g.heads, p.c.Hk), np = p.rot.R >> 1;
-    // this thread's pieces: token x / nv of the run, channels 8 (x % nv)
-    RowPiece raw[ITERS];
-    int old_next = kScaleExpLo;
-    auto fetch = [&](int h) {
+    // This thread's pieces: token x / nv of the run, channels 8 (x % nv).  Two heads' rows are
+    // on their way while a third is worked on: with one, each head took a memory latency.
+    constexpr int AHEAD = 2;
+    uint4 raw[AHEAD][ITERS];
+    int old_scale[AHEAD];
+    auto fetch = [&](int h, uint4 (&w)[ITERS], int &old) {
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
-            const int x = tid + i * kThreads, t = x / nv, v = x - t * nv;
-            if (t < n) {
-                const __nv_bfloat16 *row = src + t * stride + h * D;
-                raw[i].own = __ldg(reinterpret_cast<const uint4 *>(row + v * 8));
-                const int pc = turned ? partner_of(v * 8, p.rot) : -1;
-                if (pc >= 0) raw[i].other = __ldg(reinterpret_cast<const uint4 *>(row + pc));
-            }
+            const int x = tid + i * kThreads, t = x / nv, v = x % nv;
+            w[i] = h < h1 && t < n ? __ldg(reinterpret_cast<const uint4 *>(src + t * stride + h * D + v * 8)) : make_uint4(0, 0, 0, 0);
         }
         // a page that holds earlier tokens: its scale (no other CTA writes it)
-        if (off > 0 && page >= 0) old_next = exp_of_scale(scales[(int64_t)page * p.c.Hk + h]);
+        old = off > 0 && page >= 0 && h < h1 ? exp_of_scale(scales[(int64_t)page * p.c.Hk + h]) : kScaleExpLo;
     };
-    fetch(h0);
-    for (int h = h0; h < h1; ++h) {
+#pragma unroll
+    for (int b = 0; b < AHEAD; ++b) fetch(h0 + b, raw[b], old_scale[b]);
+    for (int hb = h0; hb < h1; hb += AHEAD)
+#pragma unroll
+    for (int b = 0; b < AHEAD; ++b) {
+        const int h = hb + b;
+        if (h >= h1) break;
         float y[ITERS][8];
         float amax = 0.f;
-        const int old = old_next;
+        const int old = old_scale[b];
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
-            const int x = tid + i * kThreads, t = x / nv, v = x - t * nv;
+            const int x = tid + i * kThreads, t = x / nv, v = x % nv;
+            turn_piece(raw[b][i], v, turned ? cs + min(t, n - 1) * np : nullptr, p.rot, y[i]);
             if (t < n) {
-                turn_piece(raw[i], v, turned ? cs + t * np : nullptr, p.rot, y[i]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(y[i][e]));
+                for (int e = 0; e < 8; e += 2) amax = fmaxf(fmaxf(amax, fabsf(y[i][e])), fabsf(y[i][e + 1]));  // no NaN
                 if (!values && p.k_out)
                     *reinterpret_cast<uint4 *>(p.k_out + ((t0 + t) * p.c.Hk + h) * D + v * 8) =
                         Vec16<__nv_bfloat16>::store(y[i]);
             }
         }
-        if (h + 1 < h1) fetch(h + 1);
+        fetch(h + AHEAD, raw[b], old_scale[b]);
         if (page < 0) continue;
         amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
         if (lane == 0) s_max[h & 1][warp] = amax;
@@ -226,6 +238,24 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_run_kernel(con
         __syncthreads();  // also: every thread has read this head's old scale
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, s_max[h & 1][w]);
+        if (isinf(amax)) {  // rare: the largest finite value, and NaN in the infinities' places
+            amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < ITERS; ++i)
+                if ((tid + i * kThreads) / nv < n) {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        amax = fmaxf(amax, finite_abs(y[i][x]));
+                        y[i][x] = no_infinity(y[i][x]);
+                    }
+                }
+            amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+            __syncthreads();
+            if (lane == 0) s_max[h & 1][warp] = amax;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, s_max[h & 1][w]);
+        }
         const int e = block_exp(amax, off, old);
         uint8_t *dst = codes + blk * P * D;
         if (off > 0 && e > old) {
@@ -309,7 +339,10 @@ __global__ void __launch_bounds__(kStepThreads) append_step_kernel(const __grid_
     if (page < 0) return;
     float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < C; ++i) amax = fmaxf(amax, finite_abs(y[i]));
+    for (int i = 0; i < C; ++i) {
+        amax = fmaxf(amax, finite_abs(y[i]));
+        y[i] = no_infinity(y[i]);
+    }
     amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
     const int64_t blk = (int64_t)page * p.c.Hk + h;
     float *scales = values ? p.c.v_scale : p.c.k_scale;
@@ -335,7 +368,7 @@ __global__ void __launch_bounds__(kStepThreads) append_step_kernel(const __grid_
         *reinterpret_cast<uint16_t *>(dst + (int64_t)off * D + c0 + i) = (uint16_t)e4m3x2(y[i] * inv, y[i + 1] * inv);
 }
 
-template <int THREADS, int ITERS>
+template <int D, int THREADS, int ITERS>
 kda_status run(const AppendParams &p, Grid g, cudaStream_t st) {
     // A sequence's n new tokens lie in at most n / P + 2 pages.
     const int64_t runs = p.tokens / p.c.P + 2 * (int64_t)p.c.N;
@@ -353,13 +386,15 @@ kda_status run(const AppendParams &p, Grid g, cudaStream_t st) {
         return KDA_ERR_UNSUPPORTED;
     }
     g.n_kv = (int)kv;
+    // two launches where the queries alone would be several waves of CTAs
+    const bool apart = q_ctas > 16ll * sm_count();
     size_t smem = (size_t)p.c.P * p.rot.R / 2 * sizeof(float2);
-    if (p.q && smem < kRoom * sizeof(float2)) smem = kRoom * sizeof(float2);
+    if (p.q && !apart && smem < kRoom * sizeof(float2)) smem = kRoom * sizeof(float2);
     if (smem > 32 * 1024) {
         static DeviceOnce configured;
         const int dev = current_device();
         if (!configured.done(dev)) {
-            if (cudaFuncSetAttribute(append_run_kernel<THREADS, ITERS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            if (cudaFuncSetAttribute(append_run_kernel<D, THREADS, ITERS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      64 * 1024) != cudaSuccess) {
                 set_error("kv_append: cannot reserve shared memory: %s", cudaGetErrorString(cudaGetLastError()));
                 return KDA_ERR_CUDA;
@@ -367,8 +402,17 @@ kda_status run(const AppendParams &p, Grid g, cudaStream_t st) {
             configured.set(dev);
         }
     }
-    append_run_kernel<THREADS, ITERS><<<(unsigned)(kv + q_ctas), THREADS, smem, st>>>(p, g);
+    append_run_kernel<D, THREADS, ITERS><<<(unsigned)(kv + (apart ? 0 : q_ctas)), THREADS, smem, st>>>(p, g);
     note_launch();
+    if (apart) {
+        const kda_status s = check_launch("append_run_kernel");
+        if (s != KDA_OK) return s;
+        int tile = rotary_tile_tokens(p.Hq, p.c.D, p.rot.R, 8, kStepThreads, kRoom);
+        if (tile > kRoom) tile = kRoom;
+        append_queries_kernel<<<(unsigned)((p.tokens + tile - 1) / tile), kStepThreads, 0, st>>>(p, tile);
+        note_launch();
+        return check_launch("append_queries_kernel");
+    }
     return check_launch("append_run_kernel");
 }
 
@@ -395,12 +439,16 @@ kda_status launch_kv_append(const AppendParams &p, cudaStream_t st) {
     }
     // One or two 16-byte pieces of a page's rows per thread: 64 registers and full occupancy
     // (four pieces took 127, and a third of the bandwidth).
-    const int vecs = p.c.P * p.c.D / 8;
-    if (vecs <= 128) return run<128, 1>(p, g, st);
-    if (vecs <= 256) return run<256, 1>(p, g, st);
-    if (vecs <= 512) return run<256, 2>(p, g, st);
-    if (vecs <= 1024) return run<512, 2>(p, g, st);
-    return run<1024, 2>(p, g, st);
+    if (p.c.D == 128) {
+        if (p.c.P == 16) return run<128, 256, 1>(p, g, st);
+        if (p.c.P == 32) return run<128, 256, 2>(p, g, st);
+        if (p.c.P == 64) return run<128, 512, 2>(p, g, st);
+        return run<128, 1024, 2>(p, g, st);
+    }
+    if (p.c.P == 16) return run<64, 128, 1>(p, g, st);
+    if (p.c.P == 32) return run<64, 256, 1>(p, g, st);
+    if (p.c.P == 64) return run<64, 256, 2>(p, g, st);
+    return run<64, 512, 2>(p, g, st);
 }
 
 }  // namespace kda
