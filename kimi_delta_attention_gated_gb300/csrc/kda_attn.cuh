@@ -101,15 +101,16 @@ __device__ __forceinline__ uint64_t turn_of(double inv_freq) {
 }
 
 // cos and sin of 2 pi * f / 2^64.  f is split into the nearest quarter turn and a rest of at
-// most 1/8 turn, held as an integer, so the rest's value is exact however small it is; it is
-// taken as a + d, a the fp32 value and d what that leaves out.  On |a| <= pi/4 the Taylor
-// series through a^10 and a^9 leave 1e-9; the last rounding is the only one that counts.
+// most 1/8 turn, taken to 2^-32 turns (1.5e-9 rad) as a + d, a the fp32 value and d what that
+// leaves out.  On |a| <= pi/4 the Taylor series through a^10 and a^9 leave 1e-9; the last
+// rounding is the only one that counts.
 __device__ __forceinline__ void cos_sin_turn(uint64_t f, float &c, float &s) {
-    const uint32_t quarter = (uint32_t)((f + (1ull << 61)) >> 62);
-    const int64_t rest = (int64_t)(f - ((uint64_t)quarter << 62));
-    constexpr float kHi = 3.4061215800304545e-19f;  // 2 pi / 2^64
-    constexpr float kLo = (float)(6.283185307179586 / 18446744073709551616.0 - (double)kHi);
-    const float hi = (float)rest, lo = (float)(rest - (int64_t)hi);
+    const uint32_t top = (uint32_t)(f >> 32);
+    const uint32_t quarter = (top + (1u << 29)) >> 30;  // 4 is 0 again
+    const int rest = (int)(top - (quarter << 30));
+    constexpr float kHi = 1.4629180792671596e-9f;  // 2 pi / 2^32
+    constexpr float kLo = (float)(6.283185307179586 / 4294967296.0 - (double)kHi);
+    const float hi = (float)rest, lo = (float)(rest - (int)hi);
     const float a = hi * kHi;
     const float d = fmaf(hi, kHi, -a) + fmaf(hi, kLo, lo * kHi);
     const float a2 = a * a;
@@ -125,7 +126,7 @@ __device__ __forceinline__ void cos_sin_turn(uint64_t f, float &c, float &s) {
     ps = fmaf(ps, a2, -1.f / 6.f);
     ps = a + fmaf(ps * a2, a, d);
     const float x = (quarter & 1) ? ps : pc, y = (quarter & 1) ? pc : ps;
-    c = (quarter == 1 || quarter == 2) ? -x : x;
+    c = ((quarter + 1) & 2) ? -x : x;
     s = (quarter & 2) ? -y : y;
 }
 
@@ -183,8 +184,12 @@ struct Vec16<float> {
     }
 };
 
-// cos / sin (times the sign) of `n` tokens' pairs into cs[token][pair]: a
-// thread keeps to one pair, so its turn is formed once.
+// Where the cos / sin of pair j lie within a token's np pairs: eight consecutive pairs are
+// read by one lane, two at a time, so pairs 8v + 2k, 8v + 2k + 1 of all v lie together.
+__device__ __forceinline__ int cs_at(int j, int np) { return ((j >> 1) & 3) * (np >> 2) + (j >> 3) * 2 + (j & 1); }
+
+// cos / sin (times the sign) of `n` tokens' pairs into cs[token * np + cs_at(pair)]: a thread
+// keeps to one pair, so its turn is formed once.
 template <typename PosFn>
 __device__ __forceinline__ void fill_cos_sin(float2 *cs, const RotaryParams &r, int n, PosFn pos, int tid, int threads) {
     const int np = r.R >> 1;
@@ -192,10 +197,25 @@ __device__ __forceinline__ void fill_cos_sin(float2 *cs, const RotaryParams &r, 
     const int rows = threads / np, j = tid % np, row = tid / np;
     if (row >= rows) return;
     const uint64_t turn = turn_of(__ldg(r.inv_freq + j));
+    cs += cs_at(j, np);
     for (int t = row; t < n; t += rows) {
         float c, s;
         cos_sin_turn((uint64_t)(int64_t)pos(t) * turn, c, s);
-        cs[t * np + j] = make_float2(c, s * r.sign);
+        cs[t * np] = make_float2(c, s * r.sign);
+    }
+}
+
+// The same for n tokens at consecutive positions: the angle goes on by an integer addition.
+__device__ __forceinline__ void fill_cos_sin_run(float2 *cs, const RotaryParams &r, int n, int pos0, int tid, int threads) {
+    const int np = r.R >> 1, rows = threads / np, j = tid % np, row = tid / np;
+    if (row >= rows) return;
+    const uint64_t turn = turn_of(__ldg(r.inv_freq + j)), step = turn * (uint64_t)rows;
+    uint64_t f = (uint64_t)(int64_t)(pos0 + row) * turn;
+    cs += cs_at(j, np);
+    for (int t = row; t < n; t += rows, f += step) {
+        float c, s;
+        cos_sin_turn(f, c, s);
+        cs[t * np] = make_float2(c, s * r.sign);
     }
 }
 
@@ -208,6 +228,7 @@ __host__ __device__ __forceinline__ int rotary_units(int D, int R, int interleav
 // Unit u of one head: x -> y.
 template <typename T>
 __device__ __forceinline__ void rotate_unit(const T *x, T *y, const float2 *cs, int u, int R, int interleaved, float mag) {
+    const int np = R >> 1;
     using V = Vec16<T>;
     constexpr int N = V::N;
     const int nrot = interleaved ? R / N : R / (2 * N);
@@ -221,7 +242,7 @@ __device__ __forceinline__ void rotate_unit(const T *x, T *y, const float2 *cs, 
         V::load(*reinterpret_cast<const uint4 *>(x + u * N), a);
         float o[N];
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) turn_pair(a[2 * i], a[2 * i + 1], cs[u * (N / 2) + i], mag, o[2 * i], o[2 * i + 1]);
+        for (int i = 0; i < N / 2; ++i) turn_pair(a[2 * i], a[2 * i + 1], cs[cs_at(u * (N / 2) + i, np)], mag, o[2 * i], o[2 * i + 1]);
         *reinterpret_cast<uint4 *>(y + u * N) = V::store(o);
     } else {
         float b[N], oa[N], ob[N];
@@ -230,7 +251,7 @@ __device__ __forceinline__ void rotate_unit(const T *x, T *y, const float2 *cs, 
         V::load(wa, a);
         V::load(wb, b);
 #pragma unroll
-        for (int i = 0; i < N; ++i) turn_pair(a[i], b[i], cs[u * N + i], mag, oa[i], ob[i]);
+        for (int i = 0; i < N; ++i) turn_pair(a[i], b[i], cs[cs_at(u * N + i, np)], mag, oa[i], ob[i]);
         *reinterpret_cast<uint4 *>(y + u * N) = V::store(oa);
         *reinterpret_cast<uint4 *>(y + u * N + R / 2) = V::store(ob);
     }

@@ -82,13 +82,13 @@ __device__ __forceinline__ void turn_piece(const uint4 &w, int v, const float2 *
     using V = Vec16<__nv_bfloat16>;
     V::load(w, y);
     if (!cs) return;  // for the whole warp
-    const int c0 = v * 8, half = r.R >> 1;
+    const int c0 = v * 8, half = r.R >> 1, np = half;
     if (r.interleaved) {
         if (c0 >= r.R) return;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float a = y[2 * i], b = y[2 * i + 1];
-            turn_pair(a, b, cs[v * 4 + i], r.magnitude, y[2 * i], y[2 * i + 1]);
+            turn_pair(a, b, cs[cs_at(v * 4 + i, np)], r.magnitude, y[2 * i], y[2 * i + 1]);
         }
         return;
     }
@@ -104,8 +104,10 @@ __device__ __forceinline__ void turn_piece(const uint4 &w, int v, const float2 *
     float z[8];
     V::load(o, z);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        y[i] = diff_of_products(y[i], cs[j + i].x, second ? -z[i] : z[i], cs[j + i].y) * r.magnitude;
+    for (int i = 0; i < 8; ++i) {
+        const float2 w2 = cs[cs_at(j + i, np)];
+        y[i] = diff_of_products(y[i], w2.x, second ? -z[i] : z[i], w2.y) * r.magnitude;
+    }
 }
 
 // The scale's exponent of a block whose new values reach amax; off: tokens it already holds.
@@ -189,10 +191,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_run_kernel(con
     uint8_t *codes = values ? p.c.v : p.c.k;
     float *scales = values ? p.c.v_scale : p.c.k_scale;
     const bool turned = !values && p.rot.R > 0;
-    if (turned) {
-        fill_cos_sin(cs, p.rot, n, [&](int t) { return (int)(pos0 + t); }, tid, kThreads);
-        __syncthreads();
-    }
     const int h0 = part * g.heads, h1 = min(h0 + g.heads, p.c.Hk), np = p.rot.R >> 1;
     // This thread's pieces: token x / nv of the run, channels 8 (x % nv).  Two heads' rows are
     // on their way while a third is worked on: with one, each head took a memory latency.
@@ -210,6 +208,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_run_kernel(con
     };
 #pragma unroll
     for (int b = 0; b < AHEAD; ++b) fetch(h0 + b, raw[b], old_scale[b]);
+    if (turned) {
+        fill_cos_sin_run(cs, p.rot, n, (int)pos0, tid, kThreads);
+        __syncthreads();
+    }
     for (int hb = h0; hb < h1; hb += AHEAD)
 #pragma unroll
     for (int b = 0; b < AHEAD; ++b) {
