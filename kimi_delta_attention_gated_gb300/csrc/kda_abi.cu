@@ -473,6 +473,8 @@ kda_status check_cache_args(const char *fn, const void *k, const void *v, const 
                 q_heads, kv_heads);
     KDA_REQUIRE(n_seqs <= 65535 && kv_heads <= 65535 && q_heads <= (1 << 20), KDA_ERR_UNSUPPORTED,
                 "%s: at most 65535 sequences and heads", fn);
+    KDA_REQUIRE((int64_t)num_pages * kv_heads * page_size <= INT32_MAX - 256, KDA_ERR_UNSUPPORTED,
+                "%s: num_pages * kv_heads * page_size must stay below 2^31 - 256", fn);
     KDA_REQUIRE((int64_t)max_blocks * page_size <= INT32_MAX - 256, KDA_ERR_INVALID_ARG,
                 "%s: max_blocks * page_size must stay below 2^31 - 256", fn);
     KDA_REQUIRE(aligned16(k) && aligned16(v), KDA_ERR_INVALID_ARG, "%s: the cache must be 16-byte aligned", fn);
@@ -556,13 +558,14 @@ kda_status kda_device_status(void *stream) {
     const int n_dec = kda::take_decode_timeouts(st);
     const int n_conv = kda::take_short_conv_timeouts(st);
     const int n_proj = kda::take_oproj_timeouts(st);
-    const int n_attn = kda::take_attn_prompt_timeouts(st);
-    if (n_tc0 < 0 || n_prep < 0 || n_chain < 0 || n_dec < 0 || n_conv < 0 || n_proj < 0 || n_attn < 0)
+    const int n_attn_p = kda::take_attn_prompt_timeouts(st), n_attn_d = kda::take_attn_decode_timeouts(st);
+    if (n_tc0 < 0 || n_prep < 0 || n_chain < 0 || n_dec < 0 || n_conv < 0 || n_proj < 0 || n_attn_p < 0 || n_attn_d < 0)
         return KDA_ERR_CUDA;
+    const int n_attn = n_attn_p + n_attn_d;
     const int n_tc = n_tc0 + n_prep + n_chain;
     if (n_tc + n_dec + n_conv + n_proj + n_attn > 0) {
         set_error("kda_device_status: bounded waits gave up in %d prefill, %d decode, %d short-convolution, %d "
-                  "output-projection and %d prompt-attention CTAs; their outputs hold NaN",
+                  "output-projection and %d attention CTAs; their outputs hold NaN",
                   n_tc, n_dec, n_conv, n_proj, n_attn);
         return KDA_ERR_TIMEOUT;
     }

@@ -76,6 +76,7 @@ size_t attn_decode_workspace_bytes(int Hq, int Hk, int D);
 kda_status launch_attn_decode(const DecodeParams &p, cudaStream_t st);
 kda_status launch_attn_prompt(const PromptParams &p, cudaStream_t st);
 int take_attn_prompt_timeouts(cudaStream_t st);
+int take_attn_decode_timeouts(cudaStream_t st);
 
 // ---------------------------------------------------------------------------
 // angles

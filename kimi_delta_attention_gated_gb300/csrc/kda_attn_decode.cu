@@ -18,30 +18,38 @@
 // summed for the denominator and e_j * vs_j <= 2^kSlack is rounded to f16 for the product,
 // so pages of very different scales share one accumulator.
 //
-// Work split.  All (sequence, head, 16 tokens) steps are numbered in one line, and the line
-// is cut into equal pieces, one per CTA, whatever the lengths of the sequences are; every
-// CTA finds its piece from the lengths on the device.  A head that one CTA covers is written
-// at once, the others go through a workspace and attn_decode_join_kernel, which adds a
-// head's pieces in their order, so results do not depend on timing.
+// Work split.  All (sequence, head, 32 tokens) steps are numbered in one line, kPad places
+// before each head standing for what a head costs beside its steps, and the line is cut into
+// equal pieces, one per CTA, whatever the lengths of the sequences are; every CTA finds its
+// piece from the lengths on the device.  A head that one CTA covers is written at once, the
+// others go through a workspace and attn_decode_join_kernel, which adds a head's pieces in
+// their order, so results do not depend on timing.
 //
-// Copies.  Each lane copies exactly the bytes it will use (cp.async) into a ring of its own
-// in shared memory, kDepth steps ahead and across the borders of heads: no barrier and no
-// bank conflict between the copy and its use.
+// Copies.  Each warp has a ring of steps in shared memory, filled by TMA ahead of their use
+// and across the borders of heads, without a barrier between warps.  The swizzle of the rows
+// and the choice of the pieces a lane takes leave no bank conflict (64-channel values: two
+// ways).  With 16-byte copies by each lane (cp.async) the load and store pipe was the bound:
+// 148 us for 256 sequences of about 1000 tokens against XXX.
+#include <cuda.h>
 #include <cuda_fp16.h>
 
 #include "kda_attn.cuh"
+#include "kda_chunk_common.cuh"
+#include "kda_tc_ptx.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStep = 16;       // tokens of a step
-constexpr int kDepth = 3;       // steps in flight per warp
-constexpr int kMinSteps = 8;    // steps of a CTA at least
+constexpr int kStep = 32;       // tokens of a step
+constexpr int kPad = 6;         // a head's own cost in steps
+constexpr int kMinPiece = 12;   // places of a CTA at least
+constexpr uint32_t kPolls = 1u << 21;  // bound on a copy's wait: a few seconds
 constexpr float kSlack = 8.f;   // the maximum in use may lie this far below the true one (log2)
-constexpr int kCtasPerSm = 3;
 constexpr float kNegInf = -INFINITY;
+
+__device__ int g_attn_decode_timeouts = 0;
 
 template <int D, int NT>
 struct Cfg {
@@ -49,21 +57,20 @@ struct Cfg {
     static constexpr int KJ = D / 64;                   // 64-byte pieces of a key row
     static constexpr int VB = D / 8;                    // bytes of a value row per lane
     static constexpr int MT = D / 16;                   // 16-channel tiles of the output
-    static constexpr int KBYTES = kStep * D, VBYTES = kStep * D;
-    static constexpr int SLOT = KBYTES + VBYTES + 16;   // + the two scales
+    static constexpr int DEPTH = D == 128 ? 2 : 4;      // steps of a warp in flight
+    static constexpr int HALF = 16 * D;                 // bytes of 16 rows
+    static constexpr int KBYTES = kStep * D;            // a step's keys, then as many of values
+    static constexpr int SLOT = 2 * KBYTES;
     static constexpr int PITCH = D + 4;                 // fp32 row of the merge buffer
-    static constexpr int RING = kWarps * kDepth * SLOT;
-    static constexpr int MERGE = kWarps * ROWS * (PITCH + 2) * 4;
-    static constexpr int SMEM = RING + MERGE;
+    static constexpr int RING = kWarps * DEPTH * SLOT;
+    static constexpr int SCALES = RING;                 // [warp][slot] {k, v of rows 0-15; of 16-31}
+    static constexpr int BARS = SCALES + kWarps * DEPTH * 16;
+    static constexpr int MERGE = BARS + kWarps * DEPTH * 8;
+    static constexpr int SMEM = MERGE + 2 * ROWS * (PITCH + 2) * 4 + 1024;  // the ring starts on 1024 bytes
+    static constexpr int CTAS = D == 128 && NT == 2 ? 2 : 3;  // per SM, by shared memory
     static constexpr int PART = ROWS * (D + 2);         // floats of one piece in the workspace
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp8(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void cp4(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -73,14 +80,11 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Two e4m3 codes (the low / high half of w) as f16.
-__device__ __forceinline__ uint32_t widen_lo(uint32_t w) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
-}
-__device__ __forceinline__ uint32_t widen_hi(uint32_t w) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
+// The four e4m3 codes of w as two pairs of f16.
+__device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
@@ -116,12 +120,14 @@ __device__ __forceinline__ int tokens_of(const PagedCache &c, int n) {
 }
 __device__ __forceinline__ int steps_of(const PagedCache &c, int n) { return (tokens_of(c, n) + kStep - 1) / kStep; }
 
-// The line of steps: sequence n's U units (head, part of its group) lie one after another,
-// each steps_of(n) long, behind those of the sequences before.  Returns the steps of all
-// sequences (of one unit each) to every thread, and this thread's share of the prefix.
+// Places of one unit (head, part of its group) of a sequence on the line.
+__device__ __forceinline__ int places_of(int steps) { return steps ? steps + kPad : 0; }
+
+// The line: sequence n's U units lie one after another, each places_of(steps) long, behind
+// those of the sequences before.
 struct Line {
-    int64_t total;  // steps of all sequences, one unit each
-    int64_t mine;   // those before this thread's first sequence
+    int64_t total;    // places of all sequences, one unit each
+    int64_t mine;     // those before this thread's first sequence
     int first, last;  // this thread's sequences [first, last)
 };
 __device__ __forceinline__ Line measure_line(const PagedCache &c, int64_t *scan) {
@@ -131,7 +137,7 @@ __device__ __forceinline__ Line measure_line(const PagedCache &c, int64_t *scan)
     l.first = min(tid * per, c.N);
     l.last = min(l.first + per, c.N);
     int64_t own = 0;
-    for (int n = l.first; n < l.last; ++n) own += steps_of(c, n);
+    for (int n = l.first; n < l.last; ++n) own += places_of(steps_of(c, n));
     int64_t x = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -148,19 +154,27 @@ __device__ __forceinline__ Line measure_line(const PagedCache &c, int64_t *scan)
     }
     return l;
 }
-__device__ __forceinline__ int64_t piece_steps(int64_t line, int ctas) {
+__device__ __forceinline__ int64_t piece_places(int64_t line, int ctas) {
     const int64_t s = (line + ctas - 1) / ctas;
-    return s < kMinSteps ? kMinSteps : s;
+    return s < kMinPiece ? kMinPiece : s;
 }
 
-// A run of steps within one unit: [s0, s1) of unit u of sequence n.
+// A run of places within one unit, and its steps [s0, s1) (none where it lies in the padding).
 struct Segment {
     int n, u, steps, len;
     int s0, s1;
+    int head;    // key/value head of unit u
+    int places;  // of the line
 };
+__device__ __forceinline__ void set_range(Segment &g, int from, int64_t left) {
+    const int to = (int)min((int64_t)places_of(g.steps), from + left);
+    g.places = to - from;
+    g.s0 = max(from - kPad, 0);
+    g.s1 = max(to - kPad, 0);
+}
 
-// The segment that follows g on the line, with `left` steps of the piece behind it.
-__device__ __forceinline__ void next_segment(const PagedCache &c, int U, int64_t left, Segment &g) {
+// The segment that follows g on the line, with `left` places of the piece behind g.
+__device__ __forceinline__ void next_segment(const PagedCache &c, int U, int parts, int64_t left, Segment &g) {
     if (++g.u == U) {
         g.u = 0;
         do {  // left > 0: a sequence with steps follows
@@ -169,14 +183,16 @@ __device__ __forceinline__ void next_segment(const PagedCache &c, int U, int64_t
         } while (g.len == 0);
         g.steps = (g.len + kStep - 1) / kStep;
     }
-    g.s0 = 0;
-    g.s1 = (int)min((int64_t)g.steps, left);
+    g.head = parts == 1 ? g.u : g.u / parts;
+    set_range(g, 0, left);
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel(
+    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const __grid_constant__ DecodeParams p) {
     using F = Cfg<D, NT>;
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ int64_t s_scan[kWarps];
     __shared__ Segment s_seg;
     const PagedCache &c = p.c;
@@ -186,34 +202,40 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // this CTA's piece of the line
     const Line line = measure_line(c, s_scan);
-    const int64_t steps_all = line.total * U, S = piece_steps(steps_all, gridDim.x), L0 = (int64_t)blockIdx.x * S;
-    if (L0 >= steps_all) return;
-    const int64_t L1 = min(L0 + S, steps_all);
+    const int64_t all = line.total * U, S = piece_places(all, gridDim.x), L0 = (int64_t)blockIdx.x * S;
+    if (L0 >= all) return;
+    const int64_t L1 = min(L0 + S, all);
     {
         int64_t at = line.mine;  // one thread's range holds the start
         for (int n = line.first; n < line.last; ++n) {
-            const int len = tokens_of(c, n), st = (len + kStep - 1) / kStep;
-            if (st > 0 && L0 >= at * U && L0 < (at + st) * U) {
+            const int len = tokens_of(c, n), st = (len + kStep - 1) / kStep, pl = places_of(st);
+            if (st > 0 && L0 >= at * U && L0 < (at + pl) * U) {
                 const int64_t in = L0 - at * U;
                 Segment x;
                 x.n = n;
                 x.len = len;
                 x.steps = st;
-                x.u = (int)(in / st);
-                x.s0 = (int)(in - (int64_t)x.u * st);
-                x.s1 = (int)min((int64_t)st, x.s0 + (L1 - L0));
+                x.u = (int)(in / pl);
+                x.head = x.u / parts;
+                set_range(x, (int)(in - (int64_t)x.u * pl), L1 - L0);
                 s_seg = x;
             }
-            at += st;
+            at += pl;
         }
+    }
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + F::BARS) + warp * F::DEPTH;  // this warp's slots
+    if (lane == 0) {
+        for (int i = 0; i < F::DEPTH; ++i) tc::mbar_init(bars + i, 1);
+        tc::fence_mbar_init();
     }
     __syncthreads();
     Segment cur = s_seg;
 
-    // ---- the copying side: this warp's steps, kDepth ahead
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * kDepth * F::SLOT;
+    // ---- the copying side: this warp's steps, F::DEPTH ahead
+    const uint32_t ring = tc::smem_u32(smem) + warp * F::DEPTH * F::SLOT;
+    const uint32_t scales_at = tc::smem_u32(smem) + F::SCALES + warp * F::DEPTH * 16;
     Segment ld = cur;
-    int64_t ld_left = L1 - L0 - (cur.s1 - cur.s0);  // steps of the piece behind ld's segment
+    int64_t ld_left = L1 - L0 - cur.places;  // of the piece, behind ld's segment
     int ld_s = ld.s0 + warp;
     bool ld_more = true;
     auto settle = [&] {  // moves on to the segment that holds this warp's next step
@@ -222,63 +244,76 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
                 ld_more = false;
                 return;
             }
-            next_segment(c, U, ld_left, ld);
-            ld_left -= ld.s1 - ld.s0;
+            next_segment(c, U, parts, ld_left, ld);
+            ld_left -= ld.places;
             ld_s = ld.s0 + warp;
         }
     };
-    auto page_at = [&]() { return __ldg(c.block_table + (int64_t)ld.n * c.max_blocks + ld_s * kStep / c.P); };
+    // A step's rows lie in one page, or with pages of 16 in two.  Lanes 0, 1 hold the first half's
+    // page and fetch its two scales, lanes 2, 3 the second half's (-1 where there is none).
+    const bool small = c.p_shift == 4;
+    const int page_log = c.p_shift - 5, in_page = (1 << max(page_log, 0)) - 1;
+    auto page_at = [&]() {
+        const int half = lane >> 1;
+        const int blk = small ? 2 * ld_s + half : ld_s >> page_log;
+        return lane < 4 && (ld_s * 2 + half) * 16 < ld.len ? __ldg(c.block_table + (int64_t)ld.n * c.max_blocks + blk) : -1;
+    };
     settle();
-    int page = ld_more ? page_at() : 0;
-    int wr = 0;
+    int page = ld_more ? page_at() : -1;
+    int wr = 0, issued = 0;
     auto copy_step = [&] {
         if (ld_more) {
+            const bool good = (uint32_t)page < (uint32_t)c.n_pages;
             const uint32_t slot = ring + wr * F::SLOT;
-            const bool good = page >= 0 && page < c.n_pages;
-            const int64_t blk = (int64_t)(good ? page : 0) * c.Hk + ld.u / parts;
-            const int tok0 = ld_s * kStep, valid = good ? ld.len - tok0 : 0;  // tokens of the step that exist
-            const int64_t base = (blk * c.P + tok0 % c.P) * D;
-            const uint8_t *k = c.k + base, *v = c.v + base;
-#pragma unroll
-            for (int j = 0; j < F::KJ; ++j) {
-                cp16(slot + (2 * j) * 512 + lane * 16, k + g * D + 64 * j + 16 * t, g < valid ? 16 : 0);
-                cp16(slot + (2 * j + 1) * 512 + lane * 16, k + (g + 8) * D + 64 * j + 16 * t, g + 8 < valid ? 16 : 0);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int tok = 2 * t + (i & 1) + (i >> 1) * 8;
-                const uint32_t dst = slot + F::KBYTES + i * (32 * F::VB) + lane * F::VB;
-                if (F::VB == 16)
-                    cp16(dst, v + tok * D + 16 * g, tok < valid ? 16 : 0);
-                else
-                    cp8(dst, v + tok * D + 8 * g, tok < valid ? 8 : 0);
-            }
-            if (lane < 2) {
-                const uint32_t dst = slot + F::KBYTES + F::VBYTES + lane * 4;
+            if (lane < 4) {
+                const uint32_t dst = scales_at + wr * 16 + lane * 4;
                 if (good)
-                    cp4(dst, (lane ? c.v_scale : c.k_scale) + blk);
+                    cp4(dst, ((lane & 1) ? c.v_scale : c.k_scale) + (int64_t)page * c.Hk + ld.head);
                 else  // no such page: its tokens' scores are NaN, and so is the output
                     asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst), "f"(__int_as_float(0x7fc00000)) : "memory");
             }
+            const int row = good ? ((int)(((int64_t)page * c.Hk + ld.head) << c.p_shift)) + (small ? 0 : (ld_s & in_page) << 5) : -1;
+            const int row2 = __shfl_sync(0xffffffffu, row, 2);
+            if (lane == 0) {
+                const int rows = (row >= 0 ? small ? 16 : 32 : 0) + (small && row2 >= 0 ? 16 : 0);
+                tc::mbar_arrive_expect_tx(bars + wr, rows * 2 * D);
+                if (row >= 0) {
+                    tc::tma_load_2d(slot, &map_k, bars + wr, 0, row);
+                    tc::tma_load_2d(slot + F::KBYTES, &map_v, bars + wr, 0, row);
+                }
+                if (small && row2 >= 0) {
+                    tc::tma_load_2d(slot + F::HALF, &map_k, bars + wr, 0, row2);
+                    tc::tma_load_2d(slot + F::KBYTES + F::HALF, &map_v, bars + wr, 0, row2);
+                }
+            }
+            ++issued;
             ld_s += kWarps;
-            settle();
+            if (ld_s >= ld.s1) settle();
             if (ld_more) page = page_at();  // the next step's page number is on its way meanwhile
-            wr = wr + 1 == kDepth ? 0 : wr + 1;
+            wr = wr + 1 == F::DEPTH ? 0 : wr + 1;
         }
         cp_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) copy_step();
+    for (int i = 0; i < F::DEPTH; ++i) copy_step();
 
     // ---- the computing side
-    float *merge = reinterpret_cast<float *>(smem + F::RING);  // [warp][row][PITCH] sums, then M and l
-    float *merge_m = merge + kWarps * F::ROWS * F::PITCH, *merge_l = merge_m + kWarps * F::ROWS;
+    float *merge = reinterpret_cast<float *>(smem + F::MERGE);  // [2][row][PITCH] sums, then M and l
+    float *merge_m = merge + 2 * F::ROWS * F::PITCH, *merge_l = merge_m + 2 * F::ROWS;
     const float log2e_scale = p.scale * 1.4426950408889634f;
     int64_t left = L1 - L0;
-    int rd = 0;
+    // where this lane's pieces of a step lie: 16-byte piece x of row r is at x ^ (r % 8) of its 128
+    // bytes, or at x ^ (r / 2 % 4) of 64
+    const int k_at[2] = {D == 128 ? g * 128 + (((2 * t) ^ g) << 4) : g * 64 + ((t ^ (g >> 1)) << 4),
+                         g * 128 + (((2 * t + 1) ^ g) << 4)};
+    const int v_at[2] = {D == 128 ? 2 * t * 128 + ((g ^ (2 * t)) << 4) : 2 * t * 64 + (((g >> 1) ^ t) << 4) + 8 * (g & 1),
+                         D == 128 ? (2 * t + 1) * 128 + ((g ^ (2 * t + 1)) << 4)
+                                  : (2 * t + 1) * 64 + (((g >> 1) ^ t) << 4) + 8 * (g & 1)};
+    int rd = 0, failed = 0;
+    uint32_t rd_phase = 0;
     bool first = true;
     while (true) {
-        const int h = cur.u / parts, r0 = (cur.u - h * parts) * F::ROWS;  // first query head of the unit in its group
+        const int h = cur.head, r0 = (cur.u - h * parts) * F::ROWS;  // first query head of the unit in its group
         // queries: f16, each row scaled by a power of two to at most 2 so that nothing overflows
         uint32_t qf[NT][F::KJ * 4][2];
         float row_scale[NT][2];  // of the two rows whose scores this lane holds
@@ -292,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
             for (int j = 0; j < F::KJ; ++j)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    w[j][i] = r < group ? __ldg(reinterpret_cast<const uint4 *>(q + 64 * j + 16 * t + 8 * i))
+                    w[j][i] = r < group ? __ldg(reinterpret_cast<const uint4 *>(q + 16 * (F::KJ * t + j) + 8 * i))
                                         : make_uint4(0, 0, 0, 0);
                     const uint32_t u[4] = {w[j][i].x, w[j][i].y, w[j][i].z, w[j][i].w};
 #pragma unroll
@@ -328,46 +363,66 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
             l[nt][0] = l[nt][1] = 0.f;
         }
         for (int s = cur.s0 + warp; s < cur.s1; s += kWarps) {
-            copy_step();
-            cp_wait<kDepth - 1>();
+            cp_wait<F::DEPTH - 1>();
+            if (!tc::mbar_wait(bars + rd, rd_phase, kPolls)) failed = 1;
             __syncwarp();
-            const uint8_t *slot = smem + (warp * kDepth + rd) * F::SLOT;
-            rd = rd + 1 == kDepth ? 0 : rd + 1;
-            const float2 sc = *reinterpret_cast<const float2 *>(slot + F::KBYTES + F::VBYTES);
-            float S[NT][4] = {};
+            const uint8_t *slot = smem + (warp * F::DEPTH + rd) * F::SLOT;
+            const float4 sc = *reinterpret_cast<const float4 *>(smem + F::SCALES + (warp * F::DEPTH + rd) * 16);
+            const float ks[2] = {sc.x, sc.z}, vs[2] = {sc.y, sc.w};
+            float S[2][NT][4] = {};
 #pragma unroll
-            for (int j = 0; j < F::KJ; ++j) {
-                const uint4 a = *reinterpret_cast<const uint4 *>(slot + (2 * j) * 512 + lane * 16);
-                const uint4 b = *reinterpret_cast<const uint4 *>(slot + (2 * j + 1) * 512 + lane * 16);
-                const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+            for (int j = 0; j < F::KJ; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t a0 = widen_lo(wa[i]), a1 = widen_lo(wb[i]), a2 = widen_hi(wa[i]), a3 = widen_hi(wb[i]);
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 a = *reinterpret_cast<const uint4 *>(slot + h * F::HALF + k_at[j]);
+                    const uint4 b = *reinterpret_cast<const uint4 *>(slot + h * F::HALF + F::HALF / 2 + k_at[j]);
+                    const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16(S[nt], a0, a1, a2, a3, qf[nt][4 * j + i][0], qf[nt][4 * j + i][1]);
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t a0, a1, a2, a3;
+                        widen(wa[i], a0, a2);
+                        widen(wb[i], a1, a3);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_f16(S[h][nt], a0, a1, a2, a3, qf[nt][4 * j + i][0], qf[nt][4 * j + i][1]);
+                    }
                 }
-            }
-            const int tok0 = s * kStep;
-            const bool in0 = tok0 + g < cur.len, in1 = tok0 + g + 8 < cur.len;
-            // reference of the value scale: its binary exponent
-            const float ev = (float)((int)((__float_as_uint(sc.y) >> 23) & 0xFFu) - 127);
-            uint32_t pb[NT][2];
+            const bool tail = (s + 1) * kStep > cur.len;  // places behind the last token
             bool over = false;
+            float ev[2];  // reference of the value scale: its binary exponent
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float c0 = row_scale[nt][0] * sc.x, c1 = row_scale[nt][1] * sc.x;
-                S[nt][0] = in0 ? S[nt][0] * c0 : kNegInf;
-                S[nt][1] = in0 ? S[nt][1] * c1 : kNegInf;
-                S[nt][2] = in1 ? S[nt][2] * c0 : kNegInf;
-                S[nt][3] = in1 ? S[nt][3] * c1 : kNegInf;
-                over |= fmaxf(S[nt][0], S[nt][2]) + ev > M[nt][0] + kSlack || fmaxf(S[nt][1], S[nt][3]) + ev > M[nt][1] + kSlack;
+            for (int h = 0; h < 2; ++h) {
+                ev[h] = (float)((int)((__float_as_uint(vs[h]) >> 23) & 0xFFu) - 127);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float c0 = row_scale[nt][0] * ks[h], c1 = row_scale[nt][1] * ks[h];
+                    S[h][nt][0] *= c0;
+                    S[h][nt][1] *= c1;
+                    S[h][nt][2] *= c0;
+                    S[h][nt][3] *= c1;
+                }
+                if (tail) {
+                    const int tok = s * kStep + 16 * h + g;
+                    if (s * kStep + 16 * h >= cur.len) ev[h] = kNegInf;  // this half's scales stand for nothing
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        S[h][nt][0] = tok < cur.len ? S[h][nt][0] : kNegInf;
+                        S[h][nt][1] = tok < cur.len ? S[h][nt][1] : kNegInf;
+                        S[h][nt][2] = tok + 8 < cur.len ? S[h][nt][2] : kNegInf;
+                        S[h][nt][3] = tok + 8 < cur.len ? S[h][nt][3] : kNegInf;
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    over |= fmaxf(S[h][nt][0], S[h][nt][2]) > M[nt][0] + (kSlack - ev[h]) ||
+                            fmaxf(S[h][nt][1], S[h][nt][3]) > M[nt][1] + (kSlack - ev[h]);
             }
             if (__any_sync(0xffffffffu, over)) {  // raise the maximum and bring the sums to it
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float m = fmaxf(S[nt][e], S[nt][e + 2]) + ev;
+                        float m = fmaxf(fmaxf(S[0][nt][e], S[0][nt][e + 2]) + ev[0], fmaxf(S[1][nt][e], S[1][nt][e + 2]) + ev[1]);
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -383,111 +438,167 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
                     }
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float m0 = M[nt][0] == kNegInf ? 0.f : M[nt][0], m1 = M[nt][1] == kNegInf ? 0.f : M[nt][1];
-                const float e0 = ex2(S[nt][0] - m0), e1 = ex2(S[nt][1] - m1), e2 = ex2(S[nt][2] - m0), e3 = ex2(S[nt][3] - m1);
-                l[nt][0] += e0 + e2;
-                l[nt][1] += e1 + e3;
-                pb[nt][0] = transpose8(pack_half(e0 * sc.y, e1 * sc.y));
-                pb[nt][1] = transpose8(pack_half(e2 * sc.y, e3 * sc.y));
-            }
-            const uint8_t *vs = slot + F::KBYTES + lane * F::VB;
-            uint32_t vw[4][F::VB / 4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (F::VB == 16) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(vs + i * 32 * F::VB);
-                    vw[i][0] = x.x;
-                    vw[i][1] = x.y;
-                    vw[i][F::VB / 4 - 2] = x.z;
-                    vw[i][F::VB / 4 - 1] = x.w;
-                } else {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(vs + i * 32 * F::VB);
-                    vw[i][0] = x.x;
-                    vw[i][1] = x.y;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < F::VB / 4; ++i) {
-                const uint32_t x = __byte_perm(vw[0][i], vw[1][i], 0x5140), y = __byte_perm(vw[0][i], vw[1][i], 0x7362);
-                const uint32_t z = __byte_perm(vw[2][i], vw[3][i], 0x5140), w = __byte_perm(vw[2][i], vw[3][i], 0x7362);
-                const uint32_t x0 = widen_lo(x), x1 = widen_hi(x), z0 = widen_lo(z), z1 = widen_hi(z);
-                const uint32_t y0 = widen_lo(y), y1 = widen_hi(y), w0 = widen_lo(w), w1 = widen_hi(w);
+            for (int h = 0; h < 2; ++h) {
+                uint32_t pb[NT][2];
+                const float vscale = tail && s * kStep + 16 * h >= cur.len ? 0.f : vs[h];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16(acc[nt][2 * i], x0, x1, z0, z1, pb[nt][0], pb[nt][1]);
-                    mma_f16(acc[nt][2 * i + 1], y0, y1, w0, w1, pb[nt][0], pb[nt][1]);
+                    const float m0 = M[nt][0] == kNegInf ? 0.f : M[nt][0], m1 = M[nt][1] == kNegInf ? 0.f : M[nt][1];
+                    const float e0 = ex2(S[h][nt][0] - m0), e1 = ex2(S[h][nt][1] - m1), e2 = ex2(S[h][nt][2] - m0),
+                                e3 = ex2(S[h][nt][3] - m1);
+                    l[nt][0] += e0 + e2;
+                    l[nt][1] += e1 + e3;
+                    pb[nt][0] = transpose8(pack_half(e0 * vscale, e1 * vscale));
+                    pb[nt][1] = transpose8(pack_half(e2 * vscale, e3 * vscale));
+                }
+                const uint8_t *v = slot + F::KBYTES + h * F::HALF;
+                uint32_t vw[4][F::VB / 4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint8_t *at = v + v_at[i & 1] + (i >> 1) * (F::HALF / 2);
+                    if (F::VB == 16) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(at);
+                        vw[i][0] = x.x;
+                        vw[i][1] = x.y;
+                        vw[i][F::VB / 4 - 2] = x.z;
+                        vw[i][F::VB / 4 - 1] = x.w;
+                    } else {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(at);
+                        vw[i][0] = x.x;
+                        vw[i][1] = x.y;
+                    }
+                }
+                if (tail) {  // a zero weight would turn a NaN behind the last token into one
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (s * kStep + 16 * h + 2 * t + (i & 1) + (i >> 1) * 8 >= cur.len) {
+#pragma unroll
+                            for (int x = 0; x < F::VB / 4; ++x) vw[i][x] = 0;
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < F::VB / 4; ++i) {
+                    const uint32_t x = __byte_perm(vw[0][i], vw[1][i], 0x5140), y = __byte_perm(vw[0][i], vw[1][i], 0x7362);
+                    const uint32_t z = __byte_perm(vw[2][i], vw[3][i], 0x5140), w = __byte_perm(vw[2][i], vw[3][i], 0x7362);
+                    uint32_t x0, x1, y0, y1, z0, z1, w0, w1;
+                    widen(x, x0, x1);
+                    widen(y, y0, y1);
+                    widen(z, z0, z1);
+                    widen(w, w0, w1);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(acc[nt][2 * i], x0, x1, z0, z1, pb[nt][0], pb[nt][1]);
+                        mma_f16(acc[nt][2 * i + 1], y0, y1, w0, w1, pb[nt][0], pb[nt][1]);
+                    }
                 }
             }
+            if (++rd == F::DEPTH) rd = 0, rd_phase ^= 1;
+            __syncwarp();  // every lane has read the slot: it is filled again
+            copy_step();
+        }
+        failed = __any_sync(0xffffffffu, failed);
+        if (failed) {  // a copy's wait gave up: the sums stand for nothing
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) l[nt][0] = l[nt][1] = __int_as_float(0x7fc00000);
         }
 
-        // ---- the warps' sums of this unit together
-        __syncthreads();  // the buffer's previous use is over
+        // ---- the warps' sums of this unit together: the upper two warps' into the lower two's
+        // registers, then the two of those
+        if (cur.s1 > cur.s0) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = nt * 8 + 2 * t + e;
-                float x = l[nt][e];
-                x += __shfl_xor_sync(0xffffffffu, x, 4);
-                x += __shfl_xor_sync(0xffffffffu, x, 8);
-                x += __shfl_xor_sync(0xffffffffu, x, 16);
-                if (g == 0) {
-                    merge_m[warp * F::ROWS + r] = M[nt][e];
-                    merge_l[warp * F::ROWS + r] = x;
+                for (int e = 0; e < 2; ++e) {
+                    float x = l[nt][e];
+                    x += __shfl_xor_sync(0xffffffffu, x, 4);
+                    x += __shfl_xor_sync(0xffffffffu, x, 8);
+                    x += __shfl_xor_sync(0xffffffffu, x, 16);
+                    l[nt][e] = x;
                 }
-                float *dst = merge + (warp * F::ROWS + r) * F::PITCH + g * F::VB;
+            float *buf = merge + (warp & 1) * F::ROWS * F::PITCH + g * F::VB;
+            float *buf_m = merge_m + (warp & 1) * F::ROWS, *buf_l = merge_l + (warp & 1) * F::ROWS;
+            auto put = [&] {
 #pragma unroll
-                for (int j = 0; j < F::MT; ++j)
-                    *reinterpret_cast<float2 *>(dst + 2 * j) = make_float2(acc[nt][j][e], acc[nt][j][e + 2]);
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = nt * 8 + 2 * t + e;
+                        if (g == 0) {
+                            buf_m[r] = M[nt][e];
+                            buf_l[r] = l[nt][e];
+                        }
+#pragma unroll
+                        for (int j = 0; j < F::MT; ++j)
+                            *reinterpret_cast<float2 *>(buf + r * F::PITCH + 2 * j) = make_float2(acc[nt][j][e], acc[nt][j][e + 2]);
+                    }
+            };
+            __syncthreads();  // the buffer's previous use is over
+            if (warp >= 2) put();
+            __syncthreads();
+            if (warp < 2) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = nt * 8 + 2 * t + e;
+                        const float mo = buf_m[r], m = fmaxf(M[nt][e], mo);
+                        const float fa = m == kNegInf ? 1.f : ex2(M[nt][e] - m), fb = m == kNegInf ? 1.f : ex2(mo - m);
+                        M[nt][e] = m;
+                        l[nt][e] = l[nt][e] * fa + buf_l[r] * fb;
+#pragma unroll
+                        for (int j = 0; j < F::MT; ++j) {
+                            const float2 x = *reinterpret_cast<const float2 *>(buf + r * F::PITCH + 2 * j);
+                            acc[nt][j][e] = acc[nt][j][e] * fa + x.x * fb;
+                            acc[nt][j][e + 2] = acc[nt][j][e + 2] * fa + x.y * fb;
+                        }
+                    }
+                __syncwarp();  // every lane has read M and l
+                put();
             }
-        __syncthreads();
-        const bool whole = cur.s0 == 0 && cur.s1 == cur.steps;
-        float *part = p.ws + ((int64_t)blockIdx.x * 2 + (first ? 0 : 1)) * F::PART;
-        for (int i = tid; i < F::ROWS * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
-            float m = kNegInf;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, merge_m[w * F::ROWS + r]);
-            float sum = 0.f;
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float mw = merge_m[w * F::ROWS + r], f = m == kNegInf ? 1.f : ex2(mw - m);
-                const float4 x = *reinterpret_cast<const float4 *>(merge + (w * F::ROWS + r) * F::PITCH + d);
-                sum += f * merge_l[w * F::ROWS + r];
-                a.x += f * x.x;
-                a.y += f * x.y;
-                a.z += f * x.z;
-                a.w += f * x.w;
-            }
-            if (!whole) {
-                *reinterpret_cast<float4 *>(part + r * D + d) = a;
-                if (d == 0) {
-                    part[F::ROWS * D + r] = m;
-                    part[F::ROWS * D + F::ROWS + r] = sum;
+            __syncthreads();
+            const bool whole = cur.s0 == 0 && cur.s1 == cur.steps;
+            float *part = p.ws + ((int64_t)blockIdx.x * 2 + (first ? 0 : 1)) * F::PART;
+            for (int i = tid; i < F::ROWS * (D / 4); i += kThreads) {
+                const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+                const float ma = merge_m[r], mb = merge_m[F::ROWS + r], m = fmaxf(ma, mb);
+                const float fa = m == kNegInf ? 1.f : ex2(ma - m), fb = m == kNegInf ? 1.f : ex2(mb - m);
+                const float4 x = *reinterpret_cast<const float4 *>(merge + r * F::PITCH + d);
+                const float4 y = *reinterpret_cast<const float4 *>(merge + (F::ROWS + r) * F::PITCH + d);
+                const float4 a = make_float4(fa * x.x + fb * y.x, fa * x.y + fb * y.y, fa * x.z + fb * y.z, fa * x.w + fb * y.w);
+                const float sum = fa * merge_l[r] + fb * merge_l[F::ROWS + r];
+                if (!whole) {
+                    *reinterpret_cast<float4 *>(part + r * D + d) = a;
+                    if (d == 0) {
+                        part[F::ROWS * D + r] = m;
+                        part[F::ROWS * D + F::ROWS + r] = sum;
+                    }
+                } else if (r0 + r < group) {
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    const int64_t row = (int64_t)cur.n * p.Hq + h * group + r0 + r;
+                    if (p.o_bf16) {
+                        uint2 w;
+                        w.x = pack_bf16x2(a.x * inv, a.y * inv);
+                        w.y = pack_bf16x2(a.z * inv, a.w * inv);
+                        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.o) + row * D + d) = w;
+                    } else {
+                        *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + row * D + d) =
+                            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+                    }
+                    if (p.lse && d == 0) p.lse[row] = sum == 0.f ? kNegInf : (log2f(sum) + m) * 0.6931471805599453f;
                 }
-            } else if (r0 + r < group) {
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                const int64_t row = (int64_t)cur.n * p.Hq + h * group + r0 + r;
-                if (p.o_bf16) {
-                    uint2 w;
-                    w.x = pack_bf16x2(a.x * inv, a.y * inv);
-                    w.y = pack_bf16x2(a.z * inv, a.w * inv);
-                    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.o) + row * D + d) = w;
-                } else {
-                    *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + row * D + d) =
-                        make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-                }
-                if (p.lse && d == 0) p.lse[row] = sum == 0.f ? kNegInf : (log2f(sum) + m) * 0.6931471805599453f;
             }
         }
         first = false;
-        left -= cur.s1 - cur.s0;
+        left -= cur.places;
         if (left <= 0) break;
-        next_segment(c, U, left, cur);
+        next_segment(c, U, parts, left, cur);
     }
     cp_wait<0>();
+    // after a failure copies may still be under way: they land before the CTA ends
+    if (failed) {
+        for (int i = max(0, issued - F::DEPTH); i < issued; ++i) tc::mbar_wait(bars + i % F::DEPTH, (i / F::DEPTH) & 1, kPolls);
+        if (lane == 0) atomicAdd(&g_attn_decode_timeouts, 1);
+    }
 }
 
 // Adds the pieces of one query row in their order along the line; a CTA for each (sequence,
@@ -507,7 +618,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_join_kernel(const __grid
     const Line line = measure_line(c, s_scan);
     if (n >= line.first && n < line.last) {
         int64_t at = line.mine;
-        for (int i = line.first; i < n; ++i) at += steps_of(c, i);
+        for (int i = line.first; i < n; ++i) at += places_of(steps_of(c, i));
         s_at = at;
     }
     __syncthreads();
@@ -517,8 +628,8 @@ __global__ void __launch_bounds__(kThreads) attn_decode_join_kernel(const __grid
     float a[C] = {};
     float m = kNegInf, l = 0.f;
     if (steps > 0) {
-        const int64_t S = piece_steps(line.total * U, ctas), Ls = s_at * U + (int64_t)u * steps;
-        const int64_t c0 = Ls / S, c1 = (Ls + steps - 1) / S;
+        const int64_t S = piece_places(line.total * U, ctas), Ls = s_at * U + (int64_t)u * places_of(steps);
+        const int64_t c0 = (Ls + kPad) / S, c1 = (Ls + places_of(steps) - 1) / S;  // of its first and last step
         if (c0 == c1) return;  // written by its CTA
         for (int64_t k = c0 + warp; k <= c1; k += kWarps) {
             // the unit is the first of its CTA's segments unless the CTA began before it
@@ -566,13 +677,30 @@ __global__ void __launch_bounds__(kThreads) attn_decode_join_kernel(const __grid
     if (p.lse && tid == 0) p.lse[row] = sum == 0.f ? kNegInf : (log2f(sum) + m) * 0.6931471805599453f;
 }
 
-int decode_ctas() { return kCtasPerSm * sm_count(); }
+// The cache's rows (D bytes each) in boxes of a step's rows, or of a page's where those are fewer.
+bool encode(chunk::EncodeTiledFn enc, CUtensorMap *map, const void *base, const PagedCache &c) {
+    const cuuint64_t dims[2] = {(cuuint64_t)c.D, (cuuint64_t)c.n_pages * c.Hk * c.P};
+    const cuuint64_t strides[1] = {(cuuint64_t)c.D};
+    const cuuint32_t box[2] = {(cuuint32_t)c.D, (cuuint32_t)(c.P < kStep ? c.P : kStep)}, es[2] = {1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, c.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) set_error("attn_decode: cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return r == CUDA_SUCCESS;
+}
 
 template <int D, int NT>
 kda_status run(const DecodeParams &p, cudaStream_t st) {
     using F = Cfg<D, NT>;
+    chunk::EncodeTiledFn enc = reinterpret_cast<chunk::EncodeTiledFn>(tensor_map_encoder());
+    if (!enc) {
+        set_error("attn_decode: cuTensorMapEncodeTiled is not available from the driver");
+        return KDA_ERR_CUDA;
+    }
+    CUtensorMap mk, mv;
+    if (!encode(enc, &mk, p.c.k, p.c) || !encode(enc, &mv, p.c.v, p.c)) return KDA_ERR_CUDA;
     static DeviceOnce configured;
-    const int dev = current_device(), ctas = decode_ctas();
+    const int dev = current_device(), ctas = F::CTAS * sm_count();
     if (!configured.done(dev)) {
         if (cudaFuncSetAttribute(attn_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM) !=
             cudaSuccess) {
@@ -581,7 +709,7 @@ kda_status run(const DecodeParams &p, cudaStream_t st) {
         }
         configured.set(dev);
     }
-    attn_decode_kernel<D, NT><<<ctas, kThreads, F::SMEM, st>>>(p);
+    attn_decode_kernel<D, NT><<<ctas, kThreads, F::SMEM, st>>>(mk, mv, p);
     note_launch();
     kda_status s = check_launch("attn_decode_kernel");
     if (s != KDA_OK) return s;
@@ -606,9 +734,26 @@ kda_status run(const DecodeParams &p, cudaStream_t st) {
 
 }  // namespace
 
+int take_attn_decode_timeouts(cudaStream_t st) {
+    int n = 0;
+    const int zero = 0;
+    if (cudaMemcpyFromSymbolAsync(&n, g_attn_decode_timeouts, sizeof(int), 0, cudaMemcpyDeviceToHost, st) !=
+            cudaSuccess ||
+        cudaMemcpyToSymbolAsync(g_attn_decode_timeouts, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess) {
+        set_error("attn_decode: cannot read the timeout counter: %s", cudaGetErrorString(cudaGetLastError()));
+        return -1;
+    }
+    return n;
+}
+
 size_t attn_decode_workspace_bytes(int Hq, int Hk, int D) {
-    const int rows = Hq / Hk <= 8 ? 8 : 16;
-    return (size_t)decode_ctas() * 2 * rows * (D + 2) * sizeof(float);
+    // two pieces per CTA at most
+    const bool wide = Hq / Hk > 8;
+    const int ctas = (D == 128 ? wide ? Cfg<128, 2>::CTAS : Cfg<128, 1>::CTAS : wide ? Cfg<64, 2>::CTAS : Cfg<64, 1>::CTAS) *
+                     sm_count();
+    return (size_t)ctas * 2 * (wide ? 16 : 8) * (D + 2) * sizeof(float);
 }
 
 kda_status launch_attn_decode(const DecodeParams &p, cudaStream_t st) {
