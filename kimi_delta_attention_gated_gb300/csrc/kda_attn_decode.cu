@@ -312,6 +312,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
     int rd = 0, failed = 0;
     uint32_t rd_phase = 0;
     bool first = true;
+    // A unit's queries: each lane the 16-byte pieces of its row that its products take.
+    uint4 qw[NT][F::KJ][2];
+    auto fetch_queries = [&](const Segment &x) {
+        const int r0 = (x.u - x.head * parts) * F::ROWS;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = r0 + nt * 8 + g;
+            const __nv_bfloat16 *q = p.q + x.n * p.q_stride + (int64_t)(x.head * group + r) * D;
+#pragma unroll
+            for (int j = 0; j < F::KJ; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    qw[nt][j][i] = r < group ? __ldg(reinterpret_cast<const uint4 *>(q + 16 * (F::KJ * t + j) + 8 * i))
+                                             : make_uint4(0, 0, 0, 0);
+        }
+    };
+    fetch_queries(cur);
     while (true) {
         const int h = cur.head, r0 = (cur.u - h * parts) * F::ROWS;  // first query head of the unit in its group
         // queries: f16, each row scaled by a power of two to at most 2 so that nothing overflows
@@ -319,17 +336,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
         float row_scale[NT][2];  // of the two rows whose scores this lane holds
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int r = r0 + nt * 8 + g;
-            const __nv_bfloat16 *q = p.q + cur.n * p.q_stride + (int64_t)(h * group + r) * D;
-            uint4 w[F::KJ][2];
             uint32_t amax = 0;
 #pragma unroll
             for (int j = 0; j < F::KJ; ++j)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    w[j][i] = r < group ? __ldg(reinterpret_cast<const uint4 *>(q + 16 * (F::KJ * t + j) + 8 * i))
-                                        : make_uint4(0, 0, 0, 0);
-                    const uint32_t u[4] = {w[j][i].x, w[j][i].y, w[j][i].z, w[j][i].w};
+                    const uint4 w = qw[nt][j][i];
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const uint32_t lo = (u[e] << 16) & 0x7FFF0000u, hi = u[e] & 0x7FFF0000u;
@@ -345,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
             for (int j = 0; j < F::KJ; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint4 x = w[j][i >> 1];
+                    const uint4 x = qw[nt][j][i >> 1];
                     const uint32_t lo = (i & 1) ? x.z : x.x, hi = (i & 1) ? x.w : x.y;
                     qf[nt][4 * j + i][0] = pack_half(__uint_as_float(lo << 16) * inv, __uint_as_float(lo & 0xFFFF0000u) * inv);
                     qf[nt][4 * j + i][1] = pack_half(__uint_as_float(hi << 16) * inv, __uint_as_float(hi & 0xFFFF0000u) * inv);
@@ -502,6 +515,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
             for (int nt = 0; nt < NT; ++nt) l[nt][0] = l[nt][1] = __int_as_float(0x7fc00000);
         }
 
+        // the next unit and its queries, on their way while this one's sums come together
+        left -= cur.places;
+        Segment nxt = cur;
+        if (left > 0) {
+            next_segment(c, U, parts, left, nxt);
+            fetch_queries(nxt);
+        }
+
         // ---- the warps' sums of this unit together: the upper two warps' into the lower two's
         // registers, then the two of those
         if (cur.s1 > cur.s0) {
@@ -589,9 +610,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
             }
         }
         first = false;
-        left -= cur.places;
         if (left <= 0) break;
-        next_segment(c, U, parts, left, cur);
+        cur = nxt;
     }
     cp_wait<0>();
     // after a failure copies may still be under way: they land before the CTA ends
