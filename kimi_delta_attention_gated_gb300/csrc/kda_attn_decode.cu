@@ -29,7 +29,7 @@
 // and across the borders of heads, without a barrier between warps.  The swizzle of the rows
 // and the choice of the pieces a lane takes leave no bank conflict (64-channel values: two
 // ways).  With 16-byte copies by each lane (cp.async) the load and store pipe was the bound:
-// 148 us for 256 sequences of about 1000 tokens against XXX.
+// 148 us for 256 sequences of about 1000 tokens against 116.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -42,9 +42,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kJoinMost = 512;   // threads of a joining CTA at most
 constexpr int kStep = 32;       // tokens of a step
 constexpr int kPad = 6;         // a head's own cost in steps
-constexpr int kMinPiece = 12;   // places of a CTA at least
+constexpr int kMinPiece = 8;   // places of a CTA at least
 constexpr uint32_t kPolls = 1u << 21;  // bound on a copy's wait: a few seconds
 constexpr float kSlack = 8.f;   // the maximum in use may lie this far below the true one (log2)
 constexpr float kNegInf = -INFINITY;
@@ -130,9 +131,9 @@ struct Line {
     int64_t mine;     // those before this thread's first sequence
     int first, last;  // this thread's sequences [first, last)
 };
-__device__ __forceinline__ Line measure_line(const PagedCache &c, int64_t *scan) {
+__device__ __forceinline__ Line measure_line(const PagedCache &c, int64_t *scan, int threads) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (c.N + kThreads - 1) / kThreads;
+    const int per = (c.N + threads - 1) / threads;
     Line l;
     l.first = min(tid * per, c.N);
     l.last = min(l.first + per, c.N);
@@ -148,7 +149,7 @@ __device__ __forceinline__ Line measure_line(const PagedCache &c, int64_t *scan)
     __syncthreads();
     l.mine = x - own;
     l.total = 0;
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < threads / 32; ++w) {
         if (w < warp) l.mine += scan[w];
         l.total += scan[w];
     }
@@ -187,6 +188,22 @@ __device__ __forceinline__ void next_segment(const PagedCache &c, int U, int par
     set_range(g, 0, left);
 }
 
+// Four channels of an output row (and the row's lse) from its sums.
+template <int D>
+__device__ __forceinline__ void write_row(const DecodeParams &p, int64_t row, int d, float4 a, float m, float sum) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (p.o_bf16) {
+        uint2 w;
+        w.x = pack_bf16x2(a.x * inv, a.y * inv);
+        w.y = pack_bf16x2(a.z * inv, a.w * inv);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.o) + row * D + d) = w;
+    } else {
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + row * D + d) =
+            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    }
+    if (p.lse && d == 0) p.lse[row] = sum == 0.f ? kNegInf : (log2f(sum) + m) * 0.6931471805599453f;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel(
     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const __grid_constant__ DecodeParams p) {
@@ -201,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // this CTA's piece of the line
-    const Line line = measure_line(c, s_scan);
+    const Line line = measure_line(c, s_scan, kThreads);
     const int64_t all = line.total * U, S = piece_places(all, gridDim.x), L0 = (int64_t)blockIdx.x * S;
     if (L0 >= all) return;
     const int64_t L1 = min(L0 + S, all);
@@ -594,18 +611,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
                         part[F::ROWS * D + F::ROWS + r] = sum;
                     }
                 } else if (r0 + r < group) {
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    const int64_t row = (int64_t)cur.n * p.Hq + h * group + r0 + r;
-                    if (p.o_bf16) {
-                        uint2 w;
-                        w.x = pack_bf16x2(a.x * inv, a.y * inv);
-                        w.y = pack_bf16x2(a.z * inv, a.w * inv);
-                        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.o) + row * D + d) = w;
-                    } else {
-                        *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + row * D + d) =
-                            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-                    }
-                    if (p.lse && d == 0) p.lse[row] = sum == 0.f ? kNegInf : (log2f(sum) + m) * 0.6931471805599453f;
+                    write_row<D>(p, (int64_t)cur.n * p.Hq + h * group + r0 + r, d, a, m, sum);
                 }
             }
         }
@@ -621,80 +627,90 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
     }
 }
 
-// Adds the pieces of one query row in their order along the line; a CTA for each (sequence,
-// unit, row).  Rows of sequences without tokens are written here as zero.
+// Joins the units that more than one CTA took, adding their pieces in their order along the
+// line; gridDim.y CTAs share a unit's rows, and the runs of a CTA's threads its pieces.  With
+// at least as many CTAs as units blockIdx.x is the unit; else it is a piece, and the CTA
+// looks after the unit that begins in it and goes on behind it, if there is one.  (A CTA for
+// every query row of the batch, most of which had nothing to do, took 17 us of 118 with 256
+// sequences.)  Rows of sequences without tokens are written here as zero.
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) attn_decode_join_kernel(const __grid_constant__ DecodeParams p, int ctas) {
+__global__ void __launch_bounds__(kJoinMost) attn_decode_join_kernel(const __grid_constant__ DecodeParams p, int ctas,
+                                                                     int by_unit) {
     using F = Cfg<D, NT>;
-    __shared__ int64_t s_scan[kWarps];
-    __shared__ int64_t s_at;
-    __shared__ float s_acc[kWarps][D], s_m[kWarps], s_l[kWarps];
-    constexpr int C = D / 32;
+    __shared__ int64_t s_scan[kJoinMost / 32];
+    __shared__ int64_t s_begin;
+    __shared__ Segment s_seg;
+    __shared__ float4 s_acc[kJoinMost];
+    __shared__ float s_m[kJoinMost], s_l[kJoinMost];
     const PagedCache &c = p.c;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int group = p.Hq / c.Hk, parts = (group + F::ROWS - 1) / F::ROWS, U = c.Hk * parts;
-    const int qh = blockIdx.x, n = blockIdx.y;  // query head, sequence
-    const int h = qh / group, in = qh - h * group, u = h * parts + in / F::ROWS, r = in % F::ROWS;
-    const Line line = measure_line(c, s_scan);
-    if (n >= line.first && n < line.last) {
-        int64_t at = line.mine;
-        for (int i = line.first; i < n; ++i) at += places_of(steps_of(c, i));
-        s_at = at;
-    }
+    const int tid = threadIdx.x, group = p.Hq / c.Hk, parts = (group + F::ROWS - 1) / F::ROWS, U = c.Hk * parts;
+    const int rows = F::ROWS / gridDim.y, items = rows * (D / 4), groups = blockDim.x / items;  // four channels an item
+    const Line line = measure_line(c, s_scan, blockDim.x);
+    const int64_t all = line.total * U, S = piece_places(all, ctas), L0 = (int64_t)blockIdx.x * S, L1 = min(L0 + S, all);
+    if (tid == 0) s_seg.n = -1;
     __syncthreads();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t row = (int64_t)n * p.Hq + qh;
-    const int steps = steps_of(c, n);
-    float a[C] = {};
-    float m = kNegInf, l = 0.f;
-    if (steps > 0) {
-        const int64_t S = piece_places(line.total * U, ctas), Ls = s_at * U + (int64_t)u * places_of(steps);
-        const int64_t c0 = (Ls + kPad) / S, c1 = (Ls + places_of(steps) - 1) / S;  // of its first and last step
-        if (c0 == c1) return;  // written by its CTA
-        for (int64_t k = c0 + warp; k <= c1; k += kWarps) {
-            // the unit is the first of its CTA's segments unless the CTA began before it
-            const float *part = p.ws + (k * 2 + (k * S >= Ls ? 0 : 1)) * F::PART;
-            const float mk = __ldcg(part + F::ROWS * D + r), lk = __ldcg(part + F::ROWS * D + F::ROWS + r);
-            float x[C];
-            if (C == 4) {
-                const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + r * D) + lane);
-                x[0] = y.x;
-                x[1] = y.y;
-                x[C - 2] = y.z;
-                x[C - 1] = y.w;
-            } else {
-                const float2 y = __ldcg(reinterpret_cast<const float2 *>(part + r * D) + lane);
-                x[0] = y.x;
-                x[1] = y.y;
+    if (by_unit || L0 < L1) {
+        const int un = blockIdx.x / U;  // by_unit: the unit's sequence
+        int64_t at = line.mine;
+        for (int n = line.first; n < line.last; ++n) {
+            const int st = steps_of(c, n), pl = places_of(st);
+            if (st > 0 && (by_unit ? n == un : L1 - 1 >= at * U && L1 - 1 < (at + pl) * U)) {
+                s_seg.u = by_unit ? blockIdx.x - un * U : (int)((L1 - 1 - at * U) / pl);
+                s_seg.steps = st;
+                s_seg.n = n;
+                s_begin = at * U + (int64_t)s_seg.u * pl;
             }
-            const float mn = fmaxf(m, mk);
-            const float f = mn == kNegInf ? 1.f : ex2(m - mn), fk = mn == kNegInf ? 1.f : ex2(mk - mn);
-            m = mn;
-            l = l * f + lk * fk;
-#pragma unroll
-            for (int i = 0; i < C; ++i) a[i] = a[i] * f + x[i] * fk;
+            at += pl;
         }
     }
-#pragma unroll
-    for (int i = 0; i < C; ++i) s_acc[warp][lane * C + i] = a[i];
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
-    }
     __syncthreads();
-    if (tid >= D) return;
-    m = kNegInf;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w]);
-    float sum = 0.f, x = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const float f = m == kNegInf ? 1.f : ex2(s_m[w] - m);
-        sum += f * s_l[w];
-        x += f * s_acc[w][tid];
+    const int n = s_seg.n, u = s_seg.u, steps = s_seg.steps;
+    const int64_t begin = s_begin;  // of the unit, on the line
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.y == gridDim.y - 1)
+        for (int e = blockIdx.x; e < c.N; e += gridDim.x) {
+            if (tokens_of(c, e) > 0) continue;
+            const int64_t row = (int64_t)e * p.Hq;
+            for (int i = tid; i < p.Hq * D; i += blockDim.x) st_out(p.o, row * D + i, 0.f, p.o_bf16);
+            if (p.lse)
+                for (int i = tid; i < p.Hq; i += blockDim.x) p.lse[row + i] = kNegInf;
+        }
+    if (n < 0) return;
+    const int64_t c0 = (begin + kPad) / S, c1 = (begin + kPad + steps - 1) / S;  // CTAs of its first and last step
+    if (c1 == c0 || (!by_unit && c0 != blockIdx.x)) return;
+    const int item = tid % items, r = rows * blockIdx.y + item / (D / 4), d = item % (D / 4) * 4;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = kNegInf, l = 0.f;
+    const int pieces = (int)(c1 - c0) + 1, used = min(groups, pieces), per = (pieces + used - 1) / used;
+    const int64_t k0 = c0 + (int64_t)(tid / items) * per, k1 = min(k0 + per, c1 + 1);
+#pragma unroll 4
+    for (int64_t k = k0; k < k1; ++k) {
+        // the unit is the first of its CTA's segments unless the CTA began before it
+        const float *part = p.ws + (k * 2 + (k * S >= begin ? 0 : 1)) * F::PART;
+        const float mk = __ldcg(part + F::ROWS * D + r), lk = __ldcg(part + F::ROWS * D + F::ROWS + r);
+        const float4 x = __ldcg(reinterpret_cast<const float4 *>(part + r * D + d));
+        const float mn = fmaxf(m, mk);
+        const float f = mn == kNegInf ? 1.f : ex2(m - mn), fk = mn == kNegInf ? 1.f : ex2(mk - mn);
+        m = mn;
+        l = l * f + lk * fk;
+        a = make_float4(a.x * f + x.x * fk, a.y * f + x.y * fk, a.z * f + x.z * fk, a.w * f + x.w * fk);
     }
-    st_out(p.o, row * D + tid, sum == 0.f ? 0.f : x / sum, p.o_bf16);
-    if (p.lse && tid == 0) p.lse[row] = sum == 0.f ? kNegInf : (log2f(sum) + m) * 0.6931471805599453f;
+    s_acc[tid] = a;
+    s_m[tid] = m;
+    s_l[tid] = l;
+    __syncthreads();
+    const int h = parts == 1 ? u : u / parts, head = (u - h * parts) * F::ROWS + r;  // within the group
+    if (tid >= items || head >= group) return;
+    for (int i = 1; i < used; ++i) m = fmaxf(m, s_m[tid + i * items]);
+    float sum = 0.f;
+    a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < used; ++i) {
+        const float mk = s_m[tid + i * items], f = m == kNegInf ? 1.f : ex2(mk - m);
+        const float4 x = s_acc[tid + i * items];
+        sum += f * s_l[tid + i * items];
+        a = make_float4(a.x + f * x.x, a.y + f * x.y, a.z + f * x.z, a.w + f * x.w);
+    }
+    write_row<D>(p, (int64_t)n * p.Hq + h * group + head, d, a, m, sum);
 }
 
 // The cache's rows (D bytes each) in boxes of a step's rows, or of a page's where those are fewer.
@@ -734,15 +750,19 @@ kda_status run(const DecodeParams &p, cudaStream_t st) {
     kda_status s = check_launch("attn_decode_kernel");
     if (s != KDA_OK) return s;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.Hq, p.c.N, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    // few units (of which each may have many pieces): large CTAs for two rows each; else as many
+    // as are resident at once, so that none waits for others that wait for the first kernel
+    const int group = p.Hq / p.c.Hk, units = p.c.N * p.c.Hk * ((group + F::ROWS - 1) / F::ROWS);
+    const bool few = (int64_t)units * (F::ROWS / 2) <= 4 * sm_count();
+    cfg.gridDim = dim3(units < ctas ? units : ctas, few ? F::ROWS / 2 : 2, 1);
+    cfg.blockDim = dim3(few ? 512 : 256, 1, 1);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];  // starts while the first kernel ends; waits for it before it reads
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D, NT>, p, ctas);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D, NT>, p, ctas, units < ctas ? 1 : 0);
     note_launch();
     if (e != cudaSuccess) {
         set_error("attn_decode_join_kernel: %s", cudaGetErrorString(e));
