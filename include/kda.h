@@ -562,14 +562,14 @@ kda_status kda_kv_append(const void *k, int64_t k_stride, const void *v, int64_t
  *             [0, max_blocks * page_size].  0 gives a zero row and lse -INFINITY.
  *   o         [n_seqs, q_heads, dim] o_dtype
  *   lse       [n_seqs, q_heads] float or NULL: log(sum_j e^(scale q . K_j))
- *   workspace device scratch of kda_attn_decode_workspace_size(q_heads, kv_heads, dim)
- *             bytes, 16-byte aligned; calls that may overlap on the GPU (two captured
- *             graphs among them) need workspaces of their own
+ *   workspace device scratch of kda_attn_decode_workspace_size(n_seqs, q_heads, kv_heads,
+ *             dim, max_blocks * page_size) bytes, 16-byte aligned; calls that may overlap on
+ *             the GPU (two captured graphs among them) need workspaces of their own
  * What lies in a page behind a sequence's last token is not read into the result, whatever
  * it is.  A sequence with a page number out of [0, num_pages) gives NaN rows.
  * dim 64 or 128; page_size 16, 32, 64 or 128.  Results do not depend on timing.
  */
-size_t kda_attn_decode_workspace_size(int q_heads, int kv_heads, int dim);
+size_t kda_attn_decode_workspace_size(int n_seqs, int q_heads, int kv_heads, int dim, int64_t max_tokens);
 
 kda_status kda_attn_decode(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
                            const float *k_scale, const float *v_scale, int num_pages, int page_size,

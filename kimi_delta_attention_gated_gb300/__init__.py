@@ -104,7 +104,7 @@ def _load():
         lib.kda_rotary.argtypes = [P, I, L, P, P, F, I, I, I, P, L, L, I, I, P]
         lib.kda_kv_append.argtypes = [P, L, P, L, L, I, I, P, P, P, P, I, I, P, I, P, P, I, P, F, I, I, P, L, I, P, P, P]
         lib.kda_attn_decode.argtypes = [P, L, P, P, P, P, I, I, P, I, P, I, I, I, I, F, P, I, P, P, Z, P]
-        lib.kda_attn_decode_workspace_size.argtypes = [I, I, I]
+        lib.kda_attn_decode_workspace_size.argtypes = [I, I, I, I, L]
         lib.kda_attn_decode_workspace_size.restype = Z
         lib.kda_attn_prompt.argtypes = [P, L, P, L, P, L, L, L, I, I, I, I, P, P, I, F, P, I, P, P]
         for fn in ("kda_rotary", "kda_kv_append", "kda_attn_decode", "kda_attn_prompt"):
@@ -828,9 +828,10 @@ def kv_append(k, v, cache, block_table, context_lens, *, cu_seqlens=None, inv_fr
     return q_out, k_out
 
 
-def attn_decode_workspace_size(q_heads, kv_heads, dim) -> int:
-    """Bytes of workspace one attn_decode call needs."""
-    return int(_load().kda_attn_decode_workspace_size(int(q_heads), int(kv_heads), int(dim)))
+def attn_decode_workspace_size(n_seqs, q_heads, kv_heads, dim, max_tokens) -> int:
+    """Bytes of workspace one attn_decode call needs; max_tokens: what the block table can hold,
+    max_blocks * page_size."""
+    return int(_load().kda_attn_decode_workspace_size(int(n_seqs), int(q_heads), int(kv_heads), int(dim), int(max_tokens)))
 
 
 def attn_decode(q, cache, block_table, seq_lens, *, scale=None, out_dtype=torch.bfloat16, return_lse=False, o=None,
@@ -852,14 +853,15 @@ def attn_decode(q, cache, block_table, seq_lens, *, scale=None, out_dtype=torch.
     rows, max_blocks = block_table.shape
     if rows != N or seq_lens.shape[0] != N:
         raise ValueError("block_table and seq_lens must have one row per query")
+    device = q.device
     if o is None:
-        o = torch.empty((N, Hq, D), dtype=out_dtype, device=q.device)
+        o = torch.empty((N, Hq, D), dtype=out_dtype, device=device)
     elif o.shape != q.shape:
         raise ValueError("o must be like q")
-    lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+    lse = torch.empty((N, Hq), dtype=torch.float32, device=device) if return_lse else None
     if workspace is None:
-        need = lib.kda_attn_decode_workspace_size(Hq, Hk, D)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        need = lib.kda_attn_decode_workspace_size(N, Hq, Hk, D, max_blocks * P)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
     else:
         need = workspace.numel() * workspace.element_size()
         if workspace.get_device() != index or not workspace.is_contiguous():

@@ -888,9 +888,11 @@ kda_status kda_kv_append(const void *k, int64_t k_stride, const void *v, int64_t
     return kda::launch_kv_append(p, (cudaStream_t)stream);
 }
 
-size_t kda_attn_decode_workspace_size(int q_heads, int kv_heads, int dim) {
-    if (q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads != 0 || (dim != 64 && dim != 128)) return 0;
-    return kda::attn_decode_workspace_bytes(q_heads, kv_heads, dim);
+size_t kda_attn_decode_workspace_size(int n_seqs, int q_heads, int kv_heads, int dim, int64_t max_tokens) {
+    if (n_seqs < 0 || q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads != 0 || (dim != 64 && dim != 128) ||
+        max_tokens < 0 || max_tokens > INT32_MAX)
+        return 0;
+    return kda::attn_decode_workspace_bytes(n_seqs, q_heads, kv_heads, dim, max_tokens);
 }
 
 kda_status kda_attn_decode(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
@@ -914,7 +916,8 @@ kda_status kda_attn_decode(const void *q, int64_t q_stride, const void *k_cache,
         KDA_REQUIRE(aligned16(ptr), KDA_ERR_INVALID_ARG, "%s: q, o and the workspace must be 16-byte aligned", fn);
     KDA_REQUIRE(aligned_to(lse, 4), KDA_ERR_INVALID_ARG, "%s: lse must be 4-byte aligned", fn);
     if (n_seqs == 0) return KDA_OK;
-    const size_t need = kda::attn_decode_workspace_bytes(q_heads, kv_heads, dim);
+    const size_t need =
+        kda::attn_decode_workspace_bytes(n_seqs, q_heads, kv_heads, dim, (int64_t)max_blocks * page_size);
     KDA_REQUIRE(workspace && workspace_bytes >= need, KDA_ERR_INVALID_ARG,
                 "%s: the workspace holds %zu bytes, this call needs %zu (kda_attn_decode_workspace_size)", fn,
                 workspace ? workspace_bytes : (size_t)0, need);

@@ -72,7 +72,7 @@ struct PromptParams {
 kda_status launch_rotary(const void *x, int bf16, int64_t x_stride, const int32_t *positions, const RotaryParams &r,
                          void *out, int64_t out_stride, int64_t T, int H, int D, cudaStream_t st);
 kda_status launch_kv_append(const AppendParams &p, cudaStream_t st);
-size_t attn_decode_workspace_bytes(int Hq, int Hk, int D);
+size_t attn_decode_workspace_bytes(int64_t N, int Hq, int Hk, int D, int64_t max_tokens);
 kda_status launch_attn_decode(const DecodeParams &p, cudaStream_t st);
 kda_status launch_attn_prompt(const PromptParams &p, cudaStream_t st);
 int take_attn_prompt_timeouts(cudaStream_t st);

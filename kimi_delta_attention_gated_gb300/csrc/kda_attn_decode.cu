@@ -725,6 +725,21 @@ bool encode(chunk::EncodeTiledFn enc, CUtensorMap *map, const void *base, const 
     return r == CUDA_SUCCESS;
 }
 
+// CTAs of a call: what the GPU holds at once, or as many as pieces are possible at all.
+template <int D, int NT>
+int decode_ctas(int64_t N, int Hq, int Hk, int64_t max_tokens) {
+    using F = Cfg<D, NT>;
+    const int64_t most = (int64_t)F::CTAS * sm_count(), group = Hq / Hk;
+    const int64_t units = N * Hk * ((group + F::ROWS - 1) / F::ROWS);
+    const int64_t pieces = (units * ((max_tokens + kStep - 1) / kStep + kPad) + kMinPiece - 1) / kMinPiece;
+    return (int)(pieces < most ? pieces : most);
+}
+
+template <int D, int NT>
+size_t workspace_bytes(int64_t N, int Hq, int Hk, int64_t max_tokens) {
+    return (size_t)decode_ctas<D, NT>(N, Hq, Hk, max_tokens) * 2 * Cfg<D, NT>::PART * sizeof(float);  // two pieces per CTA
+}
+
 template <int D, int NT>
 kda_status run(const DecodeParams &p, cudaStream_t st) {
     using F = Cfg<D, NT>;
@@ -736,7 +751,7 @@ kda_status run(const DecodeParams &p, cudaStream_t st) {
     CUtensorMap mk, mv;
     if (!encode(enc, &mk, p.c.k, p.c) || !encode(enc, &mv, p.c.v, p.c)) return KDA_ERR_CUDA;
     static DeviceOnce configured;
-    const int dev = current_device(), ctas = F::CTAS * sm_count();
+    const int dev = current_device(), ctas = decode_ctas<D, NT>(p.c.N, p.Hq, p.c.Hk, (int64_t)p.c.max_blocks * p.c.P);
     if (!configured.done(dev)) {
         if (cudaFuncSetAttribute(attn_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM) !=
             cudaSuccess) {
@@ -788,12 +803,10 @@ int take_attn_decode_timeouts(cudaStream_t st) {
     return n;
 }
 
-size_t attn_decode_workspace_bytes(int Hq, int Hk, int D) {
-    // two pieces per CTA at most
+size_t attn_decode_workspace_bytes(int64_t N, int Hq, int Hk, int D, int64_t max_tokens) {
     const bool wide = Hq / Hk > 8;
-    const int ctas = (D == 128 ? wide ? Cfg<128, 2>::CTAS : Cfg<128, 1>::CTAS : wide ? Cfg<64, 2>::CTAS : Cfg<64, 1>::CTAS) *
-                     sm_count();
-    return (size_t)ctas * 2 * (wide ? 16 : 8) * (D + 2) * sizeof(float);
+    if (D == 128) return wide ? workspace_bytes<128, 2>(N, Hq, Hk, max_tokens) : workspace_bytes<128, 1>(N, Hq, Hk, max_tokens);
+    return wide ? workspace_bytes<64, 2>(N, Hq, Hk, max_tokens) : workspace_bytes<64, 1>(N, Hq, Hk, max_tokens);
 }
 
 kda_status launch_attn_decode(const DecodeParams &p, cudaStream_t st) {

@@ -159,7 +159,7 @@ def test_graph_replays_with_grown_lengths():
     o, lse, q, cache, table, sl = case([700, 20], 2, 4, 64, 16, seed=17)
     dt = table.cuda()
     out = torch.empty_like(o)
-    ws = torch.empty(kda.attn_decode_workspace_size(8, 2, 64), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(kda.attn_decode_workspace_size(2, 8, 2, 64, dt.shape[1] * 16), dtype=torch.uint8, device="cuda")
     short = torch.tensor([1, 1], dtype=torch.int32, device="cuda")
     kda.attn_decode(q, cache, dt, short, o=out, workspace=ws)
     torch.cuda.synchronize()
