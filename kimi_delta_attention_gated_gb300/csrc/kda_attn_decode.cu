@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
         }
         for (int s = cur.s0 + warp; s < cur.s1; s += kWarps) {
             cp_wait<F::DEPTH - 1>();
-            if (!tc::mbar_wait(bars + rd, rd_phase, kPolls)) failed = 1;
+            if (!failed && !tc::mbar_wait(bars + rd, rd_phase, kPolls)) failed = 1;
             __syncwarp();
             const uint8_t *slot = smem + (warp * F::DEPTH + rd) * F::SLOT;
             const float4 sc = *reinterpret_cast<const float4 *>(smem + F::SCALES + (warp * F::DEPTH + rd) * 16);

@@ -19,7 +19,11 @@
 //                   next S together, so that one tile's softmax runs beside the other's
 //                   products; a warp has done its waiting (100 to 200 cycles a barrier) when
 //                   its turn comes
-//   warp 10         TMA: the two query tiles once, then rings of key and value blocks
+//   warp 10         TMA: the query tiles, and rings of key and value blocks
+//   warp 11         finds the next work items
+// CTAs are persistent, one per SM; work items (a run of query rows of a sequence, and a head
+// or a pair) are taken longest first, in rounds of alternating direction.  Loads, scores and
+// rings go on across items, so that an item's beginning runs beside the last one's end.
 // TMEM: S_0, S_1 (P over them), O_0, O_1, 128 columns each.
 //
 // Weights are rounded to bf16 because the product takes one type and the values are bf16;
@@ -42,8 +46,9 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = 128;             // query rows of a tile, and keys of a block
-constexpr int kMmaWarp = 8, kTmaWarp = 10;
-constexpr int kThreads = 352;
+constexpr int kMmaWarp = 8, kTmaWarp = 10, kItemWarp = 11;
+constexpr int kThreads = 384;
+constexpr int kItemReaders = 11;       // warps that follow the work items
 constexpr uint32_t kPolls = 1u << 21;  // a few seconds; a CTA waits for nothing but its own warps and loads
 constexpr float kSlack = 40.f;         // log2: how far a score may exceed the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -52,10 +57,13 @@ __device__ int g_attn_prompt_timeouts = 0;
 
 template <int D, int DV>
 struct Cfg {
-    static constexpr uint32_t QB = kTile * D * 2, KB = kTile * D * 2, VB = kTile * DV * 2;
-    static constexpr int KST = D == 64 ? 4 : 2, VST = D == 64 ? 4 : D == 192 ? 1 : 2;
+    // A block's values come whole, or with 192 channels, where shared memory holds one block of
+    // them, in two halves, each free for its successor when both tiles' products have read it.
+    static constexpr int NV = D == 192 ? 2 : 1, VROWS = kTile / NV;
+    static constexpr uint32_t QB = kTile * D * 2, KB = kTile * D * 2, VB = VROWS * DV * 2;
+    static constexpr int KST = D == 64 ? 4 : 2, VST = D == 64 ? 4 : 2;
     static constexpr uint32_t Q = 0, K = 2 * QB, V = K + KST * KB, BARS = V + VST * VB;
-    static constexpr int NBAR = 2 + 2 * KST + 2 * VST + 1 + 2 + 4 + 2 + 2;
+    static constexpr int NBAR = 4 + 2 * KST + 2 * VST + 1 + 2 + 4 + 2 + 2 + 4;
     static constexpr uint32_t SMEM = BARS + NBAR * 8 + 64 + 1024;
     static_assert(SMEM <= 232448, "shared memory budget");
     static constexpr uint32_t T_S = 0, T_O = 256;  // TMEM columns of tile 0; tile 1's follow 128 later
@@ -65,6 +73,11 @@ struct Args {
     PromptParams p;
     int pair_heads;  // 1: two heads of a group share their rows; 0: 256 rows of one head
     int n_heads;     // work items per unit: head pairs, or heads
+    int items;       // work items at most
+};
+
+struct Item {
+    int found, seq, row0, head;  // head: number of the pair, or of the head
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *r) {
@@ -107,12 +120,47 @@ __device__ __forceinline__ bool elect_one() {
     return ok != 0;
 }
 
+// 4 x 4 matrix of 16-byte pieces over four neighbouring lanes, transposed: lane i's piece q
+// becomes lane q's piece i.
+__device__ __forceinline__ void transpose_quad(uint32_t (&w)[16]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int m = 1; m <= 2; m <<= 1) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (q & m) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t give = up ? w[4 * q + e] : w[4 * (q | m) + e];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, m);
+                if (up)
+                    w[4 * q + e] = got;
+                else
+                    w[4 * (q | m) + e] = got;
+            }
+        }
+    }
+}
+
 // The weights stored so far are in TMEM: tells the products' warp (one arrival per warp).
 __device__ __forceinline__ void hand_over(uint64_t *bar) {
     tmem_wait_st();
     fence_before_sync();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// A barrier of two warps that also says whether any of their threads has `x`.
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(id)
+        : "memory");
+    return r != 0;
 }
 
 // The turn of the product warps: barrier 1 gives it to tile 0's, barrier 2 to tile 1's.
@@ -183,9 +231,9 @@ __device__ __forceinline__ int units_from(int2 x, int shift, int key) {
     return all - (((y + rows - 1) >> shift) - 1);
 }
 
-// The rank-th unit of 2^shift rows: its sequence and its first row; false if there are fewer.  One warp;
-// scratch: room for p.N int2 in shared memory.
-__device__ bool find_unit(const PromptParams &p, int shift, int rank, int2 *scratch, int &seq, int &row0) {
+// The rank-th unit of 2^shift rows: its sequence and its first row; false if there are fewer.
+// One warp; up to 32 sequences are held by its lanes.
+__device__ bool find_unit(const PromptParams &p, int shift, int rank, int &seq, int &row0) {
     const int lane = threadIdx.x & 31, rows = 1 << shift;
     if (!p.cu_q) {  // equal lengths: round by round
         const int nq = (int)(p.Tq / p.N), all = (nq + rows - 1) >> shift, u = all - 1 - rank / p.N;
@@ -197,17 +245,21 @@ __device__ bool find_unit(const PromptParams &p, int shift, int rank, int2 *scra
         row0 = (((seq_of(p, 0).nq + rows - 1) >> shift) - 1 - rank) * rows;
         return row0 >= 0;
     }
+    auto load = [&](int n) {
+        const Seq s = seq_of(p, n);
+        return make_int2(s.nq, s.nk - s.nq);
+    };
+    const int2 held = lane < p.N ? load(lane) : make_int2(0, 0);
     int lo = INT_MAX, hi = INT_MIN;  // keys lie in (lo, hi]
     for (int n = lane; n < p.N; n += 32) {
         const Seq s = seq_of(p, n);
-        scratch[n] = make_int2(s.nq, s.nk - s.nq);
         if (s.nq == 0) continue;
         lo = min(lo, s.nk - s.nq);
         hi = max(hi, s.nk);
     }
-    auto count = [&](int key) {  // each lane reads what it wrote
-        int c = 0;
-        for (int n = lane; n < p.N; n += 32) c += units_from(scratch[n], shift, key);
+    auto count = [&](int key) {
+        int c = units_from(held, shift, key);
+        for (int n = lane + 32; n < p.N; n += 32) c += units_from(load(n), shift, key);
         return __reduce_add_sync(0xffffffffu, c);
     };
     lo = __reduce_min_sync(0xffffffffu, lo);
@@ -225,7 +277,7 @@ __device__ bool find_unit(const PromptParams &p, int shift, int rank, int2 *scra
         const int n = n0 + lane;
         int u = -1;
         if (n < p.N) {
-            const int2 x = scratch[n];
+            const int2 x = n0 ? load(n) : held;
             const int a = units_from(x, shift, lo);
             if (a > units_from(x, shift, lo + 1)) u = ((x.x + rows - 1) >> shift) - a;
         }
@@ -294,37 +346,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm), sb16 = sb >> 4;
-    uint64_t *q_full = reinterpret_cast<uint64_t *>(sm + L::BARS);  // [2]
-    uint64_t *k_full = q_full + 2, *k_empty = k_full + L::KST;
+    uint64_t *q_full = reinterpret_cast<uint64_t *>(sm + L::BARS), *q_empty = q_full + 2;  // [2] each
+    uint64_t *k_full = q_empty + 2, *k_empty = k_full + L::KST;
     uint64_t *v_full = k_empty + L::KST, *v_empty = v_full + L::VST;
     uint64_t *v_raw = v_empty + L::VST;                             // a last value block, before its tail is zeroed
     uint64_t *s_full = v_raw + 1, *p_ready = s_full + 2;            // p_ready[tile * 2 + half]
-    uint64_t *o_full = p_ready + 4;
-    uint64_t *drain = o_full + 2;
-    int *work = reinterpret_cast<int *>(drain + 2);                 // [0] found, [1] sequence, [2] first row
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(work + 4);
-    volatile int *abort_flag = work + 5;                            // a bounded wait gave up
+    uint64_t *o_full = p_ready + 4, *drain = o_full + 2;
+    uint64_t *i_full = drain + 2, *i_empty = i_full + 2;            // the work items' two slots
+    Item *slots = reinterpret_cast<Item *>(i_empty + 2);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(slots + 2);
+    volatile int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);  // a bounded wait gave up
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    const int item = blockIdx.x % a.n_heads, rank = blockIdx.x / a.n_heads;
-    if (warp == 0) {
-        int seq = 0, row0 = 0;
-        const bool found = find_unit(p, a.pair_heads ? 7 : 8, rank, reinterpret_cast<int2 *>(sm), seq, row0);
-        fence_async_smem();  // the scratch is the loads' room from here on
-        if (lane == 0) {
-            work[0] = found;
-            work[1] = seq;
-            work[2] = row0;
-        }
-    }
-    if (warp == 1 && lane == 0) {
+    if (warp == 0 && lane == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, 1);
+            mbar_init(q_empty + i, 1);
             mbar_init(s_full + i, 1);
             mbar_init(p_ready + 2 * i, 4);
             mbar_init(p_ready + 2 * i + 1, 4);
             mbar_init(o_full + i, 1);
             mbar_init(drain + i, 1);
+            mbar_init(i_full + i, 1);
+            mbar_init(i_empty + i, kItemReaders);
         }
         for (int i = 0; i < L::KST; ++i) {
             mbar_init(k_full + i, 1);
@@ -348,44 +392,81 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     fence_after_sync();
     const uint32_t tb = *tmem_slot;
+    const int group = p.Hq / p.Hk;
     int failed = 0;
-    if (work[0]) {
-        const Seq s = seq_of(p, work[1]);
-        const int row0 = work[2], group = p.Hq / p.Hk;
-        const int head0 = a.pair_heads ? 2 * item : item, kvh = head0 / group;
-        auto tile_row = [&](int t) { return a.pair_heads ? row0 : row0 + t * kTile; };
-        // key blocks that tile t sees
-        auto tile_blocks = [&](int t) {
-            const int r = tile_row(t), last = min(r + kTile, s.nq) - 1;
-            if (r >= s.nq) return 0;
-            const int seen = max(0, min(s.nk, last + 1 + s.nk - s.nq));
-            return (seen + kTile - 1) / kTile;
-        };
-        const int n0 = tile_blocks(0), n1 = tile_blocks(1), nb = max(n0, n1);
-        auto wait = [&](uint64_t *bar, uint32_t parity) {
-            for (uint32_t i = 0; i < kPolls; ++i) {
-                if (mbar_try_wait(bar, parity)) return true;
-                if (*abort_flag) break;
-            }
-            *abort_flag = 1;
-            return false;
-        };
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        for (uint32_t i = 0; i < kPolls; ++i) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if (*abort_flag) break;
+        }
+        *abort_flag = 1;
+        return false;
+    };
+    // This CTA's k-th work item; one warp.
+    auto find_item = [&](int k) {
+        const int64_t i = (int64_t)k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        Item it = {0, 0, 0, (int)(i % a.n_heads)};
+        if (i < a.items) it.found = find_unit(p, a.pair_heads ? 7 : 8, (int)(i / a.n_heads), it.seq, it.row0);
+        return it;
+    };
+    // The same from the item warp, for a warp that follows them all; false when a wait gave up.
+    auto take_item = [&](int k, Item &it) {
+        if (!__all_sync(0xffffffffu, wait(i_full + (k & 1), (k >> 1) & 1))) return false;
+        it = slots[k & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(i_empty + (k & 1));
+        return true;
+    };
+    auto tile_row = [&](const Item &it, int t) { return a.pair_heads ? it.row0 : it.row0 + t * kTile; };
+    // Key blocks that tile t of an item sees.
+    auto tile_blocks = [&](const Item &it, const Seq &s, int t) {
+        const int r = tile_row(it, t), last = min(r + kTile, s.nq) - 1;
+        if (r >= s.nq) return 0;
+        const int seen = max(0, min(s.nk, last + 1 + s.nk - s.nq));
+        return (seen + kTile - 1) / kTile;
+    };
 
-        if (warp == kTmaWarp) {
-            // ---- loads
-            uint32_t raw = 0;
-            int nk_issued = 0, nv_issued = 0;
+    if (warp == kItemWarp) {
+        // ---- work items, two ahead
+        for (int k = 0;; ++k) {
+            if (k >= 2 && !wait(i_empty + (k & 1), ((k >> 1) - 1) & 1)) {
+                failed = 1;
+                break;
+            }
+            const Item it = find_item(k);
+            if (lane == 0) {
+                slots[k & 1] = it;
+                mbar_arrive(i_full + (k & 1));
+            }
+            __syncwarp();
+            if (!it.found) break;
+        }
+    } else if (warp == kTmaWarp) {
+        // ---- loads
+        uint32_t raw = 0;
+        int nq_issued[2] = {0, 0}, nk_issued = 0, nv_issued = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            Item it;
+            ok = take_item(k, it);
+            if (!ok || !it.found) break;
+            const Seq s = seq_of(p, it.seq);
+            const int head0 = a.pair_heads ? 2 * it.head : it.head, kvh = head0 / group;
+            const int n0 = tile_blocks(it, s, 0), n1 = tile_blocks(it, s, 1), nb = max(n0, n1);
             auto load_q = [&](int t) {
+                if (nq_issued[t] > 0 && !wait(q_empty + t, (nq_issued[t] - 1) & 1)) return false;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(q_full + t, L::QB);
                     for (int x = 0; x < D; x += 64)
                         tma_load_3d(sb + L::Q + t * L::QB + (x / 64) * kTile * 128, &map_q, q_full + t, x,
-                                    a.pair_heads ? head0 + t : head0, s.q0 + tile_row(t));
+                                    a.pair_heads ? head0 + t : head0, s.q0 + tile_row(it, t));
                 }
+                ++nq_issued[t];
+                return true;
             };
             auto load_k = [&](int j) {
-                const int st = j % L::KST;
-                if (j >= L::KST && !wait(k_empty + st, (j / L::KST - 1) & 1)) return false;
+                const int i = nk_issued, st = i % L::KST;
+                if (i >= L::KST && !wait(k_empty + st, (i / L::KST - 1) & 1)) return false;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(k_full + st, L::KB);
                     for (int x = 0; x < D; x += 64)
@@ -395,26 +476,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++nk_issued;
                 return true;
             };
-            auto load_v = [&](int j) {
-                const int st = j % L::VST;
-                if (j >= L::VST && !wait(v_empty + st, (j / L::VST - 1) & 1)) return false;
-                const int rows = s.nk - j * kTile;  // of the sequence
-                uint64_t *bar = rows < kTile ? v_raw : v_full + st;
+            auto load_v = [&](int j, int h) {
+                const int i = nv_issued, st = i % L::VST;
+                if (i >= L::VST && !wait(v_empty + st, (i / L::VST - 1) & 1)) return false;
+                const int rows = max(0, s.nk - j * kTile - h * L::VROWS);  // of the sequence
+                uint64_t *bar = rows < L::VROWS ? v_raw : v_full + st;
                 const uint32_t base = L::V + st * L::VB;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar, L::VB);
                     for (int x = 0; x < DV; x += 64)
-                        tma_load_3d(sb + base + (x / 64) * kTile * 128, &map_v, bar, x, kvh, s.k0 + j * kTile);
+                        tma_load_3d(sb + base + (x / 64) * L::VROWS * 128, &map_v, bar, x, kvh,
+                                    s.k0 + j * kTile + h * L::VROWS);
                 }
-                if (rows < kTile) {
-                    const bool ok = wait(v_raw, raw++ & 1);
-                    if (!ok) {  // the copy must still land before the CTA may exit
-                        mbar_wait(v_raw, (raw - 1) & 1, kPolls);
-                        return false;
-                    }
-                    for (int i = lane; i < (kTile - rows) * (DV / 64) * 8; i += 32) {
+                if (rows < L::VROWS) {
+                    const bool landed = wait(v_raw, raw & 1);
+                    if (!landed) mbar_wait(v_raw, raw & 1, kPolls);  // the copy must still land before the CTA may end
+                    ++raw;
+                    if (!landed) return false;
+                    for (int i = lane; i < (L::VROWS - rows) * (DV / 64) * 8; i += 32) {
                         const int r = rows + i / ((DV / 64) * 8), q = i % ((DV / 64) * 8);
-                        st_shared_v4(sb + base + (q >> 3) * kTile * 128 + r * 128 + (q & 7) * 16, 0, 0, 0, 0);
+                        st_shared_v4(sb + base + (q >> 3) * L::VROWS * 128 + r * 128 + (q & 7) * 16, 0, 0, 0, 0);
                     }
                     fence_async_smem();
                     __syncwarp();
@@ -423,111 +504,151 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++nv_issued;
                 return true;
             };
-            bool ok = true;
-            if (n0) load_q(0);
-            if (nb) ok = load_k(0);
-            if (n1) load_q(1);
+            if (n0) ok = load_q(0);
+            if (ok && nb) ok = load_k(0);
+            if (ok && n1) ok = load_q(1);
             for (int j = 0; j < nb && ok; ++j) {
-                if (j + 1 < nb && L::KST > 1) ok = load_k(j + 1);
-                if (ok) ok = load_v(j);
+                if (j + 1 < nb) ok = load_k(j + 1);
+                for (int h = 0; h < L::NV && ok; ++h) ok = load_v(j, h);
             }
-            if (!ok) failed = 1;
-            // every load lands before the CTA may exit
-            if (n0) mbar_wait(q_full, 0, kPolls);
-            if (n1) mbar_wait(q_full + 1, 0, kPolls);
-            for (int j = max(0, nk_issued - L::KST); j < nk_issued; ++j)
-                mbar_wait(k_full + j % L::KST, (j / L::KST) & 1, kPolls);
-            for (int j = max(0, nv_issued - L::VST); j < nv_issued; ++j)
-                mbar_wait(v_full + j % L::VST, (j / L::VST) & 1, kPolls);
-        } else if (warp >= kMmaWarp) {
-            // ---- products of tile t.  One thread's instructions come one at a time, about five
-            // cycles each, so the descriptors are bases plus constants.
-            const int t = warp - kMmaWarp, nt = t ? n1 : n0;
-            const uint32_t id_s = idesc_bf16(kTile, kTile, false, false, p.scale < 0.f);
-            const uint32_t id_o = idesc_bf16(kTile, DV, false, true);
-            const uint32_t lo_kmajor = sb16 | (16u >> 4) << 16, lo_v = sb16 | (kTile * 128u >> 4) << 16;
-            const uint32_t q_lo = lo_kmajor + ((L::Q + t * L::QB) >> 4), t_s = tb + L::T_S + t * 128, t_o = tb + L::T_O + t * 128;
-            auto scores = [&](uint32_t k_lo) {
+            ok = __all_sync(0xffffffffu, ok);
+        }
+        if (!ok) failed = 1;
+        // every load lands before the CTA may end
+        for (int t = 0; t < 2; ++t)
+            if (nq_issued[t]) mbar_wait(q_full + t, (nq_issued[t] - 1) & 1, kPolls);
+        for (int j = max(0, nk_issued - L::KST); j < nk_issued; ++j)
+            mbar_wait(k_full + j % L::KST, (j / L::KST) & 1, kPolls);
+        for (int j = max(0, nv_issued - L::VST); j < nv_issued; ++j)
+            mbar_wait(v_full + j % L::VST, (j / L::VST) & 1, kPolls);
+    } else if (warp >= kMmaWarp) {
+        // ---- products of tile t.  One thread's instructions come one at a time, about five
+        // cycles each, so the descriptors are bases plus constants.
+        const int t = warp - kMmaWarp;
+        const uint32_t id_s = idesc_bf16(kTile, kTile, false, false, p.scale < 0.f);
+        const uint32_t id_o = idesc_bf16(kTile, DV, false, true);
+        const uint32_t lo_kmajor = sb16 | (16u >> 4) << 16, lo_v = sb16 | (L::VROWS * 128u >> 4) << 16;
+        const uint32_t q_lo = lo_kmajor + ((L::Q + t * L::QB) >> 4), t_s = tb + L::T_S + t * 128, t_o = tb + L::T_O + t * 128;
+        int ks = 0, vs = 0;       // ring places of the next keys and values
+        uint32_t kp = 0, vp = 0;  // and the parities of their rounds
+        uint32_t blocks = 0, tiles = 0;  // of this tile so far: key blocks, and items with any
+        bool begun = false, ok = true;
+        auto scores = [&] {
+            const uint32_t k_lo = lo_kmajor + (L::K >> 4) + ks * (L::KB >> 4);
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x) {
-                    const uint32_t off = ((x / 4) * kTile * 128 + (x % 4) * 32) >> 4;
-                    mma_ss(t_s, desc_of(q_lo + off), desc_of(k_lo + off), id_s, x > 0);
-                }
+            for (int x = 0; x < D / 16; ++x) {
+                const uint32_t off = ((x / 4) * kTile * 128 + (x % 4) * 32) >> 4;
+                mma_ss(t_s, desc_of(q_lo + off), desc_of(k_lo + off), id_s, x > 0);
+            }
+            mma_commit(s_full + t);
+            mma_commit(k_empty + ks);
+        };
+        // A half's product with its values, the last of both of a slot letting go of it.
+        auto weigh = [&](int h, int slot, bool more) {
+            const uint32_t v_lo = lo_v + (L::V >> 4) + slot * (L::VB >> 4) + (L::NV == 1 ? h * 4 * (2048 >> 4) : 0);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                mma_ts(t_o, t_s + (4 * h + x) * 8, desc_of(v_lo + x * (2048 >> 4)), id_o, x > 0 ? 1u : more);
+            if (L::NV == 2 || h == 1) mma_commit(v_empty + slot);
+        };
+        for (int k = 0;; ++k) {
+            Item it;
+            // both product warps go on or stop together: each waits for the other's turns
+            const bool taken = take_item(k, it);
+            if (pair_any(3, !ok || !taken)) {
+                failed = 1;
+                break;
+            }
+            if (!it.found) break;
+            const Seq s = seq_of(p, it.seq);
+            const int n0 = tile_blocks(it, s, 0), n1 = tile_blocks(it, s, 1), nb = max(n0, n1), nt = t ? n1 : n0;
+            auto next_keys = [&] {
+                if (++ks == L::KST) ks = 0, kp ^= 1;
             };
-            bool ok = true;
-            if (nt) {
-                ok = wait(q_full + t, 0) && wait(k_full, 0);
+            if (nt) ok = wait(q_full + t, tiles & 1);
+            if (nb) {
+                ok = ok && wait(k_full + ks, kp);
                 fence_after_sync();
                 if (ok && elect_one()) {
-                    scores(lo_kmajor + (L::K >> 4));
-                    mma_commit(s_full + t);
-                    mma_commit(k_empty);
+                    if (nt) {
+                        scores();
+                        if (nt == 1) mma_commit(q_empty + t);
+                    } else {
+                        mbar_arrive(k_empty + ks);  // every block is let go of by both tiles
+                    }
                 }
-            } else if (nb) {  // every block is let go of by both tiles
-                ok = wait(k_full, 0);
-                if (ok && elect_one()) mbar_arrive(k_empty);
+                next_keys();
             }
-            int ks = 0, vs = 0;       // ring places of the next keys and of this block's values
-            uint32_t kp = 0, vp = 0;  // and the parities of their rounds
             for (int j = 0; j < nb; ++j) {
-                if (++ks == L::KST) ks = 0, kp ^= 1;
-                const bool mine = j < nt, next = j + 1 < nt;
-                // (an idle tile follows the rings too, and lets go of every block)
+                const bool mine = j < nt, next = j + 1 < nt, more = j + 1 < nb;  // (an idle tile follows the rings too)
                 ok = ok && wait(v_full + vs, vp);
-                if (j + 1 < nb) ok = ok && wait(k_full + ks, kp);
-                if (mine) ok = ok && wait(p_ready + 2 * t, j & 1);
+                if (more) ok = ok && wait(k_full + ks, kp);
+                if (mine) ok = ok && wait(p_ready + 2 * t, (blocks + j) & 1);
                 fence_after_sync();
-                if (t || j) turn_wait(1 + t);
-                const uint32_t k_lo = lo_kmajor + (L::K >> 4) + ks * (L::KB >> 4), v_lo = lo_v + (L::V >> 4) + vs * (L::VB >> 4);
-                if (mine && ok && elect_one()) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        mma_ts(t_o, t_s + x * 8, desc_of(v_lo + (x * 2048 >> 4)), id_o, x > 0 ? 1u : j > 0);
+                if (t || begun) turn_wait(1 + t);
+                begun = true;
+                if (mine && ok && elect_one()) weigh(0, vs, j > 0);
+                __syncwarp();
+                const int vs0 = vs;
+                if (L::NV == 2) {
+                    if (!mine && ok && lane == 0) mbar_arrive(v_empty + vs0);
+                    if (++vs == L::VST) vs = 0, vp ^= 1;
+                    ok = ok && wait(v_full + vs, vp);
                 }
-                if (mine) ok = ok && wait(p_ready + 2 * t + 1, j & 1);
+                if (mine) ok = ok && wait(p_ready + 2 * t + 1, (blocks + j) & 1);
                 fence_after_sync();
                 if (ok && elect_one()) {
                     if (mine) {
-#pragma unroll
-                        for (int x = 4; x < 8; ++x) mma_ts(t_o, t_s + x * 8, desc_of(v_lo + (x * 2048 >> 4)), id_o, 1u);
-                        mma_commit(v_empty + vs);
+                        weigh(1, vs, true);
                         // the next scores overwrite this block's weights: behind the product in the same queue
                         if (next) {
-                            scores(k_lo);
-                            mma_commit(s_full + t);
-                            mma_commit(k_empty + ks);
+                            scores();
+                            if (j + 2 == nt) mma_commit(q_empty + t);
                         } else {
                             mma_commit(o_full + t);
                         }
                     } else {
                         mbar_arrive(v_empty + vs);
                     }
-                    if (!next && j + 1 < nb) mbar_arrive(k_empty + ks);
+                    if (!next && more) mbar_arrive(k_empty + ks);
                 }
                 __syncwarp();
-                if (!t || j + 1 < nb) turn_pass(2 - t);
+                turn_pass(2 - t);
+                if (more) next_keys();
                 if (++vs == L::VST) vs = 0, vp ^= 1;
             }
-            if (!ok) failed = 1;
-            // nothing issued may still run, and no commit arrive, once the CTA has ended
-            if (elect_one()) {
-                mma_commit(drain + t);
-                mbar_wait(drain + t, 0, kPolls);
-            }
-            __syncwarp();
-        } else {
-            // ---- softmax of tile t, a thread per row
-            const int t = warp >> 2, nt = t ? n1 : n0, m_row = (warp & 3) * 32 + lane;
-            const int row = tile_row(t) + m_row, head = a.pair_heads ? head0 + t : head0;
-            const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-            const uint32_t t_s = tb + lane_base + L::T_S + t * 128, t_o = tb + lane_base + L::T_O + t * 128;
+            blocks += nt;
+            tiles += nt > 0;
+            ok = __all_sync(0xffffffffu, ok);
+        }
+        if (!t && begun) turn_wait(1);  // the other warp's last turn was passed here
+        // nothing issued may still run, and no commit arrive, once the CTA has ended
+        if (elect_one()) {
+            mma_commit(drain + t);
+            mbar_wait(drain + t, 0, kPolls);
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax of tile t, a thread per row
+        const int t = warp >> 2, m_row = (warp & 3) * 32 + lane;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t t_s = tb + lane_base + L::T_S + t * 128, t_o = tb + lane_base + L::T_O + t * 128;
+        const float c = fabsf(p.scale) * kLog2e;
+        uint32_t blocks = 0, tiles = 0;  // of this tile so far: key blocks, and items with any
+        bool ok = true;
+        int k = 0;
+        for (; ok; ++k) {
+            Item it;
+            ok = take_item(k, it);
+            if (!ok || !it.found) break;
+            const Seq s = seq_of(p, it.seq);
+            const int nt = tile_blocks(it, s, t), row0 = tile_row(it, t), row = row0 + m_row;
+            const int head = a.pair_heads ? 2 * it.head + t : it.head;
             const int seen = max(0, min(s.nk, row + 1 + s.nk - s.nq));
-            const int seen_first = max(0, min(s.nk, tile_row(t) + 1 + s.nk - s.nq));  // of the tile's first row
-            const float c = fabsf(p.scale) * kLog2e;
+            const int seen_first = max(0, min(s.nk, row0 + 1 + s.nk - s.nq));  // of the tile's first row
             float m = -INFINITY, l = 0.f;
-            bool ok = true;
-            for (int j = 0; j < nt; ++j) {
-                ok = wait(s_full + t, j & 1);
+            for (int j = 0; j < nt; ++j, ++blocks) {
+                ok = wait(s_full + t, blocks & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 fence_after_sync();
@@ -579,74 +700,80 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
             }
-            if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait(o_full + t, 0));
+            if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait(o_full + t, tiles & 1));
+            tiles += nt > 0;
             fence_after_sync();
-            if (!ok) failed = 1;
+            if (row0 >= s.nq) continue;  // the item has no such tile
             const bool live = row < s.nq;
             const int64_t out = (int64_t)(s.q0 + row) * p.Hq + head;
             const float inv = !ok ? __int_as_float(0x7fc00000) : l == 0.f ? 0.f : 1.f / l;
-            // The rows go out through the tile's query room in shared memory (the products that read
-            // it are done), so that a warp writes whole rows: lanes writing a row each touch 32
-            // lines per store, 4,400 cycles a tile instead of about 1,000.
+            // Four lanes exchange 16-byte pieces of their rows, so that they write 64 bytes of a row
+            // together (lanes writing a row each touch 32 lines per store).
+            const int first = row0 + (warp & 3) * 32 + (lane & ~3);  // of the four rows
+            const int esz = p.o_bf16 ? 2 : 4;
+            uint8_t *o_rows = static_cast<uint8_t *>(p.o) + ((int64_t)(s.q0 + first) * p.Hq + head) * DV * esz + (lane & 3) * 16;
+            const int64_t pitch = (int64_t)p.Hq * DV * esz;
             bool nan = false;
-            const uint32_t stage = sb + L::Q + t * L::QB + (warp & 3) * (32 * DV * 2);
-            const int row_bytes = p.o_bf16 ? DV * 2 : DV * 4, chunks = row_bytes / 16;
-            const int halves = p.o_bf16 ? 1 : 2;  // fp32 rows go out in two halves of their channels
-            for (int h = 0; h < halves; ++h) {
-                const int d_end = DV / halves;
 #pragma unroll 1
-                for (int d = 0; d < d_end; d += 32) {
-                    float r[32];
-                    if (ok && nt > 0) {
-                        tmem_ld32(t_o + h * d_end + d, r);
-                        tmem_wait_ld();
+            for (int d = 0; d < DV; d += 32) {
+                float r[32];
+                if (ok && nt > 0) {
+                    tmem_ld32(t_o + d, r);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; i += 16)
-                            asm volatile("" : "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]),
-                                         "+f"(r[i + 5]), "+f"(r[i + 6]), "+f"(r[i + 7]), "+f"(r[i + 8]), "+f"(r[i + 9]),
-                                         "+f"(r[i + 10]), "+f"(r[i + 11]), "+f"(r[i + 12]), "+f"(r[i + 13]),
-                                         "+f"(r[i + 14]), "+f"(r[i + 15]));
-                    } else {
+                    for (int i = 0; i < 32; i += 16)
+                        asm volatile("" : "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]),
+                                     "+f"(r[i + 5]), "+f"(r[i + 6]), "+f"(r[i + 7]), "+f"(r[i + 8]), "+f"(r[i + 9]),
+                                     "+f"(r[i + 10]), "+f"(r[i + 11]), "+f"(r[i + 12]), "+f"(r[i + 13]), "+f"(r[i + 14]),
+                                     "+f"(r[i + 15]));
+                } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) r[i] = 0.f;
-                    }
+                    for (int i = 0; i < 32; ++i) r[i] = 0.f;
+                }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        r[i] *= inv;
-                        nan |= isnan(r[i]);
-                    }
-                    // 16-byte piece q of row `lane` lies at q ^ (lane % 8) of its 2 * DV bytes
-                    const uint32_t base = stage + lane * (DV * 2);
-                    if (p.o_bf16) {
+                for (int i = 0; i < 32; ++i) {
+                    r[i] *= inv;
+                    nan |= isnan(r[i]);
+                }
+                auto store = [&](uint32_t (&w)[16], int byte) {
+                    transpose_quad(w);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            st_shared_v4(base + (((d / 8 + i) ^ (lane & 7)) << 4), pack_bf16x2(r[8 * i], r[8 * i + 1]),
-                                         pack_bf16x2(r[8 * i + 2], r[8 * i + 3]), pack_bf16x2(r[8 * i + 4], r[8 * i + 5]),
-                                         pack_bf16x2(r[8 * i + 6], r[8 * i + 7]));
-                    } else {
+                    for (int i = 0; i < 4; ++i)
+                        if (first + i < s.nq)
+                            *reinterpret_cast<uint4 *>(o_rows + i * pitch + byte) =
+                                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                };
+                uint32_t w[16];
+                if (p.o_bf16) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            st_shared_v4(base + (((d / 4 + i) ^ (lane & 7)) << 4), __float_as_uint(r[4 * i]),
-                                         __float_as_uint(r[4 * i + 1]), __float_as_uint(r[4 * i + 2]),
-                                         __float_as_uint(r[4 * i + 3]));
+                    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(r[2 * i], r[2 * i + 1]);
+                    store(w, d * 2);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(r[16 * h + i]);
+                        store(w, (d + 16 * h) * 4);
                     }
                 }
-                __syncwarp();
-                const int per = chunks / halves;  // pieces of a row in this pass
-                uint8_t *o = static_cast<uint8_t *>(p.o) + ((int64_t)(s.q0 + tile_row(t) + (warp & 3) * 32) * p.Hq + head) * row_bytes;
-                const int live_rows = min(32, s.nq - (tile_row(t) + (warp & 3) * 32));
-#pragma unroll 4
-                for (int i = lane; i < live_rows * per; i += 32) {
-                    const int rr = i / per, q = i - rr * per;
-                    const uint4 w = *reinterpret_cast<const uint4 *>(
-                        sm + (stage - sb) + rr * (DV * 2) + ((q ^ (rr & 7)) << 4));
-                    *reinterpret_cast<uint4 *>(o + (int64_t)rr * p.Hq * row_bytes + h * (row_bytes / 2) + q * 16) = w;
-                }
-                __syncwarp();
             }
+            __syncwarp();
             if (live) {
                 if (p.lse) p.lse[out] = !ok ? __int_as_float(0x7fc00000) : l == 0.f ? -INFINITY : (log2f(l) + m) * kLn2;
                 if (nan && ok) rescue_row<D, DV>(p, s, row, head, seen, nt, m, l, copysignf(c, p.scale));
+            }
+        }
+        if (!ok) {  // what this CTA still had to do: NaN
+            failed = 1;
+            for (;; ++k) {
+                const Item it = find_item(k);
+                if (!it.found) break;
+                const Seq s = seq_of(p, it.seq);
+                const int row = tile_row(it, t) + m_row, head = a.pair_heads ? 2 * it.head + t : it.head;
+                if (row >= s.nq) continue;
+                const int64_t out = (int64_t)(s.q0 + row) * p.Hq + head;
+                for (int d = 0; d < DV; ++d) st_out(p.o, out * DV + d, __int_as_float(0x7fc00000), p.o_bf16);
+                if (p.lse) p.lse[out] = __int_as_float(0x7fc00000);
             }
         }
     }
@@ -657,12 +784,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // A tensor of rows (heads of `dim` bf16 elements, `stride` elements from row to row) in boxes
-// of 64 channels x 1 head x 128 rows.
+// of 64 channels x 1 head x box_rows.
 bool encode(chunk::EncodeTiledFn enc, CUtensorMap *map, const void *base, int dim, int heads, int64_t rows,
-            int64_t stride) {
+            int64_t stride, int box_rows) {
     const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
     const cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)stride * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)kTile}, es[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows}, es[3] = {1, 1, 1};
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -691,10 +818,10 @@ kda_status run(const PromptParams &p, cudaStream_t st) {
     CUtensorMap mq, mk, mv;
     // without keys nothing is loaded; the map still needs an address
     const bool keys = p.Tk > 0;
-    if (!encode(enc, &mq, p.q, D, p.Hq, p.Tq, p.q_stride) ||
-        !encode(enc, &mk, keys ? p.k : p.q, D, keys ? p.Hk : p.Hq, keys ? p.Tk : p.Tq, keys ? p.k_stride : p.q_stride) ||
+    if (!encode(enc, &mq, p.q, D, p.Hq, p.Tq, p.q_stride, kTile) ||
+        !encode(enc, &mk, keys ? p.k : p.q, D, keys ? p.Hk : p.Hq, keys ? p.Tk : p.Tq, keys ? p.k_stride : p.q_stride, kTile) ||
         !encode(enc, &mv, keys ? p.v : p.q, keys ? DV : D, keys ? p.Hk : p.Hq, keys ? p.Tk : p.Tq,
-                keys ? p.v_stride : p.q_stride))
+                keys ? p.v_stride : p.q_stride, L::VROWS))
         return KDA_ERR_CUDA;
     Args a;
     memset(&a, 0, sizeof(a));
@@ -702,12 +829,14 @@ kda_status run(const PromptParams &p, cudaStream_t st) {
     a.pair_heads = (p.Hq / p.Hk) % 2 == 0;
     a.n_heads = a.pair_heads ? p.Hq / 2 : p.Hq;
     // A sequence of n rows has at most n / rows + 1 units.
-    const int64_t grid = (p.Tq / (a.pair_heads ? kTile : 2 * kTile) + p.N) * a.n_heads;
-    if (grid > INT32_MAX) {
+    const int64_t items = (p.Tq / (a.pair_heads ? kTile : 2 * kTile) + p.N) * a.n_heads;
+    if (items > INT32_MAX) {
         set_error("kda_attn_prompt: too many tokens");
         return KDA_ERR_UNSUPPORTED;
     }
-    attn_prompt_kernel<D, DV><<<(unsigned)grid, kThreads, L::SMEM, st>>>(mq, mk, mv, a);
+    a.items = (int)items;
+    const int sms = sm_count();
+    attn_prompt_kernel<D, DV><<<a.items < sms ? a.items : sms, kThreads, L::SMEM, st>>>(mq, mk, mv, a);
     note_launch();
     return check_launch("attn_prompt_kernel");
 }
