@@ -658,10 +658,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait_ld64(x);
                 wait_ld64(x + 64);
                 if ((j + 1) * kTile > seen_first) {
-                    const int lim = seen - j * kTile;  // of this block's keys, how many the row sees
+                    // keys behind what the row sees, by runs of 32: those that the warp's first row sees whole
+                    // need no look
+                    const int lim = seen - j * kTile, w_lo = __shfl_sync(0xffffffffu, lim, 0);
 #pragma unroll
-                    for (int i = 0; i < 128; ++i)
-                        if (i >= lim) x[i] = -INFINITY;
+                    for (int q = 0; q < 4; ++q) {
+                        if (32 * q + 32 <= w_lo) continue;
+#pragma unroll
+                        for (int i = 32 * q; i < 32 * q + 32; ++i)
+                            if (i >= lim) x[i] = -INFINITY;
+                    }
                 }
                 float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -713,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int esz = p.o_bf16 ? 2 : 4;
             uint8_t *o_rows = static_cast<uint8_t *>(p.o) + ((int64_t)(s.q0 + first) * p.Hq + head) * DV * esz + (lane & 3) * 16;
             const int64_t pitch = (int64_t)p.Hq * DV * esz;
-            bool nan = false;
+            float odd = 0.f;  // 0, or NaN where an output is not finite
 #pragma unroll 1
             for (int d = 0; d < DV; d += 32) {
                 float r[32];
@@ -733,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     r[i] *= inv;
-                    nan |= isnan(r[i]);
+                    odd = fmaf(r[i], 0.f, odd);
                 }
                 auto store = [&](uint32_t (&w)[16], int byte) {
                     transpose_quad(w);
@@ -760,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (live) {
                 if (p.lse) p.lse[out] = !ok ? __int_as_float(0x7fc00000) : l == 0.f ? -INFINITY : (log2f(l) + m) * kLn2;
-                if (nan && ok) rescue_row<D, DV>(p, s, row, head, seen, nt, m, l, copysignf(c, p.scale));
+                if (isnan(odd) && ok) rescue_row<D, DV>(p, s, row, head, seen, nt, m, l, copysignf(c, p.scale));
             }
         }
         if (!ok) {  // what this CTA still had to do: NaN
