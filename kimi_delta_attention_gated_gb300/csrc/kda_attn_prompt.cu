@@ -90,6 +90,26 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *r) {
           "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
         : "r"(taddr));
 }
+// A TMA load with a priority in L2: queries are read once and leave first, keys and values are
+// read again by other work items.
+__device__ __forceinline__ void tma_load_hint(uint32_t dst, const void *tmap, uint64_t *bar, int x, int y, int z, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, "
+        "%4}], [%5], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ uint64_t leave_first() {
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint64_t leave_last() {
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
 // Waits for the loads issued so far; naming the registers keeps their uses behind the wait.
 __device__ __forceinline__ void wait_ld64(float *r) {
     tmem_wait_ld();
@@ -443,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kTmaWarp) {
         // ---- loads
+        const uint64_t once = leave_first(), again = leave_last();
         uint32_t raw = 0;
         int nq_issued[2] = {0, 0}, nk_issued = 0, nv_issued = 0;
         bool ok = true;
@@ -458,8 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) {
                     mbar_arrive_expect_tx(q_full + t, L::QB);
                     for (int x = 0; x < D; x += 64)
-                        tma_load_3d(sb + L::Q + t * L::QB + (x / 64) * kTile * 128, &map_q, q_full + t, x,
-                                    a.pair_heads ? head0 + t : head0, s.q0 + tile_row(it, t));
+                        tma_load_hint(sb + L::Q + t * L::QB + (x / 64) * kTile * 128, &map_q, q_full + t, x,
+                                      a.pair_heads ? head0 + t : head0, s.q0 + tile_row(it, t), once);
                 }
                 ++nq_issued[t];
                 return true;
@@ -470,8 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) {
                     mbar_arrive_expect_tx(k_full + st, L::KB);
                     for (int x = 0; x < D; x += 64)
-                        tma_load_3d(sb + L::K + st * L::KB + (x / 64) * kTile * 128, &map_k, k_full + st, x, kvh,
-                                    s.k0 + j * kTile);
+                        tma_load_hint(sb + L::K + st * L::KB + (x / 64) * kTile * 128, &map_k, k_full + st, x, kvh,
+                                      s.k0 + j * kTile, again);
                 }
                 ++nk_issued;
                 return true;
@@ -485,8 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar, L::VB);
                     for (int x = 0; x < DV; x += 64)
-                        tma_load_3d(sb + base + (x / 64) * L::VROWS * 128, &map_v, bar, x, kvh,
-                                    s.k0 + j * kTile + h * L::VROWS);
+                        tma_load_hint(sb + base + (x / 64) * L::VROWS * 128, &map_v, bar, x, kvh,
+                                      s.k0 + j * kTile + h * L::VROWS, again);
                 }
                 if (rows < L::VROWS) {
                     const bool landed = wait(v_raw, raw & 1);
@@ -746,8 +767,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (first + i < s.nq)
-                            *reinterpret_cast<uint4 *>(o_rows + i * pitch + byte) =
-                                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                            __stcs(reinterpret_cast<uint4 *>(o_rows + i * pitch + byte),
+                                   make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
                 };
                 uint32_t w[16];
                 if (p.o_bf16) {
