@@ -96,6 +96,7 @@ uint64_t kda_launch_count(void);
  * into every output it was responsible for (the state, o and y of its (sequence,
  * head) units, or the y and state rows of its convolution tiles; a decode CTA also
  * poisons every later unit it owned), and counts the event in a device-side counter.
+ * (An attention CTA poisons the rows that it had not written yet.)
  * The compute calls are asynchronous and cannot see this, so this call synchronises
  * `stream` (a cudaStream_t; NULL = the legacy default stream), reads the counters of
  * the current device and clears them.  Returns KDA_ERR_TIMEOUT if any wait gave up
@@ -540,8 +541,10 @@ kda_status kda_rotary(const void *x, kda_dtype dtype, int64_t x_stride, const in
  *                NULL: nothing is rotated (rotary_dim 0)
  *   q, q_out     [tokens, q_heads, dim] bf16, q q_stride apart, q_out dense; both or neither
  *   k_out        [tokens, kv_heads, dim] bf16, dense, or NULL: the rotated keys
+ * Rows of q_out and k_out that belong to no sequence are left as they are.
  * dim 64 or 128; page_size 16, 32, 64 or 128 (KDA_ERR_UNSUPPORTED otherwise).
- * No page may be written for two sequences in one call.
+ * No page may be written for two sequences in one call (pages that are only read, full ones of
+ * a shared beginning, may stand in several rows of block_table).
  */
 kda_status kda_kv_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride, int64_t tokens,
                          int kv_heads, int dim, void *k_cache, void *v_cache, float *k_scale, float *v_scale,

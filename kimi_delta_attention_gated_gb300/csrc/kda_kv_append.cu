@@ -62,11 +62,16 @@ __device__ __forceinline__ int position_of(const AppendParams &p, int64_t t) {
     return max(p.c.lens[lo], 0) + (int)(t - p.cu_seqlens[lo]);
 }
 
-// One query tile.
+// One query tile; rows of no sequence are left out.
 template <int THREADS>
 __device__ __forceinline__ void rotate_queries(const AppendParams &p, int tile, int q_tile, float2 *cs, int *pos) {
-    const int64_t t0 = (int64_t)tile * q_tile;
-    const int n = (int)min((int64_t)q_tile, p.tokens - t0), tid = threadIdx.x;
+    int64_t t0 = (int64_t)tile * q_tile, t1 = min(t0 + q_tile, p.tokens);
+    if (p.cu_seqlens) {
+        t0 = max(t0, (int64_t)p.cu_seqlens[0]);
+        t1 = min(t1, (int64_t)p.cu_seqlens[p.c.N]);
+        if (t0 >= t1) return;
+    }
+    const int n = (int)(t1 - t0), tid = threadIdx.x;
     for (int t = tid; t < n; t += THREADS) pos[t] = position_of(p, t0 + t);
     __syncthreads();
     fill_cos_sin(cs, p.rot, n, [&](int t) { return pos[t]; }, tid, THREADS);

@@ -229,6 +229,53 @@ def test_strided_rows_and_bad_bounds():
             assert torch.equal(bits(a), bits(b)), i
 
 
+@pytest.mark.parametrize("T", [40, 9000])
+def test_rows_of_no_sequence_are_left_alone(T):
+    """cu_seqlens that begins behind row 0 and ends before the last row; 9000 rows of 64 heads take the
+    form with a launch of its own for the queries."""
+    Hk, Hq, D, P = 1, 64, 64, 16
+    g = gen(6)
+    k = torch.randn((T, Hk, D), generator=g, device="cuda").bfloat16()
+    q = torch.randn((T, Hq, D), generator=g, device="cuda").bfloat16()
+    lo, hi = 5, T - 7
+    pages = -(-(hi - lo) // P)
+    cache = kda.kv_cache(pages, Hk, D, P)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    f, _ = kda.rotary_inv_freq(D)
+    qo, ko = torch.full_like(q, 9.0), torch.full_like(k, 9.0)
+    kda.kv_append(k, k, cache, table, zero, cu_seqlens=torch.tensor([lo, hi], dtype=torch.int32, device="cuda"),
+                  inv_freq=f, q=q, q_out=qo, k_out=ko)
+    for out, x in ((qo, q), (ko, k)):
+        assert (out[:lo] == 9).all() and (out[hi:] == 9).all()
+        want = kda.rotary(x[lo:hi], torch.arange(hi - lo, dtype=torch.int32, device="cuda"), f)
+        assert torch.equal(out[lo:hi], want)
+
+
+def test_graph_replays_append_where_the_lengths_say():
+    """A captured step: each replay appends one token further on, as the lengths are counted up."""
+    N, Hk, D, P = 3, 2, 64, 16
+    table, pages = table_for([40] * N, P, 7)
+    f, _ = kda.rotary_inv_freq(D)
+    caches = [kda.kv_cache(pages, Hk, D, P) for _ in range(2)]
+    ctx = torch.tensor([0, 15, 20], dtype=torch.int32, device="cuda")
+    x = torch.randn((N, Hk, D), generator=gen(8), device="cuda").bfloat16()
+    dt = table.cuda()
+    kda.kv_append(x, x, kda.kv_cache(pages, Hk, D, P), dt, ctx, inv_freq=f)  # loaded before the capture
+    torch.cuda.synchronize()
+    graph, c = torch.cuda.CUDAGraph(), ctx.clone()
+    with torch.cuda.graph(graph):
+        kda.kv_append(x, x, caches[0], dt, c, inv_freq=f)
+    for _ in range(5):
+        graph.replay()
+        kda.kv_append(x, x, caches[1], dt, ctx, inv_freq=f)
+        c += 1
+        ctx += 1
+    torch.cuda.synchronize()
+    for a, b in zip(*caches):
+        assert torch.equal(bits(a), bits(b))
+
+
 def test_refusals():
     cache = kda.kv_cache(2, 2, 64, 16)
     x = torch.zeros((3, 2, 64), device="cuda").bfloat16()
