@@ -217,6 +217,37 @@ def test_append_then_attend():
             ref.check(f"o[{n}, {h}]", o[n, hs], want, tol)
 
 
+def test_sequences_that_share_pages():
+    """Two sequences with the same beginning: the pages stand in both rows of the table."""
+    o, lse, q, cache, table, sl = case([100, 70], 2, 4, 64, 16, seed=18)
+    table[1, :4] = table[0, :4]
+    o2, l2 = kda.attn_decode(q, cache, table.cuda(), sl, return_lse=True)
+    verify(o2, l2, q, cache, table, [100, 70])
+
+
+def test_two_calls_at_once():
+    """Two streams at the same time, each with a workspace from torch's allocator."""
+    a, b = case([3000, 17], 2, 4, 128, 16, seed=19), case([900, 900, 5], 2, 4, 128, 16, seed=20)
+    tables = [x[4].cuda() for x in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(10):
+        for i, (x, st) in enumerate(zip((a, b), streams)):
+            with torch.cuda.stream(st):
+                outs[i].append(kda.attn_decode(x[2], x[3], tables[i], x[5]))
+    torch.cuda.synchronize()
+    for x, got in zip((a, b), outs):
+        assert all(torch.equal(y, x[0]) for y in got)
+
+
+@pytest.mark.parametrize("Hk,G", [(1, 1), (1, 12), (4, 4)])
+def test_one_long_sequence(Hk, G):
+    """One sequence cut into as many pieces as the GPU takes; sampled against 64 bits."""
+    case([30000], Hk, G, 128, 128, seed=21)
+    case([30000], Hk, G, 64, 16, seed=22)
+
+
 def test_refusals():
     cache = kda.kv_cache(4, 2, 64, 16)
     q = torch.zeros((2, 4, 64), device="cuda").bfloat16()

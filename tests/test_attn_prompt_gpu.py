@@ -194,6 +194,36 @@ def test_same_bits_again_on_another_stream_and_from_a_graph():
     assert torch.equal(out, o)
 
 
+def test_two_calls_at_once():
+    """Two streams at the same time, and the KDA prefill beside them."""
+    from kimi_delta_attention_gated_gb300.inputs import make_inputs
+    x, y = make(900, 900, 4, 2, 64, 64, 14), make(1500, 1500, 2, 2, 192, 128, 15)
+    want = [kda.attn_prompt(*x), kda.attn_prompt(*y)]
+    d = make_inputs("prefill", device="cuda", T=200, H=2)
+    kd = lambda: kda.chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["beta"], scale=d["scale"])[0]
+    want.append(kd())
+    calls = [lambda: kda.attn_prompt(*x), lambda: kda.attn_prompt(*y), kd]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    outs = [[] for _ in calls]
+    for _ in range(8):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                outs[i].append(calls[i]())
+    torch.cuda.synchronize()
+    kda.device_status()
+    for w, got in zip(want, outs):
+        assert all(torch.equal(g, w) for g in got)
+
+
+def test_equal_lengths_without_cu_seqlens_and_more_keys():
+    """Dense batches: q [B, T, ..] with k, v [B, S, ..], S more and less than T."""
+    for B, T, S in ((3, 130, 300), (2, 200, 50), (40, 3, 3)):
+        q, k, v = make(B * T, B * S, 2, 1, 128, 128, B)
+        o, lse = kda.attn_prompt(q.unflatten(0, (B, T)), k.unflatten(0, (B, S)), v.unflatten(0, (B, S)), return_lse=True)
+        verify(o.flatten(0, 1), lse.flatten(0, 1), q, k, v, [T] * B, [S] * B)
+
+
 def test_the_prompt_and_the_decode_agree():
     """The last row of a prompt against one decode step over the appended cache: the same attention but
     for the cache's 8 bits."""
