@@ -64,7 +64,7 @@ struct Cfg {
     static constexpr int KST = D == 64 ? 4 : 2, VST = D == 64 ? 4 : 2;
     static constexpr uint32_t Q = 0, K = 2 * QB, V = K + KST * KB, BARS = V + VST * VB;
     static constexpr int NBAR = 4 + 2 * KST + 2 * VST + 1 + 2 + 4 + 2 + 2 + 4;
-    static constexpr uint32_t SMEM = BARS + NBAR * 8 + 64 + 1024;
+    static constexpr uint32_t SMEM = BARS + NBAR * 8 + 96 + 1024;
     static_assert(SMEM <= 232448, "shared memory budget");
     static constexpr uint32_t T_S = 0, T_O = 256;  // TMEM columns of tile 0; tile 1's follow 128 later
 };
@@ -76,8 +76,13 @@ struct Args {
     int items;       // work items at most
 };
 
+// Query and key rows of a sequence.
+struct Seq {
+    int q0, nq, k0, nk;
+};
 struct Item {
-    int found, seq, row0, head;  // head: number of the pair, or of the head
+    Seq s;
+    int found, row0, head;  // head: number of the pair, or of the head
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *r) {
@@ -217,10 +222,7 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Query and key rows of sequence n, clamped to the tensors.
-struct Seq {
-    int q0, nq, k0, nk;
-};
+// Sequence n, clamped to the tensors.
 __device__ __forceinline__ Seq seq_of(const PromptParams &p, int n) {
     auto range = [&p](const int32_t *cu, int n, int64_t T, int &at, int &len) {
         if (!cu) {  // equal lengths
@@ -240,78 +242,94 @@ __device__ __forceinline__ Seq seq_of(const PromptParams &p, int n) {
     return s;
 }
 
-// Units (runs of `rows` query rows of one sequence), longest first.  A unit's key is the
-// number of keys its last row sees (not clamped at 0: it grows strictly within a sequence).
-// x: the sequence's queries and how many more keys it has.  Its units with a key of at least
-// `key`:
-__device__ __forceinline__ int units_from(int2 x, int shift, int key) {
-    const int rows = 1 << shift, all = (x.x + rows - 1) >> shift, y = key - x.y;  // the last row's number has to reach y
-    if (y <= 0) return all;
-    if (y > x.x) return 0;
-    return all - (((y + rows - 1) >> shift) - 1);
-}
+// Work units, runs of 2^shift query rows of one sequence, longest first: one warp's search, asked
+// for ever higher ranks.  A unit's level is the number of keys its first row sees, above the
+// smallest of any first unit and in units of 2^shift, so that a sequence has units on as many levels
+// as it has units, one each.  The warp holds 128 sequences, and takes the next 128 when those
+// are through (the order then holds within them).
+struct UnitSearch {
+    int next = 0;               // first sequence not taken yet
+    int before = 0, total = 0;  // units of the sequences before those held, and of those
+    int top = 0;                // no unit asked for from now on lies above this level
+    int all[4], base[4];        // a lane's sequences: their units, and the first one's level
 
-// The rank-th unit of 2^shift rows: its sequence and its first row; false if there are fewer.
-// One warp; up to 32 sequences are held by its lanes.
-__device__ bool find_unit(const PromptParams &p, int shift, int rank, int &seq, int &row0) {
-    const int lane = threadIdx.x & 31, rows = 1 << shift;
-    if (!p.cu_q) {  // equal lengths: round by round
-        const int nq = (int)(p.Tq / p.N), all = (nq + rows - 1) >> shift, u = all - 1 - rank / p.N;
-        seq = rank % p.N;
-        row0 = u * rows;
-        return u >= 0;
-    }
-    if (p.N == 1) {
-        row0 = (((seq_of(p, 0).nq + rows - 1) >> shift) - 1 - rank) * rows;
-        return row0 >= 0;
-    }
-    auto load = [&](int n) {
-        const Seq s = seq_of(p, n);
-        return make_int2(s.nq, s.nk - s.nq);
-    };
-    const int2 held = lane < p.N ? load(lane) : make_int2(0, 0);
-    int lo = INT_MAX, hi = INT_MIN;  // keys lie in (lo, hi]
-    for (int n = lane; n < p.N; n += 32) {
-        const Seq s = seq_of(p, n);
-        if (s.nq == 0) continue;
-        lo = min(lo, s.nk - s.nq);
-        hi = max(hi, s.nk);
-    }
-    auto count = [&](int key) {
-        int c = units_from(held, shift, key);
-        for (int n = lane + 32; n < p.N; n += 32) c += units_from(load(n), shift, key);
+    __device__ int above(int level) const {  // held units at or above a level
+        int c = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c += all[e] - min(max(level - base[e], 0), all[e]);
         return __reduce_add_sync(0xffffffffu, c);
-    };
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lo > hi || rank >= count(lo)) return false;
-    while (lo < hi) {  // the largest key with more than `rank` units from it on
-        const int m = (int)(((int64_t)lo + hi + 1) >> 1);
-        if (count(m) > rank)
-            lo = m;
-        else
-            hi = m - 1;
     }
-    int left = rank - count(lo + 1);  // among the sequences with a unit of key lo, in order
-    for (int n0 = 0; n0 < p.N; n0 += 32) {
-        const int n = n0 + lane;
-        int u = -1;
-        if (n < p.N) {
-            const int2 x = n0 ? load(n) : held;
-            const int a = units_from(x, shift, lo);
-            if (a > units_from(x, shift, lo + 1)) u = ((x.x + rows - 1) >> shift) - a;
+    __device__ void take(const PromptParams &p, int shift) {
+        const int lane = threadIdx.x & 31;
+        int more[4], least = INT_MAX, units = 0, levels = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int n = next + e * 32 + lane;
+            all[e] = more[e] = 0;
+            if (n >= p.N) continue;
+            const Seq s = seq_of(p, n);
+            all[e] = (int)(((int64_t)s.nq + (1 << shift) - 1) >> shift);
+            more[e] = s.nk - s.nq;
+            if (all[e]) least = min(least, more[e]);
         }
-        const uint32_t has = __ballot_sync(0xffffffffu, u >= 0);
-        if (left < __popc(has)) {
-            const int src = __fns(has, 0, left + 1);
-            seq = n0 + src;
-            row0 = __shfl_sync(0xffffffffu, u, src) * rows;
-            return true;
+        least = __reduce_min_sync(0xffffffffu, least);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            base[e] = all[e] ? (int)(((uint32_t)more[e] - (uint32_t)least) >> shift) : 0;
+            units += all[e];
+            levels = max(levels, base[e] + all[e]);
         }
-        left -= __popc(has);
+        before += total;
+        total = __reduce_add_sync(0xffffffffu, units);
+        top = __reduce_max_sync(0xffffffffu, levels) - 1;
+        next += 128;
     }
-    return false;
-}
+    // The rank-th unit: its sequence and first row; false if there are fewer.
+    __device__ bool find(const PromptParams &p, int shift, int rank, int &seq, int &row0) {
+        if (!p.cu_q) {  // equal lengths: round by round
+            const int nq = (int)(p.Tq / p.N), u = ((nq + (1 << shift) - 1) >> shift) - 1 - rank / p.N;
+            seq = rank % p.N;
+            row0 = u << shift;
+            return u >= 0;
+        }
+        if (p.N == 1) {
+            if (!next) all[0] = (seq_of(p, 0).nq + (1 << shift) - 1) >> shift, next = 1;
+            seq = 0;
+            row0 = (all[0] - 1 - rank) << shift;
+            return row0 >= 0;
+        }
+        while (rank >= before + total) {
+            if (next >= p.N) return false;
+            take(p, shift);
+        }
+        rank -= before;
+        int lo = 0;  // the highest level with more than `rank` units from it on
+        while (lo < top) {
+            const int m = (lo + top + 1) >> 1;
+            if (above(m) > rank)
+                lo = m;
+            else
+                top = m - 1;
+        }
+        int left = rank - above(lo + 1);  // in the order of the sequences
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int u = lo - base[e];
+            const bool has = u >= 0 && u < all[e];
+            const uint32_t who = __ballot_sync(0xffffffffu, has);
+            const uint32_t it = __ballot_sync(0xffffffffu, has && __popc(who & ((1u << lane) - 1)) == left);
+            if (it) {
+                const int src = __ffs(it) - 1;
+                seq = next - 128 + e * 32 + src;
+                row0 = __shfl_sync(0xffffffffu, u, src) << shift;
+                return true;
+            }
+            left -= __popc(who);
+        }
+        return false;
+    }
+};
 
 // Weights 2^(c y - m) of 32 scores y, left as bf16 pairs in the words y[0, 16); their sum is
 // added to s (two pairs of halves).
@@ -423,18 +441,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         return false;
     };
     // This CTA's k-th work item; one warp.
-    auto find_item = [&](int k) {
+    auto find_item = [&](UnitSearch &units, int k) {
         const int64_t i = (int64_t)k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        Item it = {0, 0, 0, (int)(i % a.n_heads)};
-        if (i < a.items) it.found = find_unit(p, a.pair_heads ? 7 : 8, (int)(i / a.n_heads), it.seq, it.row0);
+        Item it = {{0, 0, 0, 0}, 0, 0, (int)i % a.n_heads};
+        int seq = 0;
+        if (i < a.items) it.found = units.find(p, a.pair_heads ? 7 : 8, (int)i / a.n_heads, seq, it.row0);
+        if (it.found) it.s = seq_of(p, seq);
         return it;
     };
     // The same from the item warp, for a warp that follows them all; false when a wait gave up.
-    auto take_item = [&](int k, Item &it) {
-        if (!__all_sync(0xffffffffu, wait(i_full + (k & 1), (k >> 1) & 1))) return false;
-        it = slots[k & 1];
+    auto see_item = [&](int k) { return __all_sync(0xffffffffu, wait(i_full + (k & 1), (k >> 1) & 1)) != 0; };
+    auto leave_item = [&](int k) {
         __syncwarp();
         if (lane == 0) mbar_arrive(i_empty + (k & 1));
+    };
+    auto take_item = [&](int k, Item &it) {
+        if (!see_item(k)) return false;
+        it = slots[k & 1];
+        leave_item(k);
         return true;
     };
     auto tile_row = [&](const Item &it, int t) { return a.pair_heads ? it.row0 : it.row0 + t * kTile; };
@@ -442,18 +466,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto tile_blocks = [&](const Item &it, const Seq &s, int t) {
         const int r = tile_row(it, t), last = min(r + kTile, s.nq) - 1;
         if (r >= s.nq) return 0;
-        const int seen = max(0, min(s.nk, last + 1 + s.nk - s.nq));
+        const int seen = max(0, min(s.nk, last + 1 + (s.nk - s.nq)));
         return (seen + kTile - 1) / kTile;
     };
 
     if (warp == kItemWarp) {
         // ---- work items, two ahead
+        UnitSearch units;
         for (int k = 0;; ++k) {
             if (k >= 2 && !wait(i_empty + (k & 1), ((k >> 1) - 1) & 1)) {
                 failed = 1;
                 break;
             }
-            const Item it = find_item(k);
+            const Item it = find_item(units, k);
             if (lane == 0) {
                 slots[k & 1] = it;
                 mbar_arrive(i_full + (k & 1));
@@ -471,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Item it;
             ok = take_item(k, it);
             if (!ok || !it.found) break;
-            const Seq s = seq_of(p, it.seq);
+            const Seq s = it.s;
             const int head0 = a.pair_heads ? 2 * it.head : it.head, kvh = head0 / group;
             const int n0 = tile_blocks(it, s, 0), n1 = tile_blocks(it, s, 1), nb = max(n0, n1);
             auto load_q = [&](int t) {
@@ -581,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             if (!it.found) break;
-            const Seq s = seq_of(p, it.seq);
+            const Seq s = it.s;
             const int n0 = tile_blocks(it, s, 0), n1 = tile_blocks(it, s, 1), nb = max(n0, n1), nt = t ? n1 : n0;
             auto next_keys = [&] {
                 if (++ks == L::KST) ks = 0, kp ^= 1;
@@ -656,17 +681,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t t_s = tb + lane_base + L::T_S + t * 128, t_o = tb + lane_base + L::T_O + t * 128;
         const float c = fabsf(p.scale) * kLog2e;
         uint32_t blocks = 0, tiles = 0;  // of this tile so far: key blocks, and items with any
-        bool ok = true;
+        bool ok = see_item(0);
         int k = 0;
-        for (; ok; ++k) {
-            Item it;
-            ok = take_item(k, it);
-            if (!ok || !it.found) break;
-            const Seq s = seq_of(p, it.seq);
-            const int nt = tile_blocks(it, s, t), row0 = tile_row(it, t), row = row0 + m_row;
-            const int head = a.pair_heads ? 2 * it.head + t : it.head;
-            const int seen = max(0, min(s.nk, row + 1 + s.nk - s.nq));
-            const int seen_first = max(0, min(s.nk, row0 + 1 + s.nk - s.nq));  // of the tile's first row
+        for (; ok && slots[k & 1].found; ++k) {
+            int nt, seen, seen_first;  // what the loop over the keys needs of the item; the rest is read again behind it
+            {
+                const Item it = slots[k & 1];
+                const int row0 = tile_row(it, t), row = row0 + m_row, more = it.s.nk - it.s.nq;
+                nt = tile_blocks(it, it.s, t);
+                seen = max(0, min(it.s.nk, row + 1 + more));
+                seen_first = max(0, min(it.s.nk, row0 + 1 + more));  // of the tile's first row
+            }
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < nt; ++j, ++blocks) {
                 ok = wait(s_full + t, blocks & 1);
@@ -727,75 +752,87 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
             }
-            if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait(o_full + t, tiles & 1));
-            tiles += nt > 0;
-            fence_after_sync();
-            if (row0 >= s.nq) continue;  // the item has no such tile
+            // What does not need O comes before the wait for it: the next item, the row's factor and places.
+            const Item it = slots[k & 1];
+            const Seq s = it.s;
+            const int row0 = tile_row(it, t), row = row0 + m_row, head = a.pair_heads ? 2 * it.head + t : it.head;
+            leave_item(k);
+            const bool more = !ok || see_item(k + 1);
             const bool live = row < s.nq;
             const int64_t out = (int64_t)(s.q0 + row) * p.Hq + head;
-            const float inv = !ok ? __int_as_float(0x7fc00000) : l == 0.f ? 0.f : 1.f / l;
+            float inv = l == 0.f ? 0.f : 1.f / l, lse = l == 0.f ? -INFINITY : (log2f(l) + m) * kLn2;
             // Four lanes exchange 16-byte pieces of their rows, so that they write 64 bytes of a row
             // together (lanes writing a row each touch 32 lines per store).
             const int first = row0 + (warp & 3) * 32 + (lane & ~3);  // of the four rows
             const int esz = p.o_bf16 ? 2 : 4;
             uint8_t *o_rows = static_cast<uint8_t *>(p.o) + ((int64_t)(s.q0 + first) * p.Hq + head) * DV * esz + (lane & 3) * 16;
             const int64_t pitch = (int64_t)p.Hq * DV * esz;
-            float odd = 0.f;  // 0, or NaN where an output is not finite
+            if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait(o_full + t, tiles & 1));
+            tiles += nt > 0;
+            fence_after_sync();
+            if (!ok) inv = lse = __int_as_float(0x7fc00000);
+            if (row0 < s.nq) {  // (else the item has no such tile)
+                const float2 inv2 = make_float2(inv, inv), zero = make_float2(0.f, 0.f);
+                float2 odd[4] = {zero, zero, zero, zero};  // 0, or NaN where an output is not finite
 #pragma unroll 1
-            for (int d = 0; d < DV; d += 32) {
-                float r[32];
-                if (ok && nt > 0) {
-                    tmem_ld32(t_o + d, r);
-                    tmem_wait_ld();
+                for (int d = 0; d < DV; d += 64) {
+                    float r[64];
+                    if (ok && nt > 0) {
+                        tmem_ld32(t_o + d, r);
+                        tmem_ld32(t_o + d + 32, r + 32);
+                        wait_ld64(r);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 16)
-                        asm volatile("" : "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]),
-                                     "+f"(r[i + 5]), "+f"(r[i + 6]), "+f"(r[i + 7]), "+f"(r[i + 8]), "+f"(r[i + 9]),
-                                     "+f"(r[i + 10]), "+f"(r[i + 11]), "+f"(r[i + 12]), "+f"(r[i + 13]), "+f"(r[i + 14]),
-                                     "+f"(r[i + 15]));
-                } else {
+                        for (int i = 0; i < 64; ++i) r[i] = 0.f;
+                    }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = 0.f;
-                }
+                    for (int i = 0; i < 32; ++i) {
+                        const float2 x = fma2(make_float2(r[2 * i], r[2 * i + 1]), inv2, zero);
+                        odd[i & 3] = fma2(x, zero, odd[i & 3]);
+                        r[2 * i] = x.x;
+                        r[2 * i + 1] = x.y;
+                    }
+                    auto store = [&](uint32_t (&w)[16], int byte) {
+                        transpose_quad(w);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    r[i] *= inv;
-                    odd = fmaf(r[i], 0.f, odd);
-                }
-                auto store = [&](uint32_t (&w)[16], int byte) {
-                    transpose_quad(w);
+                        for (int i = 0; i < 4; ++i)
+                            if (first + i < s.nq)
+                                __stcs(reinterpret_cast<uint4 *>(o_rows + i * pitch + byte),
+                                       make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+                    };
+                    uint32_t w[16];
+                    if (p.o_bf16) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (first + i < s.nq)
-                            __stcs(reinterpret_cast<uint4 *>(o_rows + i * pitch + byte),
-                                   make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
-                };
-                uint32_t w[16];
-                if (p.o_bf16) {
+                        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(r[2 * i], r[2 * i + 1]);
-                    store(w, d * 2);
-                } else {
+                            for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(r[32 * h + 2 * i], r[32 * h + 2 * i + 1]);
+                            store(w, (d + 32 * h) * 2);
+                        }
+                    } else {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                        for (int h = 0; h < 4; ++h) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(r[16 * h + i]);
-                        store(w, (d + 16 * h) * 4);
+                            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(r[16 * h + i]);
+                            store(w, (d + 16 * h) * 4);
+                        }
                     }
                 }
+                __syncwarp();
+                if (live) {
+                    if (p.lse) p.lse[out] = lse;
+                    const float2 any = add2(add2(odd[0], odd[1]), add2(odd[2], odd[3]));
+                    if (isnan(any.x + any.y) && ok) rescue_row<D, DV>(p, s, row, head, seen, nt, m, l, copysignf(c, p.scale));
+                }
             }
-            __syncwarp();
-            if (live) {
-                if (p.lse) p.lse[out] = !ok ? __int_as_float(0x7fc00000) : l == 0.f ? -INFINITY : (log2f(l) + m) * kLn2;
-                if (isnan(odd) && ok) rescue_row<D, DV>(p, s, row, head, seen, nt, m, l, copysignf(c, p.scale));
-            }
+            ok = ok && more;
         }
         if (!ok) {  // what this CTA still had to do: NaN
             failed = 1;
+            UnitSearch units;
             for (;; ++k) {
-                const Item it = find_item(k);
+                const Item it = find_item(units, k);
                 if (!it.found) break;
-                const Seq s = seq_of(p, it.seq);
+                const Seq s = it.s;
                 const int row = tile_row(it, t) + m_row, head = a.pair_heads ? 2 * it.head + t : it.head;
                 if (row >= s.nq) continue;
                 const int64_t out = (int64_t)(s.q0 + row) * p.Hq + head;
