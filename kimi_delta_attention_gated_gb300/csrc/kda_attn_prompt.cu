@@ -48,6 +48,9 @@ using namespace tc;
 constexpr int kTile = 128;             // query rows of a tile, and keys of a block
 constexpr int kMmaWarp = 8, kTmaWarp = 10, kItemWarp = 11;
 constexpr int kThreads = 384;
+constexpr int kFewRegs = 104, kManyRegs = 200;  // a thread's registers in warps 8-11 and 0-7
+constexpr int kLaunchRegs = 168;                // and at launch, which must cover them
+static_assert(kFewRegs * 128 + kManyRegs * 256 <= kLaunchRegs * kThreads, "a larger share would be waited for without end");
 constexpr int kItemReaders = 11;       // warps that follow the work items
 constexpr uint32_t kPolls = 1u << 21;  // a few seconds; a CTA waits for nothing but its own warps and loads
 constexpr float kSlack = 40.f;         // log2: how far a score may exceed the reference
@@ -470,211 +473,217 @@ __global__ void __launch_bounds__(kThreads, 1)
         return (seen + kTile - 1) / kTile;
     };
 
-    if (warp == kItemWarp) {
-        // ---- work items, two ahead
-        UnitSearch units;
-        for (int k = 0;; ++k) {
-            if (k >= 2 && !wait(i_empty + (k & 1), ((k >> 1) - 1) & 1)) {
-                failed = 1;
-                break;
+    // The softmax keeps 128 scores and what goes with them in registers: it takes some over from
+    // the other warps (with 168 each some were spilled).
+    if (warp >= kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        if (warp == kItemWarp) {
+            // ---- work items, two ahead
+            UnitSearch units;
+            for (int k = 0;; ++k) {
+                if (k >= 2 && !wait(i_empty + (k & 1), ((k >> 1) - 1) & 1)) {
+                    failed = 1;
+                    break;
+                }
+                const Item it = find_item(units, k);
+                if (lane == 0) {
+                    slots[k & 1] = it;
+                    mbar_arrive(i_full + (k & 1));
+                }
+                __syncwarp();
+                if (!it.found) break;
             }
-            const Item it = find_item(units, k);
-            if (lane == 0) {
-                slots[k & 1] = it;
-                mbar_arrive(i_full + (k & 1));
+        } else if (warp == kTmaWarp) {
+            // ---- loads
+            const uint64_t once = leave_first(), again = leave_last();
+            uint32_t raw = 0;
+            int nq_issued[2] = {0, 0}, nk_issued = 0, nv_issued = 0;
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                Item it;
+                ok = take_item(k, it);
+                if (!ok || !it.found) break;
+                const Seq s = it.s;
+                const int head0 = a.pair_heads ? 2 * it.head : it.head, kvh = head0 / group;
+                const int n0 = tile_blocks(it, s, 0), n1 = tile_blocks(it, s, 1), nb = max(n0, n1);
+                auto load_q = [&](int t) {
+                    if (nq_issued[t] > 0 && !wait(q_empty + t, (nq_issued[t] - 1) & 1)) return false;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(q_full + t, L::QB);
+                        for (int x = 0; x < D; x += 64)
+                            tma_load_hint(sb + L::Q + t * L::QB + (x / 64) * kTile * 128, &map_q, q_full + t, x,
+                                          a.pair_heads ? head0 + t : head0, s.q0 + tile_row(it, t), once);
+                    }
+                    ++nq_issued[t];
+                    return true;
+                };
+                auto load_k = [&](int j) {
+                    const int i = nk_issued, st = i % L::KST;
+                    if (i >= L::KST && !wait(k_empty + st, (i / L::KST - 1) & 1)) return false;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(k_full + st, L::KB);
+                        for (int x = 0; x < D; x += 64)
+                            tma_load_hint(sb + L::K + st * L::KB + (x / 64) * kTile * 128, &map_k, k_full + st, x, kvh,
+                                          s.k0 + j * kTile, again);
+                    }
+                    ++nk_issued;
+                    return true;
+                };
+                auto load_v = [&](int j, int h) {
+                    const int i = nv_issued, st = i % L::VST;
+                    if (i >= L::VST && !wait(v_empty + st, (i / L::VST - 1) & 1)) return false;
+                    const int rows = max(0, s.nk - j * kTile - h * L::VROWS);  // of the sequence
+                    uint64_t *bar = rows < L::VROWS ? v_raw : v_full + st;
+                    const uint32_t base = L::V + st * L::VB;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar, L::VB);
+                        for (int x = 0; x < DV; x += 64)
+                            tma_load_hint(sb + base + (x / 64) * L::VROWS * 128, &map_v, bar, x, kvh,
+                                          s.k0 + j * kTile + h * L::VROWS, again);
+                    }
+                    if (rows < L::VROWS) {
+                        const bool landed = wait(v_raw, raw & 1);
+                        if (!landed) mbar_wait(v_raw, raw & 1, kPolls);  // the copy must still land before the CTA may end
+                        ++raw;
+                        if (!landed) return false;
+                        for (int i = lane; i < (L::VROWS - rows) * (DV / 64) * 8; i += 32) {
+                            const int r = rows + i / ((DV / 64) * 8), q = i % ((DV / 64) * 8);
+                            st_shared_v4(sb + base + (q >> 3) * L::VROWS * 128 + r * 128 + (q & 7) * 16, 0, 0, 0, 0);
+                        }
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(v_full + st);
+                    }
+                    ++nv_issued;
+                    return true;
+                };
+                if (n0) ok = load_q(0);
+                if (ok && nb) ok = load_k(0);
+                if (ok && n1) ok = load_q(1);
+                for (int j = 0; j < nb && ok; ++j) {
+                    if (j + 1 < nb) ok = load_k(j + 1);
+                    for (int h = 0; h < L::NV && ok; ++h) ok = load_v(j, h);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            if (!ok) failed = 1;
+            // every load lands before the CTA may end
+            for (int t = 0; t < 2; ++t)
+                if (nq_issued[t]) mbar_wait(q_full + t, (nq_issued[t] - 1) & 1, kPolls);
+            for (int j = max(0, nk_issued - L::KST); j < nk_issued; ++j)
+                mbar_wait(k_full + j % L::KST, (j / L::KST) & 1, kPolls);
+            for (int j = max(0, nv_issued - L::VST); j < nv_issued; ++j)
+                mbar_wait(v_full + j % L::VST, (j / L::VST) & 1, kPolls);
+        } else {
+            // ---- products of tile t.  One thread's instructions come one at a time, about five
+            // cycles each, so the descriptors are bases plus constants.
+            const int t = warp - kMmaWarp;
+            const uint32_t id_s = idesc_bf16(kTile, kTile, false, false, p.scale < 0.f);
+            const uint32_t id_o = idesc_bf16(kTile, DV, false, true);
+            const uint32_t lo_kmajor = sb16 | (16u >> 4) << 16, lo_v = sb16 | (L::VROWS * 128u >> 4) << 16;
+            const uint32_t q_lo = lo_kmajor + ((L::Q + t * L::QB) >> 4), t_s = tb + L::T_S + t * 128, t_o = tb + L::T_O + t * 128;
+            int ks = 0, vs = 0;       // ring places of the next keys and values
+            uint32_t kp = 0, vp = 0;  // and the parities of their rounds
+            uint32_t blocks = 0, tiles = 0;  // of this tile so far: key blocks, and items with any
+            bool begun = false, ok = true;
+            auto scores = [&] {
+                const uint32_t k_lo = lo_kmajor + (L::K >> 4) + ks * (L::KB >> 4);
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    const uint32_t off = ((x / 4) * kTile * 128 + (x % 4) * 32) >> 4;
+                    mma_ss(t_s, desc_of(q_lo + off), desc_of(k_lo + off), id_s, x > 0);
+                }
+                mma_commit(s_full + t);
+                mma_commit(k_empty + ks);
+            };
+            // A half's product with its values, the last of both of a slot letting go of it.
+            auto weigh = [&](int h, int slot, bool more) {
+                const uint32_t v_lo = lo_v + (L::V >> 4) + slot * (L::VB >> 4) + (L::NV == 1 ? h * 4 * (2048 >> 4) : 0);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    mma_ts(t_o, t_s + (4 * h + x) * 8, desc_of(v_lo + x * (2048 >> 4)), id_o, x > 0 ? 1u : more);
+                if (L::NV == 2 || h == 1) mma_commit(v_empty + slot);
+            };
+            for (int k = 0;; ++k) {
+                Item it;
+                // both product warps go on or stop together: each waits for the other's turns
+                const bool taken = take_item(k, it);
+                if (pair_any(3, !ok || !taken)) {
+                    failed = 1;
+                    break;
+                }
+                if (!it.found) break;
+                const Seq s = it.s;
+                const int n0 = tile_blocks(it, s, 0), n1 = tile_blocks(it, s, 1), nb = max(n0, n1), nt = t ? n1 : n0;
+                auto next_keys = [&] {
+                    if (++ks == L::KST) ks = 0, kp ^= 1;
+                };
+                if (nt) ok = wait(q_full + t, tiles & 1);
+                if (nb) {
+                    ok = ok && wait(k_full + ks, kp);
+                    fence_after_sync();
+                    if (ok && elect_one()) {
+                        if (nt) {
+                            scores();
+                            if (nt == 1) mma_commit(q_empty + t);
+                        } else {
+                            mbar_arrive(k_empty + ks);  // every block is let go of by both tiles
+                        }
+                    }
+                    next_keys();
+                }
+                for (int j = 0; j < nb; ++j) {
+                    const bool mine = j < nt, next = j + 1 < nt, more = j + 1 < nb;  // (an idle tile follows the rings too)
+                    ok = ok && wait(v_full + vs, vp);
+                    if (more) ok = ok && wait(k_full + ks, kp);
+                    if (mine) ok = ok && wait(p_ready + 2 * t, (blocks + j) & 1);
+                    fence_after_sync();
+                    if (t || begun) turn_wait(1 + t);
+                    begun = true;
+                    if (mine && ok && elect_one()) weigh(0, vs, j > 0);
+                    __syncwarp();
+                    const int vs0 = vs;
+                    if (L::NV == 2) {
+                        if (!mine && ok && lane == 0) mbar_arrive(v_empty + vs0);
+                        if (++vs == L::VST) vs = 0, vp ^= 1;
+                        ok = ok && wait(v_full + vs, vp);
+                    }
+                    if (mine) ok = ok && wait(p_ready + 2 * t + 1, (blocks + j) & 1);
+                    fence_after_sync();
+                    if (ok && elect_one()) {
+                        if (mine) {
+                            weigh(1, vs, true);
+                            // the next scores overwrite this block's weights: behind the product in the same queue
+                            if (next) {
+                                scores();
+                                if (j + 2 == nt) mma_commit(q_empty + t);
+                            } else {
+                                mma_commit(o_full + t);
+                            }
+                        } else {
+                            mbar_arrive(v_empty + vs);
+                        }
+                        if (!next && more) mbar_arrive(k_empty + ks);
+                    }
+                    __syncwarp();
+                    turn_pass(2 - t);
+                    if (more) next_keys();
+                    if (++vs == L::VST) vs = 0, vp ^= 1;
+                }
+                blocks += nt;
+                tiles += nt > 0;
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            if (!t && begun) turn_wait(1);  // the other warp's last turn was passed here
+            // nothing issued may still run, and no commit arrive, once the CTA has ended
+            if (elect_one()) {
+                mma_commit(drain + t);
+                mbar_wait(drain + t, 0, kPolls);
             }
             __syncwarp();
-            if (!it.found) break;
         }
-    } else if (warp == kTmaWarp) {
-        // ---- loads
-        const uint64_t once = leave_first(), again = leave_last();
-        uint32_t raw = 0;
-        int nq_issued[2] = {0, 0}, nk_issued = 0, nv_issued = 0;
-        bool ok = true;
-        for (int k = 0; ok; ++k) {
-            Item it;
-            ok = take_item(k, it);
-            if (!ok || !it.found) break;
-            const Seq s = it.s;
-            const int head0 = a.pair_heads ? 2 * it.head : it.head, kvh = head0 / group;
-            const int n0 = tile_blocks(it, s, 0), n1 = tile_blocks(it, s, 1), nb = max(n0, n1);
-            auto load_q = [&](int t) {
-                if (nq_issued[t] > 0 && !wait(q_empty + t, (nq_issued[t] - 1) & 1)) return false;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(q_full + t, L::QB);
-                    for (int x = 0; x < D; x += 64)
-                        tma_load_hint(sb + L::Q + t * L::QB + (x / 64) * kTile * 128, &map_q, q_full + t, x,
-                                      a.pair_heads ? head0 + t : head0, s.q0 + tile_row(it, t), once);
-                }
-                ++nq_issued[t];
-                return true;
-            };
-            auto load_k = [&](int j) {
-                const int i = nk_issued, st = i % L::KST;
-                if (i >= L::KST && !wait(k_empty + st, (i / L::KST - 1) & 1)) return false;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(k_full + st, L::KB);
-                    for (int x = 0; x < D; x += 64)
-                        tma_load_hint(sb + L::K + st * L::KB + (x / 64) * kTile * 128, &map_k, k_full + st, x, kvh,
-                                      s.k0 + j * kTile, again);
-                }
-                ++nk_issued;
-                return true;
-            };
-            auto load_v = [&](int j, int h) {
-                const int i = nv_issued, st = i % L::VST;
-                if (i >= L::VST && !wait(v_empty + st, (i / L::VST - 1) & 1)) return false;
-                const int rows = max(0, s.nk - j * kTile - h * L::VROWS);  // of the sequence
-                uint64_t *bar = rows < L::VROWS ? v_raw : v_full + st;
-                const uint32_t base = L::V + st * L::VB;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar, L::VB);
-                    for (int x = 0; x < DV; x += 64)
-                        tma_load_hint(sb + base + (x / 64) * L::VROWS * 128, &map_v, bar, x, kvh,
-                                      s.k0 + j * kTile + h * L::VROWS, again);
-                }
-                if (rows < L::VROWS) {
-                    const bool landed = wait(v_raw, raw & 1);
-                    if (!landed) mbar_wait(v_raw, raw & 1, kPolls);  // the copy must still land before the CTA may end
-                    ++raw;
-                    if (!landed) return false;
-                    for (int i = lane; i < (L::VROWS - rows) * (DV / 64) * 8; i += 32) {
-                        const int r = rows + i / ((DV / 64) * 8), q = i % ((DV / 64) * 8);
-                        st_shared_v4(sb + base + (q >> 3) * L::VROWS * 128 + r * 128 + (q & 7) * 16, 0, 0, 0, 0);
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(v_full + st);
-                }
-                ++nv_issued;
-                return true;
-            };
-            if (n0) ok = load_q(0);
-            if (ok && nb) ok = load_k(0);
-            if (ok && n1) ok = load_q(1);
-            for (int j = 0; j < nb && ok; ++j) {
-                if (j + 1 < nb) ok = load_k(j + 1);
-                for (int h = 0; h < L::NV && ok; ++h) ok = load_v(j, h);
-            }
-            ok = __all_sync(0xffffffffu, ok);
-        }
-        if (!ok) failed = 1;
-        // every load lands before the CTA may end
-        for (int t = 0; t < 2; ++t)
-            if (nq_issued[t]) mbar_wait(q_full + t, (nq_issued[t] - 1) & 1, kPolls);
-        for (int j = max(0, nk_issued - L::KST); j < nk_issued; ++j)
-            mbar_wait(k_full + j % L::KST, (j / L::KST) & 1, kPolls);
-        for (int j = max(0, nv_issued - L::VST); j < nv_issued; ++j)
-            mbar_wait(v_full + j % L::VST, (j / L::VST) & 1, kPolls);
-    } else if (warp >= kMmaWarp) {
-        // ---- products of tile t.  One thread's instructions come one at a time, about five
-        // cycles each, so the descriptors are bases plus constants.
-        const int t = warp - kMmaWarp;
-        const uint32_t id_s = idesc_bf16(kTile, kTile, false, false, p.scale < 0.f);
-        const uint32_t id_o = idesc_bf16(kTile, DV, false, true);
-        const uint32_t lo_kmajor = sb16 | (16u >> 4) << 16, lo_v = sb16 | (L::VROWS * 128u >> 4) << 16;
-        const uint32_t q_lo = lo_kmajor + ((L::Q + t * L::QB) >> 4), t_s = tb + L::T_S + t * 128, t_o = tb + L::T_O + t * 128;
-        int ks = 0, vs = 0;       // ring places of the next keys and values
-        uint32_t kp = 0, vp = 0;  // and the parities of their rounds
-        uint32_t blocks = 0, tiles = 0;  // of this tile so far: key blocks, and items with any
-        bool begun = false, ok = true;
-        auto scores = [&] {
-            const uint32_t k_lo = lo_kmajor + (L::K >> 4) + ks * (L::KB >> 4);
-#pragma unroll
-            for (int x = 0; x < D / 16; ++x) {
-                const uint32_t off = ((x / 4) * kTile * 128 + (x % 4) * 32) >> 4;
-                mma_ss(t_s, desc_of(q_lo + off), desc_of(k_lo + off), id_s, x > 0);
-            }
-            mma_commit(s_full + t);
-            mma_commit(k_empty + ks);
-        };
-        // A half's product with its values, the last of both of a slot letting go of it.
-        auto weigh = [&](int h, int slot, bool more) {
-            const uint32_t v_lo = lo_v + (L::V >> 4) + slot * (L::VB >> 4) + (L::NV == 1 ? h * 4 * (2048 >> 4) : 0);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                mma_ts(t_o, t_s + (4 * h + x) * 8, desc_of(v_lo + x * (2048 >> 4)), id_o, x > 0 ? 1u : more);
-            if (L::NV == 2 || h == 1) mma_commit(v_empty + slot);
-        };
-        for (int k = 0;; ++k) {
-            Item it;
-            // both product warps go on or stop together: each waits for the other's turns
-            const bool taken = take_item(k, it);
-            if (pair_any(3, !ok || !taken)) {
-                failed = 1;
-                break;
-            }
-            if (!it.found) break;
-            const Seq s = it.s;
-            const int n0 = tile_blocks(it, s, 0), n1 = tile_blocks(it, s, 1), nb = max(n0, n1), nt = t ? n1 : n0;
-            auto next_keys = [&] {
-                if (++ks == L::KST) ks = 0, kp ^= 1;
-            };
-            if (nt) ok = wait(q_full + t, tiles & 1);
-            if (nb) {
-                ok = ok && wait(k_full + ks, kp);
-                fence_after_sync();
-                if (ok && elect_one()) {
-                    if (nt) {
-                        scores();
-                        if (nt == 1) mma_commit(q_empty + t);
-                    } else {
-                        mbar_arrive(k_empty + ks);  // every block is let go of by both tiles
-                    }
-                }
-                next_keys();
-            }
-            for (int j = 0; j < nb; ++j) {
-                const bool mine = j < nt, next = j + 1 < nt, more = j + 1 < nb;  // (an idle tile follows the rings too)
-                ok = ok && wait(v_full + vs, vp);
-                if (more) ok = ok && wait(k_full + ks, kp);
-                if (mine) ok = ok && wait(p_ready + 2 * t, (blocks + j) & 1);
-                fence_after_sync();
-                if (t || begun) turn_wait(1 + t);
-                begun = true;
-                if (mine && ok && elect_one()) weigh(0, vs, j > 0);
-                __syncwarp();
-                const int vs0 = vs;
-                if (L::NV == 2) {
-                    if (!mine && ok && lane == 0) mbar_arrive(v_empty + vs0);
-                    if (++vs == L::VST) vs = 0, vp ^= 1;
-                    ok = ok && wait(v_full + vs, vp);
-                }
-                if (mine) ok = ok && wait(p_ready + 2 * t + 1, (blocks + j) & 1);
-                fence_after_sync();
-                if (ok && elect_one()) {
-                    if (mine) {
-                        weigh(1, vs, true);
-                        // the next scores overwrite this block's weights: behind the product in the same queue
-                        if (next) {
-                            scores();
-                            if (j + 2 == nt) mma_commit(q_empty + t);
-                        } else {
-                            mma_commit(o_full + t);
-                        }
-                    } else {
-                        mbar_arrive(v_empty + vs);
-                    }
-                    if (!next && more) mbar_arrive(k_empty + ks);
-                }
-                __syncwarp();
-                turn_pass(2 - t);
-                if (more) next_keys();
-                if (++vs == L::VST) vs = 0, vp ^= 1;
-            }
-            blocks += nt;
-            tiles += nt > 0;
-            ok = __all_sync(0xffffffffu, ok);
-        }
-        if (!t && begun) turn_wait(1);  // the other warp's last turn was passed here
-        // nothing issued may still run, and no commit arrive, once the CTA has ended
-        if (elect_one()) {
-            mma_commit(drain + t);
-            mbar_wait(drain + t, 0, kPolls);
-        }
-        __syncwarp();
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         // ---- softmax of tile t, a thread per row
         const int t = warp >> 2, m_row = (warp & 3) * 32 + lane;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -771,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tiles += nt > 0;
             fence_after_sync();
             if (!ok) inv = lse = __int_as_float(0x7fc00000);
-            if (row0 < s.nq) {  // (else the item has no such tile)
+            if (row0 + (warp & 3) * 32 < s.nq) {  // (else the warp has no such rows)
                 const float2 inv2 = make_float2(inv, inv), zero = make_float2(0.f, 0.f);
                 float2 odd[4] = {zero, zero, zero, zero};  // 0, or NaN where an output is not finite
 #pragma unroll 1
@@ -875,6 +884,12 @@ kda_status run(const PromptParams &p, cudaStream_t st) {
         if (cudaFuncSetAttribute(attn_prompt_kernel<D, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) !=
             cudaSuccess) {
             set_error("attn_prompt: cannot reserve shared memory: %s", cudaGetErrorString(cudaGetLastError()));
+            return KDA_ERR_CUDA;
+        }
+        cudaFuncAttributes attr;
+        if (cudaFuncGetAttributes(&attr, attn_prompt_kernel<D, DV>) != cudaSuccess || attr.numRegs < kLaunchRegs) {
+            cudaGetLastError();
+            set_error("attn_prompt: built with fewer registers than its warps share out");
             return KDA_ERR_CUDA;
         }
         configured.set(dev);
