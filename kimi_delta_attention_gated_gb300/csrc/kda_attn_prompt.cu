@@ -48,7 +48,7 @@ using namespace tc;
 constexpr int kTile = 128;             // query rows of a tile, and keys of a block
 constexpr int kMmaWarp = 8, kTmaWarp = 10, kItemWarp = 11;
 constexpr int kThreads = 384;
-constexpr int kFewRegs = 104, kManyRegs = 200;  // a thread's registers in warps 8-11 and 0-7
+constexpr int kFewRegs = 120, kManyRegs = 192;  // a thread's registers in warps 8-11 and 0-7
 constexpr int kLaunchRegs = 168;                // and at launch, which must cover them
 static_assert(kFewRegs * 128 + kManyRegs * 256 <= kLaunchRegs * kThreads, "a larger share would be waited for without end");
 constexpr int kItemReaders = 11;       // warps that follow the work items
