@@ -81,40 +81,6 @@ __device__ __forceinline__ void rotate_queries(const AppendParams &p, int tile, 
                                THREADS);
 }
 
-// Channels [8v, 8v + 8) of a head's row w, turned with cs (null: as they are); the row's
-// pieces lie in consecutive lanes, so the half layout's partner comes from another lane.
-__device__ __forceinline__ void turn_piece(const uint4 &w, int v, const float2 *cs, const RotaryParams &r, float (&y)[8]) {
-    using V = Vec16<__nv_bfloat16>;
-    V::load(w, y);
-    if (!cs) return;  // for the whole warp
-    const int c0 = v * 8, half = r.R >> 1, np = half;
-    if (r.interleaved) {
-        if (c0 >= r.R) return;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = y[2 * i], b = y[2 * i + 1];
-            turn_pair(a, b, cs[cs_at(v * 4 + i, np)], r.magnitude, y[2 * i], y[2 * i + 1]);
-        }
-        return;
-    }
-    const bool second = c0 >= half;
-    const int lane = threadIdx.x & 31, j = second ? c0 - half : c0;
-    const int from = c0 >= r.R ? lane : second ? lane - (half >> 3) : lane + (half >> 3);
-    uint4 o;
-    o.x = __shfl_sync(0xffffffffu, w.x, from);
-    o.y = __shfl_sync(0xffffffffu, w.y, from);
-    o.z = __shfl_sync(0xffffffffu, w.z, from);
-    o.w = __shfl_sync(0xffffffffu, w.w, from);
-    if (c0 >= r.R) return;
-    float z[8];
-    V::load(o, z);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float2 w2 = cs[cs_at(j + i, np)];
-        y[i] = diff_of_products(y[i], w2.x, second ? -z[i] : z[i], w2.y) * r.magnitude;
-    }
-}
-
 // The scale's exponent of a block whose new values reach amax; off: tokens it already holds.
 __device__ __forceinline__ int block_exp(float amax, int off, int old) {
     const int need = scale_exp(amax);
@@ -132,10 +98,10 @@ __global__ void __launch_bounds__(kStepThreads) append_queries_kernel(const __gr
     rotate_queries<kStepThreads>(p, blockIdx.x, q_tile, cs, s_pos);
 }
 
-template <int D, int THREADS, int ITERS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_run_kernel(const __grid_constant__ AppendParams p,
-                                                                             const __grid_constant__ Grid g) {
-    constexpr int kThreads = THREADS, kWarps = THREADS / 32;
+template <int D, int P>
+__global__ void __launch_bounds__(P *D / 16, 1024 / (P * D / 16)) append_run_kernel(const __grid_constant__ AppendParams p,
+                                                                                   const __grid_constant__ Grid g) {
+    constexpr int kThreads = P * D / 16, kWarps = kThreads / 32;
     extern __shared__ float2 cs[];
     __shared__ int s_pos[kRoom];
     __shared__ int s_seq, s_run;
@@ -146,8 +112,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_run_kernel(con
         rotate_queries<kThreads>(p, blockIdx.x - g.n_kv, g.q_tile, cs, s_pos);
         return;
     }
-    constexpr int nv = D >> 3;
-    const int P = p.c.P;
     const int values = blockIdx.x & 1, part = (blockIdx.x >> 1) % g.head_parts, unit = (blockIdx.x >> 1) / g.head_parts;
     // the unit-th run over all sequences
     if (tid == 0) s_seq = -1;
@@ -191,25 +155,33 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_run_kernel(con
     int page = block < p.c.max_blocks ? p.c.block_table[(int64_t)seq * p.c.max_blocks + block] : -1;
     if (page >= p.c.n_pages) page = -1;  // no such page: the tokens are dropped (their rotated copies are not)
 
-    const __nv_bfloat16 *src = (values ? p.v : p.k) + t0 * (values ? p.v_stride : p.k_stride);
     const int64_t stride = values ? p.v_stride : p.k_stride;
-    uint8_t *codes = values ? p.c.v : p.c.k;
-    float *scales = values ? p.c.v_scale : p.c.k_scale;
     const bool turned = !values && p.rot.R > 0;
     const int h0 = part * g.heads, h1 = min(h0 + g.heads, p.c.Hk), np = p.rot.R >> 1;
-    // This thread's pieces: token x / nv of the run, channels 8 (x % nv).  Two heads' rows are
-    // on their way while a third is worked on: with one, each head took a memory latency.
+    // This thread's share of every head: two 16-byte pieces of one token, which in the rotated
+    // part hold each other's partners and use the same eight cos / sin pairs.
+    constexpr int U = D / 16;
+    const int t = tid / U, u = tid % U, nrot = turned ? p.rot.R >> 4 : 0;
+    const bool live = t < n, apart = u < nrot && !p.rot.interleaved;
+    const int c0 = apart ? 8 * u : 16 * u, c1 = apart ? 8 * u + np : 16 * u + 8;
+    const __nv_bfloat16 *src = (values ? p.v : p.k) + (t0 + t) * stride + h0 * D;
+    __nv_bfloat16 *turned_to = !values && p.k_out ? p.k_out + ((t0 + t) * p.c.Hk + h0) * D : nullptr;
+    const int64_t block0 = (int64_t)page * p.c.Hk;
+    uint8_t *codes = (values ? p.c.v : p.c.k) + (block0 + h0) * (P * D);
+    float *scales = (values ? p.c.v_scale : p.c.k_scale) + block0;
+    // Two heads' rows are on their way while a third is worked on: with one, each head took a
+    // memory latency.
     constexpr int AHEAD = 2;
-    uint4 raw[AHEAD][ITERS];
+    uint4 raw[AHEAD][2];
     int old_scale[AHEAD];
-    auto fetch = [&](int h, uint4 (&w)[ITERS], int &old) {
-#pragma unroll
-        for (int i = 0; i < ITERS; ++i) {
-            const int x = tid + i * kThreads, t = x / nv, v = x % nv;
-            w[i] = h < h1 && t < n ? __ldg(reinterpret_cast<const uint4 *>(src + t * stride + h * D + v * 8)) : make_uint4(0, 0, 0, 0);
+    auto fetch = [&](int h, uint4 (&w)[2], int &old) {
+        if (live && h < h1) {
+            w[0] = __ldg(reinterpret_cast<const uint4 *>(src + c0));
+            w[1] = __ldg(reinterpret_cast<const uint4 *>(src + c1));
         }
+        src += D;
         // a page that holds earlier tokens: its scale (no other CTA writes it)
-        old = off > 0 && page >= 0 && h < h1 ? exp_of_scale(scales[(int64_t)page * p.c.Hk + h]) : kScaleExpLo;
+        old = off > 0 && page >= 0 && h < h1 ? exp_of_scale(scales[h]) : kScaleExpLo;
     };
 #pragma unroll
     for (int b = 0; b < AHEAD; ++b) fetch(h0 + b, raw[b], old_scale[b]);
@@ -217,71 +189,79 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_run_kernel(con
         fill_cos_sin_run(cs, p.rot, n, (int)pos0, tid, kThreads);
         __syncthreads();
     }
+    const float2 *turns = cs + t * np;
     for (int hb = h0; hb < h1; hb += AHEAD)
 #pragma unroll
     for (int b = 0; b < AHEAD; ++b) {
         const int h = hb + b;
         if (h >= h1) break;
-        float y[ITERS][8];
+        float y[2][8];
         float amax = 0.f;
         const int old = old_scale[b];
+        if (live) {
+            Vec16<__nv_bfloat16>::load(raw[b][0], y[0]);
+            Vec16<__nv_bfloat16>::load(raw[b][1], y[1]);
+            if (u < nrot) {
 #pragma unroll
-        for (int i = 0; i < ITERS; ++i) {
-            const int x = tid + i * kThreads, t = x / nv, v = x % nv;
-            turn_piece(raw[b][i], v, turned ? cs + min(t, n - 1) * np : nullptr, p.rot, y[i]);
-            if (t < n) {
+                for (int i = 0; i < 8; ++i) {
+                    const float2 w = turns[cs_at(8 * u + i, np)];
+                    if (p.rot.interleaved) {
+                        float *z = &y[i >> 2][2 * (i & 3)];
+                        turn_pair(z[0], z[1], w, p.rot.magnitude, z[0], z[1]);
+                    } else {
+                        turn_pair(y[0][i], y[1][i], w, p.rot.magnitude, y[0][i], y[1][i]);
+                    }
+                }
+            }
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) amax = fmaxf(fmaxf(amax, fabsf(y[i][e])), fabsf(y[i][e + 1]));  // no NaN
-                if (!values && p.k_out)
-                    *reinterpret_cast<uint4 *>(p.k_out + ((t0 + t) * p.c.Hk + h) * D + v * 8) =
-                        Vec16<__nv_bfloat16>::store(y[i]);
+            for (int i = 0; i < 8; ++i) amax = fmaxf(fmaxf(amax, fabsf(y[0][i])), fabsf(y[1][i]));  // no NaN
+            if (turned_to) {
+                *reinterpret_cast<uint4 *>(turned_to + c0) = Vec16<__nv_bfloat16>::store(y[0]);
+                *reinterpret_cast<uint4 *>(turned_to + c1) = Vec16<__nv_bfloat16>::store(y[1]);
             }
         }
+        if (turned_to) turned_to += D;
         fetch(h + AHEAD, raw[b], old_scale[b]);
         if (page < 0) continue;
         amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
         if (lane == 0) s_max[h & 1][warp] = amax;
-        const int64_t blk = (int64_t)page * p.c.Hk + h;
         __syncthreads();  // also: every thread has read this head's old scale
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, s_max[h & 1][w]);
+        auto largest = [&] { return __uint_as_float(__reduce_max_sync(0xffffffffu, lane < kWarps ? __float_as_uint(s_max[h & 1][lane]) : 0u)); };
+        amax = largest();
         if (isinf(amax)) {  // rare: the largest finite value, and NaN in the infinities' places
             amax = 0.f;
+            if (live) {
 #pragma unroll
-            for (int i = 0; i < ITERS; ++i)
-                if ((tid + i * kThreads) / nv < n) {
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        amax = fmaxf(amax, finite_abs(y[i][x]));
-                        y[i][x] = no_infinity(y[i][x]);
-                    }
+                for (int i = 0; i < 16; ++i) {
+                    amax = fmaxf(amax, finite_abs(y[i >> 3][i & 7]));
+                    y[i >> 3][i & 7] = no_infinity(y[i >> 3][i & 7]);
                 }
+            }
             amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
             __syncthreads();
             if (lane == 0) s_max[h & 1][warp] = amax;
             __syncthreads();
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, s_max[h & 1][w]);
+            amax = largest();
         }
         const int e = block_exp(amax, off, old);
-        uint8_t *dst = codes + blk * P * D;
         if (off > 0 && e > old) {
             const float f = exp2_int(max(old - e, -126));
-            uint32_t *w = reinterpret_cast<uint32_t *>(dst);
+            uint32_t *w = reinterpret_cast<uint32_t *>(codes);
             for (int i = tid; i < off * D / 4; i += kThreads) w[i] = rescale_codes(w[i], f);
         }
-        if (tid == 0) scales[blk] = exp2_int(e);
+        if (tid == 0) scales[h] = exp2_int(e);
         const float inv = exp2_int(-e);
-#pragma unroll
-        for (int i = 0; i < ITERS; ++i) {
-            const int x = tid + i * kThreads, t = x / nv, v = x - t * nv;
-            if (t < n) {
+        if (live) {
+            auto put = [&](const float (&y)[8], int c) {
                 uint2 w;
-                w.x = e4m3x2(y[i][0] * inv, y[i][1] * inv) | e4m3x2(y[i][2] * inv, y[i][3] * inv) << 16;
-                w.y = e4m3x2(y[i][4] * inv, y[i][5] * inv) | e4m3x2(y[i][6] * inv, y[i][7] * inv) << 16;
-                *reinterpret_cast<uint2 *>(dst + (int64_t)(off + t) * D + v * 8) = w;
-            }
+                w.x = e4m3x2(y[0] * inv, y[1] * inv) | e4m3x2(y[2] * inv, y[3] * inv) << 16;
+                w.y = e4m3x2(y[4] * inv, y[5] * inv) | e4m3x2(y[6] * inv, y[7] * inv) << 16;
+                *reinterpret_cast<uint2 *>(codes + (off + t) * D + c) = w;
+            };
+            put(y[0], c0);
+            put(y[1], c1);
         }
+        codes += P * D;
     }
 }
 
@@ -375,8 +355,9 @@ __global__ void __launch_bounds__(kStepThreads) append_step_kernel(const __grid_
         *reinterpret_cast<uint16_t *>(dst + (int64_t)off * D + c0 + i) = (uint16_t)e4m3x2(y[i] * inv, y[i + 1] * inv);
 }
 
-template <int D, int THREADS, int ITERS>
+template <int D, int P>
 kda_status run(const AppendParams &p, Grid g, cudaStream_t st) {
+    constexpr int THREADS = P * D / 16;
     // A sequence's n new tokens lie in at most n / P + 2 pages.
     const int64_t runs = p.tokens / p.c.P + 2 * (int64_t)p.c.N;
     g.q_tile = p.q ? rotary_tile_tokens(p.Hq, p.c.D, p.rot.R, 8, THREADS, kRoom) : 1;
@@ -401,7 +382,7 @@ kda_status run(const AppendParams &p, Grid g, cudaStream_t st) {
         static DeviceOnce configured;
         const int dev = current_device();
         if (!configured.done(dev)) {
-            if (cudaFuncSetAttribute(append_run_kernel<D, THREADS, ITERS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            if (cudaFuncSetAttribute(append_run_kernel<D, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      64 * 1024) != cudaSuccess) {
                 set_error("kv_append: cannot reserve shared memory: %s", cudaGetErrorString(cudaGetLastError()));
                 return KDA_ERR_CUDA;
@@ -409,7 +390,7 @@ kda_status run(const AppendParams &p, Grid g, cudaStream_t st) {
             configured.set(dev);
         }
     }
-    append_run_kernel<D, THREADS, ITERS><<<(unsigned)(kv + (apart ? 0 : q_ctas)), THREADS, smem, st>>>(p, g);
+    append_run_kernel<D, P><<<(unsigned)(kv + (apart ? 0 : q_ctas)), THREADS, smem, st>>>(p, g);
     note_launch();
     if (apart) {
         const kda_status s = check_launch("append_run_kernel");
@@ -444,18 +425,16 @@ kda_status launch_kv_append(const AppendParams &p, cudaStream_t st) {
         note_launch();
         return check_launch("append_step_kernel");
     }
-    // One or two 16-byte pieces of a page's rows per thread: 64 registers and full occupancy
-    // (four pieces took 127, and a third of the bandwidth).
     if (p.c.D == 128) {
-        if (p.c.P == 16) return run<128, 256, 1>(p, g, st);
-        if (p.c.P == 32) return run<128, 256, 2>(p, g, st);
-        if (p.c.P == 64) return run<128, 512, 2>(p, g, st);
-        return run<128, 1024, 2>(p, g, st);
+        if (p.c.P == 16) return run<128, 16>(p, g, st);
+        if (p.c.P == 32) return run<128, 32>(p, g, st);
+        if (p.c.P == 64) return run<128, 64>(p, g, st);
+        return run<128, 128>(p, g, st);
     }
-    if (p.c.P == 16) return run<64, 128, 1>(p, g, st);
-    if (p.c.P == 32) return run<64, 256, 1>(p, g, st);
-    if (p.c.P == 64) return run<64, 256, 2>(p, g, st);
-    return run<64, 512, 2>(p, g, st);
+    if (p.c.P == 16) return run<64, 16>(p, g, st);
+    if (p.c.P == 32) return run<64, 32>(p, g, st);
+    if (p.c.P == 64) return run<64, 64>(p, g, st);
+    return run<64, 128>(p, g, st);
 }
 
 }  // namespace kda
