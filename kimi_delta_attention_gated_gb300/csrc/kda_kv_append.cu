@@ -96,6 +96,9 @@ __global__ void __launch_bounds__(kStepThreads) append_queries_kernel(const __gr
     __shared__ float2 cs[kRoom];
     __shared__ int s_pos[kRoom];
     rotate_queries<kStepThreads>(p, blockIdx.x, q_tile, cs, s_pos);
+    // Its CTAs start while the runs' last ones are at work, and share nothing with them; the launch
+    // must not end before the runs' has.
+    if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int D, int P>
@@ -108,6 +111,7 @@ __global__ void __launch_bounds__(P *D / 16, 1024 / (P * D / 16)) append_run_ker
     __shared__ int s_scan[kWarps];
     __shared__ float s_max[2][kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the queries' launch, where there is one
     if ((int)blockIdx.x >= g.n_kv) {
         rotate_queries<kThreads>(p, blockIdx.x - g.n_kv, g.q_tile, cs, s_pos);
         return;
@@ -397,8 +401,22 @@ kda_status run(const AppendParams &p, Grid g, cudaStream_t st) {
         if (s != KDA_OK) return s;
         int tile = rotary_tile_tokens(p.Hq, p.c.D, p.rot.R, 8, kStepThreads, kRoom);
         if (tile > kRoom) tile = kRoom;
-        append_queries_kernel<<<(unsigned)((p.tokens + tile - 1) / tile), kStepThreads, 0, st>>>(p, tile);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)((p.tokens + tile - 1) / tile));
+        cfg.blockDim = dim3(kStepThreads);
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, append_queries_kernel, p, tile);
         note_launch();
+        if (e != cudaSuccess) {
+            set_error("append_queries_kernel: %s", cudaGetErrorString(e));
+            cudaGetLastError();
+            return KDA_ERR_CUDA;
+        }
         return check_launch("append_queries_kernel");
     }
     return check_launch("append_run_kernel");
