@@ -113,9 +113,10 @@ kda_status kda_device_status(void *stream);
  * The decode step's copy waits (kda_recurrent_step, kda_recurrent_step_logits with
  * K = V = 128), the short convolution's tile waits (kda_short_conv_fwd over a prompt)
  * and the fused tensor-core prefill's tile and blob waits (kda_chunk_fwd,
- * kda_chunk_fwd_logits without a workspace or with one in the concurrent form) poll
- * their mbarrier at most this many times before they give up, for the calls made after
- * this one (process-wide).  polls < 0 restores the default (2^26); 0 makes every such
+ * kda_chunk_fwd_logits without a workspace or with one in the concurrent form) and the
+ * attention kernels' tile waits (kda_attn_decode, kda_attn_prompt) poll their mbarrier at most this many times before they give up, for the calls made after
+ * this one (process-wide).  polls < 0 restores the default (2^26; the attention kernels never
+ * poll more than 2^21 times); 0 makes every such
  * wait give up at once, which tests of the failure handling use (kda_device_status then
  * reports KDA_ERR_TIMEOUT and the outputs hold NaN).  The waits that let copies in
  * flight land before a CTA exits, the tensor-core waits, and the split form's kernels

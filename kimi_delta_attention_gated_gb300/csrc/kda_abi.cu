@@ -1,6 +1,7 @@
 // kda_abi.cu -- the extern "C" boundary of libkda: argument validation, path
 // selection and launch bookkeeping.  Declarations and their documentation are
 // in include/kda.h.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -946,6 +947,7 @@ kda_status kda_attn_decode(const void *q, int64_t q_stride, const void *k_cache,
     p.o_bf16 = o_dtype == KDA_BF16;
     p.lse = lse;
     p.ws = static_cast<float *>(workspace);
+    p.polls = std::min(kda::wait_polls(), kda::kAttnPolls);
     return kda::launch_attn_decode(p, (cudaStream_t)stream);
 }
 
@@ -1016,6 +1018,7 @@ kda_status kda_attn_prompt(const void *q, int64_t q_stride, const void *k, int64
     p.o = o;
     p.o_bf16 = o_dtype == KDA_BF16;
     p.lse = lse;
+    p.polls = std::min(kda::wait_polls(), kda::kAttnPolls);
     return kda::launch_attn_prompt(p, (cudaStream_t)stream);
 }
 

@@ -45,6 +45,10 @@ struct AppendParams {
     __nv_bfloat16 *q_out, *k_out; // dense [tokens, Hq, D] / [tokens, Hk, D]; k_out may be null
 };
 
+// Bound on the attention kernels' waits, a few seconds: a CTA waits for nothing but its own warps
+// and copies.  The first-line waits on copies take a lower one from kda_set_wait_limit.
+constexpr uint32_t kAttnPolls = 1u << 21;
+
 struct DecodeParams {
     PagedCache c;                 // lens: tokens in the cache
     const __nv_bfloat16 *q;       // rows of Hq * D, q_stride elements apart
@@ -55,6 +59,7 @@ struct DecodeParams {
     int o_bf16;
     float *lse;                   // [N, Hq] or null
     float *ws;                    // partial results
+    uint32_t polls;               // bound on the copies' waits
 };
 
 struct PromptParams {
@@ -67,6 +72,7 @@ struct PromptParams {
     void *o;                         // [Tq, Hq, DV]
     int o_bf16;
     float *lse;                      // [Tq, Hq] or null
+    uint32_t polls;                  // bound on the copies' waits
 };
 
 kda_status launch_rotary(const void *x, int bf16, int64_t x_stride, const int32_t *positions, const RotaryParams &r,

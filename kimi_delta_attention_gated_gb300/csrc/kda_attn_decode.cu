@@ -46,7 +46,6 @@ constexpr int kJoinMost = 512;   // threads of a joining CTA at most
 constexpr int kStep = 32;       // tokens of a step
 constexpr int kPad = 6;         // a head's own cost in steps
 constexpr int kMinPiece = 8;   // places of a CTA at least
-constexpr uint32_t kPolls = 1u << 21;  // bound on a copy's wait: a few seconds
 constexpr float kSlack = 8.f;   // the maximum in use may lie this far below the true one (log2)
 constexpr float kNegInf = -INFINITY;
 
@@ -278,8 +277,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
     settle();
     int page = ld_more ? page_at() : -1;
     int wr = 0, issued = 0;
+    int failed = 0;  // a copy's wait gave up: no further copies, NaN in what is left
     auto copy_step = [&] {
-        if (ld_more) {
+        if (ld_more && !failed) {
             const bool good = (uint32_t)page < (uint32_t)c.n_pages;
             const uint32_t slot = ring + wr * F::SLOT;
             if (lane < 4) {
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
     const int v_at[2] = {D == 128 ? 2 * t * 128 + ((g ^ (2 * t)) << 4) : 2 * t * 64 + (((g >> 1) ^ t) << 4) + 8 * (g & 1),
                          D == 128 ? (2 * t + 1) * 128 + ((g ^ (2 * t + 1)) << 4)
                                   : (2 * t + 1) * 64 + (((g >> 1) ^ t) << 4) + 8 * (g & 1)};
-    int rd = 0, failed = 0;
+    int rd = 0;
     uint32_t rd_phase = 0;
     bool first = true;
     // A unit's queries: each lane the 16-byte pieces of its row that its products take.
@@ -394,8 +394,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
         }
         for (int s = cur.s0 + warp; s < cur.s1; s += kWarps) {
             cp_wait<F::DEPTH - 1>();
-            if (!failed && !tc::mbar_wait(bars + rd, rd_phase, kPolls)) failed = 1;
-            __syncwarp();
+            if (!failed && !tc::mbar_wait(bars + rd, rd_phase, p.polls)) failed = 1;
+            failed = __any_sync(0xffffffffu, failed);
             const uint8_t *slot = smem + (warp * F::DEPTH + rd) * F::SLOT;
             const float4 sc = *reinterpret_cast<const float4 *>(smem + F::SCALES + (warp * F::DEPTH + rd) * 16);
             const float ks[2] = {sc.x, sc.z}, vs[2] = {sc.y, sc.w};
@@ -526,7 +526,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
             __syncwarp();  // every lane has read the slot: it is filled again
             copy_step();
         }
-        failed = __any_sync(0xffffffffu, failed);
         if (failed) {  // a copy's wait gave up: the sums stand for nothing
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) l[nt][0] = l[nt][1] = __int_as_float(0x7fc00000);
@@ -622,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
     cp_wait<0>();
     // after a failure copies may still be under way: they land before the CTA ends
     if (failed) {
-        for (int i = max(0, issued - F::DEPTH); i < issued; ++i) tc::mbar_wait(bars + i % F::DEPTH, (i / F::DEPTH) & 1, kPolls);
+        for (int i = max(0, issued - F::DEPTH); i < issued; ++i) tc::mbar_wait(bars + i % F::DEPTH, (i / F::DEPTH) & 1, kAttnPolls);
         if (lane == 0) atomicAdd(&g_attn_decode_timeouts, 1);
     }
 }

@@ -52,7 +52,6 @@ constexpr int kFewRegs = 120, kManyRegs = 192;  // a thread's registers in warps
 constexpr int kLaunchRegs = 168;                // and at launch, which must cover them
 static_assert(kFewRegs * 128 + kManyRegs * 256 <= kLaunchRegs * kThreads, "a larger share would be waited for without end");
 constexpr int kItemReaders = 11;       // warps that follow the work items
-constexpr uint32_t kPolls = 1u << 21;  // a few seconds; a CTA waits for nothing but its own warps and loads
 constexpr float kSlack = 40.f;         // log2: how far a score may exceed the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -435,14 +434,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tb = *tmem_slot;
     const int group = p.Hq / p.Hk;
     int failed = 0;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        for (uint32_t i = 0; i < kPolls; ++i) {
+    auto wait_for = [&](uint64_t *bar, uint32_t parity, uint32_t polls) {
+        for (uint32_t i = 0; i < polls; ++i) {
             if (mbar_try_wait(bar, parity)) return true;
             if (*abort_flag) break;
         }
         *abort_flag = 1;
         return false;
     };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_for(bar, parity, kAttnPolls); };
+    auto wait_copy = [&](uint64_t *bar, uint32_t parity) { return wait_for(bar, parity, p.polls); };
+    // The same where the warp's lanes have to go on or stop together.
+    auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
     // This CTA's k-th work item; one warp.
     auto find_item = [&](UnitSearch &units, int k) {
         const int64_t i = (int64_t)k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
@@ -453,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return it;
     };
     // The same from the item warp, for a warp that follows them all; false when a wait gave up.
-    auto see_item = [&](int k) { return __all_sync(0xffffffffu, wait(i_full + (k & 1), (k >> 1) & 1)) != 0; };
+    auto see_item = [&](int k) { return wait_all(i_full + (k & 1), (k >> 1) & 1); };
     auto leave_item = [&](int k) {
         __syncwarp();
         if (lane == 0) mbar_arrive(i_empty + (k & 1));
@@ -481,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- work items, two ahead
             UnitSearch units;
             for (int k = 0;; ++k) {
-                if (k >= 2 && !wait(i_empty + (k & 1), ((k >> 1) - 1) & 1)) {
+                if (k >= 2 && !wait_all(i_empty + (k & 1), ((k >> 1) - 1) & 1)) {
                     failed = 1;
                     break;
                 }
@@ -494,7 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!it.found) break;
             }
         } else if (warp == kTmaWarp) {
-            // ---- loads
+            // ---- loads.  One lane issues them, so that its waits need no agreement, up to an item's last
+            // values: rows behind the sequence's end are there zeroed by the whole warp.
             const uint64_t once = leave_first(), again = leave_last();
             uint32_t raw = 0;
             int nq_issued[2] = {0, 0}, nk_issued = 0, nv_issued = 0;
@@ -508,72 +512,83 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int n0 = tile_blocks(it, s, 0), n1 = tile_blocks(it, s, 1), nb = max(n0, n1);
                 auto load_q = [&](int t) {
                     if (nq_issued[t] > 0 && !wait(q_empty + t, (nq_issued[t] - 1) & 1)) return false;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(q_full + t, L::QB);
-                        for (int x = 0; x < D; x += 64)
-                            tma_load_hint(sb + L::Q + t * L::QB + (x / 64) * kTile * 128, &map_q, q_full + t, x,
-                                          a.pair_heads ? head0 + t : head0, s.q0 + tile_row(it, t), once);
-                    }
+                    mbar_arrive_expect_tx(q_full + t, L::QB);
+#pragma unroll
+                    for (int x = 0; x < D; x += 64)
+                        tma_load_hint(sb + L::Q + t * L::QB + (x / 64) * kTile * 128, &map_q, q_full + t, x,
+                                      a.pair_heads ? head0 + t : head0, s.q0 + tile_row(it, t), once);
                     ++nq_issued[t];
                     return true;
                 };
                 auto load_k = [&](int j) {
                     const int i = nk_issued, st = i % L::KST;
                     if (i >= L::KST && !wait(k_empty + st, (i / L::KST - 1) & 1)) return false;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(k_full + st, L::KB);
-                        for (int x = 0; x < D; x += 64)
-                            tma_load_hint(sb + L::K + st * L::KB + (x / 64) * kTile * 128, &map_k, k_full + st, x, kvh,
-                                          s.k0 + j * kTile, again);
-                    }
+                    mbar_arrive_expect_tx(k_full + st, L::KB);
+#pragma unroll
+                    for (int x = 0; x < D; x += 64)
+                        tma_load_hint(sb + L::K + st * L::KB + (x / 64) * kTile * 128, &map_k, k_full + st, x, kvh,
+                                      s.k0 + j * kTile, again);
                     ++nk_issued;
                     return true;
                 };
-                auto load_v = [&](int j, int h) {
-                    const int i = nv_issued, st = i % L::VST;
-                    if (i >= L::VST && !wait(v_empty + st, (i / L::VST - 1) & 1)) return false;
-                    const int rows = max(0, s.nk - j * kTile - h * L::VROWS);  // of the sequence
-                    uint64_t *bar = rows < L::VROWS ? v_raw : v_full + st;
-                    const uint32_t base = L::V + st * L::VB;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(bar, L::VB);
-                        for (int x = 0; x < DV; x += 64)
-                            tma_load_hint(sb + base + (x / 64) * L::VROWS * 128, &map_v, bar, x, kvh,
-                                          s.k0 + j * kTile + h * L::VROWS, again);
+                auto issue_v = [&](int j, int h, int st, uint64_t *bar) {
+                    mbar_arrive_expect_tx(bar, L::VB);
+#pragma unroll
+                    for (int x = 0; x < DV; x += 64)
+                        tma_load_hint(sb + L::V + st * L::VB + (x / 64) * L::VROWS * 128, &map_v, bar, x, kvh,
+                                      s.k0 + j * kTile + h * L::VROWS, again);
+                };
+                auto v_free = [&](int st) { return nv_issued < L::VST || wait(v_empty + st, (nv_issued / L::VST - 1) & 1); };
+                if (lane == 0) {
+                    if (n0) ok = load_q(0);
+                    if (ok && nb) ok = load_k(0);
+                    if (ok && n1) ok = load_q(1);
+                    for (int j = 0; j + 1 < nb && ok; ++j) {
+                        ok = load_k(j + 1);
+                        for (int h = 0; h < L::NV && ok; ++h) {
+                            const int st = nv_issued % L::VST;
+                            ok = v_free(st);
+                            if (!ok) break;
+                            issue_v(j, h, st, v_full + st);
+                            ++nv_issued;
+                        }
                     }
+                }
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+                nv_issued = __shfl_sync(0xffffffffu, nv_issued, 0);
+                for (int h = 0; h < L::NV && nb > 0 && ok; ++h) {
+                    const int st = nv_issued % L::VST;
+                    const int rows = max(0, s.nk - (nb - 1) * kTile - h * L::VROWS);  // of the sequence
+                    ok = __all_sync(0xffffffffu, v_free(st)) != 0;
+                    if (!ok) break;
+                    if (lane == 0) issue_v(nb - 1, h, st, rows < L::VROWS ? v_raw : v_full + st);
                     if (rows < L::VROWS) {
-                        const bool landed = wait(v_raw, raw & 1);
-                        if (!landed) mbar_wait(v_raw, raw & 1, kPolls);  // the copy must still land before the CTA may end
+                        ok = __all_sync(0xffffffffu, wait(v_raw, raw & 1)) != 0;
+                        if (!ok) mbar_wait(v_raw, raw & 1, kAttnPolls);  // the copy must still land before the CTA may end
                         ++raw;
-                        if (!landed) return false;
+                        if (!ok) break;
                         for (int i = lane; i < (L::VROWS - rows) * (DV / 64) * 8; i += 32) {
                             const int r = rows + i / ((DV / 64) * 8), q = i % ((DV / 64) * 8);
-                            st_shared_v4(sb + base + (q >> 3) * L::VROWS * 128 + r * 128 + (q & 7) * 16, 0, 0, 0, 0);
+                            st_shared_v4(sb + L::V + st * L::VB + (q >> 3) * L::VROWS * 128 + r * 128 + (q & 7) * 16, 0, 0, 0, 0);
                         }
                         fence_async_smem();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(v_full + st);
                     }
                     ++nv_issued;
-                    return true;
-                };
-                if (n0) ok = load_q(0);
-                if (ok && nb) ok = load_k(0);
-                if (ok && n1) ok = load_q(1);
-                for (int j = 0; j < nb && ok; ++j) {
-                    if (j + 1 < nb) ok = load_k(j + 1);
-                    for (int h = 0; h < L::NV && ok; ++h) ok = load_v(j, h);
                 }
-                ok = __all_sync(0xffffffffu, ok);
             }
             if (!ok) failed = 1;
             // every load lands before the CTA may end
-            for (int t = 0; t < 2; ++t)
-                if (nq_issued[t]) mbar_wait(q_full + t, (nq_issued[t] - 1) & 1, kPolls);
-            for (int j = max(0, nk_issued - L::KST); j < nk_issued; ++j)
-                mbar_wait(k_full + j % L::KST, (j / L::KST) & 1, kPolls);
-            for (int j = max(0, nv_issued - L::VST); j < nv_issued; ++j)
-                mbar_wait(v_full + j % L::VST, (j / L::VST) & 1, kPolls);
+            if (lane == 0) {
+                for (int t = 0; t < 2; ++t)
+                    if (nq_issued[t]) mbar_wait(q_full + t, (nq_issued[t] - 1) & 1, kAttnPolls);
+                for (int j = max(0, nk_issued - L::KST); j < nk_issued; ++j)
+                    mbar_wait(k_full + j % L::KST, (j / L::KST) & 1, kAttnPolls);
+                for (int j = max(0, nv_issued - L::VST); j < nv_issued; ++j)
+                    mbar_wait(v_full + j % L::VST, (j / L::VST) & 1, kAttnPolls);
+            }
+            __syncwarp();
         } else {
             // ---- products of tile t.  One thread's instructions come one at a time, about five
             // cycles each, so the descriptors are bases plus constants.
@@ -618,11 +633,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto next_keys = [&] {
                     if (++ks == L::KST) ks = 0, kp ^= 1;
                 };
-                if (nt) ok = wait(q_full + t, tiles & 1);
+                if (nt) ok = wait_copy(q_full + t, tiles & 1);
                 if (nb) {
                     ok = ok && wait(k_full + ks, kp);
                     fence_after_sync();
-                    if (ok && elect_one()) {
+                    if (elect_one() && ok) {
                         if (nt) {
                             scores();
                             if (nt == 1) mma_commit(q_empty + t);
@@ -640,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_after_sync();
                     if (t || begun) turn_wait(1 + t);
                     begun = true;
-                    if (mine && ok && elect_one()) weigh(0, vs, j > 0);
+                    if (mine && elect_one() && ok) weigh(0, vs, j > 0);
                     __syncwarp();
                     const int vs0 = vs;
                     if (L::NV == 2) {
@@ -650,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (mine) ok = ok && wait(p_ready + 2 * t + 1, (blocks + j) & 1);
                     fence_after_sync();
-                    if (ok && elect_one()) {
+                    if (elect_one() && ok) {
                         if (mine) {
                             weigh(1, vs, true);
                             // the next scores overwrite this block's weights: behind the product in the same queue
@@ -678,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // nothing issued may still run, and no commit arrive, once the CTA has ended
             if (elect_one()) {
                 mma_commit(drain + t);
-                mbar_wait(drain + t, 0, kPolls);
+                mbar_wait(drain + t, 0, kAttnPolls);
             }
             __syncwarp();
         }
@@ -703,8 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < nt; ++j, ++blocks) {
-                ok = wait(s_full + t, blocks & 1);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = wait_all(s_full + t, blocks & 1);
                 if (!ok) break;
                 fence_after_sync();
                 float x[128];
@@ -776,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int esz = p.o_bf16 ? 2 : 4;
             uint8_t *o_rows = static_cast<uint8_t *>(p.o) + ((int64_t)(s.q0 + first) * p.Hq + head) * DV * esz + (lane & 3) * 16;
             const int64_t pitch = (int64_t)p.Hq * DV * esz;
-            if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait(o_full + t, tiles & 1));
+            if (ok && nt > 0) ok = wait_all(o_full + t, tiles & 1);
             tiles += nt > 0;
             fence_after_sync();
             if (!ok) inv = lse = __int_as_float(0x7fc00000);
