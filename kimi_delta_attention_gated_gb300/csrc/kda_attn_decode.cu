@@ -51,6 +51,14 @@ constexpr float kNegInf = -INFINITY;
 
 __device__ int g_attn_decode_timeouts = 0;
 
+// Named barriers of some of a CTA's warps.
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+    asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 template <int D, int NT>
 struct Cfg {
     static constexpr int ROWS = 8 * NT;                 // query heads of a unit
@@ -326,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
     const int v_at[2] = {D == 128 ? 2 * t * 128 + ((g ^ (2 * t)) << 4) : 2 * t * 64 + (((g >> 1) ^ t) << 4) + 8 * (g & 1),
                          D == 128 ? (2 * t + 1) * 128 + ((g ^ (2 * t + 1)) << 4)
                                   : (2 * t + 1) * 64 + (((g >> 1) ^ t) << 4) + 8 * (g & 1)};
-    int rd = 0;
+    int rd = 0, odd = 0;
     uint32_t rd_phase = 0;
     bool first = true;
     // A unit's queries: each lane the 16-byte pieces of its row that its products take.
@@ -539,8 +547,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
             fetch_queries(nxt);
         }
 
-        // ---- the warps' sums of this unit together: the upper two warps' into the lower two's
-        // registers, then the two of those
+        // ---- the warps' sums of this unit together: one pair of warps leaves its sums and goes on with the
+        // next unit, the other adds them to its own, and then the two of those.  The pairs change
+        // parts from unit to unit, so the buffer's last readers are the next to fill it.
         if (cur.s1 > cur.s0) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -569,10 +578,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
                             *reinterpret_cast<float2 *>(buf + r * F::PITCH + 2 * j) = make_float2(acc[nt][j][e], acc[nt][j][e + 2]);
                     }
             };
-            __syncthreads();  // the buffer's previous use is over
-            if (warp >= 2) put();
-            __syncthreads();
-            if (warp < 2) {
+            const bool leaves = (warp >> 1) == (odd ? 0 : 1);
+            const int pair = 3 + (warp >> 1), filled = 1 + odd;
+            odd ^= 1;
+            bar_sync(pair, 64);  // both have read what they left here last
+            if (leaves) {
+                put();
+                bar_arrive(filled, kThreads);
+            } else {
+                bar_sync(filled, kThreads);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -591,26 +605,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
                     }
                 __syncwarp();  // every lane has read M and l
                 put();
-            }
-            __syncthreads();
-            const bool whole = cur.s0 == 0 && cur.s1 == cur.steps;
-            float *part = p.ws + ((int64_t)blockIdx.x * 2 + (first ? 0 : 1)) * F::PART;
-            for (int i = tid; i < F::ROWS * (D / 4); i += kThreads) {
-                const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
-                const float ma = merge_m[r], mb = merge_m[F::ROWS + r], m = fmaxf(ma, mb);
-                const float fa = m == kNegInf ? 1.f : ex2(ma - m), fb = m == kNegInf ? 1.f : ex2(mb - m);
-                const float4 x = *reinterpret_cast<const float4 *>(merge + r * F::PITCH + d);
-                const float4 y = *reinterpret_cast<const float4 *>(merge + (F::ROWS + r) * F::PITCH + d);
-                const float4 a = make_float4(fa * x.x + fb * y.x, fa * x.y + fb * y.y, fa * x.z + fb * y.z, fa * x.w + fb * y.w);
-                const float sum = fa * merge_l[r] + fb * merge_l[F::ROWS + r];
-                if (!whole) {
-                    *reinterpret_cast<float4 *>(part + r * D + d) = a;
-                    if (d == 0) {
-                        part[F::ROWS * D + r] = m;
-                        part[F::ROWS * D + F::ROWS + r] = sum;
+                bar_sync(pair, 64);
+                const bool whole = cur.s0 == 0 && cur.s1 == cur.steps;
+                float *part = p.ws + ((int64_t)blockIdx.x * 2 + (first ? 0 : 1)) * F::PART;
+                for (int i = tid & 63; i < F::ROWS * (D / 4); i += 64) {
+                    const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+                    const float ma = merge_m[r], mb = merge_m[F::ROWS + r], m = fmaxf(ma, mb);
+                    const float fa = m == kNegInf ? 1.f : ex2(ma - m), fb = m == kNegInf ? 1.f : ex2(mb - m);
+                    const float4 x = *reinterpret_cast<const float4 *>(merge + r * F::PITCH + d);
+                    const float4 y = *reinterpret_cast<const float4 *>(merge + (F::ROWS + r) * F::PITCH + d);
+                    const float4 a = make_float4(fa * x.x + fb * y.x, fa * x.y + fb * y.y, fa * x.z + fb * y.z, fa * x.w + fb * y.w);
+                    const float sum = fa * merge_l[r] + fb * merge_l[F::ROWS + r];
+                    if (!whole) {
+                        *reinterpret_cast<float4 *>(part + r * D + d) = a;
+                        if (d == 0) {
+                            part[F::ROWS * D + r] = m;
+                            part[F::ROWS * D + F::ROWS + r] = sum;
+                        }
+                    } else if (r0 + r < group) {
+                        write_row<D>(p, (int64_t)cur.n * p.Hq + h * group + r0 + r, d, a, m, sum);
                     }
-                } else if (r0 + r < group) {
-                    write_row<D>(p, (int64_t)cur.n * p.Hq + h * group + r0 + r, d, a, m, sum);
                 }
             }
         }
