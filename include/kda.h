@@ -114,8 +114,8 @@ kda_status kda_device_status(void *stream);
  * K = V = 128), the short convolution's tile waits (kda_short_conv_fwd over a prompt)
  * and the fused tensor-core prefill's tile and blob waits (kda_chunk_fwd,
  * kda_chunk_fwd_logits without a workspace or with one in the concurrent form) and the
- * attention kernels' tile waits (kda_attn_decode, kda_attn_prompt) poll their mbarrier at most this many times before they give up, for the calls made after
- * this one (process-wide).  polls < 0 restores the default (2^26; the attention kernels never
+ * attention kernels' tile waits (kda_attn_decode, kda_attn_prompt) poll their mbarrier at
+ * most this many times before they give up, for the calls made after this one (process-wide).  polls < 0 restores the default (2^26; the attention kernels never
  * poll more than 2^21 times); 0 makes every such
  * wait give up at once, which tests of the failure handling use (kda_device_status then
  * reports KDA_ERR_TIMEOUT and the outputs hold NaN).  The waits that let copies in
@@ -602,11 +602,19 @@ kda_status kda_attn_decode(const void *q, int64_t q_stride, const void *k_cache,
  * (dim, dim_v) one of (64, 64), (128, 128), (192, 128) (KDA_ERR_UNSUPPORTED otherwise); q_heads a
  * multiple of kv_heads; scale finite and not 0.  Nothing a row does not see enters its result,
  * be it infinite or NaN.  The weights are rounded to bf16 for the product with v.
+ *
+ *   workspace    device scratch of kda_attn_prompt_workspace_size(...) bytes, 16-byte aligned, for
+ *                this call alone, or NULL.  With few rows and heads for the GPU's SMs the size is
+ *                not 0, and a call with the workspace divides each row's keys among several
+ *                CTAs and joins their sums (rounded differently than in one go).
  */
+size_t kda_attn_prompt_workspace_size(int64_t q_rows, int64_t k_rows, int q_heads, int kv_heads, int dim_v, int n_seqs);
+
 kda_status kda_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                            int64_t v_stride, int64_t q_rows, int64_t k_rows, int q_heads, int kv_heads, int dim,
                            int dim_v, const int32_t *cu_seqlens, const int32_t *cu_seqlens_k, int n_seqs, float scale,
-                           void *o, kda_dtype o_dtype, float *lse, void *stream);
+                           void *o, kda_dtype o_dtype, float *lse, void *workspace, size_t workspace_bytes,
+                           void *stream);
 
 #ifdef __cplusplus
 }

@@ -33,7 +33,7 @@ __all__ = ["chunk_fwd", "chunk_fwd_logits", "recurrent_fwd", "recurrent_step", "
            "gated_rmsnorm", "short_conv", "o_proj", "launch_count", "device_status", "set_wait_limit",
            "workspace_size", "release_workspaces", "prepass_hits",
            "KVCache", "kv_cache", "rotary_inv_freq", "rotary", "kv_append", "attn_decode", "attn_decode_workspace_size",
-           "attn_prompt",
+           "attn_prompt", "attn_prompt_workspace_size",
            "library_path", "KDAError", "MODE_AUTO", "MODE_TENSOR", "MODE_FP32", "MODE_SPLIT"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -106,7 +106,9 @@ def _load():
         lib.kda_attn_decode.argtypes = [P, L, P, P, P, P, I, I, P, I, P, I, I, I, I, F, P, I, P, P, Z, P]
         lib.kda_attn_decode_workspace_size.argtypes = [I, I, I, I, L]
         lib.kda_attn_decode_workspace_size.restype = Z
-        lib.kda_attn_prompt.argtypes = [P, L, P, L, P, L, L, L, I, I, I, I, P, P, I, F, P, I, P, P]
+        lib.kda_attn_prompt.argtypes = [P, L, P, L, P, L, L, L, I, I, I, I, P, P, I, F, P, I, P, P, Z, P]
+        lib.kda_attn_prompt_workspace_size.argtypes = [L, L, I, I, I, I]
+        lib.kda_attn_prompt_workspace_size.restype = Z
         for fn in ("kda_rotary", "kda_kv_append", "kda_attn_decode", "kda_attn_prompt"):
             getattr(lib, fn).restype = ctypes.c_int
         lib.kda_device_status.argtypes = [P]
@@ -872,8 +874,15 @@ def attn_decode(q, cache, block_table, seq_lens, *, scale=None, out_dtype=torch.
     return (o, lse) if return_lse else o
 
 
+def attn_prompt_workspace_size(q_rows, k_rows, q_heads, kv_heads, dim_v, n_seqs=1) -> int:
+    """Bytes of workspace with which one attn_prompt call divides its keys among more CTAs; 0
+    where it would not."""
+    return int(_load().kda_attn_prompt_workspace_size(int(q_rows), int(k_rows), int(q_heads), int(kv_heads), int(dim_v),
+                                                      int(n_seqs)))
+
+
 def attn_prompt(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, scale=None, out_dtype=torch.bfloat16, return_lse=False,
-                o=None):
+                o=None, workspace="auto"):
     """Causal attention over whole prompts: q [T, q_heads, D], k [S, kv_heads, D],
     v [S, kv_heads, DV] bf16 (rows may be strided), (D, DV) one of (64, 64), (128, 128),
     (192, 128); query head h reads key/value head h // (q_heads // kv_heads).
@@ -884,7 +893,12 @@ def attn_prompt(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, scale=None, out_
     i + 1 + (keys - queries) keys: more keys than queries continue a context, and a row that
     sees nothing is zero.  scale: default D^-0.5.  Returns o like q with DV channels or, with
     return_lse, (o, lse) with lse the fp32 log-sum-exp of each row's scores.  Host tensors are
-    copied to the device and the results back."""
+    copied to the device and the results back.
+
+    With few rows and heads the keys are divided among CTAs, whose sums go through a workspace:
+    "auto" takes it from torch's allocator for the call; a uint8 tensor of
+    attn_prompt_workspace_size(...) bytes is used for this call alone; None goes through every
+    row's keys in one go."""
     lib = _lib or _load()
     if not q.is_cuda:
         dev = _device_of(k, v, cu_seqlens, cu_seqlens_k)
@@ -922,7 +936,19 @@ def attn_prompt(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, scale=None, out_
     elif o.shape != shape:
         raise ValueError("o must be like q with v's channels")
     lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device) if return_lse else None
+    ws, need = None, 0
+    if workspace is not None:
+        need = lib.kda_attn_prompt_workspace_size(T, S, Hq, Hk, DV, N)
+        if isinstance(workspace, torch.Tensor):
+            if workspace.get_device() != index or not workspace.is_contiguous():
+                raise ValueError("workspace must be a contiguous tensor on q's device")
+            ws, need = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        elif workspace != "auto":
+            raise ValueError('workspace must be "auto", None or a device tensor')
+        elif need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            ws = workspace.data_ptr()
     _call(lib.kda_attn_prompt, index, qp, qs, kp, ks, vp, vs, T, S, Hq, Hk, D, DV, cu, cuk, N,
           D ** -0.5 if scale is None else float(scale), _dense(o, "o", o.dtype, len(shape), index), _dt(o),
-          None if lse is None else lse.data_ptr())
+          None if lse is None else lse.data_ptr(), ws, need)
     return (o, lse) if return_lse else o

@@ -951,10 +951,18 @@ kda_status kda_attn_decode(const void *q, int64_t q_stride, const void *k_cache,
     return kda::launch_attn_decode(p, (cudaStream_t)stream);
 }
 
+size_t kda_attn_prompt_workspace_size(int64_t q_rows, int64_t k_rows, int q_heads, int kv_heads, int dim_v, int n_seqs) {
+    if (q_rows <= 0 || q_rows > (1 << 30) || k_rows < 0 || k_rows > (1 << 30) || q_heads <= 0 || q_heads > 65535 ||
+        kv_heads <= 0 || q_heads % kv_heads != 0 || n_seqs <= 0 || n_seqs > 16384 || (dim_v != 64 && dim_v != 128))
+        return 0;
+    return kda::attn_prompt_workspace_bytes(q_rows, k_rows, n_seqs, q_heads, kv_heads, dim_v);
+}
+
 kda_status kda_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                            int64_t v_stride, int64_t q_rows, int64_t k_rows, int q_heads, int kv_heads, int dim,
                            int dim_v, const int32_t *cu_seqlens, const int32_t *cu_seqlens_k, int n_seqs, float scale,
-                           void *o, kda_dtype o_dtype, float *lse, void *stream) {
+                           void *o, kda_dtype o_dtype, float *lse, void *workspace, size_t workspace_bytes,
+                           void *stream) {
     kda::g_err[0] = 0;
     const char *fn = "kda_attn_prompt";
     KDA_REQUIRE(q_rows >= 0 && k_rows >= 0 && q_heads > 0 && kv_heads > 0 && n_seqs >= 0, KDA_ERR_INVALID_ARG,
@@ -990,14 +998,21 @@ kda_status kda_attn_prompt(const void *q, int64_t q_stride, const void *k, int64
         KDA_REQUIRE(aligned16(ptr), KDA_ERR_INVALID_ARG, "%s: q, k, v and o must be 16-byte aligned", fn);
     KDA_REQUIRE(aligned_to(lse, 4) && aligned_to(cu_seqlens, 4) && aligned_to(cu_seqlens_k, 4), KDA_ERR_INVALID_ARG,
                 "%s: lse and cu_seqlens must be 4-byte aligned", fn);
+    KDA_REQUIRE(aligned16(workspace), KDA_ERR_INVALID_ARG, "%s: the workspace must be 16-byte aligned", fn);
+    if (q_rows == 0) return KDA_OK;
+    const size_t need = kda::attn_prompt_workspace_bytes(q_rows, k_rows, n_seqs, q_heads, kv_heads, dim_v);
+    KDA_REQUIRE(!workspace || workspace_bytes >= need, KDA_ERR_INVALID_ARG,
+                "%s: the workspace holds %zu bytes, this call uses %zu (kda_attn_prompt_workspace_size)", fn,
+                workspace_bytes, need);
     const size_t cu_bytes = ((size_t)n_seqs + 1) * 4;
     const Span in[] = {{q, strided_bytes(q_rows, qr, q_stride, 2), "q"},
                        {k, strided_bytes(k_rows, kr, k_stride, 2), "k"},
                        {v, strided_bytes(k_rows, vr, v_stride, 2), "v"},
                        {cu_seqlens, cu_bytes, "cu_seqlens"},
                        {cu_seqlens_k, cu_bytes, "cu_seqlens_k"}};
-    const Span out[] = {{o, (size_t)q_rows * orow * esize(o_dtype), "o"}, {lse, (size_t)q_rows * q_heads * 4, "lse"}};
-    if ((s = check_apart(fn, in, 5, out, 2)) != KDA_OK) return s;
+    const Span out[] = {{o, (size_t)q_rows * orow * esize(o_dtype), "o"}, {lse, (size_t)q_rows * q_heads * 4, "lse"},
+                        {workspace, need, "the workspace"}};
+    if ((s = check_apart(fn, in, 5, out, 3)) != KDA_OK) return s;
     kda::PromptParams p;
     p.q = static_cast<const __nv_bfloat16 *>(q);
     p.k = static_cast<const __nv_bfloat16 *>(k);
@@ -1018,6 +1033,7 @@ kda_status kda_attn_prompt(const void *q, int64_t q_stride, const void *k, int64
     p.o = o;
     p.o_bf16 = o_dtype == KDA_BF16;
     p.lse = lse;
+    p.ws = need ? static_cast<float *>(workspace) : nullptr;
     p.polls = std::min(kda::wait_polls(), kda::kAttnPolls);
     return kda::launch_attn_prompt(p, (cudaStream_t)stream);
 }

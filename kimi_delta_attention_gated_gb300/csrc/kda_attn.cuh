@@ -72,6 +72,7 @@ struct PromptParams {
     void *o;                         // [Tq, Hq, DV]
     int o_bf16;
     float *lse;                      // [Tq, Hq] or null
+    float *ws;                       // sums of parts of the keys, or null: every row's keys in one go
     uint32_t polls;                  // bound on the copies' waits
 };
 
@@ -81,6 +82,7 @@ kda_status launch_kv_append(const AppendParams &p, cudaStream_t st);
 size_t attn_decode_workspace_bytes(int64_t N, int Hq, int Hk, int D, int64_t max_tokens);
 kda_status launch_attn_decode(const DecodeParams &p, cudaStream_t st);
 kda_status launch_attn_prompt(const PromptParams &p, cudaStream_t st);
+size_t attn_prompt_workspace_bytes(int64_t Tq, int64_t Tk, int N, int Hq, int Hk, int DV);
 int take_attn_prompt_timeouts(cudaStream_t st);
 int take_attn_decode_timeouts(cudaStream_t st);
 

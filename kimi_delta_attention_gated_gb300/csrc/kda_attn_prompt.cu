@@ -36,6 +36,8 @@
 #include <cuda.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "kda_attn.cuh"
 #include "kda_chunk_common.cuh"
 #include "kda_tc_ptx.cuh"
@@ -76,6 +78,7 @@ struct Args {
     int pair_heads;  // 1: two heads of a group share their rows; 0: 256 rows of one head
     int n_heads;     // work items per unit: head pairs, or heads
     int items;       // work items at most
+    int parts;       // work items of a unit and head, each with its share of the key blocks
 };
 
 // Query and key rows of a sequence.
@@ -85,7 +88,12 @@ struct Seq {
 struct Item {
     Seq s;
     int found, row0, head;  // head: number of the pair, or of the head
+    int lo, hi, place;      // in the form with parts: its key blocks [lo, hi), and where its sums go
 };
+
+// What a part leaves in the workspace: the 2 x 128 rows' O, their m and their l.
+template <int DV>
+constexpr int kPartFloats = 2 * kTile * (DV + 2);
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *r) {
     asm volatile(
@@ -348,11 +356,11 @@ __device__ __forceinline__ void weights32(float *y, float c, float m, float2 (&s
     }
 }
 
-// One row computed alone, without what it does not see: m and l are its softmax's (they never
-// include masked scores).  Taken only where a NaN came out and a masked value is not finite.
+// One row computed alone, without what it does not see, over the keys [from, seen): m and l are
+// its softmax's (they never include masked scores).  part: where a part's sums go, or null.  Taken only where a NaN came out and a masked value is not finite.
 template <int D, int DV>
-__device__ __noinline__ void rescue_row(const PromptParams &p, const Seq &s, int row, int head, int seen, int blocks,
-                                        float m, float l, float c) {
+__device__ __noinline__ void rescue_row(const PromptParams &p, const Seq &s, int row, int head, int from, int seen,
+                                        int blocks, float m, float l, float c, float *part) {
     const int kvh = head / (p.Hq / p.Hk);
     const __nv_bfloat16 *v0 = p.v + (int64_t)s.k0 * p.v_stride + (int64_t)kvh * DV;
     bool masked_bad = false;
@@ -361,10 +369,10 @@ __device__ __noinline__ void rescue_row(const PromptParams &p, const Seq &s, int
     if (!masked_bad) return;  // the NaN comes from what the row sees
     const __nv_bfloat16 *q = p.q + (int64_t)(s.q0 + row) * p.q_stride + (int64_t)head * D;
     const __nv_bfloat16 *k0 = p.k + (int64_t)s.k0 * p.k_stride + (int64_t)kvh * D;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
     for (int d0 = 0; d0 < DV; d0 += 16) {
         float acc[16] = {};
-        for (int j = 0; j < seen; ++j) {
+        for (int j = from; j < seen; ++j) {
             float dot = 0.f;
             for (int d = 0; d < D; ++d) dot = fmaf(__bfloat162float(q[d]), __bfloat162float(k0[j * p.k_stride + d]), dot);
             const float w = ex2(fmaf(dot, c, -m));
@@ -372,12 +380,16 @@ __device__ __noinline__ void rescue_row(const PromptParams &p, const Seq &s, int
             for (int d = 0; d < 16; ++d) acc[d] = fmaf(w, __bfloat162float(v0[j * p.v_stride + d0 + d]), acc[d]);
         }
 #pragma unroll
-        for (int d = 0; d < 16; ++d)
-            st_out(p.o, ((int64_t)(s.q0 + row) * p.Hq + head) * DV + d0 + d, acc[d] * inv, p.o_bf16);
+        for (int d = 0; d < 16; ++d) {
+            if (part)
+                part[d0 + d] = acc[d];
+            else
+                st_out(p.o, ((int64_t)(s.q0 + row) * p.Hq + head) * DV + d0 + d, acc[d] * inv, p.o_bf16);
+        }
     }
 }
 
-template <int D, int DV>
+template <int D, int DV, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Args a) {
@@ -398,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);  // a bounded wait gave up
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    if (SPLIT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0 && lane == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, 1);
@@ -446,13 +459,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait_copy = [&](uint64_t *bar, uint32_t parity) { return wait_for(bar, parity, p.polls); };
     // The same where the warp's lanes have to go on or stop together.
     auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    auto tile_row = [&](const Item &it, int t) { return a.pair_heads ? it.row0 : it.row0 + t * kTile; };
+    // Key blocks of an item that its tile t sees.
+    auto tile_blocks = [&](const Item &it, const Seq &s, int t) {
+        const int r = tile_row(it, t), last = min(r + kTile, s.nq) - 1;
+        if (r >= s.nq) return 0;
+        const int seen = max(0, min(s.nk, last + 1 + (s.nk - s.nq)));
+        const int n = (seen + kTile - 1) / kTile;
+        return SPLIT ? max(0, min(n, it.hi) - it.lo) : n;
+    };
     // This CTA's k-th work item; one warp.
     auto find_item = [&](UnitSearch &units, int k) {
         const int64_t i = (int64_t)k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        Item it = {{0, 0, 0, 0}, 0, 0, (int)i % a.n_heads};
+        const int u = SPLIT ? (int)i / a.parts : (int)i, part = SPLIT ? (int)i - u * a.parts : 0;
+        Item it = {{0, 0, 0, 0}, 0, 0, u % a.n_heads, 0, INT_MAX, (int)i};
         int seq = 0;
-        if (i < a.items) it.found = units.find(p, a.pair_heads ? 7 : 8, (int)i / a.n_heads, seq, it.row0);
+        if (i < a.items) it.found = units.find(p, a.pair_heads ? 7 : 8, u / a.n_heads, seq, it.row0);
         if (it.found) it.s = seq_of(p, seq);
+        if (SPLIT && it.found) {
+            const int nb = max(tile_blocks(it, it.s, 0), tile_blocks(it, it.s, 1));
+            it.lo = (int)((int64_t)nb * part / a.parts);
+            it.hi = (int)((int64_t)nb * (part + 1) / a.parts);
+        }
         return it;
     };
     // The same from the item warp, for a warp that follows them all; false when a wait gave up.
@@ -467,15 +495,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         leave_item(k);
         return true;
     };
-    auto tile_row = [&](const Item &it, int t) { return a.pair_heads ? it.row0 : it.row0 + t * kTile; };
-    // Key blocks that tile t of an item sees.
-    auto tile_blocks = [&](const Item &it, const Seq &s, int t) {
-        const int r = tile_row(it, t), last = min(r + kTile, s.nq) - 1;
-        if (r >= s.nq) return 0;
-        const int seen = max(0, min(s.nk, last + 1 + (s.nk - s.nq)));
-        return (seen + kTile - 1) / kTile;
-    };
-
     // The softmax keeps 128 scores and what goes with them in registers: it takes some over from
     // the other warps (with 168 each some were spilled).
     if (warp >= kMmaWarp) {
@@ -509,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok || !it.found) break;
                 const Seq s = it.s;
                 const int head0 = a.pair_heads ? 2 * it.head : it.head, kvh = head0 / group;
-                const int n0 = tile_blocks(it, s, 0), n1 = tile_blocks(it, s, 1), nb = max(n0, n1);
+                const int n0 = tile_blocks(it, s, 0), n1 = tile_blocks(it, s, 1), nb = max(n0, n1), j0 = SPLIT ? it.lo : 0;
                 auto load_q = [&](int t) {
                     if (nq_issued[t] > 0 && !wait(q_empty + t, (nq_issued[t] - 1) & 1)) return false;
                     mbar_arrive_expect_tx(q_full + t, L::QB);
@@ -527,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int x = 0; x < D; x += 64)
                         tma_load_hint(sb + L::K + st * L::KB + (x / 64) * kTile * 128, &map_k, k_full + st, x, kvh,
-                                      s.k0 + j * kTile, again);
+                                      s.k0 + (j0 + j) * kTile, again);
                     ++nk_issued;
                     return true;
                 };
@@ -536,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int x = 0; x < DV; x += 64)
                         tma_load_hint(sb + L::V + st * L::VB + (x / 64) * L::VROWS * 128, &map_v, bar, x, kvh,
-                                      s.k0 + j * kTile + h * L::VROWS, again);
+                                      s.k0 + (j0 + j) * kTile + h * L::VROWS, again);
                 };
                 auto v_free = [&](int st) { return nv_issued < L::VST || wait(v_empty + st, (nv_issued / L::VST - 1) & 1); };
                 if (lane == 0) {
@@ -558,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 nv_issued = __shfl_sync(0xffffffffu, nv_issued, 0);
                 for (int h = 0; h < L::NV && nb > 0 && ok; ++h) {
                     const int st = nv_issued % L::VST;
-                    const int rows = max(0, s.nk - (nb - 1) * kTile - h * L::VROWS);  // of the sequence
+                    const int rows = max(0, s.nk - (j0 + nb - 1) * kTile - h * L::VROWS);  // of the sequence
                     ok = __all_sync(0xffffffffu, v_free(st)) != 0;
                     if (!ok) break;
                     if (lane == 0) issue_v(nb - 1, h, st, rows < L::VROWS ? v_raw : v_full + st);
@@ -715,6 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 nt = tile_blocks(it, it.s, t);
                 seen = max(0, min(it.s.nk, row + 1 + more));
                 seen_first = max(0, min(it.s.nk, row0 + 1 + more));  // of the tile's first row
+                if (SPLIT) seen -= it.lo * kTile, seen_first -= it.lo * kTile;  // keys of this part
             }
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < nt; ++j, ++blocks) {
@@ -783,22 +803,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool more = !ok || see_item(k + 1);
             const bool live = row < s.nq;
             const int64_t out = (int64_t)(s.q0 + row) * p.Hq + head;
-            float inv = l == 0.f ? 0.f : 1.f / l, lse = l == 0.f ? -INFINITY : (log2f(l) + m) * kLn2;
+            float inv = SPLIT ? 1.f : l == 0.f ? 0.f : 1.f / l, lse = l == 0.f ? -INFINITY : (log2f(l) + m) * kLn2;
             // Four lanes exchange 16-byte pieces of their rows, so that they write 64 bytes of a row
             // together (lanes writing a row each touch 32 lines per store).
             const int first = row0 + (warp & 3) * 32 + (lane & ~3);  // of the four rows
-            const int esz = p.o_bf16 ? 2 : 4;
-            uint8_t *o_rows = static_cast<uint8_t *>(p.o) + ((int64_t)(s.q0 + first) * p.Hq + head) * DV * esz + (lane & 3) * 16;
-            const int64_t pitch = (int64_t)p.Hq * DV * esz;
+            float *part = SPLIT ? a.p.ws + (int64_t)it.place * kPartFloats<DV> : nullptr;
+            const bool bf16 = !SPLIT && p.o_bf16;
+            const int esz = bf16 ? 2 : 4;
+            uint8_t *o_rows = SPLIT ? reinterpret_cast<uint8_t *>(part + (t * kTile + first - row0) * DV) + (lane & 3) * 16
+                                    : static_cast<uint8_t *>(p.o) + ((int64_t)(s.q0 + first) * p.Hq + head) * DV * esz + (lane & 3) * 16;
+            const int64_t pitch = (int64_t)(SPLIT ? 1 : p.Hq) * DV * esz;
             if (ok && nt > 0) ok = wait_all(o_full + t, tiles & 1);
             tiles += nt > 0;
             fence_after_sync();
-            if (!ok) inv = lse = __int_as_float(0x7fc00000);
+            if (!ok) inv = lse = l = __int_as_float(0x7fc00000);
             if (row0 + (warp & 3) * 32 < s.nq) {  // (else the warp has no such rows)
                 const float2 inv2 = make_float2(inv, inv), zero = make_float2(0.f, 0.f);
                 float2 odd[4] = {zero, zero, zero, zero};  // 0, or NaN where an output is not finite
 #pragma unroll 1
-                for (int d = 0; d < DV; d += 64) {
+                for (int d = SPLIT && nt == 0 ? DV : 0; d < DV; d += 64) {
                     float r[64];
                     if (ok && nt > 0) {
                         tmem_ld32(t_o + d, r);
@@ -819,12 +842,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         transpose_quad(w);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (first + i < s.nq)
-                                __stcs(reinterpret_cast<uint4 *>(o_rows + i * pitch + byte),
-                                       make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+                            if (first + i < s.nq) {
+                                const uint4 x = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                                uint4 *at = reinterpret_cast<uint4 *>(o_rows + i * pitch + byte);
+                                if (SPLIT)
+                                    *at = x;
+                                else
+                                    __stcs(at, x);
+                            }
                     };
                     uint32_t w[16];
-                    if (p.o_bf16) {
+                    if (bf16) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -842,9 +870,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (live) {
-                    if (p.lse) p.lse[out] = lse;
+                    if (SPLIT) {
+                        part[2 * kTile * DV + t * kTile + m_row] = m;
+                        part[2 * kTile * (DV + 1) + t * kTile + m_row] = l;
+                    } else if (p.lse) {
+                        p.lse[out] = lse;
+                    }
                     const float2 any = add2(add2(odd[0], odd[1]), add2(odd[2], odd[3]));
-                    if (isnan(any.x + any.y) && ok) rescue_row<D, DV>(p, s, row, head, seen, nt, m, l, copysignf(c, p.scale));
+                    const int from = SPLIT ? it.lo * kTile : 0;
+                    if (isnan(any.x + any.y) && ok)
+                        rescue_row<D, DV>(p, s, row, head, from, from + seen, from / kTile + nt, m, l, copysignf(c, p.scale),
+                                          SPLIT ? part + (t * kTile + m_row) * DV : nullptr);
                 }
             }
             ok = ok && more;
@@ -858,6 +894,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Seq s = it.s;
                 const int row = tile_row(it, t) + m_row, head = a.pair_heads ? 2 * it.head + t : it.head;
                 if (row >= s.nq) continue;
+                if (SPLIT) {
+                    float *part = a.p.ws + (int64_t)it.place * kPartFloats<DV> + 2 * kTile * DV + t * kTile + m_row;
+                    part[0] = 0.f;
+                    part[2 * kTile] = __int_as_float(0x7fc00000);
+                    continue;
+                }
                 const int64_t out = (int64_t)(s.q0 + row) * p.Hq + head;
                 for (int d = 0; d < DV; ++d) st_out(p.o, out * DV + d, __int_as_float(0x7fc00000), p.o_bf16);
                 if (p.lse) p.lse[out] = __int_as_float(0x7fc00000);
@@ -868,6 +910,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (__syncthreads_or(failed) && threadIdx.x == 0) atomicAdd(&g_attn_prompt_timeouts, 1);
     fence_after_sync();
     if (warp == kMmaWarp) tmem_dealloc(tb, 512);
+}
+
+// Joins the parts of a unit and head: 32 of their 2 x 128 rows a CTA, four channels a thread.
+constexpr int kJoinThreads = 256, kJoinRows = 32;
+template <int DV>
+__global__ void __launch_bounds__(kJoinThreads) attn_prompt_join_kernel(const __grid_constant__ Args a) {
+    const PromptParams &p = a.p;
+    __shared__ Seq s_seq;
+    __shared__ int s_row0;  // or -1
+    const int unit = blockIdx.x / a.n_heads, pair = blockIdx.x % a.n_heads;
+    if (threadIdx.x < 32) {
+        UnitSearch units;
+        int seq = 0, row0 = 0;
+        const bool found = units.find(p, a.pair_heads ? 7 : 8, unit, seq, row0);
+        const Seq s = seq_of(p, seq);
+        if (threadIdx.x == 0) {
+            s_seq = s;
+            s_row0 = found ? row0 : -1;
+        }
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (s_row0 < 0) return;
+    constexpr int LANES = DV / 4;  // of a row
+    const int d = threadIdx.x % LANES * 4;
+    for (int r0 = 0; r0 < kJoinRows; r0 += kJoinThreads / LANES) {
+        const int r = blockIdx.y * kJoinRows + r0 + threadIdx.x / LANES, t = r / kTile;
+        const int row = s_row0 + (a.pair_heads ? r % kTile : r), head = a.pair_heads ? 2 * pair + t : pair;
+        if (row >= s_seq.nq) continue;
+        const float *part = p.ws + (int64_t)blockIdx.x * a.parts * kPartFloats<DV>;
+        float M = -INFINITY, L = 0.f;
+        for (int i = 0; i < a.parts; ++i) M = fmaxf(M, part[(int64_t)i * kPartFloats<DV> + 2 * kTile * DV + r]);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < a.parts; ++i) {
+            const float *x = part + (int64_t)i * kPartFloats<DV>;
+            const float l = x[2 * kTile * (DV + 1) + r];
+            if (l == 0.f) continue;  // the part saw nothing, and may have left no O
+            const float f = ex2(x[2 * kTile * DV + r] - M);
+            const float4 y = *reinterpret_cast<const float4 *>(x + r * DV + d);
+            L = fmaf(l, f, L);
+            o.x = fmaf(y.x, f, o.x);
+            o.y = fmaf(y.y, f, o.y);
+            o.z = fmaf(y.z, f, o.z);
+            o.w = fmaf(y.w, f, o.w);
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const int64_t out = (int64_t)(s_seq.q0 + row) * p.Hq + head;
+        if (p.o_bf16)
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.o) + out * DV + d) =
+                make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        else
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + out * DV + d) =
+                make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (p.lse && d == 0) p.lse[out] = L == 0.f ? -INFINITY : (log2f(L) + M) * kLn2;
+    }
 }
 
 // A tensor of rows (heads of `dim` bf16 elements, `stride` elements from row to row) in boxes
@@ -884,8 +981,43 @@ bool encode(chunk::EncodeTiledFn enc, CUtensorMap *map, const void *base, int di
     return r == CUDA_SUCCESS;
 }
 
-template <int D, int DV>
-kda_status run(const PromptParams &p, cudaStream_t st) {
+struct Shape {
+    int pair_heads, n_heads, parts;
+    int64_t units;  // at most: a sequence of n rows has at most n / rows + 1
+};
+
+// Work items of a call, and how many share the keys of a unit and head.  With few units the
+// longest alone would set the time, and most SMs would idle; each part costs an item's beginning and
+// end (about 2.5 blocks of 128 keys) and the joining launch (about 3.5).  The number of parts with
+// the least estimate for sequences of equal lengths is taken, for at most three items an SM.
+// Two heads over 4096 tokens, channels 128: 50 us whole, XXX in parts.
+Shape shape_of(int64_t Tq, int64_t Tk, int N, int Hq, int Hk) {
+    Shape x;
+    x.pair_heads = (Hq / Hk) % 2 == 0;
+    x.n_heads = x.pair_heads ? Hq / 2 : Hq;
+    x.parts = 1;
+    const int rows = x.pair_heads ? kTile : 2 * kTile, sms = sm_count();
+    x.units = Tq / rows + N;
+    const int64_t q = Tq / N, k = Tk / N, per = (q + rows - 1) / rows, items = per * N * x.n_heads;
+    if (items * 2 > 3 * sms || k <= kTile) return x;
+    double total = 0, best = 0;  // in key blocks
+    int64_t longest = 0;
+    for (int64_t u = 0; u < per; ++u) {
+        const int64_t seen = std::min(q, (u + 1) * rows) + k - q, n = seen > 0 ? (seen + kTile - 1) / kTile : 0;
+        total += (double)n * N * x.n_heads;
+        longest = std::max(longest, n);
+    }
+    for (int s = 1; s <= 32 && s <= longest && (s == 1 || x.units * x.n_heads * s <= 3 * sms); ++s) {
+        const int64_t rounds = (items * s + sms - 1) / sms;
+        const double run = std::max((double)((longest + s - 1) / s), (rounds > 1 ? 1.2 : 1.0) * total / sms);
+        const double t = 2.5 * rounds + run + (s > 1 ? 3.5 : 0.0);
+        if (s == 1 || t < best) best = t, x.parts = s;
+    }
+    return x;
+}
+
+template <int D, int DV, bool SPLIT>
+kda_status launch(const PromptParams &p, const Shape &shape, cudaStream_t st) {
     using L = Cfg<D, DV>;
     chunk::EncodeTiledFn enc = reinterpret_cast<chunk::EncodeTiledFn>(tensor_map_encoder());
     if (!enc) {
@@ -894,14 +1026,14 @@ kda_status run(const PromptParams &p, cudaStream_t st) {
     }
     static DeviceOnce configured;
     const int dev = current_device();
+    const auto kernel = attn_prompt_kernel<D, DV, SPLIT>;
     if (!configured.done(dev)) {
-        if (cudaFuncSetAttribute(attn_prompt_kernel<D, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) !=
-            cudaSuccess) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess) {
             set_error("attn_prompt: cannot reserve shared memory: %s", cudaGetErrorString(cudaGetLastError()));
             return KDA_ERR_CUDA;
         }
         cudaFuncAttributes attr;
-        if (cudaFuncGetAttributes(&attr, attn_prompt_kernel<D, DV>) != cudaSuccess || attr.numRegs < kLaunchRegs) {
+        if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess || attr.numRegs < kLaunchRegs) {
             cudaGetLastError();
             set_error("attn_prompt: built with fewer registers than its warps share out");
             return KDA_ERR_CUDA;
@@ -919,19 +1051,43 @@ kda_status run(const PromptParams &p, cudaStream_t st) {
     Args a;
     memset(&a, 0, sizeof(a));
     a.p = p;
-    a.pair_heads = (p.Hq / p.Hk) % 2 == 0;
-    a.n_heads = a.pair_heads ? p.Hq / 2 : p.Hq;
-    // A sequence of n rows has at most n / rows + 1 units.
-    const int64_t items = (p.Tq / (a.pair_heads ? kTile : 2 * kTile) + p.N) * a.n_heads;
+    a.pair_heads = shape.pair_heads;
+    a.n_heads = shape.n_heads;
+    a.parts = SPLIT ? shape.parts : 1;
+    const int64_t items = shape.units * a.n_heads * a.parts;
     if (items > INT32_MAX) {
         set_error("kda_attn_prompt: too many tokens");
         return KDA_ERR_UNSUPPORTED;
     }
     a.items = (int)items;
     const int sms = sm_count();
-    attn_prompt_kernel<D, DV><<<a.items < sms ? a.items : sms, kThreads, L::SMEM, st>>>(mq, mk, mv, a);
+    kernel<<<a.items < sms ? a.items : sms, kThreads, L::SMEM, st>>>(mq, mk, mv, a);
     note_launch();
-    return check_launch("attn_prompt_kernel");
+    const kda_status s = check_launch("attn_prompt_kernel");
+    if (!SPLIT || s != KDA_OK) return s;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.items / a.parts, 2 * kTile / kJoinRows);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];  // starts while the first kernel ends; waits for it before it reads
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_prompt_join_kernel<DV>, a);
+    note_launch();
+    if (e != cudaSuccess) {
+        set_error("attn_prompt_join_kernel: %s", cudaGetErrorString(e));
+        cudaGetLastError();
+        return KDA_ERR_CUDA;
+    }
+    return check_launch("attn_prompt_join_kernel");
+}
+
+template <int D, int DV>
+kda_status run(const PromptParams &p, cudaStream_t st) {
+    const Shape shape = shape_of(p.Tq, p.Tk, p.N, p.Hq, p.Hk);
+    return p.ws && shape.parts > 1 ? launch<D, DV, true>(p, shape, st) : launch<D, DV, false>(p, shape, st);
 }
 
 }  // namespace
@@ -948,6 +1104,11 @@ int take_attn_prompt_timeouts(cudaStream_t st) {
         return -1;
     }
     return n;
+}
+
+size_t attn_prompt_workspace_bytes(int64_t Tq, int64_t Tk, int N, int Hq, int Hk, int DV) {
+    const Shape x = shape_of(Tq, Tk, N, Hq, Hk);
+    return x.parts == 1 ? 0 : (size_t)(x.units * x.n_heads * x.parts) * (2 * kTile * (DV + 2)) * sizeof(float);
 }
 
 kda_status launch_attn_prompt(const PromptParams &p, cudaStream_t st) {

@@ -117,14 +117,15 @@ def test_decode_workspace(lib):
 
 def prompt(lib, **over):
     a = dict(q=fake(0), qs=512, k=fake(1), ks=256, v=fake(2), vs=256, Tq=8, Tk=8, Hq=4, Hk=2, D=128, DV=128, cu=fake(3),
-             cuk=None, N=2, scale=0.1, o=fake(4), dt=BF16, lse=fake(5))
+             cuk=None, N=2, scale=0.1, o=fake(4), dt=BF16, lse=fake(5), ws=None, wsb=0)
     a.update(over)
     return lib.kda_attn_prompt(*(a[k] for k in ("q", "qs", "k", "ks", "v", "vs", "Tq", "Tk", "Hq", "Hk", "D", "DV", "cu", "cuk",
-                                                "N", "scale", "o", "dt", "lse")), None)
+                                                "N", "scale", "o", "dt", "lse", "ws", "wsb")), None)
 
 
 @pytest.mark.parametrize("over,code", [
     (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(o=None), INVALID),
+    (dict(ws=fake(7) + 4), INVALID),
     (dict(D=192), INVALID),                                # 192/128 is built; the strides do not fit it
     (dict(D=64), UNSUPPORTED), (dict(DV=64), UNSUPPORTED), (dict(D=96, DV=96), UNSUPPORTED), (dict(Hq=3), INVALID),
     (dict(Hq=0), INVALID), (dict(Tq=-1), INVALID), (dict(Tk=9), INVALID), (dict(cu=None, cuk=fake(6)), INVALID),
@@ -136,6 +137,15 @@ def prompt(lib, **over):
 def test_prompt_refuses(lib, over, code):
     assert prompt(lib, **over) == code
     assert lib.kda_last_error()
+
+
+def test_prompt_workspace(lib):
+    size = lib.kda_attn_prompt_workspace_size
+    for bad in ((0, 8, 4, 2, 128, 1), (8, -1, 4, 2, 128, 1), (8, 8, 5, 2, 128, 1), (8, 8, 4, 2, 96, 1), (8, 8, 4, 2, 128, 0)):
+        assert size(*bad) == 0
+    assert size(100, 100, 8, 2, 64, 1) == 0          # one block of keys
+    assert size(8192, 8192, 32, 8, 128, 1) == 0      # work items enough
+    assert size(5, 5, 1, 1, 64, 10) == 0             # fewer rows than sequences
 
 
 def test_inv_freq_scalings():

@@ -2,7 +2,9 @@
 per output: the weights' rounding to bf16 (half a step, relative to sum p |v|), one rounding to the
 output's type, and the scores' fp32 accumulation, whose error moves every weight: at most 2^-20 of
 the largest sum |q||k| * scale (192 products, each accumulation step losing at most two units of
-2^-24 of the running size; the exponential's argument is held to 2^-22 of the score)."""
+2^-24 of the running size; the exponential's argument is held to 2^-22 of the score).  Where the keys
+are divided, the sums of at most 32 parts are joined in fp32: a factor within 2^-22 and 33 roundings,
+37 * 2^-24 of sum p |v|."""
 import math
 
 import pytest
@@ -50,6 +52,7 @@ def verify(o, lse, q, k, v, nq, nk, scale=None, heads=None, rows=None):
             want, wl, av, size = ref.attend(ref.f64(q[sel, h]), ref.f64(k[k0:k0 + b, h // G]), ref.f64(v[k0:k0 + b, h // G]),
                                             scale, (at + 1 + b - a).tolist())
             moved = 2.0 ** -20 * size + 2.0 ** -20
+            moved = moved + 37 * 2.0 ** -24
             tol = (ref.HALF_BF16 + 2 * moved)[:, None] * av
             tol = tol + (ref.HALF_BF16 if o.dtype == torch.bfloat16 else 2.0 ** -20) * want.abs()
             ref.check(f"o[{n}, head {h}]", o[sel, h], want, tol)
@@ -191,7 +194,10 @@ def test_same_bits_again_on_another_stream_and_from_a_graph():
     cu.copy_(cum([0, 1000]))
     graph.replay()
     torch.cuda.synchronize()
-    assert torch.equal(out, o)
+    # (how the keys are divided goes by the number of sequences, so the eager call is one of two as well)
+    assert torch.equal(out, kda.attn_prompt(q, k, v, cu_seqlens=cu))
+    whole = kda.attn_prompt(q, k, v, cu_seqlens=cu, workspace=None)
+    assert torch.equal(whole, kda.attn_prompt(q, k, v, workspace=None))
 
 
 def test_two_calls_at_once():
