@@ -912,10 +912,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) tmem_dealloc(tb, 512);
 }
 
-// Joins the parts of a unit and head: 32 of their 2 x 128 rows a CTA, four channels a thread.
-constexpr int kJoinThreads = 256, kJoinRows = 32;
+// Joins the parts of a unit and head: `rows` of their 2 x 128 rows a CTA, four channels a thread;
+// four parts are on their way at a time (one after the other, 8 parts took 15 us).
+constexpr int kJoinThreads = 256;
 template <int DV>
-__global__ void __launch_bounds__(kJoinThreads) attn_prompt_join_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kJoinThreads) attn_prompt_join_kernel(const __grid_constant__ Args a, int rows) {
     const PromptParams &p = a.p;
     __shared__ Seq s_seq;
     __shared__ int s_row0;  // or -1
@@ -935,25 +936,39 @@ __global__ void __launch_bounds__(kJoinThreads) attn_prompt_join_kernel(const __
     if (s_row0 < 0) return;
     constexpr int LANES = DV / 4;  // of a row
     const int d = threadIdx.x % LANES * 4;
-    for (int r0 = 0; r0 < kJoinRows; r0 += kJoinThreads / LANES) {
-        const int r = blockIdx.y * kJoinRows + r0 + threadIdx.x / LANES, t = r / kTile;
+    const float *part = p.ws + (int64_t)blockIdx.x * a.parts * kPartFloats<DV>;
+    for (int r0 = 0; r0 < rows; r0 += kJoinThreads / LANES) {
+        const int r = blockIdx.y * rows + r0 + threadIdx.x / LANES, t = r / kTile;
         const int row = s_row0 + (a.pair_heads ? r % kTile : r), head = a.pair_heads ? 2 * pair + t : pair;
         if (row >= s_seq.nq) continue;
-        const float *part = p.ws + (int64_t)blockIdx.x * a.parts * kPartFloats<DV>;
         float M = -INFINITY, L = 0.f;
-        for (int i = 0; i < a.parts; ++i) M = fmaxf(M, part[(int64_t)i * kPartFloats<DV> + 2 * kTile * DV + r]);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < a.parts; ++i) {
-            const float *x = part + (int64_t)i * kPartFloats<DV>;
-            const float l = x[2 * kTile * (DV + 1) + r];
-            if (l == 0.f) continue;  // the part saw nothing, and may have left no O
-            const float f = ex2(x[2 * kTile * DV + r] - M);
-            const float4 y = *reinterpret_cast<const float4 *>(x + r * DV + d);
-            L = fmaf(l, f, L);
-            o.x = fmaf(y.x, f, o.x);
-            o.y = fmaf(y.y, f, o.y);
-            o.z = fmaf(y.z, f, o.z);
-            o.w = fmaf(y.w, f, o.w);
+        for (int i0 = 0; i0 < a.parts; i0 += 4) {
+            float m[4], l[4];
+            float4 y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float *x = part + (int64_t)(i0 + i) * kPartFloats<DV>;
+                const bool is = i0 + i < a.parts;
+                m[i] = is ? __ldcg(x + 2 * kTile * DV + r) : -INFINITY;
+                l[i] = is ? __ldcg(x + 2 * kTile * (DV + 1) + r) : 0.f;
+                y[i] = is ? __ldcg(reinterpret_cast<const float4 *>(x + r * DV + d)) : o;
+            }
+            const float next = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), M);
+            const float g = M == -INFINITY ? 1.f : ex2(M - next);  // (all zero so far)
+            M = next;
+            L *= g;
+            o = make_float4(o.x * g, o.y * g, o.z * g, o.w * g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (l[i] == 0.f) continue;  // the part saw nothing, and may have left no O
+                const float f = ex2(m[i] - M);
+                L = fmaf(l[i], f, L);
+                o.x = fmaf(y[i].x, f, o.x);
+                o.y = fmaf(y[i].y, f, o.y);
+                o.z = fmaf(y[i].z, f, o.z);
+                o.w = fmaf(y[i].w, f, o.w);
+            }
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
         const int64_t out = (int64_t)(s_seq.q0 + row) * p.Hq + head;
@@ -987,10 +1002,13 @@ struct Shape {
 };
 
 // Work items of a call, and how many share the keys of a unit and head.  With few units the
-// longest alone would set the time, and most SMs would idle; each part costs an item's beginning and
-// end (about 2.5 blocks of 128 keys) and the joining launch (about 3.5).  The number of parts with
-// the least estimate for sequences of equal lengths is taken, for at most three items an SM.
-// Two heads over 4096 tokens, channels 128: 50 us whole, XXX in parts.
+// longest alone would set the time, and most SMs would idle.  A part costs an item's beginning and
+// end (about 2.5 blocks of 128 keys), the joining launch (3.5), and its sums' way through L2 (0.012
+// for each part of the call).  The number of parts with the least estimate for sequences of equal
+// lengths is taken, for at most three items an SM.  Channels 128, whole and in parts:
+// 2 heads over one key head, 1024 tokens 16.8 and 12.2 us, 8192 tokens 88 and 36 us; 128 queries
+// over 4096 keys with 32/8 heads 48 and 18 us; 16/4 heads over 2048 tokens 27.7 and 30.8 us, which
+// the estimate leaves whole.
 Shape shape_of(int64_t Tq, int64_t Tk, int N, int Hq, int Hk) {
     Shape x;
     x.pair_heads = (Hq / Hk) % 2 == 0;
@@ -1010,7 +1028,7 @@ Shape shape_of(int64_t Tq, int64_t Tk, int N, int Hq, int Hk) {
     for (int s = 1; s <= 32 && s <= longest && (s == 1 || x.units * x.n_heads * s <= 3 * sms); ++s) {
         const int64_t rounds = (items * s + sms - 1) / sms;
         const double run = std::max((double)((longest + s - 1) / s), (rounds > 1 ? 1.2 : 1.0) * total / sms);
-        const double t = 2.5 * rounds + run + (s > 1 ? 3.5 : 0.0);
+        const double t = 2.5 * rounds + run + (s > 1 ? 3.5 + 0.012 * items * s : 0.0);
         if (s == 1 || t < best) best = t, x.parts = s;
     }
     return x;
@@ -1066,7 +1084,9 @@ kda_status launch(const PromptParams &p, const Shape &shape, cudaStream_t st) {
     const kda_status s = check_launch("attn_prompt_kernel");
     if (!SPLIT || s != KDA_OK) return s;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.items / a.parts, 2 * kTile / kJoinRows);
+    int rows = kJoinThreads / (DV / 4);  // more where that would be many waves of CTAs
+    while (rows < 64 && (int64_t)(a.items / a.parts) * (2 * kTile / rows) > 8 * sms) rows *= 2;
+    cfg.gridDim = dim3(a.items / a.parts, 2 * kTile / rows);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];  // starts while the first kernel ends; waits for it before it reads
@@ -1074,7 +1094,7 @@ kda_status launch(const PromptParams &p, const Shape &shape, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_prompt_join_kernel<DV>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_prompt_join_kernel<DV>, a, rows);
     note_launch();
     if (e != cudaSuccess) {
         set_error("attn_prompt_join_kernel: %s", cudaGetErrorString(e));

@@ -53,11 +53,12 @@ def test_a_chunk_behind_a_context(D, DV, nq, nk):
 
 
 @pytest.mark.parametrize("D,DV", DIMS)
-def test_ragged_batches(D, DV):
+@pytest.mark.parametrize("long,divides", [(1000, False), (4000, True)])
+def test_ragged_batches(D, DV, long, divides):
     """Lengths far from their mean, empty sequences, more parts than a sequence has key blocks."""
-    nq, nk = [1000, 0, 3, 129, 500, 40], [1000, 7, 2000, 129, 450, 40]
+    nq, nk = [long, 0, 3, 129, 500, 40], [long, 7, 2000, 129, 450, 40]
     q, k, v = make(sum(nq) + 9, sum(nk), 2, 2, D, DV, 5)
-    assert size(q, k, v, len(nq)) > 0
+    assert (size(q, k, v, len(nq)) > 0) == divides
     o = torch.full((q.shape[0], 2, DV), 5.0, dtype=torch.bfloat16, device="cuda")
     o, lse = kda.attn_prompt(q, k, v, cu_seqlens=cum(nq), cu_seqlens_k=cum(nk), o=o, return_lse=True)
     assert (o[sum(nq):] == 5).all()  # rows of no sequence
