@@ -197,6 +197,11 @@ struct Vec16<float> {
 // read by one lane, two at a time, so pairs 8v + 2k, 8v + 2k + 1 of all v lie together.
 __device__ __forceinline__ int cs_at(int j, int np) { return ((j >> 1) & 3) * (np >> 2) + (j >> 3) * 2 + (j & 1); }
 
+// Pairs j and j + 1 (j even): 16 bytes.
+__device__ __forceinline__ float4 cs_two(const float2 *cs, int j, int np) {
+    return *reinterpret_cast<const float4 *>(cs + cs_at(j, np));
+}
+
 // cos / sin (times the sign) of `n` tokens' pairs into cs[token * np + cs_at(pair)]: a thread
 // keeps to one pair, so its turn is formed once.
 template <typename PosFn>
@@ -251,7 +256,11 @@ __device__ __forceinline__ void rotate_unit(const T *x, T *y, const float2 *cs, 
         V::load(*reinterpret_cast<const uint4 *>(x + u * N), a);
         float o[N];
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) turn_pair(a[2 * i], a[2 * i + 1], cs[cs_at(u * (N / 2) + i, np)], mag, o[2 * i], o[2 * i + 1]);
+        for (int i = 0; i < N / 2; i += 2) {
+            const float4 w = cs_two(cs, u * (N / 2) + i, np);
+            turn_pair(a[2 * i], a[2 * i + 1], make_float2(w.x, w.y), mag, o[2 * i], o[2 * i + 1]);
+            turn_pair(a[2 * i + 2], a[2 * i + 3], make_float2(w.z, w.w), mag, o[2 * i + 2], o[2 * i + 3]);
+        }
         *reinterpret_cast<uint4 *>(y + u * N) = V::store(o);
     } else {
         float b[N], oa[N], ob[N];
@@ -260,7 +269,11 @@ __device__ __forceinline__ void rotate_unit(const T *x, T *y, const float2 *cs, 
         V::load(wa, a);
         V::load(wb, b);
 #pragma unroll
-        for (int i = 0; i < N; ++i) turn_pair(a[i], b[i], cs[cs_at(u * N + i, np)], mag, oa[i], ob[i]);
+        for (int i = 0; i < N; i += 2) {
+            const float4 w = cs_two(cs, u * N + i, np);
+            turn_pair(a[i], b[i], make_float2(w.x, w.y), mag, oa[i], ob[i]);
+            turn_pair(a[i + 1], b[i + 1], make_float2(w.z, w.w), mag, oa[i + 1], ob[i + 1]);
+        }
         *reinterpret_cast<uint4 *>(y + u * N) = V::store(oa);
         *reinterpret_cast<uint4 *>(y + u * N + R / 2) = V::store(ob);
     }
@@ -271,9 +284,16 @@ template <typename T>
 __device__ __forceinline__ void rotate_rows(const T *x, int64_t xs, T *y, int64_t ys, const float2 *cs,
                                             const RotaryParams &r, int n, int H, int D, int tid, int threads) {
     const int U = rotary_units(D, r.R, r.interleaved, Vec16<T>::N), per = H * U, np = r.R >> 1;
-    for (int i = tid; i < n * per; i += threads) {
-        const int t = i / per, rem = i - t * per, h = rem / U, u = rem - h * U;
-        rotate_unit<T>(x + t * xs + (int64_t)h * D, y + t * ys + (int64_t)h * D, cs + t * np, u, r.R, r.interleaved, r.magnitude);
+    // unit `tid` and then every threads-th, taken apart by additions
+    const int dt = threads / per, dh = (threads - dt * per) / U, du = threads - dt * per - dh * U;
+    int t = tid / per, h = (tid - t * per) / U, u = tid - t * per - h * U;
+    while (t < n) {
+        rotate_unit<T>(x + t * xs + h * D, y + t * ys + h * D, cs + t * np, u, r.R, r.interleaved, r.magnitude);
+        t += dt;
+        h += dh;
+        u += du;
+        if (u >= U) u -= U, ++h;
+        if (h >= H) h -= H, ++t;
     }
 }
 

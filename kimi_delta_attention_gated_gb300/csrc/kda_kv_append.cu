@@ -92,8 +92,8 @@ __device__ __forceinline__ int block_exp(float amax, int off, int old) {
 
 // The queries of a long call, in a launch of their own: their CTAs need half the registers of
 // a run's.  (In one launch the eight prompts of [512, 16384] tokens took 442 us.)
-__global__ void __launch_bounds__(kStepThreads) append_queries_kernel(const __grid_constant__ AppendParams p, int q_tile) {
-    __shared__ float2 cs[kRoom];
+__global__ void __launch_bounds__(kStepThreads, 8) append_queries_kernel(const __grid_constant__ AppendParams p, int q_tile) {
+    __shared__ __align__(16) float2 cs[kRoom];
     __shared__ int s_pos[kRoom];
     rotate_queries<kStepThreads>(p, blockIdx.x, q_tile, cs, s_pos);
     // Its CTAs start while the runs' last ones are at work, and share nothing with them; the launch
@@ -105,7 +105,7 @@ template <int D, int P>
 __global__ void __launch_bounds__(P *D / 16, 1024 / (P * D / 16)) append_run_kernel(const __grid_constant__ AppendParams p,
                                                                                    const __grid_constant__ Grid g) {
     constexpr int kThreads = P * D / 16, kWarps = kThreads / 32;
-    extern __shared__ float2 cs[];
+    extern __shared__ __align__(16) float2 cs[];
     __shared__ int s_pos[kRoom];
     __shared__ int s_seq, s_run;
     __shared__ int s_scan[kWarps];
@@ -207,13 +207,16 @@ __global__ void __launch_bounds__(P *D / 16, 1024 / (P * D / 16)) append_run_ker
             Vec16<__nv_bfloat16>::load(raw[b][1], y[1]);
             if (u < nrot) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 w = turns[cs_at(8 * u + i, np)];
+                for (int i = 0; i < 8; i += 2) {
+                    const float4 w = cs_two(turns, 8 * u + i, np);
+                    const float2 w0 = make_float2(w.x, w.y), w1 = make_float2(w.z, w.w);
                     if (p.rot.interleaved) {
                         float *z = &y[i >> 2][2 * (i & 3)];
-                        turn_pair(z[0], z[1], w, p.rot.magnitude, z[0], z[1]);
+                        turn_pair(z[0], z[1], w0, p.rot.magnitude, z[0], z[1]);
+                        turn_pair(z[2], z[3], w1, p.rot.magnitude, z[2], z[3]);
                     } else {
-                        turn_pair(y[0][i], y[1][i], w, p.rot.magnitude, y[0][i], y[1][i]);
+                        turn_pair(y[0][i], y[1][i], w0, p.rot.magnitude, y[0][i], y[1][i]);
+                        turn_pair(y[0][i + 1], y[1][i + 1], w1, p.rot.magnitude, y[0][i + 1], y[1][i + 1]);
                     }
                 }
             }
@@ -277,7 +280,7 @@ __global__ void __launch_bounds__(kStepThreads) append_step_kernel(const __grid_
                                                                    const __grid_constant__ Grid g) {
     constexpr int kThreads = kStepThreads, kWarps = kThreads / 32;
     constexpr int C = D / 32;  // channels of a lane
-    __shared__ float2 cs[kRoom];
+    __shared__ __align__(16) float2 cs[kRoom];
     __shared__ int s_pos[kRoom];
     if ((int)blockIdx.x >= g.n_kv) {
         rotate_queries<kThreads>(p, blockIdx.x - g.n_kv, g.q_tile, cs, s_pos);

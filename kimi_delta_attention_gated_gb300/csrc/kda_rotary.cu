@@ -17,7 +17,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const T *x, int64_t xs, const int32_t *positions,
                                                           const RotaryParams r, T *out, int64_t os, int64_t tokens,
                                                           int H, int D, int tile) {
-    __shared__ float2 cs[kRoom];
+    __shared__ __align__(16) float2 cs[kRoom];
     const int64_t t0 = (int64_t)blockIdx.x * tile;
     const int n = (int)min((int64_t)tile, tokens - t0);
     fill_cos_sin(cs, r, n, [&](int t) { return __ldg(positions + t0 + t); }, threadIdx.x, kThreads);
