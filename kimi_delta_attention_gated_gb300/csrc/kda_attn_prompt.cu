@@ -75,10 +75,15 @@ struct Cfg {
     static constexpr uint32_t QB = kTile * D * 2, KB = kTile * D * 2, VB = VROWS * DV * 2;
     static constexpr int KST = D == 64 ? 4 : 2, VST = D == 64 ? 4 : 2;
     static constexpr uint32_t Q = 0, K = 2 * QB, V = K + KST * KB, BARS = V + VST * VB;
-    static constexpr int NBAR = 4 + 2 * KST + 2 * VST + 1 + 2 + 4 + 2 + 2 + 4;
+    static constexpr int NBAR = 4 + 2 * KST + 2 * VST + 1 + 2 + 4 + 2 + 2 + 4 + 4;
     static constexpr uint32_t SMEM = BARS + NBAR * 8 + 96 + 1024;
     static_assert(SMEM <= 232448, "shared memory budget");
-    static constexpr uint32_t T_S = 0, T_O = 256;  // TMEM columns of tile 0; tile 1's follow 128 later
+    // TMEM columns of tile 0's scores, output and weights.  Where the output is narrow the weights have
+    // columns of their own: a block's scores are then formed while the softmax works on the last
+    // ones; else they lie over the scores.
+    static constexpr bool AHEAD = 2 * (kTile + DV + kTile / 2) <= 512;
+    static constexpr uint32_t T_S = 0, T_O = 2 * kTile, T_P = AHEAD ? T_O + 2 * DV : T_S;
+    static constexpr uint32_t P_STEP = AHEAD ? kTile / 2 : kTile;  // from tile 0's weights to tile 1's
 };
 
 struct Args {
@@ -413,7 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *s_full = v_raw + 1, *p_ready = s_full + 2;            // p_ready[tile * 2 + half]
     uint64_t *o_full = p_ready + 4, *drain = o_full + 2;
     uint64_t *i_full = drain + 2, *i_empty = i_full + 2;            // the work items' two slots
-    Item *slots = reinterpret_cast<Item *>(i_empty + 2);
+    uint64_t *s_free = i_empty + 2, *p_free = s_free + 2;           // scores read; weights multiplied (AHEAD)
+    Item *slots = reinterpret_cast<Item *>(p_free + 2);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(slots + 2);
     volatile int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);  // a bounded wait gave up
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -430,6 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(drain + i, 1);
             mbar_init(i_full + i, 1);
             mbar_init(i_empty + i, kItemReaders);
+            mbar_init(s_free + i, 4);
+            mbar_init(p_free + i, 1);
         }
         for (int i = 0; i < L::KST; ++i) {
             mbar_init(k_full + i, 1);
@@ -623,7 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t id_s = idesc_bf16(kTile, kTile, false, false, p.scale < 0.f);
             const uint32_t id_o = idesc_bf16(kTile, DV, false, true);
             const uint32_t lo_kmajor = sb16 | (16u >> 4) << 16, lo_v = sb16 | (L::VROWS * 128u >> 4) << 16;
-            const uint32_t q_lo = lo_kmajor + ((L::Q + t * L::QB) >> 4), t_s = tb + L::T_S + t * 128, t_o = tb + L::T_O + t * 128;
+            const uint32_t q_lo = lo_kmajor + ((L::Q + t * L::QB) >> 4), t_s = tb + L::T_S + t * kTile, t_o = tb + L::T_O + t * DV,
+                           t_p = tb + L::T_P + t * L::P_STEP;
             int ks = 0, vs = 0;       // ring places of the next keys and values
             uint32_t kp = 0, vp = 0;  // and the parities of their rounds
             uint32_t blocks = 0, tiles = 0;  // of this tile so far: key blocks, and items with any
@@ -643,10 +652,65 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t v_lo = lo_v + (L::V >> 4) + slot * (L::VB >> 4) + (L::NV == 1 ? h * 4 * (2048 >> 4) : 0);
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    mma_ts(t_o, t_s + (4 * h + x) * 8, desc_of(v_lo + x * (2048 >> 4)), id_o, x > 0 ? 1u : more);
+                    mma_ts(t_o, t_p + (4 * h + x) * 8, desc_of(v_lo + x * (2048 >> 4)), id_o, x > 0 ? 1u : more);
                 if (L::NV == 2 || h == 1) mma_commit(v_empty + slot);
             };
-            for (int k = 0;; ++k) {
+            // With weights of their own each tile's products go ahead as their operands come: the scores of
+            // block j + 1, then the product of block j.
+            uint32_t scored = 0;  // blocks with scores so far
+            for (int k = 0; L::AHEAD; ++k) {
+                Item it;
+                if (!ok || !take_item(k, it)) {
+                    failed = 1;
+                    break;
+                }
+                if (!it.found) break;
+                const int n0 = tile_blocks(it, it.s, 0), n1 = tile_blocks(it, it.s, 1), nb = max(n0, n1), nt = t ? n1 : n0;
+                if (nt) ok = wait_copy(q_full + t, tiles & 1);
+                for (int j = -1; j < nb; ++j) {
+                    if (j + 1 < nb) {
+                        const bool mine = j + 1 < nt;
+                        ok = ok && wait(k_full + ks, kp);
+                        if (mine && scored > 0) ok = ok && wait(s_free + t, (scored - 1) & 1);
+                        fence_after_sync();
+                        if (elect_one() && ok) {
+                            if (mine) {
+                                scores();
+                                if (j + 2 == nt) mma_commit(q_empty + t);
+                            } else {
+                                mbar_arrive(k_empty + ks);  // every block is let go of by both tiles
+                            }
+                        }
+                        __syncwarp();
+                        scored += mine;
+                        if (++ks == L::KST) ks = 0, kp ^= 1;
+                    }
+                    if (j < 0) continue;
+                    const bool mine = j < nt;
+                    ok = ok && wait(v_full + vs, vp);
+                    if (mine) ok = ok && wait(p_ready + 2 * t, (blocks + j) & 1);
+                    fence_after_sync();
+                    if (mine && elect_one() && ok) weigh(0, vs, j > 0);
+                    __syncwarp();
+                    if (mine) ok = ok && wait(p_ready + 2 * t + 1, (blocks + j) & 1);
+                    fence_after_sync();
+                    if (elect_one() && ok) {
+                        if (mine) {
+                            weigh(1, vs, true);
+                            mma_commit(p_free + t);
+                            if (j + 1 == nt) mma_commit(o_full + t);
+                        } else {
+                            mbar_arrive(v_empty + vs);
+                        }
+                    }
+                    __syncwarp();
+                    if (++vs == L::VST) vs = 0, vp ^= 1;
+                }
+                blocks += nt;
+                tiles += nt > 0;
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            for (int k = 0; !L::AHEAD; ++k) {
                 Item it;
                 // both product warps go on or stop together: each waits for the other's turns
                 const bool taken = take_item(k, it);
@@ -729,7 +793,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- softmax of tile t, a thread per row
         const int t = warp >> 2, m_row = (warp & 3) * 32 + lane;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t t_s = tb + lane_base + L::T_S + t * 128, t_o = tb + lane_base + L::T_O + t * 128;
+        const uint32_t t_s = tb + lane_base + L::T_S + t * kTile, t_o = tb + lane_base + L::T_O + t * DV,
+                       t_p = tb + lane_base + L::T_P + t * L::P_STEP;
         const float c = fabsf(p.scale) * kLog2e;
         uint32_t blocks = 0, tiles = 0;  // of this tile so far: key blocks, and items with any
         bool ok = see_item(0);
@@ -745,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (SPLIT) seen -= it.lo * kTile, seen_first -= it.lo * kTile;  // keys of this part
             }
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < nt; ++j, ++blocks) {
+            for (int j = 0; j < nt && ok; ++j, ++blocks) {
                 ok = wait_all(s_full + t, blocks & 1);
                 if (!ok) break;
                 fence_after_sync();
@@ -754,6 +819,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 128; i += 32) tmem_ld32(t_s + i, x + i);
                 wait_ld64(x);
                 wait_ld64(x + 64);
+                if (L::AHEAD) {
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_free + t);
+                }
                 if ((j + 1) * kTile > seen_first) {
                     // keys behind what the row sees, by runs of 32: those that the warp's first row sees whole
                     // need no look
@@ -775,11 +845,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[124 + e]);
                 const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
                 const bool raise = mb > m + kSlack;
+                if (L::AHEAD && blocks > 0) {  // the last weights, and the products that O is to hold
+                    ok = wait_all(p_free + t, (blocks - 1) & 1);
+                    fence_after_sync();
+                }
                 if (__any_sync(0xffffffffu, raise)) {
                     const float f = raise ? ex2(m - mb) : 1.f;
                     if (raise) m = mb;
                     l *= f;
-                    if (j > 0) {  // the scores' arrival says that the products before them are done
+                    if (j > 0) {  // the products before are done: (AHEAD) waited for, else said by the scores' arrival
 #pragma unroll 1
                         for (int d = 0; d < DV; d += 16) {
                             uint32_t o[16];
@@ -794,11 +868,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 weights32(x, c, m, sum);
                 weights32(x + 32, c, m, sum);
-                tmem_st16x2(t_s, x, x + 32);
+                tmem_st16x2(t_p, x, x + 32);
                 weights32(x + 64, c, m, sum);
                 hand_over(p_ready + 2 * t);
                 weights32(x + 96, c, m, sum);
-                tmem_st16x2(t_s + 32, x + 64, x + 96);
+                tmem_st16x2(t_p + 32, x + 64, x + 96);
                 hand_over(p_ready + 2 * t + 1);
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
