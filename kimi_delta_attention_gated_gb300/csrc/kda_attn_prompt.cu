@@ -25,12 +25,14 @@
 // or a pair; with few of them also a part of their keys) are taken longest first, in rounds of
 // alternating direction.  Loads, scores and
 // rings go on across items, so that an item's beginning runs beside the last one's end.
-// TMEM: S_0, S_1 (P over them), O_0, O_1, 128 columns each.
+// TMEM: S_0, S_1 (P over them), O_0, O_1, 128 columns each; with 64 channels O takes 64, and P has
+// columns of its own, so that a block's scores are formed while the softmax works on the last ones
+// and the product warps need no turns (8192 tokens 275 -> 254 us).
 //
 // Weights are rounded to bf16 because the product takes one type and the values are bf16;
 // l sums the unrounded weights in fp32.
 //
-// 8192 tokens with 32 heads over 8, channels 64/64, 128/128, 192/128: 275, 317, 400 us, 1000, 1734 and
+// 8192 tokens with 32 heads over 8, channels 64/64, 128/128, 192/128: 254, 316, 400 us, 1082, 1740 and
 // 1718 TFLOP/s.  With 64 channels the softmax is the bound (a weight for 256 operations instead of
 // 512 or 640); with 128 and more the tensor pipe is busy for 70 to 75 % of the cycles, at a clock that
 // the power limit sets, and a tile's chain of scores, softmax and product is the bound.  8 packed prompts of [100, 4096] tokens, 32 heads of 192/128: 125 us,
@@ -80,7 +82,7 @@ struct Cfg {
     static_assert(SMEM <= 232448, "shared memory budget");
     // TMEM columns of tile 0's scores, output and weights.  Where the output is narrow the weights have
     // columns of their own: a block's scores are then formed while the softmax works on the last
-    // ones; else they lie over the scores.
+    // ones (254 against 275 us for 8192 tokens, 32/8 heads of 64); else they lie over the scores.
     static constexpr bool AHEAD = 2 * (kTile + DV + kTile / 2) <= 512;
     static constexpr uint32_t T_S = 0, T_O = 2 * kTile, T_P = AHEAD ? T_O + 2 * DV : T_S;
     static constexpr uint32_t P_STEP = AHEAD ? kTile / 2 : kTile;  // from tile 0's weights to tile 1's
