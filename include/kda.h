@@ -544,8 +544,8 @@ kda_status kda_rotary(const void *x, kda_dtype dtype, int64_t x_stride, const in
  *   k_out        [tokens, kv_heads, dim] bf16, dense, or NULL: the rotated keys
  * Rows of q_out and k_out that belong to no sequence are left as they are.
  * dim 64 or 128; page_size 16, 32, 64 or 128 (KDA_ERR_UNSUPPORTED otherwise).
- * No page may be written for two sequences in one call (pages that are only read, full ones of
- * a shared beginning, may stand in several rows of block_table).
+ * No page may be written for two sequences, or for two places of one, in one call (pages that
+ * are only read, full ones of a shared beginning, may stand in several rows of block_table).
  */
 kda_status kda_kv_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride, int64_t tokens,
                          int kv_heads, int dim, void *k_cache, void *v_cache, float *k_scale, float *v_scale,

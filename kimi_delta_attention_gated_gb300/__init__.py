@@ -903,7 +903,8 @@ def attn_prompt(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, scale=None, out_
     if not q.is_cuda:
         dev = _device_of(k, v, cu_seqlens, cu_seqlens_k)
         r = attn_prompt(*(_prep(t, dev) for t in (q, k, v)), cu_seqlens=_prep(cu_seqlens, dev),
-                        cu_seqlens_k=_prep(cu_seqlens_k, dev), scale=scale, out_dtype=out_dtype, return_lse=return_lse)
+                        cu_seqlens_k=_prep(cu_seqlens_k, dev), scale=scale, out_dtype=out_dtype, return_lse=return_lse,
+                        workspace=workspace)
         r = _to_host(r if return_lse else (r,), True, (o, None))
         return r if return_lse else r[0]
     index, lead, N = q.get_device(), None, 1

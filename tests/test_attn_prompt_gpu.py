@@ -117,16 +117,18 @@ def test_many_sequences():
     case(lens, lens, 2, 1, 64, 64, seed=5)
 
 
-def test_rising_and_sharp_scores():
+@pytest.mark.parametrize("D,DV", DIMS)
+def test_rising_and_sharp_scores(D, DV):
     """Scores of several hundred; keys that grow along the sequence, so that the reference maximum is
     set anew in block after block; negative and tiny scales."""
-    case([400], [400], 2, 1, 128, 128, seed=6, sharp=25.0)
-    q, k, v = make(600, 600, 2, 1, 128, 128, 7)
+    case([400], [400], 2, 1, D, DV, seed=6, sharp=25.0)
+    q, k, v = make(600, 600, 2, 1, D, DV, 7)
     q = q.abs()
     k = (k.abs().float() * torch.linspace(0.1, 4, 600, device="cuda")[:, None, None]).bfloat16()
     for scale in (None, -0.2, 1e-12):
-        o, lse = kda.attn_prompt(q, k, v, return_lse=True, scale=scale)
-        verify(o, lse, q, k, v, [600], [600], scale, rows=list(range(0, 600, 41)) + [599])
+        for ws in ("auto", None):
+            o, lse = kda.attn_prompt(q, k, v, return_lse=True, scale=scale, workspace=ws)
+            verify(o, lse, q, k, v, [600], [600], scale, rows=list(range(0, 600, 41)) + [599])
 
 
 @pytest.mark.parametrize("D,DV", DIMS)
@@ -198,6 +200,16 @@ def test_same_bits_again_on_another_stream_and_from_a_graph():
     assert torch.equal(out, kda.attn_prompt(q, k, v, cu_seqlens=cu))
     whole = kda.attn_prompt(q, k, v, cu_seqlens=cu, workspace=None)
     assert torch.equal(whole, kda.attn_prompt(q, k, v, workspace=None))
+
+
+@pytest.mark.parametrize("Hq,Hk", [(2, 1), (1, 1)])
+def test_more_than_128_sequences(Hq, Hk):
+    """More sequences than a warp holds at once (128), with and without tokens, the longest one last."""
+    lens = [(7 * n * n + 3 * n) % 61 for n in range(300)] + [0, 700]
+    q, k, v = make(sum(lens), sum(lens), Hq, Hk, 64, 64, 16)
+    for ws in ("auto", None):
+        o, lse = kda.attn_prompt(q, k, v, cu_seqlens=cum(lens), return_lse=True, workspace=ws)
+        verify(o, lse, q, k, v, lens, lens, rows=[0, 1, 7, 20, 39, 60, 127, 128, 255, 256, 600, 699])
 
 
 def test_two_calls_at_once():
