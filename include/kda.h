@@ -568,7 +568,8 @@ kda_status kda_kv_append(const void *k, int64_t k_stride, const void *v, int64_t
  *   lse       [n_seqs, q_heads] float or NULL: log(sum_j e^(scale q . K_j))
  *   workspace device scratch of kda_attn_decode_workspace_size(n_seqs, q_heads, kv_heads,
  *             dim, max_blocks * page_size) bytes, 16-byte aligned; calls that may overlap on
- *             the GPU (two captured graphs among them) need workspaces of their own
+ *             the GPU (two captured graphs among them) need workspaces of their own.  Where the
+ *             size is 0 it may be NULL.
  * What lies in a page behind a sequence's last token is not read into the result, whatever
  * it is.  A sequence with a page number out of [0, num_pages) gives NaN rows.
  * dim 64 or 128; page_size 16, 32, 64 or 128.  Results do not depend on timing.

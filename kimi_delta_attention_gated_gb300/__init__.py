@@ -862,15 +862,17 @@ def attn_decode(q, cache, block_table, seq_lens, *, scale=None, out_dtype=torch.
         raise ValueError("o must be like q")
     lse = torch.empty((N, Hq), dtype=torch.float32, device=device) if return_lse else None
     if workspace is None:
-        need = lib.kda_attn_decode_workspace_size(N, Hq, Hk, D, max_blocks * P)
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        need, ws = lib.kda_attn_decode_workspace_size(N, Hq, Hk, D, max_blocks * P), None
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            ws = workspace.data_ptr()
     else:
-        need = workspace.numel() * workspace.element_size()
+        need, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
         if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
     _call(lib.kda_attn_decode, index, qp, q_stride, *cache_args, table, max_blocks, lens, N, Hq, Hk, D,
           D ** -0.5 if scale is None else float(scale), _dense(o, "o", o.dtype, 3, index), _dt(o),
-          None if lse is None else lse.data_ptr(), workspace.data_ptr(), need)
+          None if lse is None else lse.data_ptr(), ws, need)
     return (o, lse) if return_lse else o
 
 

@@ -919,7 +919,7 @@ kda_status kda_attn_decode(const void *q, int64_t q_stride, const void *k_cache,
     if (n_seqs == 0) return KDA_OK;
     const size_t need =
         kda::attn_decode_workspace_bytes(n_seqs, q_heads, kv_heads, dim, (int64_t)max_blocks * page_size);
-    KDA_REQUIRE(workspace && workspace_bytes >= need, KDA_ERR_INVALID_ARG,
+    KDA_REQUIRE(need == 0 || (workspace && workspace_bytes >= need), KDA_ERR_INVALID_ARG,
                 "%s: the workspace holds %zu bytes, this call needs %zu (kda_attn_decode_workspace_size)", fn,
                 workspace ? workspace_bytes : (size_t)0, need);
     const size_t blocks = (size_t)num_pages * kv_heads, codes = blocks * page_size * dim;
@@ -947,6 +947,7 @@ kda_status kda_attn_decode(const void *q, int64_t q_stride, const void *k_cache,
     p.o_bf16 = o_dtype == KDA_BF16;
     p.lse = lse;
     p.ws = static_cast<float *>(workspace);
+    p.whole = 0;
     p.polls = std::min(kda::wait_polls(), kda::kAttnPolls);
     return kda::launch_attn_decode(p, (cudaStream_t)stream);
 }

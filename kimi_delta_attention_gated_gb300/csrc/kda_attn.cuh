@@ -59,6 +59,7 @@ struct DecodeParams {
     int o_bf16;
     float *lse;                   // [N, Hq] or null
     float *ws;                    // partial results
+    int whole;                    // a CTA for each (sequence, head), no partial results
     uint32_t polls;               // bound on the copies' waits
 };
 

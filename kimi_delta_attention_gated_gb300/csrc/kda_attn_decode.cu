@@ -230,11 +230,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // this CTA's piece of the line
-    const Line line = measure_line(c, s_scan, kThreads);
-    const int64_t all = line.total * U, S = piece_places(all, gridDim.x), L0 = (int64_t)blockIdx.x * S;
-    if (L0 >= all) return;
-    const int64_t L1 = min(L0 + S, all);
-    {
+    int64_t L0 = 0, L1;
+    if (p.whole) {
+        Segment x;
+        x.n = blockIdx.x / U;
+        x.u = blockIdx.x - x.n * U;
+        x.head = x.u / parts;
+        x.len = tokens_of(c, x.n);
+        x.steps = (x.len + kStep - 1) / kStep;
+        L1 = places_of(x.steps);
+        set_range(x, 0, L1);
+        if (x.len == 0) {
+            const int r0 = (x.u - x.head * parts) * F::ROWS;
+            const int64_t row = (int64_t)x.n * p.Hq + x.head * group + r0;
+            for (int i = tid; i < min(F::ROWS, group - r0) * D; i += kThreads) st_out(p.o, row * D + i, 0.f, p.o_bf16);
+            if (p.lse && tid < min(F::ROWS, group - r0)) p.lse[row + tid] = kNegInf;
+            return;
+        }
+        if (tid == 0) s_seg = x;
+    } else {
+        const Line line = measure_line(c, s_scan, kThreads);
+        const int64_t all = line.total * U, S = piece_places(all, gridDim.x);
+        L0 = (int64_t)blockIdx.x * S;
+        if (L0 >= all) return;
+        L1 = min(L0 + S, all);
         int64_t at = line.mine;  // one thread's range holds the start
         for (int n = line.first; n < line.last; ++n) {
             const int len = tokens_of(c, n), st = (len + kStep - 1) / kStep, pl = places_of(st);
@@ -743,19 +762,27 @@ bool encode(chunk::EncodeTiledFn enc, CUtensorMap *map, const void *base, const 
     return r == CUDA_SUCCESS;
 }
 
-// CTAs of a call: what the GPU holds at once, or as many as pieces are possible at all.
+// CTAs of a call: what the GPU holds at once, or as many as pieces are possible at all.  Where the
+// GPU holds a CTA for each head of each sequence and the table few tokens, heads are not cut, and
+// nothing is joined: cut and whole, 32/8 heads of 128, one sequence of 60, 500, 1000 tokens 6.4
+// and 4.4, 8.7 and 7.9, 8.8 and 12.3 us; 32 of 250, 1000, 2000 tokens 11.9 and 7.0, 18.4 and
+// 14.7, 30.8 and 27.8 us (of 2000 only when all are that long).
 template <int D, int NT>
-int decode_ctas(int64_t N, int Hq, int Hk, int64_t max_tokens) {
+int decode_ctas(int64_t N, int Hq, int Hk, int64_t max_tokens, bool &whole) {
     using F = Cfg<D, NT>;
     const int64_t most = (int64_t)F::CTAS * sm_count(), group = Hq / Hk;
     const int64_t units = N * Hk * ((group + F::ROWS - 1) / F::ROWS);
+    whole = units <= most && max_tokens <= (2 * units >= most ? 32 : 16) * kStep;
+    if (whole) return (int)units;
     const int64_t pieces = (units * ((max_tokens + kStep - 1) / kStep + kPad) + kMinPiece - 1) / kMinPiece;
     return (int)(pieces < most ? pieces : most);
 }
 
 template <int D, int NT>
 size_t workspace_bytes(int64_t N, int Hq, int Hk, int64_t max_tokens) {
-    return (size_t)decode_ctas<D, NT>(N, Hq, Hk, max_tokens) * 2 * Cfg<D, NT>::PART * sizeof(float);  // two pieces per CTA
+    bool whole;
+    const int ctas = decode_ctas<D, NT>(N, Hq, Hk, max_tokens, whole);
+    return whole ? 0 : (size_t)ctas * 2 * Cfg<D, NT>::PART * sizeof(float);  // two pieces per CTA
 }
 
 template <int D, int NT>
@@ -769,7 +796,9 @@ kda_status run(const DecodeParams &p, cudaStream_t st) {
     CUtensorMap mk, mv;
     if (!encode(enc, &mk, p.c.k, p.c) || !encode(enc, &mv, p.c.v, p.c)) return KDA_ERR_CUDA;
     static DeviceOnce configured;
-    const int dev = current_device(), ctas = decode_ctas<D, NT>(p.c.N, p.Hq, p.c.Hk, (int64_t)p.c.max_blocks * p.c.P);
+    bool whole;
+    const int dev = current_device();
+    const int ctas = decode_ctas<D, NT>(p.c.N, p.Hq, p.c.Hk, (int64_t)p.c.max_blocks * p.c.P, whole);
     if (!configured.done(dev)) {
         if (cudaFuncSetAttribute(attn_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM) !=
             cudaSuccess) {
@@ -778,10 +807,12 @@ kda_status run(const DecodeParams &p, cudaStream_t st) {
         }
         configured.set(dev);
     }
-    attn_decode_kernel<D, NT><<<ctas, kThreads, F::SMEM, st>>>(mk, mv, p);
+    DecodeParams call = p;
+    call.whole = whole;
+    attn_decode_kernel<D, NT><<<ctas, kThreads, F::SMEM, st>>>(mk, mv, call);
     note_launch();
     kda_status s = check_launch("attn_decode_kernel");
-    if (s != KDA_OK) return s;
+    if (whole || s != KDA_OK) return s;
     cudaLaunchConfig_t cfg = {};
     // few units (of which each may have many pieces): large CTAs for two rows each; else as many
     // as are resident at once, so that none waits for others that wait for the first kernel

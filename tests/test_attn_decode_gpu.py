@@ -217,6 +217,20 @@ def test_append_then_attend():
             ref.check(f"o[{n}, {h}]", o[n, hs], want, tol)
 
 
+@pytest.mark.parametrize("D,P,Hq,Hk", [(64, 16, 2, 1), (128, 64, 24, 2), (128, 128, 3, 3)])
+def test_short_tables_need_no_workspace(D, P, Hq, Hk):
+    """A table that holds few tokens: a CTA for each head, nothing to join; empty sequences among them."""
+    lens = [0, 1, 31, 33, 256, 0, 200]
+    o, lse, q, cache, table, sl = case(lens, Hk, Hq // Hk, D, P, seed=23)
+    assert kda.attn_decode_workspace_size(len(lens), Hq, Hk, D, table.shape[1] * P) == 0
+    wide = torch.full((len(lens), 40 * 128 // P), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    assert kda.attn_decode_workspace_size(len(lens), Hq, Hk, D, wide.shape[1] * P) > 0
+    o2, l2 = kda.attn_decode(q, cache, wide.cuda(), sl, return_lse=True)
+    verify(o2, l2, q, cache, wide, lens)
+    assert (o[0] == 0).all() and (lse[5] == float("-inf")).all()
+
+
 def test_sequences_that_share_pages():
     """Two sequences with the same beginning: the pages stand in both rows of the table."""
     o, lse, q, cache, table, sl = case([100, 70], 2, 4, 64, 16, seed=18)
@@ -256,7 +270,8 @@ def test_refusals():
     bad = [(dict(q=q.float()), TypeError), (dict(q=q[:1]), ValueError), (dict(seq_lens=sl.long()), TypeError),
            (dict(seq_lens=sl.cpu()), ValueError), (dict(q=torch.zeros((2, 4, 128), device="cuda").bfloat16()), ValueError),
            (dict(q=torch.zeros((2, 3, 64), device="cuda").bfloat16()), kda.KDAError),
-           (dict(workspace=torch.zeros(16, dtype=torch.uint8, device="cuda")), kda.KDAError),
+           (dict(block_table=torch.zeros((2, 300), dtype=torch.int32, device="cuda"),
+                 workspace=torch.zeros(16, dtype=torch.uint8, device="cuda")), kda.KDAError),
            (dict(scale=float("nan")), kda.KDAError), (dict(out_dtype=torch.float16), TypeError)]
     for over, err in bad:
         a = dict(q=q, cache=cache, block_table=table, seq_lens=sl)
