@@ -23,7 +23,7 @@
 // equal pieces, one per CTA, whatever the lengths of the sequences are; every CTA finds its
 // piece from the lengths on the device.  A head that one CTA covers is written at once, the
 // others go through a workspace and attn_decode_join_kernel, which adds a head's pieces in
-// their order, so results do not depend on timing.
+// their order, so results do not depend on timing.  Short sequences are not cut (decode_ctas).
 //
 // Copies.  Each warp has a ring of steps in shared memory, filled by TMA ahead of their use
 // and across the borders of heads, without a barrier between warps.  The swizzle of the rows
@@ -763,16 +763,17 @@ bool encode(chunk::EncodeTiledFn enc, CUtensorMap *map, const void *base, const 
 }
 
 // CTAs of a call: what the GPU holds at once, or as many as pieces are possible at all.  Where the
-// GPU holds a CTA for each head of each sequence and the table few tokens, heads are not cut, and
-// nothing is joined: cut and whole, 32/8 heads of 128, one sequence of 60, 500, 1000 tokens 6.4
-// and 4.4, 8.7 and 7.9, 8.8 and 12.3 us; 32 of 250, 1000, 2000 tokens 11.9 and 7.0, 18.4 and
-// 14.7, 30.8 and 27.8 us (of 2000 only when all are that long).
+// table holds few tokens, heads are not cut, each has a CTA, and nothing is joined: cut and
+// whole, 32/8 heads of 128, one sequence of 60, 500, 1000 tokens 6.4 and 4.4, 8.7 and 7.9, 8.8
+// and 12.3 us; 32 of 250, 1000 tokens 11.9 and 7.0, 18.4 and 14.7 us; 256 of [50, 150], 1000 with
+// 64/8 heads 30.9 and 26.3, 97.8 and 96.9 us.  With groups of 16, where an SM holds two CTAs,
+// many waves of them are slower: 64 sequences of 500 tokens 28.5 and 24.5, 256 82.5 and 87.7 us.
 template <int D, int NT>
 int decode_ctas(int64_t N, int Hq, int Hk, int64_t max_tokens, bool &whole) {
     using F = Cfg<D, NT>;
     const int64_t most = (int64_t)F::CTAS * sm_count(), group = Hq / Hk;
     const int64_t units = N * Hk * ((group + F::ROWS - 1) / F::ROWS);
-    whole = units <= most && max_tokens <= (2 * units >= most ? 32 : 16) * kStep;
+    whole = max_tokens <= (2 * units >= most ? 32 : 16) * kStep && units <= (NT == 1 ? INT32_MAX : 2 * most);
     if (whole) return (int)units;
     const int64_t pieces = (units * ((max_tokens + kStep - 1) / kStep + kPad) + kMinPiece - 1) / kMinPiece;
     return (int)(pieces < most ? pieces : most);

@@ -231,6 +231,15 @@ def test_short_tables_need_no_workspace(D, P, Hq, Hk):
     assert (o[0] == 0).all() and (lse[5] == float("-inf")).all()
 
 
+def test_many_short_tables():
+    """More heads than the GPU holds CTAs, whole; the lengths clamped to a table of 1024 tokens."""
+    lens = [(37 * n) % 300 for n in range(130)] + [1000]
+    o, lse, q, cache, table, sl = case(lens, 8, 1, 64, 64, seed=24)
+    assert kda.attn_decode_workspace_size(len(lens), 8, 8, 64, table.shape[1] * 64) == 0
+    o2 = kda.attn_decode(q, cache, table.cuda(), (sl + 100000) * (sl > 900) + sl * (sl <= 900))
+    assert torch.equal(o2[:-1], o[:-1])  # the last one attends to the whole table now
+
+
 def test_sequences_that_share_pages():
     """Two sequences with the same beginning: the pages stand in both rows of the table."""
     o, lse, q, cache, table, sl = case([100, 70], 2, 4, 64, 16, seed=18)
