@@ -85,7 +85,7 @@ def test_append_refuses(lib, over, code):
 
 
 def decode(lib, **over):
-    a = dict(q=fake(0), qs=512, kc=fake(1), vc=fake(2), ks=fake(3), vs=fake(4), pages=10, P=64, bt=fake(5), mb=4, lens=fake(6),
+    a = dict(q=fake(0), qs=512, kc=fake(1), vc=fake(2), ks=fake(3), vs=fake(4), pages=10, P=64, bt=fake(5), mb=40, lens=fake(6),
              N=2, Hq=4, Hk=2, D=128, scale=0.1, o=fake(7), dt=BF16, lse=fake(8), ws=fake(9), wsb=1 << 25)
     a.update(over)
     return lib.kda_attn_decode(*(a[k] for k in ("q", "qs", "kc", "vc", "ks", "vs", "pages", "P", "bt", "mb", "lens", "N", "Hq",
