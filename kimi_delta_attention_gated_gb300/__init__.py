@@ -941,7 +941,8 @@ def attn_prompt(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, scale=None, out_
     lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device) if return_lse else None
     ws, need = None, 0
     if workspace is not None:
-        need = lib.kda_attn_prompt_workspace_size(T, S, Hq, Hk, DV, N)
+        if S > 128 * N:  # (one block of keys a sequence is never divided)
+            need = lib.kda_attn_prompt_workspace_size(T, S, Hq, Hk, DV, N)
         if isinstance(workspace, torch.Tensor):
             if workspace.get_device() != index or not workspace.is_contiguous():
                 raise ValueError("workspace must be a contiguous tensor on q's device")
