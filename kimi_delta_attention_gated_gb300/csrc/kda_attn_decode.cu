@@ -428,6 +428,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
             cp_wait<F::DEPTH - 1>();
             if (!failed && !tc::mbar_wait(bars + rd, rd_phase, p.polls)) failed = 1;
             failed = __any_sync(0xffffffffu, failed);
+            __syncwarp();  // the scales came by four lanes' own copies; a vote orders no memory
             const uint8_t *slot = smem + (warp * F::DEPTH + rd) * F::SLOT;
             const float4 sc = *reinterpret_cast<const float4 *>(smem + F::SCALES + (warp * F::DEPTH + rd) * 16);
             const float ks[2] = {sc.x, sc.z}, vs[2] = {sc.y, sc.w};
