@@ -45,8 +45,9 @@ struct AppendParams {
     __nv_bfloat16 *q_out, *k_out; // dense [tokens, Hq, D] / [tokens, Hk, D]; k_out may be null
 };
 
-// Bound on the attention kernels' waits, a few seconds: a CTA waits for nothing but its own warps
-// and copies.  The first-line waits on copies take a lower one from kda_set_wait_limit.
+// Bound on the attention kernels' waits, 8 s (a poll that finds nothing takes 3.8 us, measured): a
+// CTA waits for nothing but its own warps and copies, none of which does work of unbounded length
+// while another waits.  The first-line waits on copies take a lower one from kda_set_wait_limit.
 constexpr uint32_t kAttnPolls = 1u << 21;
 
 struct DecodeParams {

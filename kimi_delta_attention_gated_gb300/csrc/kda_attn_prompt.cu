@@ -41,8 +41,9 @@
 //
 // What is masked never reaches a result: masked scores are replaced, not added to; value
 // rows behind the sequence's end are zeroed in shared memory (a zero weight would turn an
-// infinity there into NaN); a row that comes out NaN is looked at again, and where a value
-// of a later token of its own block caused it, it is computed alone (rescue_row).
+// infinity there into NaN); where a row comes out NaN and a value of a later token of its own
+// blocks caused it, the channels concerned are computed alone (rescue_row), when the
+// CTA's items are through: such a row may see any number of keys, and no bounded wait may run meanwhile.
 #include <cuda.h>
 #include <string.h>
 
@@ -356,6 +357,36 @@ struct UnitSearch {
     }
 };
 
+// First row of an item's tile t.
+__device__ __forceinline__ int first_row(const Args &a, const Item &it, int t) {
+    return a.pair_heads ? it.row0 : it.row0 + t * kTile;
+}
+// Key blocks of an item that its tile t sees.
+template <bool SPLIT>
+__device__ __forceinline__ int blocks_of(const Args &a, const Item &it, const Seq &s, int t) {
+    const int r = first_row(a, it, t), last = min(r + kTile, s.nq) - 1;
+    if (r >= s.nq) return 0;
+    const int seen = max(0, min(s.nk, last + 1 + (s.nk - s.nq)));
+    const int n = (seen + kTile - 1) / kTile;
+    return SPLIT ? max(0, min(n, it.hi) - it.lo) : n;
+}
+// This CTA's k-th work item; one warp.
+template <bool SPLIT>
+__device__ __forceinline__ Item item_of(const Args &a, UnitSearch &units, int k) {
+    const int64_t i = (int64_t)k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    const int u = SPLIT ? (int)i / a.parts : (int)i, part = SPLIT ? (int)i - u * a.parts : 0;
+    Item it = {{0, 0, 0, 0}, 0, 0, u % a.n_heads, 0, INT_MAX, (int)i};
+    int seq = 0;
+    if (i < a.items) it.found = units.find(a.p, a.pair_heads ? 7 : 8, u / a.n_heads, seq, it.row0);
+    if (it.found) it.s = seq_of(a.p, seq);
+    if (SPLIT && it.found) {
+        const int nb = max(blocks_of<SPLIT>(a, it, it.s, 0), blocks_of<SPLIT>(a, it, it.s, 1));
+        it.lo = (int)((int64_t)nb * part / a.parts);
+        it.hi = (int)((int64_t)nb * (part + 1) / a.parts);
+    }
+    return it;
+}
+
 // Weights 2^(c y - m) of 32 scores y, left as bf16 pairs in the words y[0, 16); their sum is
 // added to s (two pairs of halves).
 __device__ __forceinline__ void weights32(float *y, float c, float m, float2 (&s)[2]) {
@@ -371,35 +402,105 @@ __device__ __forceinline__ void weights32(float *y, float c, float m, float2 (&s
     }
 }
 
-// One row computed alone, without what it does not see, over the keys [from, seen): m and l are
-// its softmax's (they never include masked scores).  part: where a part's sums go, or null.  Taken only where a NaN came out and a masked value is not finite.
+// A row's channels that a masked value spoiled, computed alone by one warp over the keys
+// [from, seen) that the row sees; its tile went through the keys up to `end`.  c: the scale in
+// units of log2; part: a part's O of this row, whose reference is part_m, or null.  A row that is
+// finite, or whose masked values are, is left as it is.  The pass goes backwards and ends when
+// every channel concerned is NaN by what the row sees, as behind the valid part of a padded sequence.
 template <int D, int DV>
-__device__ __noinline__ void rescue_row(const PromptParams &p, const Seq &s, int row, int head, int from, int seen,
-                                        int blocks, float m, float l, float c, float *part) {
-    const int kvh = head / (p.Hq / p.Hk);
-    const __nv_bfloat16 *v0 = p.v + (int64_t)s.k0 * p.v_stride + (int64_t)kvh * DV;
-    bool masked_bad = false;
-    for (int j = seen; j < min(blocks * kTile, s.nk) && !masked_bad; ++j)
-        for (int d = 0; d < DV; ++d) masked_bad |= !isfinite(__bfloat162float(v0[j * p.v_stride + d]));
-    if (!masked_bad) return;  // the NaN comes from what the row sees
-    const __nv_bfloat16 *q = p.q + (int64_t)(s.q0 + row) * p.q_stride + (int64_t)head * D;
+__device__ __forceinline__ void rescue_row(const PromptParams &p, const Seq &s, int row, int head, int from, int seen, int end,
+                                        float c, float *part, float part_m) {
+    constexpr int C = DV / 32;  // channels of a lane
+    constexpr uint32_t kAll = 0xffffffffu;
+    const int lane = threadIdx.x & 31, kvh = head / (p.Hq / p.Hk), d0 = lane * C;
+    const int64_t out = ((int64_t)(s.q0 + row) * p.Hq + head) * DV + d0;
+    const __nv_bfloat16 *v0 = p.v + (int64_t)s.k0 * p.v_stride + (int64_t)kvh * DV + d0;
+    uint32_t odd = 0, bad = 0;  // bits: outputs that are not finite, and among them masked values that are not
+#pragma unroll
+    for (int e = 0; e < C; ++e) {
+        const float x = part ? part[d0 + e]
+                             : p.o_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.o)[out + e])
+                                        : static_cast<const float *>(p.o)[out + e];
+        odd |= (uint32_t)!isfinite(x) << e;
+    }
+    if (!__any_sync(kAll, odd != 0)) return;
+    for (int j = max(seen, from); j < end; ++j)
+#pragma unroll
+        for (int e = 0; e < C; ++e) bad |= (uint32_t)!isfinite(__bfloat162float(v0[j * p.v_stride + e])) << e;
+    bad &= odd;
+    if (!__any_sync(kAll, bad != 0)) return;
+    const uint4 *q = reinterpret_cast<const uint4 *>(p.q + (int64_t)(s.q0 + row) * p.q_stride + (int64_t)head * D);
     const __nv_bfloat16 *k0 = p.k + (int64_t)s.k0 * p.k_stride + (int64_t)kvh * D;
-    const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
-    for (int d0 = 0; d0 < DV; d0 += 16) {
-        float acc[16] = {};
-        for (int j = from; j < seen; ++j) {
+    float acc[C] = {}, m = -INFINITY, l = 0.f;
+    for (int j1 = seen; j1 > from; j1 -= 32) {
+        const int j0 = max(from, j1 - 32), n = j1 - j0;
+        float score = -INFINITY;  // of this lane's key
+        if (lane < n) {
+            const uint4 *k = reinterpret_cast<const uint4 *>(k0 + (j0 + lane) * p.k_stride);
             float dot = 0.f;
-            for (int d = 0; d < D; ++d) dot = fmaf(__bfloat162float(q[d]), __bfloat162float(k0[j * p.k_stride + d]), dot);
-            const float w = ex2(fmaf(dot, c, -m));
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {
+                float a[8], b[8];
+                Vec16<__nv_bfloat16>::load(__ldg(q + i), a);
+                Vec16<__nv_bfloat16>::load(__ldg(k + i), b);
 #pragma unroll
-            for (int d = 0; d < 16; ++d) acc[d] = fmaf(w, __bfloat162float(v0[j * p.v_stride + d0 + d]), acc[d]);
+                for (int e = 0; e < 8; ++e) dot = fmaf(a[e], b[e], dot);
+            }
+            score = dot * c;
         }
+        float most = score;
 #pragma unroll
-        for (int d = 0; d < 16; ++d) {
-            if (part)
-                part[d0 + d] = acc[d];
-            else
-                st_out(p.o, ((int64_t)(s.q0 + row) * p.Hq + head) * DV + d0 + d, acc[d] * inv, p.o_bf16);
+        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, o));
+        most = fmaxf(most, m);
+        const float f = most == -INFINITY ? 1.f : ex2(m - most), w = ex2(score - (most == -INFINITY ? 0.f : most));
+        m = most;
+        float sum = w;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+        l = fmaf(l, f, sum);
+#pragma unroll
+        for (int e = 0; e < C; ++e) acc[e] *= f;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float wi = __shfl_sync(kAll, w, i);
+#pragma unroll
+            for (int e = 0; e < C; ++e) acc[e] = fmaf(wi, __bfloat162float(v0[(j0 + i) * p.v_stride + e]), acc[e]);
+        }
+        bool open = false;
+#pragma unroll
+        for (int e = 0; e < C; ++e) open |= (bad >> e & 1) && !isnan(acc[e]);
+        if (!__any_sync(kAll, open)) break;
+    }
+    const float f = part ? (m == -INFINITY ? 0.f : ex2(m - part_m)) : l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < C; ++e) {
+        if (!(bad >> e & 1)) continue;
+        if (part)
+            part[d0 + e] = acc[e] * f;
+        else
+            st_out(p.o, out + e, acc[e] * f, p.o_bf16);
+    }
+}
+
+// The same for the rows of all of a softmax warp's items, which it has written.
+template <int D, int DV, bool SPLIT>
+__device__ __forceinline__ void rescue_rows(const Args &a) {
+    const PromptParams &p = a.p;
+    const int warp = threadIdx.x >> 5, t = warp >> 2;
+    UnitSearch units;
+    for (int k = 0;; ++k) {
+        const Item it = item_of<SPLIT>(a, units, k);
+        if (!it.found) break;
+        const Seq s = it.s;
+        const int row0 = first_row(a, it, t), head = a.pair_heads ? 2 * it.head + t : it.head;
+        const int from = SPLIT ? it.lo * kTile : 0, end = min(s.nk, from + blocks_of<SPLIT>(a, it, s, t) * kTile);
+        float *part = SPLIT ? p.ws + (int64_t)it.place * kPartFloats<DV> : nullptr;
+        for (int r = (warp & 3) * 32; r < (warp & 3) * 32 + 32 && row0 + r < s.nq; ++r) {
+            const int seen = max(0, min(end, row0 + r + 1 + s.nk - s.nq));
+            if (SPLIT && seen <= from) continue;  // the part's sums of this row are not read
+            rescue_row<D, DV>(p, s, row0 + r, head, from, seen, end, p.scale * kLog2e,
+                              SPLIT ? part + (t * kTile + r) * DV : nullptr,
+                              SPLIT ? part[2 * kTile * DV + t * kTile + r] : 0.f);
         }
     }
 }
@@ -424,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item *slots = reinterpret_cast<Item *>(p_free + 2);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(slots + 2);
     volatile int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);  // a bounded wait gave up
+    volatile int *spoiled = abort_flag + 1;  // a row came out NaN
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (SPLIT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -450,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(v_empty + i, 2);
         }
         mbar_init(v_raw, 1);
-        *abort_flag = 0;
+        *abort_flag = *spoiled = 0;
         fence_mbar_init();
     }
     if (warp == kTmaWarp && lane < 3)
@@ -477,30 +579,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait_copy = [&](uint64_t *bar, uint32_t parity) { return wait_for(bar, parity, p.polls); };
     // The same where the warp's lanes have to go on or stop together.
     auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-    auto tile_row = [&](const Item &it, int t) { return a.pair_heads ? it.row0 : it.row0 + t * kTile; };
-    // Key blocks of an item that its tile t sees.
-    auto tile_blocks = [&](const Item &it, const Seq &s, int t) {
-        const int r = tile_row(it, t), last = min(r + kTile, s.nq) - 1;
-        if (r >= s.nq) return 0;
-        const int seen = max(0, min(s.nk, last + 1 + (s.nk - s.nq)));
-        const int n = (seen + kTile - 1) / kTile;
-        return SPLIT ? max(0, min(n, it.hi) - it.lo) : n;
-    };
-    // This CTA's k-th work item; one warp.
-    auto find_item = [&](UnitSearch &units, int k) {
-        const int64_t i = (int64_t)k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        const int u = SPLIT ? (int)i / a.parts : (int)i, part = SPLIT ? (int)i - u * a.parts : 0;
-        Item it = {{0, 0, 0, 0}, 0, 0, u % a.n_heads, 0, INT_MAX, (int)i};
-        int seq = 0;
-        if (i < a.items) it.found = units.find(p, a.pair_heads ? 7 : 8, u / a.n_heads, seq, it.row0);
-        if (it.found) it.s = seq_of(p, seq);
-        if (SPLIT && it.found) {
-            const int nb = max(tile_blocks(it, it.s, 0), tile_blocks(it, it.s, 1));
-            it.lo = (int)((int64_t)nb * part / a.parts);
-            it.hi = (int)((int64_t)nb * (part + 1) / a.parts);
-        }
-        return it;
-    };
+    auto tile_row = [&](const Item &it, int t) { return first_row(a, it, t); };
+    auto tile_blocks = [&](const Item &it, const Seq &s, int t) { return blocks_of<SPLIT>(a, it, s, t); };
+    auto find_item = [&](UnitSearch &units, int k) { return item_of<SPLIT>(a, units, k); };
     // The same from the item warp, for a warp that follows them all; false when a wait gave up.
     auto see_item = [&](int k) { return wait_all(i_full + (k & 1), (k >> 1) & 1); };
     auto leave_item = [&](int k) {
@@ -961,10 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         p.lse[out] = lse;
                     }
                     const float2 any = add2(add2(odd[0], odd[1]), add2(odd[2], odd[3]));
-                    const int from = SPLIT ? it.lo * kTile : 0;
-                    if (isnan(any.x + any.y) && ok)
-                        rescue_row<D, DV>(p, s, row, head, from, from + seen, from / kTile + nt, m, l, copysignf(c, p.scale),
-                                          SPLIT ? part + (t * kTile + m_row) * DV : nullptr);
+                    if (isnan(any.x + any.y)) *spoiled = 1;
                 }
             }
             ok = ok && more;
@@ -991,9 +1069,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     fence_before_sync();
-    if (__syncthreads_or(failed) && threadIdx.x == 0) atomicAdd(&g_attn_prompt_timeouts, 1);
+    const bool gave_up = __syncthreads_or(failed);
+    if (gave_up && threadIdx.x == 0) atomicAdd(&g_attn_prompt_timeouts, 1);
     fence_after_sync();
     if (warp == kMmaWarp) tmem_dealloc(tb, 512);
+    // Here no warp waits for another any more, however many keys such a row sees.
+    if (warp < kMmaWarp && !gave_up && *spoiled) rescue_rows<D, DV, SPLIT>(a);
 }
 
 // Joins the parts of a unit and head: `rows` of their 2 x 128 rows a CTA, four channels a thread;
