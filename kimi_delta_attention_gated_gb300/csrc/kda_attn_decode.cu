@@ -14,9 +14,13 @@
 // lane takes 16 contiguous bytes of a row and no transposition through shared memory is
 // needed; P goes from the one product's layout to the other's by movmatrix.
 //
-// The value scale is folded into P: with M >= max_j (s_j + log2 vs_j), e_j = 2^(s_j - M) is
-// summed for the denominator and e_j * vs_j <= 2^kSlack is rounded to f16 for the product,
-// so pages of very different scales share one accumulator.
+// The value scale is folded into P: with M the largest s_j + log2 vs_j so far less kTop,
+// e_j = 2^(s_j - M) is summed for the denominator and e_j * vs_j, at most 2^15, is rounded to f16
+// for the product, so pages of very different scales share one accumulator.  f16 takes up to
+// 2^-25 from a weight below 2^-14.  That is nothing beside sums that hold a weight of 2^kTop, unless
+// its value is near zero (a first token that takes nearly all the weight may have such a value):
+// the output is then what the others make of it.  So a warp whose sums come out that small
+// goes through its steps again (again_with_rest).
 //
 // Work split.  All (sequence, head, 32 tokens) steps are numbered in one line, kPad places
 // before each head standing for what a head costs beside its steps, and the line is cut into
@@ -33,7 +37,7 @@
 //
 // 256 sequences of about 1000 tokens, 64 heads over 8 of 128, pages of 64: 98 us, 5.4 TB/s (80 % of
 // a copy's rate); 8 of [8192, 131072] tokens, 40 heads over 8, pages of 16: 114 us, 5.9 TB/s (87 %);
-// one of 1000 tokens: 8.7 us, both launches and their latencies.  The stream itself runs at
+// one of 1000 tokens: 9.0 us, both launches and their latencies.  The stream itself runs at
 // 6.0 to 6.3 TB/s; the rest is about 8 us of finding the pieces, first copies, and joining.
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -51,7 +55,10 @@ constexpr int kJoinMost = 512;   // threads of a joining CTA at most
 constexpr int kStep = 32;       // tokens of a step
 constexpr int kPad = 6;         // a head's own cost in steps
 constexpr int kMinPiece = 8;   // places of a CTA at least
-constexpr float kSlack = 8.f;   // the maximum in use may lie this far below the true one (log2)
+constexpr float kSlack = 4.f;   // the maximum in use may lie this far below the true one (log2)
+constexpr float kTop = 10.f;    // a weight at that maximum is 2^kTop, times the scale's fraction below 2
+constexpr int kUp = 40;         // 2^-25 times 2^kUp is 2^15, and down to 2^-54 it stays normal in f16
+constexpr float kLeast = 6.103515625e-5f;  // 2^-14, the least normal f16 number
 constexpr float kNegInf = -INFINITY;
 
 __device__ int g_attn_decode_timeouts = 0;
@@ -124,6 +131,150 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// The lesser of two pairs of f16 numbers, each by itself (of a NaN and a number the number).
+__device__ __forceinline__ uint32_t min_half2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Adds the product of 16 tokens' weights, packed to f16 in the layout of the scores, with their
+// values at v (v_at: this lane's pieces; live: tokens there are); REST: the weights are 2^kUp times
+// what they stand for.
+template <int D, int NT, bool REST>
+__device__ __forceinline__ void add_products(float (&acc)[NT][D / 16][4], const uint32_t (&w)[NT][2], const uint8_t *v, int v_at0,
+                                             int v_at1, int live) {
+    using F = Cfg<D, NT>;
+    const int t = threadIdx.x & 3;
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) pb[nt][e] = transpose8(w[nt][e]);
+    uint32_t vw[4][F::VB / 4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint8_t *at = v + ((i & 1) ? v_at1 : v_at0) + (i >> 1) * (F::HALF / 2);
+        if (F::VB == 16) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(at);
+            vw[i][0] = x.x;
+            vw[i][1] = x.y;
+            vw[i][F::VB / 4 - 2] = x.z;
+            vw[i][F::VB / 4 - 1] = x.w;
+        } else {
+            const uint2 x = *reinterpret_cast<const uint2 *>(at);
+            vw[i][0] = x.x;
+            vw[i][1] = x.y;
+        }
+    }
+    if (live < 16) {  // a zero weight would turn a NaN behind the last token into one
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (2 * t + (i & 1) + (i >> 1) * 8 >= live) {
+#pragma unroll
+                for (int x = 0; x < F::VB / 4; ++x) vw[i][x] = 0;
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < F::VB / 4; ++i) {
+        const uint32_t x = __byte_perm(vw[0][i], vw[1][i], 0x5140), y = __byte_perm(vw[0][i], vw[1][i], 0x7362);
+        const uint32_t z = __byte_perm(vw[2][i], vw[3][i], 0x5140), u = __byte_perm(vw[2][i], vw[3][i], 0x7362);
+        uint32_t x0, x1, y0, y1, z0, z1, u0, u1;
+        widen(x, x0, x1);
+        widen(y, y0, y1);
+        widen(z, z0, z1);
+        widen(u, u0, u1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if (!REST) {
+                mma_f16(acc[nt][2 * i], x0, x1, z0, z1, pb[nt][0], pb[nt][1]);
+                mma_f16(acc[nt][2 * i + 1], y0, y1, u0, u1, pb[nt][0], pb[nt][1]);
+                continue;
+            }
+            float a[4] = {}, b[4] = {};
+            mma_f16(a, x0, x1, z0, z1, pb[nt][0], pb[nt][1]);
+            mma_f16(b, y0, y1, u0, u1, pb[nt][0], pb[nt][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                acc[nt][2 * i][e] = fmaf(a[e], exp2_int(-kUp), acc[nt][2 * i][e]);
+                acc[nt][2 * i + 1][e] = fmaf(b[e], exp2_int(-kUp), acc[nt][2 * i + 1][e]);
+            }
+        }
+    }
+}
+
+// A warp's sums over its steps s0, s0 + kWarps, .. of a unit anew, from global memory: the rows' M
+// are known, and what f16 takes from a weight below 2^-14 is multiplied too, 2^kUp times as large.
+// Seldom taken, and slow; a check in each step, with the rest at once, cost every call 5 to 15 %
+// with groups above 8, and a look at the weights' least alone 5 %.
+template <int D, int NT>
+struct Again {
+    uint32_t q[NT][D / 16][2];
+    float row_scale[NT][2], M[NT][2], acc[NT][D / 16][4];
+};
+template <int D, int NT>
+__device__ __noinline__ void again_with_rest(const DecodeParams &p, int n, int head, int len, int s0, int s1, Again<D, NT> &a) {
+    using F = Cfg<D, NT>;
+    const PagedCache &c = p.c;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float acc[NT][F::MT][4] = {};
+    for (int h = 2 * s0; h < 2 * s1; h += h & 1 ? 2 * kWarps - 1 : 1) {  // halves of steps
+        const int live = len - 16 * h;
+        if (live <= 0) break;
+        const int page = __ldg(c.block_table + (int64_t)n * c.max_blocks + (16 * h >> c.p_shift));
+        const bool good = (uint32_t)page < (uint32_t)c.n_pages;
+        const int64_t block = (int64_t)(good ? page : 0) * c.Hk + head, at = ((block << c.p_shift) + (16 * h & (c.P - 1))) * D;
+        const float ks = good ? c.k_scale[block] : __int_as_float(0x7fc00000), vs = c.v_scale[block];
+        const uint8_t *v = c.v + at;
+        const int v0 = 2 * t * D + g * F::VB;
+        uint32_t codes = 0;  // values that are all zero (a cache not filled yet) add nothing
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int x = 0; x < F::VB; x += 4)
+                codes |= *reinterpret_cast<const uint32_t *>(v + v0 + (i & 1) * D + (i >> 1) * 8 * D + x);
+        if (good && vs == vs && !__any_sync(0xffffffffu, codes & 0x7F7F7F7Fu)) continue;
+        float S[NT][4] = {};
+#pragma unroll
+        for (int j = 0; j < F::KJ; ++j) {
+            const uint8_t *k = c.k + at + g * D + 16 * (F::KJ * t + j);
+            const uint4 x = *reinterpret_cast<const uint4 *>(k), y = *reinterpret_cast<const uint4 *>(k + 8 * D);
+            const uint32_t wa[4] = {x.x, x.y, x.z, x.w}, wb[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t a0, a1, a2, a3;
+                widen(wa[i], a0, a2);
+                widen(wb[i], a1, a3);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_f16(S[nt], a0, a1, a2, a3, a.q[nt][4 * j + i][0], a.q[nt][4 * j + i][1]);
+            }
+        }
+        uint32_t x[NT][2], r[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float w[4], z[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float m = a.M[nt][e & 1];
+                w[e] = g + (e >> 1) * 8 < live ? ex2(S[nt][e] * (a.row_scale[nt][e & 1] * ks) - (m == kNegInf ? 0.f : m)) * vs : 0.f;
+                z[e] = w[e] < kLeast ? (w[e] - __half2float(__float2half_rn(w[e]))) * exp2_int(kUp) : 0.f;
+            }
+            x[nt][0] = pack_half(w[0], w[1]);
+            x[nt][1] = pack_half(w[2], w[3]);
+            r[nt][0] = pack_half(z[0], z[1]);
+            r[nt][1] = pack_half(z[2], z[3]);
+        }
+        add_products<D, NT, false>(acc, x, v, v0, v0 + D, live);
+        add_products<D, NT, true>(acc, r, v, v0, v0 + D, live);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < F::MT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a.acc[nt][j][e] = acc[nt][j][e];
 }
 
 // Tokens and steps of sequence n, its length clamped to what its block table can hold.
@@ -477,8 +628,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    over |= fmaxf(S[h][nt][0], S[h][nt][2]) > M[nt][0] + (kSlack - ev[h]) ||
-                            fmaxf(S[h][nt][1], S[h][nt][3]) > M[nt][1] + (kSlack - ev[h]);
+                    over |= fmaxf(S[h][nt][0], S[h][nt][2]) > M[nt][0] + (kTop + kSlack - ev[h]) ||
+                            fmaxf(S[h][nt][1], S[h][nt][3]) > M[nt][1] + (kTop + kSlack - ev[h]);
             }
             if (__any_sync(0xffffffffu, over)) {  // raise the maximum and bring the sums to it
 #pragma unroll
@@ -489,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                        m = fmaxf(m, M[nt][e]);
+                        m = fmaxf(m - kTop, M[nt][e]);
                         const float f = m == kNegInf ? 1.f : ex2(M[nt][e] - m);
                         M[nt][e] = m;
                         l[nt][e] *= f;
@@ -502,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                uint32_t pb[NT][2];
+                uint32_t x[NT][2];
                 const float vscale = tail && s * kStep + 16 * h >= cur.len ? 0.f : vs[h];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -511,53 +662,47 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
                                 e3 = ex2(S[h][nt][3] - m1);
                     l[nt][0] += e0 + e2;
                     l[nt][1] += e1 + e3;
-                    pb[nt][0] = transpose8(pack_half(e0 * vscale, e1 * vscale));
-                    pb[nt][1] = transpose8(pack_half(e2 * vscale, e3 * vscale));
+                    x[nt][0] = pack_half(e0 * vscale, e1 * vscale);
+                    x[nt][1] = pack_half(e2 * vscale, e3 * vscale);
                 }
-                const uint8_t *v = slot + F::KBYTES + h * F::HALF;
-                uint32_t vw[4][F::VB / 4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint8_t *at = v + v_at[i & 1] + (i >> 1) * (F::HALF / 2);
-                    if (F::VB == 16) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(at);
-                        vw[i][0] = x.x;
-                        vw[i][1] = x.y;
-                        vw[i][F::VB / 4 - 2] = x.z;
-                        vw[i][F::VB / 4 - 1] = x.w;
-                    } else {
-                        const uint2 x = *reinterpret_cast<const uint2 *>(at);
-                        vw[i][0] = x.x;
-                        vw[i][1] = x.y;
-                    }
-                }
-                if (tail) {  // a zero weight would turn a NaN behind the last token into one
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (s * kStep + 16 * h + 2 * t + (i & 1) + (i >> 1) * 8 >= cur.len) {
-#pragma unroll
-                            for (int x = 0; x < F::VB / 4; ++x) vw[i][x] = 0;
-                        }
-                }
-#pragma unroll
-                for (int i = 0; i < F::VB / 4; ++i) {
-                    const uint32_t x = __byte_perm(vw[0][i], vw[1][i], 0x5140), y = __byte_perm(vw[0][i], vw[1][i], 0x7362);
-                    const uint32_t z = __byte_perm(vw[2][i], vw[3][i], 0x5140), w = __byte_perm(vw[2][i], vw[3][i], 0x7362);
-                    uint32_t x0, x1, y0, y1, z0, z1, w0, w1;
-                    widen(x, x0, x1);
-                    widen(y, y0, y1);
-                    widen(z, z0, z1);
-                    widen(w, w0, w1);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(acc[nt][2 * i], x0, x1, z0, z1, pb[nt][0], pb[nt][1]);
-                        mma_f16(acc[nt][2 * i + 1], y0, y1, w0, w1, pb[nt][0], pb[nt][1]);
-                    }
-                }
+                add_products<D, NT, false>(acc, x, slot + F::KBYTES + h * F::HALF, v_at[0], v_at[1],
+                                           tail ? cur.len - s * kStep - 16 * h : 16);
             }
             if (++rd == F::DEPTH) rd = 0, rd_phase ^= 1;
             __syncwarp();  // every lane has read the slot: it is filled again
             copy_step();
+        }
+        {
+            // f16 takes 2^-25 at most from a weight below 2^-14, and a value's code is at most 448: over this warp's
+            // tokens, as many as 32 times `enough` says, less than 2^-11 (half a step of f16) of `enough`.
+            const float enough = (float)((cur.s1 - cur.s0) / kWarps + 1);
+            float sums = INFINITY;  // the least row's largest sum among this lane's channels
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float a = 0.f;
+#pragma unroll
+                    for (int j = 0; j < F::MT; ++j) a = fmaxf(fmaxf(a, fabsf(acc[nt][j][e])), fabsf(acc[nt][j][e + 2]));
+                    sums = fminf(sums, a);
+                }
+            if (__any_sync(0xffffffffu, sums < enough) && cur.s0 + warp < cur.s1 && !failed) {
+                Again<D, NT> x;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int i = 0; i < F::KJ * 4; ++i) x.q[nt][i][0] = qf[nt][i][0], x.q[nt][i][1] = qf[nt][i][1];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) x.row_scale[nt][e] = row_scale[nt][e], x.M[nt][e] = M[nt][e];
+                }
+                again_with_rest<D, NT>(p, cur.n, cur.head, cur.len, cur.s0 + warp, cur.s1, x);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < F::MT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[nt][j][e] = x.acc[nt][j][e];
+            }
         }
         if (failed) {  // a copy's wait gave up: the sums stand for nothing
 #pragma unroll

@@ -1,0 +1,95 @@
+"""GPU tests of the decode's weights and sums over their whole range (kda_attn_decode): tokens far above
+all others, whose values are zero.  Tolerances as in test_attn_decode_gpu.py: half a step of f16 of the
+sum of p |v|, whatever the largest weight is."""
+import pytest
+import torch
+
+import kimi_delta_attention_gated_gb300 as kda
+from tests.test_attn_decode_gpu import gen, verify
+from tests.test_kv_append_gpu import filled_cache, table_for
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from kimi_delta_attention_gated_gb300 import build
+    build.build()
+
+
+def attend(q, cache, table, lens, P, wide, **kw):
+    """With the table as it is, or as wide as a server's (the cut form)."""
+    if wide:
+        table = torch.cat([table, torch.full((len(lens), 2048 // P), -1, dtype=torch.int32)], 1)
+    o, lse = kda.attn_decode(q, cache, table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), return_lse=True, **kw)
+    torch.cuda.synchronize()
+    return o, lse
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("at", [0, 37])
+@pytest.mark.parametrize("nats", [6.0, 12.0, 15.0, 18.0, 22.0, 40.0])
+@pytest.mark.parametrize("Hk,G,D,P", [(2, 4, 128, 16), (1, 1, 64, 64), (1, 16, 128, 32), (2, 12, 64, 16)])
+def test_one_token_far_above_the_others(Hk, G, D, P, nats, at, wide):
+    """A first (or a middle) token takes nearly all the weight and has a value of zero: the output is what
+    the others make of it.  Every second query head sees it half as far above."""
+    lens = [260, 64, 1000, 33][: 2 if at else 4]
+    lens = [max(n, at + 3) for n in lens]
+    table, pages = table_for(lens, P, 51)
+    cache = filled_cache(pages, Hk, P, D, 51, (-4, -3))
+    q = torch.full((len(lens), Hk * G, D), 1.0, device="cuda")
+    q[:, 1::2] = 0.5
+    # scores: D * (the channels' mean of code * scale) * D^-0.5; others' keys hardly reach one nat
+    cache.k.copy_((torch.randn(cache.k.shape, generator=gen(52), device="cuda") * 8).to(torch.float8_e4m3fn))
+    for n in range(len(lens)):
+        page = int(table[n, at // P])
+        code = nats * D ** -0.5 / cache.k_scale[page]  # one for each head
+        cache.k[page, :, at % P] = code[:, None].expand(Hk, D).to(torch.float8_e4m3fn)
+        cache.v[page, :, at % P] = torch.zeros((Hk, D), device="cuda").to(torch.float8_e4m3fn)
+    q = q.bfloat16()
+    o, lse = attend(q, cache, table, lens, P, wide, out_dtype=torch.float32)
+    assert o.isfinite().all()
+    verify(o, lse, q, cache, table, lens)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("D,P,G", [(128, 64, 4), (64, 16, 16)])
+def test_weights_of_every_size(D, P, G, wide):
+    """Scores that fall by a fifth of a nat from token to token, from 100 nats down, and every value small
+    where the weight is large: v grows as the weight falls, over 14 powers of two."""
+    n, Hk = 500, 1
+    table, pages = table_for([n], P, 53)
+    cache = filled_cache(pages, Hk, P, D, 53, (-4, -3))
+    cache.k.zero_()
+    drop = torch.linspace(0, 1, n)
+    codes = (100.0 * (1 - drop) * D ** 0.5 / 2 ** -4 / D)  # in every channel, the query being one
+    for j in range(n):
+        page, off = int(table[0, j // P]), j % P
+        cache.k_scale[page], cache.v_scale[page] = 2.0 ** -4, 2.0 ** (4 * (j // P) * P // 128)
+        cache.k[page, :, off] = codes[j].expand(Hk, D).cuda().to(torch.float8_e4m3fn)
+    q = torch.full((1, Hk * G, D), 1.0, device="cuda").bfloat16() * torch.linspace(0.1, 1, Hk * G, device="cuda")[None, :, None]
+    q = q.bfloat16()
+    o, lse = attend(q, cache, table, [n], P, wide, out_dtype=torch.float32)
+    assert o.isfinite().all()
+    verify(o, lse, q, cache, table, [n])
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("D,G", [(128, 4), (64, 12)])
+def test_small_and_zero_values(D, G, wide):
+    """Values that use little of the codes' range under a scale of one, values that are all zero, and
+    both behind a token that takes the weight."""
+    lens, Hk, P = [700, 700, 90], 2, 32
+    table, pages = table_for(lens, P, 54)
+    cache = filled_cache(pages, Hk, P, D, 54, (-4, -3))
+    cache.v_scale.fill_(1.0)
+    cache.v.copy_((0.02 * torch.randn(cache.v.shape, generator=gen(55), device="cuda")).to(torch.float8_e4m3fn))
+    cache.v.view(torch.uint8)[table[1, : -(-lens[1] // P)].long().cuda()] = 0
+    q = (3 * torch.randn((len(lens), Hk * G, D), generator=gen(56), device="cuda")).bfloat16()
+    o, lse = attend(q, cache, table, lens, P, wide, out_dtype=torch.float32)
+    verify(o, lse, q, cache, table, lens)
+    assert (o[1] == 0).all()
+    cache.v_scale[int(table[1, 3]), 1] = float("nan")  # zero codes under a scale that is no number
+    o2, lse2 = attend(q, cache, table, lens, P, wide, out_dtype=torch.float32)
+    assert o2[1, G:].isnan().all() and torch.equal(o2[1, :G], o[1, :G]) and torch.equal(o2[[0, 2]], o[[0, 2]])
+    assert torch.equal(lse2[[0, 2]], lse[[0, 2]]) and torch.equal(lse2[1, :G], lse[1, :G])
