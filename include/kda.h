@@ -561,7 +561,8 @@ kda_status kda_kv_append(const void *k, int64_t k_stride, const void *v, int64_t
  * K_j and V_j the cached (code * scale) rows of head i / (q_heads / kv_heads).
  *
  *   q         [n_seqs, q_heads, dim] bf16, q_stride apart; q_heads a multiple of kv_heads
- *   cache     as kda_kv_append; scales may be any positive floats
+ *   cache     as kda_kv_append; scales may be any positive floats, value scales from 2^-126 to
+ *             2^120
  *   seq_lens  [n_seqs] int32: tokens to attend to (with the new one), clamped to
  *             [0, max_blocks * page_size].  0 gives a zero row and lse -INFINITY.
  *   o         [n_seqs, q_heads, dim] o_dtype

@@ -14,8 +14,8 @@
 // lane takes 16 contiguous bytes of a row and no transposition through shared memory is
 // needed; P goes from the one product's layout to the other's by movmatrix.
 //
-// The value scale is folded into P: with M the largest s_j + log2 vs_j so far less kTop,
-// e_j = 2^(s_j - M) is summed for the denominator and e_j * vs_j, at most 2^15, is rounded to f16
+// The value scale is folded into P: with M the largest s_j + log2 vs_j so far less kRef,
+// e_j = 2^(s_j - M) is summed for the denominator and e_j * vs_j * 2^(kTop - kRef), at most 2^15, is rounded to f16
 // for the product, so pages of very different scales share one accumulator.  f16 takes up to
 // 2^-25 from a weight below 2^-14.  That is nothing beside sums that hold a weight of 2^kTop, unless
 // its value is near zero (a first token that takes nearly all the weight may have such a value):
@@ -56,7 +56,12 @@ constexpr int kStep = 32;       // tokens of a step
 constexpr int kPad = 6;         // a head's own cost in steps
 constexpr int kMinPiece = 8;   // places of a CTA at least
 constexpr float kSlack = 4.f;   // the maximum in use may lie this far below the true one (log2)
-constexpr float kTop = 10.f;    // a weight at that maximum is 2^kTop, times the scale's fraction below 2
+constexpr int kTop = 10;        // a weight at that maximum is 2^kTop, times the scale's fraction below 2
+// How far M lies below the maximum, and what the value scales are multiplied with to make up for it.  Sums of
+// 2^(s - M) then stay within fp32 for value scales from 2^-126 to 2^120: M goes by a scale of at least
+// 2^kLeastScale, so that each is at most 2^(kSlack + kRef - kLeastScale) = 2^94 (2^31 of them 2^125),
+// and at least 2^(kRef - 120) where the scale decides, 2^24 above what is flushed.
+constexpr int kRef = 18, kLeastScale = -72;
 constexpr int kUp = 40;         // 2^-25 times 2^kUp is 2^15, and down to 2^-54 it stays normal in f16
 constexpr float kLeast = 6.103515625e-5f;  // 2^-14, the least normal f16 number
 constexpr float kNegInf = -INFINITY;
@@ -226,7 +231,8 @@ __device__ __noinline__ void again_with_rest(const DecodeParams &p, int n, int h
         const int page = __ldg(c.block_table + (int64_t)n * c.max_blocks + (16 * h >> c.p_shift));
         const bool good = (uint32_t)page < (uint32_t)c.n_pages;
         const int64_t block = (int64_t)(good ? page : 0) * c.Hk + head, at = ((block << c.p_shift) + (16 * h & (c.P - 1))) * D;
-        const float ks = good ? c.k_scale[block] : __int_as_float(0x7fc00000), vs = c.v_scale[block];
+        const float ks = good ? c.k_scale[block] : __int_as_float(0x7fc00000),
+                    vs = c.v_scale[block] * exp2_int(kTop - kRef);
         const uint8_t *v = c.v + at;
         const int v0 = 2 * t * D + g * F::VB;
         uint32_t codes = 0;  // values that are all zero (a cache not filled yet) add nothing
@@ -276,6 +282,11 @@ __device__ __noinline__ void again_with_rest(const DecodeParams &p, int n, int h
 #pragma unroll
             for (int e = 0; e < 4; ++e) a.acc[nt][j][e] = acc[nt][j][e];
 }
+
+// The factor that brings sums from one reference to another, as its square root: value scales far apart
+// put references more than 126 powers of two apart, while the sums' sizes make up for it.
+__device__ __forceinline__ float root_factor(float from, float to) { return to == kNegInf ? 1.f : ex2(0.5f * (from - to)); }
+__device__ __forceinline__ float bring(float x, float root) { return x * root * root; }
 
 // Tokens and steps of sequence n, its length clamped to what its block table can hold.
 __device__ __forceinline__ int tokens_of(const PagedCache &c, int n) {
@@ -354,7 +365,7 @@ __device__ __forceinline__ void next_segment(const PagedCache &c, int U, int par
 // Four channels of an output row (and the row's lse) from its sums.
 template <int D>
 __device__ __forceinline__ void write_row(const DecodeParams &p, int64_t row, int d, float4 a, float m, float sum) {
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : exp2_int(kRef - kTop) / sum;
     if (p.o_bf16) {
         uint2 w;
         w.x = pack_bf16x2(a.x * inv, a.y * inv);
@@ -606,7 +617,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
             float ev[2];  // reference of the value scale: its binary exponent
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                ev[h] = (float)((int)((__float_as_uint(vs[h]) >> 23) & 0xFFu) - 127);
+                const int be = (int)(__float_as_uint(vs[h]) >> 23) & 0xFF;
+                ev[h] = (float)(be == 0xFF ? 0 : max(be - 127, kLeastScale));  // a NaN moves nothing
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const float c0 = row_scale[nt][0] * ks[h], c1 = row_scale[nt][1] * ks[h];
@@ -628,8 +640,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    over |= fmaxf(S[h][nt][0], S[h][nt][2]) > M[nt][0] + (kTop + kSlack - ev[h]) ||
-                            fmaxf(S[h][nt][1], S[h][nt][3]) > M[nt][1] + (kTop + kSlack - ev[h]);
+                    over |= fmaxf(S[h][nt][0], S[h][nt][2]) > M[nt][0] + (kRef + kSlack - ev[h]) ||
+                            fmaxf(S[h][nt][1], S[h][nt][3]) > M[nt][1] + (kRef + kSlack - ev[h]);
             }
             if (__any_sync(0xffffffffu, over)) {  // raise the maximum and bring the sums to it
 #pragma unroll
@@ -640,21 +652,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                        m = fmaxf(m - kTop, M[nt][e]);
-                        const float f = m == kNegInf ? 1.f : ex2(M[nt][e] - m);
+                        m = fmaxf(m - kRef, M[nt][e]);
+                        const float f = root_factor(M[nt][e], m);
                         M[nt][e] = m;
-                        l[nt][e] *= f;
+                        l[nt][e] = bring(l[nt][e], f);
 #pragma unroll
                         for (int j = 0; j < F::MT; ++j) {
-                            acc[nt][j][e] *= f;
-                            acc[nt][j][e + 2] *= f;
+                            acc[nt][j][e] = bring(acc[nt][j][e], f);
+                            acc[nt][j][e + 2] = bring(acc[nt][j][e + 2], f);
                         }
                     }
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t x[NT][2];
-                const float vscale = tail && s * kStep + 16 * h >= cur.len ? 0.f : vs[h];
+                const float vscale = tail && s * kStep + 16 * h >= cur.len ? 0.f : vs[h] * exp2_int(kTop - kRef);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const float m0 = M[nt][0] == kNegInf ? 0.f : M[nt][0], m1 = M[nt][1] == kNegInf ? 0.f : M[nt][1];
@@ -763,14 +775,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
                     for (int e = 0; e < 2; ++e) {
                         const int r = nt * 8 + 2 * t + e;
                         const float mo = buf_m[r], m = fmaxf(M[nt][e], mo);
-                        const float fa = m == kNegInf ? 1.f : ex2(M[nt][e] - m), fb = m == kNegInf ? 1.f : ex2(mo - m);
+                        const float fa = root_factor(M[nt][e], m), fb = root_factor(mo, m);
                         M[nt][e] = m;
-                        l[nt][e] = l[nt][e] * fa + buf_l[r] * fb;
+                        l[nt][e] = bring(l[nt][e], fa) + bring(buf_l[r], fb);
 #pragma unroll
                         for (int j = 0; j < F::MT; ++j) {
                             const float2 x = *reinterpret_cast<const float2 *>(buf + r * F::PITCH + 2 * j);
-                            acc[nt][j][e] = acc[nt][j][e] * fa + x.x * fb;
-                            acc[nt][j][e + 2] = acc[nt][j][e + 2] * fa + x.y * fb;
+                            acc[nt][j][e] = bring(acc[nt][j][e], fa) + bring(x.x, fb);
+                            acc[nt][j][e + 2] = bring(acc[nt][j][e + 2], fa) + bring(x.y, fb);
                         }
                     }
                 __syncwarp();  // every lane has read M and l
@@ -781,11 +793,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
                 for (int i = tid & 63; i < F::ROWS * (D / 4); i += 64) {
                     const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
                     const float ma = merge_m[r], mb = merge_m[F::ROWS + r], m = fmaxf(ma, mb);
-                    const float fa = m == kNegInf ? 1.f : ex2(ma - m), fb = m == kNegInf ? 1.f : ex2(mb - m);
+                    const float fa = root_factor(ma, m), fb = root_factor(mb, m);
                     const float4 x = *reinterpret_cast<const float4 *>(merge + r * F::PITCH + d);
                     const float4 y = *reinterpret_cast<const float4 *>(merge + (F::ROWS + r) * F::PITCH + d);
-                    const float4 a = make_float4(fa * x.x + fb * y.x, fa * x.y + fb * y.y, fa * x.z + fb * y.z, fa * x.w + fb * y.w);
-                    const float sum = fa * merge_l[r] + fb * merge_l[F::ROWS + r];
+                    const float4 a = make_float4(bring(x.x, fa) + bring(y.x, fb), bring(x.y, fa) + bring(y.y, fb),
+                                                 bring(x.z, fa) + bring(y.z, fb), bring(x.w, fa) + bring(y.w, fb));
+                    const float sum = bring(merge_l[r], fa) + bring(merge_l[F::ROWS + r], fb);
                     if (!whole) {
                         *reinterpret_cast<float4 *>(part + r * D + d) = a;
                         if (d == 0) {
@@ -873,10 +886,11 @@ __global__ void __launch_bounds__(kJoinMost) attn_decode_join_kernel(const __gri
         const float mk = __ldcg(part + F::ROWS * D + r), lk = __ldcg(part + F::ROWS * D + F::ROWS + r);
         const float4 x = __ldcg(reinterpret_cast<const float4 *>(part + r * D + d));
         const float mn = fmaxf(m, mk);
-        const float f = mn == kNegInf ? 1.f : ex2(m - mn), fk = mn == kNegInf ? 1.f : ex2(mk - mn);
+        const float f = root_factor(m, mn), fk = root_factor(mk, mn);
         m = mn;
-        l = l * f + lk * fk;
-        a = make_float4(a.x * f + x.x * fk, a.y * f + x.y * fk, a.z * f + x.z * fk, a.w * f + x.w * fk);
+        l = bring(l, f) + bring(lk, fk);
+        a = make_float4(bring(a.x, f) + bring(x.x, fk), bring(a.y, f) + bring(x.y, fk), bring(a.z, f) + bring(x.z, fk),
+                        bring(a.w, f) + bring(x.w, fk));
     }
     s_acc[tid] = a;
     s_m[tid] = m;
@@ -888,10 +902,10 @@ __global__ void __launch_bounds__(kJoinMost) attn_decode_join_kernel(const __gri
     float sum = 0.f;
     a = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i = 0; i < used; ++i) {
-        const float mk = s_m[tid + i * items], f = m == kNegInf ? 1.f : ex2(mk - m);
+        const float f = root_factor(s_m[tid + i * items], m);
         const float4 x = s_acc[tid + i * items];
-        sum += f * s_l[tid + i * items];
-        a = make_float4(a.x + f * x.x, a.y + f * x.y, a.z + f * x.z, a.w + f * x.w);
+        sum += bring(s_l[tid + i * items], f);
+        a = make_float4(a.x + bring(x.x, f), a.y + bring(x.y, f), a.z + bring(x.z, f), a.w + bring(x.w, f));
     }
     write_row<D>(p, (int64_t)n * p.Hq + h * group + head, d, a, m, sum);
 }

@@ -93,3 +93,36 @@ def test_small_and_zero_values(D, G, wide):
     o2, lse2 = attend(q, cache, table, lens, P, wide, out_dtype=torch.float32)
     assert o2[1, G:].isnan().all() and torch.equal(o2[1, :G], o[1, :G]) and torch.equal(o2[[0, 2]], o[[0, 2]])
     assert torch.equal(lse2[[0, 2]], lse[[0, 2]]) and torch.equal(lse2[1, :G], lse[1, :G])
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("D,P,G", [(128, 16, 4), (64, 64, 16)])
+@pytest.mark.parametrize("exp", [(-126, -110), (-120, -119), (-126, 119), (100, 119), (-75, -65)])
+def test_value_scales_of_any_size(exp, D, P, G, wide):
+    """Value scales from 2^-126 to 2^118, alike and mixed page by page: the weights' sum, and with it the
+    log-sum-exp, does not depend on them."""
+    lens, Hk = [900, 77, 1], 2
+    table, pages = table_for(lens, P, 57)
+    cache = filled_cache(pages, Hk, P, D, 57, (-6, -4))
+    cache.v_scale.copy_(torch.exp2(torch.randint(*exp, cache.v_scale.shape, generator=gen(58), device="cuda").double()).float())
+    assert (cache.v_scale > 0).all() and cache.v_scale.isfinite().all()
+    q = torch.randn((len(lens), Hk * G, D), generator=gen(59), device="cuda").bfloat16()
+    o, lse = attend(q, cache, table, lens, P, wide, out_dtype=torch.float32)
+    assert o.isfinite().all()
+    verify(o, lse, q, cache, table, lens)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_the_log_sum_of_a_head_whose_value_scale_is_no_number(wide):
+    lens, Hk, G, D, P = [300, 60], 2, 4, 64, 16
+    table, pages = table_for(lens, P, 60)
+    cache = filled_cache(pages, Hk, P, D, 60)
+    q = (2 * torch.randn((len(lens), Hk * G, D), generator=gen(61), device="cuda")).bfloat16()
+    o, lse = attend(q, cache, table, lens, P, wide)
+    cache.v_scale[int(table[0, 2]), 1] = float("nan")
+    cache.v_scale[int(table[1, 0]), 0] = float("inf")
+    o2, lse2 = attend(q, cache, table, lens, P, wide)
+    assert o2[0, G:].isnan().all() and not o2[1, :G].isfinite().any()
+    assert torch.equal(o2[0, :G], o[0, :G]) and torch.equal(o2[1, G:], o[1, G:])
+    cache.v_scale.fill_(1.0)
+    verify(attend(q, cache, table, lens, P, wide)[0], lse2, q, cache, table, lens)
