@@ -142,11 +142,12 @@ __device__ __forceinline__ void cos_sin_turn(uint64_t f, float &c, float &s) {
 }
 
 // a * b - c * d with the product's rounding error carried (two extra FMAs): within 1.5 ulp,
-// so an 8-bit code chosen from it rarely differs from the exact value's.
+// so an 8-bit code chosen from it rarely differs from the exact value's.  An infinite product has
+// no such error (inf - inf is NaN, of which fminf makes a number), and the difference stays infinite.
 __device__ __forceinline__ float diff_of_products(float a, float b, float c, float d) {
     const float w = c * d;
     const float e = fmaf(-c, d, w);
-    return fmaf(a, b, -w) + e;
+    return fmaf(a, b, -w) + fminf(e, 3.4028234663852886e38f);
 }
 
 // The pair (a, b) turned: magnitude * (a cos - b sin, b cos + a sin).
