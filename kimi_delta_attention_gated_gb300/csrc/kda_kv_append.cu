@@ -63,7 +63,7 @@ __device__ __forceinline__ int position_of(const AppendParams &p, int64_t t) {
         else
             hi = m - 1;
     }
-    return max(p.c.lens[lo], 0) + (int)(t - p.cu_seqlens[lo]);
+    return max(p.c.lens[lo], 0) + (int)(t - max(p.cu_seqlens[lo], 0));  // clamped as in new_tokens
 }
 
 // One query tile; rows of no sequence are left out.

@@ -1,0 +1,48 @@
+"""GPU tests of an append's positions (kda_kv_append) where cu_seqlens leaves the rows and where places
+pass 2^31: keys and queries of one token turn by the same angle."""
+import pytest
+import torch
+
+import kimi_delta_attention_gated_gb300 as kda
+from tests import attn_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from kimi_delta_attention_gated_gb300 import build
+    build.build()
+
+
+def rows(T, H, D, seed):
+    return torch.randn((T, H, D), generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda").bfloat16()
+
+
+def turned(x, pos, f, mag):
+    want = ref.rotary(ref.f64(x), pos, f.cpu(), mag)
+    return want, ref.HALF_BF16 * want.abs() + ref.ROTARY_ROUNDINGS * ref.HALF_F32 * ref.rotary_size(ref.f64(x), 2 * f.numel(), mag, "half")
+
+
+@pytest.mark.parametrize("Hq,T", [(4, 21), (64, 9000)])  # the second with the queries in a launch of their own
+@pytest.mark.parametrize("cu", [[-5, 10 ** 6], [-(2 ** 31), 8, 2 ** 31 - 1], [-7, -3, 5, 10 ** 6]])
+def test_bounds_are_clamped_for_keys_and_queries(cu, Hq, T):
+    Hk, D, P = 1, 64, 16
+    N, ctx = len(cu) - 1, [3, 100, 40][: len(cu) - 1]
+    lo = [min(max(c, 0), T) for c in cu]
+    pos = torch.cat([torch.arange(c, c + b - a) for c, a, b in zip(ctx, lo[:-1], lo[1:])])
+    assert pos.numel() == T
+    need = [-(-(c + b - a) // P) for c, a, b in zip(ctx, lo[:-1], lo[1:])]
+    table = torch.full((N, max(need)), -1, dtype=torch.int32)
+    at = 0
+    for n, m in enumerate(need):
+        table[n, :m] = torch.arange(at, at + m, dtype=torch.int32)
+        at += m
+    q, k = rows(T, Hq, D, 81), rows(T, Hk, D, 82)
+    f, mag = kda.rotary_inv_freq(D)
+    cache = kda.kv_cache(at, Hk, D, P)
+    qr, kr = kda.kv_append(k, k, cache, table.cuda(), torch.tensor(ctx, dtype=torch.int32, device="cuda"),
+                           cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"), inv_freq=f, magnitude=mag, q=q,
+                           return_k=True)
+    for got, x in ((qr, q), (kr, k)):
+        ref.check("rotated", got, *turned(x, pos, f, mag))
