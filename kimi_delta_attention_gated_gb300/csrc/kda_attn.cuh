@@ -223,11 +223,12 @@ __device__ __forceinline__ void fill_cos_sin(float2 *cs, const RotaryParams &r, 
 }
 
 // The same for n tokens at consecutive positions: the angle goes on by an integer addition.
-__device__ __forceinline__ void fill_cos_sin_run(float2 *cs, const RotaryParams &r, int n, int pos0, int tid, int threads) {
+__device__ __forceinline__ void fill_cos_sin_run(float2 *cs, const RotaryParams &r, int n, int64_t pos0, int tid,
+                                                 int threads) {
     const int np = r.R >> 1, rows = threads / np, j = tid % np, row = tid / np;
     if (row >= rows) return;
     const uint64_t turn = turn_of(__ldg(r.inv_freq + j)), step = turn * (uint64_t)rows;
-    uint64_t f = (uint64_t)(int64_t)(pos0 + row) * turn;
+    uint64_t f = (uint64_t)(pos0 + row) * turn;
     cs += cs_at(j, np);
     for (int t = row; t < n; t += rows, f += step) {
         float c, s;

@@ -52,8 +52,9 @@ __device__ __forceinline__ int runs_of(const AppendParams &p, int n) {
     return len > 0 ? (int)(((int64_t)ctx + len - 1) / p.c.P - ctx / p.c.P) + 1 : 0;
 }
 
-// Position of token t (-> its angle), by bisection of cu_seqlens.
-__device__ __forceinline__ int position_of(const AppendParams &p, int64_t t) {
+// Position of token t (-> its angle), by bisection of cu_seqlens.  Lengths and rows are int32, their
+// sum is not: positions are unsigned.
+__device__ __forceinline__ uint32_t position_of(const AppendParams &p, int64_t t) {
     if (!p.cu_seqlens) return max(p.c.lens[t], 0);
     int lo = 0, hi = p.c.N - 1;  // the last sequence that starts at or before t
     while (lo < hi) {
@@ -63,12 +64,12 @@ __device__ __forceinline__ int position_of(const AppendParams &p, int64_t t) {
         else
             hi = m - 1;
     }
-    return max(p.c.lens[lo], 0) + (int)(t - max(p.cu_seqlens[lo], 0));  // clamped as in new_tokens
+    return (uint32_t)max(p.c.lens[lo], 0) + (uint32_t)(t - max(p.cu_seqlens[lo], 0));  // clamped as in new_tokens
 }
 
 // One query tile; rows of no sequence are left out.
 template <int THREADS>
-__device__ __forceinline__ void rotate_queries(const AppendParams &p, int tile, int q_tile, float2 *cs, int *pos) {
+__device__ __forceinline__ void rotate_queries(const AppendParams &p, int tile, int q_tile, float2 *cs, uint32_t *pos) {
     int64_t t0 = (int64_t)tile * q_tile, t1 = min(t0 + q_tile, p.tokens);
     if (p.cu_seqlens) {
         t0 = max(t0, (int64_t)p.cu_seqlens[0]);
@@ -99,7 +100,7 @@ __device__ __forceinline__ int block_exp(float amax, int off, int old) {
 // this was measured.)
 __global__ void __launch_bounds__(kStepThreads, 8) append_queries_kernel(const __grid_constant__ AppendParams p, int q_tile) {
     __shared__ __align__(16) float2 cs[kRoom];
-    __shared__ int s_pos[kRoom];
+    __shared__ uint32_t s_pos[kRoom];
     rotate_queries<kStepThreads>(p, blockIdx.x, q_tile, cs, s_pos);
     // Its CTAs start while the runs' last ones are at work, and share nothing with them; the launch
     // must not end before the runs' has.
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(P *D / 16, 1024 / (P * D / 16)) append_run_ker
                                                                                    const __grid_constant__ Grid g) {
     constexpr int kThreads = P * D / 16, kWarps = kThreads / 32;
     extern __shared__ __align__(16) float2 cs[];
-    __shared__ int s_pos[kRoom];
+    __shared__ uint32_t s_pos[kRoom];
     __shared__ int s_seq, s_run;
     __shared__ int s_scan[kWarps];
     __shared__ float s_max[2][kWarps];
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(P *D / 16, 1024 / (P * D / 16)) append_run_ker
 #pragma unroll
     for (int b = 0; b < AHEAD; ++b) fetch(h0 + b, raw[b], old_scale[b]);
     if (turned) {
-        fill_cos_sin_run(cs, p.rot, n, (int)pos0, tid, kThreads);
+        fill_cos_sin_run(cs, p.rot, n, pos0, tid, kThreads);
         __syncthreads();
     }
     const float2 *turns = cs + t * np;
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(kStepThreads) append_step_kernel(const __grid_
     constexpr int kThreads = kStepThreads, kWarps = kThreads / 32;
     constexpr int C = D / 32;  // channels of a lane
     __shared__ __align__(16) float2 cs[kRoom];
-    __shared__ int s_pos[kRoom];
+    __shared__ uint32_t s_pos[kRoom];
     if ((int)blockIdx.x >= g.n_kv) {
         rotate_queries<kThreads>(p, blockIdx.x - g.n_kv, g.q_tile, cs, s_pos);
         return;

@@ -46,3 +46,22 @@ def test_bounds_are_clamped_for_keys_and_queries(cu, Hq, T):
                            return_k=True)
     for got, x in ((qr, q), (kr, k)):
         ref.check("rotated", got, *turned(x, pos, f, mag))
+
+
+@pytest.mark.parametrize("Hq,T", [(2, 6), (64, 9000)])
+@pytest.mark.parametrize("ctx", [2 ** 31 - 1, 2 ** 31 - 4])
+def test_places_that_pass_2_to_the_31(ctx, Hq, T):
+    """A sequence's places behind the table are not stored, but its keys and queries are turned by their
+    place all the same, which an int32 does not hold from 2^31 on."""
+    Hk, D, P = 1, 64, 16
+    q, k = rows(T, Hq, D, 83), rows(T, Hk, D, 84)
+    f, mag = kda.rotary_inv_freq(D, base=1e6)
+    cache = kda.kv_cache(1, Hk, D, P)
+    qr, kr = kda.kv_append(k, k, cache, torch.zeros((1, 1), dtype=torch.int32, device="cuda"),
+                           torch.tensor([ctx], dtype=torch.int32, device="cuda"),
+                           cu_seqlens=torch.tensor([0, T], dtype=torch.int32, device="cuda"), inv_freq=f, magnitude=mag, q=q,
+                           return_k=True)
+    pos = torch.arange(ctx, ctx + T)
+    for got, x in ((qr, q), (kr, k)):
+        ref.check("rotated", got, *turned(x, pos, f, mag))
+    assert (cache.k.view(torch.uint8) == 0).all() and (cache.k_scale == 1).all()
