@@ -671,9 +671,10 @@ def _layout(layout):
 
 
 # The current device and a device's current stream without torch.cuda's lazy-initialisation
-# and type checks, which cost more than a small kernel runs.
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# and type checks, which cost more than a small kernel runs.  (A torch built without CUDA has
+# neither, nor any tensor with which a call gets this far.)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _call(fn, index, *args):
