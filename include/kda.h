@@ -505,8 +505,9 @@ typedef enum kda_rotary_layout {
  *
  *   x, out     [tokens, heads, dim] dtype, x_stride / out_stride apart; out may be x itself
  *              (same pointer, same stride), no other overlap
- *   positions  [tokens] int32, any values: angles are reduced exactly
- *   inv_freq   [rotary_dim / 2] double, radians per position (scaled for long contexts by
+ *   positions  [tokens] int32, any values: angles are formed and reduced in integers, within
+ *              positions * 2^-64 turns; cos and sin carry fp32's relative precision
+ *   inv_freq   [rotary_dim / 2] double, finite, radians per position (scaled for long contexts by
  *              the caller), magnitude the factor that such a scaling puts on the rotated part
  *   inverse    1: the transposed rotation (angles negated), which undoes a rotation of
  *              magnitude 1 and is the gradient of any

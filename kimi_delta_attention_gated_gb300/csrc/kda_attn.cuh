@@ -92,8 +92,9 @@ int take_attn_decode_timeouts(cudaStream_t st);
 // angles
 
 // One pair's turn per position as a 64-bit binary fraction of a full turn.  The fraction of
-// position p is then the integer product p * turn modulo 2^64, exact for any position: the
-// reduction to one turn is the integers' own wrap-around.  Formed from the double's 53-bit
+// position p is then the integer product p * turn modulo 2^64: the reduction to one turn is the
+// integers' own wrap-around and loses nothing, so that the angle is off by the turn's own cut at
+// 2^-64, p times (7e-10 rad at 2^31).  Formed from the double's 53-bit
 // integer m and exponent with 64-bit integers (this GPU's double-precision rate is 1/50 of
 // its integer rate): m * 2^e / (2 pi) = m * C * 2^(e - 66) with C = 2^66 / (2 pi).
 __device__ __forceinline__ uint64_t turn_of(double inv_freq) {
@@ -112,16 +113,18 @@ __device__ __forceinline__ uint64_t turn_of(double inv_freq) {
 }
 
 // cos and sin of 2 pi * f / 2^64.  f is split into the nearest quarter turn and a rest of at
-// most 1/8 turn, taken to 2^-32 turns (1.5e-9 rad) as a + d, a the fp32 value and d what that
-// leaves out.  On |a| <= pi/4 the Taylor series through a^10 and a^9 leave 1e-9; the last
-// rounding is the only one that counts.
+// most 1/8 turn, taken as a + d, a the fp32 value of its first 32 bits and d what that and those
+// bits leave out, so that the sine of a small angle has all its bits.  On |a| <= pi/4 the Taylor
+// series through a^10 and a^9 leave 1e-9 of cos and sin; the last rounding is the only one that
+// counts.
 __device__ __forceinline__ void cos_sin_turn(uint64_t f, float &c, float &s) {
-    const uint32_t top = (uint32_t)(f >> 32);
+    const int low = (int)(uint32_t)f;  // signed: the first 32 bits are rounded
+    const uint32_t top = (uint32_t)(f >> 32) + (low < 0);
     const uint32_t quarter = (top + (1u << 29)) >> 30;  // 4 is 0 again
     const int rest = (int)(top - (quarter << 30));
     constexpr float kHi = 1.4629180792671596e-9f;  // 2 pi / 2^32
     constexpr float kLo = (float)(6.283185307179586 / 4294967296.0 - (double)kHi);
-    const float hi = (float)rest, lo = (float)(rest - (int)hi);
+    const float hi = (float)rest, lo = fmaf((float)low, 2.3283064365386963e-10f, (float)(rest - (int)hi));  // 2^-32
     const float a = hi * kHi;
     const float d = fmaf(hi, kHi, -a) + fmaf(hi, kLo, lo * kHi);
     const float a2 = a * a;

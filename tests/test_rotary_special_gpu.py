@@ -73,3 +73,22 @@ def test_infinities_in_an_append(step, layout):
     for t in range(T):
         code = cache.k[t if step else 0, :, 3 + t].float().cpu()
         assert torch.equal(code.isnan(), ~want[t].isfinite())
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("base,scaling", [(1e6, None), (1e4, "linear"), (1e9, "yarn")])
+def test_the_sine_of_a_small_angle(base, scaling, layout):
+    """Pairs whose second channel is zero: the second output is a sine alone, and is held to fp32's own
+    precision however slowly the pair turns."""
+    R = 128
+    f, mag = kda.rotary_inv_freq(R, base=base, scaling=scaling, factor=32.0)
+    pos = torch.tensor([1, 2, 3, 7, 100, 4097, -1, -5], dtype=torch.int32, device="cuda")
+    x = make(pos.numel(), 2, R, torch.float32, 74)
+    second = slice(R // 2, R) if layout == "half" else slice(1, R, 2)
+    x[..., second] = 0
+    y = kda.rotary(x, pos, f, magnitude=mag, layout=layout)
+    want = ref.rotary(ref.f64(x), pos.cpu(), f.cpu(), mag, layout)
+    # the angle's turn per position is cut at 2^-64 turns; the rest are roundings relative to the sine
+    cut = 2.0 ** -64 * 2 * torch.pi * pos.cpu().double().abs()[:, None, None] * 8
+    tol = ref.ROTARY_ROUNDINGS * ref.HALF_F32 * want.abs() + cut
+    ref.check("sines", y[..., second], want[..., second], tol[..., second])
