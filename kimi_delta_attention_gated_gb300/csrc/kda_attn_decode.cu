@@ -542,7 +542,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
     fetch_queries(cur);
     while (true) {
         const int h = cur.head, r0 = (cur.u - h * parts) * F::ROWS;  // first query head of the unit in its group
-        // queries: f16, each row scaled by a power of two to at most 2 so that nothing overflows
+        // queries: f16, each row scaled by a power of two so that its largest lies in [2^14, 2^15): nothing
+        // overflows, and what lies up to 2^31 below it is exact (8 bits down to 2^-24, the least f16 number)
         uint32_t qf[NT][F::KJ * 4][2];
         float row_scale[NT][2];  // of the two rows whose scores this lane holds
 #pragma unroll
@@ -563,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
                 }
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            const int e = min(max((int)(amax >> 23) - 127, -100), 126);
+            const int e = min(max((int)(amax >> 23) - 127, -100), 126) - 14;
             const float inv = exp2_int(-e);
 #pragma unroll
             for (int j = 0; j < F::KJ; ++j)

@@ -126,3 +126,20 @@ def test_the_log_sum_of_a_head_whose_value_scale_is_no_number(wide):
     assert torch.equal(o2[0, :G], o[0, :G]) and torch.equal(o2[1, G:], o[1, G:])
     cache.v_scale.fill_(1.0)
     verify(attend(q, cache, table, lens, P, wide)[0], lse2, q, cache, table, lens)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("Hk,G,D,P", [(2, 4, 128, 16), (1, 12, 64, 64)])
+@pytest.mark.parametrize("far", [12, 16, 20, 24])
+def test_a_query_channel_far_above_the_others(Hk, G, D, P, far, wide):
+    """One channel of each query 2^far above the others, where every key is zero: the scores are what the
+    other channels make of them."""
+    lens = [300, 40]
+    table, pages = table_for(lens, P, 62)
+    cache = filled_cache(pages, Hk, P, D, 62, (-5, -3))
+    cache.k[..., 3] = torch.zeros(cache.k.shape[:3], device="cuda").to(torch.float8_e4m3fn)
+    q = torch.randn((len(lens), Hk * G, D), generator=gen(63), device="cuda")
+    q[..., 3] = 2.0 ** far
+    q = q.bfloat16()
+    o, lse = attend(q, cache, table, lens, P, wide, out_dtype=torch.float32)
+    verify(o, lse, q, cache, table, lens)
