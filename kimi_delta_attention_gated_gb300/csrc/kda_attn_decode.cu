@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
                 }
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            const int e = min(max((int)(amax >> 23) - 127, -100), 126) - 14;
+            const int e = max((int)(amax >> 23) - 127, -100) - 14;
             const float inv = exp2_int(-e);
 #pragma unroll
             for (int j = 0; j < F::KJ; ++j)

@@ -143,3 +143,18 @@ def test_a_query_channel_far_above_the_others(Hk, G, D, P, far, wide):
     q = q.bfloat16()
     o, lse = attend(q, cache, table, lens, P, wide, out_dtype=torch.float32)
     verify(o, lse, q, cache, table, lens)
+
+
+@pytest.mark.parametrize("big", [2.0 ** 127, 3.3e38, 2.0 ** -120])
+def test_queries_at_the_types_ends(big):
+    """The largest bf16 numbers, and among the smallest normal ones."""
+    lens, Hk, G, D, P = [200], 1, 4, 64, 16
+    table, pages = table_for(lens, P, 64)
+    cache = filled_cache(pages, Hk, P, D, 64)
+    q = torch.randn((1, Hk * G, D), generator=gen(65), device="cuda").sign() * torch.rand((1, Hk * G, D), generator=gen(66), device="cuda")
+    q[..., 0] = 1.0
+    q = (q.double() * big).bfloat16()
+    assert q.isfinite().all()
+    scale = 0.1 / big if big > 1 else 2.0 ** 100
+    o, lse = attend(q, cache, table, lens, P, False, out_dtype=torch.float32, scale=scale)
+    verify(o, lse, q, cache, table, lens, scale)
