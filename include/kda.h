@@ -115,10 +115,10 @@ kda_status kda_device_status(void *stream);
  * and the fused tensor-core prefill's tile and blob waits (kda_chunk_fwd,
  * kda_chunk_fwd_logits without a workspace or with one in the concurrent form) and the
  * attention kernels' tile waits (kda_attn_decode, kda_attn_prompt) poll their mbarrier at
- * most this many times before they give up, for the calls made after this one (process-wide).  polls < 0 restores the default (2^26; the attention kernels never
- * poll more than 2^21 times); 0 makes every such
- * wait give up at once, which tests of the failure handling use (kda_device_status then
- * reports KDA_ERR_TIMEOUT and the outputs hold NaN).  The waits that let copies in
+ * most this many times before they give up, for the calls made after this one
+ * (process-wide).  polls < 0 restores the default (2^26; the attention kernels never poll
+ * more than 2^21 times); 0 makes every such wait give up at once, which tests of the failure
+ * handling use (kda_device_status then reports KDA_ERR_TIMEOUT and the outputs hold NaN).  The waits that let copies in
  * flight land before a CTA exits, the tensor-core waits, and the split form's kernels
  * always keep their full bound.  Returns KDA_OK, or
  * KDA_ERR_INVALID_ARG above 2^32 - 1.  No counterpart on the pages.
@@ -481,10 +481,12 @@ kda_status kda_o_proj(const void *y, const void *w_o, void *out, kda_dtype out_d
 /*
  * Full attention.  The hybrid stacks interleave KDA layers with layers of full attention
  * (nnterp encyclopedia "Kimi-Linear", section 03: one block in four; Kimi-K3 atlas
- * "final-block-state", the layer-type schedule).  The four calls below are what such a
- * layer computes around its projections: positions, the paged 8-bit key/value cache, the
- * decode step's attention over that cache and the prompt's attention.  The pages give no
- * kernels for these; the formulas are stated here.
+ * "final-block-state", the layer-type schedule).  The four calls below serve such layers
+ * of hybrid stacks with grouped heads: positions, a paged 8-bit key/value cache, the decode
+ * step's attention over that cache and the prompt's attention.  The pages give no kernels
+ * for these; the formulas are stated here.  Of Kimi-Linear's own full-attention layers,
+ * which have no rotary positions, keys of 192 channels and values of 128, only the
+ * prompt's attention takes the widths; the cache has one width, 64 or 128, for both.
  *
  * Rows of q, k and v may lie a stride apart (slices of a fused projection): a stride is the
  * distance of one token's row to the next in elements, at least heads * dim and a multiple
@@ -544,7 +546,8 @@ kda_status kda_rotary(const void *x, kda_dtype dtype, int64_t x_stride, const in
  *   q, q_out     [tokens, q_heads, dim] bf16, q q_stride apart, q_out dense; both or neither
  *   k_out        [tokens, kv_heads, dim] bf16, dense, or NULL: the rotated keys
  * Rows of q_out and k_out that belong to no sequence are left as they are.
- * dim 64 or 128; page_size 16, 32, 64 or 128 (KDA_ERR_UNSUPPORTED otherwise).
+ * dim 64 or 128; page_size 16, 32, 64 or 128; at most 65535 sequences and 65535 cache heads;
+ * num_pages * kv_heads * page_size below 2^31 - 256 (KDA_ERR_UNSUPPORTED otherwise).
  * No page may be written for two sequences, or for two places of one, in one call (pages that
  * are only read, full ones of a shared beginning, may stand in several rows of block_table).
  */
@@ -577,7 +580,10 @@ kda_status kda_kv_append(const void *k, int64_t k_stride, const void *v, int64_t
  * most 2^-11 of the largest sum of weights times |values| among 8 or 16 neighbouring channels.
  * What lies in a page behind a sequence's last token is not read into the result, whatever
  * it is.  A sequence with a page number out of [0, num_pages) gives NaN rows.
- * dim 64 or 128; page_size 16, 32, 64 or 128.  Results do not depend on timing.
+ * dim 64 or 128; page_size 16, 32, 64 or 128; limits as kda_kv_append.  Results do not
+ * depend on timing.  Whether sequences are cut into pieces, which takes the workspace, goes by
+ * the block table's width, not by the lengths on the device: a table no wider than the
+ * sequences need serves short ones faster, in other last bits.
  */
 size_t kda_attn_decode_workspace_size(int n_seqs, int q_heads, int kv_heads, int dim, int64_t max_tokens);
 
@@ -606,7 +612,7 @@ kda_status kda_attn_decode(const void *q, int64_t q_stride, const void *k_cache,
  *   cu_seqlens_k [n_seqs + 1] int32: the same for the keys.  NULL: as cu_seqlens where that is
  *       given (k_rows == q_rows), else n_seqs sequences of k_rows / n_seqs rows.
  * (dim, dim_v) one of (64, 64), (128, 128), (192, 128) (KDA_ERR_UNSUPPORTED otherwise); q_heads a
- * multiple of kv_heads; scale finite and not 0.  Nothing a row does not see enters its result,
+ * multiple of kv_heads; at most 2^30 rows, 65535 heads and 16384 sequences; scale finite and not 0.  Nothing a row does not see enters its result,
  * be it infinite or NaN.  The weights are rounded to bf16 for the product with v.
  *
  *   workspace    device scratch of kda_attn_prompt_workspace_size(...) bytes, 16-byte aligned, for

@@ -38,7 +38,10 @@
 // 256 sequences of about 1000 tokens, 64 heads over 8 of 128, pages of 64: 98 us, 5.4 TB/s (80 % of
 // a copy's rate); 8 of [8192, 131072] tokens, 40 heads over 8, pages of 16: 114 us, 5.9 TB/s (87 %);
 // one of 1000 tokens: 9.0 us, both launches and their latencies.  The stream itself runs at
-// 6.0 to 6.3 TB/s; the rest is about 8 us of finding the pieces, first copies, and joining.
+// 6.0 to 6.3 TB/s; the rest is about 8 us of finding the pieces, first copies, and joining.  128 heads
+// over 8 (groups of 16), the same 256 sequences: 133 us; 255 registers leave an SM eight warps, and
+// a step's chain of products, exponentials and products is the bound (issue slots 37 %, DRAM 53 %).
+// 64 channels, 64 and 128 heads over 8: 69 and 87 us.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -925,10 +928,11 @@ bool encode(chunk::EncodeTiledFn enc, CUtensorMap *map, const void *base, const 
 
 // CTAs of a call: what the GPU holds at once, or as many as pieces are possible at all.  Where the
 // table holds few tokens, heads are not cut, each has a CTA, and nothing is joined: cut and
-// whole, 32/8 heads of 128, one sequence of 60, 500, 1000 tokens 6.4 and 4.4, 8.7 and 7.9, 8.8
-// and 12.3 us; 32 of 250, 1000 tokens 11.9 and 7.0, 18.4 and 14.7 us; 256 of [50, 150], 1000 with
-// 64/8 heads 30.9 and 26.3, 97.8 and 96.9 us.  With groups of 16, where an SM holds two CTAs,
-// many waves of them are slower: 64 sequences of 500 tokens 28.5 and 24.5, 256 82.5 and 87.7 us.
+// whole, 32/8 heads of 128, one sequence of 60, 500 tokens 6.5 and 4.5, 9.0 and 8.2 us (1000: 8.8
+// and 12.3 when the rule was made); 32 of 250, 1000 tokens 12.3 and 7.5, 22.2 and 17.8 us; 256 of
+// [50, 150], [900, 1000] with 64/8 heads 35.0 and 30.4, 93.9 and 93.4 us.  With groups of 16, where
+// an SM holds two CTAs, many waves of them are slower: 64 sequences of 500 tokens 32.7 and 29.8,
+// 256 82.5 and 87.7 us when the rule was made.
 template <int D, int NT>
 int decode_ctas(int64_t N, int Hq, int Hk, int64_t max_tokens, bool &whole) {
     using F = Cfg<D, NT>;

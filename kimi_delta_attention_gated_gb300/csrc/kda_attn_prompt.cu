@@ -5,8 +5,9 @@
 //
 // Flash form: key blocks of 128 tokens pass by, and each row keeps a reference m, the sum l
 // of 2^(s - m) and the weighted sum O of the values (s the scores in units of log2).  m is the
-// row's maximum when it was last set, at first that of its first 64 keys; it is set anew (and l,
-// O brought to it) only when a score exceeds it by more than kSlack.  Weights, l and O are all
+// row's maximum when it was last set, at first that of its first block of 128 keys (of its part's,
+// where the keys are divided); it is set anew (and l, O brought to it) only when a score exceeds it
+// by more than kSlack.  Weights, l and O are all
 // floating, so which m is used costs no precision, and O is hardly ever touched.
 //
 // A CTA takes two query tiles of 128 rows: two heads of one key/value head where the group
@@ -33,11 +34,13 @@
 // l sums the unrounded weights in fp32.
 //
 // 8192 tokens with 32 heads over 8, channels 64/64, 128/128, 192/128: 254, 316, 400 us, 1082, 1740 and
-// 1718 TFLOP/s.  With 64 channels the softmax is the bound (a weight for 256 operations instead of
-// 512 or 640); with 128 and more the tensor pipe is busy for 70 to 75 % of the cycles, at a clock that
-// the power limit sets, and a tile's chain of scores, softmax and product is the bound.  8 packed prompts of [100, 4096] tokens, 32 heads of 192/128: 125 us,
-// where each item's beginning and end (about 4 us of queries, first scores and output) count.
-// 100 tokens: 6.9 us.
+// 1718 TFLOP/s in runs of a few passes; in long runs the power limit lowers the clock (2400 passes of
+// 128/128: 339 us at 1740 MHz).  With 128 and more channels the tensor pipe is busy for 70 to 75 % of the
+// cycles and a tile's chain of scores, softmax and product is the bound; with 64, where a weight
+// comes for 256 operations instead of 512 or 640, that chain too: the tensor pipe is busy for 42 %
+// of the cycles, the special functions' for 42 %, the issue slots for 44 % (4096 tokens).  8 packed
+// prompts of [100, 4096] tokens, 32 heads of 192/128: 125 to 132 us (tensor pipe 56 %), where each
+// item's beginning and end (about 4 us of queries, first scores and output) count.  100 tokens: 6.8 us.
 //
 // What is masked never reaches a result: masked scores are replaced, not added to; value
 // rows behind the sequence's end are zeroed in shared memory (a zero weight would turn an

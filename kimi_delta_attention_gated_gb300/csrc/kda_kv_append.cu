@@ -16,9 +16,9 @@
 // decode step) has a warp for each (sequence, head).  Queries are rotated by further CTAs
 // of the same launch, or in a launch of their own beside the last runs.
 // Eight prompts of [512, 16384] tokens, 32 query and 8 cache heads of 128, rotated keys written
-// too: 294 us, 84 % of a copy's rate: the runs 115 us (instructions, 65 % of the issue slots, and a
-// barrier for each head), the queries 180 us (90 %).  One token each of 256 sequences: 5.4 us;
-// 37 pieces of [1, 100] tokens: 5.0 us, launch and latency.
+// too: 300 us, 83 % of a copy's rate: the runs 117 us (instructions, 65 % of the issue slots, and a
+// barrier for each head), the queries 183 us (88 %).  One token each of 256 sequences: 5.5 us;
+// 37 pieces of [1, 100] tokens: 4.9 us, launch and latency.
 #include "kda_attn.cuh"
 
 namespace kda {

@@ -5,9 +5,9 @@
 //
 // Memory bound: x is read once and written once.  A CTA takes a few tokens, forms their
 // cos and sin once (shared by all heads) in shared memory and then turns 16-byte vectors.
-// 8192 tokens of 96 heads of 128, bf16: 64.5 us, 6.2 TB/s (92 % of a copy's rate); 4099 tokens of
-// 12 heads of 64, fp32, a quarter turned: 6.9 us, of which the launch and one wave of CTAs take most;
-// 8 tokens of 32 heads: 2.9 us, an empty launch's time.
+// 8192 tokens of 96 heads of 128, bf16: 65.9 us, 6.1 TB/s (90 % of a copy's rate); 4099 tokens of
+// 12 heads of 64, fp32, half of each turned: 6.8 us, of which the launch and one wave of CTAs take
+// most; 8 tokens of 32 heads: 2.9 us, an empty launch's time.
 #include "kda_attn.cuh"
 
 namespace kda {
