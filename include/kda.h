@@ -577,7 +577,8 @@ kda_status kda_kv_append(const void *k, int64_t k_stride, const void *v, int64_t
  *             size is 0 it may be NULL.
  * Scores, their maxima and all sums are fp32; the weights are rounded to f16 for the product with
  * the values: a relative error of 2^-12 each, of the largest and the smallest alike, or in all at
- * most 2^-11 of the largest sum of weights times |values| among 8 or 16 neighbouring channels.
+ * most 2^-9 (half a step of bf16) of the largest sum of weights times |values| among 8 or 16
+ * channels, which is reached only by codes of 448 throughout.
  * What lies in a page behind a sequence's last token is not read into the result, whatever
  * it is.  A sequence with a page number out of [0, num_pages) gives NaN rows.
  * dim 64 or 128; page_size 16, 32, 64 or 128; limits as kda_kv_append.  Results do not

@@ -58,11 +58,11 @@ constexpr int kJoinMost = 512;   // threads of a joining CTA at most
 constexpr int kStep = 32;       // tokens of a step
 constexpr int kPad = 6;         // a head's own cost in steps
 constexpr int kMinPiece = 8;   // places of a CTA at least
-constexpr float kSlack = 4.f;   // the maximum in use may lie this far below the true one (log2)
-constexpr int kTop = 10;        // a weight at that maximum is 2^kTop, times the scale's fraction below 2
+constexpr float kSlack = 2.f;   // the maximum in use may lie this far below the true one (log2)
+constexpr int kTop = 12;        // a weight at that maximum is 2^kTop, times the scale's fraction below 2
 // How far M lies below the maximum, and what the value scales are multiplied with to make up for it.  Sums of
 // 2^(s - M) then stay within fp32 for value scales from 2^-126 to 2^120: M goes by a scale of at least
-// 2^kLeastScale, so that each is at most 2^(kSlack + kRef - kLeastScale) = 2^94 (2^31 of them 2^125),
+// 2^kLeastScale, so that each is at most 2^(kSlack + kRef - kLeastScale) = 2^92 (2^31 of them 2^123),
 // and at least 2^(kRef - 120) where the scale decides, 2^24 above what is flushed.
 constexpr int kRef = 18, kLeastScale = -72;
 constexpr int kUp = 40;         // 2^-25 times 2^kUp is 2^15, and down to 2^-54 it stays normal in f16
@@ -690,8 +690,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attn_decode_kernel
         }
         {
             // f16 takes 2^-25 at most from a weight below 2^-14, and a value's code is at most 448: over this warp's
-            // tokens, as many as 32 times `enough` says, less than 2^-11 (half a step of f16) of `enough`.
-            const float enough = (float)((cur.s1 - cur.s0) / kWarps + 1);
+            // tokens, as many as 128 times `enough` says, less than 2^-9 (half a step of bf16) of `enough`.  (Most
+            // codes are far smaller; with a quarter of this, values of 0.05 under a scale of one sent long
+            // sequences through their steps twice, 268 us for 113.)
+            const float enough = 0.25f * (float)((cur.s1 - cur.s0) / kWarps + 1);
             float sums = INFINITY;  // the least row's largest sum among this lane's channels
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
