@@ -35,11 +35,11 @@
 // ways).  With 16-byte copies by each lane (cp.async) the load and store pipe was the bound,
 // 148 us for 256 sequences of about 1000 tokens against 116 at that stage.
 //
-// 256 sequences of about 1000 tokens, 64 heads over 8 of 128, pages of 64: 98 us, 5.4 TB/s (80 % of
-// a copy's rate); 8 of [8192, 131072] tokens, 40 heads over 8, pages of 16: 114 us, 5.9 TB/s (87 %);
+// 256 sequences of about 1000 tokens, 64 heads over 8 of 128, pages of 64: 97 us, 5.5 TB/s (81 % of
+// a copy's rate); 8 of [8192, 131072] tokens, 40 heads over 8, pages of 16: 113 us, 6.0 TB/s (88 %);
 // one of 1000 tokens: 9.0 us, both launches and their latencies.  The stream itself runs at
 // 6.0 to 6.3 TB/s; the rest is about 8 us of finding the pieces, first copies, and joining.  128 heads
-// over 8 (groups of 16), the same 256 sequences: 133 us; 255 registers leave an SM eight warps, and
+// over 8 (groups of 16), the same 256 sequences: 134 us; 255 registers leave an SM eight warps, and
 // a step's chain of products, exponentials and products is the bound (issue slots 37 %, DRAM 53 %).
 // 64 channels, 64 and 128 heads over 8: 69 and 87 us.
 #include <cuda.h>

@@ -96,8 +96,7 @@ __device__ __forceinline__ int block_exp(float amax, int off, int old) {
 // runs (any number of tokens per sequence)
 
 // The queries of a long call, in a launch of their own: their CTAs need half the registers of
-// a run's.  (In one launch the eight prompts of [512, 16384] tokens took 442 us, in two 378, when
-// this was measured.)
+// a run's.
 __global__ void __launch_bounds__(kStepThreads, 8) append_queries_kernel(const __grid_constant__ AppendParams p, int q_tile) {
     __shared__ __align__(16) float2 cs[kRoom];
     __shared__ uint32_t s_pos[kRoom];
@@ -387,8 +386,11 @@ kda_status run(const AppendParams &p, Grid g, cudaStream_t st) {
         return KDA_ERR_UNSUPPORTED;
     }
     g.n_kv = (int)kv;
-    // two launches where the queries alone would be several waves of CTAs
-    const bool apart = q_ctas > 16ll * sm_count();
+    // Two launches where the queries alone fill the GPU, four CTAs an SM or more.  One launch and two,
+    // 32/8 heads of 128, rotated keys kept: 1200 tokens 12.3 and 14.1 us, 2500 23.7 and 23.1, 5000 35.5
+    // and 32.4, 9000 60 and 54, 20000 106 and 91, 60000 308 and 262; 16/2 heads of 64, pages of 16: 9000
+    // tokens 14.8 and 14.4, 40000 51 and 46.
+    const bool apart = q_ctas > 4ll * sm_count();
     size_t smem = (size_t)p.c.P * p.rot.R / 2 * sizeof(float2);
     if (p.q && !apart && smem < kRoom * sizeof(float2)) smem = kRoom * sizeof(float2);
     if (smem > 32 * 1024) {
