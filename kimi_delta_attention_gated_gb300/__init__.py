@@ -639,8 +639,10 @@ def rotary_inv_freq(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, origi
     0.1 ln(factor) + 1)."""
     if rotary_dim <= 0 or rotary_dim % 2:
         raise ValueError("rotary_dim must be even and positive")
-    if not factor >= 1.0:
-        raise ValueError("factor must be at least 1")
+    if not 1.0 <= factor < math.inf:
+        raise ValueError("factor must be finite and at least 1")
+    if not 0.0 < base < math.inf:
+        raise ValueError("base must be finite and positive")
     pair = torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim
     if scaling == "ntk" and rotary_dim > 2:
         base = base * factor ** (rotary_dim / (rotary_dim - 2))
@@ -843,7 +845,8 @@ def attn_decode(q, cache, block_table, seq_lens, *, scale=None, out_dtype=torch.
     be strided), seq_lens int32 [N] tokens to attend to (the new one included), block_table
     int32 [N, max_blocks].  scale: default dim^-0.5.  Returns o [N, q_heads, dim] (zero for an
     empty sequence, NaN where a needed page number is out of range) or, with return_lse,
-    (o, lse [N, q_heads] fp32).  workspace: a uint8 tensor of attn_decode_workspace_size(...)
+    (o, lse [N, q_heads] fp32).  A block_table no wider than the sequences need serves short ones
+    faster (they are then not cut into pieces).  workspace: a uint8 tensor of attn_decode_workspace_size(...)
     bytes for this call alone, or None: taken from torch's allocator for the call."""
     lib = _lib or _load()
     index, Hk, P, D, cache_args = _cache_args(cache)

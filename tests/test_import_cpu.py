@@ -21,3 +21,16 @@ def test_without_torchs_cuda_bindings():
             "    else: raise SystemExit('not refused')\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_inv_freq_refuses_a_base_without_angles():
+    import pytest
+
+    from kimi_delta_attention_gated_gb300 import rotary_inv_freq
+    for base in (0.0, -10000.0, float("inf"), float("nan")):
+        for scaling in (None, "ntk", "yarn"):
+            with pytest.raises(ValueError):
+                rotary_inv_freq(64, base=base, scaling=scaling, factor=2.0, device="cpu")
+    for factor in (float("inf"), float("nan")):
+        with pytest.raises(ValueError):
+            rotary_inv_freq(64, scaling="yarn", factor=factor, device="cpu")
