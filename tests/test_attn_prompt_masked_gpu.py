@@ -76,3 +76,18 @@ def test_several_values_in_the_tile_and_rows_that_see_none():
         clean = v.nan_to_num(0.0, 0.0, 0.0)
         verify(o[:110].bfloat16(), None, q[:110], k[:10], clean[:10], [110], [10])
         assert o[..., 3:].isfinite().all()
+
+
+@pytest.mark.parametrize("scale", [None, -0.3])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_scales_and_types(scale, out):
+    """Rows computed alone with a negative scale and fp32 outputs, whole and in parts."""
+    T, at = 700, 650
+    q, k, v = make(T, T, 2, 1, 128, 128, 44)
+    clean = v.clone()
+    v[at, 0, 100] = float("nan")
+    for ws in ("auto", None):
+        o, lse = kda.attn_prompt(q, k, v, return_lse=True, scale=scale, out_dtype=out, workspace=ws)
+        verify(o[:at], lse[:at], q[:at], k[:at], clean[:at], [at], [at], scale, rows=[0, 511, 512, 513, 600, 639, 640, 649])
+        assert o[at:, :, 100].isnan().all() and o[at:, :, :100].isfinite().all()
+    kda.device_status()

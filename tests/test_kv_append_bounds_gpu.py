@@ -65,3 +65,45 @@ def test_places_that_pass_2_to_the_31(ctx, Hq, T):
     for got, x in ((qr, q), (kr, k)):
         ref.check("rotated", got, *turned(x, pos, f, mag))
     assert (cache.k.view(torch.uint8) == 0).all() and (cache.k_scale == 1).all()
+
+
+def test_a_long_append_captured_and_on_two_streams():
+    """The form with a launch of its own for the queries, whose CTAs begin beside the last runs: replayed
+    with new rows, and two at once; what follows in the stream sees both launches' results."""
+    T, Hk, Hq, D, P = 3000, 2, 16, 128, 32
+    f, mag = kda.rotary_inv_freq(D)
+    pages = -(-T // P)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    zero, cu = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    sets = [(rows(T, Hq, D, 90 + i), rows(T, Hk, D, 95 + i)) for i in range(3)]
+
+    def call(q, k, cache):
+        before = kda.launch_count()
+        qr, kr = kda.kv_append(k, k, cache, table, zero, cu_seqlens=cu, inv_freq=f, magnitude=mag, q=q, return_k=True)
+        assert kda.launch_count() == before + 2
+        return [qr.clone(), kr.clone(), *(t.view(torch.uint8).clone() for t in cache)]  # copies behind it in the stream
+
+    want = [call(q, k, kda.kv_cache(pages, Hk, D, P)) for q, k in sets]
+    ref.check("queries", want[0][0], *turned(sets[0][0], torch.arange(T), f, mag))
+    q, k = (t.clone() for t in sets[0])
+    cache = kda.kv_cache(pages, Hk, D, P)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = call(q, k, cache)
+    for s, w in zip(sets, want):
+        q.copy_(s[0])
+        k.copy_(s[1])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, w))
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    caches = [kda.kv_cache(pages, Hk, D, P) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(call(*sets[i], caches[i]))
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        assert all(torch.equal(a, b) for r in runs for a, b in zip(r, w))
