@@ -629,6 +629,116 @@ kda_status kda_attn_prompt(const void *q, int64_t q_stride, const void *k, int64
                            void *o, kda_dtype o_dtype, float *lse, void *workspace, size_t workspace_bytes,
                            void *stream);
 
+/*
+ * Latent attention.  The hybrid stacks' own full-attention layers (nnterp encyclopedia
+ * "Kimi-Linear", section "Printout": kv_a_proj_with_mqa, kv_b_proj; keys of 192 channels, values of
+ * 128) keep one row [c | r] a token: c a latent of KDA_LATENT_DIM channels of which every head's own
+ * 128 key and 128 value channels are linear images, and r KDA_LATENT_SHARED key channels that all
+ * heads share.  The calls below serve such layers in both forms:
+ *   absorbed (steps, drafted tokens, pieces over a cache): kda_latent_append, kda_latent_queries,
+ *       kda_attn_latent, kda_latent_values;
+ *   expanded (whole prompts): kda_latent_append (its rows_out), kda_latent_expand, then
+ *       kda_attn_prompt with 192 and 128 channels.
+ * Kimi-Linear turns no channels by position; other stacks turn the shared ones, which the calls
+ * can.  The pages give no kernels for these; the formulas are stated here.
+ *
+ * w_kv [heads, KDA_LATENT_KEY + KDA_LATENT_VALUE, KDA_LATENT_DIM] bf16 is the projection's weight as
+ * trained (nn.Linear), a head's key rows before its value rows.  The cache is [num_pages, page_size,
+ * KDA_LATENT_ROW] bf16; token j of sequence n lies at place j % page_size of page
+ * block_table[n][j / page_size].  page_size 16, 32, 64 or 128; at most 65535 sequences, 2^30 tokens
+ * and 4096 heads; num_pages * page_size below 2^31 - 256 (KDA_ERR_UNSUPPORTED otherwise).  Strides and
+ * index arrays are as in the calls above.
+ */
+#define KDA_LATENT_DIM 512
+#define KDA_LATENT_SHARED 64
+#define KDA_LATENT_ROW (KDA_LATENT_DIM + KDA_LATENT_SHARED)
+#define KDA_LATENT_KEY 128
+#define KDA_LATENT_VALUE 128
+
+/*
+ * kda_latent_append -- appends new tokens' rows to the paged cache:
+ *     [c | r] -> [c / sqrt(mean(c^2) + eps) * norm_w | r turned by the token's place].
+ *
+ *   x            [tokens, KDA_LATENT_ROW] bf16, x_stride apart
+ *   context_lens, cu_seqlens, block_table, and tokens without a page: as kda_kv_append.  No two
+ *                tokens of a call may have the same place in a page.
+ *   norm_w       [KDA_LATENT_DIM] float, eps finite and at least 2^-100; NULL: c is stored as it is
+ *   inv_freq     as kda_rotary, of the first rotary_dim shared channels (at most
+ *                KDA_LATENT_SHARED); NULL: nothing is turned (rotary_dim 0)
+ *   rows_out     [tokens, KDA_LATENT_ROW] bf16, dense, or NULL: the same rows, for
+ *                kda_latent_expand.  Rows that belong to no sequence are left as they are.
+ */
+kda_status kda_latent_append(const void *x, int64_t x_stride, int64_t tokens, void *cache, int num_pages, int page_size,
+                             const int32_t *block_table, int max_blocks, const int32_t *context_lens,
+                             const int32_t *cu_seqlens, int n_seqs, const float *norm_w, float eps, const double *inv_freq,
+                             float magnitude, int rotary_dim, int layout, void *rows_out, void *stream);
+
+/*
+ * kda_latent_queries -- queries taken into the latent's space:
+ *     out[t][h] = [ sum_n q[t][h][n] w_kv[h][n][.], n < 128 | q[t][h][128 .. 192) turned by positions[t] ].
+ *
+ *   q          [tokens, heads, 192] bf16, q_stride apart
+ *   positions  [tokens] int32, with inv_freq as in kda_latent_append; both or neither
+ *   out        [tokens, heads, KDA_LATENT_ROW] bf16
+ */
+kda_status kda_latent_queries(const void *q, int64_t q_stride, int64_t tokens, int heads, const void *w_kv,
+                              const int32_t *positions, const double *inv_freq, float magnitude, int rotary_dim, int layout,
+                              void *out, void *stream);
+
+/*
+ * kda_attn_latent -- causal attention of the tokens of a call over the cache, in the latent's space.
+ *
+ *     o[t][h] = sum_{j < seen} softmax_j(scale * q[t][h] . row_j) row_j[0 .. 512),
+ * seen = seq_lens[n] - (tokens of sequence n in the call) + i + 1 for its i-th token: the call's own
+ * tokens are in the cache already (kda_latent_append) and counted by seq_lens.  A token that sees
+ * nothing gives zero rows and lse -INFINITY.
+ *
+ *   q           [tokens, heads, KDA_LATENT_ROW] bf16, q_stride apart (kda_latent_queries)
+ *   cu_seqlens  [n_seqs + 1] int32: sequence n's tokens are rows [cu_seqlens[n], cu_seqlens[n + 1])
+ *               (clamped to [0, tokens]); rows of no sequence are left as they are.  NULL: one token
+ *               per sequence, tokens == n_seqs
+ *   seq_lens    [n_seqs] int32, clamped to [0, max_blocks * page_size]
+ *   scale       not 0, within 2^100 (192^-1/2 for the layer)
+ *   o           [tokens, heads, KDA_LATENT_DIM] o_dtype
+ *   lse         [tokens, heads] float or NULL: log(sum_j e^(scale q . row_j))
+ *   workspace   device scratch of kda_attn_latent_workspace_size(n_seqs, tokens, heads, max_blocks *
+ *               page_size) bytes, 16-byte aligned; calls that may overlap on the GPU (two captured
+ *               graphs among them) need workspaces of their own.  Where the size is 0 it may be NULL.
+ * Scores, their maxima and all sums are fp32; the weights are rounded to bf16 for the product with the
+ * rows.  What a row does not see does not enter its result, be it infinite or NaN, nor what lies in
+ * a page behind a sequence's last token.  A page number out of [0, num_pages) gives NaN to the rows that
+ * need the page, and to others only of the same call's neighbouring tokens of that sequence.
+ * Results do not depend on timing.  Any number of tokens per sequence is taken; for whole
+ * prompts the expanded form needs a third of the operations.
+ */
+size_t kda_attn_latent_workspace_size(int n_seqs, int64_t tokens, int heads, int64_t max_tokens);
+
+kda_status kda_attn_latent(const void *q, int64_t q_stride, int64_t tokens, int heads, const void *cache, int num_pages,
+                           int page_size, const int32_t *block_table, int max_blocks, const int32_t *seq_lens,
+                           const int32_t *cu_seqlens, int n_seqs, float scale, void *o, kda_dtype o_dtype, float *lse,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_latent_values -- the attention's output taken back to each head's value channels:
+ *     out[t][h][i] = sum_c o[t][h][c] w_kv[h][128 + i][c].
+ *
+ *   o    [tokens, heads, KDA_LATENT_DIM] bf16, o_stride apart
+ *   out  [tokens, heads, KDA_LATENT_VALUE] bf16 (the y of kda_o_proj)
+ */
+kda_status kda_latent_values(const void *o, int64_t o_stride, int64_t tokens, int heads, const void *w_kv, void *out,
+                             void *stream);
+
+/*
+ * kda_latent_expand -- every head's keys and values from rows of latents, for kda_attn_prompt:
+ *     k[t][h] = [ sum_c rows[t][c] w_kv[h][i][c], i < 128 | rows[t][512 .. 576) ],
+ *     v[t][h][i] = sum_c rows[t][c] w_kv[h][128 + i][c].
+ *
+ *   rows  [tokens, KDA_LATENT_ROW] bf16, rows_stride apart
+ *   k     [tokens, heads, 192], v [tokens, heads, 128], bf16
+ */
+kda_status kda_latent_expand(const void *rows, int64_t rows_stride, int64_t tokens, int heads, const void *w_kv, void *k,
+                             void *v, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -15,6 +15,12 @@ The full-attention layers beside the KDA layers:
   kv_append       keys and values into a paged 8-bit cache (kv_cache), rotated on the way
   attn_decode     one query token per sequence over that cache
   attn_prompt     causal attention over whole (packed) prompts
+Layers of full attention with one latent row a token for all heads (latent attention):
+  latent_append   rows into a paged cache (latent_cache), normalised and turned on the way
+  latent_queries  queries taken into the latent's space
+  attn_latent     causal attention over that cache, any number of tokens per sequence
+  latent_values   its output taken back to the heads' value channels
+  latent_expand   whole keys and values of packed rows, for attn_prompt
 
 Inputs may live on the host: they are copied to the current CUDA device, and the
 results are copied back to the host, which makes the call end-to-end.
@@ -34,6 +40,8 @@ __all__ = ["chunk_fwd", "chunk_fwd_logits", "recurrent_fwd", "recurrent_step", "
            "workspace_size", "release_workspaces", "prepass_hits",
            "KVCache", "kv_cache", "rotary_inv_freq", "rotary", "kv_append", "attn_decode", "attn_decode_workspace_size",
            "attn_prompt", "attn_prompt_workspace_size",
+           "latent_cache", "latent_append", "latent_queries", "attn_latent", "attn_latent_workspace_size", "latent_values",
+           "latent_expand",
            "library_path", "KDAError", "MODE_AUTO", "MODE_TENSOR", "MODE_FP32", "MODE_SPLIT"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -109,7 +117,15 @@ def _load():
         lib.kda_attn_prompt.argtypes = [P, L, P, L, P, L, L, L, I, I, I, I, P, P, I, F, P, I, P, P, Z, P]
         lib.kda_attn_prompt_workspace_size.argtypes = [L, L, I, I, I, I]
         lib.kda_attn_prompt_workspace_size.restype = Z
-        for fn in ("kda_rotary", "kda_kv_append", "kda_attn_decode", "kda_attn_prompt"):
+        lib.kda_latent_append.argtypes = [P, L, L, P, I, I, P, I, P, P, I, P, F, P, F, I, I, P, P]
+        lib.kda_latent_queries.argtypes = [P, L, L, I, P, P, P, F, I, I, P, P]
+        lib.kda_latent_values.argtypes = [P, L, L, I, P, P, P]
+        lib.kda_latent_expand.argtypes = [P, L, L, I, P, P, P, P]
+        lib.kda_attn_latent.argtypes = [P, L, L, I, P, I, I, P, I, P, P, I, F, P, I, P, P, Z, P]
+        lib.kda_attn_latent_workspace_size.argtypes = [I, L, I, L]
+        lib.kda_attn_latent_workspace_size.restype = Z
+        for fn in ("kda_rotary", "kda_kv_append", "kda_attn_decode", "kda_attn_prompt", "kda_latent_append",
+                   "kda_latent_queries", "kda_latent_values", "kda_latent_expand", "kda_attn_latent"):
             getattr(lib, fn).restype = ctypes.c_int
         lib.kda_device_status.argtypes = [P]
         lib.kda_device_status.restype = ctypes.c_int
@@ -960,3 +976,221 @@ def attn_prompt(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, scale=None, out_
           D ** -0.5 if scale is None else float(scale), _dense(o, "o", o.dtype, len(shape), index), _dt(o),
           None if lse is None else lse.data_ptr(), ws, need)
     return (o, lse) if return_lse else o
+
+
+# ---------------------------------------------------------------------------
+# latent attention: one row [c 512 | r 64] a token for all heads
+
+LATENT_DIM, LATENT_SHARED, LATENT_ROW = 512, 64, 576
+LATENT_KEY, LATENT_VALUE, LATENT_QUERY = 128, 128, 192
+
+
+def latent_cache(num_pages, page_size=64, device=None) -> torch.Tensor:
+    """An empty paged cache of latent rows, bf16 [num_pages, page_size, 576], on the device (default:
+    the current CUDA device)."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    return torch.zeros((num_pages, page_size, LATENT_ROW), dtype=torch.bfloat16, device=device)
+
+
+def _latent_cache_args(cache):
+    """(device index, (address, pages, page_size))."""
+    if not isinstance(cache, torch.Tensor) or cache.get_device() < 0:
+        raise ValueError("the cache must lie on a CUDA device")
+    index = cache.get_device()
+    at = _dense(cache, "cache", torch.bfloat16, 3, index)
+    pages, P, row = cache.shape
+    if row != LATENT_ROW:
+        raise ValueError(f"the cache must be [pages, page_size, {LATENT_ROW}]")
+    return index, (at, pages, P)
+
+
+def _latent_weight(w_kv, heads, index):
+    """w_kv [H, 256, 512], or the projection's weight [H * 256, 512] -> its address."""
+    if isinstance(w_kv, torch.Tensor) and w_kv.dim() == 2 and w_kv.shape[0] % (LATENT_KEY + LATENT_VALUE) == 0:
+        w_kv = w_kv.unflatten(0, (-1, LATENT_KEY + LATENT_VALUE))
+    at = _dense(w_kv, "w_kv", torch.bfloat16, 3, index)
+    if tuple(w_kv.shape[1:]) != (LATENT_KEY + LATENT_VALUE, LATENT_DIM) or heads not in (None, w_kv.shape[0]):
+        raise ValueError(f"w_kv must be [heads, {LATENT_KEY + LATENT_VALUE}, {LATENT_DIM}], a head's key rows before its "
+                         "value rows")
+    return at, w_kv.shape[0]
+
+
+def _latent_out(out, name, shape, device, index):
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        return out, out.data_ptr()
+    at = _dense(out, name, torch.bfloat16, len(shape), index)
+    if out.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    return out, at
+
+
+def latent_append(x, cache, block_table, context_lens, *, cu_seqlens=None, norm_w=None, eps=1e-5, inv_freq=None,
+                  magnitude=1.0, layout="half", return_rows=False, rows_out=None):
+    """Appends new tokens' latent rows to a paged cache (``latent_cache``, in place).
+
+    x [T, 576] bf16 (may be a slice of a fused projection): the latent's 512 channels, then the 64 key
+    channels that the heads share.  norm_w fp32 [512]: the latent is divided by its root mean square
+    (eps inside the root) and multiplied by norm_w; None: stored as it is.  inv_freq
+    (``rotary_inv_freq`` of at most 64 channels): the first shared channels are turned by the token's
+    place in its sequence; None: not.  context_lens, cu_seqlens and block_table as ``kv_append``.
+    Returns the rows, bf16 [T, 576], if return_rows or rows_out is given (for ``latent_expand``),
+    else None."""
+    lib = _lib or _load()
+    lay = _layout(layout)
+    index, cache_args = _latent_cache_args(cache)
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != LATENT_ROW:
+        raise ValueError(f"x must be [tokens, {LATENT_ROW}]")
+    x, xp, x_stride = _rows(x.unsqueeze(1), "x", torch.bfloat16, index)
+    T = x.shape[0]
+    table = _dense(block_table, "block_table", torch.int32, 2, index)
+    ctx = _dense(context_lens, "context_lens", torch.int32, 1, index)
+    N, max_blocks = block_table.shape
+    if context_lens.shape[0] != N:
+        raise ValueError("context_lens must have one entry per row of block_table")
+    cu = w = freq = rows = None
+    R = 0
+    if cu_seqlens is not None:
+        cu = _dense(cu_seqlens, "cu_seqlens", torch.int32, 1, index)
+        if cu_seqlens.shape[0] != N + 1:
+            raise ValueError("cu_seqlens must have one entry more than block_table has rows")
+    if norm_w is not None:
+        w = _dense(norm_w, "norm_w", torch.float32, 1, index)
+        if norm_w.shape[0] != LATENT_DIM:
+            raise ValueError(f"norm_w must have {LATENT_DIM} entries")
+    if inv_freq is not None:
+        freq, R = _dense(inv_freq, "inv_freq", torch.float64, 1, index), 2 * inv_freq.shape[0]
+    if return_rows or rows_out is not None:
+        rows_out, rows = _latent_out(rows_out, "rows_out", (T, LATENT_ROW), x.device, index)
+    _call(lib.kda_latent_append, index, xp, x_stride, T, *cache_args, table, max_blocks, ctx, cu, N, w, float(eps), freq,
+          magnitude, R, lay, rows)
+    return rows_out
+
+
+def latent_queries(q, w_kv, *, positions=None, inv_freq=None, magnitude=1.0, layout="half", out=None):
+    """Queries taken into the latent's space: q [T, H, 192] bf16 (rows may be strided), w_kv bf16
+    [H, 256, 512] or [H * 256, 512] (the projection from the latent, a head's 128 key rows before its
+    128 value rows) -> [T, H, 576]: the first 128 channels times the head's key rows, then the other 64,
+    turned by positions (int32 [T]) with inv_freq as ``latent_append`` does (None: as they are).
+    Host tensors are copied to the device and the result back."""
+    lib = _lib or _load()
+    lay = _layout(layout)
+    if not q.is_cuda:
+        dev = _device_of(w_kv, positions, inv_freq)
+        r = latent_queries(_prep(q, dev), _prep(w_kv, dev), positions=_prep(positions, dev), inv_freq=_prep(inv_freq, dev),
+                           magnitude=magnitude, layout=layout)
+        return _to_host((r,), True, (out,))[0]
+    index = q.get_device()
+    q, qp, q_stride = _rows(q, "q", torch.bfloat16, index)
+    T, H, D = q.shape
+    if D != LATENT_QUERY:
+        raise ValueError(f"q must be [tokens, heads, {LATENT_QUERY}]")
+    w, _ = _latent_weight(w_kv, H, index)
+    pos = freq = None
+    R = 0
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq come together")
+    if inv_freq is not None:
+        freq, R = _dense(inv_freq, "inv_freq", torch.float64, 1, index), 2 * inv_freq.shape[0]
+        pos = _dense(positions, "positions", torch.int32, 1, index)
+        if positions.shape[0] != T:
+            raise ValueError("positions must have one entry per token")
+    out, op = _latent_out(out, "out", (T, H, LATENT_ROW), q.device, index)
+    _call(lib.kda_latent_queries, index, qp, q_stride, T, H, w, pos, freq, magnitude, R, lay, op)
+    return out
+
+
+def attn_latent_workspace_size(n_seqs, tokens, heads, max_tokens) -> int:
+    """Bytes of workspace one attn_latent call needs; max_tokens: what the block table can hold,
+    max_blocks * page_size."""
+    return int(_load().kda_attn_latent_workspace_size(int(n_seqs), int(tokens), int(heads), int(max_tokens)))
+
+
+def attn_latent(q, cache, block_table, seq_lens, *, cu_seqlens=None, scale=None, out_dtype=torch.bfloat16,
+                return_lse=False, o=None, workspace=None):
+    """Causal attention over the paged latent cache: q [T, H, 576] bf16 (``latent_queries``; rows may
+    be strided), seq_lens int32 [N] tokens in the cache, the call's own included, block_table int32
+    [N, max_blocks].  cu_seqlens int32 [N + 1] on the device: which rows belong to which sequence (drafted
+    tokens, a piece of a prompt); None: one token per sequence (T = N).  The i-th of a sequence's n
+    tokens sees its first seq_lens - n + i + 1 rows.  scale: default 192^-0.5.
+
+    Returns o [T, H, 512] (zero for a token that sees nothing, NaN where a needed page number is out of
+    range; ``latent_values`` takes it to the heads' values) or, with return_lse, (o, lse [T, H]
+    fp32).  workspace: a uint8 tensor of attn_latent_workspace_size(...) bytes for this call alone,
+    or None: taken from torch's allocator for the call."""
+    lib = _lib or _load()
+    index, cache_args = _latent_cache_args(cache)
+    q, qp, q_stride = _rows(q, "q", torch.bfloat16, index)
+    T, H, D = q.shape
+    if D != LATENT_ROW:
+        raise ValueError(f"q must be [tokens, heads, {LATENT_ROW}]")
+    table = _dense(block_table, "block_table", torch.int32, 2, index)
+    lens = _dense(seq_lens, "seq_lens", torch.int32, 1, index)
+    N, max_blocks = block_table.shape
+    if seq_lens.shape[0] != N:
+        raise ValueError("seq_lens must have one entry per row of block_table")
+    cu = None
+    if cu_seqlens is not None:
+        cu = _dense(cu_seqlens, "cu_seqlens", torch.int32, 1, index)
+        if cu_seqlens.shape[0] != N + 1:
+            raise ValueError("cu_seqlens must have one entry more than block_table has rows")
+    elif T != N:
+        raise ValueError("without cu_seqlens there is one token per sequence")
+    device, shape = q.device, (T, H, LATENT_DIM)
+    if o is None:
+        o = torch.empty(shape, dtype=out_dtype, device=device)
+    elif o.shape != shape:
+        raise ValueError(f"o must be {list(shape)}")
+    lse = torch.empty((T, H), dtype=torch.float32, device=device) if return_lse else None
+    if workspace is None:
+        need, ws = lib.kda_attn_latent_workspace_size(N, T, H, max_blocks * cache_args[2]), None
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            ws = workspace.data_ptr()
+    else:
+        need, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    _call(lib.kda_attn_latent, index, qp, q_stride, T, H, *cache_args, table, max_blocks, lens, cu, N,
+          LATENT_QUERY ** -0.5 if scale is None else float(scale), _dense(o, "o", o.dtype, 3, index), _dt(o),
+          None if lse is None else lse.data_ptr(), ws, need)
+    return (o, lse) if return_lse else o
+
+
+def latent_values(o, w_kv, *, out=None):
+    """The attention's output taken back to each head's value channels: o [T, H, 512] bf16 (rows may be
+    strided), w_kv as ``latent_queries`` -> [T, H, 128] (the y of ``o_proj``).  Host tensors are copied
+    to the device and the result back."""
+    lib = _lib or _load()
+    if not o.is_cuda:
+        dev = _device_of(w_kv)
+        return _to_host((latent_values(_prep(o, dev), _prep(w_kv, dev)),), True, (out,))[0]
+    index = o.get_device()
+    o, op, o_stride = _rows(o, "o", torch.bfloat16, index)
+    T, H, D = o.shape
+    if D != LATENT_DIM:
+        raise ValueError(f"o must be [tokens, heads, {LATENT_DIM}]")
+    w, _ = _latent_weight(w_kv, H, index)
+    out, yp = _latent_out(out, "out", (T, H, LATENT_VALUE), o.device, index)
+    _call(lib.kda_latent_values, index, op, o_stride, T, H, w, yp)
+    return out
+
+
+def latent_expand(rows, w_kv, *, k_out=None, v_out=None):
+    """Every head's keys and values from latent rows (``latent_append``'s): rows [T, 576] bf16 (may be a
+    slice of a wider tensor), w_kv as ``latent_queries`` -> (k [T, H, 192], v [T, H, 128]) for
+    ``attn_prompt``.  Host tensors are copied to the device and the results back."""
+    lib = _lib or _load()
+    if not rows.is_cuda:
+        dev = _device_of(w_kv)
+        return _to_host(latent_expand(_prep(rows, dev), _prep(w_kv, dev)), True, (k_out, v_out))
+    index = rows.get_device()
+    if rows.dim() != 2 or rows.shape[1] != LATENT_ROW:
+        raise ValueError(f"rows must be [tokens, {LATENT_ROW}]")
+    rows, rp, r_stride = _rows(rows.unsqueeze(1), "rows", torch.bfloat16, index)
+    T = rows.shape[0]
+    w, H = _latent_weight(w_kv, None, index)
+    k, kp = _latent_out(k_out, "k_out", (T, H, LATENT_QUERY), rows.device, index)
+    v, vp = _latent_out(v_out, "v_out", (T, H, LATENT_VALUE), rows.device, index)
+    _call(lib.kda_latent_expand, index, rp, r_stride, T, H, w, kp, vp)
+    return k, v

@@ -10,6 +10,7 @@
 
 #include "kda_attn.cuh"
 #include "kda_internal.cuh"
+#include "kda_latent.cuh"
 
 namespace kda {
 
@@ -486,6 +487,43 @@ kda_status check_cache_args(const char *fn, const void *k, const void *v, const 
     return KDA_OK;
 }
 
+// The paged cache of latent rows and what says where a sequence's tokens lie in it.
+kda_status check_latent_cache(const char *fn, const void *cache, int num_pages, int page_size, const int32_t *table,
+                              int max_blocks, const int32_t *lens, const int32_t *cu, int n_seqs, int64_t tokens) {
+    KDA_REQUIRE(num_pages > 0 && max_blocks > 0 && n_seqs >= 0 && tokens >= 0, KDA_ERR_INVALID_ARG,
+                "%s: need positive num_pages and max_blocks, n_seqs >= 0 and tokens >= 0", fn);
+    KDA_REQUIRE(page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128, KDA_ERR_UNSUPPORTED,
+                "%s: page_size=%d (supported: 16, 32, 64, 128)", fn, page_size);
+    KDA_REQUIRE(cache, KDA_ERR_INVALID_ARG, "%s: the cache must not be NULL", fn);
+    KDA_REQUIRE(n_seqs == 0 || (table && lens), KDA_ERR_INVALID_ARG, "%s: block_table and the lengths must not be NULL", fn);
+    KDA_REQUIRE(tokens == 0 || n_seqs > 0, KDA_ERR_INVALID_ARG, "%s: tokens without sequences", fn);
+    KDA_REQUIRE(cu || tokens == n_seqs, KDA_ERR_INVALID_ARG,
+                "%s: without cu_seqlens there is one token per sequence (tokens=%lld, n_seqs=%d)", fn, (long long)tokens, n_seqs);
+    KDA_REQUIRE(n_seqs <= 65535 && tokens <= (1 << 30), KDA_ERR_UNSUPPORTED, "%s: at most 65535 sequences and 2^30 tokens", fn);
+    KDA_REQUIRE((int64_t)num_pages * page_size <= INT32_MAX - 256, KDA_ERR_UNSUPPORTED,
+                "%s: num_pages * page_size must stay below 2^31 - 256", fn);
+    KDA_REQUIRE((int64_t)max_blocks * page_size <= INT32_MAX - 256, KDA_ERR_INVALID_ARG,
+                "%s: max_blocks * page_size must stay below 2^31 - 256", fn);
+    KDA_REQUIRE(aligned16(cache), KDA_ERR_INVALID_ARG, "%s: the cache must be 16-byte aligned", fn);
+    const void *words[] = {table, lens, cu};
+    for (const void *ptr : words)
+        KDA_REQUIRE(aligned_to(ptr, 4), KDA_ERR_INVALID_ARG, "%s: block_table, lengths and cu_seqlens must be 4-byte aligned", fn);
+    return KDA_OK;
+}
+
+// Arguments of the products with the projection from the latent: rows of `row` elements.
+kda_status check_latent_product(const char *fn, const void *x, const char *x_name, int64_t stride, int64_t row, int64_t tokens,
+                                int heads, const void *w, const void *out, const void *out2) {
+    KDA_REQUIRE(tokens >= 0 && heads > 0, KDA_ERR_INVALID_ARG, "%s: need tokens >= 0 and heads > 0", fn);
+    KDA_REQUIRE(tokens <= (1 << 30) && heads <= 4096 && (tokens + 127) / 128 * heads <= INT32_MAX / 8, KDA_ERR_UNSUPPORTED,
+                "%s: at most 4096 heads, 2^30 tokens and 2^28 tiles of 128 tokens of a head", fn);
+    KDA_REQUIRE(w && (tokens == 0 || (x && out && out2)), KDA_ERR_INVALID_ARG, "%s: no tensor may be NULL", fn);
+    const void *ptrs[] = {x, w, out, out2};
+    for (const void *ptr : ptrs)
+        KDA_REQUIRE(aligned16(ptr), KDA_ERR_INVALID_ARG, "%s: every tensor must be 16-byte aligned", fn);
+    return check_stride(fn, x_name, stride, row, 2);
+}
+
 // No output shares bytes with an input or with another output.
 kda_status check_apart(const char *fn, const Span *in, int n_in, const Span *out, int n_out) {
     for (int i = 0; i < n_out; ++i) {
@@ -560,14 +598,16 @@ kda_status kda_device_status(void *stream) {
     const int n_conv = kda::take_short_conv_timeouts(st);
     const int n_proj = kda::take_oproj_timeouts(st);
     const int n_attn_p = kda::take_attn_prompt_timeouts(st), n_attn_d = kda::take_attn_decode_timeouts(st);
-    if (n_tc0 < 0 || n_prep < 0 || n_chain < 0 || n_dec < 0 || n_conv < 0 || n_proj < 0 || n_attn_p < 0 || n_attn_d < 0)
+    const int n_attn_l = kda::take_attn_latent_timeouts(st), n_lat = kda::take_latent_product_timeouts(st);
+    if (n_tc0 < 0 || n_prep < 0 || n_chain < 0 || n_dec < 0 || n_conv < 0 || n_proj < 0 || n_attn_p < 0 || n_attn_d < 0 ||
+        n_attn_l < 0 || n_lat < 0)
         return KDA_ERR_CUDA;
-    const int n_attn = n_attn_p + n_attn_d;
+    const int n_attn = n_attn_p + n_attn_d + n_attn_l;
     const int n_tc = n_tc0 + n_prep + n_chain;
-    if (n_tc + n_dec + n_conv + n_proj + n_attn > 0) {
+    if (n_tc + n_dec + n_conv + n_proj + n_attn + n_lat > 0) {
         set_error("kda_device_status: bounded waits gave up in %d prefill, %d decode, %d short-convolution, %d "
-                  "output-projection and %d attention CTAs; their outputs hold NaN",
-                  n_tc, n_dec, n_conv, n_proj, n_attn);
+                  "output-projection, %d attention and %d latent-product CTAs; their outputs hold NaN",
+                  n_tc, n_dec, n_conv, n_proj, n_attn, n_lat);
         return KDA_ERR_TIMEOUT;
     }
     return KDA_OK;
@@ -1037,6 +1077,182 @@ kda_status kda_attn_prompt(const void *q, int64_t q_stride, const void *k, int64
     p.ws = need ? static_cast<float *>(workspace) : nullptr;
     p.polls = std::min(kda::wait_polls(), kda::kAttnPolls);
     return kda::launch_attn_prompt(p, (cudaStream_t)stream);
+}
+
+kda_status kda_latent_append(const void *x, int64_t x_stride, int64_t tokens, void *cache, int num_pages, int page_size,
+                             const int32_t *block_table, int max_blocks, const int32_t *context_lens,
+                             const int32_t *cu_seqlens, int n_seqs, const float *norm_w, float eps, const double *inv_freq,
+                             float magnitude, int rotary_dim, int layout, void *rows_out, void *stream) {
+    kda::g_err[0] = 0;
+    const char *fn = "kda_latent_append";
+    kda_status s = check_latent_cache(fn, cache, num_pages, page_size, block_table, max_blocks, context_lens, cu_seqlens, n_seqs,
+                                      tokens);
+    if (s != KDA_OK) return s;
+    if ((s = check_rotary_args(fn, inv_freq, magnitude, rotary_dim, layout, kda::kShared)) != KDA_OK) return s;
+    KDA_REQUIRE(tokens == 0 || x, KDA_ERR_INVALID_ARG, "%s: x must not be NULL", fn);
+    // (2^-100: mean(c^2) + eps keeps its precision down to the smallest sums that fp32 holds)
+    KDA_REQUIRE(!norm_w || (std::isfinite(eps) && eps >= 7.888609052210118e-31f), KDA_ERR_INVALID_ARG,
+                "%s: eps must be finite and at least 2^-100", fn);
+    KDA_REQUIRE(aligned16(x) && aligned16(rows_out), KDA_ERR_INVALID_ARG, "%s: x and rows_out must be 16-byte aligned", fn);
+    KDA_REQUIRE(aligned_to(norm_w, 4), KDA_ERR_INVALID_ARG, "%s: norm_w must be 4-byte aligned", fn);
+    if ((s = check_stride(fn, "x", x_stride, kda::kRow, 2)) != KDA_OK) return s;
+    const Span in[] = {{x, strided_bytes(tokens, kda::kRow, x_stride, 2), "x"},
+                       {block_table, (size_t)n_seqs * max_blocks * 4, "block_table"},
+                       {context_lens, (size_t)n_seqs * 4, "context_lens"},
+                       {cu_seqlens, ((size_t)n_seqs + 1) * 4, "cu_seqlens"},
+                       {norm_w, (size_t)kda::kLatent * 4, "norm_w"},
+                       {inv_freq, (size_t)rotary_dim / 2 * 8, "inv_freq"}};
+    const Span out[] = {{cache, (size_t)num_pages * page_size * kda::kRow * 2, "the cache"},
+                        {rows_out, (size_t)tokens * kda::kRow * 2, "rows_out"}};
+    if ((s = check_apart(fn, in, 6, out, 2)) != KDA_OK) return s;
+    kda::LatentAppendParams p;
+    p.c = kda::LatentCache{static_cast<__nv_bfloat16 *>(cache), block_table, context_lens, num_pages, max_blocks, page_size,
+                           n_seqs, __builtin_ctz(page_size)};
+    p.x = static_cast<const __nv_bfloat16 *>(x);
+    p.x_stride = x_stride;
+    p.tokens = tokens;
+    p.cu_seqlens = cu_seqlens;
+    p.norm_w = norm_w;
+    p.eps = eps;
+    p.rot = kda::RotaryParams{inv_freq, magnitude, rotary_dim, layout == KDA_ROTARY_INTERLEAVED, 1.f};
+    p.rows_out = static_cast<__nv_bfloat16 *>(rows_out);
+    return kda::launch_latent_append(p, (cudaStream_t)stream);
+}
+
+kda_status kda_latent_queries(const void *q, int64_t q_stride, int64_t tokens, int heads, const void *w_kv,
+                              const int32_t *positions, const double *inv_freq, float magnitude, int rotary_dim, int layout,
+                              void *out, void *stream) {
+    kda::g_err[0] = 0;
+    const char *fn = "kda_latent_queries";
+    const int64_t row = (int64_t)heads * kda::kHeadQuery;
+    kda_status s = check_latent_product(fn, q, "q", q_stride, row, tokens, heads, w_kv, out, out);
+    if (s != KDA_OK) return s;
+    if ((s = check_rotary_args(fn, inv_freq, magnitude, rotary_dim, layout, kda::kShared)) != KDA_OK) return s;
+    KDA_REQUIRE(tokens == 0 || (rotary_dim > 0) == (positions != nullptr), KDA_ERR_INVALID_ARG,
+                "%s: positions and inv_freq come together", fn);
+    KDA_REQUIRE(aligned_to(positions, 4), KDA_ERR_INVALID_ARG, "%s: positions must be 4-byte aligned", fn);
+    const Span in[] = {{q, strided_bytes(tokens, row, q_stride, 2), "q"},
+                       {w_kv, (size_t)heads * 256 * kda::kLatent * 2, "w_kv"},
+                       {positions, (size_t)tokens * 4, "positions"},
+                       {inv_freq, (size_t)rotary_dim / 2 * 8, "inv_freq"}};
+    const Span outs[] = {{out, (size_t)tokens * heads * kda::kRow * 2, "out"}};
+    if ((s = check_apart(fn, in, 4, outs, 1)) != KDA_OK) return s;
+    kda::LatentProductParams p = {};
+    p.what = kda::kLatentQueries;
+    p.x = static_cast<const __nv_bfloat16 *>(q);
+    p.x_stride = q_stride;
+    p.tokens = tokens;
+    p.H = heads;
+    p.w = static_cast<const __nv_bfloat16 *>(w_kv);
+    p.positions = positions;
+    p.rot = kda::RotaryParams{inv_freq, magnitude, rotary_dim, layout == KDA_ROTARY_INTERLEAVED, 1.f};
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.polls = std::min(kda::wait_polls(), kda::kAttnPolls);
+    return kda::launch_latent_product(p, (cudaStream_t)stream);
+}
+
+kda_status kda_latent_values(const void *o, int64_t o_stride, int64_t tokens, int heads, const void *w_kv, void *out,
+                             void *stream) {
+    kda::g_err[0] = 0;
+    const char *fn = "kda_latent_values";
+    const int64_t row = (int64_t)heads * kda::kLatent;
+    kda_status s = check_latent_product(fn, o, "o", o_stride, row, tokens, heads, w_kv, out, out);
+    if (s != KDA_OK) return s;
+    const Span in[] = {{o, strided_bytes(tokens, row, o_stride, 2), "o"}, {w_kv, (size_t)heads * 256 * kda::kLatent * 2, "w_kv"}};
+    const Span outs[] = {{out, (size_t)tokens * heads * kda::kHeadValue * 2, "out"}};
+    if ((s = check_apart(fn, in, 2, outs, 1)) != KDA_OK) return s;
+    kda::LatentProductParams p = {};
+    p.what = kda::kLatentValues;
+    p.x = static_cast<const __nv_bfloat16 *>(o);
+    p.x_stride = o_stride;
+    p.tokens = tokens;
+    p.H = heads;
+    p.w = static_cast<const __nv_bfloat16 *>(w_kv);
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.polls = std::min(kda::wait_polls(), kda::kAttnPolls);
+    return kda::launch_latent_product(p, (cudaStream_t)stream);
+}
+
+kda_status kda_latent_expand(const void *rows, int64_t rows_stride, int64_t tokens, int heads, const void *w_kv, void *k,
+                             void *v, void *stream) {
+    kda::g_err[0] = 0;
+    const char *fn = "kda_latent_expand";
+    kda_status s = check_latent_product(fn, rows, "rows", rows_stride, kda::kRow, tokens, heads, w_kv, k, v);
+    if (s != KDA_OK) return s;
+    const Span in[] = {{rows, strided_bytes(tokens, kda::kRow, rows_stride, 2), "rows"},
+                       {w_kv, (size_t)heads * 256 * kda::kLatent * 2, "w_kv"}};
+    const Span outs[] = {{k, (size_t)tokens * heads * kda::kHeadQuery * 2, "k"}, {v, (size_t)tokens * heads * kda::kHeadValue * 2, "v"}};
+    if ((s = check_apart(fn, in, 2, outs, 2)) != KDA_OK) return s;
+    kda::LatentProductParams p = {};
+    p.what = kda::kLatentExpand;
+    p.x = static_cast<const __nv_bfloat16 *>(rows);
+    p.x_stride = rows_stride;
+    p.tokens = tokens;
+    p.H = heads;
+    p.w = static_cast<const __nv_bfloat16 *>(w_kv);
+    p.out = static_cast<__nv_bfloat16 *>(k);
+    p.out2 = static_cast<__nv_bfloat16 *>(v);
+    p.polls = std::min(kda::wait_polls(), kda::kAttnPolls);
+    return kda::launch_latent_product(p, (cudaStream_t)stream);
+}
+
+size_t kda_attn_latent_workspace_size(int n_seqs, int64_t tokens, int heads, int64_t max_tokens) {
+    if (n_seqs <= 0 || n_seqs > 65535 || tokens <= 0 || tokens > (1 << 30) || heads <= 0 || heads > 4096 || max_tokens < 0 ||
+        max_tokens > INT32_MAX - 256)
+        return 0;
+    return kda::attn_latent_workspace_bytes(n_seqs, tokens, heads, max_tokens);
+}
+
+kda_status kda_attn_latent(const void *q, int64_t q_stride, int64_t tokens, int heads, const void *cache, int num_pages,
+                           int page_size, const int32_t *block_table, int max_blocks, const int32_t *seq_lens,
+                           const int32_t *cu_seqlens, int n_seqs, float scale, void *o, kda_dtype o_dtype, float *lse,
+                           void *workspace, size_t workspace_bytes, void *stream) {
+    kda::g_err[0] = 0;
+    const char *fn = "kda_attn_latent";
+    kda_status s = check_latent_cache(fn, cache, num_pages, page_size, block_table, max_blocks, seq_lens, cu_seqlens, n_seqs,
+                                      tokens);
+    if (s != KDA_OK) return s;
+    KDA_REQUIRE(heads > 0, KDA_ERR_INVALID_ARG, "%s: need heads > 0", fn);
+    KDA_REQUIRE(heads <= 4096, KDA_ERR_UNSUPPORTED, "%s: at most 4096 heads", fn);
+    KDA_REQUIRE(dtype_ok(o_dtype), KDA_ERR_UNSUPPORTED, "%s: unsupported dtype", fn);
+    KDA_REQUIRE(scale != 0.f && std::fabs(scale) <= 1.2676506002282294e30f, KDA_ERR_INVALID_ARG,
+                "%s: scale must not be 0 and lie within 2^100", fn);
+    KDA_REQUIRE(tokens == 0 || (q && o), KDA_ERR_INVALID_ARG, "%s: q and o must not be NULL", fn);
+    const int64_t row = (int64_t)heads * kda::kRow;
+    if ((s = check_stride(fn, "q", q_stride, row, 2)) != KDA_OK) return s;
+    const void *ptrs[] = {q, o, workspace};
+    for (const void *ptr : ptrs)
+        KDA_REQUIRE(aligned16(ptr), KDA_ERR_INVALID_ARG, "%s: q, o and the workspace must be 16-byte aligned", fn);
+    KDA_REQUIRE(aligned_to(lse, 4), KDA_ERR_INVALID_ARG, "%s: lse must be 4-byte aligned", fn);
+    if (tokens == 0) return KDA_OK;
+    const size_t need = kda::attn_latent_workspace_bytes(n_seqs, tokens, heads, (int64_t)max_blocks * page_size);
+    KDA_REQUIRE(need == 0 || (workspace && workspace_bytes >= need), KDA_ERR_INVALID_ARG,
+                "%s: the workspace holds %zu bytes, this call needs %zu (kda_attn_latent_workspace_size)", fn,
+                workspace ? workspace_bytes : (size_t)0, need);
+    const Span in[] = {{q, strided_bytes(tokens, row, q_stride, 2), "q"},
+                       {cache, (size_t)num_pages * page_size * kda::kRow * 2, "the cache"},
+                       {block_table, (size_t)n_seqs * max_blocks * 4, "block_table"},
+                       {seq_lens, (size_t)n_seqs * 4, "seq_lens"},
+                       {cu_seqlens, ((size_t)n_seqs + 1) * 4, "cu_seqlens"}};
+    const Span out[] = {{o, (size_t)tokens * heads * kda::kLatent * esize(o_dtype), "o"},
+                        {lse, (size_t)tokens * heads * 4, "lse"},
+                        {workspace, need, "the workspace"}};
+    if ((s = check_apart(fn, in, 5, out, 3)) != KDA_OK) return s;
+    kda::AttnLatentParams p;
+    p.c = kda::LatentCache{static_cast<__nv_bfloat16 *>(const_cast<void *>(cache)), block_table, seq_lens, num_pages, max_blocks,
+                           page_size, n_seqs, __builtin_ctz(page_size)};
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.q_stride = q_stride;
+    p.tokens = (int)tokens;
+    p.H = heads;
+    p.cu_seqlens = cu_seqlens;
+    p.scale = scale;
+    p.o = o;
+    p.o_bf16 = o_dtype == KDA_BF16;
+    p.lse = lse;
+    p.ws = static_cast<float *>(workspace);
+    p.polls = std::min(kda::wait_polls(), kda::kAttnPolls);
+    return kda::launch_attn_latent(p, (cudaStream_t)stream);
 }
 
 }  // extern "C"

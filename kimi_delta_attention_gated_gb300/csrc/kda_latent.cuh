@@ -1,0 +1,92 @@
+// kda_latent.cuh -- definitions shared by the latent-attention operators: the paged cache of one
+// vector a token and its append (kda_latent_append.cu), the products with the projection from the
+// latent to each head's keys and values (kda_latent_proj.cu), and attention over the cache
+// (kda_attn_latent.cu).
+//
+// A token's row is [c | r]: c the 512 channels of the latent, from which every head's 128 key and
+// 128 value channels are linear images, k_h = Wk_h c and v_h = Wv_h c, and r 64 key channels that
+// all heads share.  A head's score of a query (qn | qr) of 128 + 64 channels is
+//     qn . Wk_h c + qr . r = (Wk_h^T qn | qr) . (c | r),
+// and its output sum_j p_j Wv_h c_j = Wv_h (sum_j p_j c_j): attention can run on the rows
+// themselves, with queries of 576 channels and outputs of 512, as over one key head for all.
+#pragma once
+
+#include "kda_attn.cuh"
+
+namespace kda {
+
+constexpr int kLatent = 512;               // channels of the latent
+constexpr int kShared = 64;                // key channels that the heads share
+constexpr int kRow = kLatent + kShared;    // a token's row
+constexpr int kHeadKey = 128, kHeadValue = 128;
+constexpr int kHeadQuery = kHeadKey + kShared;
+
+struct LatentCache {
+    __nv_bfloat16 *rows;          // [pages, P, kRow]
+    const int32_t *block_table;   // [N, max_blocks]
+    const int32_t *lens;          // [N] tokens in the cache
+    int n_pages, max_blocks, P, N;
+    int p_shift;                  // P = 1 << p_shift
+};
+
+struct LatentAppendParams {
+    LatentCache c;                // lens: tokens before this call
+    const __nv_bfloat16 *x;       // rows of kRow, x_stride elements apart
+    int64_t x_stride, tokens;
+    const int32_t *cu_seqlens;    // [N + 1] or null: one token per sequence
+    const float *norm_w;          // [kLatent] or null: not normalised
+    float eps;
+    RotaryParams rot;             // of the shared channels; R at most kShared
+    __nv_bfloat16 *rows_out;      // [tokens, kRow] or null
+};
+
+enum LatentProduct { kLatentQueries = 0, kLatentValues = 1, kLatentExpand = 2 };
+
+struct LatentProductParams {
+    int what;                     // a LatentProduct
+    const __nv_bfloat16 *x;       // rows x_stride elements apart
+    int64_t x_stride, tokens;
+    int H;
+    const __nv_bfloat16 *w;       // [H, kHeadKey + kHeadValue, kLatent]
+    const int32_t *positions;     // [tokens] (queries), where rot.inv_freq is given
+    RotaryParams rot;
+    __nv_bfloat16 *out, *out2;    // dense; expand: keys and values
+    uint32_t polls;
+};
+
+struct AttnLatentParams {
+    LatentCache c;                // lens: tokens to attend to, the call's own included
+    const __nv_bfloat16 *q;       // rows of H * kRow, q_stride elements apart
+    int64_t q_stride;
+    int tokens, H;
+    const int32_t *cu_seqlens;    // [N + 1] or null: one token per sequence
+    float scale;
+    void *o;                      // [tokens, H, kLatent]
+    int o_bf16;
+    float *lse;                   // [tokens, H] or null
+    float *ws;                    // sums of parts of the tokens
+    uint32_t polls;               // bound on the copies' waits
+};
+
+kda_status launch_latent_append(const LatentAppendParams &p, cudaStream_t st);
+kda_status launch_latent_product(const LatentProductParams &p, cudaStream_t st);
+size_t attn_latent_workspace_bytes(int64_t N, int64_t tokens, int H, int64_t max_tokens);
+kda_status launch_attn_latent(const AttnLatentParams &p, cudaStream_t st);
+int take_latent_product_timeouts(cudaStream_t st);
+int take_attn_latent_timeouts(cudaStream_t st);
+
+// Rows of sequence n in a call, clamped to the tensors.
+__device__ __forceinline__ void call_rows(const int32_t *cu, int64_t tokens, int n, int64_t &t0, int &len) {
+    if (!cu) {
+        t0 = n;
+        len = 1;
+        return;
+    }
+    int64_t a = __ldg(cu + n), b = __ldg(cu + n + 1);
+    a = max((int64_t)0, min(a, tokens));
+    b = max(a, min(b, tokens));
+    t0 = a;
+    len = (int)(b - a);
+}
+
+}  // namespace kda
