@@ -693,7 +693,8 @@ kda_status kda_latent_queries(const void *q, int64_t q_stride, int64_t tokens, i
  * tokens are in the cache already (kda_latent_append) and counted by seq_lens.  A token that sees
  * nothing gives zero rows and lse -INFINITY.
  *
- *   q           [tokens, heads, KDA_LATENT_ROW] bf16, q_stride apart (kda_latent_queries)
+ *   q           [tokens, heads, KDA_LATENT_ROW] bf16, q_stride apart (kda_latent_queries); at most 2^24
+ *               tokens
  *   cu_seqlens  [n_seqs + 1] int32: sequence n's tokens are rows [cu_seqlens[n], cu_seqlens[n + 1])
  *               (clamped to [0, tokens]); rows of no sequence are left as they are.  NULL: one token
  *               per sequence, tokens == n_seqs

@@ -1197,7 +1197,7 @@ kda_status kda_latent_expand(const void *rows, int64_t rows_stride, int64_t toke
 }
 
 size_t kda_attn_latent_workspace_size(int n_seqs, int64_t tokens, int heads, int64_t max_tokens) {
-    if (n_seqs <= 0 || n_seqs > 65535 || tokens <= 0 || tokens > (1 << 30) || heads <= 0 || heads > 4096 || max_tokens < 0 ||
+    if (n_seqs <= 0 || n_seqs > 65535 || tokens <= 0 || tokens > (1 << 24) || heads <= 0 || heads > 4096 || max_tokens < 0 ||
         max_tokens > INT32_MAX - 256)
         return 0;
     return kda::attn_latent_workspace_bytes(n_seqs, tokens, heads, max_tokens);
@@ -1213,7 +1213,7 @@ kda_status kda_attn_latent(const void *q, int64_t q_stride, int64_t tokens, int 
                                       tokens);
     if (s != KDA_OK) return s;
     KDA_REQUIRE(heads > 0, KDA_ERR_INVALID_ARG, "%s: need heads > 0", fn);
-    KDA_REQUIRE(heads <= 4096, KDA_ERR_UNSUPPORTED, "%s: at most 4096 heads", fn);
+    KDA_REQUIRE(heads <= 4096 && tokens <= (1 << 24), KDA_ERR_UNSUPPORTED, "%s: at most 4096 heads and 2^24 tokens", fn);
     KDA_REQUIRE(dtype_ok(o_dtype), KDA_ERR_UNSUPPORTED, "%s: unsupported dtype", fn);
     KDA_REQUIRE(scale != 0.f && std::fabs(scale) <= 1.2676506002282294e30f, KDA_ERR_INVALID_ARG,
                 "%s: scale must not be 0 and lie within 2^100", fn);

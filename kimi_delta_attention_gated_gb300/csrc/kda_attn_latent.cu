@@ -39,11 +39,11 @@ using namespace tc;
 
 constexpr int kStep = 64;               // cached tokens of a step
 constexpr int kTileRows = 64;           // query rows of a tile at most
-constexpr int kSoftWarps = 4, kMmaWarp = 4, kLoadWarp = 5;
-constexpr int kThreads = 192;
+constexpr int kSoftWarps = 4, kScoreWarp = 4, kValueWarp = 5, kLoadWarp = 6;
+constexpr int kThreads = 224;
 constexpr int kSlots = 4;               // work items under way
 constexpr int kPad = 4;                 // a unit's own cost in steps
-constexpr int kMinPiece = 6;            // places of a CTA at least
+constexpr int kMinPiece = 2;            // places of a CTA at least
 constexpr int kMaxUnits = 12, kMaxShared = 4;  // ring places at most
 constexpr uint32_t kUnitBytes = kStep * 256, kSharedBytes = kStep * 128;
 constexpr uint32_t kTmemO = 2 * kStep;  // TMEM columns: scores of two steps, then O^T
@@ -51,7 +51,6 @@ constexpr float kSlack = 8.f;           // log2: how far a score may exceed the 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNaN = __builtin_nanf("");
 constexpr int kMaxSmem = 232448;
-constexpr uint32_t kProductPolls = 1u << 27;  // of the products' warp, which looks without waiting: seconds
 
 __device__ int g_attn_latent_timeouts = 0;
 
@@ -60,7 +59,9 @@ struct Plan {
     int parts;        // tiles that share a token's heads
     int G;            // tiles of a unit
     int pieces;       // of the line
-    int cut;          // units may be cut; else each lies in the piece where it begins
+    int cut;          // units may be cut; else piece i is the i-th unit
+    int64_t most_units;  // of the call at most
+    int units_one;    // of a sequence with one token
     int n;            // rows of a tile as the products' N: hp * tk, a multiple of 16
     int units, shared;  // ring places
     uint32_t at_p, at_units, at_shared, at_bars;  // shared memory
@@ -84,15 +85,14 @@ struct Item {
 };
 
 struct Bars {
-    uint64_t q_full, q_empty, o_free, p_ready, p_free, drain;
-    uint64_t s_full[2], s_free[2];
-    uint64_t i_full[kSlots], i_empty[kSlots];
-    uint64_t u_full[kMaxUnits], u_empty[kMaxUnits];
-    uint64_t r_full[kMaxShared], r_empty[kMaxShared];
+    uint64_t o_free, p_ready, s_free[2];  // arrivals: the softmax's warps
+    uint64_t i_empty[kSlots];             // and the products' threads
+    uint64_t q_full, q_empty, p_free, drain[2], s_full[2], i_full[kSlots];  // one
+    uint64_t u_full[kMaxUnits], u_empty[kMaxUnits], r_full[kMaxShared], r_empty[kMaxShared];
     Item slots[kSlots];
     int64_t row_at[kTileRows];   // a row's place in o, or -1
     float factor[kTileRows];
-    int64_t scan[kThreads / 32];
+    int64_t scan[kThreads / 32][2];
     int64_t start_begin;
     int start_seq;
     uint32_t tmem;
@@ -109,10 +109,12 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *r) {
+// 16 lanes of 64 columns: the lower half of the warp's threads reads columns 0 to 31, the upper half the
+// same lanes' columns 32 to 63.
+__device__ __forceinline__ void tmem_ld_halves(uint32_t taddr, float *r) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32], 32;"
         : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
           "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
           "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
@@ -139,16 +141,6 @@ __device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float *r) {
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
     return (uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32 | lo;
 }
-// Whether a phase is over, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
 // A barrier of the softmax's warps that also says whether any of their threads has `x`.
 __device__ __forceinline__ bool soft_any(bool x) {
     uint32_t r;
@@ -170,43 +162,53 @@ __device__ __forceinline__ int tokens_of(const LatentCache &c, int n) {
     return (int)max((int64_t)0, min((int64_t)__ldg(c.lens + n), room));
 }
 __host__ __device__ __forceinline__ int steps_of(int tokens) { return (int)(((int64_t)tokens + kStep - 1) / kStep); }
-// Units of a sequence with nq rows in the call.
-__host__ __device__ __forceinline__ int64_t units_of(const Plan &pl, int64_t nq) {
-    const int64_t tiles = (nq + pl.tk - 1) / pl.tk * pl.parts;
-    return (tiles + pl.G - 1) / pl.G;
+// Units of a sequence with nq rows in the call (tiles stay below 2^31: 2^24 rows, 64 tiles of a token).
+__host__ __device__ __forceinline__ int units_of(const Plan &pl, int nq) {
+    if (nq <= 1) return nq * pl.units_one;
+    const uint32_t tiles = ((uint32_t)nq + pl.tk - 1) / pl.tk * pl.parts;
+    return (int)((tiles + pl.G - 1) / pl.G);
 }
-__device__ __forceinline__ int64_t places_of(const Args &a, int n) {
+// Its units, and their places on the line.
+__device__ __forceinline__ int units_of(const Args &a, int n) {
     int64_t t0;
     int nq;
     call_rows(a.p.cu_seqlens, a.p.tokens, n, t0, nq);
-    return nq == 0 ? 0 : units_of(a.plan, nq) * (steps_of(tokens_of(a.p.c, n)) + kPad);
+    return units_of(a.plan, nq);
 }
+__device__ __forceinline__ int64_t unit_places(const Args &a, int n) { return steps_of(tokens_of(a.p.c, n)) + kPad; }
 
-// Every thread's share of the sequences measured: the line's length, and where the share begins.
+// Every thread's share [first, last) of the sequences measured: the line's length, and the places (and
+// units) of the sequences before the share.
 struct Line {
-    int64_t total, mine;
+    int64_t total, mine, units;
     int first, last;
 };
-__device__ __forceinline__ Line measure_line(const Args &a, int64_t *scan, int threads) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = a.p.c.N, per = (N + threads - 1) / threads;
+template <int THREADS>
+__device__ __forceinline__ Line measure_line(const Args &a, int64_t (*scan)[2]) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = a.p.c.N, per = (N + THREADS - 1) / THREADS;
     Line l;
     l.first = min(tid * per, N);
     l.last = min(l.first + per, N);
-    int64_t own = 0;
-    for (int n = l.first; n < l.last; ++n) own += places_of(a, n);
-    int64_t x = own;
+    int64_t own = 0, own_units = 0;
+    for (int n = l.first; n < l.last; ++n) {
+        const int64_t u = units_of(a, n);
+        own_units += u;
+        own += u * unit_places(a, n);
+    }
+    int64_t x = own, y = own_units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const int64_t dx = __shfl_up_sync(0xffffffffu, x, o), dy = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) x += dx, y += dy;
     }
-    if (lane == 31) scan[warp] = x;
+    if (lane == 31) scan[warp][0] = x, scan[warp][1] = y;
     __syncthreads();
     l.mine = x - own;
+    l.units = y - own_units;
     l.total = 0;
-    for (int w = 0; w < threads / 32; ++w) {
-        if (w < warp) l.mine += scan[w];
-        l.total += scan[w];
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) l.mine += scan[w][0], l.units += scan[w][1];
+        l.total += scan[w][0];
     }
     return l;
 }
@@ -216,24 +218,37 @@ __host__ __device__ __forceinline__ int64_t piece_places(int64_t total, int piec
 struct Tile {
     int t0, tokens, head0, seen0, steps;
 };
-__device__ __forceinline__ Tile tile_of(const Plan &pl, int64_t t0, int nq, int len, int64_t r) {
-    const int64_t i0 = r / pl.parts * pl.tk;
+__device__ __forceinline__ Tile tile_of(const Plan &pl, int64_t t0, int nq, int len, int r) {
+    const int of = r / pl.parts, i0 = of * pl.tk;
     Tile t;
-    t.head0 = (int)(r % pl.parts) * pl.hp;
-    t.tokens = (int)max((int64_t)0, min((int64_t)pl.tk, nq - i0));
-    t.t0 = (int)(t0 + i0);
-    t.seen0 = (int)(len - nq + i0 + 1);
+    t.head0 = (r - of * pl.parts) * pl.hp;
+    t.tokens = max(0, min(pl.tk, nq - i0));
+    t.t0 = (int)t0 + i0;
+    t.seen0 = len - nq + i0 + 1;
     t.steps = t.tokens > 0 ? steps_of(max(0, t.seen0 + t.tokens - 1)) : 0;
     return t;
 }
-__device__ __forceinline__ int64_t part_floats(const Plan &pl) { return (int64_t)pl.hp * pl.tk * (kLatent + 2); }
+// What a part leaves in the workspace (two a CTA; behind them a JoinHead for each CTA): O as [128-channel block][row / 4][channel][row % 4], the rows' references
+// and their sums.
+__host__ __device__ __forceinline__ int64_t part_floats(const Plan &pl) { return (int64_t)pl.n * (kLatent + 2); }
+
+// What the joining launch has to know of the tile that begins in a piece and goes on behind it.
+struct __align__(16) JoinHead {
+    int t0, tokens, head0, last;  // its rows; tokens 0: there is none; the piece of its last step
+};
+
+__device__ __forceinline__ int4 *join_head(const Args &a, int cta) {
+    return reinterpret_cast<int4 *>(a.p.ws + (int64_t)a.plan.pieces * a.plan.G * 2 * part_floats(a.plan)) + cta;
+}
 
 // Goes through the work items of one tile place `g` of a piece.
 struct Walk {
-    int64_t L0, L1, begin, u, units;  // the piece, the next unit's place on the line, its number in its sequence
-    int n, nq, len;
+    int64_t L0, L1, S, begin;  // the piece, the next unit's place on the line (without cuts: units)
+    int n, u, units, nq, len;  // the next unit: its sequence, and number there
     int64_t t0;
-    __device__ void open(const Args &a) {  // the sequence n, or the next one with rows
+    bool open;
+    JoinHead join;
+    __device__ void look(const Args &a) {  // at sequence n, or the next one with rows
         for (;; ++n) {
             if (n >= a.p.c.N) return;
             call_rows(a.p.cu_seqlens, a.p.tokens, n, t0, nq);
@@ -241,18 +256,19 @@ struct Walk {
         }
         len = tokens_of(a.p.c, n);
         units = units_of(a.plan, nq);
+        open = true;
     }
-    __device__ void start(const Args &a, int64_t l0, int64_t l1, int seq, int64_t seq_begin) {
+    __device__ void start(const Args &a, int64_t l0, int64_t l1, int64_t s, int seq, int64_t seq_begin) {
         L0 = l0;
         L1 = l1;
-        n = seq;
-        if (n < 0) {
-            n = a.p.c.N;
-            return;
-        }
-        open(a);
-        const int64_t per = steps_of(len) + kPad;
-        u = (l0 - seq_begin) / per;
+        S = s;
+        open = false;
+        join.t0 = join.tokens = join.head0 = join.last = 0;
+        n = seq < 0 ? a.p.c.N : seq;
+        if (n >= a.p.c.N) return;
+        look(a);
+        const int64_t per = a.plan.cut ? steps_of(len) + kPad : 1;
+        u = (int)((l0 - seq_begin) / per);
         begin = seq_begin + u * per;
     }
     __device__ Item next(const Args &a, int piece, int g) {
@@ -261,15 +277,17 @@ struct Walk {
         it.found = 0;
         it.bad = 0;
         while (n < a.p.c.N && begin < L1) {
+            if (!open) look(a);
+            if (n >= a.p.c.N) break;
             const int steps = steps_of(len);
             const int64_t first = begin + kPad, at = begin;
             const Tile t = tile_of(pl, t0, nq, len, u * pl.G + g);
             it.seq = n;
-            begin += steps + kPad;
+            begin += pl.cut ? steps + kPad : 1;
             if (++u == units) {
                 ++n;
                 u = 0;
-                open(a);
+                open = false;
             }
             if (t.tokens == 0) continue;
             it.t0 = t.t0;
@@ -278,7 +296,7 @@ struct Walk {
             it.seen0 = t.seen0;
             it.part = -1;
             if (!pl.cut || t.steps == 0) {
-                if (at < L0) continue;
+                if (at < L0) continue;  // the piece's before
                 it.s0 = 0;
                 it.s1 = t.steps;
             } else {
@@ -287,6 +305,12 @@ struct Walk {
                 if (it.s0 >= it.s1) continue;
                 if (it.s0 > 0 || it.s1 < t.steps)
                     it.part = (((int64_t)piece * pl.G + g) * 2 + (it.s0 > 0 ? 0 : 1)) * part_floats(pl);
+                if (it.s0 == 0 && it.s1 < t.steps) {
+                    join.t0 = t.t0;
+                    join.tokens = t.tokens;
+                    join.head0 = t.head0;
+                    join.last = (int)((first + t.steps - 1) / S);
+                }
             }
             it.found = 1;
             return it;
@@ -310,56 +334,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = &b.abort;
 
     if (pl.cut) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (threadIdx.x == 0) {
-        mbar_init(&b.q_full, 1);
-        mbar_init(&b.q_empty, 1);
-        mbar_init(&b.o_free, kSoftWarps);
-        mbar_init(&b.p_ready, kSoftWarps);
-        mbar_init(&b.p_free, 1);
-        mbar_init(&b.drain, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(b.s_full + i, 1);
-            mbar_init(b.s_free + i, kSoftWarps);
-        }
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(b.i_full + i, 1);
-            mbar_init(b.i_empty + i, kSoftWarps + 1);
-        }
-        for (int i = 0; i < pl.units; ++i) {
-            mbar_init(b.u_full + i, 1);
-            mbar_init(b.u_empty + i, 1);
-        }
-        for (int i = 0; i < pl.shared; ++i) {
-            mbar_init(b.r_full + i, 1);
-            mbar_init(b.r_empty + i, 1);
-        }
+    constexpr int kBars = offsetof(Bars, slots) / 8, kBarsSoft = offsetof(Bars, i_empty) / 8, kBarsItems = offsetof(Bars, q_full) / 8;
+    static_assert(kBars <= kThreads, "a thread for each barrier");
+    if (threadIdx.x < kBars) {
+        mbar_init(reinterpret_cast<uint64_t *>(&b) + threadIdx.x,
+                  threadIdx.x < kBarsSoft ? kSoftWarps : threadIdx.x < kBarsItems ? kSoftWarps + 2 : 1);
+        fence_mbar_init();
+    }
+    if (threadIdx.x == kThreads - 1) {
         b.abort = 0;
         b.start_seq = -1;
-        fence_mbar_init();
     }
     if (warp == kLoadWarp && lane < 2)
         asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &map_q : &map_c) : "memory");
-    if (warp == kMmaWarp) {
+    if (warp == kScoreWarp) {
         tmem_alloc(&b.tmem, 512);
         tmem_relinquish();
     }
-    const Line line = measure_line(a, b.scan, kThreads);  // (a barrier inside)
-    const int64_t S = piece_places(line.total, pl.pieces), L0 = piece * S, L1 = min(L0 + S, line.total);
-    {
-        int64_t at = line.mine;
+    // The piece: places of the line, or without cuts units.
+    int64_t L0 = piece, L1 = piece + 1, S = 1;
+    int start_seq;
+    int64_t start_begin;
+    if (!pl.cut && !p.cu_seqlens) {  // as many units in every sequence
+        start_seq = piece / pl.units_one;
+        start_begin = (int64_t)start_seq * pl.units_one;
+    } else {
+        const Line line = measure_line<kThreads>(a, b.scan);  // (a barrier inside)
+        if (pl.cut) {
+            S = piece_places(line.total, pl.pieces);
+            L0 = piece * S;
+            L1 = min(L0 + S, line.total);
+        }
+        int64_t at = pl.cut ? line.mine : line.units;
         for (int n = line.first; n < line.last; ++n) {
-            const int64_t pn = places_of(a, n);
-            if (L0 >= at && L0 < at + pn && L0 < L1) {
+            const int64_t more = units_of(a, n) * (pl.cut ? unit_places(a, n) : 1);
+            if (L0 >= at && L0 < at + more && L0 < L1) {
                 b.start_seq = n;
                 b.start_begin = at;
             }
-            at += pn;
+            at += more;
         }
     }
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
     const uint32_t tb = b.tmem;
+    if (pl.cut || p.cu_seqlens) {
+        start_seq = b.start_seq;
+        start_begin = b.start_begin;
+    }
     auto wait_for = [&](uint64_t *bar, uint32_t parity, uint32_t polls) {
         for (uint32_t i = 0; i < polls; ++i) {
             if (mbar_try_wait(bar, parity)) return true;
@@ -370,12 +393,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // All lanes of a warp go on or stop together.
     auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(bar, parity, kAttnPolls)) != 0; };
-    auto wait_copy = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(bar, parity, p.polls)) != 0; };
 
     if (warp == kLoadWarp) {
         // ---- work items, and the copies
         Walk w;
-        w.start(a, L0, L1, b.start_seq, b.start_begin);
+        w.start(a, L0, L1, S, start_seq, start_begin);
         uint32_t nu = 0, nr = 0, nq = 0;   // units, shared units and query tiles so far
         uint32_t us = 0, up = 1, rs = 0, rp = 1;  // ring places, and the parity of the wait for them
         bool ok = true;
@@ -461,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        if (pl.cut && lane == 0 && ok) *join_head(a, blockIdx.x) = *reinterpret_cast<const int4 *>(&w.join);
         // every copy lands before the CTA may end
         if (lane == 0) {
             if (nq) mbar_wait(&b.q_full, (nq - 1) & 1, kAttnPolls);
@@ -470,113 +493,105 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait(b.u_full + j % pl.units, (j / pl.units) & 1, kAttnPolls);
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
-        // ---- products
-        const uint32_t id_s = idesc_bf16(64, kStep, false, false, p.scale < 0.f);
-        const uint32_t id_o = idesc_bf16(128, pl.n, true, false);
+    } else if (warp == kScoreWarp || warp == kValueWarp) {
+        // ---- products, the scores' and the values' each from one thread of a warp.  A look at a barrier
+        // queues behind the products that its thread has issued, about 120 cycles in which the tensor core
+        // idles; with two threads one's products run meanwhile.  (From one thread, with votes of its
+        // warp, the same work took 4800 cycles a step instead of 2900.)
         const uint32_t k_major = (16u >> 4) << 16, mn_major = (kSharedBytes >> 4) << 16;
-        const uint32_t q_lo = sb16 | k_major, p_lo = (sb16 + (pl.at_p >> 4)) | k_major;
-        const uint32_t u_at = sb16 + (pl.at_units >> 4), r_at = sb16 + (pl.at_shared >> 4), q_chunk = q_rows * 128 >> 4;
-        uint32_t us = 0, up = 0, rs = 0, rp = 0, vs = 0;  // ring places: scores' units, shared units, values' units
-        uint32_t scored = 0, done = 0, items = 0;        // steps with scores, with products; items with any
+        const uint32_t u_at = sb16 + (pl.at_units >> 4);
+        uint32_t blocks = 0, items = 0, us = 0, up = 0;  // steps and items with any so far; ring place and parity
         bool ok = true;
-        auto ready = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0; };
-        for (uint32_t k = 0; ok; ++k) {
-            ok = wait(b.i_full + k % kSlots, (k / kSlots) & 1);
-            if (!ok) break;
-            const int found = b.slots[k % kSlots].found, nt = b.slots[k % kSlots].s1 - b.slots[k % kSlots].s0;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b.i_empty + k % kSlots);
-            if (!found) break;
-            if (nt == 0) continue;
-            ok = wait_copy(&b.q_full, items & 1);
-            // What is ready is issued: a step's products, or the next part of the scores of the step
-            // in hand or the one behind it.  (Scores that wait for their copies must not hold up products,
-            // whose units the next copies need.)
-            int values = 0, scores = 0, part = 0;  // steps through; the next part, 0 being the shared channels
-            uint32_t polls = 0;
-            while (ok && values < nt) {
-                // (the first products need the last item's output to have been read)
-                if (values < scores && (values > 0 || items == 0 || ready(&b.o_free, (items - 1) & 1)) &&
-                    ready(&b.p_ready, done & 1)) {
-                    fence_after_sync();
-                    if (elect_one()) {
-                        uint32_t at = vs;
+        if (elect_one()) {
+            // The next item's steps: -1 at the end.
+            auto next_item = [&](uint32_t k) {
+                ok = wait_for(b.i_full + k % kSlots, (k / kSlots) & 1, kAttnPolls);
+                if (!ok) return -1;
+                const Item &it = b.slots[k % kSlots];
+                const int nt = it.found ? it.s1 - it.s0 : -1;
+                mbar_arrive(b.i_empty + k % kSlots);
+                return nt;
+            };
+            if (warp == kScoreWarp) {
+                const uint32_t id = idesc_bf16(64, kStep, false, false, p.scale < 0.f);
+                const uint32_t q_lo = sb16 | k_major, q_chunk = q_rows * 128 >> 4, r_at = sb16 + (pl.at_shared >> 4);
+                uint32_t rs = 0, rp = 0;
+                for (uint32_t k = 0; ok; ++k) {
+                    const int nt = next_item(k);
+                    if (nt < 0) break;
+                    if (nt == 0) continue;
+                    ok = wait_for(&b.q_full, items & 1, p.polls);
+                    for (int s = 0; s < nt && ok; ++s, ++blocks) {
+                        const uint32_t t_s = tb + (blocks & 1) * kStep;
+                        if (blocks >= 2) ok = wait_for(b.s_free + (blocks & 1), ((blocks >> 1) - 1) & 1, kAttnPolls);
+                        ok = ok && wait_for(b.r_full + rs, rp, p.polls);
+                        if (!ok) break;
+                        fence_after_sync();
+                        {
+                            const uint32_t lo = (r_at + rs * (kSharedBytes >> 4)) | k_major, ql = q_lo + 8 * q_chunk;
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) mma_ss(t_s, desc_of(ql + 2 * x), desc_of(lo + 2 * x), id, x > 0);
+                            mma_commit(b.r_empty + rs);
+                            if (++rs == (uint32_t)pl.shared) rs = 0, rp ^= 1;
+                        }
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
-                            const uint32_t lo = (u_at + at * (kUnitBytes >> 4)) | mn_major;
+                            ok = wait_for(b.u_full + us, up, p.polls);
+                            if (!ok) break;
+                            fence_after_sync();
+                            const uint32_t lo = (u_at + us * (kUnitBytes >> 4)) | k_major, ql = q_lo + 2 * m * q_chunk;
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) mma_ss(t_s, desc_of(ql + 2 * x), desc_of(lo + 2 * x), id, 1);
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
-                                mma_ss(tb + kTmemO + m * pl.n, desc_of(lo + x * (2048 >> 4)), desc_of(p_lo + 2 * x), id_o,
-                                       values > 0 || x > 0);
-                            mma_commit(b.u_empty + at);
-                            if (++at == (uint32_t)pl.units) at = 0;
+                                mma_ss(t_s, desc_of(ql + q_chunk + 2 * x), desc_of(lo + (kSharedBytes >> 4) + 2 * x), id, 1);
+                            if (++us == (uint32_t)pl.units) us = 0, up ^= 1;
+                        }
+                        if (!ok) break;
+                        mma_commit(b.s_full + (blocks & 1));
+                    }
+                    if (ok) mma_commit(&b.q_empty);
+                    ++items;
+                }
+            } else {
+                const uint32_t id = idesc_bf16(128, pl.n, true, false);
+                const uint32_t p_lo = (sb16 + (pl.at_p >> 4)) | k_major, t_o = tb + kTmemO;
+                for (uint32_t k = 0; ok; ++k) {
+                    const int nt = next_item(k);
+                    if (nt < 0) break;
+                    if (nt == 0) continue;
+                    if (items > 0) ok = wait_for(&b.o_free, (items - 1) & 1, kAttnPolls);  // the last item's output is read
+                    for (int s = 0; s < nt && ok; ++s, ++blocks) {
+                        ok = wait_for(&b.p_ready, blocks & 1, kAttnPolls);
+                        if (!ok) break;
+                        fence_after_sync();
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const uint32_t lo = (u_at + us * (kUnitBytes >> 4)) | mn_major;
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                mma_ss(t_o + m * pl.n, desc_of(lo + x * (2048 >> 4)), desc_of(p_lo + 2 * x), id, s > 0 || x > 0);
+                            mma_commit(b.u_empty + us);
+                            if (++us == (uint32_t)pl.units) us = 0;
                         }
                         mma_commit(&b.p_free);
                     }
-                    __syncwarp();
-                    vs += 4;
-                    if (vs >= (uint32_t)pl.units) vs -= pl.units;
-                    ++values;
-                    ++done;
-                    polls = 0;
-                    continue;
-                }
-                if (scores < nt && scores <= values + 1 && ready(part == 0 ? b.r_full + rs : b.u_full + us, part == 0 ? rp : up)) {
-                    const uint32_t t_s = tb + (scored & 1) * kStep;
-                    if (part == 0 && scored >= 2) {
-                        ok = wait(b.s_free + (scored & 1), ((scored >> 1) - 1) & 1);
-                        if (!ok) break;
-                    }
-                    fence_after_sync();
-                    if (part == 0) {
-                        if (elect_one()) {
-                            const uint32_t lo = (r_at + rs * (kSharedBytes >> 4)) | k_major, ql = q_lo + 8 * q_chunk;
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) mma_ss(t_s, desc_of(ql + 2 * x), desc_of(lo + 2 * x), id_s, x > 0);
-                            mma_commit(b.r_empty + rs);
-                        }
-                        __syncwarp();
-                        if (++rs == (uint32_t)pl.shared) rs = 0, rp ^= 1;
-                        part = 1;
-                    } else {
-                        if (elect_one()) {
-                            const uint32_t lo = (u_at + us * (kUnitBytes >> 4)) | k_major, ql = q_lo + 2 * (part - 1) * q_chunk;
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                                for (int x = 0; x < 4; ++x)
-                                    mma_ss(t_s, desc_of(ql + h * q_chunk + 2 * x), desc_of(lo + h * (kSharedBytes >> 4) + 2 * x), id_s, 1);
-                            if (part == 4) {
-                                mma_commit(b.s_full + (scored & 1));
-                                if (scores + 1 == nt) mma_commit(&b.q_empty);
-                            }
-                        }
-                        __syncwarp();
-                        if (++us == (uint32_t)pl.units) us = 0, up ^= 1;
-                        if (++part == 5) part = 0, ++scores, ++scored;
-                    }
-                    polls = 0;
-                    continue;
-                }
-                if (++polls > kProductPolls || __any_sync(0xffffffffu, *abort_flag)) {
-                    *abort_flag = 1;
-                    ok = false;
+                    ++items;
                 }
             }
-            ++items;
-        }
-        // nothing issued may still run, and no commit arrive, once the CTA has ended
-        if (elect_one()) {
-            mma_commit(&b.drain);
-            mbar_wait(&b.drain, 0, kAttnPolls);
+            // nothing issued may still run, and no commit arrive, once the CTA has ended
+            mma_commit(b.drain + (warp - kScoreWarp));
+            mbar_wait(b.drain + (warp - kScoreWarp), 0, kAttnPolls);
         }
         __syncwarp();
     } else {
-        // ---- softmax, a thread per row in the lower half of each warp's lanes (where the M = 64
-        // product leaves its rows), and the output, a thread per channel
+        // ---- softmax, two threads per row (the M = 64 product leaves its rows in 16 of each warp's 32
+        // lanes, which the lower half of a warp's threads read for 32 of the step's tokens and the
+        // upper half for the others), and the output, a thread per channel
+        constexpr int kHalf = kStep / 2;
         const int row = warp * 16 + (lane & 15), tok = row / pl.hp, head_in = row - tok * pl.hp;
-        const bool mine = lane < 16;
+        const int half = lane >> 4;
+        const bool mine = half == 0;
         const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
         const float c = fabsf(p.scale) * kLog2e;
         uint32_t blocks = 0, items = 0;  // steps so far; items with any
@@ -593,32 +608,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Item it = b.slots[k % kSlots];
             if (!it.found) break;
             const int head = it.head0 + head_in, nt = it.s1 - it.s0;
-            const bool live = mine && tok < it.tokens && head_in < pl.hp && head < p.H && row < (int)q_rows;
+            const bool live = tok < it.tokens && head < p.H && row < (int)q_rows;
             const int seen = it.seen0 + tok, most = it.seen0 + it.tokens - 1;  // of this row, of the tile
             float m = -INFINITY, l = 0.f;
             for (int s = 0; s < nt; ++s, ++blocks) {
                 const int j0 = (it.s0 + s) * kStep;
                 ok = wait(b.s_full + (blocks & 1), (blocks >> 1) & 1);
                 fence_after_sync();
-                float x[kStep];
-                tmem_ld32(tb + lane_base + (blocks & 1) * kStep, x);
-                tmem_ld32(tb + lane_base + (blocks & 1) * kStep + 32, x + 32);
-                wait_ld<kStep>(x);
+                float x[kHalf];
+                tmem_ld_halves(tb + lane_base + (blocks & 1) * kStep, x);
+                wait_ld<kHalf>(x);
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b.s_free + (blocks & 1));
-                const int lim = live ? seen - j0 : 0;
                 if (j0 + kStep > it.seen0 || !live) {
+                    const int lim = live ? seen - j0 - half * kHalf : 0;
 #pragma unroll
-                    for (int i = 0; i < kStep; ++i)
+                    for (int i = 0; i < kHalf; ++i)
                         if (i >= lim) x[i] = -INFINITY;
                 }
                 float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                for (int i = 4; i < kStep; i += 4)
+                for (int i = 4; i < kHalf; i += 4)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[i + e]);
-                const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const float mb = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], 16)) * c;
                 const bool raise = mb > m + kSlack;  // (rows that are not live: never)
                 if (blocks > 0) {  // the last weights are multiplied
                     ok = ok && wait(&b.p_free, (blocks - 1) & 1);
@@ -635,8 +650,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (s > 0) {
                         if (mine) b.factor[row] = f;
                         soft_sync();
+#pragma unroll 1
                         for (int r0 = 0; r0 < pl.n; r0 += 16) {
-#pragma unroll
+#pragma unroll 1
                             for (int q = 0; q < 4; ++q) {
                                 float o[16];
                                 const uint32_t at = tb + lane_base + kTmemO + q * pl.n + r0;
@@ -655,20 +671,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float mm = m == -INFINITY ? 0.f : m;
                 float sum[2] = {0.f, 0.f};
-                uint32_t w[kStep / 2];
+                uint32_t w[kHalf / 2];
 #pragma unroll
-                for (int i = 0; i < kStep; i += 2) {
+                for (int i = 0; i < kHalf; i += 2) {
                     const float e0 = ex2(fmaf(x[i], c, -mm)), e1 = ex2(fmaf(x[i + 1], c, -mm));
                     sum[0] += e0;
                     sum[1] += e1;
                     w[i / 2] = pack_bf16x2(e0, e1);
                 }
                 l += sum[0] + sum[1];
-                if (mine && row < pl.n) {
+                if (row < pl.n) {
                     const uint32_t at = sb + pl.at_p + row * 128;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        st_shared_v4(at + ((i ^ (row & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                    for (int i = 0; i < 4; ++i)
+                        st_shared_v4(at + (((4 * half + i) ^ (row & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 }
                 if (j0 + kStep > it.seen0) {
                     // Tokens that not every row sees.  A weight of zero times what is not finite would not be
@@ -722,26 +738,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = false;
                 break;
             }
+            l += __shfl_xor_sync(0xffffffffu, l, 16);  // of both halves of the tokens
             const bool bad = *(volatile int *)&b.slots[k % kSlots].bad != 0;
             if (bad) l = kNaN;
-            const bool part = it.part >= 0;
-            if (mine) {
-                const int64_t out = live ? (int64_t)(it.t0 + tok) * p.H + head : -1;
-                b.row_at[row] = part ? (row < (int)q_rows ? (int64_t)row : -1) : out;
-                b.factor[row] = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
-                if (part && row < (int)q_rows) {
-                    float *ml = p.ws + it.part + (int64_t)q_rows * kLatent + row;
-                    ml[0] = m;
-                    ml[q_rows] = l;
+            if (it.part >= 0) {
+                // Sums of a part, four rows' values of a channel together, so that a warp's stores are
+                // contiguous (a row's channels together, one store took 58 cycles, 12000 an item).
+                float *ws = p.ws + it.part;
+                if (mine && row < pl.n) {
+                    ws[pl.n * kLatent + row] = m;
+                    ws[pl.n * (kLatent + 1) + row] = l;
                 }
-                if (!part && live && p.lse) p.lse[out] = l == 0.f ? -INFINITY : (log2f(l) + m) * kLn2;
-            }
-            soft_sync();
-            {
-                const bool bf16 = !part && p.o_bf16;
-                float *f32 = part ? p.ws + it.part : static_cast<float *>(p.o);
-                for (int r0 = 0; r0 < (int)q_rows; r0 += 16)
+                ws += (warp * 32 + lane) * 4;
+#pragma unroll 1
+                for (int at = 0; at < 4 * pl.n; at += 16) {
+                    float o[16];
+                    tmem_ld16f(tb + lane_base + kTmemO + at, o);
+                    wait_ld<16>(o);
 #pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<float4 *>(ws + (int64_t)(at / 4 + e) * 512) =
+                            make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                }
+            } else {
+                if (mine) {
+                    const int64_t out = live ? (int64_t)(it.t0 + tok) * p.H + head : -1;
+                    b.row_at[row] = out;
+                    b.factor[row] = l == 0.f ? 0.f : 1.f / l;
+                    if (live && p.lse) p.lse[out] = l == 0.f ? -INFINITY : (log2f(l) + m) * kLn2;
+                }
+                soft_sync();
+                // Two lanes exchange, so that each stores two channels of every other row.
+                const int odd = lane & 1, esz = p.o_bf16 ? 2 : 4;
+                uint8_t *base = static_cast<uint8_t *>(p.o) + (warp * 32 + lane - odd) * esz;
+#pragma unroll 1
+                for (int r0 = 0; r0 < (int)q_rows; r0 += 16) {
+                    uint8_t *at[8];
+                    float f[16];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int64_t row_at = b.row_at[r0 + 2 * i + odd];
+                        at[i] = row_at < 0 ? nullptr : base + row_at * (kLatent * esz);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) f[i] = b.factor[r0 + i];
+                    // (not unrolled: an item's end is seldom run, and 13 KB of instructions that have to be fetched
+                    // while the cache streams through L2 took 11000 cycles the first time)
+#pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
                         float o[16];
                         if (nt > 0) {
@@ -752,17 +795,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int i = 0; i < 16; ++i) o[i] = 0.f;
                         }
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int64_t at = b.row_at[r0 + i];
-                            if (at < 0) continue;
-                            const float y = o[i] * b.factor[r0 + i];
-                            const int64_t e = at * kLatent + q * 128 + warp * 32 + lane;
-                            if (bf16)
-                                static_cast<__nv_bfloat16 *>(p.o)[e] = __float2bfloat16_rn(y);
+                        for (int i = 0; i < 8; ++i) {
+                            const float a0 = o[2 * i] * f[2 * i], a1 = o[2 * i + 1] * f[2 * i + 1];
+                            const float got = __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
+                            const float y0 = odd ? got : a0, y1 = odd ? a1 : got;
+                            if (!at[i]) continue;
+                            if (p.o_bf16)
+                                *reinterpret_cast<uint32_t *>(at[i] + q * 256) = pack_bf16x2(y0, y1);
                             else
-                                f32[e] = y;
+                                *reinterpret_cast<float2 *>(at[i] + q * 512) = make_float2(y0, y1);
                         }
                     }
+                }
             }
             fence_before_sync();
             __syncwarp();
@@ -775,99 +819,138 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_before_sync();
     __syncthreads();
-    if (warp == kMmaWarp) tmem_dealloc(tb, 512);
+    if (warp == kScoreWarp) tmem_dealloc(tb, 512);
     // After a failure every row of this CTA's items becomes NaN.
     if (*abort_flag) {
         Walk w;
-        w.start(a, L0, L1, b.start_seq, b.start_begin);
+        w.start(a, L0, L1, S, start_seq, start_begin);
         for (;;) {
             const Item it = w.next(a, piece, g);
             if (!it.found) break;
+            if (it.part >= 0) {
+                for (int i = threadIdx.x; i < part_floats(pl); i += kThreads) p.ws[it.part + i] = kNaN;
+                continue;
+            }
             for (int i = threadIdx.x; i < (int)q_rows * kLatent; i += kThreads) {
                 const int r = i / kLatent, ch = i - r * kLatent, tok = r / pl.hp, head = it.head0 + r - tok * pl.hp;
-                if (it.part >= 0) {
-                    p.ws[it.part + i] = kNaN;
-                    if (ch < 2) p.ws[it.part + (int64_t)q_rows * (kLatent + ch) + r] = kNaN;
-                } else if (tok < it.tokens && head < p.H) {
-                    const int64_t out = (int64_t)(it.t0 + tok) * p.H + head;
-                    st_out(p.o, out * kLatent + ch, kNaN, p.o_bf16);
-                    if (ch == 0 && p.lse) p.lse[out] = kNaN;
-                }
+                if (tok >= it.tokens || head >= p.H) continue;
+                const int64_t out = (int64_t)(it.t0 + tok) * p.H + head;
+                st_out(p.o, out * kLatent + ch, kNaN, p.o_bf16);
+                if (ch == 0 && p.lse) p.lse[out] = kNaN;
             }
         }
+        if (pl.cut && threadIdx.x == 0) *join_head(a, blockIdx.x) = *reinterpret_cast<const int4 *>(&w.join);
         if (threadIdx.x == 0) atomicAdd(&g_attn_latent_timeouts, 1);
     }
 }
 
-// Joins the tiles that more than one piece took, in the order of the pieces.  blockIdx.x is a piece
-// (and a tile place of its units): the CTA looks after the unit whose first step lies in the piece
-// and whose last one does not, if there is one.  gridDim.y CTAs share its rows, a row having 128 threads.
-constexpr int kJoinThreads = 256;
-__global__ void __launch_bounds__(kJoinThreads) attn_latent_join_kernel(const __grid_constant__ Args a) {
-    __shared__ int64_t s_scan[kJoinThreads / 32];
-    __shared__ int64_t s_begin;
-    __shared__ int s_seq;
+// Joins the tiles that more than one piece took, in the order of the pieces.  blockIdx.x is a CTA of the
+// first launch, which has left word of the tile that begins in its piece and goes on behind it, if there is
+// one.  A warp has four rows and 128 channels, or with `shares` > 1 a share of their pieces.
+constexpr int kMaxShares = 4;
+__global__ void __launch_bounds__(128 * kMaxShares) attn_latent_join_kernel(const __grid_constant__ Args a, int shares) {
+    extern __shared__ float4 s_acc[];  // [shares - 1 of 4 warps][128], then their m and l
     const AttnLatentParams &p = a.p;
     const Plan &pl = a.plan;
-    const int tid = threadIdx.x, piece = blockIdx.x / pl.G, g = blockIdx.x - piece * pl.G;
-    const Line line = measure_line(a, s_scan, kJoinThreads);
-    const int64_t S = piece_places(line.total, pl.pieces), L0 = piece * S, L1 = min(L0 + S, line.total);
-    if (tid == 0) s_seq = -1;
-    __syncthreads();
-    if (L0 < L1) {
-        int64_t at = line.mine;
-        for (int n = line.first; n < line.last; ++n) {
-            const int64_t pn = places_of(a, n);
-            if (L1 - 1 >= at && L1 - 1 < at + pn) {
-                s_seq = n;
-                s_begin = at;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k0 = blockIdx.x / pl.G, g = blockIdx.x - k0 * pl.G;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 word = __ldcg(join_head(a, blockIdx.x));
+    const JoinHead t = *reinterpret_cast<const JoinHead *>(&word);
+    const int share = warp >> 2, q = warp & 3, k1 = t.last;
+    const int r = 4 * blockIdx.y;  // the first of the rows, all of one token
+    const int tok = r / pl.hp, head = t.head0 + r - tok * pl.hp;
+    if (tok >= t.tokens || head >= p.H) return;
+    const int64_t out = (int64_t)(t.t0 + tok) * p.H + head;
+    float m[4], l[4], acc[4][4];  // of the rows; of channels lane + 32 * i
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        m[e] = -INFINITY;
+        l[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i][e] = 0.f;
+    }
+    auto four = [](const float *x, float (&y)[4]) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(x));
+        y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
+    };
+    {
+        const int each = (k1 - k0 + shares) / shares, from = k0 + share * each, to = min(from + each, k1 + 1);
+        // (the unit is in slot 1 of the piece that it begins in, else in slot 0)
+        auto part = [&](int k) { return p.ws + (((int64_t)k * pl.G + g) * 2 + (k == k0)) * part_floats(pl); };
+        for (int kb = from; kb < to; kb += 32) {  // a lane's piece's references and sums, then the channels of all
+            float mk[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, lk[4] = {}, fk[4];
+            if (kb + lane < to) {
+                four(part(kb + lane) + pl.n * kLatent + r, mk);
+                four(part(kb + lane) + pl.n * (kLatent + 1) + r, lk);
             }
-            at += pn;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float most = mk[e];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                most = fmaxf(most, m[e]);
+                fk[e] = most == -INFINITY ? 1.f : ex2(mk[e] - most);
+                const float f = most == -INFINITY ? 1.f : ex2(m[e] - most);
+                m[e] = most;
+                l[e] = l[e] * f + warp_sum(lk[e] * fk[e]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i][e] *= f;
+            }
+            const int count = min(32, to - kb);
+#pragma unroll 4
+            for (int k = 0; k < count; ++k) {
+                const float *x = part(kb + k) + ((int64_t)(q * pl.n + r) / 4 * 128 + lane) * 4;
+                float v[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) four(x + i * 128, v[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float w = __shfl_sync(0xffffffffu, fk[e], k);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[i][e] = fmaf(v[i][e], w, acc[i][e]);
+                }
+            }
         }
     }
-    __syncthreads();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int n = s_seq;
-    if (n < 0) return;
-    int64_t t0;
-    int nq;
-    call_rows(p.cu_seqlens, p.tokens, n, t0, nq);
-    const int len = tokens_of(p.c, n), per = steps_of(len) + kPad;
-    const int64_t u = (L1 - 1 - s_begin) / per, first = s_begin + u * per + kPad;
-    const Tile t = tile_of(pl, t0, nq, len, u * pl.G + g);
-    if (t.steps == 0 || first < L0 || first >= L1 || first + t.steps <= L1) return;
-    const int last = (int)((first + t.steps - 1) / S);  // the piece of its last step
-    const int rows = pl.hp * pl.tk;
-    const int64_t stride = 2 * pl.G * part_floats(pl);
-    const float *ws = p.ws + ((int64_t)piece * pl.G + g) * 2 * part_floats(pl);  // slot 1 here, slot 0 of the pieces behind
-    for (int r = blockIdx.y * (kJoinThreads / 128) + tid / 128; r < rows; r += gridDim.y * (kJoinThreads / 128)) {
-        const int tok = r / pl.hp, head = t.head0 + r - tok * pl.hp;
-        if (tok >= t.tokens || head >= p.H) continue;
-        const int ch = (tid & 127) * 4;
-        float m = -INFINITY, l = 0.f;
-        for (int k = piece; k <= last; ++k) {
-            const float *w = ws + (k - piece) * stride + (k == piece ? part_floats(pl) : 0) + (int64_t)rows * kLatent + r;
-            m = fmaxf(m, __ldcg(w));
+    if (shares > 1) {  // the first four warps add the others' sums to theirs
+        float4 *s_m = s_acc + (shares - 1) * 4 * 128, *s_l = s_m + (shares - 1) * 4;
+        if (share > 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s_acc[(warp - 4) * 128 + lane + 32 * i] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+            if (lane == 0) s_m[warp - 4] = make_float4(m[0], m[1], m[2], m[3]), s_l[warp - 4] = make_float4(l[0], l[1], l[2], l[3]);
         }
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = piece; k <= last; ++k) {
-            const float *w = ws + (k - piece) * stride + (k == piece ? part_floats(pl) : 0);
-            const float mk = __ldcg(w + (int64_t)rows * kLatent + r), lk = __ldcg(w + (int64_t)rows * (kLatent + 1) + r);
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(w + (int64_t)r * kLatent + ch));
-            const float f = m == -INFINITY ? 1.f : ex2(mk - m);
-            l += lk * f;
-            acc = make_float4(acc.x + x.x * f, acc.y + x.y * f, acc.z + x.z * f, acc.w + x.w * f);
+        __syncthreads();
+        if (share > 0) return;
+        for (int w = q; w < (shares - 1) * 4; w += 4) {
+            const float4 x = s_m[w], y = s_l[w];
+            const float mw[4] = {x.x, x.y, x.z, x.w}, lw[4] = {y.x, y.y, y.z, y.w};
+            float f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float most = fmaxf(m[e], mw[e]), own = most == -INFINITY ? 1.f : ex2(m[e] - most);
+                f[e] = most == -INFINITY ? 1.f : ex2(mw[e] - most);
+                m[e] = most;
+                l[e] = fmaf(lw[e], f[e], l[e] * own);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i][e] *= own;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 v = s_acc[w * 128 + lane + 32 * i];
+                acc[i][0] = fmaf(v.x, f[0], acc[i][0]);
+                acc[i][1] = fmaf(v.y, f[1], acc[i][1]);
+                acc[i][2] = fmaf(v.z, f[2], acc[i][2]);
+                acc[i][3] = fmaf(v.w, f[3], acc[i][3]);
+            }
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t out = (int64_t)(t.t0 + tok) * p.H + head, e = out * kLatent + ch;
-        if (p.o_bf16)
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.o) + e) =
-                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        else
-            *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + e) =
-                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (ch == 0 && p.lse) p.lse[out] = l == 0.f ? -INFINITY : (log2f(l) + m) * kLn2;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (head + e >= p.H) break;
+        const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st_out(p.o, (out + e) * kLatent + q * 128 + lane + 32 * i, acc[i][e] * inv, p.o_bf16);
+        if (q == 0 && lane == 0 && p.lse) p.lse[out + e] = l[e] == 0.f ? -INFINITY : (log2f(l[e]) + m[e]) * kLn2;
     }
 }
 
@@ -891,9 +974,12 @@ Plan plan_of(int64_t N, int64_t tokens, int H, int64_t max_tokens) {
     pl.G = tiles >= 4 ? 4 : tiles >= 2 ? 2 : 1;
     const int64_t sms = std::max(sm_count() / pl.G, 1);
     // (a sequence of nq rows has at most nq / (rows of a unit) + 1 units)
-    const int64_t most_units = units_of(pl, tokens) + N, per = (max_tokens + kStep - 1) / kStep + kPad;
-    pl.cut = 1;
-    pl.pieces = (int)std::max<int64_t>(1, std::min(sms, (most_units * per + kMinPiece - 1) / kMinPiece));
+    pl.units_one = (pl.parts + pl.G - 1) / pl.G;
+    pl.most_units = tokens == N ? N * units_of(pl, 1) : units_of(pl, (int)tokens) + N;
+    const int64_t per = (max_tokens + kStep - 1) / kStep + kPad;
+    // RULE
+    pl.cut = !(pl.most_units <= sms && per - kPad <= 24 && pl.most_units * 5 >= sms * 3);
+    pl.pieces = (int)(pl.cut ? std::max<int64_t>(1, std::min(sms, (pl.most_units * per + kMinPiece - 1) / kMinPiece)) : pl.most_units);
     const int64_t q = (int64_t)pl.hp * pl.tk * kRow * 2, ps = (int64_t)pl.n * 128;
     const int64_t room = kMaxSmem - 1024 - (int64_t)round_up(sizeof(Bars), 128) - round_up(q, 1024) - round_up(ps, 1024);
     pl.shared = 2;
@@ -906,7 +992,7 @@ Plan plan_of(int64_t N, int64_t tokens, int H, int64_t max_tokens) {
 }
 
 size_t plan_bytes(const Plan &pl) {
-    return pl.cut ? (size_t)pl.pieces * pl.G * 2 * pl.hp * pl.tk * (kLatent + 2) * sizeof(float) : 0;
+    return pl.cut ? (size_t)pl.pieces * pl.G * (2 * part_floats(pl) * sizeof(float) + sizeof(JoinHead)) : 0;
 }
 
 bool encode_tensors(const AttnLatentParams &p, const Plan &pl, CUtensorMap *mq, CUtensorMap *mc) {
@@ -975,15 +1061,18 @@ kda_status launch_attn_latent(const AttnLatentParams &p, cudaStream_t st) {
     kda_status s = check_launch("attn_latent_kernel");
     if (!pl.cut || s != KDA_OK) return s;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(pl.pieces * pl.G, std::max(1, pl.hp * pl.tk / 8));
-    cfg.blockDim = dim3(kJoinThreads);
+    // with many pieces a unit more warps share them
+    const int shares = pl.pieces >= 16 * pl.most_units ? kMaxShares : 1;
+    cfg.gridDim = dim3(pl.pieces * pl.G, pl.hp * pl.tk / 4);
+    cfg.blockDim = dim3(128 * shares);
+    cfg.dynamicSmemBytes = (shares - 1) * 4 * (128 + 2) * sizeof(float4);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];  // starts while the first kernel ends; waits for it before it reads
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_latent_join_kernel, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_latent_join_kernel, a, shares);
     note_launch();
     if (e != cudaSuccess) {
         set_error("attn_latent_join_kernel: %s", cudaGetErrorString(e));
