@@ -42,8 +42,8 @@ constexpr int kTileRows = 64;           // query rows of a tile at most
 constexpr int kSoftWarps = 4, kScoreWarp = 4, kValueWarp = 5, kLoadWarp = 6;
 constexpr int kThreads = 224;
 constexpr int kSlots = 4;               // work items under way
-constexpr int kPad = 4;                 // a unit's own cost in steps
-constexpr int kMinPiece = 2;            // places of a CTA at least
+constexpr int kPad = 2;                 // a unit's own cost in steps, where pieces have kPadFrom steps or more
+constexpr int kPadFrom = 4;
 constexpr int kMaxUnits = 12, kMaxShared = 4;  // ring places at most
 constexpr uint32_t kUnitBytes = kStep * 256, kSharedBytes = kStep * 128;
 constexpr uint32_t kTmemO = 2 * kStep;  // TMEM columns: scores of two steps, then O^T
@@ -136,6 +136,17 @@ __device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float *r) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(u[i]);
 }
+// Stores without a branch.
+__device__ __forceinline__ void store_if(bool x, void *p, __nv_bfloat16 v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.b16 [%0], %1;\n\t}" ::"l"(p),
+                 "h"(__bfloat16_as_ushort(v)), "r"((uint32_t)x)
+                 : "memory");
+}
+__device__ __forceinline__ void store_if(bool x, void *p, float v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.f32 [%0], %1;\n\t}" ::"l"(p), "f"(v),
+                 "r"((uint32_t)x)
+                 : "memory");
+}
 // A 128-byte-swizzled operand's descriptor from its low word (address / 16 and leading offset);
 // the row groups are 1024 bytes apart.
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
@@ -175,12 +186,14 @@ __device__ __forceinline__ int units_of(const Args &a, int n) {
     call_rows(a.p.cu_seqlens, a.p.tokens, n, t0, nq);
     return units_of(a.plan, nq);
 }
-__device__ __forceinline__ int64_t unit_places(const Args &a, int n) { return steps_of(tokens_of(a.p.c, n)) + kPad; }
+// Places of a unit beside its own cost (one without steps has a place too: its rows are written there).
+__device__ __forceinline__ int line_steps(int len) { return max(1, steps_of(len)); }
+__device__ __forceinline__ int seq_steps(const Args &a, int n) { return line_steps(tokens_of(a.p.c, n)); }
 
-// Every thread's share [first, last) of the sequences measured: the line's length, and the places (and
-// units) of the sequences before the share.
+// Every thread's share [first, last) of the sequences measured: the steps and units of all sequences, and
+// of those before the share.
 struct Line {
-    int64_t total, mine, units;
+    int64_t total, total_units, mine, units;
     int first, last;
 };
 template <int THREADS>
@@ -193,7 +206,7 @@ __device__ __forceinline__ Line measure_line(const Args &a, int64_t (*scan)[2]) 
     for (int n = l.first; n < l.last; ++n) {
         const int64_t u = units_of(a, n);
         own_units += u;
-        own += u * unit_places(a, n);
+        own += u * seq_steps(a, n);
     }
     int64_t x = own, y = own_units;
 #pragma unroll
@@ -205,14 +218,14 @@ __device__ __forceinline__ Line measure_line(const Args &a, int64_t (*scan)[2]) 
     __syncthreads();
     l.mine = x - own;
     l.units = y - own_units;
-    l.total = 0;
+    l.total = l.total_units = 0;
     for (int w = 0; w < THREADS / 32; ++w) {
         if (w < warp) l.mine += scan[w][0], l.units += scan[w][1];
         l.total += scan[w][0];
+        l.total_units += scan[w][1];
     }
     return l;
 }
-__host__ __device__ __forceinline__ int64_t piece_places(int64_t total, int pieces) { return (total + pieces - 1) / pieces; }
 
 // A tile's rows and what they see.
 struct Tile {
@@ -246,6 +259,7 @@ struct Walk {
     int64_t L0, L1, S, begin;  // the piece, the next unit's place on the line (without cuts: units)
     int n, u, units, nq, len;  // the next unit: its sequence, and number there
     int64_t t0;
+    int pad;
     bool open;
     JoinHead join;
     __device__ void look(const Args &a) {  // at sequence n, or the next one with rows
@@ -258,16 +272,17 @@ struct Walk {
         units = units_of(a.plan, nq);
         open = true;
     }
-    __device__ void start(const Args &a, int64_t l0, int64_t l1, int64_t s, int seq, int64_t seq_begin) {
+    __device__ void start(const Args &a, int64_t l0, int64_t l1, int64_t s, int own, int seq, int64_t seq_begin) {
         L0 = l0;
         L1 = l1;
         S = s;
+        pad = own;
         open = false;
         join.t0 = join.tokens = join.head0 = join.last = 0;
         n = seq < 0 ? a.p.c.N : seq;
         if (n >= a.p.c.N) return;
         look(a);
-        const int64_t per = a.plan.cut ? steps_of(len) + kPad : 1;
+        const int64_t per = a.plan.cut ? line_steps(len) + pad : 1;
         u = (int)((l0 - seq_begin) / per);
         begin = seq_begin + u * per;
     }
@@ -279,11 +294,10 @@ struct Walk {
         while (n < a.p.c.N && begin < L1) {
             if (!open) look(a);
             if (n >= a.p.c.N) break;
-            const int steps = steps_of(len);
-            const int64_t first = begin + kPad, at = begin;
+            const int64_t first = begin + pad, at = begin;
             const Tile t = tile_of(pl, t0, nq, len, u * pl.G + g);
             it.seq = n;
-            begin += pl.cut ? steps + kPad : 1;
+            begin += pl.cut ? line_steps(len) + pad : 1;
             if (++u == units) {
                 ++n;
                 u = 0;
@@ -345,6 +359,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         b.abort = 0;
         b.start_seq = -1;
     }
+    if (warp == kLoadWarp && !pl.cut && !p.cu_seqlens) {
+        // the length and the first pages on their way, while the rest is set up
+        const int n = piece / pl.units_one;
+        int x, y = 0;
+        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(x) : "l"(p.c.lens + n));
+        if (lane < p.c.max_blocks) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(y) : "l"(p.c.block_table + (int64_t)n * p.c.max_blocks + lane));
+        asm volatile("" ::"r"(x), "r"(y));
+    }
     if (warp == kLoadWarp && lane < 2)
         asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &map_q : &map_c) : "memory");
     if (warp == kScoreWarp) {
@@ -353,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // The piece: places of the line, or without cuts units.
     int64_t L0 = piece, L1 = piece + 1, S = 1;
+    int pad = 0;
     int start_seq;
     int64_t start_begin;
     if (!pl.cut && !p.cu_seqlens) {  // as many units in every sequence
@@ -361,13 +384,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         const Line line = measure_line<kThreads>(a, b.scan);  // (a barrier inside)
         if (pl.cut) {
-            S = piece_places(line.total, pl.pieces);
+            pad = line.total >= (int64_t)kPadFrom * pl.pieces ? kPad : 0;
+            const int64_t places = line.total + pad * line.total_units;
+            S = (places + pl.pieces - 1) / pl.pieces;
             L0 = piece * S;
-            L1 = min(L0 + S, line.total);
+            L1 = min(L0 + S, places);
         }
-        int64_t at = pl.cut ? line.mine : line.units;
+        int64_t at = pl.cut ? line.mine + pad * line.units : line.units;
         for (int n = line.first; n < line.last; ++n) {
-            const int64_t more = units_of(a, n) * (pl.cut ? unit_places(a, n) : 1);
+            const int64_t more = (int64_t)units_of(a, n) * (pl.cut ? seq_steps(a, n) + pad : 1);
             if (L0 >= at && L0 < at + more && L0 < L1) {
                 b.start_seq = n;
                 b.start_begin = at;
@@ -397,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kLoadWarp) {
         // ---- work items, and the copies
         Walk w;
-        w.start(a, L0, L1, S, start_seq, start_begin);
+        w.start(a, L0, L1, S, pad, start_seq, start_begin);
         uint32_t nu = 0, nr = 0, nq = 0;   // units, shared units and query tiles so far
         uint32_t us = 0, up = 1, rs = 0, rp = 1;  // ring places, and the parity of the wait for them
         bool ok = true;
@@ -751,12 +776,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ws += (warp * 32 + lane) * 4;
 #pragma unroll 1
-                for (int at = 0; at < 4 * pl.n; at += 16) {
-                    float o[16];
+                for (int at = 0; at < 4 * pl.n; at += 32) {
+                    float o[32];
                     tmem_ld16f(tb + lane_base + kTmemO + at, o);
-                    wait_ld<16>(o);
+                    tmem_ld16f(tb + lane_base + kTmemO + at + 16, o + 16);
+                    wait_ld<32>(o);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < 8; ++e)
                         *reinterpret_cast<float4 *>(ws + (int64_t)(at / 4 + e) * 512) =
                             make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
@@ -768,42 +794,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (live && p.lse) p.lse[out] = l == 0.f ? -INFINITY : (log2f(l) + m) * kLn2;
                 }
                 soft_sync();
-                // Two lanes exchange, so that each stores two channels of every other row.
-                const int odd = lane & 1, esz = p.o_bf16 ? 2 : 4;
-                uint8_t *base = static_cast<uint8_t *>(p.o) + (warp * 32 + lane - odd) * esz;
+                // A thread stores its channel of each row, 64 bytes of a row together in a warp.  (The time is that
+                // of the instructions, one warp on each scheduler: three for a value.  With a branch for each
+                // row that may not be there, or lanes that exchange channels for wider stores, twice as many.)
+                const int64_t esz = p.o_bf16 ? 2 : 4;
+                uint8_t *base = static_cast<uint8_t *>(p.o) + (warp * 32 + lane) * esz;
 #pragma unroll 1
                 for (int r0 = 0; r0 < (int)q_rows; r0 += 16) {
-                    uint8_t *at[8];
-                    float f[16];
+                    float o[64], f[16];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int64_t row_at = b.row_at[r0 + 2 * i + odd];
-                        at[i] = row_at < 0 ? nullptr : base + row_at * (kLatent * esz);
-                    }
+                    for (int q = 0; q < 4; ++q) tmem_ld16f(tb + lane_base + kTmemO + q * pl.n + r0, o + 16 * q);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) f[i] = b.factor[r0 + i];
-                    // (not unrolled: an item's end is seldom run, and 13 KB of instructions that have to be fetched
-                    // while the cache streams through L2 took 11000 cycles the first time)
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        float o[16];
-                        if (nt > 0) {
-                            tmem_ld16f(tb + lane_base + kTmemO + q * pl.n + r0, o);
-                            wait_ld<16>(o);
-                        } else {
+                    wait_ld<64>(o);
+                    if (nt == 0) {  // (then TMEM holds anything)
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = 0.f;
+                        for (int i = 0; i < 64; ++i) o[i] = 0.f;
+                    }
+                    if (p.o_bf16) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int64_t row_at = b.row_at[r0 + i];
+                            uint8_t *at = base + row_at * (kLatent * 2);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) store_if(row_at >= 0, at + q * 256, __float2bfloat16_rn(o[16 * q + i] * f[i]));
                         }
+                    } else {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float a0 = o[2 * i] * f[2 * i], a1 = o[2 * i + 1] * f[2 * i + 1];
-                            const float got = __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
-                            const float y0 = odd ? got : a0, y1 = odd ? a1 : got;
-                            if (!at[i]) continue;
-                            if (p.o_bf16)
-                                *reinterpret_cast<uint32_t *>(at[i] + q * 256) = pack_bf16x2(y0, y1);
-                            else
-                                *reinterpret_cast<float2 *>(at[i] + q * 512) = make_float2(y0, y1);
+                        for (int i = 0; i < 16; ++i) {
+                            const int64_t row_at = b.row_at[r0 + i];
+                            uint8_t *at = base + row_at * (kLatent * 4);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) store_if(row_at >= 0, at + q * 512, o[16 * q + i] * f[i]);
                         }
                     }
                 }
@@ -823,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // After a failure every row of this CTA's items becomes NaN.
     if (*abort_flag) {
         Walk w;
-        w.start(a, L0, L1, S, start_seq, start_begin);
+        w.start(a, L0, L1, S, pad, start_seq, start_begin);
         for (;;) {
             const Item it = w.next(a, piece, g);
             if (!it.found) break;
@@ -976,10 +998,10 @@ Plan plan_of(int64_t N, int64_t tokens, int H, int64_t max_tokens) {
     // (a sequence of nq rows has at most nq / (rows of a unit) + 1 units)
     pl.units_one = (pl.parts + pl.G - 1) / pl.G;
     pl.most_units = tokens == N ? N * units_of(pl, 1) : units_of(pl, (int)tokens) + N;
-    const int64_t per = (max_tokens + kStep - 1) / kStep + kPad;
+    const int64_t per = (max_tokens + kStep - 1) / kStep;
     // RULE
-    pl.cut = !(pl.most_units <= sms && per - kPad <= 24 && pl.most_units * 5 >= sms * 3);
-    pl.pieces = (int)(pl.cut ? std::max<int64_t>(1, std::min(sms, (pl.most_units * per + kMinPiece - 1) / kMinPiece)) : pl.most_units);
+    pl.cut = !(pl.most_units <= sms && per <= 24 && pl.most_units * 5 >= sms * 3);
+    pl.pieces = (int)(pl.cut ? std::max<int64_t>(1, std::min(sms, pl.most_units * per)) : pl.most_units);
     const int64_t q = (int64_t)pl.hp * pl.tk * kRow * 2, ps = (int64_t)pl.n * 128;
     const int64_t room = kMaxSmem - 1024 - (int64_t)round_up(sizeof(Bars), 128) - round_up(q, 1024) - round_up(ps, 1024);
     pl.shared = 2;
