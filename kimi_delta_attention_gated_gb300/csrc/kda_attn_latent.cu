@@ -62,6 +62,7 @@ struct Plan {
     int cut;          // units may be cut; else piece i is the i-th unit
     int64_t most_units;  // of the call at most
     int units_one;    // of a sequence with one token
+    int by_unit;      // the joining launch goes by units, else by pieces
     int n;            // rows of a tile as the products' N: hp * tk, a multiple of 16
     int units, shared;  // ring places
     uint32_t at_p, at_units, at_shared, at_bars;  // shared memory
@@ -93,7 +94,7 @@ struct Bars {
     int64_t row_at[kTileRows];   // a row's place in o, or -1
     float factor[kTileRows];
     int64_t scan[kThreads / 32][2];
-    int64_t start_begin;
+    int64_t start_begin, start_unit;
     int start_seq;
     uint32_t tmem;
     int abort;                   // a bounded wait gave up
@@ -241,17 +242,19 @@ __device__ __forceinline__ Tile tile_of(const Plan &pl, int64_t t0, int nq, int 
     t.steps = t.tokens > 0 ? steps_of(max(0, t.seen0 + t.tokens - 1)) : 0;
     return t;
 }
-// What a part leaves in the workspace (two a CTA; behind them a JoinHead for each CTA): O as [128-channel block][row / 4][channel][row % 4], the rows' references
+// What a part leaves in the workspace (two a CTA): O as [128-channel block][row / 4][channel][row % 4], the rows' references
 // and their sums.
 __host__ __device__ __forceinline__ int64_t part_floats(const Plan &pl) { return (int64_t)pl.n * (kLatent + 2); }
 
-// What the joining launch has to know of the tile that begins in a piece and goes on behind it.
-struct __align__(16) JoinHead {
-    int t0, tokens, head0, last;  // its rows; tokens 0: there is none; the piece of its last step
+// What the joining launch has to know of a tile that begins in a piece and goes on behind it.
+struct __align__(16) JoinWord {
+    int t0, place, first, last;  // its first row; its first head and its rows' tokens << 16; the pieces of its
+                                 // first and its last step
 };
-
-__device__ __forceinline__ int4 *join_head(const Args &a, int cta) {
-    return reinterpret_cast<int4 *>(a.p.ws + (int64_t)a.plan.pieces * a.plan.G * 2 * part_floats(a.plan)) + cta;
+// These words lie behind the parts: with by_unit one for each of a unit's G tiles, then one with
+// the number of units, else one for each CTA.  first == last: nothing to join.
+__device__ __forceinline__ int4 *join_words(const Args &a) {
+    return reinterpret_cast<int4 *>(a.p.ws + (int64_t)a.plan.pieces * a.plan.G * 2 * part_floats(a.plan));
 }
 
 // Goes through the work items of one tile place `g` of a piece.
@@ -261,7 +264,8 @@ struct Walk {
     int64_t t0;
     int pad;
     bool open;
-    JoinHead join;
+    int64_t unit;              // the next unit's number in the call
+    JoinWord join;             // of the last item that begins and is cut
     __device__ void look(const Args &a) {  // at sequence n, or the next one with rows
         for (;; ++n) {
             if (n >= a.p.c.N) return;
@@ -272,21 +276,23 @@ struct Walk {
         units = units_of(a.plan, nq);
         open = true;
     }
-    __device__ void start(const Args &a, int64_t l0, int64_t l1, int64_t s, int own, int seq, int64_t seq_begin) {
+    __device__ void start(const Args &a, int64_t l0, int64_t l1, int64_t s, int own, int seq, int64_t seq_begin, int64_t seq_unit) {
         L0 = l0;
         L1 = l1;
         S = s;
         pad = own;
         open = false;
-        join.t0 = join.tokens = join.head0 = join.last = 0;
+        join.t0 = join.place = join.first = join.last = 0;
         n = seq < 0 ? a.p.c.N : seq;
         if (n >= a.p.c.N) return;
         look(a);
         const int64_t per = a.plan.cut ? line_steps(len) + pad : 1;
         u = (int)((l0 - seq_begin) / per);
         begin = seq_begin + u * per;
+        unit = seq_unit + u;
     }
-    __device__ Item next(const Args &a, int piece, int g) {
+    // (words: by this thread the joining launch's words by unit are written)
+    __device__ Item next(const Args &a, int piece, int g, bool words) {
         const Plan &pl = a.plan;
         Item it;
         it.found = 0;
@@ -298,10 +304,15 @@ struct Walk {
             const Tile t = tile_of(pl, t0, nq, len, u * pl.G + g);
             it.seq = n;
             begin += pl.cut ? line_steps(len) + pad : 1;
+            const int64_t number = unit++;
             if (++u == units) {
                 ++n;
                 u = 0;
                 open = false;
+            }
+            if (words && pl.cut && pl.by_unit && at + (t.steps ? pad : 0) >= L0 && at + (t.steps ? pad : 0) < L1) {
+                const int last = t.steps ? (int)((first + t.steps - 1) / S) : piece;
+                join_words(a)[number * pl.G + g] = make_int4(t.t0, t.head0 | t.tokens << 16, piece, t.tokens ? last : piece);
             }
             if (t.tokens == 0) continue;
             it.t0 = t.t0;
@@ -321,8 +332,8 @@ struct Walk {
                     it.part = (((int64_t)piece * pl.G + g) * 2 + (it.s0 > 0 ? 0 : 1)) * part_floats(pl);
                 if (it.s0 == 0 && it.s1 < t.steps) {
                     join.t0 = t.t0;
-                    join.tokens = t.tokens;
-                    join.head0 = t.head0;
+                    join.place = t.head0 | t.tokens << 16;
+                    join.first = piece;
                     join.last = (int)((first + t.steps - 1) / S);
                 }
             }
@@ -377,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t L0 = piece, L1 = piece + 1, S = 1;
     int pad = 0;
     int start_seq;
-    int64_t start_begin;
+    int64_t start_begin, start_unit = 0, total_units = 0;
     if (!pl.cut && !p.cu_seqlens) {  // as many units in every sequence
         start_seq = piece / pl.units_one;
         start_begin = (int64_t)start_seq * pl.units_one;
@@ -389,15 +400,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             S = (places + pl.pieces - 1) / pl.pieces;
             L0 = piece * S;
             L1 = min(L0 + S, places);
+            total_units = line.total_units;
         }
-        int64_t at = pl.cut ? line.mine + pad * line.units : line.units;
+        int64_t at = pl.cut ? line.mine + pad * line.units : line.units, units = line.units;
         for (int n = line.first; n < line.last; ++n) {
             const int64_t more = (int64_t)units_of(a, n) * (pl.cut ? seq_steps(a, n) + pad : 1);
             if (L0 >= at && L0 < at + more && L0 < L1) {
                 b.start_seq = n;
                 b.start_begin = at;
+                b.start_unit = units;
             }
             at += more;
+            units += units_of(a, n);
         }
     }
     fence_before_sync();
@@ -407,7 +421,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (pl.cut || p.cu_seqlens) {
         start_seq = b.start_seq;
         start_begin = b.start_begin;
+        start_unit = b.start_unit;
     }
+    auto last_words = [&](const Walk &w) {
+        if (!pl.by_unit)
+            join_words(a)[blockIdx.x] = *reinterpret_cast<const int4 *>(&w.join);
+        else if (blockIdx.x == 0)
+            join_words(a)[pl.most_units * pl.G] = make_int4((int)total_units, 0, 0, 0);
+    };
     auto wait_for = [&](uint64_t *bar, uint32_t parity, uint32_t polls) {
         for (uint32_t i = 0; i < polls; ++i) {
             if (mbar_try_wait(bar, parity)) return true;
@@ -420,15 +441,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(bar, parity, kAttnPolls)) != 0; };
 
     if (warp == kLoadWarp) {
-        // ---- work items, and the copies
+        // ---- work items, and the copies of the cache
         Walk w;
-        w.start(a, L0, L1, S, pad, start_seq, start_begin);
-        uint32_t nu = 0, nr = 0, nq = 0;   // units, shared units and query tiles so far
+        w.start(a, L0, L1, S, pad, start_seq, start_begin, start_unit);
+        uint32_t nu = 0, nr = 0;           // units and shared units so far
         uint32_t us = 0, up = 1, rs = 0, rp = 1;  // ring places, and the parity of the wait for them
         bool ok = true;
         const int sub = min(kStep, p.c.P);  // rows of a copy
+        // An item and its first pages are looked up while the one before is copied.
+        struct Pages {
+            int base, subs, now, more;  // copies of the item up to its end; pages of copies base + lane, and of the 32 behind
+        };
+        const int per_step = kStep / sub, in_page = p.c.p_shift - (sub == 16 ? 4 : sub == 32 ? 5 : 6);  // log2 of a page's copies
+        auto fetch = [&](const Item &it, const Pages &q, int i) {
+            return i < q.subs ? __ldg(p.c.block_table + (int64_t)it.seq * p.c.max_blocks + (i >> in_page)) : -1;
+        };
+        auto open = [&](const Item &it) {
+            Pages q = {0, 0, -1, -1};
+            if (!it.found || it.s0 == it.s1) return q;
+            const int last = min(it.seen0 + it.tokens - 1, it.s1 * kStep);  // tokens that the tile needs
+            q.subs = (last + sub - 1) / sub;
+            q.base = it.s0 * per_step;
+            q.now = fetch(it, q, q.base + lane);
+            q.more = fetch(it, q, q.base + 32 + lane);
+            return q;
+        };
+        Item ahead = w.next(a, piece, g, lane == 0);
+        Pages pages_ahead = open(ahead);
         for (uint32_t k = 0; ok; ++k) {
-            const Item it = w.next(a, piece, g);
+            const Item it = ahead;
+            Pages pages = pages_ahead;
             const int slot = k % kSlots;
             if (k >= kSlots) ok = wait(b.i_empty + slot, (k / kSlots - 1) & 1);
             if (!ok) break;
@@ -438,23 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (!it.found) break;
+            ahead = w.next(a, piece, g, lane == 0);
+            pages_ahead = open(ahead);
             if (it.s0 == it.s1) continue;
-            if (nq > 0) ok = wait(&b.q_empty, (nq - 1) & 1);
-            if (!ok) break;
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&b.q_full, 9 * q_rows * 128);
-                for (int x = 0; x < 9; ++x)
-                    tma_load_3d(sb + x * q_rows * 128, &map_q, &b.q_full, x * 64, it.head0, it.t0);
-            }
-            ++nq;
-            const int last = min(it.seen0 + it.tokens - 1, it.s1 * kStep);  // tokens that the tile needs
-            const int per_step = kStep / sub, subs = (last + sub - 1) / sub;
-            const int32_t *table = p.c.block_table + (int64_t)it.seq * p.c.max_blocks;
-            const int in_page = p.c.p_shift - (sub == 16 ? 4 : sub == 32 ? 5 : 6);  // log2 of a page's copies
-            int base = it.s0 * per_step, pages = -1, more = -1;  // pages of copies base + lane, and of the 32 behind them
-            auto fetch = [&](int i) { return i < subs ? __ldg(table + (i >> in_page)) : -1; };
-            pages = fetch(base + lane);
-            more = fetch(base + 32 + lane);
             for (int s = it.s0; s < it.s1 && ok; ++s) {
                 int at[4], n_sub = 0;  // rows of the cache, -1: nothing to copy
 #pragma unroll
@@ -462,13 +490,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     at[j] = -1;
                     if (j >= per_step) continue;
                     const int i = s * per_step + j;
-                    if (i - base >= 32) {
-                        base += 32;
-                        pages = more;
-                        more = fetch(base + 32 + lane);
+                    if (i - pages.base >= 32) {
+                        pages.base += 32;
+                        pages.now = pages.more;
+                        pages.more = fetch(it, pages, pages.base + 32 + lane);
                     }
-                    const int page = __shfl_sync(0xffffffffu, pages, i - base);
-                    if (i >= subs) continue;
+                    const int page = __shfl_sync(0xffffffffu, pages.now, i - pages.base);
+                    if (i >= pages.subs) continue;
                     if ((uint32_t)page >= (uint32_t)p.c.n_pages) {
                         if (lane == 0) *(volatile int *)&b.slots[slot].bad = 1;
                         continue;
@@ -508,10 +536,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (pl.cut && lane == 0 && ok) *join_head(a, blockIdx.x) = *reinterpret_cast<const int4 *>(&w.join);
+        if (pl.cut && lane == 0 && ok) last_words(w);
         // every copy lands before the CTA may end
         if (lane == 0) {
-            if (nq) mbar_wait(&b.q_full, (nq - 1) & 1, kAttnPolls);
             for (uint32_t j = nr > (uint32_t)pl.shared ? nr - pl.shared : 0; j < nr; ++j)
                 mbar_wait(b.r_full + j % pl.shared, (j / pl.shared) & 1, kAttnPolls);
             for (uint32_t j = nu > (uint32_t)pl.units ? nu - pl.units : 0; j < nu; ++j)
@@ -529,11 +556,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         if (elect_one()) {
             // The next item's steps: -1 at the end.
+            int t0 = 0, head0 = 0;
             auto next_item = [&](uint32_t k) {
                 ok = wait_for(b.i_full + k % kSlots, (k / kSlots) & 1, kAttnPolls);
                 if (!ok) return -1;
                 const Item &it = b.slots[k % kSlots];
                 const int nt = it.found ? it.s1 - it.s0 : -1;
+                t0 = it.t0;
+                head0 = it.head0;
                 mbar_arrive(b.i_empty + k % kSlots);
                 return nt;
             };
@@ -545,7 +575,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int nt = next_item(k);
                     if (nt < 0) break;
                     if (nt == 0) continue;
+                    // the queries, when the last item's scores are through (from this thread, so that the cache's
+                    // copies do not wait for that: 6000 cycles at the border of two items)
+                    if (items > 0) ok = wait_for(&b.q_empty, (items - 1) & 1, kAttnPolls);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&b.q_full, 9 * q_rows * 128);
+                    for (int x = 0; x < 9; ++x) tma_load_3d(sb + x * q_rows * 128, &map_q, &b.q_full, x * 64, head0, t0);
                     ok = wait_for(&b.q_full, items & 1, p.polls);
+                    if (!ok) mbar_wait(&b.q_full, items & 1, kAttnPolls);  // it still has to land before the CTA may end
                     for (int s = 0; s < nt && ok; ++s, ++blocks) {
                         const uint32_t t_s = tb + (blocks & 1) * kStep;
                         if (blocks >= 2) ok = wait_for(b.s_free + (blocks & 1), ((blocks >> 1) - 1) & 1, kAttnPolls);
@@ -845,9 +882,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // After a failure every row of this CTA's items becomes NaN.
     if (*abort_flag) {
         Walk w;
-        w.start(a, L0, L1, S, pad, start_seq, start_begin);
+        w.start(a, L0, L1, S, pad, start_seq, start_begin, start_unit);
         for (;;) {
-            const Item it = w.next(a, piece, g);
+            const Item it = w.next(a, piece, g, threadIdx.x == 0);
             if (!it.found) break;
             if (it.part >= 0) {
                 for (int i = threadIdx.x; i < part_floats(pl); i += kThreads) p.ws[it.part + i] = kNaN;
@@ -861,27 +898,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ch == 0 && p.lse) p.lse[out] = kNaN;
             }
         }
-        if (pl.cut && threadIdx.x == 0) *join_head(a, blockIdx.x) = *reinterpret_cast<const int4 *>(&w.join);
+        if (pl.cut && threadIdx.x == 0) last_words(w);
         if (threadIdx.x == 0) atomicAdd(&g_attn_latent_timeouts, 1);
     }
 }
 
-// Joins the tiles that more than one piece took, in the order of the pieces.  blockIdx.x is a CTA of the
-// first launch, which has left word of the tile that begins in its piece and goes on behind it, if there is
-// one.  A warp has four rows and 128 channels, or with `shares` > 1 a share of their pieces.
+// Joins the tiles that more than one piece took, in the order of the pieces.  blockIdx.x is a unit's tile, or
+// with more units than pieces a CTA of the first launch, which looks after the tile that begins in its
+// piece and goes on behind it, if there is one.  A warp has four rows and 128 channels, or with
+// `shares` > 1 a share of their pieces.
 constexpr int kMaxShares = 4;
 __global__ void __launch_bounds__(128 * kMaxShares) attn_latent_join_kernel(const __grid_constant__ Args a, int shares) {
     extern __shared__ float4 s_acc[];  // [shares - 1 of 4 warps][128], then their m and l
     const AttnLatentParams &p = a.p;
     const Plan &pl = a.plan;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k0 = blockIdx.x / pl.G, g = blockIdx.x - k0 * pl.G;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = blockIdx.x / pl.G, g = blockIdx.x - which * pl.G;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 word = __ldcg(join_head(a, blockIdx.x));
-    const JoinHead t = *reinterpret_cast<const JoinHead *>(&word);
-    const int share = warp >> 2, q = warp & 3, k1 = t.last;
+    const int4 *words = join_words(a);
+    const int units = pl.by_unit ? __ldcg(&words[pl.most_units * pl.G].x) : pl.pieces;
+    const int4 word = __ldcg(words + blockIdx.x);
+    const JoinWord t = *reinterpret_cast<const JoinWord *>(&word);
+    const int share = warp >> 2, q = warp & 3, k0 = t.first, k1 = t.last;
     const int r = 4 * blockIdx.y;  // the first of the rows, all of one token
-    const int tok = r / pl.hp, head = t.head0 + r - tok * pl.hp;
-    if (tok >= t.tokens || head >= p.H) return;
+    const int tok = r / pl.hp, head = (t.place & 0xFFFF) + r - tok * pl.hp;
+    if (which >= units || k0 >= k1 || tok >= t.place >> 16 || head >= p.H) return;
     const int64_t out = (int64_t)(t.t0 + tok) * p.H + head;
     float m[4], l[4], acc[4][4];  // of the rows; of channels lane + 32 * i
 #pragma unroll
@@ -891,46 +931,38 @@ __global__ void __launch_bounds__(128 * kMaxShares) attn_latent_join_kernel(cons
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i][e] = 0.f;
     }
-    auto four = [](const float *x, float (&y)[4]) {
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(x));
-        y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
+    const int each = (k1 - k0 + shares) / shares, from = k0 + share * each, to = min(from + each, k1 + 1);
+    // (the tile is in slot 1 of the piece that it begins in, else in slot 0)
+    const int64_t floats = part_floats(pl), step = 2 * pl.G * floats;
+    const float *ws = p.ws + (from * pl.G + g) * 2 * floats + (share == 0 ? floats : 0);
+    const int at = pl.n * kLatent + r;
+    struct Four {
+        float4 m, l, x[4];
+    } now, next;
+    auto load = [&](Four &f, const float *ws) {
+        const float4 *x = reinterpret_cast<const float4 *>(ws + ((int64_t)(q * pl.n + r) / 4 * 128 + lane) * 4);
+        f.m = __ldcg(reinterpret_cast<const float4 *>(ws + at));
+        f.l = __ldcg(reinterpret_cast<const float4 *>(ws + at + pl.n));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.x[i] = __ldcg(x + 32 * i);
     };
-    {
-        const int each = (k1 - k0 + shares) / shares, from = k0 + share * each, to = min(from + each, k1 + 1);
-        // (the unit is in slot 1 of the piece that it begins in, else in slot 0)
-        auto part = [&](int k) { return p.ws + (((int64_t)k * pl.G + g) * 2 + (k == k0)) * part_floats(pl); };
-        for (int kb = from; kb < to; kb += 32) {  // a lane's piece's references and sums, then the channels of all
-            float mk[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, lk[4] = {}, fk[4];
-            if (kb + lane < to) {
-                four(part(kb + lane) + pl.n * kLatent + r, mk);
-                four(part(kb + lane) + pl.n * (kLatent + 1) + r, lk);
-            }
+    if (from < to) load(next, ws);
+    for (int k = from; k < to; ++k) {  // every lane forms the factors itself: the next part is on its way meanwhile
+        now = next;
+        if (k == k0) ws -= floats;
+        ws += step;
+        if (k + 1 < to) load(next, ws);
+        const float mk[4] = {now.m.x, now.m.y, now.m.z, now.m.w}, lk[4] = {now.l.x, now.l.y, now.l.z, now.l.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float most = mk[e];
+        for (int e = 0; e < 4; ++e) {
+            const float most = fmaxf(m[e], mk[e]), own = most == -INFINITY ? 1.f : ex2(m[e] - most);
+            const float f = most == -INFINITY ? 1.f : ex2(mk[e] - most);
+            m[e] = most;
+            l[e] = fmaf(lk[e], f, l[e] * own);
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-                most = fmaxf(most, m[e]);
-                fk[e] = most == -INFINITY ? 1.f : ex2(mk[e] - most);
-                const float f = most == -INFINITY ? 1.f : ex2(m[e] - most);
-                m[e] = most;
-                l[e] = l[e] * f + warp_sum(lk[e] * fk[e]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[i][e] *= f;
-            }
-            const int count = min(32, to - kb);
-#pragma unroll 4
-            for (int k = 0; k < count; ++k) {
-                const float *x = part(kb + k) + ((int64_t)(q * pl.n + r) / 4 * 128 + lane) * 4;
-                float v[4][4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) four(x + i * 128, v[i]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float w = __shfl_sync(0xffffffffu, fk[e], k);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[i][e] = fmaf(v[i][e], w, acc[i][e]);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const float x = e == 0 ? now.x[i].x : e == 1 ? now.x[i].y : e == 2 ? now.x[i].z : now.x[i].w;
+                acc[i][e] = fmaf(x, f, acc[i][e] * own);
             }
         }
     }
@@ -1002,6 +1034,7 @@ Plan plan_of(int64_t N, int64_t tokens, int H, int64_t max_tokens) {
     // RULE
     pl.cut = !(pl.most_units <= sms && per <= 24 && pl.most_units * 5 >= sms * 3);
     pl.pieces = (int)(pl.cut ? std::max<int64_t>(1, std::min(sms, pl.most_units * per)) : pl.most_units);
+    pl.by_unit = pl.most_units < pl.pieces;
     const int64_t q = (int64_t)pl.hp * pl.tk * kRow * 2, ps = (int64_t)pl.n * 128;
     const int64_t room = kMaxSmem - 1024 - (int64_t)round_up(sizeof(Bars), 128) - round_up(q, 1024) - round_up(ps, 1024);
     pl.shared = 2;
@@ -1014,7 +1047,8 @@ Plan plan_of(int64_t N, int64_t tokens, int H, int64_t max_tokens) {
 }
 
 size_t plan_bytes(const Plan &pl) {
-    return pl.cut ? (size_t)pl.pieces * pl.G * (2 * part_floats(pl) * sizeof(float) + sizeof(JoinHead)) : 0;
+    const int64_t words = pl.by_unit ? pl.most_units * pl.G + 1 : (int64_t)pl.pieces * pl.G;
+    return pl.cut ? (size_t)pl.pieces * pl.G * 2 * part_floats(pl) * sizeof(float) + words * sizeof(JoinWord) : 0;
 }
 
 bool encode_tensors(const AttnLatentParams &p, const Plan &pl, CUtensorMap *mq, CUtensorMap *mc) {
@@ -1085,7 +1119,7 @@ kda_status launch_attn_latent(const AttnLatentParams &p, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     // with many pieces a unit more warps share them
     const int shares = pl.pieces >= 16 * pl.most_units ? kMaxShares : 1;
-    cfg.gridDim = dim3(pl.pieces * pl.G, pl.hp * pl.tk / 4);
+    cfg.gridDim = dim3((unsigned)((pl.by_unit ? pl.most_units : pl.pieces) * pl.G), pl.hp * pl.tk / 4);
     cfg.blockDim = dim3(128 * shares);
     cfg.dynamicSmemBytes = (shares - 1) * 4 * (128 + 2) * sizeof(float4);
     cfg.stream = st;
