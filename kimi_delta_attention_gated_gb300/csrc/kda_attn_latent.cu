@@ -25,6 +25,8 @@
 // attn_latent_join_kernel adds them in their order, so results do not depend on timing.
 #include <cuda.h>
 
+#include <climits>
+
 #include <algorithm>
 #include <cstring>
 
@@ -346,7 +348,7 @@ struct Walk {
 
 __global__ void __launch_bounds__(kThreads, 1)
     attn_latent_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_c,
-                       const __grid_constant__ Args a) {
+                       const __grid_constant__ CUtensorMap map_r, const __grid_constant__ Args a) {
     const AttnLatentParams &p = a.p;
     const Plan &pl = a.plan;
     extern __shared__ uint8_t smem_raw[];
@@ -378,8 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane < p.c.max_blocks) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(y) : "l"(p.c.block_table + (int64_t)n * p.c.max_blocks + lane));
         asm volatile("" ::"r"(x), "r"(y));
     }
-    if (warp == kLoadWarp && lane < 2)
-        asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &map_q : &map_c) : "memory");
+    if (warp == kLoadWarp && lane < 3)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &map_q : lane == 1 ? &map_c : &map_r) : "memory");
     if (warp == kScoreWarp) {
         tmem_alloc(&b.tmem, 512);
         tmem_relinquish();
@@ -441,104 +443,98 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(bar, parity, kAttnPolls)) != 0; };
 
     if (warp == kLoadWarp) {
-        // ---- work items, and the copies of the cache
-        Walk w;
-        w.start(a, L0, L1, S, pad, start_seq, start_begin, start_unit);
-        uint32_t nu = 0, nr = 0;           // units and shared units so far
-        uint32_t us = 0, up = 1, rs = 0, rp = 1;  // ring places, and the parity of the wait for them
-        bool ok = true;
-        const int sub = min(kStep, p.c.P);  // rows of a copy
-        // An item and its first pages are looked up while the one before is copied.
-        struct Pages {
-            int base, subs, now, more;  // copies of the item up to its end; pages of copies base + lane, and of the 32 behind
-        };
-        const int per_step = kStep / sub, in_page = p.c.p_shift - (sub == 16 ? 4 : sub == 32 ? 5 : 6);  // log2 of a page's copies
-        auto fetch = [&](const Item &it, const Pages &q, int i) {
-            return i < q.subs ? __ldg(p.c.block_table + (int64_t)it.seq * p.c.max_blocks + (i >> in_page)) : -1;
-        };
-        auto open = [&](const Item &it) {
-            Pages q = {0, 0, -1, -1};
-            if (!it.found || it.s0 == it.s1) return q;
-            const int last = min(it.seen0 + it.tokens - 1, it.s1 * kStep);  // tokens that the tile needs
-            q.subs = (last + sub - 1) / sub;
-            q.base = it.s0 * per_step;
-            q.now = fetch(it, q, q.base + lane);
-            q.more = fetch(it, q, q.base + 32 + lane);
-            return q;
-        };
-        Item ahead = w.next(a, piece, g, lane == 0);
-        Pages pages_ahead = open(ahead);
-        for (uint32_t k = 0; ok; ++k) {
-            const Item it = ahead;
-            Pages pages = pages_ahead;
-            const int slot = k % kSlots;
-            if (k >= kSlots) ok = wait(b.i_empty + slot, (k / kSlots - 1) & 1);
-            if (!ok) break;
-            if (lane == 0) {
-                b.slots[slot] = it;
-                mbar_arrive(b.i_full + slot);
-            }
-            __syncwarp();
-            if (!it.found) break;
-            ahead = w.next(a, piece, g, lane == 0);
-            pages_ahead = open(ahead);
-            if (it.s0 == it.s1) continue;
-            for (int s = it.s0; s < it.s1 && ok; ++s) {
-                int at[4], n_sub = 0;  // rows of the cache, -1: nothing to copy
+        // ---- work items, and the copies of the cache, from one thread: a step's copies have to be issued in
+        // less than its time (with the warp's votes about each wait and two copies a unit they took 2900
+        // cycles and were the bound)
+        if (elect_one()) {
+            Walk w;
+            w.start(a, L0, L1, S, pad, start_seq, start_begin, start_unit);
+            uint32_t nu = 0, nr = 0;                  // units and shared units so far
+            uint32_t us = 0, up = 1, rs = 0, rp = 1;  // ring places, and the parity of the wait for them
+            bool ok = true;
+            const int sub = min(kStep, p.c.P), per_step = kStep / sub;                         // rows of a copy
+            const int in_page = p.c.p_shift - (sub == 16 ? 4 : sub == 32 ? 5 : 6);             // log2 of a page's copies
+            // Page numbers of a step's copies, looked up a step ahead (an item's first while the one before is
+            // copied).  kNone: behind what the tile needs.
+            constexpr int kNone = INT_MIN;
+            struct Pages {
+                int at[4];
+            };
+            auto look_up = [&](const Item &it, int s) {
+                Pages q;
+                const int last = min(it.seen0 + it.tokens - 1, it.s1 * kStep);  // tokens that the tile needs
+                const int32_t *table = p.c.block_table + (int64_t)it.seq * p.c.max_blocks;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    at[j] = -1;
-                    if (j >= per_step) continue;
                     const int i = s * per_step + j;
-                    if (i - pages.base >= 32) {
-                        pages.base += 32;
-                        pages.now = pages.more;
-                        pages.more = fetch(it, pages, pages.base + 32 + lane);
+                    q.at[j] = kNone;
+                    if (j < per_step && it.found && s < it.s1 && i * sub < last) {
+                        const int page = __ldg(table + (i >> in_page));
+                        q.at[j] = page == kNone ? -1 : page;
                     }
-                    const int page = __shfl_sync(0xffffffffu, pages.now, i - pages.base);
-                    if (i >= pages.subs) continue;
-                    if ((uint32_t)page >= (uint32_t)p.c.n_pages) {
-                        if (lane == 0) *(volatile int *)&b.slots[slot].bad = 1;
-                        continue;
-                    }
-                    at[j] = (page << p.c.p_shift) + ((i << (p.c.p_shift - in_page)) & (p.c.P - 1));
-                    ++n_sub;
                 }
-                __syncwarp();
-                // the shared channels first: their scores come first
-                ok = nr < (uint32_t)pl.shared || wait(b.r_empty + rs, rp);
+                return q;
+            };
+            Item ahead = w.next(a, piece, g, true);
+            Pages first = look_up(ahead, ahead.s0);
+            for (uint32_t k = 0; ok; ++k) {
+                const Item it = ahead;
+                Pages pages = first;
+                const int slot = k % kSlots;
+                if (k >= kSlots) ok = wait_for(b.i_empty + slot, (k / kSlots - 1) & 1, kAttnPolls);
                 if (!ok) break;
-                if (elect_one()) {
+                b.slots[slot] = it;
+                mbar_arrive(b.i_full + slot);
+                if (!it.found) break;
+                ahead = w.next(a, piece, g, true);
+                first = look_up(ahead, ahead.s0);
+                for (int s = it.s0; s < it.s1 && ok; ++s) {
+                    int at[4], n_sub = 0;  // rows of the cache, -1: nothing to copy
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        at[j] = -1;
+                        if (pages.at[j] == kNone) continue;
+                        if ((uint32_t)pages.at[j] >= (uint32_t)p.c.n_pages) {
+                            *(volatile int *)&b.slots[slot].bad = 1;
+                            continue;
+                        }
+                        at[j] = (pages.at[j] << p.c.p_shift) + (((s * per_step + j) << (p.c.p_shift - in_page)) & (p.c.P - 1));
+                        ++n_sub;
+                    }
+                    pages = look_up(it, s + 1);
+                    // the shared channels first: their scores come first
+                    ok = nr < (uint32_t)pl.shared || wait_for(b.r_empty + rs, rp, kAttnPolls);
+                    if (!ok) break;
                     mbar_arrive_expect_tx(b.r_full + rs, n_sub * sub * 128);
+                    const uint32_t r_to = sb + pl.at_shared + rs * kSharedBytes;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (at[j] >= 0)
-                            tma_load_2d(sb + pl.at_shared + rs * kSharedBytes + j * sub * 128, &map_c, b.r_full + rs, kLatent, at[j]);
-                }
-                __syncwarp();
-                ++nr;
-                if (++rs == (uint32_t)pl.shared) rs = 0, rp ^= 1;
-                for (int m = 0; m < 4; ++m) {
-                    ok = nu < (uint32_t)pl.units || wait(b.u_empty + us, up);
-                    if (!ok) break;
-                    if (elect_one()) {
+                        if (at[j] >= 0) tma_load_3d(r_to + j * sub * 128, &map_r, b.r_full + rs, 0, at[j], kLatent / 64);
+                    ++nr;
+                    if (++rs == (uint32_t)pl.shared) rs = 0, rp ^= 1;
+#pragma unroll 1
+                    for (int m = 0; m < 4; ++m) {
+                        ok = nu < (uint32_t)pl.units || wait_for(b.u_empty + us, up, kAttnPolls);
+                        if (!ok) break;
                         mbar_arrive_expect_tx(b.u_full + us, n_sub * sub * 256);
+                        const uint32_t u_to = sb + pl.at_units + us * kUnitBytes;
+                        if (per_step == 1) {  // both blocks of 64 channels at once
+                            if (at[0] >= 0) tma_load_3d(u_to, &map_c, b.u_full + us, 0, at[0], 2 * m);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (at[j] >= 0)
-                                for (int h = 0; h < 2; ++h)
-                                    tma_load_2d(sb + pl.at_units + us * kUnitBytes + h * kSharedBytes + j * sub * 128, &map_c,
-                                                b.u_full + us, m * 128 + h * 64, at[j]);
+                            for (int j = 0; j < 4; ++j)
+                                if (at[j] >= 0) {
+                                    tma_load_3d(u_to + j * sub * 128, &map_r, b.u_full + us, 0, at[j], 2 * m);
+                                    tma_load_3d(u_to + kSharedBytes + j * sub * 128, &map_r, b.u_full + us, 0, at[j], 2 * m + 1);
+                                }
+                        }
+                        ++nu;
+                        if (++us == (uint32_t)pl.units) us = 0, up ^= 1;
                     }
-                    __syncwarp();
-                    ++nu;
-                    if (++us == (uint32_t)pl.units) us = 0, up ^= 1;
                 }
             }
-        }
-        if (pl.cut && lane == 0 && ok) last_words(w);
-        // every copy lands before the CTA may end
-        if (lane == 0) {
+            if (pl.cut && ok) last_words(w);
+            // every copy lands before the CTA may end
             for (uint32_t j = nr > (uint32_t)pl.shared ? nr - pl.shared : 0; j < nr; ++j)
                 mbar_wait(b.r_full + j % pl.shared, (j / pl.shared) & 1, kAttnPolls);
             for (uint32_t j = nu > (uint32_t)pl.units ? nu - pl.units : 0; j < nu; ++j)
@@ -1051,7 +1047,7 @@ size_t plan_bytes(const Plan &pl) {
     return pl.cut ? (size_t)pl.pieces * pl.G * 2 * part_floats(pl) * sizeof(float) + words * sizeof(JoinWord) : 0;
 }
 
-bool encode_tensors(const AttnLatentParams &p, const Plan &pl, CUtensorMap *mq, CUtensorMap *mc) {
+bool encode_tensors(const AttnLatentParams &p, const Plan &pl, CUtensorMap *mq, CUtensorMap *mc, CUtensorMap *mr) {
     chunk::EncodeTiledFn enc = reinterpret_cast<chunk::EncodeTiledFn>(tensor_map_encoder());
     if (!enc) {
         set_error("attn_latent: cuTensorMapEncodeTiled is not available from the driver");
@@ -1064,12 +1060,15 @@ bool encode_tensors(const AttnLatentParams &p, const Plan &pl, CUtensorMap *mq, 
     CUresult r = enc(mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16 *>(p.q), qd, qs, qb, es,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    const cuuint64_t cd[2] = {(cuuint64_t)kRow, (cuuint64_t)p.c.n_pages * p.c.P};
-    const cuuint64_t cs[1] = {(cuuint64_t)kRow * 2};
-    const cuuint32_t cb[2] = {64, (cuuint32_t)std::min(p.c.P, kStep)};
-    if (r == CUDA_SUCCESS)
-        r = enc(mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.c.rows, cd, cs, cb, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    // The cache as [9 blocks of 64 channels][rows][64]: a copy brings two blocks of a step's rows (mc), or one of
+    // a small page's (mr), each block's rows together as the products take them.
+    const cuuint64_t cd[3] = {64, (cuuint64_t)p.c.n_pages * p.c.P, kRow / 64};
+    const cuuint64_t cs[2] = {(cuuint64_t)kRow * 2, 128};
+    for (int blocks = 1; blocks <= 2 && r == CUDA_SUCCESS; ++blocks) {
+        const cuuint32_t cb[3] = {64, (cuuint32_t)std::min(p.c.P, kStep), (cuuint32_t)blocks};
+        r = enc(blocks == 1 ? mr : mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.c.rows, cd, cs, cb, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    }
     if (r != CUDA_SUCCESS) set_error("attn_latent: cuTensorMapEncodeTiled failed (%d)", (int)r);
     return r == CUDA_SUCCESS;
 }
@@ -1101,8 +1100,8 @@ kda_status launch_attn_latent(const AttnLatentParams &p, cudaStream_t st) {
     a.p = p;
     a.plan = plan_of(p.c.N, p.tokens, p.H, (int64_t)p.c.max_blocks * p.c.P);
     const Plan &pl = a.plan;
-    CUtensorMap mq, mc;
-    if (!encode_tensors(p, pl, &mq, &mc)) return KDA_ERR_CUDA;
+    CUtensorMap mq, mc, mr;
+    if (!encode_tensors(p, pl, &mq, &mc, &mr)) return KDA_ERR_CUDA;
     static DeviceOnce configured;
     const int dev = current_device();
     if (!configured.done(dev)) {
@@ -1112,7 +1111,7 @@ kda_status launch_attn_latent(const AttnLatentParams &p, cudaStream_t st) {
         }
         configured.set(dev);
     }
-    attn_latent_kernel<<<pl.pieces * pl.G, kThreads, kMaxSmem, st>>>(mq, mc, a);
+    attn_latent_kernel<<<pl.pieces * pl.G, kThreads, kMaxSmem, st>>>(mq, mc, mr, a);
     note_launch();
     kda_status s = check_launch("attn_latent_kernel");
     if (!pl.cut || s != KDA_OK) return s;
