@@ -3,18 +3,20 @@
 //   [c | r]  ->  [c / sqrt(mean(c^2) + eps) * w | r turned by the token's place]
 //
 // in bf16, each value rounded once.  The bound is memory: 1152 bytes a token in and as many out (twice
-// where the rows are wanted densely too).  A warp takes a token, a lane two 16-byte pieces of c, so that
-// the norm needs no more than two warp sums, and eight lanes take the pieces of r.
+// where the rows are wanted densely too).  A warp takes a run of tokens, whose sequence it looks for
+// once, with the next token's row on its way; a lane has two 16-byte pieces of c, so that the norm needs
+// one warp sum, and eight lanes have the pieces of r.
 #include "kda_latent.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr float kBig = 1.152921504606847e18f;     // 2^60: squares above and below these bounds
-constexpr float kSmall = 8.673617379884035e-19f;  // 2^-60 leave fp32, so c is taken at another scale
+constexpr int kResident = 3;  // CTAs of an SM
+// Sums of squares within these bounds have lost nothing to fp32's range.
+constexpr float kLeastSum = 8.077935669463161e-28f, kMostSum = 1.329227995784916e36f;  // 2^-90, 2^120
 
-// The sequence of row t: the last one that begins at or before it; -1 if t belongs to none.
+// The sequence of row t: the last one that begins at or before it.
 __device__ __forceinline__ int sequence_of(const LatentAppendParams &p, int64_t t) {
     if (!p.cu_seqlens) return (int)t;
     int lo = 0, hi = p.c.N - 1;
@@ -25,68 +27,93 @@ __device__ __forceinline__ int sequence_of(const LatentAppendParams &p, int64_t 
         else
             hi = m - 1;
     }
-    return t >= __ldg(p.cu_seqlens + lo) && t < __ldg(p.cu_seqlens + lo + 1) ? lo : -1;
+    return lo;
 }
 
-__global__ void __launch_bounds__(kWarps * 32) latent_append_kernel(const __grid_constant__ LatentAppendParams p) {
+struct Row {
+    uint4 a, b, r;  // pieces lane and 32 + lane of c; lanes 0 to 7: piece lane of r
+};
+__device__ __forceinline__ Row load_row(const LatentAppendParams &p, int64_t t) {
+    const uint4 *x = reinterpret_cast<const uint4 *>(p.x + t * p.x_stride);
+    const int lane = threadIdx.x & 31;
+    Row y;
+    y.a = __ldcs(x + lane);
+    y.b = __ldcs(x + 32 + lane);
+    y.r = make_uint4(0, 0, 0, 0);
+    if (lane < 8) y.r = __ldcs(x + 64 + lane);
+    return y;
+}
+
+// c / sqrt(mean(c^2) + eps) * w.
+__device__ __forceinline__ void normalise(Row &y, const float (&w)[16], float eps) {
+    float v[16];
+    {
+        float h[8];
+        Vec16<__nv_bfloat16>::load(y.a, h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = h[i];
+        Vec16<__nv_bfloat16>::load(y.b, h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 + i] = h[i];
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum = fmaf(v[i], v[i], sum);
+    sum = warp_sum(sum);
+    float s = 1.f;
+    if (!(sum >= kLeastSum && sum <= kMostSum)) {  // (the same in all lanes) again at another scale
+        // (eps s^2 has to stay finite; beside an eps of 1/2 so small a sum is nothing)
+        s = !(sum <= kMostSum) ? exp2_int(-64) : eps < 0.5f ? exp2_int(64) : 1.f;
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum = fmaf(v[i] * s, v[i] * s, sum);
+        sum = warp_sum(sum);
+    }
+    const float f = rsqrtf(sum * (1.f / kLatent) + eps * s * s);
+    float h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = v[i] * s * f * w[i];
+    y.a = Vec16<__nv_bfloat16>::store(h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = v[8 + i] * s * f * w[8 + i];
+    y.b = Vec16<__nv_bfloat16>::store(h);
+}
+
+__global__ void __launch_bounds__(kWarps * 32, kResident) latent_append_kernel(const __grid_constant__ LatentAppendParams p, int run) {
     __shared__ __align__(16) float2 s_cs[kWarps][kShared / 2];
     __shared__ __align__(16) __nv_bfloat16 s_r[kWarps][kShared];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, np = p.rot.R >> 1;
+    const int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * run, t1 = min(t0 + run, p.tokens);
+    if (t0 >= t1) return;
+    Row next = load_row(p, t0);
     const uint64_t turn = lane < np ? turn_of(__ldg(p.rot.inv_freq + lane)) : 0;
     float w[16];
     if (p.norm_w) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) w[i] = __ldg(p.norm_w + (i >> 3) * 256 + lane * 8 + (i & 7));
     }
-    for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < p.tokens; t += (int64_t)gridDim.x * kWarps) {
-        const __nv_bfloat16 *x = p.x + t * p.x_stride;
-        uint4 a = __ldg(reinterpret_cast<const uint4 *>(x) + lane), b = __ldg(reinterpret_cast<const uint4 *>(x) + 32 + lane);
-        uint4 r = make_uint4(0, 0, 0, 0);
-        if (lane < 8) r = __ldg(reinterpret_cast<const uint4 *>(x + kLatent) + lane);
-        const int n = sequence_of(p, t);
-        if (n < 0) continue;  // rows of no sequence are left as they are
-        const uint32_t place = (uint32_t)max(__ldg(p.c.lens + n), 0) + (p.cu_seqlens ? (uint32_t)(t - max(__ldg(p.cu_seqlens + n), 0)) : 0u);
-        const uint32_t block = place >> p.c.p_shift;
+    int n = -1;
+    int64_t first = 0, end = 0;  // of sequence n
+    uint32_t before = 0;         // places of it that were there
+    for (int64_t t = t0; t < t1; ++t) {
+        Row y = next;
+        if (t + 1 < t1) next = load_row(p, t + 1);
+        if (n < 0 || t >= end) {
+            n = sequence_of(p, t);
+            first = p.cu_seqlens ? max(__ldg(p.cu_seqlens + n), 0) : t;
+            end = p.cu_seqlens ? __ldg(p.cu_seqlens + n + 1) : t + 1;
+            before = (uint32_t)max(__ldg(p.c.lens + n), 0);
+        }
+        if (t < first || t >= end) {  // rows of no sequence are left as they are
+            n = -1;
+            continue;
+        }
+        const uint32_t place = before + (uint32_t)(t - first), block = place >> p.c.p_shift;
         int page = -1;
         if (block < (uint32_t)p.c.max_blocks) page = __ldg(p.c.block_table + (int64_t)n * p.c.max_blocks + block);
-        if (p.norm_w) {
-            float v[16];
-            {
-                float h[8];
-                Vec16<__nv_bfloat16>::load(a, h);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = h[i];
-                Vec16<__nv_bfloat16>::load(b, h);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[8 + i] = h[i];
-            }
-            float most = 0.f, sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                most = fmaxf(most, fabsf(v[i]));
-                sum = fmaf(v[i], v[i], sum);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-            float s = 1.f;
-            if (most > kBig || most < kSmall) {
-                s = most > kBig ? exp2_int(-64) : exp2_int(64);
-                if (s > 1.f && p.eps >= 0.5f) s = 1.f;  // (eps s^2 has to stay finite; such an eps is all that counts)
-                sum = 0.f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) sum = fmaf(v[i] * s, v[i] * s, sum);
-            }
-            const float f = rsqrtf(warp_sum(sum) * (1.f / kLatent) + p.eps * s * s);
-            float h[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] = v[i] * s * f * w[i];
-            a = Vec16<__nv_bfloat16>::store(h);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] = v[8 + i] * s * f * w[8 + i];
-            b = Vec16<__nv_bfloat16>::store(h);
-        }
+        if (p.norm_w) normalise(y, w, p.eps);
         if (np > 0) {
-            if (lane < 8) reinterpret_cast<uint4 *>(s_r[warp])[lane] = r;
+            if (lane < 8) reinterpret_cast<uint4 *>(s_r[warp])[lane] = y.r;
             if (lane < np) {
                 float c, s;
                 cos_sin_turn((uint64_t)place * turn, c, s);
@@ -96,14 +123,14 @@ __global__ void __launch_bounds__(kWarps * 32) latent_append_kernel(const __grid
             if (lane < rotary_units(kShared, p.rot.R, p.rot.interleaved, 8))
                 rotate_unit<__nv_bfloat16>(s_r[warp], s_r[warp], s_cs[warp], lane, p.rot.R, p.rot.interleaved, p.rot.magnitude);
             __syncwarp();
-            if (lane < 8) r = reinterpret_cast<const uint4 *>(s_r[warp])[lane];
+            if (lane < 8) y.r = reinterpret_cast<const uint4 *>(s_r[warp])[lane];
             __syncwarp();  // read before the next token's are written
         }
-        auto put = [&](__nv_bfloat16 *y) {
-            uint4 *row = reinterpret_cast<uint4 *>(y);
-            row[lane] = a;
-            row[32 + lane] = b;
-            if (lane < 8) row[64 + lane] = r;
+        auto put = [&](__nv_bfloat16 *to) {
+            uint4 *row = reinterpret_cast<uint4 *>(to);
+            row[lane] = y.a;
+            row[32 + lane] = y.b;
+            if (lane < 8) row[64 + lane] = y.r;
         };
         if (p.rows_out) put(p.rows_out + t * kRow);
         if ((uint32_t)page < (uint32_t)p.c.n_pages)
@@ -115,8 +142,10 @@ __global__ void __launch_bounds__(kWarps * 32) latent_append_kernel(const __grid
 
 kda_status launch_latent_append(const LatentAppendParams &p, cudaStream_t st) {
     if (p.tokens == 0 || p.c.N == 0) return KDA_OK;
-    const int64_t most = 8ll * sm_count(), ctas = (p.tokens + kWarps - 1) / kWarps;
-    latent_append_kernel<<<(unsigned)(ctas < most ? ctas : most), kWarps * 32, 0, st>>>(p);
+    // one token a warp, or equal runs for the warps that the GPU holds at once
+    const int64_t warps = (int64_t)sm_count() * kResident * kWarps, run = (p.tokens + warps - 1) / warps;
+    const int64_t ctas = (p.tokens + run * kWarps - 1) / (run * kWarps);
+    latent_append_kernel<<<(unsigned)ctas, kWarps * 32, 0, st>>>(p, (int)run);
     note_launch();
     return check_launch("latent_append_kernel");
 }

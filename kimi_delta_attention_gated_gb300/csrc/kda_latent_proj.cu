@@ -13,6 +13,7 @@
 // TMA through swizzled shared memory, which also cuts off the rows behind the last token.
 #include <cuda.h>
 
+#include <algorithm>
 #include <cstring>
 
 #include "kda_chunk_common.cuh"
@@ -31,6 +32,12 @@ constexpr float kNaN = __builtin_nanf("");
 
 __device__ int g_latent_product_timeouts = 0;
 
+struct Bars {
+    uint64_t full[4], empty[4], shared, done;
+    uint32_t tmem;
+    int abort;
+};
+
 // What: a LatentProduct.  The queries' sum has two K chunks of 64, which come in one go; the others'
 // eight come through a ring.
 template <int WHAT, int NT>
@@ -39,24 +46,17 @@ struct Cfg {
     static constexpr int CHUNKS = QUERIES ? 2 : 8;
     static constexpr uint32_t A = kBlock, B = NT * 128;  // bytes of a chunk's operands
     static constexpr int STAGES = QUERIES ? 2 : NT == 256 ? 2 : NT == 128 ? 3 : 4;
-    // the tile of shared channels: behind the operands (queries), or in the ring as one more A chunk (expand)
-    static constexpr uint32_t RING = STAGES * (A + B), SHARED = EXPAND ? (CHUNKS % STAGES) * (A + B) : RING;
-    static constexpr uint32_t BARS = RING + (QUERIES ? kBlock : 0);
+    // the expansion's tile of shared channels: in the ring, as one more A chunk
+    static constexpr uint32_t RING = STAGES * (A + B), SHARED = (CHUNKS % STAGES) * (A + B);
+    static constexpr uint32_t BARS = RING;
     static constexpr int OUT_BLOCKS = (NT + 63) / 64;
-    static constexpr uint32_t SMEM = BARS + 512 + 1024;
+    static constexpr uint32_t SMEM = BARS + sizeof(Bars) + 1024;
     // where output block i is put together: the operands are through, the shared channels are not
     __host__ __device__ static constexpr uint32_t out_at(int i) { return EXPAND ? kBlock * (i + 1) : kBlock * i; }
     static_assert(!EXPAND || (SHARED == 0 && kBlock * (OUT_BLOCKS + 1) <= RING), "the shared channels lie first");
     static_assert(kBlock * OUT_BLOCKS <= RING, "the output needs the operands' room");
 };
 
-struct Bars {
-    uint64_t full[8], empty[8], shared, done;
-    uint64_t turns[kShared / 2];  // of the pairs
-    uint32_t tmem;
-    int abort;
-};
-static_assert(sizeof(Bars) <= 512, "shared memory budget");
 
 __device__ __forceinline__ bool elect_one() {
     uint32_t ok;
@@ -94,6 +94,28 @@ __device__ __forceinline__ bool rows_any(bool x) {
 }
 __device__ __forceinline__ void rows_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
+// The queries' other channels, turned, in a launch of their own that runs beside the products': a CTA's tokens
+// have their angles formed once for all heads.  (In the products' CTAs, where each head's formed them
+// anew, this was a quarter of the time; among them in one launch its CTAs held their places.)
+constexpr int kTurnThreads = 256, kTurnTokens = 32;
+__global__ void __launch_bounds__(kTurnThreads) latent_turn_kernel(const __grid_constant__ LatentProductParams p, int tokens) {
+    __shared__ __align__(16) float2 cs[kTurnTokens * kShared / 2];  // [tokens][R / 2]
+    const int64_t t0 = (int64_t)blockIdx.x * tokens;
+    const int n = (int)min((int64_t)tokens, p.tokens - t0), np = p.rot.R >> 1, units = rotary_units(kShared, p.rot.R, p.rot.interleaved, 8);
+    if (np > 0) {
+        fill_cos_sin(cs, p.rot, n, [&](int t) { return __ldg(p.positions + t0 + t); }, threadIdx.x, kTurnThreads);
+        __syncthreads();
+    }
+    for (int i = threadIdx.x; i < n * p.H * units; i += kTurnThreads) {
+        const int row = i / units, u = i - row * units, t = row / p.H, h = row - t * p.H;
+        rotate_unit<__nv_bfloat16>(p.x + (t0 + t) * p.x_stride + (int64_t)h * kHeadQuery + kHeadKey,
+                                   p.out + ((t0 + t) * p.H + h) * kRow + kLatent, cs + t * np, u, p.rot.R, p.rot.interleaved,
+                                   p.rot.magnitude);
+    }
+    // It shares nothing with the products' launch, but must not end before that has.
+    if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 template <int WHAT, int NT>
 __global__ void __launch_bounds__(kThreads)
     latent_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
@@ -103,11 +125,12 @@ __global__ void __launch_bounds__(kThreads)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
+    if (F::QUERIES) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     Bars &b = *reinterpret_cast<Bars *>(sm + F::BARS);
+    const int cta = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int NTILES = F::QUERIES ? kLatent / NT : F::EXPAND ? 1 : kHeadValue / NT;
-    const int nt = blockIdx.x % NTILES, h = blockIdx.x / NTILES % p.H, t0 = blockIdx.x / NTILES / p.H * kTile;
-    const bool with_shared = F::EXPAND || (F::QUERIES && nt == 0);
+    const int nt = cta % NTILES, h = cta / NTILES % p.H, t0 = cta / NTILES / p.H * kTile;
     volatile int *abort_flag = &b.abort;
     if (threadIdx.x == 0) {
         for (int i = 0; i < F::STAGES; ++i) {
@@ -123,7 +146,6 @@ __global__ void __launch_bounds__(kThreads)
         tmem_alloc(&b.tmem, NT);
         tmem_relinquish();
     }
-    if (F::QUERIES && threadIdx.x < p.rot.R / 2) b.turns[threadIdx.x] = turn_of(__ldg(p.rot.inv_freq + threadIdx.x));
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -141,10 +163,6 @@ __global__ void __launch_bounds__(kThreads)
             bool ok = true;
             int issued = 0;
             const int xh = F::EXPAND ? 0 : h;
-            if (F::QUERIES && with_shared) {
-                mbar_arrive_expect_tx(&b.shared, kBlock);
-                tma_load_3d(sb + F::SHARED, &map_x, &b.shared, kHeadKey, xh, t0);
-            }
             for (int i = 0; i < F::CHUNKS; ++i) {
                 const int st = i % F::STAGES;
                 if (i >= F::STAGES && !(ok = wait(b.empty + st, (i / F::STAGES - 1) & 1, kAttnPolls))) break;
@@ -163,7 +181,7 @@ __global__ void __launch_bounds__(kThreads)
                 tma_load_3d(sb + F::SHARED, &map_x, &b.shared, kLatent, 0, t0);
             }
             // every copy lands before the CTA may end
-            if (with_shared && ok) mbar_wait(&b.shared, 0, kAttnPolls);
+            if (F::EXPAND && ok) mbar_wait(&b.shared, 0, kAttnPolls);
             for (int i = issued > F::STAGES ? issued - F::STAGES : 0; i < issued; ++i)
                 mbar_wait(b.full + i % F::STAGES, (i / F::STAGES) & 1, kAttnPolls);
         }
@@ -221,30 +239,9 @@ __global__ void __launch_bounds__(kThreads)
                         tma_store_3d(&map_out, sb + F::out_at(i), nt * NT + i * 64, h, t0);
                 }
             }
-            if (with_shared) {
+            if (F::EXPAND) {
                 ok = !rows_any(!wait(&b.shared, 0, kAttnPolls));
-                const int np = p.rot.R >> 1;
-                if (F::QUERIES && ok && np > 0) {
-                    if (t0 + row < p.tokens) {
-                        const uint64_t pos = (uint64_t)(int64_t)__ldg(p.positions + t0 + row);
-                        uint8_t *x = sm + F::SHARED + row * 128;
-                        auto at = [&](int ch) {
-                            return reinterpret_cast<__nv_bfloat16 *>(x + (((ch >> 3) ^ (row & 7)) << 4) + (ch & 7) * 2);
-                        };
-                        for (int j = 0; j < np; ++j) {
-                            float c, s, y0, y1;
-                            cos_sin_turn(pos * b.turns[j], c, s);
-                            __nv_bfloat16 *e0 = at(p.rot.interleaved ? 2 * j : j), *e1 = at(p.rot.interleaved ? 2 * j + 1 : j + np);
-                            turn_pair(__bfloat162float(*e0), __bfloat162float(*e1), make_float2(c, s * p.rot.sign),
-                                      p.rot.magnitude, y0, y1);
-                            *e0 = __float2bfloat16_rn(y0);
-                            *e1 = __float2bfloat16_rn(y1);
-                        }
-                    }
-                    fence_async_smem();
-                    rows_sync();
-                }
-                if (ok && threadIdx.x == 0) tma_store_3d(&map_out, sb + F::SHARED, F::EXPAND ? kHeadKey : kLatent, h, t0);
+                if (ok && threadIdx.x == 0) tma_store_3d(&map_out, sb + F::SHARED, kHeadKey, h, t0);
             }
             if (threadIdx.x == 0) {
                 bulk_commit();
@@ -267,8 +264,6 @@ __global__ void __launch_bounds__(kThreads)
             } else {
                 const int width = F::QUERIES ? kRow : kHeadValue;
                 for (int i = 0; i < NT; ++i) p.out[head * width + nt * NT + i] = nan;
-                if (with_shared)
-                    for (int i = 0; i < kShared; ++i) p.out[head * width + kLatent + i] = nan;
             }
         }
         if (threadIdx.x == 0) atomicAdd(&g_latent_product_timeouts, 1);
@@ -328,7 +323,27 @@ kda_status run(const LatentProductParams &p, cudaStream_t st) {
     }
     kernel<<<(unsigned)ctas, kThreads, F::SMEM, st>>>(mx, mw, mo, mo2, p);
     note_launch();
-    return check_launch("latent_product_kernel");
+    const kda_status s = check_launch("latent_product_kernel");
+    if (!F::QUERIES || s != KDA_OK) return s;
+    // about four units a thread
+    const int tokens = (int)std::max<int64_t>(1, std::min<int64_t>(kTurnTokens, 4 * kTurnThreads / (8 * p.H)));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.tokens + tokens - 1) / tokens));
+    cfg.blockDim = dim3(kTurnThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, latent_turn_kernel, p, tokens);
+    note_launch();
+    if (e != cudaSuccess) {
+        set_error("latent_turn_kernel: %s", cudaGetErrorString(e));
+        cudaGetLastError();
+        return KDA_ERR_CUDA;
+    }
+    return check_launch("latent_turn_kernel");
 }
 
 }  // namespace
@@ -353,7 +368,9 @@ kda_status launch_latent_product(const LatentProductParams &p, cudaStream_t st) 
     const int64_t wide = (p.tokens + kTile - 1) / kTile * p.H;
     if (p.what == kLatentExpand) return run<kLatentExpand, 256>(p, st);
     if (p.what == kLatentQueries)
-        return wide * 4 < sm_count() ? run<kLatentQueries, 64>(p, st) : run<kLatentQueries, 128>(p, st);
+        return wide * 4 < sm_count() ? run<kLatentQueries, 64>(p, st)
+               : wide < sm_count()   ? run<kLatentQueries, 128>(p, st)
+                                     : run<kLatentQueries, 256>(p, st);
     return wide < sm_count() ? run<kLatentValues, 64>(p, st) : run<kLatentValues, 128>(p, st);
 }
 
