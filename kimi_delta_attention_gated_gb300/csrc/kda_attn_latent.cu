@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Plan &pl = a.plan;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t sb = smem_u32(sm), sb16 = sb >> 4;
+    const uint32_t sb = smem_u32(sm), sb16 = (sb & 0x3FFFF) >> 4;
     Bars &b = *reinterpret_cast<Bars *>(sm + pl.at_bars);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int piece = blockIdx.x / pl.G, g = blockIdx.x - piece * pl.G;
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY, l = 0.f;
             for (int s = 0; s < nt; ++s, ++blocks) {
                 const int j0 = (it.s0 + s) * kStep;
-                ok = wait(b.s_full + (blocks & 1), (blocks >> 1) & 1);
+                ok = ok && wait(b.s_full + (blocks & 1), (blocks >> 1) & 1);
                 fence_after_sync();
                 float x[kHalf];
                 tmem_ld_halves(tb + lane_base + (blocks & 1) * kStep, x);
@@ -693,10 +693,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 const float mb = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], 16)) * c;
                 const bool raise = mb > m + kSlack;  // (rows that are not live: never)
-                if (blocks > 0) {  // the last weights are multiplied
-                    ok = ok && wait(&b.p_free, (blocks - 1) & 1);
-                    fence_after_sync();
-                }
                 if (soft_any(raise || !ok)) {
                     if (soft_any(!ok)) {
                         ok = false;
@@ -706,8 +702,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (raise) m = mb;
                     l *= f;
                     if (s > 0) {
+                        ok = wait(&b.p_free, (blocks - 1) & 1);  // O holds all steps before
+                        fence_after_sync();
                         if (mine) b.factor[row] = f;
-                        soft_sync();
+                        if (soft_any(!ok)) {
+                            ok = false;
+                            break;
+                        }
 #pragma unroll 1
                         for (int r0 = 0; r0 < pl.n; r0 += 16) {
 #pragma unroll 1
@@ -738,6 +739,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     w[i / 2] = pack_bf16x2(e0, e1);
                 }
                 l += sum[0] + sum[1];
+                // the last weights have to be multiplied before these take their place
+                if (blocks > 0) ok = wait(&b.p_free, (blocks - 1) & 1);
+                if (!ok) continue;  // (said to the other warps at the next barrier)
                 if (row < pl.n) {
                     const uint32_t at = sb + pl.at_p + row * 128;
 #pragma unroll
@@ -788,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             // ---- output
             if (nt > 0) {
-                ok = wait(&b.p_free, (blocks - 1) & 1);
+                ok = ok && wait(&b.p_free, (blocks - 1) & 1);
                 fence_after_sync();
             }
             // (also: the last item's places and factors are read)
