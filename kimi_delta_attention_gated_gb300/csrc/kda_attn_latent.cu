@@ -41,8 +41,8 @@ using namespace tc;
 
 constexpr int kStep = 64;               // cached tokens of a step
 constexpr int kTileRows = 64;           // query rows of a tile at most
-constexpr int kSoftWarps = 4, kScoreWarp = 4, kValueWarp = 5, kLoadWarp = 6;
-constexpr int kThreads = 224;
+constexpr int kSoftWarps = 4, kScoreWarp = 4, kValueWarp = 5, kLoadWarp = 6;  // (and the one behind)
+constexpr int kThreads = 256;
 constexpr int kSlots = 4;               // work items under way
 constexpr int kPad = 2;                 // a unit's own cost in steps, where pieces have kPadFrom steps or more
 constexpr int kPadFrom = 4;
@@ -53,6 +53,7 @@ constexpr float kSlack = 8.f;           // log2: how far a score may exceed the 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNaN = __builtin_nanf("");
 constexpr int kMaxSmem = 232448;
+constexpr uint32_t kLastPolls = 256;    // for copies after a failure: a millisecond
 
 __device__ int g_attn_latent_timeouts = 0;
 
@@ -154,6 +155,26 @@ __device__ __forceinline__ void store_if(bool x, void *p, float v) {
 // the row groups are 1024 bytes apart.
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
     return (uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32 | lo;
+}
+// mbar_try_wait, mbar_arrive_expect_tx and a copy, the barrier by its shared-memory address.
+__device__ __forceinline__ bool try_at(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void expect_at(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tma_at(uint32_t dst, const void *tmap, uint32_t bar, int row, int block) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(0), "r"(row), "r"(block), "r"(bar)
+        : "memory");
 }
 // A barrier of the softmax's warps that also says whether any of their threads has `x`.
 __device__ __forceinline__ bool soft_any(bool x) {
@@ -439,106 +460,129 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 1;
         return false;
     };
+    auto wait_at = [&](uint32_t bar, uint32_t parity) {
+        for (uint32_t i = 0; i < kAttnPolls; ++i) {
+            if (try_at(bar, parity)) return true;
+            if (*abort_flag) break;
+        }
+        *abort_flag = 1;
+        return false;
+    };
     // All lanes of a warp go on or stop together.
     auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(bar, parity, kAttnPolls)) != 0; };
 
-    if (warp == kLoadWarp) {
-        // ---- work items, and the copies of the cache, from one thread: a step's copies have to be issued in
-        // less than its time (with the warp's votes about each wait and two copies a unit they took 2900
-        // cycles and were the bound)
+    if (warp >= kLoadWarp) {
+        // ---- work items, and the copies of the cache, from a thread of each of two warps: the first has a step's
+        // shared channels and units 0 and 1, the second the other two.  A thread by itself issues an instruction
+        // every five cycles or so, and the copies of a step took one thread 2200 cycles, the warp's votes about
+        // each wait and two copies a unit 2900; either was the bound.
         if (elect_one()) {
+            const int half = warp - kLoadWarp;
             Walk w;
             w.start(a, L0, L1, S, pad, start_seq, start_begin, start_unit);
-            uint32_t nu = 0, nr = 0;                  // units and shared units so far
-            uint32_t us = 0, up = 1, rs = 0, rp = 1;  // ring places, and the parity of the wait for them
+            uint32_t us = 0, up = 1;           // ring place of the step's first unit, and the parity of the wait for it (a
+                                               // barrier's phase before its first counts as over)
+            uint32_t rs = 0, rp = 1, steps = 0;
             bool ok = true;
-            const int sub = min(kStep, p.c.P), per_step = kStep / sub;                         // rows of a copy
-            const int in_page = p.c.p_shift - (sub == 16 ? 4 : sub == 32 ? 5 : 6);             // log2 of a page's copies
+            const uint32_t at_full = smem_u32(b.u_full), at_empty = smem_u32(b.u_empty), to_units = sb + pl.at_units;
+            const int sub = min(kStep, p.c.P), per_step = kStep / sub;              // rows of a copy
+            const int in_page = p.c.p_shift - (sub == 16 ? 4 : sub == 32 ? 5 : 6);  // log2 of a page's copies
+            const int page_mask = (1 << in_page) - 1, sub_shift = p.c.p_shift - in_page;
             // Page numbers of a step's copies, looked up a step ahead (an item's first while the one before is
             // copied).  kNone: behind what the tile needs.
             constexpr int kNone = INT_MIN;
             struct Pages {
                 int at[4];
             };
-            auto look_up = [&](const Item &it, int s) {
+            auto look_up = [&](const int32_t *table, int need, int s) {
                 Pages q;
-                const int last = min(it.seen0 + it.tokens - 1, it.s1 * kStep);  // tokens that the tile needs
-                const int32_t *table = p.c.block_table + (int64_t)it.seq * p.c.max_blocks;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int i = s * per_step + j;
                     q.at[j] = kNone;
-                    if (j < per_step && it.found && s < it.s1 && i * sub < last) {
+                    if (j < per_step && i < need) {
                         const int page = __ldg(table + (i >> in_page));
-                        q.at[j] = page == kNone ? -1 : page;
+                        q.at[j] = (uint32_t)page < (uint32_t)p.c.n_pages ? page : -1;
                     }
                 }
                 return q;
             };
-            Item ahead = w.next(a, piece, g, true);
-            Pages first = look_up(ahead, ahead.s0);
+            auto table_of = [&](const Item &it) { return p.c.block_table + (int64_t)it.seq * p.c.max_blocks; };
+            // Copies that the tile needs, from the sequence's first.
+            auto need_of = [&](const Item &it) {
+                return it.found && it.s1 > it.s0 ? (min(it.seen0 + it.tokens - 1, it.s1 * kStep) + sub - 1) >> sub_shift : 0;
+            };
+            Item ahead = w.next(a, piece, g, half == 0);
+            Pages first = look_up(table_of(ahead), need_of(ahead), ahead.s0);
             for (uint32_t k = 0; ok; ++k) {
                 const Item it = ahead;
                 Pages pages = first;
                 const int slot = k % kSlots;
-                if (k >= kSlots) ok = wait_for(b.i_empty + slot, (k / kSlots - 1) & 1, kAttnPolls);
-                if (!ok) break;
-                b.slots[slot] = it;
-                mbar_arrive(b.i_full + slot);
+                if (half == 0) {
+                    if (k >= kSlots) ok = wait_for(b.i_empty + slot, (k / kSlots - 1) & 1, kAttnPolls);
+                    if (!ok) break;
+                    b.slots[slot] = it;
+                    mbar_arrive(b.i_full + slot);
+                }
                 if (!it.found) break;
-                ahead = w.next(a, piece, g, true);
-                first = look_up(ahead, ahead.s0);
-                for (int s = it.s0; s < it.s1 && ok; ++s) {
-                    int at[4], n_sub = 0;  // rows of the cache, -1: nothing to copy
+                ahead = w.next(a, piece, g, half == 0);
+                first = look_up(table_of(ahead), need_of(ahead), ahead.s0);
+                const int32_t *table = table_of(it);
+                const int need = need_of(it);
+                for (int s = it.s0; s < it.s1 && ok; ++s, ++steps) {
+                    int at[4], bytes = 0;  // rows of the cache, -1: nothing to copy; of a block of 64 channels
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        at[j] = -1;
-                        if (pages.at[j] == kNone) continue;
-                        if ((uint32_t)pages.at[j] >= (uint32_t)p.c.n_pages) {
-                            *(volatile int *)&b.slots[slot].bad = 1;
-                            continue;
-                        }
-                        at[j] = (pages.at[j] << p.c.p_shift) + (((s * per_step + j) << (p.c.p_shift - in_page)) & (p.c.P - 1));
-                        ++n_sub;
+                        const int page = pages.at[j];
+                        at[j] = page < 0 ? -1 : (page << p.c.p_shift) + (((s * per_step + j) & page_mask) << sub_shift);
+                        bytes += page < 0 ? 0 : 128 << sub_shift;
+                        if (page < 0 && page != kNone && half == 0) *(volatile int *)&b.slots[slot].bad = 1;
                     }
-                    pages = look_up(it, s + 1);
-                    // the shared channels first: their scores come first
-                    ok = nr < (uint32_t)pl.shared || wait_for(b.r_empty + rs, rp, kAttnPolls);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(b.r_full + rs, n_sub * sub * 128);
-                    const uint32_t r_to = sb + pl.at_shared + rs * kSharedBytes;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (at[j] >= 0) tma_load_3d(r_to + j * sub * 128, &map_r, b.r_full + rs, 0, at[j], kLatent / 64);
-                    ++nr;
-                    if (++rs == (uint32_t)pl.shared) rs = 0, rp ^= 1;
-#pragma unroll 1
-                    for (int m = 0; m < 4; ++m) {
-                        ok = nu < (uint32_t)pl.units || wait_for(b.u_empty + us, up, kAttnPolls);
+                    pages = look_up(table, need, s + 1);
+                    if (half == 0) {  // (the shared channels first: their scores come first)
+                        ok = wait_for(b.r_empty + rs, rp, kAttnPolls);
                         if (!ok) break;
-                        mbar_arrive_expect_tx(b.u_full + us, n_sub * sub * 256);
-                        const uint32_t u_to = sb + pl.at_units + us * kUnitBytes;
+                        mbar_arrive_expect_tx(b.r_full + rs, bytes);
+                        const uint32_t to = sb + pl.at_shared + rs * kSharedBytes;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (at[j] >= 0) tma_load_3d(to + j * sub * 128, &map_r, b.r_full + rs, 0, at[j], kLatent / 64);
+                        if (++rs == (uint32_t)pl.shared) rs = 0, rp ^= 1;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int m = 2 * half + i;
+                        uint32_t place = us + m, parity = up;
+                        if (place >= (uint32_t)pl.units) place -= pl.units, parity ^= 1;
+                        ok = ok && wait_at(at_empty + place * 8, parity);
+                        if (!ok) break;
+                        const uint32_t full = at_full + place * 8, to = to_units + place * kUnitBytes;
+                        expect_at(full, 2 * bytes);
                         if (per_step == 1) {  // both blocks of 64 channels at once
-                            if (at[0] >= 0) tma_load_3d(u_to, &map_c, b.u_full + us, 0, at[0], 2 * m);
+                            if (at[0] >= 0) tma_at(to, &map_c, full, at[0], 2 * m);
                         } else {
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 if (at[j] >= 0) {
-                                    tma_load_3d(u_to + j * sub * 128, &map_r, b.u_full + us, 0, at[j], 2 * m);
-                                    tma_load_3d(u_to + kSharedBytes + j * sub * 128, &map_r, b.u_full + us, 0, at[j], 2 * m + 1);
+                                    tma_at(to + j * sub * 128, &map_r, full, at[j], 2 * m);
+                                    tma_at(to + kSharedBytes + j * sub * 128, &map_r, full, at[j], 2 * m + 1);
                                 }
                         }
-                        ++nu;
-                        if (++us == (uint32_t)pl.units) us = 0, up ^= 1;
                     }
+                    if (!ok) break;
+                    us += 4;
+                    if (us >= (uint32_t)pl.units) us -= pl.units, up ^= 1;
                 }
             }
-            if (pl.cut && ok) last_words(w);
-            // every copy lands before the CTA may end
-            for (uint32_t j = nr > (uint32_t)pl.shared ? nr - pl.shared : 0; j < nr; ++j)
-                mbar_wait(b.r_full + j % pl.shared, (j / pl.shared) & 1, kAttnPolls);
-            for (uint32_t j = nu > (uint32_t)pl.units ? nu - pl.units : 0; j < nu; ++j)
-                mbar_wait(b.u_full + j % pl.units, (j / pl.units) & 1, kAttnPolls);
+            if (half == 0 && pl.cut && ok) last_words(w);
+            // every copy lands before the CTA may end (after a failure within a step, those of that step may not have
+            // been issued: their wait runs out)
+            if (half == 0)
+                for (uint32_t j = steps > (uint32_t)pl.shared ? steps - pl.shared : 0; j < steps + !ok; ++j)
+                    mbar_wait(b.r_full + j % pl.shared, (j / pl.shared) & 1, ok ? kAttnPolls : kLastPolls);
+            const uint32_t fills = 4 * (steps + !ok), units = pl.units;
+            for (uint32_t j = fills > units ? fills - units : 0; j < fills; ++j)
+                if ((int)(j & 3) >> 1 == half) mbar_wait(b.u_full + j % units, (j / units) & 1, ok ? kAttnPolls : kLastPolls);
         }
         __syncwarp();
     } else if (warp == kScoreWarp || warp == kValueWarp) {
