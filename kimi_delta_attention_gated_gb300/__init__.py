@@ -1004,15 +1004,34 @@ def _latent_cache_args(cache):
     return index, (at, pages, P)
 
 
+def _latent_rows(t, name, index):
+    """[tokens, 576] bf16 on device `index`, rows a 16-byte multiple apart (else copied) -> (tensor,
+    address, tokens, stride)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.get_device() != index or t.dim() != 2:
+        _refuse(t, name, torch.bfloat16, 2, index)
+    n, d = t.shape
+    if d != LATENT_ROW:
+        raise ValueError(f"{name} must be [tokens, {LATENT_ROW}]")
+    s0, s1 = t.stride()
+    at = t.data_ptr()
+    if at % 16 or s1 != 1 or s0 % 8 or (s0 < d and n > 1):
+        t = t.clone(memory_format=torch.contiguous_format)
+        return t, t.data_ptr(), n, d
+    return t, at, n, max(s0, d)
+
+
 def _latent_weight(w_kv, heads, index):
-    """w_kv [H, 256, 512], or the projection's weight [H * 256, 512] -> its address."""
-    if isinstance(w_kv, torch.Tensor) and w_kv.dim() == 2 and w_kv.shape[0] % (LATENT_KEY + LATENT_VALUE) == 0:
-        w_kv = w_kv.unflatten(0, (-1, LATENT_KEY + LATENT_VALUE))
-    at = _dense(w_kv, "w_kv", torch.bfloat16, 3, index)
-    if tuple(w_kv.shape[1:]) != (LATENT_KEY + LATENT_VALUE, LATENT_DIM) or heads not in (None, w_kv.shape[0]):
+    """w_kv [H, 256, 512], or the projection's weight [H * 256, 512] -> (address, H)."""
+    dim = w_kv.dim() if isinstance(w_kv, torch.Tensor) else 3
+    at = _dense(w_kv, "w_kv", torch.bfloat16, 2 if dim == 2 else 3, index)
+    shape = w_kv.shape
+    rows = shape[0] if dim == 2 else shape[0] * shape[1]
+    H = rows // (LATENT_KEY + LATENT_VALUE)
+    if (shape[-1] != LATENT_DIM or rows != H * (LATENT_KEY + LATENT_VALUE) or (dim == 3 and shape[0] != H)
+            or (heads is not None and heads != H)):
         raise ValueError(f"w_kv must be [heads, {LATENT_KEY + LATENT_VALUE}, {LATENT_DIM}], a head's key rows before its "
                          "value rows")
-    return at, w_kv.shape[0]
+    return at, H
 
 
 def _latent_out(out, name, shape, device, index):
@@ -1039,10 +1058,7 @@ def latent_append(x, cache, block_table, context_lens, *, cu_seqlens=None, norm_
     lib = _lib or _load()
     lay = _layout(layout)
     index, cache_args = _latent_cache_args(cache)
-    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != LATENT_ROW:
-        raise ValueError(f"x must be [tokens, {LATENT_ROW}]")
-    x, xp, x_stride = _rows(x.unsqueeze(1), "x", torch.bfloat16, index)
-    T = x.shape[0]
+    x, xp, T, x_stride = _latent_rows(x, "x", index)
     table = _dense(block_table, "block_table", torch.int32, 2, index)
     ctx = _dense(context_lens, "context_lens", torch.int32, 1, index)
     N, max_blocks = block_table.shape
@@ -1185,10 +1201,7 @@ def latent_expand(rows, w_kv, *, k_out=None, v_out=None):
         dev = _device_of(w_kv)
         return _to_host(latent_expand(_prep(rows, dev), _prep(w_kv, dev)), True, (k_out, v_out))
     index = rows.get_device()
-    if rows.dim() != 2 or rows.shape[1] != LATENT_ROW:
-        raise ValueError(f"rows must be [tokens, {LATENT_ROW}]")
-    rows, rp, r_stride = _rows(rows.unsqueeze(1), "rows", torch.bfloat16, index)
-    T = rows.shape[0]
+    rows, rp, T, r_stride = _latent_rows(rows, "rows", index)
     w, H = _latent_weight(w_kv, None, index)
     k, kp = _latent_out(k_out, "k_out", (T, H, LATENT_QUERY), rows.device, index)
     v, vp = _latent_out(v_out, "v_out", (T, H, LATENT_VALUE), rows.device, index)

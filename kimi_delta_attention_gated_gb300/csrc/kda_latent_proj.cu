@@ -94,24 +94,31 @@ __device__ __forceinline__ bool rows_any(bool x) {
 }
 __device__ __forceinline__ void rows_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
-// The queries' other channels, turned, in a launch of their own that runs beside the products': a CTA's tokens
-// have their angles formed once for all heads.  (In the products' CTAs, where each head's formed them
-// anew, this was a quarter of the time; among them in one launch its CTAs held their places.)
-constexpr int kTurnThreads = 256, kTurnTokens = 32;
-__global__ void __launch_bounds__(kTurnThreads) latent_turn_kernel(const __grid_constant__ LatentProductParams p, int tokens) {
-    __shared__ __align__(16) float2 cs[kTurnTokens * kShared / 2];  // [tokens][R / 2]
-    const int64_t t0 = (int64_t)blockIdx.x * tokens;
+// The queries' other channels, turned: a CTA's tokens have their angles formed once for all heads.  (In the
+// products' CTAs, where each head's formed them anew, this was a quarter of the time.)
+constexpr int kTurnTokens = 32;
+template <int THREADS>
+__device__ __forceinline__ void turn_shared(const LatentProductParams &p, int tile, int tokens, float2 *cs) {  // [tokens][R / 2]
+    const int64_t t0 = (int64_t)tile * tokens;
     const int n = (int)min((int64_t)tokens, p.tokens - t0), np = p.rot.R >> 1, units = rotary_units(kShared, p.rot.R, p.rot.interleaved, 8);
     if (np > 0) {
-        fill_cos_sin(cs, p.rot, n, [&](int t) { return __ldg(p.positions + t0 + t); }, threadIdx.x, kTurnThreads);
+        fill_cos_sin(cs, p.rot, n, [&](int t) { return __ldg(p.positions + t0 + t); }, threadIdx.x, THREADS);
         __syncthreads();
     }
-    for (int i = threadIdx.x; i < n * p.H * units; i += kTurnThreads) {
+    for (int i = threadIdx.x; i < n * p.H * units; i += THREADS) {
         const int row = i / units, u = i - row * units, t = row / p.H, h = row - t * p.H;
         rotate_unit<__nv_bfloat16>(p.x + (t0 + t) * p.x_stride + (int64_t)h * kHeadQuery + kHeadKey,
                                    p.out + ((t0 + t) * p.H + h) * kRow + kLatent, cs + t * np, u, p.rot.R, p.rot.interleaved,
                                    p.rot.magnitude);
     }
+}
+// In a launch of its own that runs beside the products': among their CTAs in one launch the turning ones
+// would hold places that the products want (256 tokens, 128 heads: 27 and 15 us).  Where all fit the GPU at once
+// it is one launch, which costs less on the host.
+constexpr int kTurnThreads = 256;
+__global__ void __launch_bounds__(kTurnThreads) latent_turn_kernel(const __grid_constant__ LatentProductParams p, int tokens) {
+    __shared__ __align__(16) float2 cs[kTurnTokens * kShared / 2];
+    turn_shared<kTurnThreads>(p, blockIdx.x, tokens, cs);
     // It shares nothing with the products' launch, but must not end before that has.
     if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -120,12 +127,18 @@ template <int WHAT, int NT>
 __global__ void __launch_bounds__(kThreads)
     latent_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                           const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_out2,
-                          const __grid_constant__ LatentProductParams p) {
+                          const __grid_constant__ LatentProductParams p, int turn_from, int turn_tokens) {
     using F = Cfg<WHAT, NT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
-    if (F::QUERIES) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (F::QUERIES) {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        if ((int)blockIdx.x >= turn_from) {
+            turn_shared<kThreads>(p, blockIdx.x - turn_from, turn_tokens, reinterpret_cast<float2 *>(sm));
+            return;
+        }
+    }
     Bars &b = *reinterpret_cast<Bars *>(sm + F::BARS);
     const int cta = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -294,7 +307,8 @@ kda_status run(const LatentProductParams &p, cudaStream_t st) {
         set_error("latent product: cuTensorMapEncodeTiled is not available from the driver");
         return KDA_ERR_CUDA;
     }
-    CUtensorMap mx, mw, mo, mo2;
+    CUtensorMap mx, mw, mo, mo2;  // (mo2: the expansion's values)
+    if (!F::EXPAND) memset(&mo2, 0, sizeof(mo2));
     const int dim = F::QUERIES ? kHeadQuery : F::EXPAND ? kRow : kLatent, out = F::QUERIES ? kRow : F::EXPAND ? kHeadQuery : kHeadValue;
     const int heads = F::EXPAND ? 1 : p.H;
     // W as [heads, 256 rows, 512 channels]: 64 channels of 64 (queries) or NT rows of a head
@@ -302,8 +316,7 @@ kda_status run(const LatentProductParams &p, cudaStream_t st) {
         !encode(enc, &mw, p.w, kLatent, kHeadKey + kHeadValue, p.H, kLatent, (int64_t)(kHeadKey + kHeadValue) * kLatent,
                 F::QUERIES ? 64 : NT, 1) ||
         !encode(enc, &mo, p.out, out, p.H, p.tokens, out, (int64_t)p.H * out, 1, kTile) ||
-        !encode(enc, &mo2, F::EXPAND ? p.out2 : p.out, F::EXPAND ? kHeadValue : out, p.H, p.tokens, F::EXPAND ? kHeadValue : out,
-                (int64_t)p.H * (F::EXPAND ? kHeadValue : out), 1, kTile))
+        (F::EXPAND && !encode(enc, &mo2, p.out2, kHeadValue, p.H, p.tokens, kHeadValue, (int64_t)p.H * kHeadValue, 1, kTile)))
         return KDA_ERR_CUDA;
     static DeviceOnce configured;
     const int dev = current_device();
@@ -321,14 +334,16 @@ kda_status run(const LatentProductParams &p, cudaStream_t st) {
         set_error("latent product: too many tokens");
         return KDA_ERR_UNSUPPORTED;
     }
-    kernel<<<(unsigned)ctas, kThreads, F::SMEM, st>>>(mx, mw, mo, mo2, p);
+    // turning CTAs with about four units a thread
+    const int tokens = (int)std::max<int64_t>(1, std::min<int64_t>(kTurnTokens, 4 * kTurnThreads / (8 * p.H)));
+    const int64_t turn_ctas = F::QUERIES ? (p.tokens + tokens - 1) / tokens : 0;
+    const bool together = ctas + turn_ctas <= sm_count();
+    kernel<<<(unsigned)(ctas + (together ? turn_ctas : 0)), kThreads, F::SMEM, st>>>(mx, mw, mo, mo2, p, (int)ctas, tokens);
     note_launch();
     const kda_status s = check_launch("latent_product_kernel");
-    if (!F::QUERIES || s != KDA_OK) return s;
-    // about four units a thread
-    const int tokens = (int)std::max<int64_t>(1, std::min<int64_t>(kTurnTokens, 4 * kTurnThreads / (8 * p.H)));
+    if (!F::QUERIES || together || s != KDA_OK) return s;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.tokens + tokens - 1) / tokens));
+    cfg.gridDim = dim3((unsigned)turn_ctas);
     cfg.blockDim = dim3(kTurnThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
