@@ -49,11 +49,13 @@ struct Cfg {
     // the expansion's tile of shared channels: in the ring, as one more A chunk
     static constexpr uint32_t RING = STAGES * (A + B), SHARED = (CHUNKS % STAGES) * (A + B);
     static constexpr uint32_t BARS = RING;
-    static constexpr int OUT_BLOCKS = (NT + 63) / 64;
+    static constexpr int OUT_BLOCKS = NT / 64;
+    static constexpr int NTILES = (QUERIES ? kLatent : EXPAND ? kHeadKey + kHeadValue : kHeadValue) / NT;  // of a head
     static constexpr uint32_t SMEM = BARS + sizeof(Bars) + 1024;
-    // where output block i is put together: the operands are through, the shared channels are not
+    // where output block i is put together: the operands are through, the expansion's shared channels are not
     __host__ __device__ static constexpr uint32_t out_at(int i) { return EXPAND ? kBlock * (i + 1) : kBlock * i; }
-    static_assert(!EXPAND || (SHARED == 0 && kBlock * (OUT_BLOCKS + 1) <= RING), "the shared channels lie first");
+    static_assert(!EXPAND || (kBlock * (OUT_BLOCKS + 1) <= RING && (SHARED == 0 || SHARED >= kBlock * (OUT_BLOCKS + 1))),
+                  "the shared channels and the output lie apart");
     static_assert(kBlock * OUT_BLOCKS <= RING, "the output needs the operands' room");
 };
 
@@ -142,8 +144,9 @@ __global__ void __launch_bounds__(kThreads)
     Bars &b = *reinterpret_cast<Bars *>(sm + F::BARS);
     const int cta = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int NTILES = F::QUERIES ? kLatent / NT : F::EXPAND ? 1 : kHeadValue / NT;
+    constexpr int NTILES = F::NTILES;
     const int nt = cta % NTILES, h = cta / NTILES % p.H, t0 = cta / NTILES / p.H * kTile;
+    const bool with_shared = F::EXPAND && nt == 0;
     volatile int *abort_flag = &b.abort;
     if (threadIdx.x == 0) {
         for (int i = 0; i < F::STAGES; ++i) {
@@ -186,15 +189,15 @@ __global__ void __launch_bounds__(kThreads)
                     for (int x = 0; x < NT / 64; ++x)
                         tma_load_3d(at + F::A + x * 64 * 128, &map_w, b.full + st, nt * NT + x * 64, i * 64, h);
                 else
-                    tma_load_3d(at + F::A, &map_w, b.full + st, i * 64, F::EXPAND ? 0 : kHeadKey + nt * NT, h);
+                    tma_load_3d(at + F::A, &map_w, b.full + st, i * 64, (F::EXPAND ? 0 : kHeadKey) + nt * NT, h);
                 ++issued;
             }
-            if (F::EXPAND && ok && (ok = wait(b.empty + F::CHUNKS % F::STAGES, (F::CHUNKS / F::STAGES - 1) & 1, kAttnPolls))) {
+            if (with_shared && ok && (ok = wait(b.empty + F::CHUNKS % F::STAGES, (F::CHUNKS / F::STAGES - 1) & 1, kAttnPolls))) {
                 mbar_arrive_expect_tx(&b.shared, kBlock);
                 tma_load_3d(sb + F::SHARED, &map_x, &b.shared, kLatent, 0, t0);
             }
             // every copy lands before the CTA may end
-            if (F::EXPAND && ok) mbar_wait(&b.shared, 0, kAttnPolls);
+            if (with_shared && ok) mbar_wait(&b.shared, 0, kAttnPolls);
             for (int i = issued > F::STAGES ? issued - F::STAGES : 0; i < issued; ++i)
                 mbar_wait(b.full + i % F::STAGES, (i / F::STAGES) & 1, kAttnPolls);
         }
@@ -246,13 +249,14 @@ __global__ void __launch_bounds__(kThreads)
                 fence_async_smem();
                 rows_sync();
                 if (threadIdx.x == 0) {
-                    if (F::EXPAND && i >= 2)
-                        tma_store_3d(&map_out2, sb + F::out_at(i), (i - 2) * 64, h, t0);
+                    const int ch = nt * NT + i * 64;
+                    if (F::EXPAND && ch >= kHeadKey)
+                        tma_store_3d(&map_out2, sb + F::out_at(i), ch - kHeadKey, h, t0);
                     else
-                        tma_store_3d(&map_out, sb + F::out_at(i), nt * NT + i * 64, h, t0);
+                        tma_store_3d(&map_out, sb + F::out_at(i), ch, h, t0);
                 }
             }
-            if (F::EXPAND) {
+            if (with_shared) {
                 ok = !rows_any(!wait(&b.shared, 0, kAttnPolls));
                 if (ok && threadIdx.x == 0) tma_store_3d(&map_out, sb + F::SHARED, kHeadKey, h, t0);
             }
@@ -272,8 +276,9 @@ __global__ void __launch_bounds__(kThreads)
         for (int r = threadIdx.x; r < kTile && t0 + r < p.tokens; r += kThreads) {
             const int64_t head = (int64_t)(t0 + r) * p.H + h;
             if (F::EXPAND) {
-                for (int i = 0; i < kHeadQuery; ++i) p.out[head * kHeadQuery + i] = nan;
-                for (int i = 0; i < kHeadValue; ++i) p.out2[head * kHeadValue + i] = nan;
+                for (int i = nt * NT; i < nt * NT + NT; ++i)
+                    *(i < kHeadKey ? p.out + head * kHeadQuery + i : p.out2 + head * kHeadValue + i - kHeadKey) = nan;
+                for (int i = kHeadKey; i < kHeadQuery && with_shared; ++i) p.out[head * kHeadQuery + i] = nan;
             } else {
                 const int width = F::QUERIES ? kRow : kHeadValue;
                 for (int i = 0; i < NT; ++i) p.out[head * width + nt * NT + i] = nan;
@@ -328,8 +333,7 @@ kda_status run(const LatentProductParams &p, cudaStream_t st) {
         }
         configured.set(dev);
     }
-    const int64_t ntiles = F::QUERIES ? kLatent / NT : F::EXPAND ? 1 : kHeadValue / NT;
-    const int64_t ctas = (p.tokens + kTile - 1) / kTile * p.H * ntiles;
+    const int64_t ctas = (p.tokens + kTile - 1) / kTile * p.H * F::NTILES;
     if (ctas > INT32_MAX || p.tokens > (1 << 30)) {
         set_error("latent product: too many tokens");
         return KDA_ERR_UNSUPPORTED;
@@ -381,7 +385,10 @@ kda_status launch_latent_product(const LatentProductParams &p, cudaStream_t st) 
     if (p.tokens == 0) return KDA_OK;
     // narrow tiles where wide ones would leave SMs without one
     const int64_t wide = (p.tokens + kTile - 1) / kTile * p.H;
-    if (p.what == kLatentExpand) return run<kLatentExpand, 256>(p, st);
+    if (p.what == kLatentExpand)
+        return wide * 2 < sm_count() ? run<kLatentExpand, 64>(p, st)
+               : wide < sm_count()   ? run<kLatentExpand, 128>(p, st)
+                                     : run<kLatentExpand, 256>(p, st);
     if (p.what == kLatentQueries)
         return wide * 4 < sm_count() ? run<kLatentQueries, 64>(p, st)
                : wide < sm_count()   ? run<kLatentQueries, 128>(p, st)
