@@ -393,6 +393,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         b.abort = 0;
         b.start_seq = -1;
     }
+    if (warp == kLoadWarp && lane < 3)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &map_q : lane == 1 ? &map_c : &map_r) : "memory");
+    if (warp == kScoreWarp) {
+        tmem_alloc(&b.tmem, 512);
+        tmem_relinquish();
+    }
+    // What is above overlaps the end of the launch before; from here on its results are read.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == kLoadWarp && !pl.cut && !p.cu_seqlens) {
         // the length and the first pages on their way, while the rest is set up
         const int n = piece / pl.units_one;
@@ -400,12 +408,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(x) : "l"(p.c.lens + n));
         if (lane < p.c.max_blocks) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(y) : "l"(p.c.block_table + (int64_t)n * p.c.max_blocks + lane));
         asm volatile("" ::"r"(x), "r"(y));
-    }
-    if (warp == kLoadWarp && lane < 3)
-        asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &map_q : lane == 1 ? &map_c : &map_r) : "memory");
-    if (warp == kScoreWarp) {
-        tmem_alloc(&b.tmem, 512);
-        tmem_relinquish();
     }
     // The piece: places of the line, or without cuts units.
     int64_t L0 = piece, L1 = piece + 1, S = 1;
@@ -1159,23 +1161,31 @@ kda_status launch_attn_latent(const AttnLatentParams &p, cudaStream_t st) {
         }
         configured.set(dev);
     }
-    attn_latent_kernel<<<pl.pieces * pl.G, kThreads, kMaxSmem, st>>>(mq, mc, mr, a);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];  // either launch starts while the one before ends, and waits for it before it reads
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(pl.pieces * pl.G);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kMaxSmem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, attn_latent_kernel, mq, mc, mr, a);
     note_launch();
+    if (e != cudaSuccess) {
+        set_error("attn_latent_kernel: %s", cudaGetErrorString(e));
+        cudaGetLastError();
+        return KDA_ERR_CUDA;
+    }
     kda_status s = check_launch("attn_latent_kernel");
     if (!pl.cut || s != KDA_OK) return s;
-    cudaLaunchConfig_t cfg = {};
     // with many pieces a unit more warps share them
     const int shares = pl.pieces >= 16 * pl.most_units ? kMaxShares : 1;
     cfg.gridDim = dim3((unsigned)((pl.by_unit ? pl.most_units : pl.pieces) * pl.G), pl.hp * pl.tk / 4);
     cfg.blockDim = dim3(128 * shares);
     cfg.dynamicSmemBytes = (shares - 1) * 4 * (128 + 2) * sizeof(float4);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];  // starts while the first kernel ends; waits for it before it reads
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_latent_join_kernel, a, shares);
+    e = cudaLaunchKernelEx(&cfg, attn_latent_join_kernel, a, shares);
     note_launch();
     if (e != cudaSuccess) {
         set_error("attn_latent_join_kernel: %s", cudaGetErrorString(e));
