@@ -1077,8 +1077,12 @@ Plan plan_of(int64_t N, int64_t tokens, int H, int64_t max_tokens) {
     pl.units_one = (pl.parts + pl.G - 1) / pl.G;
     pl.most_units = tokens == N ? N * units_of(pl, 1) : units_of(pl, (int)tokens) + N;
     const int64_t per = (max_tokens + kStep - 1) / kStep;
-    // RULE
-    pl.cut = !(pl.most_units <= sms && per <= 24 && pl.most_units * 5 >= sms * 3);
+    // Units are cut where that balances more than it costs (the sums' way through L2 and the second launch, 5 to 8
+    // us).  The lengths are not known here, only the table's width.  Cut and whole, 32 heads: 16 sequences of
+    // at most 256, 512, 1024 tokens 13.4 and 12.0, 16.0 and 16.5, 19.9 and 25.3 us; 76 of 1024, 2048 tokens 29.8 and
+    // 29.5, 44.2 and 49.5; 128 of 1024, 2048, 4096 tokens 43.2 and 34.2, 65.8 and 57.2, 109 and 102, but of
+    // 100 to 4096 tokens 67.5 and 91.2.
+    pl.cut = !(pl.most_units <= sms && (per <= 4 || per * sms <= 44 * pl.most_units));
     pl.pieces = (int)(pl.cut ? std::max<int64_t>(1, std::min(sms, pl.most_units * per)) : pl.most_units);
     pl.by_unit = pl.most_units < pl.pieces;
     const int64_t q = (int64_t)pl.hp * pl.tk * kRow * 2, ps = (int64_t)pl.n * 128;
