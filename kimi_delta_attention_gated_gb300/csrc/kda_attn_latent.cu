@@ -317,9 +317,7 @@ struct Walk {
     // (words: by this thread the joining launch's words by unit are written)
     __device__ Item next(const Args &a, int piece, int g, bool words) {
         const Plan &pl = a.plan;
-        Item it;
-        it.found = 0;
-        it.bad = 0;
+        Item it = {};
         while (n < a.p.c.N && begin < L1) {
             if (!open) look(a);
             if (n >= a.p.c.N) break;
@@ -502,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < 4; ++j) {
                     const int i = s * per_step + j;
                     q.at[j] = kNone;
-                    if (j < per_step && i < need) {
+                    if (j < per_step && (uint32_t)i < (uint32_t)need) {
                         const int page = __ldg(table + (i >> in_page));
                         q.at[j] = (uint32_t)page < (uint32_t)p.c.n_pages ? page : -1;
                     }
