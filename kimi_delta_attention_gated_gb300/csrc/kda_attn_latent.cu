@@ -41,14 +41,16 @@ using namespace tc;
 
 constexpr int kStep = 64;               // cached tokens of a step
 constexpr int kTileRows = 64;           // query rows of a tile at most
-constexpr int kSoftWarps = 4, kScoreWarp = 4, kValueWarp = 5, kLoadWarp = 6;  // (and the one behind)
-constexpr int kThreads = 256;
+constexpr int kSoftWarps = 4, kScoreWarp = 4, kValueWarp = 5, kLoadWarp = 6, kQueryWarp = 8;
+constexpr int kQueryWarps = 4;
+constexpr int kThreads = (kQueryWarp + kQueryWarps) * 32;
 constexpr int kSlots = 4;               // work items under way
 constexpr int kPad = 2;                 // a unit's own cost in steps, where pieces have kPadFrom steps or more
 constexpr int kPadFrom = 4;
 constexpr int kMaxUnits = 12, kMaxShared = 4;  // ring places at most
 constexpr uint32_t kUnitBytes = kStep * 256, kSharedBytes = kStep * 128;
-constexpr uint32_t kTmemO = 2 * kStep;  // TMEM columns: scores of two steps, then O^T
+constexpr uint32_t kTmemO = 2 * kStep, kTmemQ = kTmemO + 4 * kTileRows;  // TMEM columns: scores of two steps, O^T, queries
+constexpr int kSmemBlocks = 5;          // of a query's nine blocks of 64 channels: in shared memory, the others in TMEM
 constexpr float kSlack = 8.f;           // log2: how far a score may exceed the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNaN = __builtin_nanf("");
@@ -90,7 +92,8 @@ struct Item {
 
 struct Bars {
     uint64_t o_free, p_ready, s_free[2];  // arrivals: the softmax's warps
-    uint64_t i_empty[kSlots];             // and the products' threads
+    uint64_t i_empty[kSlots];             // and the products' threads, and the queries' warps
+    uint64_t qt_full;                     // the queries' warps
     uint64_t q_full, q_empty, p_free, drain[2], s_full[2], i_full[kSlots];  // one
     uint64_t u_full[kMaxUnits], u_empty[kMaxUnits], r_full[kMaxShared], r_empty[kMaxShared];
     Item slots[kSlots];
@@ -124,6 +127,18 @@ __device__ __forceinline__ void tmem_ld_halves(uint32_t taddr, float *r) {
           "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
           "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
         : "r"(taddr));
+}
+// The same for a store: the lower half of the warp's threads writes 16 lanes' columns 0 to 31, the upper half the
+// same lanes' columns 32 to 63.
+__device__ __forceinline__ void tmem_st_halves(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x32bx2.x32.b32 [%0], 32, {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+        "r"(r[31])
+        : "memory");
 }
 // Waits for the loads issued so far; naming the registers keeps their uses behind the wait.
 template <int N>
@@ -380,11 +395,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = &b.abort;
 
     if (pl.cut) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    constexpr int kBars = offsetof(Bars, slots) / 8, kBarsSoft = offsetof(Bars, i_empty) / 8, kBarsItems = offsetof(Bars, q_full) / 8;
+    constexpr int kBars = offsetof(Bars, slots) / 8, kBarsSoft = offsetof(Bars, i_empty) / 8, kBarsItems = offsetof(Bars, qt_full) / 8;
     static_assert(kBars <= kThreads, "a thread for each barrier");
     if (threadIdx.x < kBars) {
         mbar_init(reinterpret_cast<uint64_t *>(&b) + threadIdx.x,
-                  threadIdx.x < kBarsSoft ? kSoftWarps : threadIdx.x < kBarsItems ? kSoftWarps + 2 : 1);
+                  threadIdx.x < kBarsSoft    ? kSoftWarps
+                  : threadIdx.x < kBarsItems ? kSoftWarps + 2 + kQueryWarps
+                  : threadIdx.x == kBarsItems ? kQueryWarps
+                                              : 1);
         fence_mbar_init();
     }
     if (threadIdx.x == kThreads - 1) {
@@ -471,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // All lanes of a warp go on or stop together.
     auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(bar, parity, kAttnPolls)) != 0; };
 
-    if (warp >= kLoadWarp) {
+    if (warp >= kLoadWarp && warp < kQueryWarp) {
         // ---- work items, and the copies of the cache, from a thread of each of two warps: the first has a step's
         // shared channels and units 0 and 1, the second the other two.  A thread by itself issues an instruction
         // every five cycles or so, and the copies of a step took one thread 2200 cycles, the warp's votes about
@@ -619,10 +637,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // copies do not wait for that: 6000 cycles at the border of two items)
                     if (items > 0) ok = wait_for(&b.q_empty, (items - 1) & 1, kAttnPolls);
                     if (!ok) break;
-                    mbar_arrive_expect_tx(&b.q_full, 9 * q_rows * 128);
-                    for (int x = 0; x < 9; ++x) tma_load_3d(sb + x * q_rows * 128, &map_q, &b.q_full, x * 64, head0, t0);
+                    mbar_arrive_expect_tx(&b.q_full, kSmemBlocks * q_rows * 128);
+                    for (int x = 0; x < kSmemBlocks; ++x)
+                        tma_load_3d(sb + x * q_rows * 128, &map_q, &b.q_full, x == kSmemBlocks - 1 ? kLatent : x * 64, head0, t0);
                     ok = wait_for(&b.q_full, items & 1, p.polls);
                     if (!ok) mbar_wait(&b.q_full, items & 1, kAttnPolls);  // it still has to land before the CTA may end
+                    ok = ok && wait_for(&b.qt_full, items & 1, kAttnPolls);
                     for (int s = 0; s < nt && ok; ++s, ++blocks) {
                         const uint32_t t_s = tb + (blocks & 1) * kStep;
                         if (blocks >= 2) ok = wait_for(b.s_free + (blocks & 1), ((blocks >> 1) - 1) & 1, kAttnPolls);
@@ -630,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         fence_after_sync();
                         {
-                            const uint32_t lo = (r_at + rs * (kSharedBytes >> 4)) | k_major, ql = q_lo + 8 * q_chunk;
+                            const uint32_t lo = (r_at + rs * (kSharedBytes >> 4)) | k_major, ql = q_lo + (kSmemBlocks - 1) * q_chunk;
 #pragma unroll
                             for (int x = 0; x < 4; ++x) mma_ss(t_s, desc_of(ql + 2 * x), desc_of(lo + 2 * x), id, x > 0);
                             mma_commit(b.r_empty + rs);
@@ -643,10 +663,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             fence_after_sync();
                             const uint32_t lo = (u_at + us * (kUnitBytes >> 4)) | k_major, ql = q_lo + 2 * m * q_chunk;
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) mma_ss(t_s, desc_of(ql + 2 * x), desc_of(lo + 2 * x), id, 1);
-#pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                mma_ss(t_s, desc_of(ql + q_chunk + 2 * x), desc_of(lo + (kSharedBytes >> 4) + 2 * x), id, 1);
+                            for (int x = 0; x < 8; ++x) {
+                                const uint64_t rows = desc_of(lo + (x >> 2) * (kSharedBytes >> 4) + 2 * (x & 3));
+                                if (m < 2)
+                                    mma_ss(t_s, desc_of(ql + (x >> 2) * q_chunk + 2 * (x & 3)), rows, id, 1);
+                                else
+                                    mma_ts(t_s, tb + kTmemQ + (m - 2) * 64 + 8 * x, rows, id, 1);
+                            }
                             if (++us == (uint32_t)pl.units) us = 0, up ^= 1;
                         }
                         if (!ok) break;
@@ -684,6 +707,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             // nothing issued may still run, and no commit arrive, once the CTA has ended
             mma_commit(b.drain + (warp - kScoreWarp));
             mbar_wait(b.drain + (warp - kScoreWarp), 0, kAttnPolls);
+        }
+        __syncwarp();
+    } else if (warp >= kQueryWarp) {
+        // ---- the queries' channels 256 to 511 into TMEM, where a 64-row operand's rows lie as the product leaves
+        // its own: 32 KB of shared memory that hold half a step of the cache more
+        const int row = (warp - kQueryWarp) * 16 + (lane & 15), tok = row / pl.hp, head_in = row - tok * pl.hp;
+        const uint32_t to = tb + ((uint32_t)((warp - kQueryWarp) * 32) << 16) + kTmemQ;
+        uint32_t items = 0;
+        for (uint32_t k = 0;; ++k) {
+            if (!wait(b.i_full + k % kSlots, (k / kSlots) & 1)) break;
+            const Item it = b.slots[k % kSlots];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b.i_empty + k % kSlots);
+            if (!it.found) break;
+            if (it.s0 == it.s1) continue;
+            uint32_t r[2][32];  // a block of 64 channels: this half of the warp's 4 or 5, then 6 or 7
+            const bool live = tok < it.tokens && it.head0 + head_in < p.H && row < (int)q_rows;
+            const uint4 *q = reinterpret_cast<const uint4 *>(p.q + (int64_t)(it.t0 + tok) * p.q_stride + (int64_t)(it.head0 + head_in) * kRow +
+                                                             256 + (lane >> 4) * 64);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 v = live ? __ldg(q + j * 16 + i) : make_uint4(0, 0, 0, 0);
+                    r[j][4 * i] = v.x, r[j][4 * i + 1] = v.y, r[j][4 * i + 2] = v.z, r[j][4 * i + 3] = v.w;
+                }
+            if (items > 0 && !wait(&b.q_empty, (items - 1) & 1)) break;  // the last item's scores are through
+            fence_after_sync();
+            tmem_st_halves(to, r[0]);
+            tmem_st_halves(to + 64, r[1]);
+            tmem_wait_st();
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.qt_full);
+            ++items;
         }
         __syncwarp();
     } else {
@@ -1083,7 +1141,7 @@ Plan plan_of(int64_t N, int64_t tokens, int H, int64_t max_tokens) {
     pl.cut = !(pl.most_units <= sms && (per <= 4 || per * sms <= 44 * pl.most_units));
     pl.pieces = (int)(pl.cut ? std::max<int64_t>(1, std::min(sms, pl.most_units * per)) : pl.most_units);
     pl.by_unit = pl.most_units < pl.pieces;
-    const int64_t q = (int64_t)pl.hp * pl.tk * kRow * 2, ps = (int64_t)pl.n * 128;
+    const int64_t q = (int64_t)pl.hp * pl.tk * kSmemBlocks * 128, ps = (int64_t)pl.n * 128;
     const int64_t room = kMaxSmem - 1024 - (int64_t)round_up(sizeof(Bars), 128) - round_up(q, 1024) - round_up(ps, 1024);
     pl.shared = 2;
     pl.units = (int)std::min<int64_t>(kMaxUnits, (room - 2 * kSharedBytes) / kUnitBytes);
