@@ -10,19 +10,30 @@
 //   O^T[channels (4 x M 128) x query rows] += C^T P^T, K = 64: the same bytes of C, read MN-major.
 // O stands transposed because 64 rows of 512 channels fill only half of TMEM's lanes the other way,
 // and because its products' second operand, P^T, then is what a softmax thread writes: a
-// row's 64 weights are one swizzled 128-byte line.  Queries (72 KB) and two steps of the
-// cache (144 KB) fill the shared memory, which is what limits a tile to 64 rows.
+// row's 64 weights are one swizzled 128-byte line.
 //
-// The cache arrives by TMA in a ring of 128-channel units (the shared channels in one of their own),
-// and a unit is free again when the one product of O^T that reads it is through.  A step's
-// scores are formed while the softmax works on the last step's.  The softmax's reference moves only where a row's maximum rises by more than
-// 2^kSlack, since moving it means rescaling O^T in TMEM.
+// Shared memory is what limits a tile to 64 rows and the ring to two and a half steps of the cache: of
+// a query's nine blocks of 64 channels five lie there (40 KB), and the other four in TMEM, which a
+// product of 64 rows may read its first operand from and has room beside O^T and two steps' scores
+// (8 sequences of 60000 tokens, 96 heads: 151 to 140 us).  The cache arrives by TMA in a ring of
+// 128-channel units of 16 KB (the shared channels in one of their own of 8 KB), and a unit is free again
+// when the one product of O^T that reads it is through.  (Units of 32 KB, half the waits: 145 us.)  A step's scores
+// are formed while the softmax works on the last step's.  The softmax's reference moves only where a row's maximum
+// rises by more than 2^kSlack, since moving it means rescaling O^T in TMEM.
 //
 // Work split.  All steps of all units (a sequence's groups of `G` tiles, each tile on a CTA of
-// its own, so that the G read the same tokens at about the same time) are numbered in one line,
-// kPad places before each unit standing for what it costs beside its steps; the line is cut into
-// equal pieces.  Units that more than one CTA took leave their sums in a workspace, and
-// attn_latent_join_kernel adds them in their order, so results do not depend on timing.
+// its own, so that the G read the same tokens at about the same time and all but one find them in
+// L2) are numbered in one line, kPad places before each unit standing for what it costs beside its steps; the
+// line is cut into equal pieces.  Units that more than one CTA took leave their sums in a
+// workspace, and attn_latent_join_kernel adds them in their order, so results do not depend on timing.
+// Where the table is narrow, units stay whole and the second launch falls away: see plan_of.
+//
+// What bounds it.  Up to 64 heads: HBM.  8 sequences of 60000 tokens: 94 us with 16 heads, 103 with 64,
+// 5.9 and 5.4 TB/s of 6.7 that a copy reaches.  96 and 128 heads are two tiles and twice the products: 140 and
+// 144 us, 2300 cycles a step of which the tensor core works 1900 (S reads 72 KB of C and 40 KB of Q through
+// shared memory's 128 bytes a cycle, O^T 64 KB of C and P four times); the rest are the waits of the chain scores,
+// softmax, weights, O^T.  Short calls are launches and latencies: one sequence of 1000 tokens 14 us, of which the
+// set-up takes 3, the first data 2, the output 4 and the joining launch 5.
 #include <cuda.h>
 
 #include <climits>
@@ -47,7 +58,8 @@ constexpr int kThreads = (kQueryWarp + kQueryWarps) * 32;
 constexpr int kSlots = 4;               // work items under way
 constexpr int kPad = 2;                 // a unit's own cost in steps, where pieces have kPadFrom steps or more
 constexpr int kPadFrom = 4;
-constexpr int kMaxUnits = 12, kMaxShared = 4;  // ring places at most
+constexpr int kMaxUnits = 12;            // ring places of units at most
+constexpr uint32_t kShared = 2;         // and of the shared channels
 constexpr uint32_t kUnitBytes = kStep * 256, kSharedBytes = kStep * 128;
 constexpr uint32_t kTmemO = 2 * kStep, kTmemQ = kTmemO + 4 * kTileRows;  // TMEM columns: scores of two steps, O^T, queries
 constexpr int kSmemBlocks = 5;          // of a query's nine blocks of 64 channels: in shared memory, the others in TMEM
@@ -69,7 +81,7 @@ struct Plan {
     int units_one;    // of a sequence with one token
     int by_unit;      // the joining launch goes by units, else by pieces
     int n;            // rows of a tile as the products' N: hp * tk, a multiple of 16
-    int units, shared;  // ring places
+    int units;        // ring places
     uint32_t at_p, at_units, at_shared, at_bars;  // shared memory
 };
 
@@ -95,7 +107,7 @@ struct Bars {
     uint64_t i_empty[kSlots];             // and the products' threads, and the queries' warps
     uint64_t qt_full;                     // the queries' warps
     uint64_t q_full, q_empty, p_free, drain[2], s_full[2], i_full[kSlots];  // one
-    uint64_t u_full[kMaxUnits], u_empty[kMaxUnits], r_full[kMaxShared], r_empty[kMaxShared];
+    uint64_t u_full[kMaxUnits], u_empty[kMaxUnits], r_full[kShared], r_empty[kShared];
     Item slots[kSlots];
     int64_t row_at[kTileRows];   // a row's place in o, or -1
     float factor[kTileRows];
@@ -346,7 +358,9 @@ struct Walk {
                 u = 0;
                 open = false;
             }
-            if (words && pl.cut && pl.by_unit && at + (t.steps ? pad : 0) >= L0 && at + (t.steps ? pad : 0) < L1) {
+            // (a cu_seqlens that does not ascend may have more units than there is room for)
+            const int64_t starts = at + (t.steps ? pad : 0);
+            if (words && pl.cut && pl.by_unit && number < pl.most_units && starts >= L0 && starts < L1) {
                 const int last = t.steps ? (int)((first + t.steps - 1) / S) : piece;
                 join_words(a)[number * pl.G + g] = make_int4(t.t0, t.head0 | t.tokens << 16, piece, t.tokens ? last : piece);
             }
@@ -468,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!pl.by_unit)
             join_words(a)[blockIdx.x] = *reinterpret_cast<const int4 *>(&w.join);
         else if (blockIdx.x == 0)
-            join_words(a)[pl.most_units * pl.G] = make_int4((int)total_units, 0, 0, 0);
+            join_words(a)[pl.most_units * pl.G] = make_int4((int)min(total_units, pl.most_units), 0, 0, 0);
     };
     auto wait_for = [&](uint64_t *bar, uint32_t parity, uint32_t polls) {
         for (uint32_t i = 0; i < polls; ++i) {
@@ -492,8 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= kLoadWarp && warp < kQueryWarp) {
         // ---- work items, and the copies of the cache, from a thread of each of two warps: the first has a step's
         // shared channels and units 0 and 1, the second the other two.  A thread by itself issues an instruction
-        // every five cycles or so, and the copies of a step took one thread 2200 cycles, the warp's votes about
-        // each wait and two copies a unit 2900; either was the bound.
+        // every five cycles or so: all copies of a step took one thread 2200 cycles, or with the warp's votes about
+        // each wait 2900, and either was the bound.
         if (elect_one()) {
             const int half = warp - kLoadWarp;
             Walk w;
@@ -565,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             if (at[j] >= 0) tma_load_3d(to + j * sub * 128, &map_r, b.r_full + rs, 0, at[j], kLatent / 64);
-                        if (++rs == (uint32_t)pl.shared) rs = 0, rp ^= 1;
+                        if (++rs == kShared) rs = 0, rp ^= 1;
                     }
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -596,8 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // every copy lands before the CTA may end (after a failure within a step, those of that step may not have
             // been issued: their wait runs out)
             if (half == 0)
-                for (uint32_t j = steps > (uint32_t)pl.shared ? steps - pl.shared : 0; j < steps + !ok; ++j)
-                    mbar_wait(b.r_full + j % pl.shared, (j / pl.shared) & 1, ok ? kAttnPolls : kLastPolls);
+                for (uint32_t j = steps > kShared ? steps - kShared : 0; j < steps + !ok; ++j)
+                    mbar_wait(b.r_full + j % kShared, (j / kShared) & 1, ok ? kAttnPolls : kLastPolls);
             const uint32_t fills = 4 * (steps + !ok), units = pl.units;
             for (uint32_t j = fills > units ? fills - units : 0; j < fills; ++j)
                 if ((int)(j & 3) >> 1 == half) mbar_wait(b.u_full + j % units, (j / units) & 1, ok ? kAttnPolls : kLastPolls);
@@ -607,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- products, the scores' and the values' each from one thread of a warp.  A look at a barrier
         // queues behind the products that its thread has issued, about 120 cycles in which the tensor core
         // idles; with two threads one's products run meanwhile.  (From one thread, with votes of its
-        // warp, the same work took 4800 cycles a step instead of 2900.)
+        // warp, the same work took 4800 cycles a step, two threads then 2900.)
         const uint32_t k_major = (16u >> 4) << 16, mn_major = (kSharedBytes >> 4) << 16;
         const uint32_t u_at = sb16 + (pl.at_units >> 4);
         uint32_t blocks = 0, items = 0, us = 0, up = 0;  // steps and items with any so far; ring place and parity
@@ -654,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int x = 0; x < 4; ++x) mma_ss(t_s, desc_of(ql + 2 * x), desc_of(lo + 2 * x), id, x > 0);
                             mma_commit(b.r_empty + rs);
-                            if (++rs == (uint32_t)pl.shared) rs = 0, rp ^= 1;
+                            if (++rs == kShared) rs = 0, rp ^= 1;
                         }
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
@@ -1143,12 +1157,11 @@ Plan plan_of(int64_t N, int64_t tokens, int H, int64_t max_tokens) {
     pl.by_unit = pl.most_units < pl.pieces;
     const int64_t q = (int64_t)pl.hp * pl.tk * kSmemBlocks * 128, ps = (int64_t)pl.n * 128;
     const int64_t room = kMaxSmem - 1024 - (int64_t)round_up(sizeof(Bars), 128) - round_up(q, 1024) - round_up(ps, 1024);
-    pl.shared = 2;
-    pl.units = (int)std::min<int64_t>(kMaxUnits, (room - 2 * kSharedBytes) / kUnitBytes);
+    pl.units = (int)std::min<int64_t>(kMaxUnits, (room - kShared * kSharedBytes) / kUnitBytes);
     pl.at_p = (uint32_t)round_up(q, 1024);
     pl.at_units = pl.at_p + (uint32_t)round_up(ps, 1024);
     pl.at_shared = pl.at_units + pl.units * kUnitBytes;
-    pl.at_bars = pl.at_shared + pl.shared * kSharedBytes;
+    pl.at_bars = pl.at_shared + kShared * kSharedBytes;
     return pl;
 }
 
