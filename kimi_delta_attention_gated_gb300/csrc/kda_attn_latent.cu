@@ -21,7 +21,7 @@
 // are formed while the softmax works on the last step's.  The softmax's reference moves only where a row's maximum
 // rises by more than 2^kSlack, since moving it means rescaling O^T in TMEM.
 //
-// Work split.  All steps of all units (a sequence's groups of `G` tiles, each tile on a CTA of
+// Work split.  All steps of all units (a sequence's groups of G tiles, each tile on a CTA of
 // its own, so that the G read the same tokens at about the same time and all but one find them in
 // L2) are numbered in one line, kPad places before each unit standing for what it costs beside its steps; the
 // line is cut into equal pieces.  Units that more than one CTA took leave their sums in a
@@ -58,6 +58,8 @@ constexpr int kThreads = (kQueryWarp + kQueryWarps) * 32;
 constexpr int kSlots = 4;               // work items under way
 constexpr int kPad = 2;                 // a unit's own cost in steps, where pieces have kPadFrom steps or more
 constexpr int kPadFrom = 4;
+constexpr int kMaxShare = 8;            // tiles of a unit at most
+constexpr double kIdle = 0.08;
 constexpr int kMaxUnits = 12;            // ring places of units at most
 constexpr uint32_t kShared = 2;         // and of the shared channels
 constexpr uint32_t kUnitBytes = kStep * 256, kSharedBytes = kStep * 128;
@@ -74,12 +76,14 @@ __device__ int g_attn_latent_timeouts = 0;
 struct Plan {
     int hp, tk;       // heads (a multiple of 8) and tokens of a tile: hp * tk rows
     int parts;        // tiles that share a token's heads
-    int G;            // tiles of a unit
-    int pieces;       // of the line
+    // Two ways to split, of which the lengths decide (without cuts both are the first).
+    int G[2];         // tiles of a unit
+    int pieces[2];    // of the line
+    int units_one[2];  // units of a sequence with one token
+    int ctas;
     int cut;          // units may be cut; else piece i is the i-th unit
-    int64_t most_units;  // of the call at most
-    int units_one;    // of a sequence with one token
     int by_unit;      // the joining launch goes by units, else by pieces
+    int64_t most_places;  // tiles' places in the call's units at most
     int n;            // rows of a tile as the products' N: hp * tk, a multiple of 16
     int units;        // ring places
     uint32_t at_p, at_units, at_shared, at_bars;  // shared memory
@@ -111,7 +115,7 @@ struct Bars {
     Item slots[kSlots];
     int64_t row_at[kTileRows];   // a row's place in o, or -1
     float factor[kTileRows];
-    int64_t scan[kThreads / 32][2];
+    int64_t scan[kThreads / 32][4];
     int64_t start_begin, start_unit;
     int start_seq;
     uint32_t tmem;
@@ -225,17 +229,17 @@ __device__ __forceinline__ int tokens_of(const LatentCache &c, int n) {
 }
 __host__ __device__ __forceinline__ int steps_of(int tokens) { return (int)(((int64_t)tokens + kStep - 1) / kStep); }
 // Units of a sequence with nq rows in the call (tiles stay below 2^31: 2^24 rows, 64 tiles of a token).
-__host__ __device__ __forceinline__ int units_of(const Plan &pl, int nq) {
-    if (nq <= 1) return nq * pl.units_one;
+__host__ __device__ __forceinline__ int units_of(const Plan &pl, int way, int nq) {
+    if (nq <= 1) return nq * pl.units_one[way];
     const uint32_t tiles = ((uint32_t)nq + pl.tk - 1) / pl.tk * pl.parts;
-    return (int)((tiles + pl.G - 1) / pl.G);
+    return (int)((tiles + pl.G[way] - 1) / pl.G[way]);
 }
 // Its units, and their places on the line.
-__device__ __forceinline__ int units_of(const Args &a, int n) {
+__device__ __forceinline__ int units_of(const Args &a, int way, int n) {
     int64_t t0;
     int nq;
     call_rows(a.p.cu_seqlens, a.p.tokens, n, t0, nq);
-    return units_of(a.plan, nq);
+    return units_of(a.plan, way, nq);
 }
 // Places of a unit beside its own cost (one without steps has a place too: its rows are written there).
 __device__ __forceinline__ int line_steps(int len) { return max(1, steps_of(len)); }
@@ -246,34 +250,52 @@ __device__ __forceinline__ int seq_steps(const Args &a, int n) { return line_ste
 struct Line {
     int64_t total, total_units, mine, units;
     int first, last;
+    int way;
 };
 template <int THREADS>
-__device__ __forceinline__ Line measure_line(const Args &a, int64_t (*scan)[2]) {
+__device__ __forceinline__ Line measure_line(const Args &a, int64_t (*scan)[4]) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = a.p.c.N, per = (N + THREADS - 1) / THREADS;
     Line l;
     l.first = min(tid * per, N);
     l.last = min(l.first + per, N);
-    int64_t own = 0, own_units = 0;
+    const bool ways = a.plan.G[0] != a.plan.G[1];
+    int64_t x[2] = {}, y[2] = {};
     for (int n = l.first; n < l.last; ++n) {
-        const int64_t u = units_of(a, n);
-        own_units += u;
-        own += u * seq_steps(a, n);
-    }
-    int64_t x = own, y = own_units;
+        const int64_t steps = seq_steps(a, n);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t dx = __shfl_up_sync(0xffffffffu, x, o), dy = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) x += dx, y += dy;
+        for (int w = 0; w < 2; ++w) {
+            if (w == 1 && !ways) break;
+            const int64_t u = units_of(a, w, n);
+            y[w] += u;
+            x[w] += u * steps;
+        }
     }
-    if (lane == 31) scan[warp][0] = x, scan[warp][1] = y;
+    const int64_t own[2] = {x[0], x[1]}, own_units[2] = {y[0], y[1]};
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        if (w == 1 && !ways) break;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t dx = __shfl_up_sync(0xffffffffu, x[w], o), dy = __shfl_up_sync(0xffffffffu, y[w], o);
+            if (lane >= o) x[w] += dx, y[w] += dy;
+        }
+        if (lane == 31) scan[warp][2 * w] = x[w], scan[warp][2 * w + 1] = y[w];
+    }
     __syncthreads();
-    l.mine = x - own;
-    l.units = y - own_units;
+    l.way = 0;
+    if (ways) {  // the second way, unless it leaves too many CTAs without a tile: see share_of
+        int64_t t[2] = {};
+        for (int w = 0; w < THREADS / 32; ++w) t[0] += scan[w][0], t[1] += scan[w][2];
+        l.way = (double)t[1] * a.plan.pieces[0] <= (1. + kIdle) * (double)t[0] * a.plan.pieces[1];
+    }
+    l.mine = l.way ? x[1] - own[1] : x[0] - own[0];
+    l.units = l.way ? y[1] - own_units[1] : y[0] - own_units[0];
     l.total = l.total_units = 0;
     for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) l.mine += scan[w][0], l.units += scan[w][1];
-        l.total += scan[w][0];
-        l.total_units += scan[w][1];
+        const int64_t dx = scan[w][2 * l.way], dy = scan[w][2 * l.way + 1];
+        if (w < warp) l.mine += dx, l.units += dy;
+        l.total += dx;
+        l.total_units += dy;
     }
     return l;
 }
@@ -301,14 +323,16 @@ struct __align__(16) JoinWord {
     int t0, place, first, last;  // its first row; its first head and its rows' tokens << 16; the pieces of its
                                  // first and its last step
 };
-// These words lie behind the parts: with by_unit one for each of a unit's G tiles, then one with
-// the number of units, else one for each CTA.  first == last: nothing to join.
+// These words lie behind the parts: with by_unit one for each of a unit's G tiles, else one for each CTA, then one
+// with the number of units or pieces and with G.  first == last: nothing to join.
+__host__ __device__ __forceinline__ int64_t words_of(const Plan &pl) { return pl.by_unit ? pl.most_places : pl.ctas; }
 __device__ __forceinline__ int4 *join_words(const Args &a) {
-    return reinterpret_cast<int4 *>(a.p.ws + (int64_t)a.plan.pieces * a.plan.G * 2 * part_floats(a.plan));
+    return reinterpret_cast<int4 *>(a.p.ws + (int64_t)a.plan.ctas * 2 * part_floats(a.plan));
 }
 
 // Goes through the work items of one tile place `g` of a piece.
 struct Walk {
+    int way, G;
     int64_t L0, L1, S, begin;  // the piece, the next unit's place on the line (without cuts: units)
     int n, u, units, nq, len;  // the next unit: its sequence, and number there
     int64_t t0;
@@ -323,10 +347,12 @@ struct Walk {
             if (nq > 0) break;
         }
         len = tokens_of(a.p.c, n);
-        units = units_of(a.plan, nq);
+        units = units_of(a.plan, way, nq);
         open = true;
     }
-    __device__ void start(const Args &a, int64_t l0, int64_t l1, int64_t s, int own, int seq, int64_t seq_begin, int64_t seq_unit) {
+    __device__ void start(const Args &a, int split, int64_t l0, int64_t l1, int64_t s, int own, int seq, int64_t seq_begin, int64_t seq_unit) {
+        way = split;
+        G = a.plan.G[way];
         L0 = l0;
         L1 = l1;
         S = s;
@@ -349,7 +375,7 @@ struct Walk {
             if (!open) look(a);
             if (n >= a.p.c.N) break;
             const int64_t first = begin + pad, at = begin;
-            const Tile t = tile_of(pl, t0, nq, len, u * pl.G + g);
+            const Tile t = tile_of(pl, t0, nq, len, u * G + g);
             it.seq = n;
             begin += pl.cut ? line_steps(len) + pad : 1;
             const int64_t number = unit++;
@@ -360,9 +386,9 @@ struct Walk {
             }
             // (a cu_seqlens that does not ascend may have more units than there is room for)
             const int64_t starts = at + (t.steps ? pad : 0);
-            if (words && pl.cut && pl.by_unit && number < pl.most_units && starts >= L0 && starts < L1) {
+            if (words && pl.cut && pl.by_unit && number * G + g < pl.most_places && starts >= L0 && starts < L1) {
                 const int last = t.steps ? (int)((first + t.steps - 1) / S) : piece;
-                join_words(a)[number * pl.G + g] = make_int4(t.t0, t.head0 | t.tokens << 16, piece, t.tokens ? last : piece);
+                join_words(a)[number * G + g] = make_int4(t.t0, t.head0 | t.tokens << 16, piece, t.tokens ? last : piece);
             }
             if (t.tokens == 0) continue;
             it.t0 = t.t0;
@@ -379,7 +405,7 @@ struct Walk {
                 it.s1 = (int)min(L1 - first, (int64_t)t.steps);
                 if (it.s0 >= it.s1) continue;
                 if (it.s0 > 0 || it.s1 < t.steps)
-                    it.part = (((int64_t)piece * pl.G + g) * 2 + (it.s0 > 0 ? 0 : 1)) * part_floats(pl);
+                    it.part = (((int64_t)piece * G + g) * 2 + (it.s0 > 0 ? 0 : 1)) * part_floats(pl);
                 if (it.s0 == 0 && it.s1 < t.steps) {
                     join.t0 = t.t0;
                     join.place = t.head0 | t.tokens << 16;
@@ -404,7 +430,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sb = smem_u32(sm), sb16 = (sb & 0x3FFFF) >> 4;
     Bars &b = *reinterpret_cast<Bars *>(sm + pl.at_bars);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int piece = blockIdx.x / pl.G, g = blockIdx.x - piece * pl.G;
     const uint32_t q_rows = pl.hp * pl.tk;
     volatile int *abort_flag = &b.abort;
 
@@ -433,40 +458,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == kLoadWarp && !pl.cut && !p.cu_seqlens) {
         // the length and the first pages on their way, while the rest is set up
-        const int n = piece / pl.units_one;
+        const int n = blockIdx.x / pl.G[0] / pl.units_one[0];
         int x, y = 0;
         asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(x) : "l"(p.c.lens + n));
         if (lane < p.c.max_blocks) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(y) : "l"(p.c.block_table + (int64_t)n * p.c.max_blocks + lane));
         asm volatile("" ::"r"(x), "r"(y));
     }
     // The piece: places of the line, or without cuts units.
-    int64_t L0 = piece, L1 = piece + 1, S = 1;
-    int pad = 0;
+    int64_t L0, L1, S = 1;
+    int pad = 0, way = 0, piece;
     int start_seq;
     int64_t start_begin, start_unit = 0, total_units = 0;
     if (!pl.cut && !p.cu_seqlens) {  // as many units in every sequence
-        start_seq = piece / pl.units_one;
-        start_begin = (int64_t)start_seq * pl.units_one;
+        piece = blockIdx.x / pl.G[0];
+        L0 = piece;
+        L1 = piece + 1;
+        start_seq = piece / pl.units_one[0];
+        start_begin = (int64_t)start_seq * pl.units_one[0];
     } else {
         const Line line = measure_line<kThreads>(a, b.scan);  // (a barrier inside)
+        way = line.way;
+        piece = blockIdx.x / pl.G[way];
+        L0 = piece;
+        L1 = piece + 1;
         if (pl.cut) {
-            pad = line.total >= (int64_t)kPadFrom * pl.pieces ? kPad : 0;
+            pad = line.total >= (int64_t)kPadFrom * pl.pieces[way] ? kPad : 0;
             const int64_t places = line.total + pad * line.total_units;
-            S = (places + pl.pieces - 1) / pl.pieces;
+            S = (places + pl.pieces[way] - 1) / pl.pieces[way];
             L0 = piece * S;
             L1 = min(L0 + S, places);
             total_units = line.total_units;
         }
         int64_t at = pl.cut ? line.mine + pad * line.units : line.units, units = line.units;
         for (int n = line.first; n < line.last; ++n) {
-            const int64_t more = (int64_t)units_of(a, n) * (pl.cut ? seq_steps(a, n) + pad : 1);
+            const int64_t more = (int64_t)units_of(a, way, n) * (pl.cut ? seq_steps(a, n) + pad : 1);
             if (L0 >= at && L0 < at + more && L0 < L1) {
                 b.start_seq = n;
                 b.start_begin = at;
                 b.start_unit = units;
             }
             at += more;
-            units += units_of(a, n);
+            units += units_of(a, way, n);
         }
     }
     fence_before_sync();
@@ -478,11 +510,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         start_begin = b.start_begin;
         start_unit = b.start_unit;
     }
+    const int G = pl.G[way], g = blockIdx.x - piece * G;
     auto last_words = [&](const Walk &w) {
-        if (!pl.by_unit)
-            join_words(a)[blockIdx.x] = *reinterpret_cast<const int4 *>(&w.join);
-        else if (blockIdx.x == 0)
-            join_words(a)[pl.most_units * pl.G] = make_int4((int)min(total_units, pl.most_units), 0, 0, 0);
+        if (!pl.by_unit) join_words(a)[blockIdx.x] = *reinterpret_cast<const int4 *>(&w.join);
+        if (blockIdx.x == 0)
+            join_words(a)[words_of(pl)] = make_int4(pl.by_unit ? (int)min(total_units, pl.most_places / G) : pl.pieces[way], G, 0, 0);
     };
     auto wait_for = [&](uint64_t *bar, uint32_t parity, uint32_t polls) {
         for (uint32_t i = 0; i < polls; ++i) {
@@ -511,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
             const int half = warp - kLoadWarp;
             Walk w;
-            w.start(a, L0, L1, S, pad, start_seq, start_begin, start_unit);
+            w.start(a, way, L0, L1, S, pad, start_seq, start_begin, start_unit);
             uint32_t us = 0, up = 1;           // ring place of the step's first unit, and the parity of the wait for it (a
                                                // barrier's phase before its first counts as over)
             uint32_t rs = 0, rp = 1, steps = 0;
@@ -998,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // After a failure every row of this CTA's items becomes NaN.
     if (*abort_flag) {
         Walk w;
-        w.start(a, L0, L1, S, pad, start_seq, start_begin, start_unit);
+        w.start(a, way, L0, L1, S, pad, start_seq, start_begin, start_unit);
         for (;;) {
             const Item it = w.next(a, piece, g, threadIdx.x == 0);
             if (!it.found) break;
@@ -1028,16 +1060,16 @@ __global__ void __launch_bounds__(128 * kMaxShares) attn_latent_join_kernel(cons
     extern __shared__ float4 s_acc[];  // [shares - 1 of 4 warps][128], then their m and l
     const AttnLatentParams &p = a.p;
     const Plan &pl = a.plan;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = blockIdx.x / pl.G, g = blockIdx.x - which * pl.G;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 *words = join_words(a);
-    const int units = pl.by_unit ? __ldcg(&words[pl.most_units * pl.G].x) : pl.pieces;
-    const int4 word = __ldcg(words + blockIdx.x);
+    const int4 of = __ldcg(words + words_of(pl)), word = __ldcg(words + blockIdx.x);
+    const int G = of.y, which = blockIdx.x / G, g = blockIdx.x - which * G;
     const JoinWord t = *reinterpret_cast<const JoinWord *>(&word);
     const int share = warp >> 2, q = warp & 3, k0 = t.first, k1 = t.last;
     const int r = 4 * blockIdx.y;  // the first of the rows, all of one token
     const int tok = r / pl.hp, head = (t.place & 0xFFFF) + r - tok * pl.hp;
-    if (which >= units || k0 >= k1 || tok >= t.place >> 16 || head >= p.H) return;
+    if (which >= of.x || k0 >= k1 || tok >= t.place >> 16 || head >= p.H) return;
     const int64_t out = (int64_t)(t.t0 + tok) * p.H + head;
     float m[4], l[4], acc[4][4];  // of the rows; of channels lane + 32 * i
 #pragma unroll
@@ -1049,8 +1081,8 @@ __global__ void __launch_bounds__(128 * kMaxShares) attn_latent_join_kernel(cons
     }
     const int each = (k1 - k0 + shares) / shares, from = k0 + share * each, to = min(from + each, k1 + 1);
     // (the tile is in slot 1 of the piece that it begins in, else in slot 0)
-    const int64_t floats = part_floats(pl), step = 2 * pl.G * floats;
-    const float *ws = p.ws + (from * pl.G + g) * 2 * floats + (share == 0 ? floats : 0);
+    const int64_t floats = part_floats(pl), step = 2 * G * floats;
+    const float *ws = p.ws + (from * G + g) * 2 * floats + (share == 0 ? floats : 0);
     const int at = pl.n * kLatent + r;
     struct Four {
         float4 m, l, x[4];
@@ -1129,6 +1161,20 @@ __global__ void __launch_bounds__(128 * kMaxShares) attn_latent_join_kernel(cons
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
+// The tiles that read a sequence together, of sequences of `tiles`: as many as leave at most kIdle more of the CTAs
+// without a tile than the best does.  More of them read the cache fewer times: 16 sequences of 10000 tokens with
+// 4 rows, 64 heads (4 tiles), by 1, 2 and 4: 125, 108 and 104 us.  But what does not divide the tiles idles: with 5
+// rows by 1, 2, 4 and 5: 138, 151, 185 and 126 us.
+int share_of(int64_t tiles) {
+    const int sms = sm_count(), most = std::min(kMaxShare, sms);
+    auto cost = [&](int G) { return (double)((tiles + G - 1) / G) / (sms / G); };
+    double least = cost(1);
+    for (int G = 2; G <= most; ++G) least = std::min(least, cost(G));
+    int G = most;
+    while (cost(G) > (1. + kIdle) * least) --G;
+    return G;
+}
+
 // How a call is split.  Tiles: all heads of as many tokens as 64 rows hold, or with more than 64 heads
 // equal parts of one token's.
 Plan plan_of(int64_t N, int64_t tokens, int H, int64_t max_tokens) {
@@ -1141,20 +1187,30 @@ Plan plan_of(int64_t N, int64_t tokens, int H, int64_t max_tokens) {
     pl.tk = (int)std::max<int64_t>(1, std::min<int64_t>(kTileRows / pl.hp, avg));
     pl.n = (int)round_up(pl.hp * pl.tk, 16);
     const int64_t tiles = (avg + pl.tk - 1) / pl.tk * pl.parts;
-    pl.G = tiles >= 4 ? 4 : tiles >= 2 ? 2 : 1;
-    const int64_t sms = std::max(sm_count() / pl.G, 1);
-    // (a sequence of nq rows has at most nq / (rows of a unit) + 1 units)
-    pl.units_one = (pl.parts + pl.G - 1) / pl.G;
-    pl.most_units = tokens == N ? N * units_of(pl, 1) : units_of(pl, (int)tokens) + N;
+    // A token's tiles are shared in either way; a sequence's too where all have about as many rows.
+    pl.G[0] = share_of(pl.parts);
+    pl.G[1] = share_of(tiles);
+    int64_t most_units[2], sms[2];
+    for (int w = 0; w < 2; ++w) {
+        sms[w] = std::max(sm_count() / pl.G[w], 1);
+        pl.units_one[w] = (pl.parts + pl.G[w] - 1) / pl.G[w];
+        // (a sequence of nq rows has at most nq / (rows of a unit) + 1 units)
+        most_units[w] = tokens == N ? N * units_of(pl, w, 1) : units_of(pl, w, (int)tokens) + N;
+    }
     const int64_t per = (max_tokens + kStep - 1) / kStep;
     // Units are cut where that balances more than it costs (the sums' way through L2 and the second launch, 5 to 8
     // us).  The lengths are not known here, only the table's width.  Cut and whole, 32 heads: 16 sequences of
     // at most 256, 512, 1024 tokens 13.4 and 12.0, 16.0 and 16.5, 19.9 and 25.3 us; 76 of 1024, 2048 tokens 29.8 and
     // 29.5, 44.2 and 49.5; 128 of 1024, 2048, 4096 tokens 43.2 and 34.2, 65.8 and 57.2, 109 and 102, but of
     // 100 to 4096 tokens 67.5 and 91.2.
-    pl.cut = !(pl.most_units <= sms && (per <= 4 || per * sms <= 44 * pl.most_units));
-    pl.pieces = (int)(pl.cut ? std::max<int64_t>(1, std::min(sms, pl.most_units * per)) : pl.most_units);
-    pl.by_unit = pl.most_units < pl.pieces;
+    pl.cut = !(most_units[0] <= sms[0] && (per <= 4 || per * sms[0] <= 44 * most_units[0]));
+    if (!pl.cut) pl.G[1] = pl.G[0], pl.units_one[1] = pl.units_one[0], most_units[1] = most_units[0];
+    for (int w = 0; w < 2; ++w) {
+        pl.pieces[w] = (int)(pl.cut ? std::max<int64_t>(1, std::min(sms[w], most_units[w] * per)) : most_units[w]);
+        pl.ctas = std::max(pl.ctas, pl.pieces[w] * pl.G[w]);
+        pl.most_places = std::max(pl.most_places, most_units[w] * pl.G[w]);
+    }
+    pl.by_unit = pl.most_places < pl.ctas;
     const int64_t q = (int64_t)pl.hp * pl.tk * kSmemBlocks * 128, ps = (int64_t)pl.n * 128;
     const int64_t room = kMaxSmem - 1024 - (int64_t)round_up(sizeof(Bars), 128) - round_up(q, 1024) - round_up(ps, 1024);
     pl.units = (int)std::min<int64_t>(kMaxUnits, (room - kShared * kSharedBytes) / kUnitBytes);
@@ -1166,8 +1222,7 @@ Plan plan_of(int64_t N, int64_t tokens, int H, int64_t max_tokens) {
 }
 
 size_t plan_bytes(const Plan &pl) {
-    const int64_t words = pl.by_unit ? pl.most_units * pl.G + 1 : (int64_t)pl.pieces * pl.G;
-    return pl.cut ? (size_t)pl.pieces * pl.G * 2 * part_floats(pl) * sizeof(float) + words * sizeof(JoinWord) : 0;
+    return pl.cut ? (size_t)pl.ctas * 2 * part_floats(pl) * sizeof(float) + (words_of(pl) + 1) * sizeof(JoinWord) : 0;
 }
 
 bool encode_tensors(const AttnLatentParams &p, const Plan &pl, CUtensorMap *mq, CUtensorMap *mc, CUtensorMap *mr) {
@@ -1238,7 +1293,7 @@ kda_status launch_attn_latent(const AttnLatentParams &p, cudaStream_t st) {
     cudaLaunchAttribute attr[1];  // either launch starts while the one before ends, and waits for it before it reads
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(pl.pieces * pl.G);
+    cfg.gridDim = dim3(pl.ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kMaxSmem;
     cfg.stream = st;
@@ -1254,8 +1309,8 @@ kda_status launch_attn_latent(const AttnLatentParams &p, cudaStream_t st) {
     kda_status s = check_launch("attn_latent_kernel");
     if (!pl.cut || s != KDA_OK) return s;
     // with many pieces a unit more warps share them
-    const int shares = pl.pieces >= 16 * pl.most_units ? kMaxShares : 1;
-    cfg.gridDim = dim3((unsigned)((pl.by_unit ? pl.most_units : pl.pieces) * pl.G), pl.hp * pl.tk / 4);
+    const int shares = pl.ctas >= 16 * pl.most_places ? kMaxShares : 1;
+    cfg.gridDim = dim3((unsigned)words_of(pl), pl.hp * pl.tk / 4);
     cfg.blockDim = dim3(128 * shares);
     cfg.dynamicSmemBytes = (shares - 1) * 4 * (128 + 2) * sizeof(float4);
     e = cudaLaunchKernelEx(&cfg, attn_latent_join_kernel, a, shares);
