@@ -383,16 +383,16 @@ int take_latent_product_timeouts(cudaStream_t st) {
 
 kda_status launch_latent_product(const LatentProductParams &p, cudaStream_t st) {
     if (p.tokens == 0) return KDA_OK;
-    // narrow tiles where wide ones would leave SMs without one
+    // Narrow tiles where wide ones would leave SMs without one.  Expansion by 64, 128 and 256 outputs: 100 tokens, 16
+    // heads 5.4, 5.6, 7.6 us, 64 heads 7.5, 6.2, 7.9; 256 tokens, 72 heads 10.4, 7.7, 9.8, 128 heads 20.1, 15.6, 14.2.  Values
+    // by 64 and 128: 8 tokens, 32 heads 5.0, 5.3; 256 tokens, 72 heads 6.6, 7.5, 80 heads 10.5, 8.8.  The queries' short sum
+    // gains nothing from them: by 64, 128 and 256, 8 tokens, 32 heads 5.1, 4.6, 4.4; 256 tokens, 128 heads 17.0, 14.9, 13.6.
     const int64_t wide = (p.tokens + kTile - 1) / kTile * p.H;
+    if (p.what == kLatentQueries) return run<kLatentQueries, 256>(p, st);
     if (p.what == kLatentExpand)
-        return wide * 2 < sm_count() ? run<kLatentExpand, 64>(p, st)
+        return wide * 4 < sm_count() ? run<kLatentExpand, 64>(p, st)
                : wide < sm_count()   ? run<kLatentExpand, 128>(p, st)
                                      : run<kLatentExpand, 256>(p, st);
-    if (p.what == kLatentQueries)
-        return wide * 4 < sm_count() ? run<kLatentQueries, 64>(p, st)
-               : wide < sm_count()   ? run<kLatentQueries, 128>(p, st)
-                                     : run<kLatentQueries, 256>(p, st);
     return wide < sm_count() ? run<kLatentValues, 64>(p, st) : run<kLatentValues, 128>(p, st);
 }
 
