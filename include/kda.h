@@ -96,7 +96,8 @@ uint64_t kda_launch_count(void);
  * into every output it was responsible for (the state, o and y of its (sequence,
  * head) units, or the y and state rows of its convolution tiles; a decode CTA also
  * poisons every later unit it owned), and counts the event in a device-side counter.
- * (An attention CTA poisons the rows that it had not written yet.)
+ * (An attention CTA poisons the rows that it had not written yet, one over the latent cache all
+ * rows that it had a part of, a latent product's CTA its tile.)
  * The compute calls are asynchronous and cannot see this, so this call synchronises
  * `stream` (a cudaStream_t; NULL = the legacy default stream), reads the counters of
  * the current device and clears them.  Returns KDA_ERR_TIMEOUT if any wait gave up
@@ -114,9 +115,10 @@ kda_status kda_device_status(void *stream);
  * K = V = 128), the short convolution's tile waits (kda_short_conv_fwd over a prompt)
  * and the fused tensor-core prefill's tile and blob waits (kda_chunk_fwd,
  * kda_chunk_fwd_logits without a workspace or with one in the concurrent form) and the
- * attention kernels' tile waits (kda_attn_decode, kda_attn_prompt) poll their mbarrier at
+ * attention kernels' tile waits (kda_attn_decode, kda_attn_prompt, kda_attn_latent) and the latent
+ * products' (kda_latent_queries, kda_latent_values, kda_latent_expand) poll their mbarrier at
  * most this many times before they give up, for the calls made after this one
- * (process-wide).  polls < 0 restores the default (2^26; the attention kernels never poll
+ * (process-wide).  polls < 0 restores the default (2^26; these never poll
  * more than 2^21 times); 0 makes every such wait give up at once, which tests of the failure
  * handling use (kda_device_status then reports KDA_ERR_TIMEOUT and the outputs hold NaN).  The waits that let copies in
  * flight land before a CTA exits, the tensor-core waits, and the split form's kernels

@@ -18,7 +18,7 @@ namespace {
 thread_local char g_err[512] = "";
 std::atomic<uint64_t> g_launches{0};
 std::atomic<uint32_t> g_wait_polls{kDefaultWaitPolls};
-constexpr int kVersion = 10200;  // 1.2.0
+constexpr int kVersion = 10300;  // 1.3.0
 }  // namespace
 
 uint32_t wait_polls() { return g_wait_polls.load(std::memory_order_relaxed); }
