@@ -289,6 +289,299 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ---------------------------------------------------------------------------
+// The expansion of many tokens, by pairs of CTAs: one product of 256 tokens by a head's 256 outputs on both SMs'
+// tensor cores (cta_group::2), each CTA with its own 128 tokens and half of the head's rows of W.
+// One CTA's tiles of 128 by 256 are bound by shared memory's 128 bytes a cycle: a step of 16 channels takes 12 KB out and
+// 12 KB of copies in, 192 cycles for 128 of the tensor core.  Here W's 128 KB stay where they are for
+// all tokens of a head, so that a step takes 8 KB out and 4 KB in.  A pair takes a run of (head,
+// 256 tokens) in this order; the next head's W replaces the last's chunk by chunk; outputs leave while the
+// next product runs, in the other half of TMEM.
+// 8192 tokens, 32 heads: 52 us (tiles of 128 by 256: 68), 1.3 PFLOP/s.  A product takes 5600 cycles, of which the
+// tensor core's rate would be 4096, and the stores of its outputs about as many beside it: without them it is 42 us, without
+// the products 50.  What a CTA stores goes through the same path as what its tensor core reads.
+
+constexpr int kPairTokens = 256, kPairStages = 6, kChunks = kLatent / 64;
+constexpr uint32_t kPairA = kChunks * kBlock, kPairBars = kPairA + kPairStages * kBlock;
+constexpr uint32_t kSettlePolls = 256;  // a millisecond
+constexpr int kPairThreads = 448, kPairMmaWarp = 8, kPairLoadWarp = 9, kPairSharedWarp = 10;
+
+struct PairBars {
+    uint64_t a_full[kPairStages], w_full[kChunks], acc_empty[2];   // the first CTA's, for both
+    uint64_t a_empty[kPairStages], w_empty[kChunks], acc_full[2];  // each CTA's
+    uint64_t drain, never;
+    uint32_t tmem;
+    int abort;
+};
+constexpr uint32_t kPairSmem = kPairBars + sizeof(PairBars) + 1024;
+static_assert(kPairSmem <= 232448, "shared memory");
+
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void pair_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// As tma_load_3d, the bytes counted on a barrier of either CTA.
+__device__ __forceinline__ void pair_load_3d(uint32_t dst, const void *tmap, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
+        "%4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void pair_load_5d(uint32_t dst, const void *tmap, uint32_t bar, int x, int v) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
+        "%3, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(0), "r"(v), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives at `bar` of both CTAs when what this thread issued so far is through.
+__device__ __forceinline__ void pair_commit(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+// 16 lanes of 64 columns: of each 8 columns a thread has 2 (lane % 4) and the next, of row lane / 4 (registers 0, 1)
+// and of the row eight further (2, 3).
+__device__ __forceinline__ void tmem_ld_quads(uint32_t taddr, float *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ bool pair_try_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    latent_expand_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                              const __grid_constant__ LatentProductParams p, int tiles) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(sm);
+    PairBars &b = *reinterpret_cast<PairBars *>(sm + kPairBars);
+    const uint32_t rank = blockIdx.x & 1, lead = in_cta(sb + kPairBars, 0);  // the first CTA's barriers
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t items = (int64_t)tiles * p.H, pairs = gridDim.x >> 1, i0 = (blockIdx.x >> 1) * items / pairs,
+                  i1 = ((blockIdx.x >> 1) + 1) * items / pairs;
+    volatile int *abort_flag = &b.abort;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kPairStages; ++i) {
+            mbar_init(b.a_full + i, 1);
+            mbar_init(b.a_empty + i, 1);
+        }
+        for (int i = 0; i < kChunks; ++i) {
+            mbar_init(b.w_full + i, 1);
+            mbar_init(b.w_empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(b.acc_empty + i, 16);  // the rows' warps of both
+            mbar_init(b.acc_full + i, 1);
+        }
+        mbar_init(&b.drain, 1);
+        mbar_init(&b.never, 1);
+        b.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kPairMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&b.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    fence_before_sync();
+    __syncthreads();
+    pair_sync();
+    fence_after_sync();
+    const uint32_t tb = b.tmem;
+    auto give_up = [&] {  // both CTAs stop
+        *abort_flag = 1;
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(in_cta(smem_u32(&b.abort), rank ^ 1)), "r"(1) : "memory");
+        return false;
+    };
+    auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t polls) {
+        for (uint32_t i = 0; i < polls; ++i) {
+            if (pair_try_wait(bar, parity)) return true;
+            if (*abort_flag) return false;
+        }
+        return give_up();
+    };
+    if (warp == kPairLoadWarp) {
+        if (elect_one()) {
+            bool ok = true;
+            uint32_t c = 0, heads = 0;  // chunks of tokens so far; heads
+            for (int64_t i = i0; i < i1 && ok; ++i) {
+                const int h = (int)(i / tiles), t = (int)(i - (int64_t)h * tiles);
+                const bool fresh = i == i0 || t == 0;
+                for (int k = 0; k < kChunks && ok; ++k, ++c) {
+                    if (fresh) {
+                        if (heads > 0) ok = wait(b.w_empty + k, (heads - 1) & 1, kAttnPolls);
+                        if (!ok) break;
+                        if (rank == 0) mbar_arrive_expect_tx(b.w_full + k, 2 * kBlock);
+                        pair_load_5d(sb + k * kBlock, &map_w, lead + offsetof(PairBars, w_full) + k * 8, k * 64, 8 * h + 4 * rank);
+                    }
+                    const uint32_t st = c % kPairStages;
+                    if (c >= kPairStages) ok = wait(b.a_empty + st, (c / kPairStages - 1) & 1, kAttnPolls);
+                    if (!ok) break;
+                    if (rank == 0) mbar_arrive_expect_tx(b.a_full + st, 2 * kBlock);
+                    pair_load_3d(sb + kPairA + st * kBlock, &map_x, lead + offsetof(PairBars, a_full) + st * 8, k * 64, 0,
+                                 t * kPairTokens + rank * kTile);
+                }
+                heads += fresh;
+            }
+            // What arrives here has to before the CTA may end: the products' signs for the last chunks, which come
+            // behind the copies.  After a failure some never do: then the copies have a millisecond.
+            for (uint32_t j = c > kPairStages ? c - kPairStages : 0; j < c && ok; ++j)
+                ok = wait(b.a_empty + j % kPairStages, (j / kPairStages) & 1, kAttnPolls);
+            for (int k = 0; k < kChunks && heads > 0 && ok; ++k) ok = wait(b.w_empty + k, (heads - 1) & 1, kAttnPolls);
+        }
+        __syncwarp();
+    } else if (warp == kPairMmaWarp) {
+        if (rank == 0 && elect_one()) {
+            bool ok = true;
+            const uint32_t id = idesc_bf16(kPairTokens, 256, false, false);
+            uint32_t c = 0, heads = 0, n = 0;
+            for (int64_t i = i0; i < i1 && ok; ++i, ++n) {
+                const int t = (int)(i % tiles);
+                const bool fresh = i == i0 || t == 0, last = i == i1 - 1 || t == tiles - 1;
+                if (n >= 2) ok = wait(b.acc_empty + (n & 1), ((n >> 1) - 1) & 1, kAttnPolls);
+                if (!ok) break;
+                for (int k = 0; k < kChunks; ++k, ++c) {
+                    const uint32_t st = c % kPairStages;
+                    if (fresh) ok = wait(b.w_full + k, heads & 1, p.polls);
+                    ok = ok && wait(b.a_full + st, (c / kPairStages) & 1, p.polls);
+                    if (!ok) break;
+                    fence_after_sync();
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        pair_mma(tb + (n & 1) * 256, sdesc(sb + kPairA + st * kBlock + x * 32, 16, 1024),
+                                 sdesc(sb + k * kBlock + x * 32, 16, 1024), id, k > 0 || x > 0);
+                    pair_commit(b.a_empty + st);
+                    if (last) pair_commit(b.w_empty + k);
+                }
+                if (!ok) break;
+                pair_commit(b.acc_full + (n & 1));
+                heads += fresh;
+            }
+            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&b.drain))
+                         : "memory");
+            mbar_wait(&b.drain, 0, kAttnPolls);  // nothing may still run once the CTAs have ended
+        }
+        __syncwarp();
+    } else if (warp >= kPairSharedWarp) {
+        // ---- the shared channels, a copy that depends on nothing else: 32 rows a warp, of 128 bytes, the next
+        // tile's on their way while the last's are stored
+        const int sub = (warp - kPairSharedWarp) * 32 + (lane >> 3), piece = lane & 7;
+        uint4 r[8];
+        auto load = [&](int64_t i) {
+            const int64_t t0 = (i % tiles) * kPairTokens + rank * kTile + sub;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (i < i1 && t0 + j * 4 < p.tokens)
+                    r[j] = __ldg(reinterpret_cast<const uint4 *>(p.x + (t0 + j * 4) * p.x_stride + kLatent) + piece);
+        };
+        load(i0);
+        for (int64_t i = i0; i < i1; ++i) {
+            const int64_t h = i / tiles, t0 = (i - h * tiles) * kPairTokens + rank * kTile + sub;
+            uint4 y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = r[j];
+            load(i + 1);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (t0 + j * 4 < p.tokens) reinterpret_cast<uint4 *>(p.out + ((t0 + j * 4) * p.H + h) * kHeadQuery + kHeadKey)[piece] = y[j];
+        }
+    } else {
+        // ---- outputs: of the head's keys from the first four warps, of its values from the others, 64 bytes of a row
+        // by four threads at once, from registers.  W's rows are taken in such an order (map_w) that a thread's
+        // columns of 32 are eight outputs in a row: column 8 g + 2 c + e is output 8 c + 2 g + e.  (Through shared
+        // memory and TMA they waited behind the copies of the next tokens, 2600 cycles for 16 KB, and their 32 KB are
+        // two more places of the ring.)
+        const int group = warp >> 2, r0 = (warp & 3) * 32;
+        const int width = group == 0 ? kHeadQuery : kHeadValue;
+        __nv_bfloat16 *out = (group == 0 ? p.out : p.out2) + (lane & 3) * 8;
+        uint32_t n = 0;
+        for (int64_t i = i0; i < i1; ++i, ++n) {
+            const int h = (int)(i / tiles), t = (int)(i - (int64_t)h * tiles);
+            const int64_t t0 = (int64_t)t * kPairTokens + rank * kTile + r0;
+            if (!__all_sync(0xffffffffu, wait(b.acc_full + (n & 1), (n >> 1) & 1, kAttnPolls))) break;
+            fence_after_sync();
+            const uint32_t from = tb + ((uint32_t)r0 << 16) + (n & 1) * 256 + group * 128;
+            // All is read before the first store, so that the product after the next never waits for those.
+            uint4 y[4][4];  // 16 rows of 64 outputs each; in these a row's 32 outputs and the next, 8 rows further
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float x[32];
+                tmem_ld_quads(from + ((uint32_t)(q >> 1) << 20) + (q & 1) * 64, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) asm volatile("" : "+f"(x[e]));  // uses stay behind the wait
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float *z = x + 16 * (e & 1) + 2 * (e >> 1);
+                    y[q][e] = make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[4], z[5]), pack_bf16x2(z[8], z[9]),
+                                         pack_bf16x2(z[12], z[13]));
+                }
+            }
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                                 lead + (uint32_t)offsetof(PairBars, acc_empty) + (n & 1) * 8)
+                             : "memory");
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int64_t tok = t0 + e * 8 + (lane >> 2);
+                __nv_bfloat16 *to = out + (tok * p.H + h) * width;
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    if (tok < p.tokens) *reinterpret_cast<uint4 *>(to + 32 * v) = y[(e & 2) + (v >> 1)][(e & 1) * 2 + (v & 1)];
+            }
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (*abort_flag && threadIdx.x == 0) mbar_wait(&b.never, 0, kSettlePolls);
+    pair_sync();
+    fence_after_sync();
+    if (warp == kPairMmaWarp) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tb) : "memory");
+    if (*abort_flag) {  // a bounded wait gave up: this CTA's outputs become NaN
+        __syncthreads();
+        const __nv_bfloat16 nan = __float2bfloat16_rn(kNaN);
+        for (int64_t i = i0; i < i1; ++i) {
+            const int64_t h = i / tiles, t0 = (i - h * tiles) * kPairTokens + rank * kTile;
+            for (int r = threadIdx.x; r < kTile && t0 + r < p.tokens; r += kPairThreads) {
+                const int64_t head = (t0 + r) * p.H + h;
+                for (int e = 0; e < kHeadQuery; ++e) p.out[head * kHeadQuery + e] = nan;
+                for (int e = 0; e < kHeadValue; ++e) p.out2[head * kHeadValue + e] = nan;
+            }
+        }
+        if (threadIdx.x == 0) atomicAdd(&g_latent_product_timeouts, 1);
+    }
+    pair_sync();  // the other's TMEM is given back
+}
+
+// ---------------------------------------------------------------------------
 // host
 
 // A tensor [rows, heads, dim] of bf16 in boxes of 64 channels x 1 head x box_rows.
@@ -365,6 +658,41 @@ kda_status run(const LatentProductParams &p, cudaStream_t st) {
     return check_launch("latent_turn_kernel");
 }
 
+kda_status run_pairs(const LatentProductParams &p, cudaStream_t st) {
+    chunk::EncodeTiledFn enc = reinterpret_cast<chunk::EncodeTiledFn>(tensor_map_encoder());
+    if (!enc) {
+        set_error("latent product: cuTensorMapEncodeTiled is not available from the driver");
+        return KDA_ERR_CUDA;
+    }
+    CUtensorMap mx, mw;
+    // W as [blocks of 32 rows][4][4][2][512 channels], the fours' order turned: see the kernel's outputs
+    const cuuint64_t dims[5] = {(cuuint64_t)kLatent, 2, 4, 4, (cuuint64_t)p.H * 8};
+    const cuuint64_t strides[4] = {kLatent * 2, 8 * kLatent * 2, 2 * kLatent * 2, 32 * kLatent * 2};
+    const cuuint32_t box[5] = {64, 2, 4, 4, 4}, es[5] = {1, 1, 1, 1, 1};
+    const CUresult r = enc(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<__nv_bfloat16 *>(p.w), dims, strides, box, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        set_error("latent product: cuTensorMapEncodeTiled failed (%d)", (int)r);
+        return KDA_ERR_CUDA;
+    }
+    if (!encode(enc, &mx, p.x, kRow, 1, p.tokens, kRow, p.x_stride, 1, kTile))
+        return KDA_ERR_CUDA;
+    static DeviceOnce configured;
+    const int dev = current_device();
+    if (!configured.done(dev)) {
+        if (cudaFuncSetAttribute(latent_expand_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem) != cudaSuccess) {
+            set_error("latent product: cannot reserve shared memory: %s", cudaGetErrorString(cudaGetLastError()));
+            return KDA_ERR_CUDA;
+        }
+        configured.set(dev);
+    }
+    const int64_t tiles = (p.tokens + kPairTokens - 1) / kPairTokens, pairs = std::min<int64_t>(sm_count() / 2, tiles * p.H);
+    latent_expand_pair_kernel<<<(unsigned)(2 * pairs), kPairThreads, kPairSmem, st>>>(mx, mw, p, (int)tiles);
+    note_launch();
+    return check_launch("latent_expand_pair_kernel");
+}
+
 }  // namespace
 
 int take_latent_product_timeouts(cudaStream_t st) {
@@ -384,7 +712,9 @@ int take_latent_product_timeouts(cudaStream_t st) {
 kda_status launch_latent_product(const LatentProductParams &p, cudaStream_t st) {
     if (p.tokens == 0) return KDA_OK;
     // Narrow tiles where wide ones would leave SMs without one.  Expansion by 64, 128 and 256 outputs: 100 tokens, 16
-    // heads 5.4, 5.6, 7.6 us, 64 heads 7.5, 6.2, 7.9; 256 tokens, 72 heads 10.4, 7.7, 9.8, 128 heads 20.1, 15.6, 14.2.  Values
+    // heads 5.4, 5.6, 7.6 us, 64 heads 7.5, 6.2, 7.9; 256 tokens, 72 heads 10.4, 7.7, 9.8, 128 heads 20.1, 15.6, 14.2.  By
+    // tiles of 256 and by pairs, with 1.5 products of 256 tokens a pair 13.5, 13.5, with 1.7 11.5, 12.6, with 2.1 16.5, 14.9,
+    // with 6.7 39.5, 29.2, with 13.5 (8192 tokens, 32 heads) 68.3, 52.1.  Values
     // by 64 and 128: 8 tokens, 32 heads 5.0, 5.3; 256 tokens, 72 heads 6.6, 7.5, 80 heads 10.5, 8.8.  The queries' short sum
     // gains nothing from them: by 64, 128 and 256, 8 tokens, 32 heads 5.1, 4.6, 4.4; 256 tokens, 128 heads 17.0, 14.9, 13.6.
     const int64_t wide = (p.tokens + kTile - 1) / kTile * p.H;
@@ -392,6 +722,7 @@ kda_status launch_latent_product(const LatentProductParams &p, cudaStream_t st) 
     if (p.what == kLatentExpand)
         return wide * 4 < sm_count() ? run<kLatentExpand, 64>(p, st)
                : wide < sm_count()   ? run<kLatentExpand, 128>(p, st)
+               : (p.tokens + kPairTokens - 1) / kPairTokens * p.H >= sm_count() && p.tokens < (1 << 30) ? run_pairs(p, st)
                                      : run<kLatentExpand, 256>(p, st);
     return wide < sm_count() ? run<kLatentValues, 64>(p, st) : run<kLatentValues, 128>(p, st);
 }

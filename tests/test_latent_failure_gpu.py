@@ -64,3 +64,15 @@ def test_products(T, H):
         bad = run_with_zero_limit(call, "latent-product")
         assert all(torch.isnan(t).all() for t in bad)
         assert all(torch.equal(a, b) for a, b in zip(call(), want))
+
+
+def test_expansion_of_many_tokens():
+    """Pairs of CTAs: both give up together."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn((1100, 576), generator=g, device="cuda").bfloat16()
+    w = torch.randn((40, 256, 512), generator=g, device="cuda").bfloat16()
+    call = lambda: kda.latent_expand(x, w)
+    want = call()
+    bad = run_with_zero_limit(call, "latent-product")
+    assert all(torch.isnan(t).all() for t in bad)
+    assert all(torch.equal(a, b) for a, b in zip(call(), want))

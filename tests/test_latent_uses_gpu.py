@@ -238,3 +238,21 @@ def test_products_on_another_stream():
         layer()
     st.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, layer.results()))
+
+
+@pytest.mark.parametrize("T,H", [(300, 152), (513, 110), (1024, 80), (2305, 33), (8192, 10), (257, 160), (20000, 4)])
+def test_expansion_of_many_tokens(T, H):
+    """Tiles that end inside a pair's 256 tokens or inside the first half of them, runs that begin inside a head."""
+    g = gen(T + H)
+    x = torch.randn((T, 64 + ROW), generator=g, device="cuda").bfloat16()[:, 64:]
+    w = weights(H, T + 3)
+    big = torch.full((T + 2, H, 192), 3.0, device="cuda").bfloat16(), torch.full((T + 2, H, 128), 3.0, device="cuda").bfloat16()
+    k, v = kda.latent_expand(x, w, k_out=big[0][1:-1], v_out=big[1][1:-1])
+    kda.device_status()
+    a, b = ref.f64(x[:, :C]), ref.f64(w).flatten(0, 1)
+    want = (a @ b.T).view(T, H, 256)
+    tol = ref.HALF_BF16 * want.abs() + SUM * (a.abs() @ b.abs().T).view(T, H, 256)
+    ref.check("keys", k[..., :128], want[..., :128], tol[..., :128])
+    ref.check("values", v, want[..., 128:], tol[..., 128:])
+    assert torch.equal(k[..., 128:], x[:, None, C:].expand(T, H, R))
+    assert all((y[0] == 3).all() and (y[-1] == 3).all() for y in big)
