@@ -56,8 +56,10 @@ constexpr int kSoftWarps = 4, kScoreWarp = 4, kValueWarp = 5, kLoadWarp = 6, kQu
 constexpr int kQueryWarps = 4;
 constexpr int kThreads = (kQueryWarp + kQueryWarps) * 32;
 constexpr int kSlots = 4;               // work items under way
-constexpr int kPad = 2;                 // a unit's own cost in steps, where pieces have kPadFrom steps or more
-constexpr int kPadFrom = 4;
+// A unit's own cost in steps (its queries' copy, the first data, its output).  By 0, 2, 4 and 6: 37 sequences of 3 to 5000
+// tokens, 1 to 6 rows, 16 heads 42.3, 30.1, 26.2, 25.7 us; 170 of up to 4036, 128 heads 144, 129, 126, 126; 167 of up to
+// 737, 1 to 3 rows, 5 heads 36.6, 31.3, 31.9, 33.4.
+constexpr int kPad = 4;
 constexpr int kMaxShare = 8;            // tiles of a unit at most
 constexpr double kIdle = 0.08;
 constexpr int kMaxUnits = 12;            // ring places of units at most
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         L0 = piece;
         L1 = piece + 1;
         if (pl.cut) {
-            pad = line.total >= (int64_t)kPadFrom * pl.pieces[way] ? kPad : 0;
+            pad = kPad;
             const int64_t places = line.total + pad * line.total_units;
             S = (places + pl.pieces[way] - 1) / pl.pieces[way];
             L0 = piece * S;
