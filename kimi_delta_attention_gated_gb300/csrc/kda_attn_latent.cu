@@ -173,12 +173,20 @@ __device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float *r) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(u[i]);
 }
-// Stores without a branch.
-__device__ __forceinline__ void store_if(bool x, void *p, __nv_bfloat16 v) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.b16 [%0], %1;\n\t}" ::"l"(p),
-                 "h"(__bfloat16_as_ushort(v)), "r"((uint32_t)x)
+// 16 lanes of 16 columns: of each 8 columns a thread has 2 (lane % 4) and the next, of lane / 4 (registers 0, 1) and of
+// the lane eight further (2, 3), which is how the matrices of stmatrix lie.
+__device__ __forceinline__ void tmem_ld_quads(uint32_t taddr, float *r) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                 : "r"(taddr));
+}
+// Four 8 x 8 matrices, turned: a row of memory, 16 bytes at the address from lane 8 * matrix + row, is a column.
+__device__ __forceinline__ void st_turned(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
                  : "memory");
 }
+// Stores without a branch.
 __device__ __forceinline__ void store_if(bool x, void *p, float v) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.f32 [%0], %1;\n\t}" ::"l"(p), "f"(v),
                  "r"((uint32_t)x)
@@ -981,32 +989,64 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (live && p.lse) p.lse[out] = l == 0.f ? -INFINITY : (log2f(l) + m) * kLn2;
                 }
                 soft_sync();
-                // A thread stores its channel of each row, 64 bytes of a row together in a warp.  (The time is that
-                // of the instructions, one warp on each scheduler: three for a value.  With a branch for each
-                // row that may not be there, or lanes that exchange channels for wider stores, twice as many.)
-                const int64_t esz = p.o_bf16 ? 2 : 4;
-                uint8_t *base = static_cast<uint8_t *>(p.o) + (warp * 32 + lane) * esz;
+                if (p.o_bf16) {
+                    // 16 rows and a warp's 32 channels at a time turned in 1 KB of the weights' room, 64 bytes of a row by
+                    // four lanes.  (With a thread's channel of each row in stores of 2 bytes, 128 sequences of 1000 tokens
+                    // took 39.4 us with 64 heads, now 38.0.)
+                    const uint32_t room = sb + pl.at_p + warp * 1024;
+                    const int at_row = ((lane >> 4) << 3) + (lane & 7), at_piece = (lane >> 3) & 1;  // for st_turned
+                    __nv_bfloat16 *base = static_cast<__nv_bfloat16 *>(p.o) + warp * 32 + (lane & 3) * 8;
 #pragma unroll 1
-                for (int r0 = 0; r0 < (int)q_rows; r0 += 16) {
-                    float o[64], f[16];
+                    for (int r0 = 0; r0 < (int)q_rows; r0 += 16) {
+                        float o[64], f[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld16f(tb + lane_base + kTmemO + q * pl.n + r0, o + 16 * q);
+                        for (int i = 0; i < 8; ++i)
+                            tmem_ld_quads(tb + lane_base + ((uint32_t)(i & 1) << 20) + kTmemO + (i >> 1) * pl.n + r0, o + 8 * i);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) f[i] = b.factor[r0 + i];
-                    wait_ld<64>(o);
-                    if (nt == 0) {  // (then TMEM holds anything)
+                        for (int i = 0; i < 4; ++i) f[i] = b.factor[r0 + (i >> 1) * 8 + 2 * (lane & 3) + (i & 1)];
+                        const int64_t to[2] = {b.row_at[r0 + (lane >> 2)], b.row_at[r0 + 8 + (lane >> 2)]};
+                        wait_ld<64>(o);
+                        if (nt == 0) {  // (then TMEM holds anything)
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) o[i] = 0.f;
-                    }
-                    if (p.o_bf16) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int64_t row_at = b.row_at[r0 + i];
-                            uint8_t *at = base + row_at * (kLatent * 2);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) store_if(row_at >= 0, at + q * 256, __float2bfloat16_rn(o[16 * q + i] * f[i]));
+                            for (int i = 0; i < 64; ++i) o[i] = 0.f;
                         }
-                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {  // 16 channels
+                                const float *x = o + 16 * q + 8 * half;
+                                st_turned(room + at_row * 64 + (((2 * half + at_piece) ^ ((at_row >> 1) & 3)) << 4),
+                                          pack_bf16x2(x[0] * f[0], x[1] * f[1]), pack_bf16x2(x[2] * f[0], x[3] * f[1]),
+                                          pack_bf16x2(x[4] * f[2], x[5] * f[3]), pack_bf16x2(x[6] * f[2], x[7] * f[3]));
+                            }
+                            __syncwarp();
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int row8 = j * 8 + (lane >> 2);
+                                uint4 v;
+                                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                             : "r"(room + row8 * 64 + (((lane & 3) ^ ((row8 >> 1) & 3)) << 4)));
+                                if (to[j] >= 0) *reinterpret_cast<uint4 *>(base + to[j] * kLatent + q * 128) = v;
+                            }
+                            __syncwarp();  // read before the next is written
+                        }
+                    }
+                } else {
+                    // a thread stores its channel of each row, 128 bytes of a row together in a warp
+                    uint8_t *base = static_cast<uint8_t *>(p.o) + (warp * 32 + lane) * 4;
+#pragma unroll 1
+                    for (int r0 = 0; r0 < (int)q_rows; r0 += 16) {
+                        float o[64], f[16];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) tmem_ld16f(tb + lane_base + kTmemO + q * pl.n + r0, o + 16 * q);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) f[i] = b.factor[r0 + i];
+                        wait_ld<64>(o);
+                        if (nt == 0) {
+#pragma unroll
+                            for (int i = 0; i < 64; ++i) o[i] = 0.f;
+                        }
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const int64_t row_at = b.row_at[r0 + i];
@@ -1213,7 +1253,8 @@ Plan plan_of(int64_t N, int64_t tokens, int H, int64_t max_tokens) {
         pl.most_places = std::max(pl.most_places, most_units[w] * pl.G[w]);
     }
     pl.by_unit = pl.most_places < pl.ctas;
-    const int64_t q = (int64_t)pl.hp * pl.tk * kSmemBlocks * 128, ps = (int64_t)pl.n * 128;
+    const int64_t q = (int64_t)pl.hp * pl.tk * kSmemBlocks * 128;
+    const int64_t ps = std::max<int64_t>(pl.n * 128, kSoftWarps * 1024);  // (the output is turned there, too)
     const int64_t room = kMaxSmem - 1024 - (int64_t)round_up(sizeof(Bars), 128) - round_up(q, 1024) - round_up(ps, 1024);
     pl.units = (int)std::min<int64_t>(kMaxUnits, (room - kShared * kSharedBytes) / kUnitBytes);
     pl.at_p = (uint32_t)round_up(q, 1024);
