@@ -60,6 +60,11 @@ constexpr int kSlots = 4;               // work items under way
 // tokens, 1 to 6 rows, 16 heads 42.3, 30.1, 26.2, 25.7 us; 170 of up to 4036, 128 heads 144, 129, 126, 126; 167 of up to
 // 737, 1 to 3 rows, 5 heads 36.6, 31.3, 31.9, 33.4.
 constexpr int kPad = 4;
+constexpr int kMostPieces = 160, kMostSteps = 1 << 19;
+// What cutting costs in steps at most (the sums' way through L2, their joining): units stay whole where no piece gets that
+// much more by it.  Cut and whole: 64 sequences of 1000 tokens, 4 rows, 32 heads 47.4, 38.7 us; 256 sequences of about 1000,
+// 64 heads 81.6, 74.5, 128 heads (more by 16 steps) 110, 114; 180 of 200 to 400 tokens, 16 heads (by 10) 27.0, 31.4.
+constexpr int kCutCost = 12;
 constexpr int kMaxShare = 8;            // tiles of a unit at most
 constexpr double kIdle = 0.08;
 constexpr int kMaxUnits = 12;            // ring places of units at most
@@ -115,8 +120,13 @@ struct Bars {
     uint64_t q_full, q_empty, p_free, drain[2], s_full[2], i_full[kSlots];  // one
     uint64_t u_full[kMaxUnits], u_empty[kMaxUnits], r_full[kShared], r_empty[kShared];
     Item slots[kSlots];
-    int64_t row_at[kTileRows];   // a row's place in o, or -1
-    float factor[kTileRows];
+    union {
+        struct {
+            int64_t row_at[kTileRows];  // a row's place in o, or -1
+            float factor[kTileRows];
+        };
+        int load[kMostPieces];          // while the line is measured: steps of the units that begin in a piece
+    };
     int64_t scan[kThreads / 32][4];
     int64_t start_begin, start_unit;
     int start_seq;
@@ -343,6 +353,7 @@ __device__ __forceinline__ int4 *join_words(const Args &a) {
 // Goes through the work items of one tile place `g` of a piece.
 struct Walk {
     int way, G;
+    bool whole;                // units go whole to the piece that they begin in
     int64_t L0, L1, S, begin;  // the piece, the next unit's place on the line (without cuts: units)
     int n, u, units, nq, len;  // the next unit: its sequence, and number there
     int64_t t0;
@@ -360,8 +371,9 @@ struct Walk {
         units = units_of(a.plan, way, nq);
         open = true;
     }
-    __device__ void start(const Args &a, int split, int64_t l0, int64_t l1, int64_t s, int own, int seq, int64_t seq_begin, int64_t seq_unit) {
+    __device__ void start(const Args &a, int split, bool uncut, int64_t l0, int64_t l1, int64_t s, int own, int seq, int64_t seq_begin, int64_t seq_unit) {
         way = split;
+        whole = uncut;
         G = a.plan.G[way];
         L0 = l0;
         L1 = l1;
@@ -395,9 +407,9 @@ struct Walk {
                 open = false;
             }
             // (a cu_seqlens that does not ascend may have more units than there is room for)
-            const int64_t starts = at + (t.steps ? pad : 0);
+            const int64_t starts = at + (t.steps && !whole ? pad : 0);
             if (words && pl.cut && pl.by_unit && number * G + g < pl.most_places && starts >= L0 && starts < L1) {
-                const int last = t.steps ? (int)((first + t.steps - 1) / S) : piece;
+                const int last = t.steps && !whole ? (int)((first + t.steps - 1) / S) : piece;
                 join_words(a)[number * G + g] = make_int4(t.t0, t.head0 | t.tokens << 16, piece, t.tokens ? last : piece);
             }
             if (t.tokens == 0) continue;
@@ -406,7 +418,7 @@ struct Walk {
             it.head0 = t.head0;
             it.seen0 = t.seen0;
             it.part = -1;
-            if (!pl.cut || t.steps == 0) {
+            if (whole || t.steps == 0) {
                 if (at < L0) continue;  // the piece's before
                 it.s0 = 0;
                 it.s1 = t.steps;
@@ -454,6 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                               : 1);
         fence_mbar_init();
     }
+    if (threadIdx.x < kMostPieces) b.load[threadIdx.x] = 0;
     if (threadIdx.x == kThreads - 1) {
         b.abort = 0;
         b.start_seq = -1;
@@ -477,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The piece: places of the line, or without cuts units.
     int64_t L0, L1, S = 1;
     int pad = 0, way = 0, piece;
+    bool whole = !pl.cut;
     int start_seq;
     int64_t start_begin, start_unit = 0, total_units = 0;
     if (!pl.cut && !p.cu_seqlens) {  // as many units in every sequence
@@ -499,6 +513,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             L1 = min(L0 + S, places);
             total_units = line.total_units;
         }
+        // With a few units a piece it may take less time to leave them whole.
+        const bool look = pl.cut && 2 * total_units > pl.pieces[way] && total_units <= 8 * pl.pieces[way] && S < kMostSteps &&
+                          pl.pieces[way] <= kMostPieces;
         int64_t at = pl.cut ? line.mine + pad * line.units : line.units, units = line.units;
         for (int n = line.first; n < line.last; ++n) {
             const int64_t more = (int64_t)units_of(a, way, n) * (pl.cut ? seq_steps(a, n) + pad : 1);
@@ -507,8 +524,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 b.start_begin = at;
                 b.start_unit = units;
             }
+            if (look) {
+                // (one with many units is cut: they are too many to look at by one thread)
+                const int each = seq_steps(a, n) + pad, most = more > 8 * (int64_t)each ? 2 * kMostSteps : min(each, 2 * kMostSteps);
+                for (int64_t x = at; x < at + (most == each ? more : min(more, (int64_t)1)); x += each) atomicAdd(&b.load[x / S], most);
+            }
             at += more;
             units += units_of(a, way, n);
+        }
+        if (look) {
+            __syncthreads();
+            int most = 0;
+            for (int i = lane; i < pl.pieces[way]; i += 32) most = max(most, b.load[i]);
+            whole = __reduce_max_sync(0xffffffffu, most) <= S + min(kCutCost, 4 + pl.n / 4);
         }
     }
     fence_before_sync();
@@ -553,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
             const int half = warp - kLoadWarp;
             Walk w;
-            w.start(a, way, L0, L1, S, pad, start_seq, start_begin, start_unit);
+            w.start(a, way, whole, L0, L1, S, pad, start_seq, start_begin, start_unit);
             uint32_t us = 0, up = 1;           // ring place of the step's first unit, and the parity of the wait for it (a
                                                // barrier's phase before its first counts as over)
             uint32_t rs = 0, rp = 1, steps = 0;
@@ -1072,7 +1100,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // After a failure every row of this CTA's items becomes NaN.
     if (*abort_flag) {
         Walk w;
-        w.start(a, way, L0, L1, S, pad, start_seq, start_begin, start_unit);
+        w.start(a, way, whole, L0, L1, S, pad, start_seq, start_begin, start_unit);
         for (;;) {
             const Item it = w.next(a, piece, g, threadIdx.x == 0);
             if (!it.found) break;
