@@ -698,8 +698,8 @@ kda_status kda_latent_queries(const void *q, int64_t q_stride, int64_t tokens, i
  *   q           [tokens, heads, KDA_LATENT_ROW] bf16, q_stride apart (kda_latent_queries); at most 2^24
  *               tokens
  *   cu_seqlens  [n_seqs + 1] int32: sequence n's tokens are rows [cu_seqlens[n], cu_seqlens[n + 1])
- *               (clamped to [0, tokens]); rows of no sequence are left as they are.  NULL: one token
- *               per sequence, tokens == n_seqs
+ *               (clamped to [0, tokens], not descending); rows of no sequence are left as they are.
+ *               NULL: one token per sequence, tokens == n_seqs
  *   seq_lens    [n_seqs] int32, clamped to [0, max_blocks * page_size]
  *   scale       not 0, within 2^100 (192^-1/2 for the layer)
  *   o           [tokens, heads, KDA_LATENT_DIM] o_dtype

@@ -26,14 +26,16 @@
 // L2) are numbered in one line, kPad places before each unit standing for what it costs beside its steps; the
 // line is cut into equal pieces.  Units that more than one CTA took leave their sums in a
 // workspace, and attn_latent_join_kernel adds them in their order, so results do not depend on timing.
-// Where the table is narrow, units stay whole and the second launch falls away: see plan_of.
+// Where the lengths allow it, units go whole to the piece that they begin in; where the table's width already says so
+// (plan_of), the second launch falls away.
 //
-// What bounds it.  Up to 64 heads: HBM.  8 sequences of 60000 tokens: 94 us with 16 heads, 103 with 64,
-// 5.9 and 5.4 TB/s of 6.7 that a copy reaches.  96 and 128 heads are two tiles and twice the products: 140 and
-// 144 us, 2300 cycles a step of which the tensor core works 1900 (S reads 72 KB of C and 40 KB of Q through
+// What bounds it.  Up to 64 heads and long contexts: HBM.  8 sequences of 60000 tokens: 96 us with 16 heads, 104 with 64,
+// 5.8 and 5.3 TB/s of 6.7 that a copy reaches.  96 and 128 heads are two tiles and twice the products: 140 and
+// 143 us, 2300 cycles a step of which the tensor core works 1900 (S reads 72 KB of C and 40 KB of Q through
 // shared memory's 128 bytes a cycle, O^T 64 KB of C and P four times); the rest are the waits of the chain scores,
 // softmax, weights, O^T.  Short calls are launches and latencies: one sequence of 1000 tokens 14 us, of which the
-// set-up takes 3, the first data 2, the output 4 and the joining launch 5.
+// set-up takes 3, the first data 2, the output 3 and the joining launch 5; 128 of about 1000 tokens, 32 heads, 35 us, HBM's
+// 22 between such a beginning and end.  An item's end in the middle of a CTA's run costs about 4 steps (kPad).
 #include <cuda.h>
 
 #include <climits>
@@ -1268,11 +1270,11 @@ Plan plan_of(int64_t N, int64_t tokens, int H, int64_t max_tokens) {
         most_units[w] = tokens == N ? N * units_of(pl, w, 1) : units_of(pl, w, (int)tokens) + N;
     }
     const int64_t per = (max_tokens + kStep - 1) / kStep;
-    // Units are cut where that balances more than it costs (the sums' way through L2 and the second launch, 5 to 8
-    // us).  The lengths are not known here, only the table's width.  Cut and whole, 32 heads: 16 sequences of
-    // at most 256, 512, 1024 tokens 13.4 and 12.0, 16.0 and 16.5, 19.9 and 25.3 us; 76 of 1024, 2048 tokens 29.8 and
-    // 29.5, 44.2 and 49.5; 128 of 1024, 2048, 4096 tokens 43.2 and 34.2, 65.8 and 57.2, 109 and 102, but of
-    // 100 to 4096 tokens 67.5 and 91.2.
+    // Units are cut where that balances more than it costs (the sums' way through L2 and the second launch).  The lengths
+    // are not known here, only the table's width: where it says enough, the second launch falls away.  Cut and whole,
+    // 32 heads: 16 sequences of at most 256, 512, 1024 tokens 14.3 and 11.7, 15.9 and 15.8, 17.8 and 24.0 us; 76 of 1024,
+    // 2048 tokens 30.8 and 27.3, 44.4 and 45.4; 128 of 1024, 2048, 4096 tokens 37.7 and 32.6, 59.2 and 54.3, 108 and 96,
+    // but of 100 to 4096 tokens 68.0 and 82.8.
     pl.cut = !(most_units[0] <= sms[0] && (per <= 4 || per * sms[0] <= 44 * most_units[0]));
     if (!pl.cut) pl.G[1] = pl.G[0], pl.units_one[1] = pl.units_one[0], most_units[1] = most_units[0];
     for (int w = 0; w < 2; ++w) {

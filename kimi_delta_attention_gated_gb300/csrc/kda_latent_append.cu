@@ -6,6 +6,10 @@
 // where the rows are wanted densely too).  A warp takes a run of tokens, whose sequence it looks for
 // once, with the next token's row on its way; a lane has two 16-byte pieces of c, so that the norm needs
 // one warp sum, and eight lanes have the pieces of r.
+//
+// 86824 tokens, normalised and turned, rows wanted: 56 us, 5.4 TB/s of 6.7 that a copy reaches; without the dense rows 53
+// (57 %: each warp's chain of norm, turn and store for one token at a time), without turning 40 (75 %).  One token
+// of 256 sequences: 2.8 us, a launch.
 #include "kda_latent.cuh"
 
 namespace kda {

@@ -10,7 +10,13 @@
 // CTAs on an SM so that one's copies and stores run beside another's products.  W's inner index is the
 // latent's channel: for the values and the expansion that is the sum's index (K-major), for the queries
 // the output's (MN-major); the same bytes serve both.  Operands come by TMA, results leave by
-// TMA through swizzled shared memory, which also cuts off the rows behind the last token.
+// TMA through swizzled shared memory, which also cuts off the rows behind the last token.  The expansion of
+// many tokens has a kernel of its own for pairs of SMs.
+//
+// What bounds it, and the floor by bytes or operations: queries, 256 tokens of 128 heads with turned channels 15 us (10), bytes
+// of which half are W; 8192 of 32 heads 94 (61), each CTA's own chain of copy, product and output, two of which an SM
+// holds.  Values, 256 tokens of 128 heads 12 (8.8); 8192 of 32 heads 58 (51), 88 % of a copy's rate.  Expansion, 100 tokens of 16 heads
+// 5.3, a launch and the chain of one tile; 8192 of 32 heads 52 (36), see there.
 #include <cuda.h>
 
 #include <algorithm>
