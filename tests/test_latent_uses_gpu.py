@@ -256,3 +256,16 @@ def test_expansion_of_many_tokens(T, H):
     ref.check("values", v, want[..., 128:], tol[..., 128:])
     assert torch.equal(k[..., 128:], x[:, None, C:].expand(T, H, R))
     assert all((y[0] == 3).all() and (y[-1] == 3).all() for y in big)
+
+
+@pytest.mark.parametrize("lens,new,H", [
+    ([1000] * 64, [4] * 64, 32),                                # units whole, a few a piece
+    ([1000] * 64, [4] * 60 + [7, 0, 1, 9], 32),
+    ([900 + 3 * i % 200 for i in range(256)], None, 64),
+    ([260 + 7 * i % 90 for i in range(170)] + [0] * 10, None, 16),
+    ([300] * 170 + [9000], None, 16),                           # one sequence far longer: cut
+    ([300] * 100 + [700] * 100, [1, 2] * 100, 128),
+])
+def test_units_left_whole(lens, new, H):
+    """About as many units as pieces, of equal and of unequal lengths."""
+    case(lens, H, 64, new, seed=H + len(lens), heads=[0, H - 1], tokens=[0, 1, 3, 6, 8])
