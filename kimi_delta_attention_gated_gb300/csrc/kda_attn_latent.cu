@@ -83,7 +83,7 @@ constexpr uint32_t kLastPolls = 256;    // for copies after a failure: a millise
 __device__ int g_attn_latent_timeouts = 0;
 
 struct Plan {
-    int hp, tk;       // heads (a multiple of 8) and tokens of a tile: hp * tk rows
+    int hp, tk;       // heads and tokens of a tile: hp * tk rows
     int parts;        // tiles that share a token's heads
     // Two ways to split, of which the lengths decide (without cuts both are the first).
     int G[2];         // tiles of a unit
@@ -93,7 +93,8 @@ struct Plan {
     int cut;          // units may be cut; else piece i is the i-th unit
     int by_unit;      // the joining launch goes by units, else by pieces
     int64_t most_places;  // tiles' places in the call's units at most
-    int n;            // rows of a tile as the products' N: hp * tk, a multiple of 16
+    int n;            // rows of a tile as the products' N: hp * tk up to a multiple of 16
+    int q_rows;       // and as they lie in shared memory: up to a multiple of 8
     int units;        // ring places
     uint32_t at_p, at_units, at_shared, at_bars;  // shared memory
 };
@@ -713,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if (warp == kScoreWarp) {
                 const uint32_t id = idesc_bf16(64, kStep, false, false, p.scale < 0.f);
-                const uint32_t q_lo = sb16 | k_major, q_chunk = q_rows * 128 >> 4, r_at = sb16 + (pl.at_shared >> 4);
+                const uint32_t q_lo = sb16 | k_major, q_chunk = pl.q_rows * 128 >> 4, r_at = sb16 + (pl.at_shared >> 4);
                 uint32_t rs = 0, rp = 0;
                 for (uint32_t k = 0; ok; ++k) {
                     const int nt = next_item(k);
@@ -725,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     mbar_arrive_expect_tx(&b.q_full, kSmemBlocks * q_rows * 128);
                     for (int x = 0; x < kSmemBlocks; ++x)
-                        tma_load_3d(sb + x * q_rows * 128, &map_q, &b.q_full, x == kSmemBlocks - 1 ? kLatent : x * 64, head0, t0);
+                        tma_load_3d(sb + x * pl.q_rows * 128, &map_q, &b.q_full, x == kSmemBlocks - 1 ? kLatent : x * 64, head0, t0);
                     ok = wait_for(&b.q_full, items & 1, p.polls);
                     if (!ok) mbar_wait(&b.q_full, items & 1, kAttnPolls);  // it still has to land before the CTA may end
                     ok = ok && wait_for(&b.qt_full, items & 1, kAttnPolls);
@@ -1139,10 +1140,15 @@ __global__ void __launch_bounds__(128 * kMaxShares) attn_latent_join_kernel(cons
     const int G = of.y, which = blockIdx.x / G, g = blockIdx.x - which * G;
     const JoinWord t = *reinterpret_cast<const JoinWord *>(&word);
     const int share = warp >> 2, q = warp & 3, k0 = t.first, k1 = t.last;
-    const int r = 4 * blockIdx.y;  // the first of the rows, all of one token
-    const int tok = r / pl.hp, head = (t.place & 0xFFFF) + r - tok * pl.hp;
-    if (which >= of.x || k0 >= k1 || tok >= t.place >> 16 || head >= p.H) return;
-    const int64_t out = (int64_t)(t.t0 + tok) * p.H + head;
+    const int r = 4 * blockIdx.y;  // the first of the rows
+    if (which >= of.x || k0 >= k1) return;
+    int64_t out[4];  // their places, or -1
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int tok = (r + e) / pl.hp, head = (t.place & 0xFFFF) + r + e - tok * pl.hp;
+        out[e] = tok < t.place >> 16 && head < p.H ? (int64_t)(t.t0 + tok) * p.H + head : -1;
+    }
+    if (max(max(out[0], out[1]), max(out[2], out[3])) < 0) return;
     float m[4], l[4], acc[4][4];  // of the rows; of channels lane + 32 * i
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -1220,11 +1226,11 @@ __global__ void __launch_bounds__(128 * kMaxShares) attn_latent_join_kernel(cons
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        if (head + e >= p.H) break;
+        if (out[e] < 0) continue;
         const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st_out(p.o, (out + e) * kLatent + q * 128 + lane + 32 * i, acc[i][e] * inv, p.o_bf16);
-        if (q == 0 && lane == 0 && p.lse) p.lse[out + e] = l[e] == 0.f ? -INFINITY : (log2f(l[e]) + m[e]) * kLn2;
+        for (int i = 0; i < 4; ++i) st_out(p.o, out[e] * kLatent + q * 128 + lane + 32 * i, acc[i][e] * inv, p.o_bf16);
+        if (q == 0 && lane == 0 && p.lse) p.lse[out[e]] = l[e] == 0.f ? -INFINITY : (log2f(l[e]) + m[e]) * kLn2;
     }
 }
 
@@ -1248,16 +1254,17 @@ int share_of(int64_t tiles) {
 }
 
 // How a call is split.  Tiles: all heads of as many tokens as 64 rows hold, or with more than 64 heads
-// equal parts of one token's.
+// equal parts of one token's.  (Heads filled up to eight, as a tile's blocks need, wasted rows: 13 sequences of 81 rows, 2
+// heads 696 and now 193 us; 64 of 5 rows, 12 heads 60 and 50.)
 Plan plan_of(int64_t N, int64_t tokens, int H, int64_t max_tokens) {
     Plan pl;
     memset(&pl, 0, sizeof(pl));
     const int64_t avg = (tokens + N - 1) / N;  // rows of a sequence
     pl.parts = (H + kTileRows - 1) / kTileRows;
-    pl.hp = (int)round_up((H + pl.parts - 1) / pl.parts, 8);
-    pl.parts = (H + pl.hp - 1) / pl.hp;
+    pl.hp = (H + pl.parts - 1) / pl.parts;
     pl.tk = (int)std::max<int64_t>(1, std::min<int64_t>(kTileRows / pl.hp, avg));
     pl.n = (int)round_up(pl.hp * pl.tk, 16);
+    pl.q_rows = (int)round_up(pl.hp * pl.tk, 8);
     const int64_t tiles = (avg + pl.tk - 1) / pl.tk * pl.parts;
     // A token's tiles are shared in either way; a sequence's too where all have about as many rows.
     pl.G[0] = share_of(pl.parts);
@@ -1283,7 +1290,7 @@ Plan plan_of(int64_t N, int64_t tokens, int H, int64_t max_tokens) {
         pl.most_places = std::max(pl.most_places, most_units[w] * pl.G[w]);
     }
     pl.by_unit = pl.most_places < pl.ctas;
-    const int64_t q = (int64_t)pl.hp * pl.tk * kSmemBlocks * 128;
+    const int64_t q = (int64_t)pl.q_rows * kSmemBlocks * 128;
     const int64_t ps = std::max<int64_t>(pl.n * 128, kSoftWarps * 1024);  // (the output is turned there, too)
     const int64_t room = kMaxSmem - 1024 - (int64_t)round_up(sizeof(Bars), 128) - round_up(q, 1024) - round_up(ps, 1024);
     pl.units = (int)std::min<int64_t>(kMaxUnits, (room - kShared * kSharedBytes) / kUnitBytes);
@@ -1383,7 +1390,7 @@ kda_status launch_attn_latent(const AttnLatentParams &p, cudaStream_t st) {
     if (!pl.cut || s != KDA_OK) return s;
     // with many pieces a unit more warps share them
     const int shares = pl.ctas >= 16 * pl.most_places ? kMaxShares : 1;
-    cfg.gridDim = dim3((unsigned)words_of(pl), pl.hp * pl.tk / 4);
+    cfg.gridDim = dim3((unsigned)words_of(pl), (pl.hp * pl.tk + 3) / 4);
     cfg.blockDim = dim3(128 * shares);
     cfg.dynamicSmemBytes = (shares - 1) * 4 * (128 + 2) * sizeof(float4);
     e = cudaLaunchKernelEx(&cfg, attn_latent_join_kernel, a, shares);

@@ -269,3 +269,10 @@ def test_expansion_of_many_tokens(T, H):
 def test_units_left_whole(lens, new, H):
     """About as many units as pieces, of equal and of unequal lengths."""
     case(lens, H, 64, new, seed=H + len(lens), heads=[0, H - 1], tokens=[0, 1, 3, 6, 8])
+
+
+@pytest.mark.parametrize("H", [1, 2, 3, 5, 7, 12, 20, 50, 70, 100, 193])
+@pytest.mark.parametrize("lens,new", [([700, 130], [81, 5]), ([3000, 40, 66], [3, 2, 1]), ([90], None), ([5000, 12], None)])
+def test_tiles_of_any_heads(H, lens, new):
+    """Heads that fill a tile's rows unevenly: tokens that begin anywhere in it."""
+    case(lens, H, 32, new, seed=H, heads=sorted({0, H // 2, H - 1}), tokens=[0, 1, 2, 4, 11, 12, 31, 33, 64, 80])
