@@ -13,9 +13,9 @@
 // row's 64 weights are one swizzled 128-byte line.
 //
 // Shared memory is what limits a tile to 64 rows and the ring to two and a half steps of the cache: of
-// a query's nine blocks of 64 channels five lie there (40 KB), and the other four in TMEM, which a
+// a query's nine blocks of 64 channels five or three lie there, and the other four or six in TMEM, which a
 // product of 64 rows may read its first operand from and has room beside O^T and two steps' scores
-// (8 sequences of 60000 tokens, 96 heads: 151 to 140 us).  The cache arrives by TMA in a ring of
+// (8 sequences of 60000 tokens, 96 heads: 151 us with all in shared memory, 140 and 134).  The cache arrives by TMA in a ring of
 // 128-channel units of 16 KB (the shared channels in one of their own of 8 KB), and a unit is free again
 // when the one product of O^T that reads it is through.  (Units of 32 KB, half the waits: 145 us.)  A step's scores
 // are formed while the softmax works on the last step's.  The softmax's reference moves only where a row's maximum
@@ -30,10 +30,10 @@
 // (plan_of), the second launch falls away.
 //
 // What bounds it.  Up to 64 heads and long contexts: HBM.  8 sequences of 60000 tokens: 96 us with 16 heads, 104 with 64,
-// 5.8 and 5.3 TB/s of 6.7 that a copy reaches.  96 and 128 heads are two tiles and twice the products: 140 and
-// 143 us, 2300 cycles a step of which the tensor core works 1900 (S reads 72 KB of C and 40 KB of Q through
-// shared memory's 128 bytes a cycle, O^T 64 KB of C and P four times); the rest are the waits of the chain scores,
-// softmax, weights, O^T.  Short calls are launches and latencies: one sequence of 1000 tokens 14 us, of which the
+// 5.8 and 5.3 TB/s of 6.7 that a copy reaches.  96 and 128 heads are two tiles and twice the products: 134 and
+// 143 us, 2200 and 2300 cycles a step of which the tensor core works 1900 (S reads 72 KB of C and up to 40 KB of Q through
+// shared memory's 128 bytes a cycle, O^T 64 KB of C and P four times); the rest is the ring's depth (a place less: 152 us
+// with 128 heads; weights in two buffers instead gain nothing).  Short calls are launches and latencies: one sequence of 1000 tokens 14 us, of which the
 // set-up takes 3, the first data 2, the output 3 and the joining launch 5; 128 of about 1000 tokens, 32 heads, 35 us, HBM's
 // 22 between such a beginning and end.  An item's end in the middle of a CTA's run costs about 4 steps (kPad).
 #include <cuda.h>
@@ -72,8 +72,7 @@ constexpr double kIdle = 0.08;
 constexpr int kMaxUnits = 12;            // ring places of units at most
 constexpr uint32_t kShared = 2;         // and of the shared channels
 constexpr uint32_t kUnitBytes = kStep * 256, kSharedBytes = kStep * 128;
-constexpr uint32_t kTmemO = 2 * kStep, kTmemQ = kTmemO + 4 * kTileRows;  // TMEM columns: scores of two steps, O^T, queries
-constexpr int kSmemBlocks = 5;          // of a query's nine blocks of 64 channels: in shared memory, the others in TMEM
+constexpr uint32_t kTmemO = 2 * kStep;   // TMEM columns: scores of two steps, O^T, then queries
 constexpr float kSlack = 8.f;           // log2: how far a score may exceed the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNaN = __builtin_nanf("");
@@ -95,6 +94,7 @@ struct Plan {
     int64_t most_places;  // tiles' places in the call's units at most
     int n;            // rows of a tile as the products' N: hp * tk up to a multiple of 16
     int q_rows;       // and as they lie in shared memory: up to a multiple of 8
+    int q_units;      // of queries in shared memory: attn_latent_kernel's QU
     int units;        // ring places
     uint32_t at_p, at_units, at_shared, at_bars;  // shared memory
 };
@@ -445,6 +445,9 @@ struct Walk {
     }
 };
 
+// QU: of a query's four units of 128 channels, in shared memory; the others lie in TMEM, whose 512 columns are 128 of scores,
+// 4 n of O^T and 64 a unit.
+template <int QU>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_latent_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_c,
                        const __grid_constant__ CUtensorMap map_r, const __grid_constant__ Args a) {
@@ -456,6 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Bars &b = *reinterpret_cast<Bars *>(sm + pl.at_bars);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t q_rows = pl.hp * pl.tk;
+    constexpr int kQBlocks = 2 * QU + 1;  // of 64 channels, in shared memory; the last: the shared channels
     volatile int *abort_flag = &b.abort;
 
     if (pl.cut) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -715,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (warp == kScoreWarp) {
                 const uint32_t id = idesc_bf16(64, kStep, false, false, p.scale < 0.f);
                 const uint32_t q_lo = sb16 | k_major, q_chunk = pl.q_rows * 128 >> 4, r_at = sb16 + (pl.at_shared >> 4);
+                const uint32_t t_q = tb + kTmemO + 4 * pl.n;
                 uint32_t rs = 0, rp = 0;
                 for (uint32_t k = 0; ok; ++k) {
                     const int nt = next_item(k);
@@ -724,9 +729,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // copies do not wait for that: 6000 cycles at the border of two items)
                     if (items > 0) ok = wait_for(&b.q_empty, (items - 1) & 1, kAttnPolls);
                     if (!ok) break;
-                    mbar_arrive_expect_tx(&b.q_full, kSmemBlocks * q_rows * 128);
-                    for (int x = 0; x < kSmemBlocks; ++x)
-                        tma_load_3d(sb + x * pl.q_rows * 128, &map_q, &b.q_full, x == kSmemBlocks - 1 ? kLatent : x * 64, head0, t0);
+                    mbar_arrive_expect_tx(&b.q_full, kQBlocks * q_rows * 128);
+                    for (int x = 0; x < kQBlocks; ++x)
+                        tma_load_3d(sb + x * pl.q_rows * 128, &map_q, &b.q_full, x == kQBlocks - 1 ? kLatent : x * 64, head0, t0);
                     ok = wait_for(&b.q_full, items & 1, p.polls);
                     if (!ok) mbar_wait(&b.q_full, items & 1, kAttnPolls);  // it still has to land before the CTA may end
                     ok = ok && wait_for(&b.qt_full, items & 1, kAttnPolls);
@@ -737,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         fence_after_sync();
                         {
-                            const uint32_t lo = (r_at + rs * (kSharedBytes >> 4)) | k_major, ql = q_lo + (kSmemBlocks - 1) * q_chunk;
+                            const uint32_t lo = (r_at + rs * (kSharedBytes >> 4)) | k_major, ql = q_lo + (kQBlocks - 1) * q_chunk;
 #pragma unroll
                             for (int x = 0; x < 4; ++x) mma_ss(t_s, desc_of(ql + 2 * x), desc_of(lo + 2 * x), id, x > 0);
                             mma_commit(b.r_empty + rs);
@@ -752,10 +757,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int x = 0; x < 8; ++x) {
                                 const uint64_t rows = desc_of(lo + (x >> 2) * (kSharedBytes >> 4) + 2 * (x & 3));
-                                if (m < 2)
+                                if (m < QU)
                                     mma_ss(t_s, desc_of(ql + (x >> 2) * q_chunk + 2 * (x & 3)), rows, id, 1);
                                 else
-                                    mma_ts(t_s, tb + kTmemQ + (m - 2) * 64 + 8 * x, rows, id, 1);
+                                    mma_ts(t_s, t_q + (m - QU) * 64 + 8 * x, rows, id, 1);
                             }
                             if (++us == (uint32_t)pl.units) us = 0, up ^= 1;
                         }
@@ -797,10 +802,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp >= kQueryWarp) {
-        // ---- the queries' channels 256 to 511 into TMEM, where a 64-row operand's rows lie as the product leaves
-        // its own: 32 KB of shared memory that hold half a step of the cache more
+        // ---- the queries' other units into TMEM, where a 64-row operand's rows lie as the product leaves its own:
+        // shared memory that holds more of the cache
         const int row = (warp - kQueryWarp) * 16 + (lane & 15), tok = row / pl.hp, head_in = row - tok * pl.hp;
-        const uint32_t to = tb + ((uint32_t)((warp - kQueryWarp) * 32) << 16) + kTmemQ;
+        const uint32_t to = tb + ((uint32_t)((warp - kQueryWarp) * 32) << 16) + kTmemO + 4 * pl.n;
         uint32_t items = 0;
         for (uint32_t k = 0;; ++k) {
             if (!wait(b.i_full + k % kSlots, (k / kSlots) & 1)) break;
@@ -809,12 +814,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(b.i_empty + k % kSlots);
             if (!it.found) break;
             if (it.s0 == it.s1) continue;
-            uint32_t r[2][32];  // a block of 64 channels: this half of the warp's 4 or 5, then 6 or 7
+            uint32_t r[4 - QU][32];  // of each unit this half of the warp's 64 channels
             const bool live = tok < it.tokens && it.head0 + head_in < p.H && row < (int)q_rows;
             const uint4 *q = reinterpret_cast<const uint4 *>(p.q + (int64_t)(it.t0 + tok) * p.q_stride + (int64_t)(it.head0 + head_in) * kRow +
-                                                             256 + (lane >> 4) * 64);
+                                                             QU * 128 + (lane >> 4) * 64);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 4 - QU; ++j)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint4 v = live ? __ldg(q + j * 16 + i) : make_uint4(0, 0, 0, 0);
@@ -822,8 +827,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             if (items > 0 && !wait(&b.q_empty, (items - 1) & 1)) break;  // the last item's scores are through
             fence_after_sync();
-            tmem_st_halves(to, r[0]);
-            tmem_st_halves(to + 64, r[1]);
+#pragma unroll
+            for (int j = 0; j < 4 - QU; ++j) tmem_st_halves(to + j * 64, r[j]);
             tmem_wait_st();
             fence_before_sync();
             __syncwarp();
@@ -1290,7 +1295,11 @@ Plan plan_of(int64_t N, int64_t tokens, int H, int64_t max_tokens) {
         pl.most_places = std::max(pl.most_places, most_units[w] * pl.G[w]);
     }
     pl.by_unit = pl.most_places < pl.ctas;
-    const int64_t q = (int64_t)pl.q_rows * kSmemBlocks * 128;
+    // Up to 48 rows leave TMEM for a third unit of the queries, and so the ring a place more, which longer calls gain from:
+    // with two and three units in TMEM 8 sequences of 60000 tokens, 96 heads 140 and 134 us, 128 of 1000, 32 heads 35.1 and
+    // 33.9, but 32 of 300 12.6 and 13.1, 64 of 5 8.8 and 9.4 (three units take longer to come).
+    pl.q_units = pl.n <= 48 && pl.most_places * per >= (int64_t)8 * pl.ctas ? 1 : 2;
+    const int64_t q = (int64_t)pl.q_rows * (2 * pl.q_units + 1) * 128;
     const int64_t ps = std::max<int64_t>(pl.n * 128, kSoftWarps * 1024);  // (the output is turned there, too)
     const int64_t room = kMaxSmem - 1024 - (int64_t)round_up(sizeof(Bars), 128) - round_up(q, 1024) - round_up(ps, 1024);
     pl.units = (int)std::min<int64_t>(kMaxUnits, (room - kShared * kSharedBytes) / kUnitBytes);
@@ -1363,7 +1372,8 @@ kda_status launch_attn_latent(const AttnLatentParams &p, cudaStream_t st) {
     static DeviceOnce configured;
     const int dev = current_device();
     if (!configured.done(dev)) {
-        if (cudaFuncSetAttribute(attn_latent_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) {
+        if (cudaFuncSetAttribute(attn_latent_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(attn_latent_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) {
             set_error("attn_latent: cannot reserve shared memory: %s", cudaGetErrorString(cudaGetLastError()));
             return KDA_ERR_CUDA;
         }
@@ -1379,7 +1389,7 @@ kda_status launch_attn_latent(const AttnLatentParams &p, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, attn_latent_kernel, mq, mc, mr, a);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, pl.q_units == 1 ? attn_latent_kernel<1> : attn_latent_kernel<2>, mq, mc, mr, a);
     note_launch();
     if (e != cudaSuccess) {
         set_error("attn_latent_kernel: %s", cudaGetErrorString(e));
