@@ -5,18 +5,17 @@
 // in bf16, each value rounded once.  The bound is memory: 1152 bytes a token in and as many out (twice
 // where the rows are wanted densely too).  A warp takes a run of tokens, whose sequence it looks for
 // once, with the next token's row on its way; a lane has two 16-byte pieces of c, so that the norm needs
-// one warp sum, and eight lanes have the pieces of r.
+// one warp sum, and two channels of r.
 //
-// 86824 tokens, normalised and turned, rows wanted: 56 us, 5.4 TB/s of 6.7 that a copy reaches; without the dense rows 53
-// (57 %: each warp's chain of norm, turn and store for one token at a time), without turning 40 (75 %).  One token
-// of 256 sequences: 2.8 us, a launch.
+// 86824 tokens, normalised and turned, rows wanted: 53 us, 5.7 TB/s of 6.7 that a copy reaches; without the dense rows 39
+// (76 %), turned or not: each warp's chain of a token, a row ahead under way.  One token of 256 sequences: 2.7 us, a launch.
 #include "kda_latent.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kResident = 3;  // CTAs of an SM
+constexpr int kWarps = 4;
+constexpr int kResident = 6;  // CTAs of an SM: 24 warps (16, 24 and 32 warps: 57.9, 52.7 and 55.0 us for 86824 tokens)
 // Sums of squares within these bounds have lost nothing to fp32's range.
 constexpr float kLeastSum = 8.077935669463161e-28f, kMostSum = 1.329227995784916e36f;  // 2^-90, 2^120
 
@@ -35,7 +34,8 @@ __device__ __forceinline__ int sequence_of(const LatentAppendParams &p, int64_t 
 }
 
 struct Row {
-    uint4 a, b, r;  // pieces lane and 32 + lane of c; lanes 0 to 7: piece lane of r
+    uint4 a, b;  // pieces lane and 32 + lane of c
+    uint32_t r;  // channels 2 lane, 2 lane + 1 of r
 };
 __device__ __forceinline__ Row load_row(const LatentAppendParams &p, int64_t t) {
     const uint4 *x = reinterpret_cast<const uint4 *>(p.x + t * p.x_stride);
@@ -43,8 +43,7 @@ __device__ __forceinline__ Row load_row(const LatentAppendParams &p, int64_t t) 
     Row y;
     y.a = __ldcs(x + lane);
     y.b = __ldcs(x + 32 + lane);
-    y.r = make_uint4(0, 0, 0, 0);
-    if (lane < 8) y.r = __ldcs(x + 64 + lane);
+    y.r = __ldcs(reinterpret_cast<const uint32_t *>(x + 64) + lane);
     return y;
 }
 
@@ -70,22 +69,45 @@ __device__ __forceinline__ void normalise(Row &y, const float (&w)[16], float ep
         s = !(sum <= kMostSum) ? exp2_int(-64) : eps < 0.5f ? exp2_int(64) : 1.f;
         sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sum = fmaf(v[i] * s, v[i] * s, sum);
+        for (int i = 0; i < 16; ++i) {
+            v[i] *= s;
+            sum = fmaf(v[i], v[i], sum);
+        }
         sum = warp_sum(sum);
     }
     const float f = rsqrtf(sum * (1.f / kLatent) + eps * s * s);
     float h[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = v[i] * s * f * w[i];
+    for (int i = 0; i < 8; ++i) h[i] = v[i] * f * w[i];
     y.a = Vec16<__nv_bfloat16>::store(h);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = v[8 + i] * s * f * w[8 + i];
+    for (int i = 0; i < 8; ++i) h[i] = v[8 + i] * f * w[8 + i];
     y.b = Vec16<__nv_bfloat16>::store(h);
 }
 
+// The channels 2 lane, 2 lane + 1 of r turned, from the cos and sin of pair `lane`.  Interleaved, they are that pair; else
+// they belong to the pairs 2 lane and the next, whose other halves another lane has.  (By 16-byte pieces in a few lanes,
+// through shared memory, 86824 tokens took 53 us instead of 39.)
+__device__ __forceinline__ uint32_t turn_word(uint32_t word, float c, float s, const RotaryParams &rot) {
+    const int lane = threadIdx.x & 31, np = rot.R >> 1;
+    const float a = __uint_as_float(word << 16), b = __uint_as_float(word & 0xFFFF0000u);
+    float x, y;
+    if (rot.interleaved) {
+        turn_pair(a, b, make_float2(c, s), rot.magnitude, x, y);
+    } else {
+        const bool first = lane < np >> 1;
+        const uint32_t other = __shfl_sync(0xffffffffu, word, first ? lane + (np >> 1) : lane - (np >> 1));
+        const int pair = 2 * (first ? lane : lane - (np >> 1));
+        const float c0 = __shfl_sync(0xffffffffu, c, pair), s0 = __shfl_sync(0xffffffffu, s, pair);
+        const float c1 = __shfl_sync(0xffffffffu, c, pair + 1), s1 = __shfl_sync(0xffffffffu, s, pair + 1);
+        const uint32_t o = first ? other : other ^ 0x80008000u;  // (a' = a cos - b sin, b' = b cos + a sin)
+        x = diff_of_products(a, c0, __uint_as_float(o << 16), s0) * rot.magnitude;
+        y = diff_of_products(b, c1, __uint_as_float(o & 0xFFFF0000u), s1) * rot.magnitude;
+    }
+    return lane < np ? pack_bf16x2(x, y) : word;
+}
+
 __global__ void __launch_bounds__(kWarps * 32, kResident) latent_append_kernel(const __grid_constant__ LatentAppendParams p, int run) {
-    __shared__ __align__(16) float2 s_cs[kWarps][kShared / 2];
-    __shared__ __align__(16) __nv_bfloat16 s_r[kWarps][kShared];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, np = p.rot.R >> 1;
     const int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * run, t1 = min(t0 + run, p.tokens);
     if (t0 >= t1) return;
@@ -117,24 +139,15 @@ __global__ void __launch_bounds__(kWarps * 32, kResident) latent_append_kernel(c
         if (block < (uint32_t)p.c.max_blocks) page = __ldg(p.c.block_table + (int64_t)n * p.c.max_blocks + block);
         if (p.norm_w) normalise(y, w, p.eps);
         if (np > 0) {
-            if (lane < 8) reinterpret_cast<uint4 *>(s_r[warp])[lane] = y.r;
-            if (lane < np) {
-                float c, s;
-                cos_sin_turn((uint64_t)place * turn, c, s);
-                s_cs[warp][cs_at(lane, np)] = make_float2(c, s * p.rot.sign);
-            }
-            __syncwarp();
-            if (lane < rotary_units(kShared, p.rot.R, p.rot.interleaved, 8))
-                rotate_unit<__nv_bfloat16>(s_r[warp], s_r[warp], s_cs[warp], lane, p.rot.R, p.rot.interleaved, p.rot.magnitude);
-            __syncwarp();
-            if (lane < 8) y.r = reinterpret_cast<const uint4 *>(s_r[warp])[lane];
-            __syncwarp();  // read before the next token's are written
+            float c, sn;
+            cos_sin_turn((uint64_t)place * turn, c, sn);
+            y.r = turn_word(y.r, c, sn, p.rot);
         }
         auto put = [&](__nv_bfloat16 *to) {
             uint4 *row = reinterpret_cast<uint4 *>(to);
             row[lane] = y.a;
             row[32 + lane] = y.b;
-            if (lane < 8) row[64 + lane] = y.r;
+            reinterpret_cast<uint32_t *>(row + 64)[lane] = y.r;
         };
         if (p.rows_out) put(p.rows_out + t * kRow);
         if ((uint32_t)page < (uint32_t)p.c.n_pages)
