@@ -13,8 +13,8 @@
 // TMA through swizzled shared memory, which also cuts off the rows behind the last token.  The expansion of
 // many tokens has a kernel of its own for pairs of SMs.
 //
-// What bounds it, and the floor by bytes or operations: queries, 256 tokens of 128 heads with turned channels 15 us (10), bytes
-// of which half are W; 8192 of 32 heads 94 (61), each CTA's own chain of copy, product and output, two of which an SM
+// What bounds it, and the floor by bytes or operations: queries, 256 tokens of 128 heads with turned channels 13.5 us (10), bytes
+// of which half are W; 8192 of 32 heads 83 (61), each CTA's own chain of copy, product and output, two of which an SM
 // holds.  Values, 256 tokens of 128 heads 12 (8.8); 8192 of 32 heads 58 (51), 88 % of a copy's rate.  Expansion, 100 tokens of 16 heads
 // 5.3, a launch and the chain of one tile; 8192 of 32 heads 52 (36), see there.
 #include <cuda.h>
@@ -32,7 +32,7 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = 128;  // tokens of a tile
-constexpr int kThreads = 192, kMmaWarp = 4, kLoadWarp = 5;
+constexpr int kThreads = 192, kMmaWarp = 4, kLoadWarp = 5, kTurnWarp = 6, kTurnWarps = 8;
 constexpr uint32_t kBlock = kTile * 128;  // 64 channels of a tile's rows
 constexpr float kNaN = __builtin_nanf("");
 
@@ -58,6 +58,7 @@ struct Cfg {
     static constexpr int OUT_BLOCKS = NT / 64;
     static constexpr int NTILES = (QUERIES ? kLatent : EXPAND ? kHeadKey + kHeadValue : kHeadValue) / NT;  // of a head
     static constexpr uint32_t SMEM = BARS + sizeof(Bars) + 1024;
+    static constexpr int THREADS = kThreads + (QUERIES ? 32 * kTurnWarps : 0);
     // where output block i is put together: the operands are through, the expansion's shared channels are not
     __host__ __device__ static constexpr uint32_t out_at(int i) { return EXPAND ? kBlock * (i + 1) : kBlock * i; }
     static_assert(!EXPAND || (kBlock * (OUT_BLOCKS + 1) <= RING && (SHARED == 0 || SHARED >= kBlock * (OUT_BLOCKS + 1))),
@@ -102,51 +103,15 @@ __device__ __forceinline__ bool rows_any(bool x) {
 }
 __device__ __forceinline__ void rows_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
-// The queries' other channels, turned: a CTA's tokens have their angles formed once for all heads.  (In the
-// products' CTAs, where each head's formed them anew, this was a quarter of the time.)
-constexpr int kTurnTokens = 32;
-template <int THREADS>
-__device__ __forceinline__ void turn_shared(const LatentProductParams &p, int tile, int tokens, float2 *cs) {  // [tokens][R / 2]
-    const int64_t t0 = (int64_t)tile * tokens;
-    const int n = (int)min((int64_t)tokens, p.tokens - t0), np = p.rot.R >> 1, units = rotary_units(kShared, p.rot.R, p.rot.interleaved, 8);
-    if (np > 0) {
-        fill_cos_sin(cs, p.rot, n, [&](int t) { return __ldg(p.positions + t0 + t); }, threadIdx.x, THREADS);
-        __syncthreads();
-    }
-    for (int i = threadIdx.x; i < n * p.H * units; i += THREADS) {
-        const int row = i / units, u = i - row * units, t = row / p.H, h = row - t * p.H;
-        rotate_unit<__nv_bfloat16>(p.x + (t0 + t) * p.x_stride + (int64_t)h * kHeadQuery + kHeadKey,
-                                   p.out + ((t0 + t) * p.H + h) * kRow + kLatent, cs + t * np, u, p.rot.R, p.rot.interleaved,
-                                   p.rot.magnitude);
-    }
-}
-// In a launch of its own that runs beside the products': among their CTAs in one launch the turning ones
-// would hold places that the products want (256 tokens, 128 heads: 27 and 15 us).  Where all fit the GPU at once
-// it is one launch, which costs less on the host.
-constexpr int kTurnThreads = 256;
-__global__ void __launch_bounds__(kTurnThreads) latent_turn_kernel(const __grid_constant__ LatentProductParams p, int tokens) {
-    __shared__ __align__(16) float2 cs[kTurnTokens * kShared / 2];
-    turn_shared<kTurnThreads>(p, blockIdx.x, tokens, cs);
-    // It shares nothing with the products' launch, but must not end before that has.
-    if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 template <int WHAT, int NT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(Cfg<WHAT, NT>::THREADS)
     latent_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                           const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_out2,
-                          const __grid_constant__ LatentProductParams p, int turn_from, int turn_tokens) {
+                          const __grid_constant__ LatentProductParams p) {
     using F = Cfg<WHAT, NT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
-    if (F::QUERIES) {
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        if ((int)blockIdx.x >= turn_from) {
-            turn_shared<kThreads>(p, blockIdx.x - turn_from, turn_tokens, reinterpret_cast<float2 *>(sm));
-            return;
-        }
-    }
     Bars &b = *reinterpret_cast<Bars *>(sm + F::BARS);
     const int cta = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -232,6 +197,28 @@ __global__ void __launch_bounds__(kThreads)
             mbar_wait(&b.done, 0, kAttnPolls);  // nothing may still run once the CTA has ended
         }
         __syncwarp();
+    } else if (F::QUERIES && warp >= kTurnWarp) {
+        // The shared channels of this CTA's part of the tile's rows, turned while the product runs, two channels a
+        // lane, in warps of their own: 256 tokens, 128 heads 13.5 us (with four such warps 14.2, by the output's warps before
+        // their output 17.2, and in a launch beside this one, the angles formed once for all heads, 14.8).
+        constexpr int ROWS = kTile / NTILES / kTurnWarps;  // a warp's
+        const int r0 = t0 + nt * (kTile / NTILES) + (warp - kTurnWarp) * ROWS, np = p.rot.R >> 1;
+        const int at = np > 0 && lane < ROWS && r0 + lane < p.tokens ? __ldg(p.positions + r0 + lane) : 0;
+        uint32_t word[ROWS];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (r0 + i < p.tokens)
+                word[i] = __ldg(reinterpret_cast<const uint32_t *>(p.x + (int64_t)(r0 + i) * p.x_stride + (int64_t)h * kHeadQuery + kHeadKey) + lane);
+        const uint64_t turn = lane < np ? turn_of(__ldg(p.rot.inv_freq + lane)) : 0;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            if (np > 0) {
+                float c, s;
+                cos_sin_turn((uint64_t)(int64_t)__shfl_sync(0xffffffffu, at, i) * turn, c, s);
+                word[i] = turn_word(word[i], c, s, p.rot);
+            }
+            if (r0 + i < p.tokens) reinterpret_cast<uint32_t *>(p.out + ((int64_t)(r0 + i) * p.H + h) * kRow + kLatent)[lane] = word[i];
+        }
     } else {
         const int row = warp * 32 + lane;
         // the four warps go on or stop together, since they wait for each other at barriers
@@ -279,7 +266,7 @@ __global__ void __launch_bounds__(kThreads)
         if (threadIdx.x == 0) bulk_wait_all();
         __syncthreads();
         const __nv_bfloat16 nan = __float2bfloat16_rn(kNaN);
-        for (int r = threadIdx.x; r < kTile && t0 + r < p.tokens; r += kThreads) {
+        for (int r = threadIdx.x; r < kTile && t0 + r < p.tokens; r += F::THREADS) {
             const int64_t head = (int64_t)(t0 + r) * p.H + h;
             if (F::EXPAND) {
                 for (int i = nt * NT; i < nt * NT + NT; ++i)
@@ -637,31 +624,9 @@ kda_status run(const LatentProductParams &p, cudaStream_t st) {
         set_error("latent product: too many tokens");
         return KDA_ERR_UNSUPPORTED;
     }
-    // turning CTAs with about four units a thread
-    const int tokens = (int)std::max<int64_t>(1, std::min<int64_t>(kTurnTokens, 4 * kTurnThreads / (8 * p.H)));
-    const int64_t turn_ctas = F::QUERIES ? (p.tokens + tokens - 1) / tokens : 0;
-    const bool together = ctas + turn_ctas <= sm_count();
-    kernel<<<(unsigned)(ctas + (together ? turn_ctas : 0)), kThreads, F::SMEM, st>>>(mx, mw, mo, mo2, p, (int)ctas, tokens);
+    kernel<<<(unsigned)ctas, F::THREADS, F::SMEM, st>>>(mx, mw, mo, mo2, p);
     note_launch();
-    const kda_status s = check_launch("latent_product_kernel");
-    if (!F::QUERIES || together || s != KDA_OK) return s;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)turn_ctas);
-    cfg.blockDim = dim3(kTurnThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, latent_turn_kernel, p, tokens);
-    note_launch();
-    if (e != cudaSuccess) {
-        set_error("latent_turn_kernel: %s", cudaGetErrorString(e));
-        cudaGetLastError();
-        return KDA_ERR_CUDA;
-    }
-    return check_launch("latent_turn_kernel");
+    return check_launch("latent_product_kernel");
 }
 
 kda_status run_pairs(const LatentProductParams &p, cudaStream_t st) {
