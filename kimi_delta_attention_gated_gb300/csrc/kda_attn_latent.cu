@@ -822,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 4 - QU; ++j)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const uint4 v = live ? __ldg(q + j * 16 + i) : make_uint4(0, 0, 0, 0);
+                    const uint4 v = live ? q[j * 16 + i] : make_uint4(0, 0, 0, 0);
                     r[j][4 * i] = v.x, r[j][4 * i + 1] = v.y, r[j][4 * i + 2] = v.z, r[j][4 * i + 3] = v.w;
                 }
             if (items > 0 && !wait(&b.q_empty, (items - 1) & 1)) break;  // the last item's scores are through

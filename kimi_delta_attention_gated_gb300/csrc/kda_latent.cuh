@@ -111,4 +111,30 @@ __device__ __forceinline__ uint32_t turn_word(uint32_t word, float c, float s, c
     return lane < np ? pack_bf16x2(x, y) : word;
 }
 
+// A launch that may set up while the one before ends: what that wrote or read is touched after before_is_over only.
+template <typename... Params, typename... Args>
+cudaError_t launch_beside_end(void (*kernel)(Params...), unsigned ctas, int threads, size_t smem, cudaStream_t st, const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+inline kda_status launched(cudaError_t e, const char *what) {
+    note_launch();
+    if (e == cudaSuccess) return check_launch(what);
+    set_error("%s: %s", what, cudaGetErrorString(e));
+    cudaGetLastError();
+    return KDA_ERR_CUDA;
+}
+__device__ __forceinline__ void before_is_over() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next launch may set up from here on.
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 }  // namespace kda

@@ -8,7 +8,7 @@
 // one warp sum, and two channels of r.
 //
 // 86824 tokens, normalised and turned, rows wanted: 53 us, 5.7 TB/s of 6.7 that a copy reaches; without the dense rows 39
-// (76 %), turned or not: each warp's chain of a token, a row ahead under way.  One token of 256 sequences: 2.7 us, a launch.
+// (76 %), turned or not: each warp's chain of a token, a row ahead under way.  One token of 256 sequences: 2.2 us, a launch.
 #include "kda_latent.cuh"
 
 namespace kda {
@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kWarps * 32, kResident) latent_append_kernel(c
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, np = p.rot.R >> 1;
     const int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * run, t1 = min(t0 + run, p.tokens);
     if (t0 >= t1) return;
+    before_is_over();
     Row next = load_row(p, t0);
     const uint64_t turn = lane < np ? turn_of(__ldg(p.rot.inv_freq + lane)) : 0;
     float w[16];
@@ -140,9 +141,8 @@ kda_status launch_latent_append(const LatentAppendParams &p, cudaStream_t st) {
     // one token a warp, or equal runs for the warps that the GPU holds at once
     const int64_t warps = (int64_t)sm_count() * kResident * kWarps, run = (p.tokens + warps - 1) / warps;
     const int64_t ctas = (p.tokens + run * kWarps - 1) / (run * kWarps);
-    latent_append_kernel<<<(unsigned)ctas, kWarps * 32, 0, st>>>(p, (int)run);
-    note_launch();
-    return check_launch("latent_append_kernel");
+    const cudaError_t e = launch_beside_end(latent_append_kernel, (unsigned)ctas, kWarps * 32, 0, st, p, (int)run);
+    return launched(e, "latent_append_kernel");
 }
 
 }  // namespace kda

@@ -16,7 +16,7 @@
 // What bounds it, and the floor by bytes or operations: queries, 256 tokens of 128 heads with turned channels 13.5 us (10), bytes
 // of which half are W; 8192 of 32 heads 83 (61), each CTA's own chain of copy, product and output, two of which an SM
 // holds.  Values, 256 tokens of 128 heads 12 (8.8); 8192 of 32 heads 58 (51), 88 % of a copy's rate.  Expansion, 100 tokens of 16 heads
-// 5.3, a launch and the chain of one tile; 8192 of 32 heads 52 (36), see there.
+// 4.6, a launch and the chain of one tile; 8192 of 32 heads 52 (36), see there.
 #include <cuda.h>
 
 #include <algorithm>
@@ -133,9 +133,11 @@ __global__ void __launch_bounds__(Cfg<WHAT, NT>::THREADS)
         tmem_alloc(&b.tmem, NT);
         tmem_relinquish();
     }
+    next_may_start();
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
+    before_is_over();
     const uint32_t tb = b.tmem;
     auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t polls) {
         for (uint32_t i = 0; i < polls; ++i) {
@@ -203,12 +205,12 @@ __global__ void __launch_bounds__(Cfg<WHAT, NT>::THREADS)
         // their output 17.2, and in a launch beside this one, the angles formed once for all heads, 14.8).
         constexpr int ROWS = kTile / NTILES / kTurnWarps;  // a warp's
         const int r0 = t0 + nt * (kTile / NTILES) + (warp - kTurnWarp) * ROWS, np = p.rot.R >> 1;
-        const int at = np > 0 && lane < ROWS && r0 + lane < p.tokens ? __ldg(p.positions + r0 + lane) : 0;
+        const int at = np > 0 && lane < ROWS && r0 + lane < p.tokens ? __ldcg(p.positions + r0 + lane) : 0;
         uint32_t word[ROWS];
 #pragma unroll
         for (int i = 0; i < ROWS; ++i)
             if (r0 + i < p.tokens)
-                word[i] = __ldg(reinterpret_cast<const uint32_t *>(p.x + (int64_t)(r0 + i) * p.x_stride + (int64_t)h * kHeadQuery + kHeadKey) + lane);
+                word[i] = __ldcg(reinterpret_cast<const uint32_t *>(p.x + (int64_t)(r0 + i) * p.x_stride + (int64_t)h * kHeadQuery + kHeadKey) + lane);
         const uint64_t turn = lane < np ? turn_of(__ldg(p.rot.inv_freq + lane)) : 0;
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
@@ -402,10 +404,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&b.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    next_may_start();
     fence_before_sync();
     __syncthreads();
     pair_sync();
     fence_after_sync();
+    before_is_over();
     const uint32_t tb = b.tmem;
     auto give_up = [&] {  // both CTAs stop
         *abort_flag = 1;
@@ -491,7 +495,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (i < i1 && t0 + j * 4 < p.tokens)
-                    r[j] = __ldg(reinterpret_cast<const uint4 *>(p.x + (t0 + j * 4) * p.x_stride + kLatent) + piece);
+                    r[j] = __ldcg(reinterpret_cast<const uint4 *>(p.x + (t0 + j * 4) * p.x_stride + kLatent) + piece);
         };
         load(i0);
         for (int64_t i = i0; i < i1; ++i) {
@@ -624,9 +628,8 @@ kda_status run(const LatentProductParams &p, cudaStream_t st) {
         set_error("latent product: too many tokens");
         return KDA_ERR_UNSUPPORTED;
     }
-    kernel<<<(unsigned)ctas, F::THREADS, F::SMEM, st>>>(mx, mw, mo, mo2, p);
-    note_launch();
-    return check_launch("latent_product_kernel");
+    const cudaError_t e = launch_beside_end(kernel, (unsigned)ctas, F::THREADS, F::SMEM, st, mx, mw, mo, mo2, p);
+    return launched(e, "latent_product_kernel");
 }
 
 kda_status run_pairs(const LatentProductParams &p, cudaStream_t st) {
@@ -659,9 +662,8 @@ kda_status run_pairs(const LatentProductParams &p, cudaStream_t st) {
         configured.set(dev);
     }
     const int64_t tiles = (p.tokens + kPairTokens - 1) / kPairTokens, pairs = std::min<int64_t>(sm_count() / 2, tiles * p.H);
-    latent_expand_pair_kernel<<<(unsigned)(2 * pairs), kPairThreads, kPairSmem, st>>>(mx, mw, p, (int)tiles);
-    note_launch();
-    return check_launch("latent_expand_pair_kernel");
+    const cudaError_t e = launch_beside_end(latent_expand_pair_kernel, (unsigned)(2 * pairs), kPairThreads, kPairSmem, st, mx, mw, p, (int)tiles);
+    return launched(e, "latent_expand_pair_kernel");
 }
 
 }  // namespace
