@@ -983,13 +983,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b.p_ready);
             }
-            if (!ok) break;
             // ---- output
             if (nt > 0) {
                 ok = ok && wait(&b.p_free, (blocks - 1) & 1);
                 fence_after_sync();
             }
-            // (also: the last item's places and factors are read)
+            // All four warps come here, those that gave up too: a wait may run out in one warp and not in another, and
+            // one that left by itself would keep the others at this barrier for ever.  (Also: the last item's places and
+            // factors are read.)
             if (soft_any(!ok)) {
                 ok = false;
                 break;
