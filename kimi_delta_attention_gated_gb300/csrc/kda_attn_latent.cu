@@ -135,6 +135,7 @@ struct Bars {
     int start_seq;
     uint32_t tmem;
     int abort;                   // a bounded wait gave up
+    uint32_t odd;                // the last item (from 1) with a cleared row that some of its tokens see
 };
 
 __device__ __forceinline__ bool elect_one() {
@@ -476,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x < kMostPieces) b.load[threadIdx.x] = 0;
     if (threadIdx.x == kThreads - 1) {
         b.abort = 0;
+        b.odd = 0;
         b.start_seq = -1;
     }
     if (warp == kLoadWarp && lane < 3)
@@ -945,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (j0 + kStep > it.seen0) {
                     // Tokens that not every row sees.  A weight of zero times what is not finite would not be
                     // zero: behind the tile's last token everything is cleared, and before it the rows
-                    // that hold an infinity or a NaN (where a row sees one of these, its sum of weights says so).
+                    // that hold an infinity or a NaN, which those that see them get with the output.
                     for (int r = warp; r < kStep; r += kSoftWarps) {
                         if (j0 + r < it.seen0) continue;
                         uint32_t at[2];
@@ -969,6 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     odd |= (v[i] & 0x7F80u) == 0x7F80u || (v[i] & 0x7F800000u) == 0x7F800000u;
                             }
                             clear = __any_sync(0xffffffffu, odd);
+                            if (clear && lane == 0) *(volatile uint32_t *)&b.odd = k + 1;
                         }
                         if (clear) {
                             st_shared_v4(at[0], 0, 0, 0, 0);
@@ -998,6 +1001,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             l += __shfl_xor_sync(0xffffffffu, l, 16);  // of both halves of the tokens
             const bool bad = *(volatile int *)&b.slots[k % kSlots].bad != 0;
             if (bad) l = kNaN;
+            if (*(volatile uint32_t *)&b.odd == k + 1) {
+                // A channel that is infinite or NaN in a token that a row sees is NaN: the token's score is not finite either, and
+                // where it is +inf or NaN the sum of weights is NaN, but where it is -inf the weight is 0, and 0 times that channel
+                // NaN.  (As the products have it in steps that all rows see.)  A thread has a channel of each block, as in O^T.
+                const int32_t *table = p.c.block_table + (int64_t)it.seq * p.c.max_blocks;
+                const int j1 = min(most, it.s1 * kStep);
+#pragma unroll 1
+                for (int j = max(it.seen0, it.s0 * kStep); j < j1; ++j) {
+                    const int page = __ldg(table + (j >> p.c.p_shift));
+                    if ((uint32_t)page >= (uint32_t)p.c.n_pages) continue;  // (the rows are NaN)
+                    const uint16_t *x = reinterpret_cast<const uint16_t *>(p.c.rows) +
+                                        (((int64_t)page << p.c.p_shift) + (j & (p.c.P - 1))) * kRow + warp * 32 + lane;
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        const bool odd = (__ldg(x + q * 128) & 0x7F80u) == 0x7F80u;
+                        if (!__any_sync(0xffffffffu, odd)) continue;
+#pragma unroll 1
+                        for (int r0 = 0; r0 < pl.n; r0 += 16) {
+                            float o[16];
+                            const uint32_t at = tb + lane_base + kTmemO + q * pl.n + r0;
+                            tmem_ld16f(at, o);
+                            wait_ld<16>(o);
+                            uint32_t u[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                u[i] = __float_as_uint(odd && it.seen0 + (r0 + i) / pl.hp > j ? kNaN : o[i]);
+                            tmem_st16(at, u);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+            }
             if (it.part >= 0) {
                 // Sums of a part, four rows' values of a channel together, so that a warp's stores are
                 // contiguous (a row's channels together, one store took 58 cycles, 12000 an item).
