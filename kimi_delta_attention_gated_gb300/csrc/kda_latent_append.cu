@@ -65,8 +65,9 @@ __device__ __forceinline__ void normalise(Row &y, const float (&w)[16], float ep
     sum = warp_sum(sum);
     float s = 1.f;
     if (!(sum >= kLeastSum && sum <= kMostSum)) {  // (the same in all lanes) again at another scale
-        // (eps s^2 has to stay finite; beside an eps of 1/2 so small a sum is nothing)
-        s = !(sum <= kMostSum) ? exp2_int(-64) : eps < 0.5f ? exp2_int(64) : 1.f;
+        // (512 squares of less than 2^128 s each have to stay finite, so s^2 <= 2^-138; eps s^2, too; beside an eps of 1/2 so
+        // small a sum is nothing)
+        s = !(sum <= kMostSum) ? exp2_int(-69) : eps < 0.5f ? exp2_int(64) : 1.f;
         sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
