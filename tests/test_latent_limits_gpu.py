@@ -11,7 +11,7 @@ from tests.test_kv_append_gpu import gen, table_for
 
 pytestmark = pytest.mark.gpu
 TIMEOUT = 4
-LIMITS = [1, 1, 2, 1, 3, 1, 5, 1, 8, 1, 2, 1]
+LIMITS = [1, 2, 4, 8, 12, 16, 16, 20, 24, 28, 32, 48]
 
 
 @pytest.fixture(scope="module", autouse=True)
