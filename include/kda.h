@@ -680,7 +680,8 @@ kda_status kda_latent_append(const void *x, int64_t x_stride, int64_t tokens, vo
  *     out[t][h] = [ sum_n q[t][h][n] w_kv[h][n][.], n < 128 | q[t][h][128 .. 192) turned by positions[t] ].
  *
  *   q          [tokens, heads, 192] bf16, q_stride apart
- *   positions  [tokens] int32, with inv_freq as in kda_latent_append; both or neither
+ *   positions  [tokens] int32, any values (as kda_rotary), with inv_freq as in kda_latent_append;
+ *              both or neither
  *   out        [tokens, heads, KDA_LATENT_ROW] bf16
  */
 kda_status kda_latent_queries(const void *q, int64_t q_stride, int64_t tokens, int heads, const void *w_kv,
