@@ -217,7 +217,7 @@ def _cu(cu_seqlens, device):
 
 def _to_host(ts, host, dests=None):
     """Copy results back to the host: into the caller's host tensors when given
-    (asynchronously when they are pinned, then the stream is synchronised)."""
+    (asynchronously when they are pinned, then the stream of each result's device is synchronised)."""
     if not host:
         return ts
     out = []
@@ -230,7 +230,8 @@ def _to_host(ts, host, dests=None):
             out.append(dst)
         else:
             out.append(t.to("cpu"))
-    torch.cuda.current_stream().synchronize()
+    for device in {t.device for t in ts if t is not None and t.is_cuda}:
+        torch.cuda.current_stream(device).synchronize()
     return tuple(out)
 
 
