@@ -76,7 +76,7 @@ constexpr uint32_t kTmemO = 2 * kStep;   // TMEM columns: scores of two steps, O
 constexpr float kSlack = 8.f;           // log2: how far a score may exceed the reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNaN = __builtin_nanf("");
-constexpr int kMaxSmem = 232448;
+constexpr int kMaxSmem = 232448;        // all that a CTA may have, so that nothing else on its SM wants TMEM
 constexpr uint32_t kLastPolls = 256;    // for copies after a failure: a millisecond
 
 __device__ int g_attn_latent_timeouts = 0;

@@ -6,8 +6,8 @@
 //   expand   k[t, h] = [ sum_c x[t, c] W[h, n, c], n < 128  |  x[t, 512:576] ],
 //            v[t, h] = sum_c x[t, c] W[h, 128 + n, c]
 //
-// Matrix products of 128 tokens by NT outputs of one head on tcgen05, a tile a CTA, two to three
-// CTAs on an SM so that one's copies and stores run beside another's products.  W's inner index is the
+// Matrix products of 128 tokens by NT outputs of one head on tcgen05, a tile a CTA, two
+// CTAs on an SM (97 KB of shared memory each) so that one's copies and stores run beside the other's products.  W's inner index is the
 // latent's channel: for the values and the expansion that is the sum's index (K-major), for the queries
 // the output's (MN-major); the same bytes serve both.  Operands come by TMA, results leave by
 // TMA through swizzled shared memory, which also cuts off the rows behind the last token.  The expansion of
@@ -34,6 +34,7 @@ using namespace tc;
 constexpr int kTile = 128;  // tokens of a tile
 constexpr int kThreads = 192, kMmaWarp = 4, kLoadWarp = 5, kTurnWarp = 6, kTurnWarps = 8;
 constexpr uint32_t kBlock = kTile * 128;  // 64 channels of a tile's rows
+constexpr uint32_t kSmSmem = 228 * 1024, kCtaSmem = 1024;  // an SM's shared memory; what a CTA takes beside its own
 constexpr float kNaN = __builtin_nanf("");
 
 __device__ int g_latent_product_timeouts = 0;
@@ -64,8 +65,12 @@ struct Cfg {
     static_assert(!EXPAND || (kBlock * (OUT_BLOCKS + 1) <= RING && (SHARED == 0 || SHARED >= kBlock * (OUT_BLOCKS + 1))),
                   "the shared channels and the output lie apart");
     static_assert(kBlock * OUT_BLOCKS <= RING, "the output needs the operands' room");
+    // The next launch may set up, and take its TMEM, while a CTA of this one still asks for its own.  It gets it, since
+    // shared memory lets an SM hold two such CTAs, of either launch, whose columns fit together, and none beside a CTA
+    // that takes all columns.  A third, or one of another kernel with less shared memory, could wait for a launch that
+    // waits for it.
+    static_assert(2 * NT <= 512 && 3 * (SMEM + kCtaSmem) > kSmSmem, "two CTAs an SM, and TMEM for both");
 };
-
 
 __device__ __forceinline__ bool elect_one() {
     uint32_t ok;
@@ -309,6 +314,7 @@ struct PairBars {
 };
 constexpr uint32_t kPairSmem = kPairBars + sizeof(PairBars) + 1024;
 static_assert(kPairSmem <= 232448, "shared memory");
+static_assert(kPairSmem + kCtaSmem + Cfg<kLatentValues, 64>::SMEM + kCtaSmem > kSmSmem, "an SM for itself: all of TMEM is its own");
 
 __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
     uint32_t r;
