@@ -27,13 +27,18 @@
 // line is cut into equal pieces.  Units that more than one CTA took leave their sums in a
 // workspace, and attn_latent_join_kernel adds them in their order, so results do not depend on timing.
 // Where the lengths allow it, units go whole to the piece that they begin in; where the table's width already says so
-// (plan_of), the second launch falls away.
+// (plan_of), the second launch falls away.  A table that is wider than the sequences need keeps it: 32 heads, 64 sequences of
+// 5 tokens 9.1 and 13.6 us, 128 of about 1000 34.6 and 39.5, one of 1000 14.7 and 15.3.
+// Every unit of a sequence has places for all of the sequence's steps.  In steps and drafts that is what it takes; of a
+// fresh prompt's piece, though, the early tokens see little, and the pieces are not equal work: with 4096 fresh rows of 16 heads
+// the busiest CTA has 1.9 times the mean (510 us, of which operations need 151), with 512 rows behind 4096 1.1 (98 and 40).
 //
 // What bounds it.  Up to 64 heads and long contexts: HBM.  8 sequences of 60000 tokens: 96 us with 16 heads, 104 with 64,
 // 5.8 and 5.3 TB/s of 6.7 that a copy reaches.  96 and 128 heads are two tiles and twice the products: 134 and
-// 143 us, 2200 and 2300 cycles a step of which the tensor core works 1900 (S reads 72 KB of C and up to 40 KB of Q through
-// shared memory's 128 bytes a cycle, O^T 64 KB of C and P four times); the rest is the ring's depth (a place less: 152 us
-// with 128 heads; weights in two buffers instead gain nothing).  Short calls are launches and latencies: one sequence of 1000 tokens 14 us, of which the
+// 143 us, 2200 and 2300 cycles a step of which its operands take 1900 (S reads 72 KB of C and up to 40 KB of Q through
+// shared memory's 128 bytes a cycle, O^T 64 KB of C and P four times).  Neither that nor the tensor core binds by itself: with 16 of
+// the 36 score products left out a step gains 5%; a ring place less costs as much (152 us with 128 heads; weights in two
+// buffers instead gain nothing).  Short calls are launches and latencies: one sequence of 1000 tokens 14 us, of which the
 // set-up takes 3, the first data 2, the output 3 and the joining launch 5; 128 of about 1000 tokens, 32 heads, 35 us, HBM's
 // 22 between such a beginning and end.  An item's end in the middle of a CTA's run costs about 4 steps (kPad).
 #include <cuda.h>
@@ -265,7 +270,8 @@ __device__ __forceinline__ int units_of(const Args &a, int way, int n) {
     call_rows(a.p.cu_seqlens, a.p.tokens, n, t0, nq);
     return units_of(a.plan, way, nq);
 }
-// Places of a unit beside its own cost (one without steps has a place too: its rows are written there).
+// Places of a unit beside its own cost (one without steps has a place too: its rows are written there): the whole sequence's,
+// also where its tokens see less.
 __device__ __forceinline__ int line_steps(int len) { return max(1, steps_of(len)); }
 __device__ __forceinline__ int seq_steps(const Args &a, int n) { return line_steps(tokens_of(a.p.c, n)); }
 
@@ -924,6 +930,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         soft_sync();  // the factors may be written again
                     }
                 }
+                // The weights are rounded to bf16: a product's operands have one type, and the rows are bf16.  Off by 2^-9 each at
+                // most, independently, which over 1000 tokens adds a quarter to the outputs' own rounding to bf16; the sum that divides
+                // them is of the unrounded ones.
                 const float mm = m == -INFINITY ? 0.f : m;
                 float sum[2] = {0.f, 0.f};
                 uint32_t w[kHalf / 2];

@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(Cfg<WHAT, NT>::THREADS)
 // next product runs, in the other half of TMEM.
 // 8192 tokens, 32 heads: 52 us (tiles of 128 by 256: 68), 1.3 PFLOP/s.  A product takes 5600 cycles, of which the
 // tensor core's rate would be 4096, and the stores of its outputs about as many beside it: without them it is 42 us, without
-// the products 50.  What a CTA stores goes through the same path as what its tensor core reads.
+// the products 50: a warp's store covers 64 bytes of eight rows, and at 3.4 TB/s that is far below what the bytes need (28).
 
 constexpr int kPairTokens = 256, kPairStages = 6, kChunks = kLatent / 64;
 constexpr uint32_t kPairA = kChunks * kBlock, kPairBars = kPairA + kPairStages * kBlock;
