@@ -694,7 +694,8 @@ kda_status kda_latent_queries(const void *q, int64_t q_stride, int64_t tokens, i
  *     o[t][h] = sum_{j < seen} softmax_j(scale * q[t][h] . row_j) row_j[0 .. 512),
  * seen = seq_lens[n] - (tokens of sequence n in the call) + i + 1 for its i-th token: the call's own
  * tokens are in the cache already (kda_latent_append) and counted by seq_lens.  A token that sees
- * nothing gives zero rows and lse -INFINITY.
+ * nothing gives zero rows and lse -INFINITY, and so does one whose scores are all -INFINITY (but NaN in the channels
+ * that are infinite in a row that it sees).
  *
  *   q           [tokens, heads, KDA_LATENT_ROW] bf16, q_stride apart (kda_latent_queries); at most 2^24
  *               tokens

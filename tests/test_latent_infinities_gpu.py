@@ -89,3 +89,16 @@ def test_the_same_alone_and_beside_others():
         a, b = kda.attn_latent(q[i:i + 1], cache, dt, sl - (m - 1 - i), return_lse=True)
         assert torch.equal(a[0].isnan(), o[i].isnan()) and torch.equal(b[0].isnan(), lse[i].isnan())
     assert not o[:2].isnan().any() and o[2:, :, 9].isnan().all() and o[2:].isfinite().any()
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("L", [1, 3, 200, 9000])
+def test_all_scores_minus_infinity(L, out):
+    """Every row is infinite where the first head's query is negative (its scores are -inf) and the second's is positive."""
+    P, m = 64, min(L, 2)
+    q, cache, table, sl = make([L], 2, P, L, m)
+    cache[..., 20] = math.inf
+    q[:, 0, 20], q[:, 1, 20] = -1.0, 1.0
+    o, lse = kda.attn_latent(q, cache, table.cuda(), sl, cu_seqlens=cum([m]), return_lse=True, out_dtype=out)
+    assert (lse[:, 0] == -math.inf).all() and lse[:, 1].isnan().all() and o[:, 1].isnan().all()
+    assert o[:, 0, 20].isnan().all() and (o[:, 0, :20] == 0).all() and (o[:, 0, 21:] == 0).all()
