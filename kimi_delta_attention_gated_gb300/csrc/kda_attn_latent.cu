@@ -930,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         soft_sync();  // the factors may be written again
                     }
                 }
-                // The weights are rounded to bf16: a product's operands have one type, and the rows are bf16.  Off by 2^-9 each at
+                // The weights are rounded to bf16: a product's operands have one type, and the rows are bf16.  Off by 2^-8 each at
                 // most, independently, which over 1000 tokens adds a quarter to the outputs' own rounding to bf16; the sum that divides
                 // them is of the unrounded ones.
                 const float mm = m == -INFINITY ? 0.f : m;
